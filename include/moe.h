@@ -62,7 +62,11 @@ typedef enum {
     MOE_E_SOURCE = 7       /* the expert source callback failed or returned a short read */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+typedef enum {
+    MOE_F32 = 0,
+    MOE_BF16 = 1,
+    MOE_E4M3 = 2 /* 8-bit float (4 exponent, 3 mantissa bits): paged caches only */
+} moe_dtype;
 
 typedef enum { MOE_W_F32 = 0, MOE_W_Q8G64 = 1, MOE_W_Q4G64 = 2, MOE_W_Q2G64 = 3 } moe_wfmt;
 
@@ -486,6 +490,173 @@ moe_status moe_profile_start(moe_layer* layer, int32_t max_launches);
  * totals in `out` (host array of `cap` entries); *n_kinds receives the number
  * of kinds with at least one launch. */
 moe_status moe_profile_stop(moe_layer* layer, moe_kernel_time* out, int32_t cap, int32_t* n_kinds);
+
+/* ---- the rest of a decoder layer: norms round a block --------------------------- */
+
+/* The step between two blocks of a decoder layer, over T token rows of H
+ * channels:
+ *
+ *   a = o                                                 w_post == NULL
+ *   a = o / sqrt(mean(o^2) + eps) * (w_post + weight_offset)      otherwise
+ *   r = x + res_scale * gate * a          (gate: 1 where NULL)
+ *   h = r / sqrt(mean(r^2) + eps) * (w_pre + weight_offset)
+ *
+ * with o the block's output (moe_decode's y, an attention block's projection),
+ * x the residual stream before it and r after it, and h the next block's
+ * input. Sums and statistics are fp32; h is computed from r before r is rounded
+ * to its type. The pages name the norms of the layer only among the kernels
+ * (TurboFieldfare article, "implementation scope"). */
+typedef struct {
+    uint32_t abi_version;    /* MOE_ABI_VERSION */
+    int32_t hidden;          /* H, a multiple of 64, at most 16384 */
+    int32_t res_dtype;       /* MOE_F32 or MOE_BF16: type of x and r */
+    int32_t block_dtype;     /* MOE_F32 or MOE_BF16: type of o and gate */
+    int32_t out_dtype;       /* MOE_F32 or MOE_BF16: type of h */
+    float eps;               /* finite, >= 0 */
+    float res_scale;         /* finite */
+    float weight_offset;     /* finite; 1 for weights stored as w - 1 */
+    int64_t x_stride, o_stride, gate_stride, r_stride, h_stride; /* elements between rows, multiples of
+                                8 and at least H; gate_stride 0: one row for all tokens */
+} moe_block_norm_desc;
+
+/* One call over T >= 0 rows (T == 0 does nothing). All pointers are device
+ * memory on `device`, 16-byte aligned.
+ *   x: [T][H]; o: [T][H] or NULL (then r = x, and gate and w_post must be NULL);
+ *   gate: [T][H], one row [H] (gate_stride 0), or NULL; w_post, w_pre: fp32 [H];
+ *   r: [T][H] or NULL, may be x itself; h: [T][H] or NULL (w_pre is required iff
+ *   h is given). r and h may not overlap each other or any other input.
+ * No host synchronisation, no scratch: calls on several streams are independent.
+ * Errors: MOE_E_INVALID, MOE_E_UNSUPPORTED (H above 16384), MOE_E_CUDA. */
+moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const void* o, const void* gate,
+                          const float* w_post, const float* w_pre, void* r, void* h, int32_t T,
+                          int32_t device, void* stream);
+
+/* moe_block_norm's argument checks alone (host only, no device). */
+moe_status moe_block_norm_check(const moe_block_norm_desc* desc, const void* x, const void* o, const void* gate,
+                                const float* w_post, const float* w_pre, const void* r, const void* h, int32_t T);
+
+/* ---- the rest of a decoder layer: paged key-value cache -------------------------- */
+
+/* Keys and values of one attention layer in pages of page_size tokens. Both
+ * pools hold n_pages pages; element (page, kv head, slot, d) is at
+ * page * page_stride + head * head_stride + slot * token_stride + d, so that
+ * head-major and token-major pages are both expressed. A sequence's position p
+ * lives in slot p % page_size of page block_table[seq][p / page_size].
+ * Attention and its cache are context in the pages (Inferno README, "Memory
+ * Strategy"; TurboFieldfare article, "token generation": exact split-K/V decode
+ * attention); the layouts here are this library's. */
+typedef struct {
+    uint32_t abi_version;     /* MOE_ABI_VERSION */
+    int32_t n_heads;          /* query heads, a multiple of n_kv_heads */
+    int32_t n_kv_heads;       /* 1..256 */
+    int32_t head_dim;         /* 64, 128 or 256 */
+    int32_t page_size;        /* a multiple of 16, at most 4096 */
+    int32_t n_pages;
+    int32_t cache_dtype;      /* MOE_BF16 or MOE_E4M3 */
+    int32_t rotary_dim;       /* leading channels of a head that are rotated: 0 or a multiple of 16, <= head_dim */
+    int32_t rotary_adjacent;  /* 0: channel i pairs with i + rotary_dim / 2; 1: channel 2i with 2i + 1 */
+    int32_t max_batch;        /* largest B of moe_kv_attend, 1..1024 */
+    int64_t page_stride, head_stride, token_stride; /* elements; multiples of 16 bytes; each pool's rows
+                                 [head_dim] must not overlap */
+} moe_kv_desc;
+
+typedef struct moe_kv moe_kv;
+
+/* moe_kv_append's arguments: T token rows (T >= 0; 0 does nothing). q [T][n_heads]
+ * [head_dim] (may be NULL with q_out), k and v [T][n_kv_heads][head_dim], all
+ * device bf16 with 16-byte aligned rows; *_stride: elements between tokens, a
+ * multiple of 8 (heads of a token are contiguous). positions: device int32 [T],
+ * a negative one marks a padding token: nothing is cached and its q_out row is
+ * zero. seq: device int32 [T], the token's row of block_table, or NULL: token t
+ * belongs to row t (then T <= n_seqs). block_table: device int32
+ * [n_seqs][max_pages]. q_out: device bf16 [T][n_heads][head_dim] contiguous; may be q
+ * itself where q is contiguous. */
+typedef struct {
+    const void *q, *k, *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t* positions;
+    const int32_t* seq;
+    const int32_t* block_table;
+    int32_t T, n_seqs, max_pages;
+    void* q_out;
+} moe_kv_append_args;
+
+/* moe_kv_attend's arguments: one new token of each of B sequences (0 <= B <=
+ * max_batch; 0 does nothing). q: device bf16 [B][n_heads][head_dim], q_stride
+ * elements between sequences (a multiple of 8; heads contiguous). block_table:
+ * device int32 [B][max_pages]; lens: device int32 [B], cached tokens of each
+ * sequence, the new one included. Query head i reads key-value head
+ * i / (n_heads / n_kv_heads).
+ *   s_j = scale * q . k_j;  softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *   window > 0: only j >= len - window
+ *   out = sum_j softmax(s)_j v_j: device bf16 [B][n_heads][head_dim] contiguous
+ *   lse = log(sum_j exp(s_j)): device fp32 [B][n_heads], or NULL
+ * A sequence of length <= 0 gives out = 0 and lse = -inf. Slots at or past the
+ * length (or before the window) may hold anything, NaN included; table entries of
+ * pages that hold no attended position are not read as pages. */
+typedef struct {
+    const void* q;
+    int64_t q_stride;
+    const int32_t* block_table;
+    const int32_t* lens;
+    int32_t B, max_pages;
+    float scale, softcap;
+    int32_t window;
+    void* out;
+    float* lse;
+} moe_kv_attend_args;
+
+/* Create the handle over two page pools (device memory, borrowed: they must
+ * stay valid until moe_kv_destroy; 16-byte aligned).
+ *   inv_freq: host double [rotary_dim / 2], finite, radians per position (the
+ *     caller applies any frequency scaling); may be NULL when rotary_dim is 0.
+ *   k_scale, v_scale: host fp32 [n_kv_heads], finite and positive: a cached
+ *     e4m3 value c stands for c * scale. Required for MOE_E4M3, NULL for MOE_BF16.
+ * The handle owns the frequency table and the workspace of moe_kv_attend
+ * (moe_kv_device_bytes). As for a layer, one call at a time, and work of one
+ * handle must not overlap on the GPU. */
+moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, const double* inv_freq,
+                         const float* k_scale, const float* v_scale, int32_t device, moe_kv** out);
+void moe_kv_destroy(moe_kv* kv); /* waits for the device; NULL is ignored */
+size_t moe_kv_device_bytes(const moe_kv* kv);
+
+/* Rotate q and k by their positions (R(p) turns pair i by p * inv_freq_i, the
+ * phase kept as a 64-bit fraction of a turn, so it is exact for any position),
+ * write q to q_out, and k and v into the cache: rounded to nearest even in
+ * bf16, or divided by their scale and rounded to e4m3, saturating at +-448.
+ * A token whose sequence, page or position is outside block_table, or whose
+ * page id is outside the pool, is not cached and sets a bit for moe_kv_health.
+ * Two tokens of one call must not share a slot. */
+moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* stream);
+
+/* Attention of one new token per sequence over the cache (formulas above):
+ * fp32 scores, softmax statistics and sums. The length is read on the device
+ * (no host synchronisation, capturable in a graph). The work is split evenly
+ * over the GPU by cached tokens and joined in a fixed order, so results are
+ * bit-reproducible. A length past the block table is cut to it and an attended
+ * page id outside the pool is skipped; both set a bit for moe_kv_health. */
+moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* stream);
+
+/* The argument checks of the two calls alone (host only, no device). */
+moe_status moe_kv_append_check(const moe_kv_desc* desc, const moe_kv_append_args* args);
+moe_status moe_kv_attend_check(const moe_kv_desc* desc, const moe_kv_attend_args* args);
+
+/* Host only: where (seq, position) lives, with block_table as host memory
+ * [n_seqs][max_pages]; *offset receives the element offset of kv head `head`'s
+ * row in a pool. MOE_E_STATE when moe_kv_append would refuse the token (bits:
+ * the health bit it would set). The kernels use the same arithmetic. */
+moe_status moe_kv_locate(const moe_kv_desc* desc, const int32_t* block_table, int32_t n_seqs, int32_t max_pages,
+                         int32_t seq, int32_t position, int32_t head, int64_t* offset, uint32_t* bits);
+
+/* Wait for the handle's device work, then report what its kernels refused
+ * since the last call: MOE_E_STATE with the bits below, MOE_OK otherwise. */
+enum {
+    MOE_KV_BAD_SEQ = 1,     /* append: a sequence index outside block_table */
+    MOE_KV_BAD_LENGTH = 2,  /* a position or length past max_pages * page_size */
+    MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
+    MOE_KV_TIMEOUT = 8      /* a bounded wait inside moe_kv_attend ran out */
+};
+moe_status moe_kv_health(moe_kv* kv, uint32_t* bits);
 
 /* ---- errors ----------------------------------------------------------------- */
 

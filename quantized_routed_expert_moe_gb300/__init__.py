@@ -19,7 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libmoe_gb300.so")
 
 MOE_ABI_VERSION = 1
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_E4M3 = 0, 1, 2
 MOE_W_F32, MOE_W_Q8G64, MOE_W_Q4G64, MOE_W_Q2G64 = 0, 1, 2, 3
 STATUS = {0: "MOE_OK", 1: "MOE_E_INVALID", 2: "MOE_E_UNSUPPORTED", 3: "MOE_E_NOMEM",
           4: "MOE_E_CUDA", 5: "MOE_E_TIMEOUT", 6: "MOE_E_STATE", 7: "MOE_E_SOURCE"}
@@ -29,6 +29,8 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_expert_record_bytes", "
            "moe_layer_device_bytes", "moe_layer_set_next", "moe_layer_set_router_scoring", "moe_route", "moe_layer_selection", "moe_decode", "moe_decode_static_scratch", "moe_prefill_chunk",
            "moe_decode_tokens_host", "moe_cache_stage", "moe_cache_prefetch", "moe_cache_prefetch_stats", "moe_cache_stats", "moe_cache_residency", "moe_cache_usage", "moe_cache_pin", "moe_hottest", "moe_cache_pin_hottest", "moe_lfu_trace", "moe_lfu_trace_pinned",
            "moe_profile_start", "moe_profile_stop", "moe_layer_set_option", "moe_layer_check", "moe_trace_read_split",
+           "moe_block_norm", "moe_block_norm_check", "moe_kv_create", "moe_kv_destroy", "moe_kv_device_bytes", "moe_kv_append", "moe_kv_attend",
+           "moe_kv_append_check", "moe_kv_attend_check", "moe_kv_locate", "moe_kv_health",
            "moe_status_str", "moe_last_error")
 
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
@@ -36,6 +38,7 @@ MOE_STATIC_SCRATCH_BYTES = 256 * 1024
 MOE_OPT_TEST_STALL_SHARED, MOE_OPT_TRACE = 2, 3
 MOE_OPT_HOST_TIMEOUT_MS, MOE_OPT_TEST_STALL_COPIES_MS, MOE_OPT_CACHE_DEVICE = 4, 5, 6
 MOE_MAX_TOP_K = 8
+MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT = 1, 2, 4, 8
 
 
 class MoEError(RuntimeError):
@@ -66,6 +69,36 @@ class moe_layer_desc(ctypes.Structure):
 class moe_cache_stats_t(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_uint64), ("hits", ctypes.c_uint64), ("misses", ctypes.c_uint64),
                 ("bytes_h2d", ctypes.c_uint64), ("stage_ns", ctypes.c_uint64)]
+
+
+class moe_block_norm_desc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("hidden", ctypes.c_int32), ("res_dtype", ctypes.c_int32),
+                ("block_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("res_scale", ctypes.c_float), ("weight_offset", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("o_stride", ctypes.c_int64), ("gate_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64),
+                ("h_stride", ctypes.c_int64)]
+
+
+class moe_kv_desc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("n_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+                ("cache_dtype", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("rotary_adjacent", ctypes.c_int32),
+                ("max_batch", ctypes.c_int32), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64)]
+
+
+class moe_kv_append_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64), ("positions", ctypes.c_void_p),
+                ("seq", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("T", ctypes.c_int32),
+                ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("q_out", ctypes.c_void_p)]
+
+
+class moe_kv_attend_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("block_table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
+                ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
 
 
 class moe_kernel_time(ctypes.Structure):
@@ -150,6 +183,31 @@ def lib() -> ctypes.CDLL:
             L.moe_layer_selection.argtypes = [vp, i32, vp, vp, vp]
             L.moe_trace_read_split.restype = st
             L.moe_trace_read_split.argtypes = [vp, vp, i32]
+            nd, kd = ctypes.POINTER(moe_block_norm_desc), ctypes.POINTER(moe_kv_desc)
+            ap, at = ctypes.POINTER(moe_kv_append_args), ctypes.POINTER(moe_kv_attend_args)
+            L.moe_block_norm.restype = st
+            L.moe_block_norm.argtypes = [nd, vp, vp, vp, vp, vp, vp, vp, i32, i32, vp]
+            L.moe_block_norm_check.restype = st
+            L.moe_block_norm_check.argtypes = [nd, vp, vp, vp, vp, vp, vp, vp, i32]
+            L.moe_kv_create.restype = st
+            L.moe_kv_create.argtypes = [kd, vp, vp, vp, vp, vp, i32, ctypes.POINTER(vp)]
+            L.moe_kv_destroy.restype = None
+            L.moe_kv_destroy.argtypes = [vp]
+            L.moe_kv_device_bytes.restype = sz
+            L.moe_kv_device_bytes.argtypes = [vp]
+            L.moe_kv_append.restype = st
+            L.moe_kv_append.argtypes = [vp, ap, vp]
+            L.moe_kv_attend.restype = st
+            L.moe_kv_attend.argtypes = [vp, at, vp]
+            L.moe_kv_append_check.restype = st
+            L.moe_kv_append_check.argtypes = [kd, ap]
+            L.moe_kv_attend_check.restype = st
+            L.moe_kv_attend_check.argtypes = [kd, at]
+            L.moe_kv_locate.restype = st
+            L.moe_kv_locate.argtypes = [kd, vp, i32, i32, i32, i32, i32, ctypes.POINTER(ctypes.c_int64),
+                                        ctypes.POINTER(ctypes.c_uint32)]
+            L.moe_kv_health.restype = st
+            L.moe_kv_health.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
             L.moe_status_str.restype = ctypes.c_char_p
             L.moe_status_str.argtypes = [st]
             L.moe_last_error.restype = ctypes.c_char_p
@@ -417,6 +475,73 @@ def moe_layer_selection(handle, T, ids, w, stream=None):
     _check(lib().moe_layer_selection(handle, T, _addr(ids), _addr(w), _stream(stream)), "moe_layer_selection")
 
 
+# ---------------------------------------------------------------------------
+# the rest of a decoder layer: block norms, paged key-value cache
+# ---------------------------------------------------------------------------
+
+def moe_block_norm(desc, x, o, gate, w_post, w_pre, r, h, T, device=0, stream=None) -> None:
+    _check(lib().moe_block_norm(ctypes.byref(desc), _addr(x), _addr(o), _addr(gate), _addr(w_post), _addr(w_pre),
+                                _addr(r), _addr(h), T, device, _stream(stream)), "moe_block_norm")
+
+
+def moe_block_norm_check(desc, x, o, gate, w_post, w_pre, r, h, T) -> None:
+    """The argument checks of moe_block_norm alone (host only)."""
+    _check(lib().moe_block_norm_check(ctypes.byref(desc), _addr(x), _addr(o), _addr(gate), _addr(w_post),
+                                      _addr(w_pre), _addr(r), _addr(h), T), "moe_block_norm_check")
+
+
+def moe_kv_create(desc, k_pages, v_pages, inv_freq=None, k_scale=None, v_scale=None, device: int = 0) -> int:
+    """Create a cache handle over two borrowed page pools; inv_freq float64 and
+    the scales float32 are host arrays, copied."""
+    out = ctypes.c_void_p()
+    _check(lib().moe_kv_create(ctypes.byref(desc), _addr(k_pages), _addr(v_pages), _addr(inv_freq), _addr(k_scale),
+                               _addr(v_scale), device, ctypes.byref(out)), "moe_kv_create")
+    return out.value
+
+
+def moe_kv_destroy(handle) -> None:
+    lib().moe_kv_destroy(handle)
+
+
+def moe_kv_device_bytes(handle) -> int:
+    return int(lib().moe_kv_device_bytes(handle))
+
+
+def moe_kv_append(handle, args: moe_kv_append_args, stream=None) -> None:
+    _check(lib().moe_kv_append(handle, ctypes.byref(args), _stream(stream)), "moe_kv_append")
+
+
+def moe_kv_attend(handle, args: moe_kv_attend_args, stream=None) -> None:
+    _check(lib().moe_kv_attend(handle, ctypes.byref(args), _stream(stream)), "moe_kv_attend")
+
+
+def moe_kv_append_check(desc, args) -> None:
+    """The argument checks of moe_kv_append alone (host only)."""
+    _check(lib().moe_kv_append_check(ctypes.byref(desc), ctypes.byref(args)), "moe_kv_append_check")
+
+
+def moe_kv_attend_check(desc, args) -> None:
+    """The argument checks of moe_kv_attend alone (host only)."""
+    _check(lib().moe_kv_attend_check(ctypes.byref(desc), ctypes.byref(args)), "moe_kv_attend_check")
+
+
+def moe_kv_locate(desc, block_table, seq: int, position: int, head: int = 0) -> int:
+    """Element offset of a cached row in a pool; block_table: host int32 [n_seqs][max_pages]."""
+    import numpy as np
+    t = np.ascontiguousarray(block_table, dtype=np.int32)
+    off, bits = ctypes.c_int64(), ctypes.c_uint32()
+    _check(lib().moe_kv_locate(ctypes.byref(desc), t.ctypes.data, t.shape[0], t.shape[1], seq, position, head,
+                               ctypes.byref(off), ctypes.byref(bits)), "moe_kv_locate")
+    return off.value
+
+
+def moe_kv_health(handle) -> tuple[int, int]:
+    """(status, health bits) of what the handle's kernels refused since the last call."""
+    bits = ctypes.c_uint32()
+    st = lib().moe_kv_health(handle, ctypes.byref(bits))
+    return st, bits.value
+
+
 MOE_TRACE_MAX_CTAS = 1024
 MOE_TRACE_KERNELS = 5
 SPLIT_TRACE_KERNELS = ("router", "gateup", "down", "prefill_gemm_gateup", "prefill_gemm_down")
@@ -527,3 +652,172 @@ class MoELayer:
     @property
     def device_bytes(self):
         return moe_layer_device_bytes(self.handle)
+
+
+def _dtype_id(t) -> int:
+    name = str(t.dtype).rsplit(".", 1)[-1]
+    ids = {"float32": MOE_F32, "bfloat16": MOE_BF16, "float8_e4m3fn": MOE_E4M3}
+    if name not in ids:
+        raise TypeError(f"no moe_dtype for {t.dtype}")
+    return ids[name]
+
+
+def _want(t, name: str, shape, dtype: str, device=None, inner=None):
+    """Reject a tensor of another shape, type or device before its address is
+    taken; the last `inner` dimensions must be contiguous (None: all)."""
+    if tuple(t.shape) != tuple(shape) or str(t.dtype) != f"torch.{dtype}":
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
+    step = 1
+    for d in reversed(range(len(shape) - (len(shape) if inner is None else inner), len(shape))):
+        if shape[d] != 1 and t.stride(d) != step:
+            raise ValueError(f"{name}: its last dimensions must be contiguous, strides are {tuple(t.stride())}")
+        step *= shape[d]
+    return t
+
+
+def _row_stride(t, width: int) -> int:
+    """Elements between rows of a [rows, ...] tensor (a single row has no stride of its own)."""
+    return t.stride(0) if t.shape[0] > 1 else width
+
+
+class BlockNorm:
+    """The norms between two blocks of a decoder layer (moe_block_norm): keeps
+    the weights, fp32 [hidden] on the device; w_post and w_pre may be None."""
+
+    def __init__(self, hidden: int, w_post=None, w_pre=None, eps: float = 1e-6, scale: float = 1.0,
+                 weight_offset: float = 0.0):
+        self.hidden, self.eps, self.scale, self.weight_offset = hidden, eps, scale, weight_offset
+        for name, w in (("w_post", w_post), ("w_pre", w_pre)):
+            if w is not None:
+                _want(w, name, (hidden,), "float32")
+        self.w_post, self.w_pre = w_post, w_pre
+
+    def run(self, x, o=None, r=None, h=None, gate=None, stream=None):
+        """x [T, H] residual, o [T, H] the block's output or None, r [T, H]
+        (may be x) and h [T, H] the outputs (either may be None), gate [T, H],
+        [1, H] or [H] of o's type."""
+        H = self.hidden
+        if x.dim() != 2 or x.device.type != "cuda":
+            raise ValueError("x must be a CUDA tensor [T, hidden]")
+        T, dev = x.shape[0], x.device
+
+        def rows(t, name, like=None):
+            if t is None:
+                return 0
+            _want(t, name, (T, H), str((t if like is None else like).dtype)[6:], dev, 1)
+            return _row_stride(t, H)
+
+        for w in (self.w_post, self.w_pre):
+            if w is not None and w.device != dev:
+                raise ValueError(f"the norm's weights are on {w.device}, x on {dev}")
+        gs = 0
+        if gate is not None:
+            if o is None:
+                raise ValueError("gate needs o")
+            if gate.dim() == 1 or (gate.shape[0] == 1 and T != 1):
+                _want(gate.reshape(-1), "gate", (H,), str(o.dtype)[6:], dev)
+            else:
+                gs = rows(gate, "gate", o)
+        desc = moe_block_norm_desc(MOE_ABI_VERSION, H, _dtype_id(x), _dtype_id(o) if o is not None else MOE_BF16,
+                                   _dtype_id(h) if h is not None else MOE_BF16, self.eps, self.scale,
+                                   self.weight_offset, rows(x, "x"), rows(o, "o"), gs, rows(r, "r", x), rows(h, "h"))
+        moe_block_norm(desc, x, o, gate, self.w_post if o is not None else None,
+                       self.w_pre if h is not None else None, r, h, T, dev.index or 0, stream)
+
+
+class KVCache:
+    """Owns one cache handle over two page pools, tensors [n_pages, n_kv_heads,
+    page_size, head_dim] of bfloat16 or float8_e4m3fn in any memory order whose
+    last dimension is contiguous (token-major pages: a permuted view)."""
+
+    def __init__(self, k_pages, v_pages, n_heads: int, inv_freq=None, interleaved: bool = False, k_scale=None,
+                 v_scale=None, max_batch: int = 1):
+        import numpy as np
+        n_pages, hk, page, d = k_pages.shape
+        if k_pages.device.type != "cuda" or v_pages.device != k_pages.device:
+            raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
+        if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride() or v_pages.dtype != k_pages.dtype:
+            raise ValueError("k_pages and v_pages must have one shape, type and memory order")
+        if k_pages.stride(3) != 1:
+            raise ValueError("the last dimension of the pools must be contiguous")
+        freq = None if inv_freq is None else np.ascontiguousarray(inv_freq, dtype=np.float64)
+        scales = [None if s is None else np.ascontiguousarray(s, dtype=np.float32) for s in (k_scale, v_scale)]
+        for s in scales:
+            if s is not None and s.shape != (hk,):
+                raise ValueError("k_scale and v_scale hold one value per key-value head")
+        self.k_pages, self.v_pages = k_pages, v_pages
+        self.desc = moe_kv_desc(MOE_ABI_VERSION, n_heads, hk, d, page, n_pages, _dtype_id(k_pages),
+                                0 if freq is None else 2 * freq.size, int(interleaved), max_batch,
+                                k_pages.stride(0), k_pages.stride(1), k_pages.stride(2))
+        self.handle = moe_kv_create(self.desc, k_pages, v_pages, freq if freq is None or freq.size else None,
+                                    scales[0], scales[1], k_pages.device.index or 0)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            moe_kv_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *a):
+        self.close()
+
+    def append(self, q, k, v, positions, block_table, q_out=None, seq=None, stream=None):
+        """Rotate and cache T tokens: q [T, n_heads, d] (or None with q_out), k
+        and v [T, n_kv_heads, d], positions and seq int32 [T], block_table int32
+        [n_seqs, max_pages]."""
+        d, dev = self.desc, self.k_pages.device
+        T, hk, hq, dim = k.shape[0], d.n_kv_heads, d.n_heads, d.head_dim
+        _want(k, "k", (T, hk, dim), "bfloat16", dev, 2)
+        _want(v, "v", (T, hk, dim), "bfloat16", dev, 2)
+        if q is not None:
+            _want(q, "q", (T, hq, dim), "bfloat16", dev, 2)
+        if q_out is not None:
+            _want(q_out, "q_out", (T, hq, dim), "bfloat16", dev)
+        _want(positions, "positions", (T,), "int32", dev)
+        if seq is not None:
+            _want(seq, "seq", (T,), "int32", dev)
+        _want(block_table, "block_table", tuple(block_table.shape), "int32", dev)
+        n_seqs, max_pages = block_table.shape
+        args = moe_kv_append_args(_addr(q), _addr(k), _addr(v), 0 if q is None else _row_stride(q, hq * dim),
+                                  _row_stride(k, hk * dim), _row_stride(v, hk * dim), _addr(positions), _addr(seq),
+                                  _addr(block_table), T, n_seqs, max_pages, _addr(q_out))
+        moe_kv_append(self.handle, args, stream)
+
+    def attend(self, q, block_table, lens, out, lse=None, scale=None, softcap: float = 0.0, window: int = 0,
+               stream=None):
+        """Attention of one new token per sequence: q and out [B, n_heads, d]
+        bf16, lens int32 [B], block_table int32 [B, max_pages], lse fp32
+        [B, n_heads] or None; scale defaults to 1 / sqrt(d)."""
+        d, dev = self.desc, self.k_pages.device
+        B = q.shape[0]
+        _want(q, "q", (B, d.n_heads, d.head_dim), "bfloat16", dev, 2)
+        _want(out, "out", (B, d.n_heads, d.head_dim), "bfloat16", dev)
+        _want(lens, "lens", (B,), "int32", dev)
+        _want(block_table, "block_table", (B, block_table.shape[1]), "int32", dev)
+        if lse is not None:
+            _want(lse, "lse", (B, d.n_heads), "float32", dev)
+        args = moe_kv_attend_args(_addr(q), _row_stride(q, d.n_heads * d.head_dim), _addr(block_table), _addr(lens), B,
+                                  block_table.shape[1], d.head_dim ** -0.5 if scale is None else scale, softcap,
+                                  window, _addr(out), _addr(lse))
+        moe_kv_attend(self.handle, args, stream)
+
+    def locate(self, block_table, seq: int, position: int, head: int = 0) -> int:
+        """Element offset of a cached row in a pool (block_table on the host)."""
+        return moe_kv_locate(self.desc, block_table, seq, position, head)
+
+    def health(self):
+        return moe_kv_health(self.handle)
+
+    @property
+    def device_bytes(self):
+        return moe_kv_device_bytes(self.handle)

@@ -1,0 +1,433 @@
+// Paged key-value cache: handle, argument checks, and the append with the
+// position rotation on the way.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+#include <string>
+#include <vector>
+
+#include "kv_cache.h"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+moe_status check_desc(const moe_kv_desc* d) {
+    if (!d) return fail(MOE_E_INVALID, "desc is NULL");
+    if (d->abi_version != MOE_ABI_VERSION) return fail(MOE_E_INVALID, "abi_version mismatch");
+    if (d->n_kv_heads < 1 || d->n_kv_heads > 256) return fail(MOE_E_INVALID, "n_kv_heads must be in 1..256");
+    if (d->n_heads < 1 || d->n_heads > 4096 || d->n_heads % d->n_kv_heads)
+        return fail(MOE_E_INVALID, "n_heads must be a positive multiple of n_kv_heads, at most 4096");
+    if (d->head_dim != 64 && d->head_dim != 128 && d->head_dim != 256)
+        return fail(MOE_E_UNSUPPORTED, "head_dim must be 64, 128 or 256");
+    if (d->page_size < 16 || d->page_size > 4096 || d->page_size % 16)
+        return fail(MOE_E_UNSUPPORTED, "page_size must be a multiple of 16 in 16..4096");
+    if (d->n_pages < 1) return fail(MOE_E_INVALID, "n_pages must be positive");
+    if (d->cache_dtype != MOE_BF16 && d->cache_dtype != MOE_E4M3)
+        return fail(MOE_E_UNSUPPORTED, "cache_dtype must be MOE_BF16 or MOE_E4M3");
+    if (d->rotary_dim < 0 || d->rotary_dim % 16 || d->rotary_dim > d->head_dim)
+        return fail(MOE_E_INVALID, "rotary_dim must be 0 or a multiple of 16, at most head_dim");
+    if (d->rotary_adjacent != 0 && d->rotary_adjacent != 1) return fail(MOE_E_INVALID, "rotary_adjacent must be 0 or 1");
+    if (d->max_batch < 1 || d->max_batch > 1024) return fail(MOE_E_INVALID, "max_batch must be in 1..1024");
+    // the rows of a page, in either order, without overlap: the smaller of the
+    // two inner strides steps over rows, the larger over all of the smaller's
+    const int64_t step = d->cache_dtype == MOE_E4M3 ? 16 : 8;
+    const int64_t D = d->head_dim, H = d->n_kv_heads, P = d->page_size;
+    for (int64_t st : {d->page_stride, d->head_stride, d->token_stride})
+        if (st < D || st % step || st > ((int64_t)1 << 38))
+            return fail(MOE_E_INVALID, "strides must be multiples of 16 bytes, at least head_dim and at most 2^38");
+    const bool head_major = d->head_stride >= d->token_stride;
+    const int64_t inner = head_major ? d->token_stride * P : d->head_stride * H;
+    const int64_t outer = head_major ? d->head_stride * H : d->token_stride * P;
+    if ((head_major ? d->head_stride : d->token_stride) < inner || d->page_stride < outer) {
+        // a dimension of one row needs no room of its own
+        const bool one = head_major ? H == 1 : P == 1;
+        if (!(one && d->page_stride >= inner)) return fail(MOE_E_INVALID, "rows of a page overlap");
+    }
+    return MOE_OK;
+}
+
+KvShape shape_of(const moe_kv_desc& d) {
+    KvShape s{};
+    s.n_heads = d.n_heads;
+    s.n_kv_heads = d.n_kv_heads;
+    s.head_dim = d.head_dim;
+    s.page_size = d.page_size;
+    s.n_pages = d.n_pages;
+    s.rotary_dim = d.rotary_dim;
+    s.rotary_adjacent = d.rotary_adjacent;
+    s.e4m3 = d.cache_dtype == MOE_E4M3;
+    s.page_stride = d.page_stride;
+    s.head_stride = d.head_stride;
+    s.token_stride = d.token_stride;
+    return s;
+}
+
+moe_status check_table(const int32_t* table, int n_seqs, int max_pages, int page_size) {
+    if (!table) return fail(MOE_E_INVALID, "block_table is NULL");
+    if (n_seqs < 1) return fail(MOE_E_INVALID, "n_seqs must be positive");
+    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX)
+        return fail(MOE_E_INVALID, "max_pages must be positive, and max_pages * page_size below 2^31");
+    return MOE_OK;
+}
+
+moe_status check_append(const moe_kv_desc* d, const moe_kv_append_args* a) {
+    moe_status st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!a) return fail(MOE_E_INVALID, "args is NULL");
+    if (a->T < 0) return fail(MOE_E_INVALID, "T must not be negative");
+    if (a->T == 0) return MOE_OK;
+    if (!a->k || !a->v || !a->positions) return fail(MOE_E_INVALID, "k, v or positions is NULL");
+    if (!a->q != !a->q_out) return fail(MOE_E_INVALID, "q and q_out go together");
+    st = check_table(a->block_table, a->n_seqs, a->max_pages, d->page_size);
+    if (st != MOE_OK) return st;
+    if (!a->seq && a->T > a->n_seqs) return fail(MOE_E_INVALID, "T exceeds n_seqs, and seq is NULL");
+    for (const void* p : {a->q, a->k, a->v, static_cast<const void*>(a->q_out)})
+        if (!aligned16(p)) return fail(MOE_E_INVALID, "q, k, v and q_out must be 16-byte aligned");
+    const int64_t D = d->head_dim;
+    if (a->k_stride % 8 || a->v_stride % 8 || a->k_stride < D * d->n_kv_heads || a->v_stride < D * d->n_kv_heads ||
+        (a->q && (a->q_stride % 8 || a->q_stride < D * d->n_heads)))
+        return fail(MOE_E_INVALID, "token strides must be multiples of 8 and cover a token's heads");
+    if (a->q && a->q_out == a->q && a->q_stride != D * d->n_heads && a->T > 1)
+        return fail(MOE_E_INVALID, "q_out may be q only where q is contiguous");
+    return MOE_OK;
+}
+
+moe_status check_attend(const moe_kv_desc* d, const moe_kv_attend_args* a) {
+    moe_status st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!a) return fail(MOE_E_INVALID, "args is NULL");
+    if (a->B < 0 || a->B > d->max_batch) return fail(MOE_E_INVALID, "B must be in 0..max_batch");
+    if (!std::isfinite(a->scale)) return fail(MOE_E_INVALID, "scale must be finite");
+    if (!std::isfinite(a->softcap) || a->softcap < 0) return fail(MOE_E_INVALID, "softcap must be finite and >= 0");
+    if (a->window < 0) return fail(MOE_E_INVALID, "window must be >= 0");
+    if (a->B == 0) return MOE_OK;
+    if (!a->q || !a->lens || !a->out) return fail(MOE_E_INVALID, "q, lens or out is NULL");
+    st = check_table(a->block_table, a->B, a->max_pages, d->page_size);
+    if (st != MOE_OK) return st;
+    if (!aligned16(a->q) || !aligned16(a->out)) return fail(MOE_E_INVALID, "q and out must be 16-byte aligned");
+    if (a->q_stride % 8 || a->q_stride < (int64_t)d->head_dim * d->n_heads)
+        return fail(MOE_E_INVALID, "q_stride must be a multiple of 8 and cover the heads");
+    return MOE_OK;
+}
+
+// ---- append ---------------------------------------------------------------------
+//
+// A head is D / 16 groups of 16 channels, two 16-byte vectors each: a rotated
+// group holds 8 pairs (channels 8g.. and rotary_dim / 2 + 8g.., or the 8 adjacent
+// pairs from 16g), a group past rotary_dim is copied. One thread moves one group
+// of one head of one token and reads both vectors before it writes, so q may be
+// rotated in place.
+//
+// The angle p * inv_freq is kept as a 64-bit fraction of a turn: turns =
+// frac(inv_freq / 2 pi) * 2^64, and p * turns mod 2^64 is the exact phase of
+// any position, where a 32-bit product loses the phase from 10^5 or so. The
+// upper 32 bits (2^-32 of a turn) go to sincospif.
+
+struct Vec8 {
+    float v[8];
+};
+
+__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    Vec8 r;
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        r.v[2 * i] = __uint_as_float(w[i] << 16);
+        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const Vec8& r) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]),
+                                              pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7]));
+}
+
+// e4m3 of r / scale: a true division, so that the value stored is the nearest
+// one to the quotient; saturating, NaN stays NaN.
+__device__ __forceinline__ void store8(uint8_t* p, const Vec8& r, float scale) {
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(r.v[4 * i], scale), __fdiv_rn(r.v[4 * i + 1], scale)), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(__fdiv_rn(r.v[4 * i + 2], scale), __fdiv_rn(r.v[4 * i + 3], scale)), __NV_SATFINITE, __NV_E4M3);
+        w[i] = lo | hi << 16;
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+__device__ __forceinline__ void phase(uint64_t turns, int position, float& c, float& s) {
+    const uint64_t ph = turns * (uint64_t)position;
+    sincospif((float)(int32_t)(ph >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+}
+
+struct AppendArgs {
+    moe_kv_append_args a;
+    KvShape s;
+    void *k_pages, *v_pages;
+    const uint64_t* turns;
+    const float *k_scale, *v_scale;
+    unsigned* health;
+};
+
+__global__ void __launch_bounds__(256) k_kv_append(const AppendArgs p) {
+    const KvShape& s = p.s;
+    const int groups = s.head_dim / 16;
+    const int q_heads = p.a.q ? s.n_heads : 0;
+    const int heads = q_heads + 2 * s.n_kv_heads;
+    const int64_t total = (int64_t)p.a.T * heads * groups;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
+        const int g = (int)(i % groups);
+        const int64_t th = i / groups;
+        const int head = (int)(th % heads);
+        const int t = (int)(th / heads);
+        const int pos = p.a.positions[t];
+        const bool is_q = head < q_heads;
+        const bool is_v = head >= q_heads + s.n_kv_heads;
+        const int hk = is_v ? head - q_heads - s.n_kv_heads : head - q_heads;
+        const bool turned = !is_v && 16 * g < s.rotary_dim;
+        // channels of the group's two vectors
+        const int c0 = turned && !s.rotary_adjacent ? 8 * g : 16 * g;
+        const int c1 = turned && !s.rotary_adjacent ? s.rotary_dim / 2 + 8 * g : 16 * g + 8;
+        const __nv_bfloat16* src =
+            is_q ? static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)t * p.a.q_stride + (int64_t)head * s.head_dim
+            : is_v ? static_cast<const __nv_bfloat16*>(p.a.v) + (int64_t)t * p.a.v_stride + (int64_t)hk * s.head_dim
+                   : static_cast<const __nv_bfloat16*>(p.a.k) + (int64_t)t * p.a.k_stride + (int64_t)hk * s.head_dim;
+        Vec8 a{}, b{};
+        if (pos >= 0) {
+            a = load8(src + c0);
+            b = load8(src + c1);
+            if (turned) {
+                if (s.rotary_adjacent) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float c, sn;
+                        phase(p.turns[8 * g + j], pos, c, sn);
+                        float* v = j < 4 ? a.v : b.v;
+                        const float x = v[2 * (j & 3)], y = v[2 * (j & 3) + 1];
+                        v[2 * (j & 3)] = x * c - y * sn;
+                        v[2 * (j & 3) + 1] = y * c + x * sn;
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float c, sn;
+                        phase(p.turns[8 * g + j], pos, c, sn);
+                        const float x = a.v[j], y = b.v[j];
+                        a.v[j] = x * c - y * sn;
+                        b.v[j] = y * c + x * sn;
+                    }
+                }
+            }
+        }
+        if (is_q) {
+            __nv_bfloat16* dst =
+                static_cast<__nv_bfloat16*>(p.a.q_out) + ((int64_t)t * s.n_heads + head) * s.head_dim;
+            store8(dst + c0, a);
+            store8(dst + c1, b);
+            continue;
+        }
+        if (pos < 0) continue;
+        uint32_t bits = 0;
+        const int page = kv_page(s, p.a.block_table, p.a.n_seqs, p.a.max_pages, p.a.seq ? p.a.seq[t] : t, pos, bits);
+        if (page < 0) {
+            if (g == 0) atomicOr(p.health, bits);
+            continue;
+        }
+        const int64_t off = kv_offset(s, page, hk, pos % s.page_size);
+        void* pool = is_v ? p.v_pages : p.k_pages;
+        if (s.e4m3) {
+            const float sc = (is_v ? p.v_scale : p.k_scale)[hk];
+            store8(static_cast<uint8_t*>(pool) + off + c0, a, sc);
+            store8(static_cast<uint8_t*>(pool) + off + c1, b, sc);
+        } else {
+            store8(static_cast<__nv_bfloat16*>(pool) + off + c0, a);
+            store8(static_cast<__nv_bfloat16*>(pool) + off + c1, b);
+        }
+    }
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_kv_append_check(const moe_kv_desc* desc, const moe_kv_append_args* args) {
+    return check_append(desc, args);
+}
+
+moe_status moe_kv_attend_check(const moe_kv_desc* desc, const moe_kv_attend_args* args) {
+    return check_attend(desc, args);
+}
+
+moe_status moe_kv_locate(const moe_kv_desc* desc, const int32_t* block_table, int32_t n_seqs, int32_t max_pages,
+                         int32_t seq, int32_t position, int32_t head, int64_t* offset, uint32_t* bits) {
+    moe_status st = check_desc(desc);
+    if (st != MOE_OK) return st;
+    st = check_table(block_table, n_seqs, max_pages, desc->page_size);
+    if (st != MOE_OK) return st;
+    if (!offset) return fail(MOE_E_INVALID, "offset is NULL");
+    if (head < 0 || head >= desc->n_kv_heads) return fail(MOE_E_INVALID, "head outside 0..n_kv_heads-1");
+    const KvShape s = shape_of(*desc);
+    uint32_t b = 0;
+    const int page = kv_page(s, block_table, n_seqs, max_pages, seq, position, b);
+    if (bits) *bits = b;
+    if (page < 0) return fail(MOE_E_STATE, "the position has no slot (health bits " + std::to_string(b) + ")");
+    *offset = kv_offset(s, page, head, position % s.page_size);
+    return MOE_OK;
+}
+
+moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, const double* inv_freq,
+                         const float* k_scale, const float* v_scale, int32_t device, moe_kv** out) {
+    if (!out) return fail(MOE_E_INVALID, "out is NULL");
+    *out = nullptr;
+    moe_status st = check_desc(desc);
+    if (st != MOE_OK) return st;
+    if (!k_pages || !v_pages || !aligned16(k_pages) || !aligned16(v_pages))
+        return fail(MOE_E_INVALID, "k_pages and v_pages must be non-NULL and 16-byte aligned");
+    const int half = desc->rotary_dim / 2, Hk = desc->n_kv_heads;
+    if (half && !inv_freq) return fail(MOE_E_INVALID, "inv_freq is required where rotary_dim > 0");
+    for (int i = 0; i < half; ++i)
+        if (!std::isfinite(inv_freq[i])) return fail(MOE_E_INVALID, "inv_freq must be finite");
+    const bool e4m3 = desc->cache_dtype == MOE_E4M3;
+    if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr))
+        return fail(MOE_E_INVALID, "k_scale and v_scale go with an e4m3 cache, and only with it");
+    for (int h = 0; e4m3 && h < Hk; ++h)
+        if (!(std::isfinite(k_scale[h]) && k_scale[h] > 0 && std::isfinite(v_scale[h]) && v_scale[h] > 0))
+            return fail(MOE_E_INVALID, "k_scale and v_scale must be finite and positive");
+
+    DeviceGuard g(device);
+    if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
+    moe_kv* kv = new (std::nothrow) moe_kv();
+    if (!kv) return fail(MOE_E_NOMEM, "host memory");
+    Kv& K = kv->K;
+    K.d = *desc;
+    K.s = shape_of(*desc);
+    K.device = device;
+    K.k_pages = k_pages;
+    K.v_pages = v_pages;
+    auto bail = [&](moe_status s) {
+        std::string m = moe_last_error();
+        moe_kv_destroy(kv);
+        return fail(s, m);
+    };
+    cudaError_t e = cudaDeviceGetAttribute(&K.num_sms, cudaDevAttrMultiProcessorCount, device);
+    if (e != cudaSuccess) return bail(cuda_fail(e, "cudaDeviceGetAttribute"));
+
+    size_t need = 0;
+    auto add = [&](size_t b) {
+        const size_t off = need;
+        need += (b + 255) / 256 * 256;
+        return off;
+    };
+    const size_t o_turns = add((size_t)std::max(half, 1) * 8), o_ks = add((size_t)Hk * 4), o_vs = add((size_t)Hk * 4),
+                 o_health = add(4);
+    size_t free_b = 0, total_b = 0;
+    e = cudaMemGetInfo(&free_b, &total_b);
+    if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemGetInfo"));
+    if (need > free_b) return bail(fail(MOE_E_NOMEM, "the workspace does not fit in free device memory"));
+    e = cudaMalloc(&K.block, need);
+    if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMalloc"));
+    K.device_bytes = need;
+    uint8_t* base = static_cast<uint8_t*>(K.block);
+    K.turns = reinterpret_cast<uint64_t*>(base + o_turns);
+    K.k_scale = reinterpret_cast<float*>(base + o_ks);
+    K.v_scale = reinterpret_cast<float*>(base + o_vs);
+    K.health = reinterpret_cast<unsigned*>(base + o_health);
+
+    // inv_freq / 2 pi in double keeps 2^-53 of a turn per position; its fraction
+    // times 2^64 is rounded to an integer
+    std::vector<uint64_t> turns(std::max(half, 1), 0);
+    for (int i = 0; i < half; ++i) {
+        const double t = inv_freq[i] / 6.283185307179586476925287;
+        const double f = t - std::floor(t);
+        turns[i] = f >= 1.0 ? 0 : (uint64_t)std::ldexp(f, 64);
+    }
+    std::vector<float> ks(Hk, 1.0f), vs(Hk, 1.0f);
+    if (e4m3) {
+        ks.assign(k_scale, k_scale + Hk);
+        vs.assign(v_scale, v_scale + Hk);
+    }
+    e = cudaMemset(K.block, 0, need);
+    if (e == cudaSuccess) e = cudaMemcpy(K.turns, turns.data(), turns.size() * 8, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(K.k_scale, ks.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(K.v_scale, vs.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
+    // the set-up ran on the legacy stream: finish it before any other stream may run a call
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) return bail(cuda_fail(e, "moe_kv_create set-up"));
+    *out = kv;
+    return MOE_OK;
+}
+
+void moe_kv_destroy(moe_kv* kv) {
+    if (!kv) return;
+    DeviceGuard g(kv->K.device);
+    if (kv->K.block) {
+        cudaDeviceSynchronize();
+        cudaFree(kv->K.block);
+    }
+    delete kv;
+}
+
+size_t moe_kv_device_bytes(const moe_kv* kv) { return kv ? kv->K.device_bytes : 0; }
+
+moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* stream) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    Kv& K = kv->K;
+    moe_status st = check_append(&K.d, args);
+    if (st != MOE_OK) return st;
+    if (args->T == 0) return MOE_OK;
+    DeviceGuard g(K.device);
+    if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
+    const AppendArgs p{*args, K.s, K.k_pages, K.v_pages, K.turns, K.k_scale, K.v_scale, K.health};
+    const int64_t total =
+        (int64_t)args->T * ((args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads) * (K.s.head_dim / 16);
+    const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)K.num_sms * 64);
+    k_kv_append<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? MOE_OK : cuda_fail(e, "append launch");
+}
+
+moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* stream) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    Kv& K = kv->K;
+    moe_status st = check_attend(&K.d, args);
+    if (st != MOE_OK) return st;
+    if (args->B == 0) return MOE_OK;
+    DeviceGuard g(K.device);
+    if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
+    return kv_attend_launch(K, *args, static_cast<cudaStream_t>(stream));
+}
+
+moe_status moe_kv_health(moe_kv* kv, uint32_t* bits) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    DeviceGuard g(kv->K.device);
+    if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
+    MOE_CUDA_TRY(cudaDeviceSynchronize());
+    uint32_t v = 0;
+    MOE_CUDA_TRY(cudaMemcpy(&v, kv->K.health, 4, cudaMemcpyDeviceToHost));
+    if (bits) *bits = v;
+    if (!v) return MOE_OK;
+    MOE_CUDA_TRY(cudaMemset(kv->K.health, 0, 4));
+    return fail(MOE_E_STATE, "kernels refused part of their work (health bits " + std::to_string(v) + ")");
+}
+
+}  // extern "C"

@@ -1,0 +1,62 @@
+// The paged key-value cache: what its translation units share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+#include "moe.h"
+
+namespace moe {
+
+// Shape and strides of a cache as the kernels see them.
+struct KvShape {
+    int n_heads, n_kv_heads, head_dim, page_size, n_pages, rotary_dim, rotary_adjacent, e4m3;
+    int64_t page_stride, head_stride, token_stride;  // elements
+};
+
+// Page of (seq, position), or -1 with a health bit. The one place where a block
+// table is turned into a page, on the host (moe_kv_locate) and in the kernels.
+__host__ __device__ inline int kv_page(const KvShape& s, const int32_t* table, int n_seqs, int max_pages, int seq,
+                                       int position, uint32_t& bits) {
+    if (seq < 0 || seq >= n_seqs) {
+        bits |= MOE_KV_BAD_SEQ;
+        return -1;
+    }
+    const int at = position / s.page_size;
+    if (position < 0 || at >= max_pages) {
+        bits |= MOE_KV_BAD_LENGTH;
+        return -1;
+    }
+    const int page = table[(int64_t)seq * max_pages + at];
+    if (page < 0 || page >= s.n_pages) {
+        bits |= MOE_KV_BAD_PAGE;
+        return -1;
+    }
+    return page;
+}
+
+// Element offset of a row of a pool; 64-bit throughout.
+__host__ __device__ inline int64_t kv_offset(const KvShape& s, int page, int head, int slot) {
+    return (int64_t)page * s.page_stride + (int64_t)head * s.head_stride + (int64_t)slot * s.token_stride;
+}
+
+struct Kv {
+    moe_kv_desc d{};
+    KvShape s{};
+    int device = 0, num_sms = 0;
+    void *k_pages = nullptr, *v_pages = nullptr;
+    uint64_t* turns = nullptr;   // [rotary_dim / 2] turns per position, as a fraction of 2^64
+    float *k_scale = nullptr, *v_scale = nullptr;  // [n_kv_heads], ones for a bf16 cache
+    unsigned* health = nullptr;
+    void* block = nullptr;       // the allocation that holds all of the above
+    size_t device_bytes = 0;
+};
+
+moe_status kv_attend_launch(Kv& kv, const moe_kv_attend_args& a, cudaStream_t s);
+
+}  // namespace moe
+
+struct moe_kv {
+    moe::Kv K;
+};
