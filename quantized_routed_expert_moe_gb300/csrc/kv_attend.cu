@@ -1,99 +1,734 @@
 // Attention of one new token per sequence over a paged key-value cache.
+//
+// Every cached key and value is read once and used by the G = n_heads /
+// n_kv_heads queries of its head, so the kernel is a stream over the cache:
+// its floor is the cached bytes at the copy rate.
+//
+// Split. The attended tokens of every (sequence, head tile) are cut into chunks
+// of 8 KB of keys and 8 KB of values; all chunks of the call, numbered sequence by
+// sequence, are dealt out evenly and contiguously to one resident CTA per SM,
+// from the lengths as they stand on the device. A ragged batch, one long
+// sequence and thousands of short ones are balanced alike, and the call is one
+// launch. A (sequence, head tile) that is cut between CTAs is joined by the one of
+// them that finishes last, in CTA order, so the result does not depend on which
+// one that is.
+//
+// Within a CTA each of four warps takes every fourth chunk on its own: it copies
+// its chunks by TMA into its own ring of shared-memory stages (the swizzle lets
+// ldmatrix read them without bank conflicts), keeps its own running maximum, sum
+// and output, and meets the others only where a (sequence, head tile) ends. The
+// copies run ahead over those ends, so about 190 KB per SM are in flight or
+// waiting at any time, where the copy rate times the memory latency asks for 45.
+//
+// Products. The tokens are the rows of the matrix instruction and the query
+// heads its 8 columns (mma m16n8k16), S^T = K Q^T and O^T = V^T P^T: up to 8 heads
+// per key-value head cost half of what padding the heads to 16 rows would. P^T is
+// turned into the second product's operand by movmatrix. At 2 G FLOP per cached
+// byte the legacy tensor path has several times the rate that the copy allows.
+// Scores, maxima, sums and outputs are fp32. The weights are rounded once to
+// the operand type of the second product, bf16 for a bf16 cache (2^-8 relative,
+// like the output), fp16 for an e4m3 cache (2^-11), whose keys, values and scaled
+// queries are exact in fp16; the sum is taken before that rounding.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
 #include "kv_cache.h"
 #include "moe_internal.h"
+#include "sm100.cuh"
 
 namespace moe {
 
 namespace {
 
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kRing = 48 * 1024;   // bytes of stages per warp
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
+template <int D_, bool FP8_, int NT_>
+struct Cfg {
+    static constexpr int D = D_, NT = NT_;
+    static constexpr bool FP8 = FP8_;
+    static constexpr int RB = D * (FP8 ? 1 : 2);              // bytes of a row
+    static constexpr int CT = RB >= 512 ? 16 : RB >= 256 ? 32 : 64;  // tokens of a chunk
+    static constexpr int LINE = RB < 128 ? RB : 128;          // bytes of a shared-memory row (the swizzle's width)
+    static constexpr int COLS = RB / LINE;                    // column blocks of a row
+    static constexpr int HALF = CT * RB;                      // bytes of a chunk's keys (or values)
+    static constexpr int STAGES = kRing / (2 * HALF);
+    static constexpr int HEADS = 8 * NT;
+    static constexpr int MT = CT / 16, KS = D / 16, DT = D / 16;
+    static constexpr int OPAD = D + 4;                        // floats of a head in the join buffer
+    static constexpr size_t ring_bytes = (size_t)kWarps * kRing;
+    static constexpr int JH = D == 256 ? 4 : 8;               // heads joined at a time (shared memory)
+    static constexpr size_t join_bytes = (size_t)kWarps * JH * OPAD * 4;
+    static constexpr size_t smem = 1024 + ring_bytes + join_bytes;
+};
+
 struct AttendArgs {
     moe_kv_attend_args a;
     KvShape s;
-    const void *k_pages, *v_pages;
     const float *k_scale, *v_scale;
     unsigned* health;
+    float* part_o;      // [CTA][2][16][head_dim]
+    float2* part_ml;    // [CTA][2][16]: maximum (base two), sum
+    int* arrived;       // [max_batch * head tiles], zero between calls
+    int box_rows;       // tokens of one TMA box
 };
 
-constexpr int kWarps = 4;
-
-__device__ __forceinline__ float load_cached(const void* pool, int e4m3, int64_t at) {
-    if (!e4m3) return __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
-    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(pool)[at], __NV_E4M3);
-    return __half2float(__half(h));
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+template <bool FP8>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (FP8)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, "
+                     "%9}, {%0, %1, %2, %3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// two e4m3 values (a low, b high byte) as an fp16 pair, exact
+__device__ __forceinline__ uint32_t e4m3_pair(uint32_t v16) {
+    uint32_t d;
+    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(d) : "r"(v16));
+    return d;
+}
+template <bool FP8>
+__device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
+    if constexpr (FP8) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
+                                            uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
+        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(pol)
+        : "memory");
 }
 
-// One CTA per (query head, sequence): the warps take positions in turn, a lane
-// holds D / 32 channels, the softmax runs with a running maximum and sum, and
-// the warps' results are joined in shared memory.
-template <int D>
-__global__ void __launch_bounds__(32 * kWarps) k_kv_attend_rows(const AttendArgs p) {
-    constexpr int C = D / 32;
-    __shared__ float sm_o[kWarps][D], sm_m[kWarps], sm_l[kWarps];
+// Shared address of byte `col` of row `row` of a chunk half: rows of LINE bytes,
+// 16-byte units exchanged within 8 (128-byte lines) or 4 (64-byte lines) of them as
+// the TMA swizzle does.
+template <class C>
+__device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int col) {
+    if constexpr (C::LINE == 128)
+        return base + (col >> 7) * (C::CT * 128) + row * 128 + ((col & 127) ^ ((row & 7) << 4));
+    else
+        return base + row * 64 + (col ^ (((row >> 1) & 3) << 4));
+}
+
+// A position in the chunk sequence: unit u, in the segment (sequence b, head
+// tile ht) of units [beg, end).
+struct Place {
+    int64_t u, beg, end;
+    int b, ht;
+};
+
+template <class C>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_kv_attend(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    constexpr int NT = C::NT, CT = C::CT, D = C::D;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t sm_pre[1025];            // chunks before sequence b
+    __shared__ int64_t sm_wsum[kWarps];
+    __shared__ int sm_len[1024];
+    __shared__ __align__(8) uint64_t sm_bar[kWarps][C::STAGES];
+    __shared__ uint32_t sm_rows[kWarps][C::STAGES];  // which groups of 16 rows a stage holds
+    __shared__ float sm_m[kWarps][C::HEADS], sm_l[kWarps][C::HEADS];
+    __shared__ int sm_last, sm_abort;
+
     const KvShape& s = p.s;
-    const int head = blockIdx.x, b = blockIdx.y, hk = head / (s.n_heads / s.n_kv_heads);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int g = lane >> 2, j = lane & 3;
+    const uint32_t ring = ((bw::saddr(smem_raw) + 1023) & ~1023u) + warp * kRing;
+    float* join = reinterpret_cast<float*>(smem_raw + (((bw::saddr(smem_raw) + 1023) & ~1023u) - bw::saddr(smem_raw)) +
+                                           C::ring_bytes);
     uint32_t bits = 0;
-    int len = max(p.a.lens[b], 0);
-    if (len > p.a.max_pages * s.page_size) {
-        len = p.a.max_pages * s.page_size;
-        bits |= MOE_KV_BAD_LENGTH;
+
+    if (lane < C::STAGES) bw::mbar_init(bw::saddr(&sm_bar[warp][lane]), 1);
+    if (threadIdx.x == 0) sm_abort = 0;
+    bw::mbar_fence_init();
+
+    // ---- chunks of every sequence, summed ------------------------------------------
+    const int G = s.n_heads / s.n_kv_heads;
+    const int tiles = (G + C::HEADS - 1) / C::HEADS;   // head tiles per key-value head
+    const int HT = s.n_kv_heads * tiles;
+    const int B = p.a.B;
+    // a sequence attends to tokens [first_of(len), len)
+    auto first_of = [&](int len) { return p.a.window > 0 ? max(0, len - p.a.window) : 0; };
+    {
+        const int most = p.a.max_pages * s.page_size;
+        const int per = (B + kThreads - 1) / kThreads;
+        const int b0 = threadIdx.x * per, b1 = min(B, b0 + per);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            int len = max(p.a.lens[b], 0);
+            if (len > most) {
+                len = most;
+                bits |= MOE_KV_BAD_LENGTH;
+            }
+            sm_len[b] = len;
+            const int n = (len + CT - 1) / CT - first_of(len) / CT;
+            sm_pre[b + 1] = n;
+            mine += n;
+        }
+        int64_t incl = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(~0u, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sm_wsum[warp] = incl;
+        __syncthreads();
+        int64_t run = incl - mine;
+        for (int w = 0; w < warp; ++w) run += sm_wsum[w];
+        for (int b = b0; b < b1; ++b) {
+            run += sm_pre[b + 1];
+            sm_pre[b + 1] = run;
+        }
+        if (threadIdx.x == 0) sm_pre[0] = 0;
+        __syncthreads();
     }
-    const int first = p.a.window > 0 ? max(0, len - p.a.window) : 0;
-    const float ks = p.k_scale[hk], vs = p.v_scale[hk];
-    float q[C], o[C], m = -INFINITY, l = 0.f;
-    for (int c = 0; c < C; ++c) {
-        q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(
-            p.a.q)[(int64_t)b * p.a.q_stride + (int64_t)head * D + lane + 32 * c]);
-        o[c] = 0.f;
+    const int64_t total = sm_pre[B] * HT;
+    // no more CTAs than chunks: each of them has at least one, so a segment's CTAs are consecutive
+    const int64_t ctas = min((int64_t)gridDim.x, total), me = blockIdx.x;
+    const int64_t u0 = me < ctas ? me * total / ctas : 0, u1 = me < ctas ? (me + 1) * total / ctas : 0;
+
+    // sequences with nothing to attend to
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        if (sm_pre[b + 1] != sm_pre[b]) continue;
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)b * s.n_heads * D);
+        for (int i = threadIdx.x; i < s.n_heads * (D / 4); i += kThreads) o[i] = make_uint2(0, 0);
+        if (p.a.lse)
+            for (int i = threadIdx.x; i < s.n_heads; i += kThreads) p.a.lse[(int64_t)b * s.n_heads + i] = -INFINITY;
     }
-    for (int j = first + warp; j < len; j += kWarps) {
-        const int page = kv_page(s, p.a.block_table, p.a.B, p.a.max_pages, b, j, bits);
-        if (page < 0) continue;
-        const int64_t at = kv_offset(s, page, hk, j % s.page_size) + lane;
-        float x = 0.f;
-        for (int c = 0; c < C; ++c) x += q[c] * load_cached(p.k_pages, s.e4m3, at + 32 * c);
-        for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(~0u, x, i);
-        x *= p.a.scale * ks;
-        if (p.a.softcap > 0.f) x = p.a.softcap * tanhf(x / p.a.softcap);
-        const float mn = fmaxf(m, x), w = expf(x - mn), f = m == -INFINITY ? 0.f : expf(m - mn);
-        l = l * f + w;
-        for (int c = 0; c < C; ++c) o[c] = o[c] * f + w * load_cached(p.v_pages, s.e4m3, at + 32 * c);
-        m = mn;
+
+    if (u0 < u1) {
+        // segment of unit u0
+        Place at;
+        {
+            int lo = 0, hi = B;   // sm_pre[lo] * HT <= u0 < sm_pre[hi] * HT
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (sm_pre[mid] * HT <= u0) lo = mid;
+                else hi = mid;
+            }
+            const int64_t n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT;
+            at.b = lo;
+            at.ht = (int)((u0 - base) / n);
+            at.beg = base + at.ht * n;
+            at.end = at.beg + n;
+            at.u = u0;
+        }
+        // to the segment that holds unit u (u only grows)
+        auto seek = [&](Place& q, int64_t u) {
+            q.u = u;
+            while (u >= q.end) {
+                const int64_t n = q.end - q.beg;
+                if (++q.ht < HT) {
+                    q.beg = q.end;
+                    q.end += n;
+                } else {
+                    q.ht = 0;
+                    do ++q.b;
+                    while (sm_pre[q.b + 1] == sm_pre[q.b]);
+                    q.beg = sm_pre[q.b] * HT;
+                    q.end = q.beg + (sm_pre[q.b + 1] - sm_pre[q.b]);
+                }
+            }
+        };
+
+        // ---- the copies of this warp ----------------------------------------------------
+        // Box i of a chunk: rows [box * box_rows, ...), one column block, keys or
+        // values; lane i looks its page up one chunk ahead of its issue.
+        const int boxes = CT / p.box_rows;
+        const int bx = lane % boxes, col = (lane / boxes) % C::COLS, is_v = lane / (boxes * C::COLS);
+        const bool issuer = lane < boxes * C::COLS * 2;
+        const uint64_t pol = bw::l2_evict_first();
+        const uint32_t box_bytes = p.box_rows * C::LINE;
+        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        Place nx = at;             // the chunk whose pages are being looked up
+        int nx_page = -1, nx_slot = 0;
+        bool nx_live = false, nx_read = false;
+        auto lookup = [&](int64_t u) {
+            nx_live = u < u1;
+            if (!nx_live) return;
+            seek(nx, u);
+            nx_page = -1;
+            nx_read = false;
+            if (!issuer) return;
+            const int len = sm_len[nx.b], first = first_of(len);
+            const int tok = (first / CT + (int)(u - nx.beg)) * CT + bx * p.box_rows;
+            if (tok < len && tok + p.box_rows > first) {
+                // not looked at before the issue, an iteration later
+                nx_read = true;
+                nx_page = p.a.block_table[(int64_t)nx.b * p.a.max_pages + tok / s.page_size];
+                nx_slot = tok % s.page_size;
+            }
+        };
+        int issued = 0;
+        auto issue = [&]() {       // the looked-up chunk into the next stage
+            const int st = issued % C::STAGES;
+            const uint32_t bar = bw::saddr(&sm_bar[warp][st]);
+            if (nx_read && (nx_page < 0 || nx_page >= s.n_pages)) {
+                bits |= MOE_KV_BAD_PAGE;
+                nx_page = -1;
+            }
+            const unsigned have = __ballot_sync(~0u, nx_page >= 0);
+            if (lane == 0) {
+                bw::mbar_arrive_tx(bar, __popc(have) * box_bytes);
+                uint32_t rows = 0;
+                for (int i = 0; i < boxes; ++i)
+                    if (have >> i & 1) rows |= ((1u << (p.box_rows / 16)) - 1) << (i * p.box_rows / 16);
+                sm_rows[warp][st] = rows;
+            }
+            __syncwarp();
+            if (nx_page >= 0)
+                tma_load_4d(ring + st * 2 * C::HALF + is_v * C::HALF + col * (CT * 128) + bx * p.box_rows * C::LINE, tm,
+                            col * (C::FP8 ? 128 : 64), nx_slot, nx.ht / tiles, nx_page, bar, pol);
+            ++issued;
+        };
+        int64_t ahead = u0 + warp;
+        lookup(ahead);
+        for (int i = 0; i < C::STAGES && nx_live; ++i) {
+            issue();
+            lookup(ahead += kWarps);
+        }
+
+        // ---- segments ------------------------------------------------------------------
+        int done = 0;                    // chunks of this warp consumed
+        int64_t cur = u0 + warp;         // this warp's next chunk
+        for (seek(at, u0);; seek(at, at.end)) {
+            const int64_t seg_end = min(at.end, u1);
+            const int hk = at.ht / tiles, h0 = hk * G + (at.ht % tiles) * C::HEADS;
+            const int heads = min(C::HEADS, G - (at.ht % tiles) * C::HEADS);
+            const int len = sm_len[at.b], first = first_of(len);
+
+            // queries: operand B of S^T = K Q^T (column g of head tile nt)
+            uint32_t qf[C::KS][NT][2];
+            float coef[NT][2];           // score in base two per accumulator unit, heads 2j and 2j + 1
+            float m[NT][2], l[NT][2], o[C::DT][NT][4];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                const bool real = nt * 8 + g < heads;
+                const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)at.b * p.a.q_stride +
+                                          (int64_t)(h0 + nt * 8 + g) * D;
+                float unit = 1.f;
+                if constexpr (!C::FP8) {
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            qf[ks][nt][i] = real ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * j + 8 * i) : 0u;
+                } else {
+                    // channels 4j..4j+3 of a step stand at k = 2j, 2j+1, 2j+8, 2j+9, as the
+                    // bytes of the keys do. The head's queries are scaled by a power of two
+                    // to below 2^15, where fp16 holds their 8 bits.
+                    float top = 0.f;
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks) {
+                        const uint2 v = real ? *reinterpret_cast<const uint2*>(qp + 16 * ks + 4 * j) : make_uint2(0, 0);
+                        qf[ks][nt][0] = v.x;
+                        qf[ks][nt][1] = v.y;
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ks][nt][i] << 16)),
+                                                   fabsf(__uint_as_float(qf[ks][nt][i] & 0xffff0000u))));
+                    }
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                    // 2^(14 - e) with e the exponent of top, kept within fp32's normal range
+                    const int e = (int)(__float_as_uint(top) >> 23) - 127;
+                    const int a = top < INFINITY ? max(-112, min(126, 14 - e)) : 0;
+                    const float up = __int_as_float((a + 127) << 23);
+                    unit = __int_as_float((127 - a) << 23);
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t v = qf[ks][nt][i];
+                            qf[ks][nt][i] =
+                                pack_pair<true>(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
+                        }
+                }
+                const float k = p.k_scale[hk] * p.a.scale;
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    coef[nt][c] = k * __shfl_sync(~0u, unit, (2 * j + c) * 4);
+                    if (p.a.softcap == 0.f) coef[nt][c] *= kLog2e;
+                    m[nt][c] = -INFINITY;
+                    l[nt][c] = 0.f;
+                }
+#pragma unroll
+                for (int dt = 0; dt < C::DT; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[dt][nt][i] = 0.f;
+            }
+
+            for (; cur < seg_end; cur += kWarps) {
+                const int st = done % C::STAGES;
+                const uint32_t kt = ring + st * 2 * C::HALF, vt = kt + C::HALF;
+                bw::mbar_wait(bw::saddr(&sm_bar[warp][st]), (done / C::STAGES) & 1, &sm_abort, p.health, MOE_KV_TIMEOUT);
+                __syncwarp();
+                const int tok0 = (first / CT + (int)(cur - at.beg)) * CT;
+                const uint32_t rows = sm_rows[warp][st];
+                const bool whole = tok0 >= first && tok0 + CT <= len && rows == (1u << C::MT) - 1;
+
+                float sc[C::MT][NT][4];
+#pragma unroll
+                for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) sc[mt][nt][i] = 0.f;
+                if constexpr (!C::FP8) {
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt) {
+                            uint32_t a[4];
+                            ldm4(a, tile_at<C>(kt, mt * 16 + row, ks * 32 + cb));
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma<false>(sc[mt][nt], a, qf[ks][nt][0], qf[ks][nt][1]);
+                        }
+                } else {
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ks += 2)
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt) {
+                            uint32_t r[4];
+                            ldm4(r, tile_at<C>(kt, mt * 16 + row, ks * 16 + cb));
+#pragma unroll
+                            for (int k2 = 0; k2 < 2; ++k2) {
+                                const uint32_t a[4] = {e4m3_pair(r[2 * k2]), e4m3_pair(r[2 * k2 + 1]),
+                                                       e4m3_pair(r[2 * k2] >> 16), e4m3_pair(r[2 * k2 + 1] >> 16)};
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma<true>(sc[mt][nt], a, qf[ks + k2][nt][0], qf[ks + k2][nt][1]);
+                            }
+                        }
+                }
+
+                // which of this lane's tokens are attended: rows g and g + 8 of each tile
+                auto seen = [&](int t) {
+                    const int tok = tok0 + t;
+                    return tok >= first && tok < len && (rows >> (t >> 4) & 1);
+                };
+                uint32_t pf[C::MT][NT][2];   // weights: operand B of O^T = V^T P^T
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    float mx[2] = {m[nt][0], m[nt][1]};
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            float x = sc[mt][nt][i] * coef[nt][i & 1];
+                            if (p.a.softcap != 0.f) {
+                                // tanh(z) = 1 - 2 / (exp(2 z) + 1): off by 2^-22 of the cap
+                                const float e = ex2(x * (2.f * kLog2e / p.a.softcap));
+                                x = (p.a.softcap - 2.f * p.a.softcap / (e + 1.f)) * kLog2e;
+                            }
+                            if (!whole && !seen(mt * 16 + g + (i & 2) * 4)) x = -INFINITY;
+                            sc[mt][nt][i] = x;
+                            mx[i & 1] = fmaxf(mx[i & 1], x);
+                        }
+                    float f[2], base[2];
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 4));
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 8));
+                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 16));
+                        base[c] = mx[c] == -INFINITY ? 0.f : mx[c];
+                        f[c] = ex2(m[nt][c] - base[c]);
+                        m[nt][c] = mx[c];
+                        l[nt][c] *= f[c];
+                    }
+                    if (__any_sync(~0u, f[0] != 1.f || f[1] != 1.f))
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) o[dt][nt][i] *= f[i & 1];
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        float w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            w[i] = ex2(sc[mt][nt][i] - base[i & 1]);
+                            l[nt][i & 1] += w[i];
+                        }
+                        pf[mt][nt][0] = transpose8(pack_pair<C::FP8>(w[0], w[1]));
+                        pf[mt][nt][1] = transpose8(pack_pair<C::FP8>(w[2], w[3]));
+                    }
+                }
+
+                // values: tokens that are not attended may hold anything, so their bits are cleared
+#pragma unroll
+                for (int mt = 0; mt < C::MT; ++mt) {
+                    uint32_t keep[2] = {~0u, ~0u};
+                    if (!whole)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            keep[i] = (seen(mt * 16 + 8 * i + 2 * j) ? 0xffffu : 0u) |
+                                      (seen(mt * 16 + 8 * i + 2 * j + 1) ? 0xffff0000u : 0u);
+                    if constexpr (!C::FP8) {
+                        const int row = (lane & 7) + (lane >> 4) * 8, cb = ((lane >> 3) & 1) * 16;
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt) {
+                            uint32_t a[4];
+                            ldm4t(a, tile_at<C>(vt, mt * 16 + row, dt * 32 + cb));
+                            if (!whole) {
+                                a[0] &= keep[0];
+                                a[1] &= keep[0];
+                                a[2] &= keep[1];
+                                a[3] &= keep[1];
+                            }
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) mma<false>(o[dt][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+                        }
+                    } else {
+                        const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; dt += 2) {
+                            uint32_t r[4];
+                            ldm4t(r, tile_at<C>(vt, mt * 16 + row, dt * 16 + cb));
+#pragma unroll
+                            for (int d2 = 0; d2 < 2; ++d2) {
+                                // bytes: channels 2g, 2g + 1 of token 2j, then of token 2j + 1
+                                const uint32_t x = __byte_perm(r[2 * d2], 0, 0x3120);
+                                const uint32_t y = __byte_perm(r[2 * d2 + 1], 0, 0x3120);
+                                uint32_t a[4] = {e4m3_pair(x), e4m3_pair(x >> 16), e4m3_pair(y), e4m3_pair(y >> 16)};
+                                if (!whole) {
+                                    a[0] &= keep[0];
+                                    a[1] &= keep[0];
+                                    a[2] &= keep[1];
+                                    a[3] &= keep[1];
+                                }
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt)
+                                    mma<true>(o[dt + d2][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+                            }
+                        }
+                    }
+                }
+                ++done;
+                __syncwarp();   // every lane has read the stage before it is filled again
+                if (nx_live) {
+                    issue();
+                    lookup(ahead += kWarps);
+                }
+            }
+
+            // ---- the warps' results are joined -------------------------------------------
+            const bool split = at.beg < u0 || at.end > u1;
+            const int slot = blockIdx.x * 2 + (at.beg < u0 ? 0 : 1);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float v = l[nt][c];
+                    v += __shfl_xor_sync(~0u, v, 4);
+                    v += __shfl_xor_sync(~0u, v, 8);
+                    v += __shfl_xor_sync(~0u, v, 16);
+                    if (g == 0) {
+                        sm_m[warp][nt * 8 + 2 * j + c] = m[nt][c];
+                        sm_l[warp][nt * 8 + 2 * j + c] = v;
+                    }
+                }
+            const float vs = p.v_scale[hk];
+#pragma unroll
+            for (int part = 0; part < C::HEADS / C::JH; ++part) {
+                const int nt = part * C::JH / 8, p0 = part * C::JH;
+                if (p0 >= heads) break;
+                float* mine = join + warp * C::JH * C::OPAD;
+                if ((nt * 8 + 2 * j) / C::JH == part)
+#pragma unroll
+                for (int dt = 0; dt < C::DT; ++dt)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int d = dt * 16 + (C::FP8 ? 2 * g + (i >> 1) : g + (i >> 1) * 8);
+                        mine[((2 * j) % C::JH + (i & 1)) * C::OPAD + d] = o[dt][nt][i];
+                    }
+                __syncthreads();
+                const int hs = min(C::JH, heads - p0);
+                for (int it = threadIdx.x; it < hs * (D / 4); it += kThreads) {
+                    const int h = it / (D / 4), d = it % (D / 4) * 4, hh = p0 + h;
+                    float M = sm_m[0][hh];
+                    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][hh]);
+                    const float mb = M == -INFINITY ? 0.f : M;
+                    float L = 0.f;
+                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int w = 0; w < kWarps; ++w) {
+                        const float f = ex2(sm_m[w][hh] - mb);
+                        const float4 v = *reinterpret_cast<const float4*>(join + (w * C::JH + h) * C::OPAD + d);
+                        L += f * sm_l[w][hh];
+                        a.x += f * v.x;
+                        a.y += f * v.y;
+                        a.z += f * v.z;
+                        a.w += f * v.w;
+                    }
+                    if (split) {
+                        *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * 16 + hh) * D + d) = a;
+                        if (d == 0) p.part_ml[slot * 16 + hh] = make_float2(M, L);
+                    } else {
+                        const float r = L == 0.f ? 0.f : vs / L;
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) +
+                                                  ((int64_t)at.b * s.n_heads + h0 + hh) * D + d) =
+                            make_uint2(pack_pair<false>(a.x * r, a.y * r), pack_pair<false>(a.z * r, a.w * r));
+                        if (d == 0 && p.a.lse)
+                            p.a.lse[(int64_t)at.b * s.n_heads + h0 + hh] =
+                                L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+                    }
+                }
+                __syncthreads();
+            }
+
+            // ---- and those of the CTAs that share the segment ------------------------------
+            if (split) {
+                // CTA of unit u: the largest c with c * total / ctas <= u
+                const int c0 = (int)(((at.beg + 1) * ctas - 1) / total), c1 = (int)((at.end * ctas - 1) / total);
+                const int n = c1 - c0 + 1;
+                int* arrived = p.arrived + (int64_t)at.b * HT + at.ht;
+                __threadfence();
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    sm_last = atomicAdd(arrived, 1) == n - 1;
+                    if (sm_last) *arrived = 0;   // for the next call
+                }
+                __syncthreads();
+                if (sm_last) {
+                    __threadfence();
+                    // the first CTA's part is its second slot (its segment begins there), the
+                    // others' their first
+                    auto slot_of = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
+                    for (int it = threadIdx.x; it < heads * (D / 4); it += kThreads) {
+                        const int h = it / (D / 4), d = it % (D / 4) * 4;
+                        float M = -INFINITY, L = 0.f;
+                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+                        for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + h]).x);
+                        const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll 8
+                        for (int i = 0; i < n; ++i) {
+                            const float2 ml = __ldcg(&p.part_ml[slot_of(i) * 16 + h]);
+                            const float4 v = __ldcg(
+                                reinterpret_cast<const float4*>(p.part_o + ((int64_t)slot_of(i) * 16 + h) * D + d));
+                            const float f = ex2(ml.x - mb);
+                            L += f * ml.y;
+                            a.x += f * v.x;
+                            a.y += f * v.y;
+                            a.z += f * v.z;
+                            a.w += f * v.w;
+                        }
+                        const float r = L == 0.f ? 0.f : vs / L;
+                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) +
+                                                  ((int64_t)at.b * s.n_heads + h0 + h) * D + d) =
+                            make_uint2(pack_pair<false>(a.x * r, a.y * r), pack_pair<false>(a.z * r, a.w * r));
+                        if (d == 0 && p.a.lse)
+                            p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+                    }
+                }
+            }
+            if (at.end >= u1) break;
+        }
     }
-    for (int c = 0; c < C; ++c) sm_o[warp][lane + 32 * c] = o[c];
-    if (lane == 0) {
-        sm_m[warp] = m;
-        sm_l[warp] = l;
-        if (bits) atomicOr(p.health, bits);
+    if (bits) atomicOr(p.health, bits);
+}
+
+template <class C>
+cudaError_t launch(const Kv& K, const AttendArgs& p, cudaStream_t stream) {
+    k_kv_attend<C><<<K.num_sms, kThreads, C::smem, stream>>>(p, K.tm_k, K.tm_v);
+    return cudaGetLastError();
+}
+
+// The kernel of a cache: more than 8 heads per key-value head share one pass
+// over it as 16 columns; 16 columns of 256 channels would not fit the registers,
+// so those take a pass per 8 heads.
+template <class F>
+auto pick(const KvShape& s, F f) {
+    const bool two = s.n_heads / s.n_kv_heads > 8;
+    if (s.e4m3) {
+        if (s.head_dim == 64) return two ? f(Cfg<64, true, 2>{}) : f(Cfg<64, true, 1>{});
+        if (s.head_dim == 128) return two ? f(Cfg<128, true, 2>{}) : f(Cfg<128, true, 1>{});
+        return f(Cfg<256, true, 1>{});
     }
-    __syncthreads();
-    float M = -INFINITY, L = 0.f;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w]);
-    for (int w = 0; w < kWarps; ++w) L += sm_m[w] == -INFINITY ? 0.f : sm_l[w] * expf(sm_m[w] - M);
-    for (int d = threadIdx.x; d < D; d += 32 * kWarps) {
-        float x = 0.f;
-        for (int w = 0; w < kWarps; ++w) x += sm_m[w] == -INFINITY ? 0.f : sm_o[w][d] * expf(sm_m[w] - M);
-        static_cast<__nv_bfloat16*>(p.a.out)[((int64_t)b * s.n_heads + head) * D + d] =
-            __float2bfloat16_rn(L == 0.f ? 0.f : x * vs / L);
-    }
-    if (p.a.lse && threadIdx.x == 0)
-        p.a.lse[(int64_t)b * s.n_heads + head] = L == 0.f ? -INFINITY : M + logf(L);
+    if (s.head_dim == 64) return two ? f(Cfg<64, false, 2>{}) : f(Cfg<64, false, 1>{});
+    if (s.head_dim == 128) return two ? f(Cfg<128, false, 2>{}) : f(Cfg<128, false, 1>{});
+    return f(Cfg<256, false, 1>{});
 }
 
 }  // namespace
 
+size_t kv_attend_workspace(const Kv& K, size_t out[3]) {
+    const int G = K.s.n_heads / K.s.n_kv_heads;
+    const int heads = pick(K.s, [](auto c) { return decltype(c)::HEADS; });
+    out[0] = (size_t)K.num_sms * 2 * 16 * K.s.head_dim * 4;
+    out[1] = (size_t)K.num_sms * 2 * 16 * 8;
+    out[2] = (size_t)K.d.max_batch * K.s.n_kv_heads * ((G + heads - 1) / heads) * 4;
+    return out[0] + out[1] + out[2];
+}
+
+cudaError_t kv_attend_setup(Kv& K) {
+    const int ct = pick(K.s, [](auto c) { return decltype(c)::CT; });
+    const uint32_t line = pick(K.s, [](auto c) { return decltype(c)::LINE; });
+    K.box_rows = 16;
+    while (K.box_rows * 2 <= ct && K.s.page_size % (K.box_rows * 2) == 0) K.box_rows *= 2;
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const size_t es = K.s.e4m3 ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)K.s.head_dim, (cuuint64_t)K.s.page_size, (cuuint64_t)K.s.n_kv_heads,
+                                (cuuint64_t)K.s.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)K.s.token_stride * es, (cuuint64_t)K.s.head_stride * es,
+                                   (cuuint64_t)K.s.page_stride * es};
+    const cuuint32_t box[4] = {(cuuint32_t)(line / es), (cuuint32_t)K.box_rows, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encode(i ? &K.tm_v : &K.tm_k, K.s.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                   i ? K.v_pages : K.k_pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    return pick(K.s, [](auto c) {
+        using C = decltype(c);
+        return cudaFuncSetAttribute(k_kv_attend<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+    });
+}
+
 moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t stream) {
-    const AttendArgs p{a, K.s, K.k_pages, K.v_pages, K.k_scale, K.v_scale, K.health};
-    const dim3 grid(K.s.n_heads, a.B);
-    if (K.s.head_dim == 64) k_kv_attend_rows<64><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else if (K.s.head_dim == 128) k_kv_attend_rows<128><<<grid, 32 * kWarps, 0, stream>>>(p);
-    else k_kv_attend_rows<256><<<grid, 32 * kWarps, 0, stream>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const AttendArgs p{a, K.s, K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml, K.arrived, K.box_rows};
+    const cudaError_t e = pick(K.s, [&](auto c) { return launch<decltype(c)>(K, p, stream); });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend launch");
 }
 

@@ -72,8 +72,9 @@ KvShape shape_of(const moe_kv_desc& d) {
 moe_status check_table(const int32_t* table, int n_seqs, int max_pages, int page_size) {
     if (!table) return fail(MOE_E_INVALID, "block_table is NULL");
     if (n_seqs < 1) return fail(MOE_E_INVALID, "n_seqs must be positive");
-    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX)
-        return fail(MOE_E_INVALID, "max_pages must be positive, and max_pages * page_size below 2^31");
+    // room above every position for the kernels' 32-bit steps
+    if (max_pages < 1 || (int64_t)max_pages * page_size > INT32_MAX - 4095)
+        return fail(MOE_E_INVALID, "max_pages must be positive, and max_pages * page_size at most 2^31 - 4096");
     return MOE_OK;
 }
 
@@ -340,6 +341,9 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     };
     const size_t o_turns = add((size_t)std::max(half, 1) * 8), o_ks = add((size_t)Hk * 4), o_vs = add((size_t)Hk * 4),
                  o_health = add(4);
+    size_t ws[3];
+    kv_attend_workspace(K, ws);
+    const size_t o_po = add(ws[0]), o_pml = add(ws[1]), o_arr = add(ws[2]);
     size_t free_b = 0, total_b = 0;
     e = cudaMemGetInfo(&free_b, &total_b);
     if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemGetInfo"));
@@ -352,6 +356,9 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     K.k_scale = reinterpret_cast<float*>(base + o_ks);
     K.v_scale = reinterpret_cast<float*>(base + o_vs);
     K.health = reinterpret_cast<unsigned*>(base + o_health);
+    K.part_o = reinterpret_cast<float*>(base + o_po);
+    K.part_ml = reinterpret_cast<float2*>(base + o_pml);
+    K.arrived = reinterpret_cast<int*>(base + o_arr);
 
     // inv_freq / 2 pi in double keeps 2^-53 of a turn per position; its fraction
     // times 2^64 is rounded to an integer
@@ -370,6 +377,7 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     if (e == cudaSuccess) e = cudaMemcpy(K.turns, turns.data(), turns.size() * 8, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaMemcpy(K.k_scale, ks.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaMemcpy(K.v_scale, vs.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = kv_attend_setup(K);
     // the set-up ran on the legacy stream: finish it before any other stream may run a call
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return bail(cuda_fail(e, "moe_kv_create set-up"));

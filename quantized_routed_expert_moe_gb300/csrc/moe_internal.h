@@ -45,6 +45,15 @@ struct DeviceGuard {
     }
 };
 
+// ---- tensor maps ---------------------------------------------------------------
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor map encoder, or NULL.
+EncodeTiled tensor_map_encoder();
+
 // ---- kernel layout of the weights ---------------------------------------------
 //
 // A quantised row of K inputs is stored as one "row record":

@@ -730,15 +730,13 @@ __global__ void __launch_bounds__(256) k_pf_combine(const float* __restrict__ yp
     }
 }
 
+}  // namespace
+
 // ---------------------------------------------------------------------------
 // host: tensor maps and launches
 // ---------------------------------------------------------------------------
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
+EncodeTiled tensor_map_encoder() {
     static EncodeTiled fn = nullptr;
     if (!fn) {
         void* p = nullptr;
@@ -751,6 +749,8 @@ EncodeTiled encoder() {
     return fn;
 }
 
+namespace {
+
 // rows of packed weights (bytes), one plane per expert record
 bool map_weight_rows(CUtensorMap* tm, const uint8_t* base, size_t row_b, int rows, int recs, size_t rec_b,
                      uint32_t box_x, CUtensorMapSwizzle swz) {
@@ -758,7 +758,7 @@ bool map_weight_rows(CUtensorMap* tm, const uint8_t* base, size_t row_b, int row
     const cuuint64_t strides[2] = {row_b, rec_b};
     const cuuint32_t box[3] = {box_x, 128, 1};
     const cuuint32_t es[3] = {1, 1, 1};
-    return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, es,
+    return tensor_map_encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(base), dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, swz, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -769,7 +769,7 @@ bool map_act(CUtensorMap* tm, void* base, int K, int rows, uint32_t box_rows) {
     const cuuint64_t strides[1] = {(cuuint64_t)K * 2};
     const cuuint32_t box[2] = {64, box_rows};
     const cuuint32_t es[2] = {1, 1};
-    return encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, es,
+    return tensor_map_encoder()(tm, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, es,
                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -802,7 +802,7 @@ cudaError_t prefill_kernel_setup(Layer& L) {
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(g1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kGemmSmem);
     if (e != cudaSuccess) return e;
-    if (!encoder()) return cudaErrorSymbolNotFound;
+    if (!tensor_map_encoder()) return cudaErrorSymbolNotFound;
     const int H = d.hidden, I = d.inter;
     // device records: every expert and the shared one (resident layers), or
     // the shared one alone (streamed layers: routed experts live in the cache slots)
