@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -654,77 +655,96 @@ class MoELayer:
         return moe_layer_device_bytes(self.handle)
 
 
-def _dtype_id(t) -> int:
-    name = str(t.dtype).rsplit(".", 1)[-1]
-    ids = {"float32": MOE_F32, "bfloat16": MOE_BF16, "float8_e4m3fn": MOE_E4M3}
-    if name not in ids:
-        raise TypeError(f"no moe_dtype for {t.dtype}")
-    return ids[name]
+def _refuse(t, name: str, shape, dtype, device: int):
+    raise ValueError(f"{name}: expected {dtype} {tuple(shape)} on cuda:{device}, last dimensions contiguous; got "
+                     f"{t.dtype} {tuple(t.shape)} on {t.device}, strides {tuple(t.stride())}")
 
 
-def _want(t, name: str, shape, dtype: str, device=None, inner=None):
-    """Reject a tensor of another shape, type or device before its address is
-    taken; the last `inner` dimensions must be contiguous (None: all)."""
-    if tuple(t.shape) != tuple(shape) or str(t.dtype) != f"torch.{dtype}":
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name}: expected a tensor on {device}, got {t.device}")
-    step = 1
-    for d in reversed(range(len(shape) - (len(shape) if inner is None else inner), len(shape))):
-        if shape[d] != 1 and t.stride(d) != step:
-            raise ValueError(f"{name}: its last dimensions must be contiguous, strides are {tuple(t.stride())}")
-        step *= shape[d]
-    return t
+def _dense(t, name: str, shape, dtype, device: int) -> int:
+    """Address of a contiguous tensor of this shape, type and CUDA device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, name, shape, dtype, device)
+    return t.data_ptr()
 
 
-def _row_stride(t, width: int) -> int:
-    """Elements between rows of a [rows, ...] tensor (a single row has no stride of its own)."""
-    return t.stride(0) if t.shape[0] > 1 else width
+def _rows(t, name: str, shape, dtype, device: int) -> int:
+    """Elements between the rows (first dimension) of a tensor of this shape,
+    type and CUDA device whose other dimensions are contiguous."""
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        _refuse(t, name, shape, dtype, device)
+    if len(shape) == 2:
+        rows, width = shape
+        if st[1] != 1:
+            _refuse(t, name, shape, dtype, device)
+    else:
+        rows, heads, width = shape
+        if st[2] != 1 or (st[1] != width and heads != 1):
+            _refuse(t, name, shape, dtype, device)
+        width *= heads
+    return st[0] if rows > 1 else width   # a single row has no stride of its own
 
 
 class BlockNorm:
     """The norms between two blocks of a decoder layer (moe_block_norm): keeps
-    the weights, fp32 [hidden] on the device; w_post and w_pre may be None."""
+    the weights, fp32 [hidden] on the device; w_post and w_pre may be None. One
+    object serves one host thread at a time."""
+
+    # moe_block_norm_desc, packed in place: the fields a call sets cost it one pack
+    _desc = struct.Struct("Iiiiifffqqqqq")
 
     def __init__(self, hidden: int, w_post=None, w_pre=None, eps: float = 1e-6, scale: float = 1.0,
                  weight_offset: float = 0.0):
+        import torch
         self.hidden, self.eps, self.scale, self.weight_offset = hidden, eps, scale, weight_offset
+        self.device = None
         for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-            if w is not None:
-                _want(w, name, (hidden,), "float32")
+            if w is None:
+                continue
+            _dense(w, name, (hidden,), torch.float32, w.get_device())
+            if self.device not in (None, w.get_device()):
+                raise ValueError("w_post and w_pre are on two devices")
+            self.device = w.get_device()
         self.w_post, self.w_pre = w_post, w_pre
+        self._ids = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+        self._buf = ctypes.create_string_buffer(ctypes.sizeof(moe_block_norm_desc))
+        vp, i32 = ctypes.c_void_p, ctypes.c_int32
+        self._call = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 8, i32, i32, vp)(("moe_block_norm", lib()))
 
     def run(self, x, o=None, r=None, h=None, gate=None, stream=None):
         """x [T, H] residual, o [T, H] the block's output or None, r [T, H]
         (may be x) and h [T, H] the outputs (either may be None), gate [T, H],
         [1, H] or [H] of o's type."""
-        H = self.hidden
-        if x.dim() != 2 or x.device.type != "cuda":
-            raise ValueError("x must be a CUDA tensor [T, hidden]")
-        T, dev = x.shape[0], x.device
-
-        def rows(t, name, like=None):
-            if t is None:
-                return 0
-            _want(t, name, (T, H), str((t if like is None else like).dtype)[6:], dev, 1)
-            return _row_stride(t, H)
-
-        for w in (self.w_post, self.w_pre):
-            if w is not None and w.device != dev:
-                raise ValueError(f"the norm's weights are on {w.device}, x on {dev}")
+        ids, H, dev = self._ids, self.hidden, x.get_device()
+        if x.dim() != 2 or dev < 0 or self.device not in (None, dev):
+            raise ValueError("x must be a CUDA tensor [T, hidden] on the weights' device")
+        shape = (x.shape[0], H)
+        res, blk, out = x.dtype, x.dtype if o is None else o.dtype, x.dtype if h is None else h.dtype
+        if res not in ids or blk not in ids or out not in ids:
+            raise TypeError("x, o and h must be float32 or bfloat16")
         gs = 0
         if gate is not None:
             if o is None:
                 raise ValueError("gate needs o")
-            if gate.dim() == 1 or (gate.shape[0] == 1 and T != 1):
-                _want(gate.reshape(-1), "gate", (H,), str(o.dtype)[6:], dev)
+            if gate.dim() == 1:
+                _dense(gate, "gate", (H,), blk, dev)
+            elif gate.shape[0] == 1:
+                _dense(gate, "gate", (1, H), blk, dev)
             else:
-                gs = rows(gate, "gate", o)
-        desc = moe_block_norm_desc(MOE_ABI_VERSION, H, _dtype_id(x), _dtype_id(o) if o is not None else MOE_BF16,
-                                   _dtype_id(h) if h is not None else MOE_BF16, self.eps, self.scale,
-                                   self.weight_offset, rows(x, "x"), rows(o, "o"), gs, rows(r, "r", x), rows(h, "h"))
-        moe_block_norm(desc, x, o, gate, self.w_post if o is not None else None,
-                       self.w_pre if h is not None else None, r, h, T, dev.index or 0, stream)
+                gs = _rows(gate, "gate", shape, blk, dev)
+        self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, H, ids[res], ids[blk], ids[out], self.eps, self.scale,
+                             self.weight_offset, _rows(x, "x", shape, res, dev),
+                             0 if o is None else _rows(o, "o", shape, blk, dev), gs,
+                             0 if r is None else _rows(r, "r", shape, res, dev),
+                             0 if h is None else _rows(h, "h", shape, out, dev))
+        st = self._call(ctypes.addressof(self._buf), x.data_ptr(), None if o is None else o.data_ptr(),
+                        None if gate is None else gate.data_ptr(),
+                        None if o is None or self.w_post is None else self.w_post.data_ptr(),
+                        None if h is None or self.w_pre is None else self.w_pre.data_ptr(),
+                        None if r is None else r.data_ptr(), None if h is None else h.data_ptr(), shape[0], dev,
+                        _stream(stream))
+        if st:
+            _check(st, "moe_block_norm")
 
 
 class KVCache:
@@ -732,11 +752,19 @@ class KVCache:
     page_size, head_dim] of bfloat16 or float8_e4m3fn in any memory order whose
     last dimension is contiguous (token-major pages: a permuted view)."""
 
+    # moe_kv_append_args and moe_kv_attend_args, packed in place
+    _append_args = struct.Struct("PPPqqqPPPiiiP")
+    _attend_args = struct.Struct("PqPPiiffiPP")
+
     def __init__(self, k_pages, v_pages, n_heads: int, inv_freq=None, interleaved: bool = False, k_scale=None,
                  v_scale=None, max_batch: int = 1):
         import numpy as np
+        import torch
+        kinds = {torch.bfloat16: MOE_BF16, torch.float8_e4m3fn: MOE_E4M3}
         n_pages, hk, page, d = k_pages.shape
-        if k_pages.device.type != "cuda" or v_pages.device != k_pages.device:
+        if k_pages.dtype not in kinds:
+            raise TypeError("the pools must be bfloat16 or float8_e4m3fn")
+        if not k_pages.is_cuda or v_pages.device != k_pages.device:
             raise ValueError("k_pages and v_pages must be CUDA tensors on one device")
         if v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride() or v_pages.dtype != k_pages.dtype:
             raise ValueError("k_pages and v_pages must have one shape, type and memory order")
@@ -748,11 +776,18 @@ class KVCache:
             if s is not None and s.shape != (hk,):
                 raise ValueError("k_scale and v_scale hold one value per key-value head")
         self.k_pages, self.v_pages = k_pages, v_pages
-        self.desc = moe_kv_desc(MOE_ABI_VERSION, n_heads, hk, d, page, n_pages, _dtype_id(k_pages),
+        self.device = k_pages.get_device()
+        self.desc = moe_kv_desc(MOE_ABI_VERSION, n_heads, hk, d, page, n_pages, kinds[k_pages.dtype],
                                 0 if freq is None else 2 * freq.size, int(interleaved), max_batch,
                                 k_pages.stride(0), k_pages.stride(1), k_pages.stride(2))
         self.handle = moe_kv_create(self.desc, k_pages, v_pages, freq if freq is None or freq.size else None,
-                                    scales[0], scales[1], k_pages.device.index or 0)
+                                    scales[0], scales[1], self.device)
+        self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
+        self._heads = (n_heads, hk, d)
+        self._buf = ctypes.create_string_buffer(max(self._append_args.size, self._attend_args.size))
+        proto = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
+        self._append_call = proto(("moe_kv_append", lib()))
+        self._attend_call = proto(("moe_kv_attend", lib()))
 
     def close(self):
         if getattr(self, "handle", None):
@@ -775,41 +810,42 @@ class KVCache:
         """Rotate and cache T tokens: q [T, n_heads, d] (or None with q_out), k
         and v [T, n_kv_heads, d], positions and seq int32 [T], block_table int32
         [n_seqs, max_pages]."""
-        d, dev = self.desc, self.k_pages.device
-        T, hk, hq, dim = k.shape[0], d.n_kv_heads, d.n_heads, d.head_dim
-        _want(k, "k", (T, hk, dim), "bfloat16", dev, 2)
-        _want(v, "v", (T, hk, dim), "bfloat16", dev, 2)
-        if q is not None:
-            _want(q, "q", (T, hq, dim), "bfloat16", dev, 2)
-        if q_out is not None:
-            _want(q_out, "q_out", (T, hq, dim), "bfloat16", dev)
-        _want(positions, "positions", (T,), "int32", dev)
-        if seq is not None:
-            _want(seq, "seq", (T,), "int32", dev)
-        _want(block_table, "block_table", tuple(block_table.shape), "int32", dev)
-        n_seqs, max_pages = block_table.shape
-        args = moe_kv_append_args(_addr(q), _addr(k), _addr(v), 0 if q is None else _row_stride(q, hq * dim),
-                                  _row_stride(k, hk * dim), _row_stride(v, hk * dim), _addr(positions), _addr(seq),
-                                  _addr(block_table), T, n_seqs, max_pages, _addr(q_out))
-        moe_kv_append(self.handle, args, stream)
+        hq, hk, d = self._heads
+        dev, bf16, i32 = self.device, self._bf16, self._i32
+        T = k.shape[0]
+        shape, table = (T, hk, d), block_table.shape
+        if len(table) != 2:
+            raise ValueError("block_table must be [n_seqs, max_pages]")
+        self._append_args.pack_into(
+            self._buf, 0, 0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            0 if q is None else _rows(q, "q", (T, hq, d), bf16, dev), _rows(k, "k", shape, bf16, dev),
+            _rows(v, "v", shape, bf16, dev), _dense(positions, "positions", (T,), i32, dev),
+            0 if seq is None else _dense(seq, "seq", (T,), i32, dev),
+            _dense(block_table, "block_table", table, i32, dev), T, table[0], table[1],
+            0 if q_out is None else _dense(q_out, "q_out", (T, hq, d), bf16, dev))
+        st = self._append_call(self.handle, ctypes.addressof(self._buf), _stream(stream))
+        if st:
+            _check(st, "moe_kv_append")
 
     def attend(self, q, block_table, lens, out, lse=None, scale=None, softcap: float = 0.0, window: int = 0,
                stream=None):
         """Attention of one new token per sequence: q and out [B, n_heads, d]
         bf16, lens int32 [B], block_table int32 [B, max_pages], lse fp32
         [B, n_heads] or None; scale defaults to 1 / sqrt(d)."""
-        d, dev = self.desc, self.k_pages.device
-        B = q.shape[0]
-        _want(q, "q", (B, d.n_heads, d.head_dim), "bfloat16", dev, 2)
-        _want(out, "out", (B, d.n_heads, d.head_dim), "bfloat16", dev)
-        _want(lens, "lens", (B,), "int32", dev)
-        _want(block_table, "block_table", (B, block_table.shape[1]), "int32", dev)
-        if lse is not None:
-            _want(lse, "lse", (B, d.n_heads), "float32", dev)
-        args = moe_kv_attend_args(_addr(q), _row_stride(q, d.n_heads * d.head_dim), _addr(block_table), _addr(lens), B,
-                                  block_table.shape[1], d.head_dim ** -0.5 if scale is None else scale, softcap,
-                                  window, _addr(out), _addr(lse))
-        moe_kv_attend(self.handle, args, stream)
+        hq, _, d = self._heads
+        dev, bf16, i32 = self.device, self._bf16, self._i32
+        B, table = q.shape[0], block_table.shape
+        shape = (B, hq, d)
+        if len(table) != 2:
+            raise ValueError("block_table must be [B, max_pages]")
+        self._attend_args.pack_into(
+            self._buf, 0, q.data_ptr(), _rows(q, "q", shape, bf16, dev),
+            _dense(block_table, "block_table", (B, table[1]), i32, dev), _dense(lens, "lens", (B,), i32, dev), B,
+            table[1], d ** -0.5 if scale is None else scale, softcap, window, _dense(out, "out", shape, bf16, dev),
+            0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
+        st = self._attend_call(self.handle, ctypes.addressof(self._buf), _stream(stream))
+        if st:
+            _check(st, "moe_kv_attend")
 
     def locate(self, block_table, seq: int, position: int, head: int = 0) -> int:
         """Element offset of a cached row in a pool (block_table on the host)."""

@@ -42,9 +42,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 48 * 1024;   // bytes of stages per warp
+constexpr int kRing = 24 * 1024;   // bytes of stages per warp
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
@@ -56,13 +56,15 @@ struct Cfg {
     static constexpr int CT = RB >= 512 ? 16 : RB >= 256 ? 32 : 64;  // tokens of a chunk
     static constexpr int LINE = RB < 128 ? RB : 128;          // bytes of a shared-memory row (the swizzle's width)
     static constexpr int COLS = RB / LINE;                    // column blocks of a row
-    static constexpr int HALF = CT * RB;                      // bytes of a chunk's keys (or values)
-    static constexpr int STAGES = kRing / (2 * HALF);
+    static constexpr int HALF = CT * RB;                      // bytes of a chunk's keys (or values): one stage
+    static constexpr int STAGES = kRing / HALF;
     static constexpr int HEADS = 8 * NT;
     static constexpr int MT = CT / 16, KS = D / 16, DT = D / 16;
+    static constexpr int UNITS = LINE / 32;                   // 32-byte steps of a line
+    static constexpr int STEPS = RB / 32;                     // and of a row
     static constexpr int OPAD = D + 4;                        // floats of a head in the join buffer
+    static constexpr int JH = 512 / D;                        // heads joined at a time (shared memory)
     static constexpr size_t ring_bytes = (size_t)kWarps * kRing;
-    static constexpr int JH = D == 256 ? 4 : 8;               // heads joined at a time (shared memory)
     static constexpr size_t join_bytes = (size_t)kWarps * JH * OPAD * 4;
     static constexpr size_t smem = 1024 + ring_bytes + join_bytes;
 };
@@ -138,15 +140,13 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm,
         : "memory");
 }
 
-// Shared address of byte `col` of row `row` of a chunk half: rows of LINE bytes,
-// 16-byte units exchanged within 8 (128-byte lines) or 4 (64-byte lines) of them as
-// the TMA swizzle does.
+// Offset of byte `col` (within one line) of row `row` of a stage: rows of LINE
+// bytes, their 16-byte units exchanged as the TMA swizzle does, within 8 of them
+// (128-byte lines) or 4 (64-byte lines). Further column blocks follow CT * LINE on.
 template <class C>
-__device__ __forceinline__ uint32_t tile_at(uint32_t base, int row, int col) {
-    if constexpr (C::LINE == 128)
-        return base + (col >> 7) * (C::CT * 128) + row * 128 + ((col & 127) ^ ((row & 7) << 4));
-    else
-        return base + row * 64 + (col ^ (((row >> 1) & 3) << 4));
+__device__ __forceinline__ uint32_t line_at(int row, int col) {
+    if constexpr (C::LINE == 128) return row * 128 + (col ^ ((row & 7) << 4));
+    else return row * 64 + (col ^ (((row >> 1) & 3) << 4));
 }
 
 // A position in the chunk sequence: unit u, in the segment (sequence b, head
@@ -270,14 +270,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
 
         // ---- the copies of this warp ----------------------------------------------------
-        // Box i of a chunk: rows [box * box_rows, ...), one column block, keys or
-        // values; lane i looks its page up one chunk ahead of its issue.
+        // Stages hold a chunk's keys, then its values, in turn. Box i of either: rows
+        // [box * box_rows, ...), one column block; lane i looks its page up a chunk ahead.
         const int boxes = CT / p.box_rows;
-        const int bx = lane % boxes, col = (lane / boxes) % C::COLS, is_v = lane / (boxes * C::COLS);
-        const bool issuer = lane < boxes * C::COLS * 2;
+        const int bx = lane % boxes, col = lane / boxes;
+        const bool issuer = col < C::COLS;
         const uint64_t pol = bw::l2_evict_first();
         const uint32_t box_bytes = p.box_rows * C::LINE;
-        const CUtensorMap* tm = is_v ? &tm_v : &tm_k;
+        const uint32_t box_at = col * (CT * C::LINE) + bx * box_bytes;
         Place nx = at;             // the chunk whose pages are being looked up
         int nx_page = -1, nx_slot = 0;
         bool nx_live = false, nx_read = false;
@@ -297,37 +297,56 @@ __global__ void __launch_bounds__(kThreads, 1)
                 nx_slot = tok % s.page_size;
             }
         };
-        int issued = 0;
-        auto issue = [&]() {       // the looked-up chunk into the next stage
-            const int st = issued % C::STAGES;
-            const uint32_t bar = bw::saddr(&sm_bar[warp][st]);
+        int64_t ahead = u0 + warp;
+        int issued = 0, put = 0;   // stages issued, and the stage after them
+        auto issue = [&]() {       // the looked-up chunk's keys or values into the next stage
             if (nx_read && (nx_page < 0 || nx_page >= s.n_pages)) {
                 bits |= MOE_KV_BAD_PAGE;
                 nx_page = -1;
             }
+            const uint32_t bar = bw::saddr(&sm_bar[warp][put]);
             const unsigned have = __ballot_sync(~0u, nx_page >= 0);
             if (lane == 0) {
                 bw::mbar_arrive_tx(bar, __popc(have) * box_bytes);
                 uint32_t rows = 0;
                 for (int i = 0; i < boxes; ++i)
                     if (have >> i & 1) rows |= ((1u << (p.box_rows / 16)) - 1) << (i * p.box_rows / 16);
-                sm_rows[warp][st] = rows;
+                sm_rows[warp][put] = rows;
             }
             __syncwarp();
             if (nx_page >= 0)
-                tma_load_4d(ring + st * 2 * C::HALF + is_v * C::HALF + col * (CT * 128) + bx * p.box_rows * C::LINE, tm,
-                            col * (C::FP8 ? 128 : 64), nx_slot, nx.ht / tiles, nx_page, bar, pol);
-            ++issued;
+                tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
+                            nx.ht / tiles, nx_page, bar, pol);
+            if (++put == C::STAGES) put = 0;
+            if (!(++issued & 1)) lookup(ahead += kWarps);
         };
-        int64_t ahead = u0 + warp;
         lookup(ahead);
-        for (int i = 0; i < C::STAGES && nx_live; ++i) {
-            issue();
-            lookup(ahead += kWarps);
+        for (int i = 0; i < C::STAGES && nx_live; ++i) issue();
+
+        // this lane's rows for ldmatrix: of operand A of K Q^T, and of V^T P^T transposed
+        uint32_t ka[C::UNITS], va[C::UNITS];
+#pragma unroll
+        for (int i = 0; i < C::UNITS; ++i) {
+            ka[i] = line_at<C>((lane & 7) + ((lane >> 3) & 1) * 8, i * 32 + (lane >> 4) * 16);
+            va[i] = C::FP8 ? ka[i] : line_at<C>((lane & 7) + (lane >> 4) * 8, i * 32 + ((lane >> 3) & 1) * 16);
         }
 
         // ---- segments ------------------------------------------------------------------
-        int done = 0;                    // chunks of this warp consumed
+        int take = 0;                    // the stage to be consumed next, and its barrier's phase
+        uint32_t phase = 0;
+        auto next_stage = [&]() {        // waits for it; the stage's shared address
+            bw::mbar_wait(bw::saddr(&sm_bar[warp][take]), phase, &sm_abort, p.health, MOE_KV_TIMEOUT);
+            __syncwarp();
+            return ring + take * C::HALF;
+        };
+        auto release = [&]() {           // every lane has read it: fill it again
+            if (++take == C::STAGES) {
+                take = 0;
+                phase ^= 1;
+            }
+            __syncwarp();
+            if (nx_live) issue();
+        };
         int64_t cur = u0 + warp;         // this warp's next chunk
         for (seek(at, u0);; seek(at, at.end)) {
             const int64_t seg_end = min(at.end, u1);
@@ -382,11 +401,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 pack_pair<true>(__uint_as_float(v << 16) * up, __uint_as_float(v & 0xffff0000u) * up);
                         }
                 }
-                const float k = p.k_scale[hk] * p.a.scale;
+                // a negative scale turns the queries, so that the largest product has the largest score
+                if (p.a.scale < 0.f)
+#pragma unroll
+                    for (int ks = 0; ks < C::KS; ++ks)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) qf[ks][nt][i] ^= 0x80008000u;
+                const float k = p.k_scale[hk] * fabsf(p.a.scale);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     coef[nt][c] = k * __shfl_sync(~0u, unit, (2 * j + c) * 4);
-                    if (p.a.softcap == 0.f) coef[nt][c] *= kLog2e;
+                    if (p.a.softcap == 0.f) coef[nt][c] *= kLog2e;   // in base two
+                    coef[nt][c] = fmaxf(coef[nt][c], 1.2e-38f);      // keeps -inf times it -inf
                     m[nt][c] = -INFINITY;
                     l[nt][c] = 0.f;
                 }
@@ -397,12 +423,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
 
             for (; cur < seg_end; cur += kWarps) {
-                const int st = done % C::STAGES;
-                const uint32_t kt = ring + st * 2 * C::HALF, vt = kt + C::HALF;
-                bw::mbar_wait(bw::saddr(&sm_bar[warp][st]), (done / C::STAGES) & 1, &sm_abort, p.health, MOE_KV_TIMEOUT);
-                __syncwarp();
                 const int tok0 = (first / CT + (int)(cur - at.beg)) * CT;
-                const uint32_t rows = sm_rows[warp][st];
+                const uint32_t rows = sm_rows[warp][take];
+                const uint32_t kt = next_stage();
                 const bool whole = tok0 >= first && tok0 + CT <= len && rows == (1u << C::MT) - 1;
 
                 float sc[C::MT][NT][4];
@@ -412,68 +435,76 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) sc[mt][nt][i] = 0.f;
-                if constexpr (!C::FP8) {
-                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
 #pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks)
+                for (int st = 0; st < C::STEPS; ++st)
 #pragma unroll
-                        for (int mt = 0; mt < C::MT; ++mt) {
-                            uint32_t a[4];
-                            ldm4(a, tile_at<C>(kt, mt * 16 + row, ks * 32 + cb));
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        uint32_t r[4];
+                        ldm4(r, kt + ka[st % C::UNITS] + (st / C::UNITS) * (CT * C::LINE) + mt * 16 * C::LINE);
+                        if constexpr (!C::FP8) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma<false>(sc[mt][nt], a, qf[ks][nt][0], qf[ks][nt][1]);
-                        }
-                } else {
-                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
-#pragma unroll
-                    for (int ks = 0; ks < C::KS; ks += 2)
-#pragma unroll
-                        for (int mt = 0; mt < C::MT; ++mt) {
-                            uint32_t r[4];
-                            ldm4(r, tile_at<C>(kt, mt * 16 + row, ks * 16 + cb));
+                            for (int nt = 0; nt < NT; ++nt) mma<false>(sc[mt][nt], r, qf[st][nt][0], qf[st][nt][1]);
+                        } else {
 #pragma unroll
                             for (int k2 = 0; k2 < 2; ++k2) {
                                 const uint32_t a[4] = {e4m3_pair(r[2 * k2]), e4m3_pair(r[2 * k2 + 1]),
                                                        e4m3_pair(r[2 * k2] >> 16), e4m3_pair(r[2 * k2 + 1] >> 16)};
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma<true>(sc[mt][nt], a, qf[ks + k2][nt][0], qf[ks + k2][nt][1]);
+                                    mma<true>(sc[mt][nt], a, qf[2 * st + k2][nt][0], qf[2 * st + k2][nt][1]);
                             }
                         }
-                }
+                    }
+                release();
 
-                // which of this lane's tokens are attended: rows g and g + 8 of each tile
+                // tanh(z) = 1 - 2 / (exp(2 z) + 1): off by 2^-22 of the cap
+                if (p.a.softcap != 0.f) {
+#pragma unroll
+                    for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float e = ex2(sc[mt][nt][i] * coef[nt][i & 1] * (2.f * kLog2e / p.a.softcap));
+                                sc[mt][nt][i] = p.a.softcap - __fdividef(2.f * p.a.softcap, e + 1.f);
+                            }
+                }
+                // which tokens are attended
                 auto seen = [&](int t) {
                     const int tok = tok0 + t;
                     return tok >= first && tok < len && (rows >> (t >> 4) & 1);
                 };
-                uint32_t pf[C::MT][NT][2];   // weights: operand B of O^T = V^T P^T
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    float mx[2] = {m[nt][0], m[nt][1]};
+                if (!whole) {
 #pragma unroll
                     for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float x = sc[mt][nt][i] * coef[nt][i & 1];
-                            if (p.a.softcap != 0.f) {
-                                // tanh(z) = 1 - 2 / (exp(2 z) + 1): off by 2^-22 of the cap
-                                const float e = ex2(x * (2.f * kLog2e / p.a.softcap));
-                                x = (p.a.softcap - 2.f * p.a.softcap / (e + 1.f)) * kLog2e;
-                            }
-                            if (!whole && !seen(mt * 16 + g + (i & 2) * 4)) x = -INFINITY;
-                            sc[mt][nt][i] = x;
-                            mx[i & 1] = fmaxf(mx[i & 1], x);
+                        for (int i = 0; i < 4; i += 2) {
+                            const bool on = seen(mt * 16 + g + i * 4);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+                                    if (!on) sc[mt][nt][i + c] = -INFINITY;
                         }
-                    float f[2], base[2];
+                }
+                uint32_t pf[C::MT][NT][2];   // weights: operand B of O^T = V^T P^T
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+                    // scores in base two are `unit` times sc, unit > 0
+                    float unit[2], base[2], f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 4));
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 8));
-                        mx[c] = fmaxf(mx[c], __shfl_xor_sync(~0u, mx[c], 16));
-                        base[c] = mx[c] == -INFINITY ? 0.f : mx[c];
+                        unit[c] = p.a.softcap != 0.f ? kLog2e : coef[nt][c];
+                        float x = sc[0][nt][c];
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt) x = fmaxf(x, fmaxf(sc[mt][nt][c], sc[mt][nt][c + 2]));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+                        x = fmaxf(m[nt][c], x * unit[c]);
+                        base[c] = x == -INFINITY ? 0.f : x;
                         f[c] = ex2(m[nt][c] - base[c]);
-                        m[nt][c] = mx[c];
+                        m[nt][c] = x;
                         l[nt][c] *= f[c];
                     }
                     if (__any_sync(~0u, f[0] != 1.f || f[1] != 1.f))
@@ -486,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            w[i] = ex2(sc[mt][nt][i] - base[i & 1]);
+                            w[i] = ex2(fmaf(sc[mt][nt][i], unit[i & 1], -base[i & 1]));
                             l[nt][i & 1] += w[i];
                         }
                         pf[mt][nt][0] = transpose8(pack_pair<C::FP8>(w[0], w[1]));
@@ -495,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
 
                 // values: tokens that are not attended may hold anything, so their bits are cleared
+                const uint32_t vt = next_stage();
 #pragma unroll
                 for (int mt = 0; mt < C::MT; ++mt) {
                     uint32_t keep[2] = {~0u, ~0u};
@@ -503,52 +535,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 2; ++i)
                             keep[i] = (seen(mt * 16 + 8 * i + 2 * j) ? 0xffffu : 0u) |
                                       (seen(mt * 16 + 8 * i + 2 * j + 1) ? 0xffff0000u : 0u);
-                    if constexpr (!C::FP8) {
-                        const int row = (lane & 7) + (lane >> 4) * 8, cb = ((lane >> 3) & 1) * 16;
 #pragma unroll
-                        for (int dt = 0; dt < C::DT; ++dt) {
-                            uint32_t a[4];
-                            ldm4t(a, tile_at<C>(vt, mt * 16 + row, dt * 32 + cb));
-                            if (!whole) {
-                                a[0] &= keep[0];
-                                a[1] &= keep[0];
-                                a[2] &= keep[1];
-                                a[3] &= keep[1];
-                            }
+                    for (int st = 0; st < C::STEPS; ++st) {
+                        uint32_t r[4];
+                        ldm4t(r, vt + va[st % C::UNITS] + (st / C::UNITS) * (CT * C::LINE) + mt * 16 * C::LINE);
+                        if constexpr (!C::FP8) {
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma<false>(o[dt][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
-                        }
-                    } else {
-                        const int row = (lane & 7) + ((lane >> 3) & 1) * 8, cb = (lane >> 4) * 16;
+                            for (int i = 0; i < 4; ++i) r[i] &= keep[i >> 1];
 #pragma unroll
-                        for (int dt = 0; dt < C::DT; dt += 2) {
-                            uint32_t r[4];
-                            ldm4t(r, tile_at<C>(vt, mt * 16 + row, dt * 16 + cb));
+                            for (int nt = 0; nt < NT; ++nt) mma<false>(o[st][nt], r, pf[mt][nt][0], pf[mt][nt][1]);
+                        } else {
 #pragma unroll
                             for (int d2 = 0; d2 < 2; ++d2) {
                                 // bytes: channels 2g, 2g + 1 of token 2j, then of token 2j + 1
                                 const uint32_t x = __byte_perm(r[2 * d2], 0, 0x3120);
                                 const uint32_t y = __byte_perm(r[2 * d2 + 1], 0, 0x3120);
-                                uint32_t a[4] = {e4m3_pair(x), e4m3_pair(x >> 16), e4m3_pair(y), e4m3_pair(y >> 16)};
-                                if (!whole) {
-                                    a[0] &= keep[0];
-                                    a[1] &= keep[0];
-                                    a[2] &= keep[1];
-                                    a[3] &= keep[1];
-                                }
+                                const uint32_t a[4] = {e4m3_pair(x) & keep[0], e4m3_pair(x >> 16) & keep[0],
+                                                       e4m3_pair(y) & keep[1], e4m3_pair(y >> 16) & keep[1]};
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
-                                    mma<true>(o[dt + d2][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+                                    mma<true>(o[2 * st + d2][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
                             }
                         }
                     }
                 }
-                ++done;
-                __syncwarp();   // every lane has read the stage before it is filled again
-                if (nx_live) {
-                    issue();
-                    lookup(ahead += kWarps);
-                }
+                release();
             }
 
             // ---- the warps' results are joined -------------------------------------------
@@ -633,32 +644,53 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // the first CTA's part is its second slot (its segment begins there), the
                     // others' their first
                     auto slot_of = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
+                    // each part's factor, a warp per head; the join buffer is free here
+                    float* fac = join;       // [heads][n]
+                    for (int h = warp; h < heads; h += kWarps) {
+                        float M = -INFINITY, L = 0.f;
+                        for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + h]).x);
+                        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+                        const float mb = M == -INFINITY ? 0.f : M;
+                        for (int i = lane; i < n; i += 32) {
+                            const float2 ml = __ldcg(&p.part_ml[slot_of(i) * 16 + h]);
+                            const float f = ex2(ml.x - mb);
+                            fac[h * n + i] = f;
+                            L += f * ml.y;
+                        }
+                        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+                        if (lane == 0) {
+                            sm_l[0][h] = L;
+                            if (p.a.lse)
+                                p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+                        }
+                    }
+                    __syncthreads();
                     for (int it = threadIdx.x; it < heads * (D / 4); it += kThreads) {
                         const int h = it / (D / 4), d = it % (D / 4) * 4;
-                        float M = -INFINITY, L = 0.f;
+                        const float* src = p.part_o + (int64_t)h * D + d;
                         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-                        for (int i = 0; i < n; ++i) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + h]).x);
-                        const float mb = M == -INFINITY ? 0.f : M;
-#pragma unroll 8
-                        for (int i = 0; i < n; ++i) {
-                            const float2 ml = __ldcg(&p.part_ml[slot_of(i) * 16 + h]);
-                            const float4 v = __ldcg(
-                                reinterpret_cast<const float4*>(p.part_o + ((int64_t)slot_of(i) * 16 + h) * D + d));
-                            const float f = ex2(ml.x - mb);
-                            L += f * ml.y;
-                            a.x += f * v.x;
-                            a.y += f * v.y;
-                            a.z += f * v.z;
-                            a.w += f * v.w;
+                        for (int i0 = 0; i0 < n; i0 += 16) {
+                            float4 v[16];
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i0 + i < n)
+                                    v[i] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)slot_of(i0 + i) * 16 * D));
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (i0 + i < n) {
+                                    const float f = fac[h * n + i0 + i];
+                                    a.x += f * v[i].x;
+                                    a.y += f * v[i].y;
+                                    a.z += f * v[i].z;
+                                    a.w += f * v[i].w;
+                                }
                         }
-                        const float r = L == 0.f ? 0.f : vs / L;
+                        const float r = sm_l[0][h] == 0.f ? 0.f : vs / sm_l[0][h];
                         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) +
                                                   ((int64_t)at.b * s.n_heads + h0 + h) * D + d) =
                             make_uint2(pack_pair<false>(a.x * r, a.y * r), pack_pair<false>(a.z * r, a.w * r));
-                        if (d == 0 && p.a.lse)
-                            p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
                     }
+                    __syncthreads();
                 }
             }
             if (at.end >= u1) break;

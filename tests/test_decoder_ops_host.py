@@ -45,6 +45,17 @@ def refused(fn, *args, status=1):
     return str(ei.value)
 
 
+def test_packed_structures_match_the_ctypes_ones():
+    """The classes pack their arguments with struct; the layouts are those of the header's types."""
+    for packed, c in ((moe.KVCache._append_args, moe.moe_kv_append_args),
+                      (moe.KVCache._attend_args, moe.moe_kv_attend_args), (moe.BlockNorm._desc, moe.moe_block_norm_desc)):
+        assert len(packed.unpack(bytes(packed.size))) == len(c._fields_)
+        buf = bytearray(ctypes.sizeof(c))
+        packed.pack_into(buf, 0, *range(1, len(c._fields_) + 1))
+        got = c.from_buffer(buf)
+        assert [getattr(got, n) for n, _ in c._fields_] == list(range(1, len(c._fields_) + 1))
+
+
 def test_good_arguments_pass():
     moe.moe_kv_append_check(kv_desc(), append_args())
     moe.moe_kv_append_check(kv_desc(), append_args(q=None, q_out=None, q_stride=0))

@@ -153,6 +153,14 @@ def test_sharp_and_flat_scores():
     c.check()
 
 
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("scale,cap", [(0.0, 0.0), (-0.09, 0.0), (0.0, 5.0), (-0.2, 3.0)])
+def test_scales_of_zero_and_below(scale, cap, dt):
+    c = Case([1, 100, 77], 4, 2, 64, 16, dt, seed=13)
+    c.scale = scale
+    c.check(softcap=cap)
+
+
 def test_strided_queries():
     c = Case([200, 31, 64], 8, 2, 64, 16, seed=5)
     wide = torch.full((3, 8 * 64 + 192), torch.nan, dtype=BF16, device="cuda")
