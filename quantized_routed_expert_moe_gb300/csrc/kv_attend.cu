@@ -4,21 +4,21 @@
 // n_kv_heads queries of its head, so the kernel is a stream over the cache:
 // its floor is the cached bytes at the copy rate.
 //
-// Split. The attended tokens of every (sequence, head tile) are cut into chunks
-// of 8 KB of keys and 8 KB of values; all chunks of the call, numbered sequence by
-// sequence, are dealt out evenly and contiguously to one resident CTA per SM,
-// from the lengths as they stand on the device. A ragged batch, one long
-// sequence and thousands of short ones are balanced alike, and the call is one
-// launch. A (sequence, head tile) that is cut between CTAs is joined by the one of
-// them that finishes last, in CTA order, so the result does not depend on which
-// one that is.
+// Split. The attended tokens of every (sequence, head tile), a segment, are cut
+// into chunks of 8 KB of keys and 8 KB of values. All chunks of the call, numbered
+// segment by segment, are dealt out evenly and contiguously to one resident CTA
+// per SM and within it to eight warps, from the lengths as they stand on the device:
+// a ragged batch, one long sequence and thousands of short ones are balanced
+// alike, in one launch. A warp that holds a whole segment writes its output; parts
+// of a segment that is cut between warps are joined by their CTA at its end, and
+// those of one cut between CTAs by the CTA that finishes last, always in order, so
+// that results do not depend on which one that is.
 //
-// Within a CTA each of four warps takes every fourth chunk on its own: it copies
-// its chunks by TMA into its own ring of shared-memory stages (the swizzle lets
-// ldmatrix read them without bank conflicts), keeps its own running maximum, sum
-// and output, and meets the others only where a (sequence, head tile) ends. The
-// copies run ahead over those ends, so about 190 KB per SM are in flight or
-// waiting at any time, where the copy rate times the memory latency asks for 45.
+// A warp copies its chunks by TMA into its own ring of stages (keys and values
+// take turns; the swizzle lets ldmatrix read them without bank conflicts) and
+// meets no other warp before its end. The copies run ahead over the ends of
+// segments: up to 128 KB per SM are in flight, where the copy rate times the
+// memory latency asks for 45; more only queues up.
 //
 // Products. The tokens are the rows of the matrix instruction and the query
 // heads its 8 columns (mma m16n8k16), S^T = K Q^T and O^T = V^T P^T: up to 8 heads
@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kRing = 24 * 1024;   // bytes of stages per warp
+constexpr int kRing = 16 * 1024;   // bytes of stages per warp
+constexpr int kMaxCtas = 160;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
@@ -62,11 +63,9 @@ struct Cfg {
     static constexpr int MT = CT / 16, KS = D / 16, DT = D / 16;
     static constexpr int UNITS = LINE / 32;                   // 32-byte steps of a line
     static constexpr int STEPS = RB / 32;                     // and of a row
-    static constexpr int OPAD = D + 4;                        // floats of a head in the join buffer
-    static constexpr int JH = 512 / D;                        // heads joined at a time (shared memory)
-    static constexpr size_t ring_bytes = (size_t)kWarps * kRing;
-    static constexpr size_t join_bytes = (size_t)kWarps * JH * OPAD * 4;
-    static constexpr size_t smem = 1024 + ring_bytes + join_bytes;
+    static constexpr int FRAGS = NT * DT;                     // output fragments of a segment, 32 lanes x float4
+    static constexpr int PART = FRAGS * 512;                  // their bytes
+    static constexpr size_t smem = 1024 + (size_t)kWarps * kRing;
 };
 
 struct AttendArgs {
@@ -74,7 +73,8 @@ struct AttendArgs {
     KvShape s;
     const float *k_scale, *v_scale;
     unsigned* health;
-    float* part_o;      // [CTA][2][16][head_dim]
+    float4* warp_o;     // [CTA][warp][FRAGS][32]: unnormalised output fragments
+    float4* part_o;     // [CTA][2][FRAGS][32]
     float2* part_ml;    // [CTA][2][16]: maximum (base two), sum
     int* arrived;       // [max_batch * head tiles], zero between calls
     int box_rows;       // tokens of one TMA box
@@ -152,33 +152,59 @@ __device__ __forceinline__ uint32_t line_at(int row, int col) {
 // A position in the chunk sequence: unit u, in the segment (sequence b, head
 // tile ht) of units [beg, end).
 struct Place {
-    int64_t u, beg, end;
-    int b, ht;
+    int u, beg, end, b, ht;
 };
+
+// One output fragment (head tile column nt, 16 channels dt) to the output rows
+// of `heads` heads from o: called by a whole warp, c and r of heads 2j and 2j + 1.
+template <class C>
+__device__ __forceinline__ void emit(__nv_bfloat16* o, int heads, int nt, int dt, const float (&c)[4], const float (&r)[2]) {
+    const int lane = threadIdx.x % 32, g = lane >> 2, j = lane & 3;
+    if constexpr (C::FP8) {   // c[0], c[2]: channels 2g, 2g + 1
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int h = nt * 8 + 2 * j + i;
+            if (h < heads)
+                *reinterpret_cast<uint32_t*>(o + (int64_t)h * C::D + dt * 16 + 2 * g) =
+                    pack_pair<false>(c[i] * r[i], c[i + 2] * r[i]);
+        }
+    } else {                  // c[0], c[2]: channels g, g + 8
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t v = transpose8(pack_pair<false>(c[2 * i] * r[0], c[2 * i + 1] * r[1]));
+            const int h = nt * 8 + g;
+            if (h < heads) *reinterpret_cast<uint32_t*>(o + (int64_t)h * C::D + dt * 16 + 8 * i + 2 * j) = v;
+        }
+    }
+}
 
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     k_kv_attend(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
     constexpr int NT = C::NT, CT = C::CT, D = C::D;
     extern __shared__ uint8_t smem_raw[];
-    __shared__ int64_t sm_pre[1025];            // chunks before sequence b
-    __shared__ int64_t sm_wsum[kWarps];
+    __shared__ int sm_pre[1025];                // chunks before sequence b
     __shared__ int sm_len[1024];
+    __shared__ int sm_wsum[kWarps];
     __shared__ __align__(8) uint64_t sm_bar[kWarps][C::STAGES];
     __shared__ uint32_t sm_rows[kWarps][C::STAGES];  // which groups of 16 rows a stage holds
-    __shared__ float sm_m[kWarps][C::HEADS], sm_l[kWarps][C::HEADS];
-    __shared__ int sm_last, sm_abort;
+    __shared__ float2 sm_ml[kWarps][2][C::HEADS];    // maximum and sum of a warp's cut segments
+    __shared__ Place sm_seg[kWarps + 1];             // the CTA's first segment, and each warp's last
+    __shared__ Place sm_cut[2];                      // segments that go on before and after the CTA
+    __shared__ int sm_on[2];
+    __shared__ __align__(8) float sm_fac[kWarps + 1][kWarps][C::HEADS];   // factors of the warps' parts of cut segments
+    __shared__ __align__(8) float sm_sum[kWarps + 1][C::HEADS];
+    __shared__ int sm_part[kWarps + 1][kWarps], sm_parts[kWarps + 1], sm_side[kWarps + 1];
+    __shared__ int sm_last[2], sm_abort;
 
     const KvShape& s = p.s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, j = lane & 3;
-    const uint32_t ring = ((bw::saddr(smem_raw) + 1023) & ~1023u) + warp * kRing;
-    float* join = reinterpret_cast<float*>(smem_raw + (((bw::saddr(smem_raw) + 1023) & ~1023u) - bw::saddr(smem_raw)) +
-                                           C::ring_bytes);
+    const uint32_t ring0 = (bw::saddr(smem_raw) + 1023) & ~1023u, ring = ring0 + warp * kRing;
     uint32_t bits = 0;
 
     if (lane < C::STAGES) bw::mbar_init(bw::saddr(&sm_bar[warp][lane]), 1);
-    if (threadIdx.x == 0) sm_abort = 0;
+    if (threadIdx.x == 0) sm_abort = sm_on[0] = sm_on[1] = 0;
     bw::mbar_fence_init();
 
     // ---- chunks of every sequence, summed ------------------------------------------
@@ -192,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int most = p.a.max_pages * s.page_size;
         const int per = (B + kThreads - 1) / kThreads;
         const int b0 = threadIdx.x * per, b1 = min(B, b0 + per);
-        int64_t mine = 0;
+        int mine = 0;
         for (int b = b0; b < b1; ++b) {
             int len = max(p.a.lens[b], 0);
             if (len > most) {
@@ -204,14 +230,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm_pre[b + 1] = n;
             mine += n;
         }
-        int64_t incl = mine;
+        int incl = mine;
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t v = __shfl_up_sync(~0u, incl, o);
+            const int v = __shfl_up_sync(~0u, incl, o);
             if (lane >= o) incl += v;
         }
         if (lane == 31) sm_wsum[warp] = incl;
         __syncthreads();
-        int64_t run = incl - mine;
+        int run = incl - mine;
         for (int w = 0; w < warp; ++w) run += sm_wsum[w];
         for (int b = b0; b < b1; ++b) {
             run += sm_pre[b + 1];
@@ -220,42 +246,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) sm_pre[0] = 0;
         __syncthreads();
     }
-    const int64_t total = sm_pre[B] * HT;
-    // no more CTAs than chunks: each of them has at least one, so a segment's CTAs are consecutive
-    const int64_t ctas = min((int64_t)gridDim.x, total), me = blockIdx.x;
-    const int64_t u0 = me < ctas ? me * total / ctas : 0, u1 = me < ctas ? (me + 1) * total / ctas : 0;
+    // Chunks of this CTA, and of its warps. No more CTAs than chunks: each of them
+    // has at least one, so a segment's CTAs are consecutive.
+    const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
+    const int ctas = min((int)gridDim.x, total), me = blockIdx.x;
+    const int share = ctas ? total / ctas : 0, rest = total - share * ctas;
+    auto cta_beg = [&](int c) { return c * share + min(c, rest); };
+    auto cta_of = [&](int u) { return u < rest * (share + 1) ? u / (share + 1) : rest + (u - rest * (share + 1)) / share; };
+    const int u0 = me < ctas ? cta_beg(me) : 0, u1 = me < ctas ? cta_beg(me + 1) : 0;
+    auto warp_beg = [&](int w) { return u0 + (int)((int64_t)(u1 - u0) * w / kWarps); };
+    const int w0 = warp_beg(warp), w1 = warp_beg(warp + 1);
+    // a warp's parts of cut segments, in its ring once that is idle: of the one that began
+    // before the warp, and of the one that goes on after it
+    auto part_at = [&](int w, int which) {
+        return reinterpret_cast<float4*>(smem_raw + (ring0 - bw::saddr(smem_raw)) + w * kRing + which * C::PART);
+    };
 
-    // sequences with nothing to attend to
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        if (sm_pre[b + 1] != sm_pre[b]) continue;
-        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)b * s.n_heads * D);
-        for (int i = threadIdx.x; i < s.n_heads * (D / 4); i += kThreads) o[i] = make_uint2(0, 0);
-        if (p.a.lse)
-            for (int i = threadIdx.x; i < s.n_heads; i += kThreads) p.a.lse[(int64_t)b * s.n_heads + i] = -INFINITY;
-    }
-
-    if (u0 < u1) {
-        // segment of unit u0
+    if (w0 < w1) {
+        // the segment of unit w0
         Place at;
         {
-            int lo = 0, hi = B;   // sm_pre[lo] * HT <= u0 < sm_pre[hi] * HT
+            int lo = 0, hi = B;   // sm_pre[lo] * HT <= w0 < sm_pre[hi] * HT
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (sm_pre[mid] * HT <= u0) lo = mid;
+                if (sm_pre[mid] * HT <= w0) lo = mid;
                 else hi = mid;
             }
-            const int64_t n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT;
+            const int n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT;
             at.b = lo;
-            at.ht = (int)((u0 - base) / n);
+            at.ht = (w0 - base) / n;
             at.beg = base + at.ht * n;
             at.end = at.beg + n;
-            at.u = u0;
+            at.u = w0;
         }
+        if (w0 == u0 && lane == 0) sm_seg[0] = at;
         // to the segment that holds unit u (u only grows)
-        auto seek = [&](Place& q, int64_t u) {
+        auto seek = [&](Place& q, int u) {
             q.u = u;
             while (u >= q.end) {
-                const int64_t n = q.end - q.beg;
+                const int n = q.end - q.beg;
                 if (++q.ht < HT) {
                     q.beg = q.end;
                     q.end += n;
@@ -275,29 +304,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int boxes = CT / p.box_rows;
         const int bx = lane % boxes, col = lane / boxes;
         const bool issuer = col < C::COLS;
-        const uint64_t pol = bw::l2_evict_first();
+        // read once, unless further head tiles of the same keys follow
+        const uint64_t pol = tiles == 1 ? bw::l2_evict_first() : bw::l2_evict_last();
         const uint32_t box_bytes = p.box_rows * C::LINE;
         const uint32_t box_at = col * (CT * C::LINE) + bx * box_bytes;
         Place nx = at;             // the chunk whose pages are being looked up
-        int nx_page = -1, nx_slot = 0;
+        int nx_page = -1, nx_slot = 0, nx_at = 0, nx_hk = 0;   // of this lane's box; nx_at: its block-table column
         bool nx_live = false, nx_read = false;
-        auto lookup = [&](int64_t u) {
-            nx_live = u < u1;
-            if (!nx_live) return;
-            seek(nx, u);
-            nx_page = -1;
-            nx_read = false;
-            if (!issuer) return;
-            const int len = sm_len[nx.b], first = first_of(len);
-            const int tok = (first / CT + (int)(u - nx.beg)) * CT + bx * p.box_rows;
-            if (tok < len && tok + p.box_rows > first) {
-                // not looked at before the issue, an iteration later
-                nx_read = true;
-                nx_page = p.a.block_table[(int64_t)nx.b * p.a.max_pages + tok / s.page_size];
-                nx_slot = tok % s.page_size;
-            }
+        // a segment's queries into L2: the load itself would wait behind the copies in flight
+        auto prefetch_q = [&](const Place& q) {
+            const int heads = min(C::HEADS, G - (q.ht % tiles) * C::HEADS);
+            const char* src = reinterpret_cast<const char*>(
+                static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)q.b * p.a.q_stride +
+                (int64_t)(q.ht / tiles * G + (q.ht % tiles) * C::HEADS) * D);
+            for (int i = lane * 128; i < heads * D * 2; i += 32 * 128)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
         };
-        int64_t ahead = u0 + warp;
+        // the pages of unit u: the first one, or the one after the last looked up
+        auto lookup = [&](int u, bool start) {
+            nx_live = u < w1;
+            if (!nx_live) return;
+            start |= u >= nx.end;
+            seek(nx, u);
+            const int len = sm_len[nx.b], first = first_of(len);
+            const int tok = (first / CT + u - nx.beg) * CT + bx * p.box_rows;
+            if (start) {
+                prefetch_q(nx);
+                nx_at = tok / s.page_size;
+                nx_slot = tok - nx_at * s.page_size;
+                nx_hk = nx.ht / tiles;
+            } else {
+                for (nx_slot += CT; nx_slot >= s.page_size; nx_slot -= s.page_size) ++nx_at;
+            }
+            // not looked at before the issue, an iteration later
+            nx_read = issuer && tok < len && tok + p.box_rows > first;
+            nx_page = nx_read ? p.a.block_table[(int64_t)nx.b * p.a.max_pages + nx_at] : -1;
+        };
+        int ahead = w0;
         int issued = 0, put = 0;   // stages issued, and the stage after them
         auto issue = [&]() {       // the looked-up chunk's keys or values into the next stage
             if (nx_read && (nx_page < 0 || nx_page >= s.n_pages)) {
@@ -316,11 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (nx_page >= 0)
                 tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
-                            nx.ht / tiles, nx_page, bar, pol);
+                            nx_hk, nx_page, bar, pol);
             if (++put == C::STAGES) put = 0;
-            if (!(++issued & 1)) lookup(ahead += kWarps);
+            if (!(++issued & 1)) lookup(++ahead, false);
         };
-        lookup(ahead);
+        lookup(ahead, true);
         for (int i = 0; i < C::STAGES && nx_live; ++i) issue();
 
         // this lane's rows for ldmatrix: of operand A of K Q^T, and of V^T P^T transposed
@@ -347,9 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (nx_live) issue();
         };
-        int64_t cur = u0 + warp;         // this warp's next chunk
-        for (seek(at, u0);; seek(at, at.end)) {
-            const int64_t seg_end = min(at.end, u1);
+        bool aside = false;
+        for (int cur = w0;; seek(at, at.end)) {
+            const int seg_end = min(at.end, w1);
             const int hk = at.ht / tiles, h0 = hk * G + (at.ht % tiles) * C::HEADS;
             const int heads = min(C::HEADS, G - (at.ht % tiles) * C::HEADS);
             const int len = sm_len[at.b], first = first_of(len);
@@ -422,8 +465,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 4; ++i) o[dt][nt][i] = 0.f;
             }
 
-            for (; cur < seg_end; cur += kWarps) {
-                const int tok0 = (first / CT + (int)(cur - at.beg)) * CT;
+            for (; cur < seg_end; ++cur) {
+                const int tok0 = (first / CT + cur - at.beg) * CT;
                 const uint32_t rows = sm_rows[warp][take];
                 const uint32_t kt = next_stage();
                 const bool whole = tok0 >= first && tok0 + CT <= len && rows == (1u << C::MT) - 1;
@@ -562,138 +605,240 @@ __global__ void __launch_bounds__(kThreads, 1)
                 release();
             }
 
-            // ---- the warps' results are joined -------------------------------------------
-            const bool split = at.beg < u0 || at.end > u1;
-            const int slot = blockIdx.x * 2 + (at.beg < u0 ? 0 : 1);
+            // ---- a whole segment is written, a part of one is set aside ----------------------
+            const bool mine = at.beg >= w0 && at.end <= w1;
+            const int which = at.beg < w0 ? 0 : 1;
+            const float vs = p.v_scale[hk];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float r[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     float v = l[nt][c];
                     v += __shfl_xor_sync(~0u, v, 4);
                     v += __shfl_xor_sync(~0u, v, 8);
                     v += __shfl_xor_sync(~0u, v, 16);
-                    if (g == 0) {
-                        sm_m[warp][nt * 8 + 2 * j + c] = m[nt][c];
-                        sm_l[warp][nt * 8 + 2 * j + c] = v;
-                    }
+                    r[c] = v == 0.f ? 0.f : vs / v;
+                    const int h = nt * 8 + 2 * j + c;
+                    if (g == 0 && mine && p.a.lse && h < heads)
+                        p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = v == 0.f ? -INFINITY : m[nt][c] * kLn2 + logf(v);
+                    if (g == 0 && !mine) sm_ml[warp][which][h] = make_float2(m[nt][c], v);
                 }
-            const float vs = p.v_scale[hk];
+                if (mine) {
+                    __nv_bfloat16* out =
+                        static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)at.b * s.n_heads + h0) * D;
 #pragma unroll
-            for (int part = 0; part < C::HEADS / C::JH; ++part) {
-                const int nt = part * C::JH / 8, p0 = part * C::JH;
-                if (p0 >= heads) break;
-                float* mine = join + warp * C::JH * C::OPAD;
-                if ((nt * 8 + 2 * j) / C::JH == part)
+                    for (int dt = 0; dt < C::DT; ++dt) emit<C>(out, heads, nt, dt, o[dt][nt], r);
+                } else if (at.end < w1) {   // the copies still run: set aside in L2
+                    float4* dst = p.warp_o + (int64_t)(me * kWarps + warp) * (C::FRAGS * 32) + lane;
 #pragma unroll
-                for (int dt = 0; dt < C::DT; ++dt)
+                    for (int dt = 0; dt < C::DT; ++dt)
+                        __stcg(dst + (nt * C::DT + dt) * 32,
+                               make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]));
+                    aside = true;
+                } else {                    // the ring is idle: shared memory
+                    float4* dst = part_at(warp, which) + lane;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int d = dt * 16 + (C::FP8 ? 2 * g + (i >> 1) : g + (i >> 1) * 8);
-                        mine[((2 * j) % C::JH + (i & 1)) * C::OPAD + d] = o[dt][nt][i];
-                    }
-                __syncthreads();
-                const int hs = min(C::JH, heads - p0);
-                for (int it = threadIdx.x; it < hs * (D / 4); it += kThreads) {
-                    const int h = it / (D / 4), d = it % (D / 4) * 4, hh = p0 + h;
-                    float M = sm_m[0][hh];
-                    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][hh]);
-                    const float mb = M == -INFINITY ? 0.f : M;
-                    float L = 0.f;
-                    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int w = 0; w < kWarps; ++w) {
-                        const float f = ex2(sm_m[w][hh] - mb);
-                        const float4 v = *reinterpret_cast<const float4*>(join + (w * C::JH + h) * C::OPAD + d);
-                        L += f * sm_l[w][hh];
-                        a.x += f * v.x;
-                        a.y += f * v.y;
-                        a.z += f * v.z;
-                        a.w += f * v.w;
-                    }
-                    if (split) {
-                        *reinterpret_cast<float4*>(p.part_o + ((int64_t)slot * 16 + hh) * D + d) = a;
-                        if (d == 0) p.part_ml[slot * 16 + hh] = make_float2(M, L);
-                    } else {
-                        const float r = L == 0.f ? 0.f : vs / L;
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) +
-                                                  ((int64_t)at.b * s.n_heads + h0 + hh) * D + d) =
-                            make_uint2(pack_pair<false>(a.x * r, a.y * r), pack_pair<false>(a.z * r, a.w * r));
-                        if (d == 0 && p.a.lse)
-                            p.a.lse[(int64_t)at.b * s.n_heads + h0 + hh] =
-                                L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-                    }
+                    for (int dt = 0; dt < C::DT; ++dt)
+                        dst[(nt * C::DT + dt) * 32] =
+                            make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]);
                 }
-                __syncthreads();
             }
+            if (at.end >= w1) break;
+        }
+        if (aside) {
+            const float4* src = p.warp_o + (int64_t)(me * kWarps + warp) * (C::FRAGS * 32) + lane;
+            float4* dst = part_at(warp, 0) + lane;
+#pragma unroll 8
+            for (int f = 0; f < C::FRAGS; ++f) dst[f * 32] = __ldcg(src + f * 32);
+        }
+        if (lane == 0) sm_seg[warp + 1] = at;
+    }
 
-            // ---- and those of the CTAs that share the segment ------------------------------
-            if (split) {
-                // CTA of unit u: the largest c with c * total / ctas <= u
-                const int c0 = (int)(((at.beg + 1) * ctas - 1) / total), c1 = (int)((at.end * ctas - 1) / total);
-                const int n = c1 - c0 + 1;
-                int* arrived = p.arrived + (int64_t)at.b * HT + at.ht;
-                __threadfence();
-                __syncthreads();
-                if (threadIdx.x == 0) {
-                    sm_last = atomicAdd(arrived, 1) == n - 1;
-                    if (sm_last) *arrived = 0;   // for the next call
-                }
-                __syncthreads();
-                if (sm_last) {
-                    __threadfence();
-                    // the first CTA's part is its second slot (its segment begins there), the
-                    // others' their first
-                    auto slot_of = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
-                    // each part's factor, a warp per head; the join buffer is free here
-                    float* fac = join;       // [heads][n]
-                    for (int h = warp; h < heads; h += kWarps) {
-                        float M = -INFINITY, L = 0.f;
-                        for (int i = lane; i < n; i += 32) M = fmaxf(M, __ldcg(&p.part_ml[slot_of(i) * 16 + h]).x);
-                        for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-                        const float mb = M == -INFINITY ? 0.f : M;
-                        for (int i = lane; i < n; i += 32) {
-                            const float2 ml = __ldcg(&p.part_ml[slot_of(i) * 16 + h]);
-                            const float f = ex2(ml.x - mb);
-                            fac[h * n + i] = f;
-                            L += f * ml.y;
-                        }
-                        for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-                        if (lane == 0) {
-                            sm_l[0][h] = L;
-                            if (p.a.lse)
-                                p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-                        }
-                    }
-                    __syncthreads();
-                    for (int it = threadIdx.x; it < heads * (D / 4); it += kThreads) {
-                        const int h = it / (D / 4), d = it % (D / 4) * 4;
-                        const float* src = p.part_o + (int64_t)h * D + d;
-                        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int i0 = 0; i0 < n; i0 += 16) {
-                            float4 v[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i0 + i < n)
-                                    v[i] = __ldcg(reinterpret_cast<const float4*>(src + (int64_t)slot_of(i0 + i) * 16 * D));
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i0 + i < n) {
-                                    const float f = fac[h * n + i0 + i];
-                                    a.x += f * v[i].x;
-                                    a.y += f * v[i].y;
-                                    a.z += f * v[i].z;
-                                    a.w += f * v[i].w;
-                                }
-                        }
-                        const float r = sm_l[0][h] == 0.f ? 0.f : vs / sm_l[0][h];
-                        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) +
-                                                  ((int64_t)at.b * s.n_heads + h0 + h) * D + d) =
-                            make_uint2(pack_pair<false>(a.x * r, a.y * r), pack_pair<false>(a.z * r, a.w * r));
-                    }
-                    __syncthreads();
+    // sequences with nothing to attend to
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        if (sm_pre[b + 1] != sm_pre[b]) continue;
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)b * s.n_heads * D);
+        for (int i = threadIdx.x; i < s.n_heads * (D / 4); i += kThreads) o[i] = make_uint2(0, 0);
+        if (p.a.lse)
+            for (int i = threadIdx.x; i < s.n_heads; i += kThreads) p.a.lse[(int64_t)b * s.n_heads + i] = -INFINITY;
+    }
+    __syncthreads();
+
+    // ---- segments cut between this CTA's warps -----------------------------------------
+    // Taken where they begin: the one that comes from before the CTA, and each that
+    // begins in a warp and goes on in the next. At most two go on beyond the CTA.
+    // Thread 8 i + x: whether segment i (sm_seg's index) is cut, and warp x's part of it.
+    if (threadIdx.x < 96) {
+        const int i = threadIdx.x / kWarps, x = threadIdx.x % kWarps;
+        bool has = false;
+        int code = 0;
+        if (i <= kWarps && u0 < u1) {
+            const int a0 = warp_beg(max(i - 1, 0)), a1 = warp_beg(i), b0 = warp_beg(x), b1 = warp_beg(x + 1);
+            if (i == 0 || a0 < a1) {
+                const int beg = sm_seg[i].beg, end = sm_seg[i].end;
+                const bool cut = i == 0 ? beg < u0 : beg >= a0 && end > a1;
+                has = cut && b0 < b1 && b1 > beg && b0 < end;
+                code = 2 * x + (beg < b0 ? 0 : 1);
+            }
+        }
+        const unsigned all = __ballot_sync(~0u, has) >> (lane & 24) & 0xff;
+        if (has) sm_part[i][__popc(all & ((1u << x) - 1))] = code;
+        if (x == 0 && i <= kWarps) sm_parts[i] = __popc(all);
+    }
+    __syncthreads();
+    for (int t = threadIdx.x; t < (kWarps + 1) * C::HEADS; t += kThreads) {
+        const int i = t / C::HEADS, h = t % C::HEADS, n = sm_parts[i];
+        if (n == 0) continue;
+        const Place q = sm_seg[i];
+        float M = -INFINITY, L = 0.f;
+        for (int k = 0; k < n; ++k) M = fmaxf(M, sm_ml[sm_part[i][k] / 2][sm_part[i][k] % 2][h].x);
+        const float mb = M == -INFINITY ? 0.f : M;
+        for (int k = 0; k < n; ++k) {
+            const float2 ml = sm_ml[sm_part[i][k] / 2][sm_part[i][k] % 2][h];
+            const float e = ex2(ml.x - mb);
+            sm_fac[i][k][h] = e;
+            L += e * ml.y;
+        }
+        sm_sum[i][h] = L;
+        const int side = q.beg < u0 ? 0 : q.end > u1 ? 1 : -1;
+        if (h == 0) sm_side[i] = side;
+        if (side >= 0) {
+            __stcg(&p.part_ml[(me * 2 + side) * 16 + h], make_float2(M, L));
+            if (h == 0) {
+                sm_cut[side] = q;
+                sm_on[side] = 1;
+            }
+        } else {
+            const int hk = q.ht / tiles, h0 = (q.ht % tiles) * C::HEADS;
+            if (p.a.lse && h0 + h < G)
+                p.a.lse[(int64_t)q.b * s.n_heads + hk * G + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+        }
+    }
+    __syncthreads();
+    // a warp per fragment of every cut segment
+    for (int i = 0, t = warp; i <= kWarps; ++i) {
+        const int n = sm_parts[i];
+        if (n == 0) continue;
+        if (t >= C::FRAGS) {
+            t -= C::FRAGS;
+            continue;
+        }
+        const Place q = sm_seg[i];
+        const int side = sm_side[i], hk = q.ht / tiles, h0 = (q.ht % tiles) * C::HEADS;
+        const float vs = p.v_scale[hk];
+        float4* dst = p.part_o + ((me * 2 + side) * C::FRAGS) * 32 + lane;
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)q.b * s.n_heads + hk * G + h0) * D;
+        for (; t < C::FRAGS; t += kWarps) {
+            const int nt = t / C::DT;
+            const float* e0 = &sm_fac[i][0][nt * 8 + 2 * j];
+            float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+            for (int k = 0; k < n; ++k) {
+                const int code = sm_part[i][k];
+                const float4 v = part_at(code / 2, code % 2)[t * 32 + lane];
+                const float2 e = *reinterpret_cast<const float2*>(e0 + k * C::HEADS);
+                a[0] += e.x * v.x;
+                a[1] += e.y * v.y;
+                a[2] += e.x * v.z;
+                a[3] += e.y * v.w;
+            }
+            if (side >= 0) {
+                __stcg(dst + t * 32, make_float4(a[0], a[1], a[2], a[3]));
+            } else {
+                const float2 L = *reinterpret_cast<const float2*>(&sm_sum[i][nt * 8 + 2 * j]);
+                const float r[2] = {L.x == 0.f ? 0.f : vs / L.x, L.y == 0.f ? 0.f : vs / L.y};
+                emit<C>(out, min(C::HEADS, G - h0), nt, t % C::DT, a, r);
+            }
+        }
+        t -= C::FRAGS;
+    }
+
+    // ---- segments cut between CTAs -------------------------------------------------------
+    __threadfence();
+    __syncthreads();
+    if (sm_on[0] || sm_on[1]) {
+        if (threadIdx.x < 2) {
+            sm_last[threadIdx.x] = 0;
+            if (sm_on[threadIdx.x]) {
+                const Place q = sm_cut[threadIdx.x];
+                int* arrived = p.arrived + q.b * HT + q.ht;
+                const int n = cta_of(q.end - 1) - cta_of(q.beg) + 1;
+                if (atomicAdd(arrived, 1) == n - 1) {
+                    sm_last[threadIdx.x] = 1;
+                    *arrived = 0;   // for the next call
                 }
             }
-            if (at.end >= u1) break;
+        }
+        __syncthreads();
+        for (int side = 0; side < 2; ++side) {
+            if (!sm_last[side]) continue;
+            __threadfence();
+            const Place q = sm_cut[side];
+            const int c0 = cta_of(q.beg), n = cta_of(q.end - 1) - c0 + 1;
+            const int hk = q.ht / tiles, h0 = hk * G + (q.ht % tiles) * C::HEADS;
+            const int heads = min(C::HEADS, G - (q.ht % tiles) * C::HEADS);
+            const float vs = p.v_scale[hk];
+            // the first CTA's part is its second (its segment begins there), the others' their first
+            auto part = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
+            // the first parts are on their way while the factors are computed
+            constexpr int BATCH = 16, STEP = 2 * C::FRAGS * 32;
+            float4 v[BATCH];
+            auto fetch = [&](int f, int i0) {
+                const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    if (i0 + i < n) v[i] = __ldcg(src + i * STEP + (i0 + i == 0 ? STEP / 2 : 0));
+            };
+            if (warp < C::FRAGS) fetch(warp, 0);
+            float* fac = reinterpret_cast<float*>(smem_raw);   // [n][HEADS]: the rings are idle
+            for (int h = warp; h < C::HEADS; h += kWarps) {
+                float2 ml[kMaxCtas / 32];
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int i = 0; i < kMaxCtas / 32; ++i) {
+                    ml[i] = lane + 32 * i < n ? __ldcg(&p.part_ml[part(lane + 32 * i) * 16 + h]) : make_float2(-INFINITY, 0.f);
+                    M = fmaxf(M, ml[i].x);
+                }
+                for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+                const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int i = 0; i < kMaxCtas / 32; ++i) {
+                    const float e = ex2(ml[i].x - mb);
+                    if (lane + 32 * i < n) fac[(lane + 32 * i) * C::HEADS + h] = e;
+                    L += e * ml[i].y;
+                }
+                for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+                if (lane == 0) {
+                    sm_sum[0][h] = L;
+                    if (p.a.lse && h < heads)
+                        p.a.lse[(int64_t)q.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
+                }
+            }
+            __syncthreads();
+#pragma unroll 1
+            for (int f = warp; f < C::FRAGS; f += kWarps) {
+                const int h = f / C::DT * 8 + 2 * j;
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                for (int i0 = 0; i0 < n; i0 += BATCH) {
+                    if (f != warp || i0) fetch(f, i0);
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (i0 + i < n) {
+                            const float2 e = *reinterpret_cast<const float2*>(fac + (i0 + i) * C::HEADS + h);
+                            a[0] += e.x * v[i].x;
+                            a[1] += e.y * v[i].y;
+                            a[2] += e.x * v[i].z;
+                            a[3] += e.y * v[i].w;
+                        }
+                }
+                const float2 L = *reinterpret_cast<const float2*>(&sm_sum[0][h]);
+                const float r[2] = {L.x == 0.f ? 0.f : vs / L.x, L.y == 0.f ? 0.f : vs / L.y};
+                emit<C>(static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)q.b * s.n_heads + h0) * D, heads, f / C::DT,
+                        f % C::DT, a, r);
+            }
+            __syncthreads();   // fac and sm_sum are free again
         }
     }
     if (bits) atomicOr(p.health, bits);
@@ -701,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class C>
 cudaError_t launch(const Kv& K, const AttendArgs& p, cudaStream_t stream) {
-    k_kv_attend<C><<<K.num_sms, kThreads, C::smem, stream>>>(p, K.tm_k, K.tm_v);
+    k_kv_attend<C><<<std::min(K.num_sms, kMaxCtas), kThreads, C::smem, stream>>>(p, K.tm_k, K.tm_v);
     return cudaGetLastError();
 }
 
@@ -723,13 +868,15 @@ auto pick(const KvShape& s, F f) {
 
 }  // namespace
 
-size_t kv_attend_workspace(const Kv& K, size_t out[3]) {
+size_t kv_attend_workspace(const Kv& K, size_t out[4]) {
     const int G = K.s.n_heads / K.s.n_kv_heads;
     const int heads = pick(K.s, [](auto c) { return decltype(c)::HEADS; });
-    out[0] = (size_t)K.num_sms * 2 * 16 * K.s.head_dim * 4;
-    out[1] = (size_t)K.num_sms * 2 * 16 * 8;
-    out[2] = (size_t)K.d.max_batch * K.s.n_kv_heads * ((G + heads - 1) / heads) * 4;
-    return out[0] + out[1] + out[2];
+    const size_t part = (size_t)heads * K.s.head_dim * 4;
+    out[0] = (size_t)K.num_sms * kWarps * part;
+    out[1] = (size_t)K.num_sms * 2 * part;
+    out[2] = (size_t)K.num_sms * 2 * 16 * 8;
+    out[3] = (size_t)K.d.max_batch * K.s.n_kv_heads * ((G + heads - 1) / heads) * 4;
+    return out[0] + out[1] + out[2] + out[3];
 }
 
 cudaError_t kv_attend_setup(Kv& K) {
@@ -759,7 +906,15 @@ cudaError_t kv_attend_setup(Kv& K) {
 }
 
 moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t stream) {
-    const AttendArgs p{a, K.s, K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml, K.arrived, K.box_rows};
+    const AttendArgs p{a,        K.s,      K.k_scale, K.v_scale, K.health,
+                       K.warp_o, K.part_o, K.part_ml, K.arrived, K.box_rows};
+    // the kernel counts chunks in 32 bits
+    const int64_t most = pick(K.s, [&](auto c) {
+        using C = decltype(c);
+        const int tiles = (K.s.n_heads / K.s.n_kv_heads + C::HEADS - 1) / C::HEADS;
+        return ((int64_t)a.max_pages * K.s.page_size / C::CT + 1) * a.B * K.s.n_kv_heads * tiles;
+    });
+    if (most > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "the block table spans more chunks than 2^31");
     const cudaError_t e = pick(K.s, [&](auto c) { return launch<decltype(c)>(K, p, stream); });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend launch");
 }
