@@ -65,17 +65,19 @@ struct Cfg {
     static constexpr int STEPS = RB / 32;                     // and of a row
     static constexpr int FRAGS = NT * DT;                     // output fragments of a segment, 32 lanes x float4
     static constexpr int PART = FRAGS * 512;                  // their bytes
-    static constexpr size_t smem = 1024 + (size_t)kWarps * kRing;
+    static constexpr size_t smem = 1024 + (size_t)kWarps * (kRing + PART);
 };
+
+// Every warp comes here once, from the end of its chunks or without any.
+__device__ __forceinline__ void warps_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
 
 struct AttendArgs {
     moe_kv_attend_args a;
     KvShape s;
     const float *k_scale, *v_scale;
     unsigned* health;
-    float4* warp_o;     // [CTA][warp][FRAGS][32]: unnormalised output fragments
-    float4* part_o;     // [CTA][2][FRAGS][32]
-    float2* part_ml;    // [CTA][2][16]: maximum (base two), sum
+    float4* part_o;     // [CTA][2][FRAGS][32]: unnormalised output fragments
+    float4* part_ml;    // [CTA][2][8]: maximum (base two) and sum of two heads
     int* arrived;       // [max_batch * head tiles], zero between calls
     int box_rows;       // tokens of one TMA box
 };
@@ -149,10 +151,10 @@ __device__ __forceinline__ uint32_t line_at(int row, int col) {
     else return row * 64 + (col ^ (((row >> 1) & 3) << 4));
 }
 
-// A position in the chunk sequence: unit u, in the segment (sequence b, head
-// tile ht) of units [beg, end).
+// A segment: sequence b, head tile `tile` of key-value head hk, units [beg, end)
+// of the chunk sequence.
 struct Place {
-    int u, beg, end, b, ht;
+    int beg, end, b, hk, tile;
 };
 
 // One output fragment (head tile column nt, 16 channels dt) to the output rows
@@ -178,6 +180,23 @@ __device__ __forceinline__ void emit(__nv_bfloat16* o, int heads, int nt, int dt
     }
 }
 
+// One joined output fragment: normalised and written, with the log-sum-exp by the
+// warp of a head's first channels.
+template <class C>
+__device__ __forceinline__ void finish(const AttendArgs& p, int b, int h0, int heads, int nt, int dt, float vs,
+                                       const float (&a)[4], const float (&M)[2], const float (&L)[2]) {
+    const int lane = threadIdx.x % 32, g = lane >> 2, j = lane & 3;
+    const float r[2] = {L[0] == 0.f ? 0.f : vs / L[0], L[1] == 0.f ? 0.f : vs / L[1]};
+    const int64_t row = (int64_t)b * p.s.n_heads + h0;
+    emit<C>(static_cast<__nv_bfloat16*>(p.a.out) + row * C::D, heads, nt, dt, a, r);
+    if (dt == 0 && g == 0 && p.a.lse)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            const int h = nt * 8 + 2 * j + c;
+            if (h < heads) p.a.lse[row + h] = L[c] == 0.f ? -INFINITY : M[c] * kLn2 + logf(L[c]);
+        }
+}
+
 template <class C>
 __global__ void __launch_bounds__(kThreads, 1)
     k_kv_attend(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
@@ -188,13 +207,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ int sm_wsum[kWarps];
     __shared__ __align__(8) uint64_t sm_bar[kWarps][C::STAGES];
     __shared__ uint32_t sm_rows[kWarps][C::STAGES];  // which groups of 16 rows a stage holds
-    __shared__ float2 sm_ml[kWarps][2][C::HEADS];    // maximum and sum of a warp's cut segments
-    __shared__ Place sm_seg[kWarps + 1];             // the CTA's first segment, and each warp's last
+    __shared__ __align__(16) float2 sm_ml[kWarps][C::HEADS];   // maximum and sum of the parts below
     __shared__ Place sm_cut[2];                      // segments that go on before and after the CTA
-    __shared__ int sm_on[2];
-    __shared__ __align__(8) float sm_fac[kWarps + 1][kWarps][C::HEADS];   // factors of the warps' parts of cut segments
-    __shared__ __align__(8) float sm_sum[kWarps + 1][C::HEADS];
-    __shared__ int sm_part[kWarps + 1][kWarps], sm_parts[kWarps + 1], sm_side[kWarps + 1];
+    __shared__ int sm_on[2], sm_c0[2], sm_n[2];      // whether there are; their CTAs
     __shared__ int sm_last[2], sm_abort;
 
     const KvShape& s = p.s;
@@ -254,13 +269,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto cta_beg = [&](int c) { return c * share + min(c, rest); };
     auto cta_of = [&](int u) { return u < rest * (share + 1) ? u / (share + 1) : rest + (u - rest * (share + 1)) / share; };
     const int u0 = me < ctas ? cta_beg(me) : 0, u1 = me < ctas ? cta_beg(me + 1) : 0;
-    auto warp_beg = [&](int w) { return u0 + (int)((int64_t)(u1 - u0) * w / kWarps); };
+    auto warp_beg = [&](int w) { return u0 + (u1 - u0) * w / kWarps; };
+    auto head_of = [&](const Place& q) { return q.hk * G + q.tile * C::HEADS; };
+    auto heads_of = [&](const Place& q) { return min(C::HEADS, G - q.tile * C::HEADS); };
     const int w0 = warp_beg(warp), w1 = warp_beg(warp + 1);
-    // a warp's parts of cut segments, in its ring once that is idle: of the one that began
-    // before the warp, and of the one that goes on after it
-    auto part_at = [&](int w, int which) {
-        return reinterpret_cast<float4*>(smem_raw + (ring0 - bw::saddr(smem_raw)) + w * kRing + which * C::PART);
-    };
+    // a warp's part of the segment that began before it
+    float4* part = reinterpret_cast<float4*>(smem_raw + (ring0 - bw::saddr(smem_raw)) + kWarps * kRing);
+
+    // sequences with nothing to attend to
+    for (int b = blockIdx.x; b < B; b += gridDim.x) {
+        if (sm_pre[b + 1] != sm_pre[b]) continue;
+        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)b * s.n_heads * D);
+        for (int i = threadIdx.x; i < s.n_heads * (D / 4); i += kThreads) o[i] = make_uint2(0, 0);
+        if (p.a.lse)
+            for (int i = threadIdx.x; i < s.n_heads; i += kThreads) p.a.lse[(int64_t)b * s.n_heads + i] = -INFINITY;
+    }
 
     if (w0 < w1) {
         // the segment of unit w0
@@ -272,30 +295,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (sm_pre[mid] * HT <= w0) lo = mid;
                 else hi = mid;
             }
-            const int n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT;
+            const int n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT, ht = (w0 - base) / n;
             at.b = lo;
-            at.ht = (w0 - base) / n;
-            at.beg = base + at.ht * n;
+            at.hk = ht / tiles;
+            at.tile = ht - at.hk * tiles;
+            at.beg = base + ht * n;
             at.end = at.beg + n;
-            at.u = w0;
         }
-        if (w0 == u0 && lane == 0) sm_seg[0] = at;
-        // to the segment that holds unit u (u only grows)
-        auto seek = [&](Place& q, int u) {
-            q.u = u;
-            while (u >= q.end) {
-                const int n = q.end - q.beg;
-                if (++q.ht < HT) {
-                    q.beg = q.end;
-                    q.end += n;
-                } else {
-                    q.ht = 0;
-                    do ++q.b;
-                    while (sm_pre[q.b + 1] == sm_pre[q.b]);
-                    q.beg = sm_pre[q.b] * HT;
-                    q.end = q.beg + (sm_pre[q.b + 1] - sm_pre[q.b]);
-                }
-            }
+        // the next segment
+        auto advance = [&](Place& q) {
+            const int n = q.end - q.beg;
+            q.beg = q.end;
+            q.end += n;
+            if (++q.tile < tiles) return;
+            q.tile = 0;
+            if (++q.hk < s.n_kv_heads) return;
+            q.hk = 0;
+            do ++q.b;
+            while (sm_pre[q.b + 1] == sm_pre[q.b]);
+            q.end = q.beg + (sm_pre[q.b + 1] - sm_pre[q.b]);
         };
 
         // ---- the copies of this warp ----------------------------------------------------
@@ -309,14 +327,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t box_bytes = p.box_rows * C::LINE;
         const uint32_t box_at = col * (CT * C::LINE) + bx * box_bytes;
         Place nx = at;             // the chunk whose pages are being looked up
-        int nx_page = -1, nx_slot = 0, nx_at = 0, nx_hk = 0;   // of this lane's box; nx_at: its block-table column
+        int nx_page = -1, nx_slot = 0, nx_at = 0;   // of this lane's box; nx_at: its block-table column
         bool nx_live = false, nx_read = false;
         // a segment's queries into L2: the load itself would wait behind the copies in flight
         auto prefetch_q = [&](const Place& q) {
-            const int heads = min(C::HEADS, G - (q.ht % tiles) * C::HEADS);
+            const int heads = heads_of(q);
             const char* src = reinterpret_cast<const char*>(
-                static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)q.b * p.a.q_stride +
-                (int64_t)(q.ht / tiles * G + (q.ht % tiles) * C::HEADS) * D);
+                static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)q.b * p.a.q_stride + (int64_t)head_of(q) * D);
             for (int i = lane * 128; i < heads * D * 2; i += 32 * 128)
                 asm volatile("prefetch.global.L2 [%0];" ::"l"(src + i));
         };
@@ -324,15 +341,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto lookup = [&](int u, bool start) {
             nx_live = u < w1;
             if (!nx_live) return;
-            start |= u >= nx.end;
-            seek(nx, u);
+            if (u == nx.end) {
+                advance(nx);
+                start = true;
+            }
             const int len = sm_len[nx.b], first = first_of(len);
             const int tok = (first / CT + u - nx.beg) * CT + bx * p.box_rows;
             if (start) {
                 prefetch_q(nx);
                 nx_at = tok / s.page_size;
                 nx_slot = tok - nx_at * s.page_size;
-                nx_hk = nx.ht / tiles;
             } else {
                 for (nx_slot += CT; nx_slot >= s.page_size; nx_slot -= s.page_size) ++nx_at;
             }
@@ -359,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (nx_page >= 0)
                 tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
-                            nx_hk, nx_page, bar, pol);
+                            nx.hk, nx_page, bar, pol);
             if (++put == C::STAGES) put = 0;
             if (!(++issued & 1)) lookup(++ahead, false);
         };
@@ -390,11 +408,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (nx_live) issue();
         };
-        bool aside = false;
-        for (int cur = w0;; seek(at, at.end)) {
+        for (int cur = w0;; advance(at)) {
             const int seg_end = min(at.end, w1);
-            const int hk = at.ht / tiles, h0 = hk * G + (at.ht % tiles) * C::HEADS;
-            const int heads = min(C::HEADS, G - (at.ht % tiles) * C::HEADS);
+            const int h0 = head_of(at), heads = heads_of(at);
             const int len = sm_len[at.b], first = first_of(len);
 
             // queries: operand B of S^T = K Q^T (column g of head tile nt)
@@ -450,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int ks = 0; ks < C::KS; ++ks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) qf[ks][nt][i] ^= 0x80008000u;
-                const float k = p.k_scale[hk] * fabsf(p.a.scale);
+                const float k = p.k_scale[at.hk] * fabsf(p.a.scale);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     coef[nt][c] = k * __shfl_sync(~0u, unit, (2 * j + c) * 4);
@@ -605,153 +621,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                 release();
             }
 
-            // ---- a whole segment is written, a part of one is set aside ----------------------
-            const bool mine = at.beg >= w0 && at.end <= w1;
-            const int which = at.beg < w0 ? 0 : 1;
-            const float vs = p.v_scale[hk];
+            // ---- the segment's end ----------------------------------------------------------
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float r[2];
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    float v = l[nt][c];
-                    v += __shfl_xor_sync(~0u, v, 4);
-                    v += __shfl_xor_sync(~0u, v, 8);
-                    v += __shfl_xor_sync(~0u, v, 16);
-                    r[c] = v == 0.f ? 0.f : vs / v;
-                    const int h = nt * 8 + 2 * j + c;
-                    if (g == 0 && mine && p.a.lse && h < heads)
-                        p.a.lse[(int64_t)at.b * s.n_heads + h0 + h] = v == 0.f ? -INFINITY : m[nt][c] * kLn2 + logf(v);
-                    if (g == 0 && !mine) sm_ml[warp][which][h] = make_float2(m[nt][c], v);
+                    l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], 4);
+                    l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], 8);
+                    l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], 16);
                 }
-                if (mine) {
-                    __nv_bfloat16* out =
-                        static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)at.b * s.n_heads + h0) * D;
+            const bool last = at.end >= w1;
+            // A segment that is cut between warps is joined by the first of them, which
+            // holds its own part in registers; the others set theirs aside.
+            const bool theirs = at.beg < w0 && w0 != u0;
+            if (theirs) {
+                float4* dst = part + warp * (C::FRAGS * 32) + lane;
 #pragma unroll
-                    for (int dt = 0; dt < C::DT; ++dt) emit<C>(out, heads, nt, dt, o[dt][nt], r);
-                } else if (at.end < w1) {   // the copies still run: set aside in L2
-                    float4* dst = p.warp_o + (int64_t)(me * kWarps + warp) * (C::FRAGS * 32) + lane;
-#pragma unroll
-                    for (int dt = 0; dt < C::DT; ++dt)
-                        __stcg(dst + (nt * C::DT + dt) * 32,
-                               make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]));
-                    aside = true;
-                } else {                    // the ring is idle: shared memory
-                    float4* dst = part_at(warp, which) + lane;
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
                     for (int dt = 0; dt < C::DT; ++dt)
                         dst[(nt * C::DT + dt) * 32] =
                             make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]);
+                    if (g == 0)
+                        *reinterpret_cast<float4*>(&sm_ml[warp][nt * 8 + 2 * j]) =
+                            make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
                 }
             }
-            if (at.end >= w1) break;
-        }
-        if (aside) {
-            const float4* src = p.warp_o + (int64_t)(me * kWarps + warp) * (C::FRAGS * 32) + lane;
-            float4* dst = part_at(warp, 0) + lane;
-#pragma unroll 8
-            for (int f = 0; f < C::FRAGS; ++f) dst[f * 32] = __ldcg(src + f * 32);
-        }
-        if (lane == 0) sm_seg[warp + 1] = at;
-    }
-
-    // sequences with nothing to attend to
-    for (int b = blockIdx.x; b < B; b += gridDim.x) {
-        if (sm_pre[b + 1] != sm_pre[b]) continue;
-        uint2* o = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + (int64_t)b * s.n_heads * D);
-        for (int i = threadIdx.x; i < s.n_heads * (D / 4); i += kThreads) o[i] = make_uint2(0, 0);
-        if (p.a.lse)
-            for (int i = threadIdx.x; i < s.n_heads; i += kThreads) p.a.lse[(int64_t)b * s.n_heads + i] = -INFINITY;
-    }
-    __syncthreads();
-
-    // ---- segments cut between this CTA's warps -----------------------------------------
-    // Taken where they begin: the one that comes from before the CTA, and each that
-    // begins in a warp and goes on in the next. At most two go on beyond the CTA.
-    // Thread 8 i + x: whether segment i (sm_seg's index) is cut, and warp x's part of it.
-    if (threadIdx.x < 96) {
-        const int i = threadIdx.x / kWarps, x = threadIdx.x % kWarps;
-        bool has = false;
-        int code = 0;
-        if (i <= kWarps && u0 < u1) {
-            const int a0 = warp_beg(max(i - 1, 0)), a1 = warp_beg(i), b0 = warp_beg(x), b1 = warp_beg(x + 1);
-            if (i == 0 || a0 < a1) {
-                const int beg = sm_seg[i].beg, end = sm_seg[i].end;
-                const bool cut = i == 0 ? beg < u0 : beg >= a0 && end > a1;
-                has = cut && b0 < b1 && b1 > beg && b0 < end;
-                code = 2 * x + (beg < b0 ? 0 : 1);
+            if (last) warps_meet();
+            if (!theirs) {
+                for (int x = warp + 1; last && x < kWarps && warp_beg(x) < at.end; ++x) {
+                    if (warp_beg(x) == warp_beg(x + 1)) continue;
+                    const float4* src = part + x * (C::FRAGS * 32) + lane;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float4 ml = *reinterpret_cast<const float4*>(&sm_ml[x][nt * 8 + 2 * j]);
+                        const float mx[2] = {ml.x, ml.z}, lx[2] = {ml.y, ml.w};
+                        float f[2], e[2];
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const float top = fmaxf(m[nt][c], mx[c]), base = top == -INFINITY ? 0.f : top;
+                            f[c] = ex2(m[nt][c] - base);
+                            e[c] = ex2(mx[c] - base);
+                            m[nt][c] = top;
+                            l[nt][c] = l[nt][c] * f[c] + lx[c] * e[c];
+                        }
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt) {
+                            const float4 v = src[(nt * C::DT + dt) * 32];
+                            o[dt][nt][0] = o[dt][nt][0] * f[0] + e[0] * v.x;
+                            o[dt][nt][1] = o[dt][nt][1] * f[1] + e[1] * v.y;
+                            o[dt][nt][2] = o[dt][nt][2] * f[0] + e[0] * v.z;
+                            o[dt][nt][3] = o[dt][nt][3] * f[1] + e[1] * v.w;
+                        }
+                    }
+                }
+                const int side = at.beg < u0 ? 0 : at.end > u1 ? 1 : -1;
+                if (side < 0) {
+                    const float vs = p.v_scale[at.hk];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt)
+                            finish<C>(p, at.b, h0, heads, nt, dt, vs, o[dt][nt], m[nt], l[nt]);
+                    }
+                } else {
+                    float4* dst = p.part_o + (me * 2 + side) * (C::FRAGS * 32) + lane;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt)
+                            __stcg(dst + (nt * C::DT + dt) * 32,
+                                   make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]));
+                        if (g == 0)
+                            __stcg(&p.part_ml[(me * 2 + side) * 8 + nt * 4 + j],
+                                   make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]));
+                    }
+                    if (lane == 0) {
+                        sm_cut[side] = at;
+                        sm_on[side] = 1;
+                    }
+                }
             }
+            if (last) break;
         }
-        const unsigned all = __ballot_sync(~0u, has) >> (lane & 24) & 0xff;
-        if (has) sm_part[i][__popc(all & ((1u << x) - 1))] = code;
-        if (x == 0 && i <= kWarps) sm_parts[i] = __popc(all);
-    }
-    __syncthreads();
-    for (int t = threadIdx.x; t < (kWarps + 1) * C::HEADS; t += kThreads) {
-        const int i = t / C::HEADS, h = t % C::HEADS, n = sm_parts[i];
-        if (n == 0) continue;
-        const Place q = sm_seg[i];
-        float M = -INFINITY, L = 0.f;
-        for (int k = 0; k < n; ++k) M = fmaxf(M, sm_ml[sm_part[i][k] / 2][sm_part[i][k] % 2][h].x);
-        const float mb = M == -INFINITY ? 0.f : M;
-        for (int k = 0; k < n; ++k) {
-            const float2 ml = sm_ml[sm_part[i][k] / 2][sm_part[i][k] % 2][h];
-            const float e = ex2(ml.x - mb);
-            sm_fac[i][k][h] = e;
-            L += e * ml.y;
-        }
-        sm_sum[i][h] = L;
-        const int side = q.beg < u0 ? 0 : q.end > u1 ? 1 : -1;
-        if (h == 0) sm_side[i] = side;
-        if (side >= 0) {
-            __stcg(&p.part_ml[(me * 2 + side) * 16 + h], make_float2(M, L));
-            if (h == 0) {
-                sm_cut[side] = q;
-                sm_on[side] = 1;
-            }
-        } else {
-            const int hk = q.ht / tiles, h0 = (q.ht % tiles) * C::HEADS;
-            if (p.a.lse && h0 + h < G)
-                p.a.lse[(int64_t)q.b * s.n_heads + hk * G + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-        }
-    }
-    __syncthreads();
-    // a warp per fragment of every cut segment
-    for (int i = 0, t = warp; i <= kWarps; ++i) {
-        const int n = sm_parts[i];
-        if (n == 0) continue;
-        if (t >= C::FRAGS) {
-            t -= C::FRAGS;
-            continue;
-        }
-        const Place q = sm_seg[i];
-        const int side = sm_side[i], hk = q.ht / tiles, h0 = (q.ht % tiles) * C::HEADS;
-        const float vs = p.v_scale[hk];
-        float4* dst = p.part_o + ((me * 2 + side) * C::FRAGS) * 32 + lane;
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)q.b * s.n_heads + hk * G + h0) * D;
-        for (; t < C::FRAGS; t += kWarps) {
-            const int nt = t / C::DT;
-            const float* e0 = &sm_fac[i][0][nt * 8 + 2 * j];
-            float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-            for (int k = 0; k < n; ++k) {
-                const int code = sm_part[i][k];
-                const float4 v = part_at(code / 2, code % 2)[t * 32 + lane];
-                const float2 e = *reinterpret_cast<const float2*>(e0 + k * C::HEADS);
-                a[0] += e.x * v.x;
-                a[1] += e.y * v.y;
-                a[2] += e.x * v.z;
-                a[3] += e.y * v.w;
-            }
-            if (side >= 0) {
-                __stcg(dst + t * 32, make_float4(a[0], a[1], a[2], a[3]));
-            } else {
-                const float2 L = *reinterpret_cast<const float2*>(&sm_sum[i][nt * 8 + 2 * j]);
-                const float r[2] = {L.x == 0.f ? 0.f : vs / L.x, L.y == 0.f ? 0.f : vs / L.y};
-                emit<C>(out, min(C::HEADS, G - h0), nt, t % C::DT, a, r);
-            }
-        }
-        t -= C::FRAGS;
+    } else {
+        warps_meet();
     }
 
     // ---- segments cut between CTAs -------------------------------------------------------
@@ -762,8 +716,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             sm_last[threadIdx.x] = 0;
             if (sm_on[threadIdx.x]) {
                 const Place q = sm_cut[threadIdx.x];
-                int* arrived = p.arrived + q.b * HT + q.ht;
-                const int n = cta_of(q.end - 1) - cta_of(q.beg) + 1;
+                int* arrived = p.arrived + (q.b * s.n_kv_heads + q.hk) * tiles + q.tile;
+                const int c0 = cta_of(q.beg), n = cta_of(q.end - 1) - c0 + 1;
+                sm_c0[threadIdx.x] = c0;
+                sm_n[threadIdx.x] = n;
                 if (atomicAdd(arrived, 1) == n - 1) {
                     sm_last[threadIdx.x] = 1;
                     *arrived = 0;   // for the next call
@@ -771,74 +727,59 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         __syncthreads();
+        __threadfence();
         for (int side = 0; side < 2; ++side) {
             if (!sm_last[side]) continue;
-            __threadfence();
             const Place q = sm_cut[side];
-            const int c0 = cta_of(q.beg), n = cta_of(q.end - 1) - c0 + 1;
-            const int hk = q.ht / tiles, h0 = hk * G + (q.ht % tiles) * C::HEADS;
-            const int heads = min(C::HEADS, G - (q.ht % tiles) * C::HEADS);
-            const float vs = p.v_scale[hk];
-            // the first CTA's part is its second (its segment begins there), the others' their first
-            auto part = [&](int i) { return (c0 + i) * 2 + (i == 0 ? 1 : 0); };
-            // the first parts are on their way while the factors are computed
-            constexpr int BATCH = 16, STEP = 2 * C::FRAGS * 32;
-            float4 v[BATCH];
-            auto fetch = [&](int f, int i0) {
-                const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    if (i0 + i < n) v[i] = __ldcg(src + i * STEP + (i0 + i == 0 ? STEP / 2 : 0));
-            };
-            if (warp < C::FRAGS) fetch(warp, 0);
-            float* fac = reinterpret_cast<float*>(smem_raw);   // [n][HEADS]: the rings are idle
-            for (int h = warp; h < C::HEADS; h += kWarps) {
-                float2 ml[kMaxCtas / 32];
-                float M = -INFINITY, L = 0.f;
-#pragma unroll
-                for (int i = 0; i < kMaxCtas / 32; ++i) {
-                    ml[i] = lane + 32 * i < n ? __ldcg(&p.part_ml[part(lane + 32 * i) * 16 + h]) : make_float2(-INFINITY, 0.f);
-                    M = fmaxf(M, ml[i].x);
-                }
-                for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
-                const float mb = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                for (int i = 0; i < kMaxCtas / 32; ++i) {
-                    const float e = ex2(ml[i].x - mb);
-                    if (lane + 32 * i < n) fac[(lane + 32 * i) * C::HEADS + h] = e;
-                    L += e * ml[i].y;
-                }
-                for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
-                if (lane == 0) {
-                    sm_sum[0][h] = L;
-                    if (p.a.lse && h < heads)
-                        p.a.lse[(int64_t)q.b * s.n_heads + h0 + h] = L == 0.f ? -INFINITY : M * kLn2 + logf(L);
-                }
-            }
-            __syncthreads();
+            const int c0 = sm_c0[side], n = sm_n[side];
+            const float vs = p.v_scale[q.hk];
+            // parts of all CTAs in order, BATCH of them in flight; the first CTA's part is its
+            // second (its segment begins there), the others' their first
+            constexpr int BATCH = 8, STEP = 2 * C::FRAGS * 32;
 #pragma unroll 1
             for (int f = warp; f < C::FRAGS; f += kWarps) {
-                const int h = f / C::DT * 8 + 2 * j;
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
+                const int nt = f / C::DT;
+                float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                 for (int i0 = 0; i0 < n; i0 += BATCH) {
-                    if (f != warp || i0) fetch(f, i0);
+                    const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
+                    const float4* sml = p.part_ml + (c0 + i0) * 16 + nt * 4 + j;
+                    float4 v[BATCH], ml[BATCH];
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i)
-                        if (i0 + i < n) {
-                            const float2 e = *reinterpret_cast<const float2*>(fac + (i0 + i) * C::HEADS + h);
-                            a[0] += e.x * v[i].x;
-                            a[1] += e.y * v[i].y;
-                            a[2] += e.x * v[i].z;
-                            a[3] += e.y * v[i].w;
-                        }
+                    for (int i = 0; i < BATCH; ++i) {
+                        const int second = i0 + i == 0;
+                        ml[i] = i0 + i < n ? __ldcg(sml + i * 16 + second * 8) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
+                        v[i] = i0 + i < n ? __ldcg(src + i * STEP + second * (STEP / 2)) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+                    float m0 = M[0], m1 = M[1];
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        m0 = fmaxf(m0, ml[i].x);
+                        m1 = fmaxf(m1, ml[i].z);
+                    }
+                    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+                    const float f0 = ex2(M[0] - b0), f1 = ex2(M[1] - b1);
+                    M[0] = m0;
+                    M[1] = m1;
+                    L[0] *= f0;
+                    L[1] *= f1;
+                    a[0] *= f0;
+                    a[1] *= f1;
+                    a[2] *= f0;
+                    a[3] *= f1;
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i) {
+                        const float e0 = ex2(ml[i].x - b0), e1 = ex2(ml[i].z - b1);
+                        L[0] += e0 * ml[i].y;
+                        L[1] += e1 * ml[i].w;
+                        a[0] += e0 * v[i].x;
+                        a[1] += e1 * v[i].y;
+                        a[2] += e0 * v[i].z;
+                        a[3] += e1 * v[i].w;
+                    }
                 }
-                const float2 L = *reinterpret_cast<const float2*>(&sm_sum[0][h]);
-                const float r[2] = {L.x == 0.f ? 0.f : vs / L.x, L.y == 0.f ? 0.f : vs / L.y};
-                emit<C>(static_cast<__nv_bfloat16*>(p.a.out) + ((int64_t)q.b * s.n_heads + h0) * D, heads, f / C::DT,
-                        f % C::DT, a, r);
+                finish<C>(p, q.b, head_of(q), heads_of(q), nt, f % C::DT, vs, a, M, L);
             }
-            __syncthreads();   // fac and sm_sum are free again
         }
     }
     if (bits) atomicOr(p.health, bits);
@@ -868,15 +809,14 @@ auto pick(const KvShape& s, F f) {
 
 }  // namespace
 
-size_t kv_attend_workspace(const Kv& K, size_t out[4]) {
+size_t kv_attend_workspace(const Kv& K, size_t out[3]) {
     const int G = K.s.n_heads / K.s.n_kv_heads;
     const int heads = pick(K.s, [](auto c) { return decltype(c)::HEADS; });
     const size_t part = (size_t)heads * K.s.head_dim * 4;
-    out[0] = (size_t)K.num_sms * kWarps * part;
-    out[1] = (size_t)K.num_sms * 2 * part;
-    out[2] = (size_t)K.num_sms * 2 * 16 * 8;
-    out[3] = (size_t)K.d.max_batch * K.s.n_kv_heads * ((G + heads - 1) / heads) * 4;
-    return out[0] + out[1] + out[2] + out[3];
+    out[0] = (size_t)K.num_sms * 2 * part;
+    out[1] = (size_t)K.num_sms * 2 * 16 * 8;
+    out[2] = (size_t)K.d.max_batch * K.s.n_kv_heads * ((G + heads - 1) / heads) * 4;
+    return out[0] + out[1] + out[2];
 }
 
 cudaError_t kv_attend_setup(Kv& K) {
@@ -906,8 +846,7 @@ cudaError_t kv_attend_setup(Kv& K) {
 }
 
 moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t stream) {
-    const AttendArgs p{a,        K.s,      K.k_scale, K.v_scale, K.health,
-                       K.warp_o, K.part_o, K.part_ml, K.arrived, K.box_rows};
+    const AttendArgs p{a, K.s, K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml, K.arrived, K.box_rows};
     // the kernel counts chunks in 32 bits
     const int64_t most = pick(K.s, [&](auto c) {
         using C = decltype(c);

@@ -341,9 +341,9 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     };
     const size_t o_turns = add((size_t)std::max(half, 1) * 8), o_ks = add((size_t)Hk * 4), o_vs = add((size_t)Hk * 4),
                  o_health = add(4);
-    size_t ws[4];
+    size_t ws[3];
     kv_attend_workspace(K, ws);
-    const size_t o_wo = add(ws[0]), o_po = add(ws[1]), o_pml = add(ws[2]), o_arr = add(ws[3]);
+    const size_t o_po = add(ws[0]), o_pml = add(ws[1]), o_arr = add(ws[2]);
     size_t free_b = 0, total_b = 0;
     e = cudaMemGetInfo(&free_b, &total_b);
     if (e != cudaSuccess) return bail(cuda_fail(e, "cudaMemGetInfo"));
@@ -356,9 +356,8 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     K.k_scale = reinterpret_cast<float*>(base + o_ks);
     K.v_scale = reinterpret_cast<float*>(base + o_vs);
     K.health = reinterpret_cast<unsigned*>(base + o_health);
-    K.warp_o = reinterpret_cast<float4*>(base + o_wo);
     K.part_o = reinterpret_cast<float4*>(base + o_po);
-    K.part_ml = reinterpret_cast<float2*>(base + o_pml);
+    K.part_ml = reinterpret_cast<float4*>(base + o_pml);
     K.arrived = reinterpret_cast<int*>(base + o_arr);
 
     // inv_freq / 2 pi in double keeps 2^-53 of a turn per position; its fraction

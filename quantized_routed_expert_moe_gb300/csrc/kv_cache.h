@@ -50,18 +50,17 @@ struct Kv {
     float *k_scale = nullptr, *v_scale = nullptr;  // [n_kv_heads], ones for a bf16 cache
     unsigned* health = nullptr;
     // attention: the page pools as tensor maps, the parts of segments that are cut between
-    // warps and between CTAs, and how many of a segment's CTAs have arrived
+    // CTAs, and how many of a segment's CTAs have arrived
     CUtensorMap tm_k{}, tm_v{};
     int box_rows = 16;
-    float4 *warp_o = nullptr, *part_o = nullptr;
-    float2* part_ml = nullptr;
+    float4 *part_o = nullptr, *part_ml = nullptr;
     int* arrived = nullptr;
     void* block = nullptr;       // the allocation that holds all of the above
     size_t device_bytes = 0;
 };
 
-// Bytes of warp_o, part_o, part_ml and arrived; needs K.d, K.s and K.num_sms.
-size_t kv_attend_workspace(const Kv& K, size_t out[4]);
+// Bytes of part_o, part_ml and arrived; needs K.d, K.s and K.num_sms.
+size_t kv_attend_workspace(const Kv& K, size_t out[3]);
 cudaError_t kv_attend_setup(Kv& K);
 moe_status kv_attend_launch(Kv& kv, const moe_kv_attend_args& a, cudaStream_t s);
 
