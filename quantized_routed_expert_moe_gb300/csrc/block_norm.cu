@@ -51,62 +51,285 @@ struct NormArgs {
     const float *w_post, *w_pre;
     void *r, *h;
     int T;
+    int ahead;   // rows on their way
 };
 
-__device__ __forceinline__ float load_as(const void* p, int t, int64_t i) {
-    return t == MOE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+// A row is cut into tiles of 256 channels; a lane holds channels 4 lane.. and 128 +
+// 4 lane.. of its tiles, so that fp32 and bf16 rows are both read in whole lines.
+// Rows pass once, around L1: it keeps the weights, which every row reads. Not the
+// read-only path, as r may be written over x.
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+    if constexpr (sizeof(T) == 4) {
+        float4 v;
+        asm volatile("ld.global.L1::no_allocate.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p) : "memory");
+        return v;
+    } else {
+        uint2 v;
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
 }
-__device__ __forceinline__ void store_as(void* p, int t, int64_t i, float v) {
-    if (t == MOE_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-    else static_cast<float*>(p)[i] = v;
+// The same by way of shared memory, in the thread's own slot: nothing to wait for but
+// the thread's own copies.
+template <typename T>
+__device__ __forceinline__ void copy4(uint32_t slot, const T* p) {
+    if constexpr (sizeof(T) == 4) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot), "l"(p) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(slot), "l"(p) : "memory");
 }
+template <typename T>
+__device__ __forceinline__ float4 slot4(uint32_t slot) {
+    if constexpr (sizeof(T) == 4) {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(slot) : "memory");
+        return v;
+    } else {
+        uint2 v;
+        asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(slot) : "memory");
+        return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                           __uint_as_float(v.y & 0xffff0000u));
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, float4 v) {
+    if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float4*>(p) = v;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
+        *reinterpret_cast<uint2*>(p) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+}
+__device__ __forceinline__ float sq(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
 
-constexpr int kThreads = 256;
-
-__device__ float block_sum(float v, float* sm) {
-    for (int i = 16; i; i >>= 1) v += __shfl_xor_sync(~0u, v, i);
-    __syncthreads();
-    if (threadIdx.x % 32 == 0) sm[threadIdx.x / 32] = v;
-    __syncthreads();
-    v = 0.f;
-    for (int i = 0; i < kThreads / 32; ++i) v += sm[i];
+// A row's sum over its warps, in a fixed order. `sm` is used again only after the
+// row's other sum, whose barrier every reader of this one has passed.
+template <bool CTA>
+__device__ __forceinline__ float row_sum(float v, float* sm) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    if constexpr (CTA) {
+        const int lane = threadIdx.x % 32;
+        if (lane == 0) sm[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = lane < blockDim.x / 32 ? sm[lane] : 0.f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+    }
     return v;
 }
 
-// One CTA per row; the row of r in shared memory, in fp32.
-__global__ void __launch_bounds__(kThreads) k_block_norm_rows(const NormArgs p) {
-    extern __shared__ float row[];
-    __shared__ float sm[kThreads / 32];
+// The rows are independent streams: read x, o and gate once, write r and h once,
+// with two sums over the row between (of o, then of r). A row stays in the registers
+// of one CTA (CTA) or of one warp, K tiles per warp. Where a CTA has many rows (AHEAD),
+// a thread copies its channels of the next p.ahead rows into shared memory, so that
+// they are on their way while this one waits for its sums.
+template <typename R, typename B, typename O, int K, bool CTA, bool AHEAD, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
+    __shared__ float sm[2][32];
+    extern __shared__ __align__(16) uint8_t slots[];
     const moe_block_norm_desc& d = p.d;
-    const int H = d.hidden;
-    for (int t = blockIdx.x; t < p.T; t += gridDim.x) {
-        float inv = 1.f;
-        if (p.w_post) {
-            float ss = 0.f;
-            for (int i = threadIdx.x; i < H; i += kThreads) {
-                const float v = load_as(p.o, d.block_dtype, t * d.o_stride + i);
-                ss += v * v;
-            }
-            inv = 1.f / sqrtf(block_sum(ss, sm) / H + d.eps);
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int warps = CTA ? blockDim.x / 32 : 1;
+    const int per = CTA ? 1 : blockDim.x / 32;   // rows of a CTA at a time
+    const int c0 = (CTA ? warp * 256 : 0) + lane * 4, left = d.hidden - c0;
+    const float inv_h = 1.f / d.hidden;
+    // vector (k, i) is channels c0 + at(k, i) ..
+    auto at = [&](int k, int i) { return k * warps * 256 + i * 128; };
+    // slots of this thread: x's vectors, o's, and the gate's where it has rows
+    const uint32_t base = (uint32_t)__cvta_generic_to_shared(slots);
+    const uint32_t stage = 2 * K * blockDim.x * 4 * (sizeof(R) + 2 * sizeof(B));       // of a row
+    const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B);   // between vectors
+    const uint32_t sx = base + threadIdx.x * 4 * sizeof(R), so = base + 2 * K * dx + threadIdx.x * 4 * sizeof(B);
+    const uint32_t sg = so + 2 * K * db;
+    const bool ga = AHEAD && p.gate && d.gate_stride != 0;
+    auto fetch = [&](int t, uint32_t at_row) {
+        const R* x = static_cast<const R*>(p.x) + t * d.x_stride + c0;
+        const B* o = static_cast<const B*>(p.o) + t * d.o_stride + c0;
+        const B* gate = static_cast<const B*>(p.gate) + t * d.gate_stride + c0;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (at(k, i) < left) {
+                    copy4(at_row + sx + (2 * k + i) * dx, x + at(k, i));
+                    if (p.o) copy4(at_row + so + (2 * k + i) * db, o + at(k, i));
+                    if (ga) copy4(at_row + sg + (2 * k + i) * db, gate + at(k, i));
+                }
+    };
+    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
+    uint32_t row = 0;   // of this row's slots
+    if constexpr (AHEAD)
+        for (int i = 0; i < p.ahead; ++i) {
+            if (t0 + (int64_t)i * step < p.T) fetch(t0 + i * step, i * stage);
+            commit();
         }
+
+    for (int t = t0; t < p.T; t += step) {
+        const R* x = static_cast<const R*>(p.x) + t * d.x_stride + c0;
+        const B* o = static_cast<const B*>(p.o) + t * d.o_stride + c0;
+        const B* gate = static_cast<const B*>(p.gate) + t * d.gate_stride + c0;
+        R* ro = static_cast<R*>(p.r) + t * d.r_stride + c0;
+        O* ho = static_cast<O*>(p.h) + t * d.h_stride + c0;
+        float4 r[K][2], a[K][2];
+        if constexpr (AHEAD) {
+            if (p.ahead == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
+            else if (p.ahead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+            else asm volatile("cp.async.wait_group 3;" ::: "memory");
+        }
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const bool on = at(k, i) < left;
+                r[k][i] = a[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (on) r[k][i] = AHEAD ? slot4<R>(row + sx + (2 * k + i) * dx) : load4(x + at(k, i));
+                if (on && p.o) a[k][i] = AHEAD ? slot4<B>(row + so + (2 * k + i) * db) : load4(o + at(k, i));
+            }
         float ss = 0.f;
-        for (int i = threadIdx.x; i < H; i += kThreads) {
-            float v = load_as(p.x, d.res_dtype, t * d.x_stride + i);
-            if (p.o) {
-                float a = load_as(p.o, d.block_dtype, t * d.o_stride + i) * inv;
-                if (p.w_post) a *= p.w_post[i] + d.weight_offset;
-                if (p.gate) a *= load_as(p.gate, d.block_dtype, t * d.gate_stride + i);
-                v += d.res_scale * a;
-            }
-            row[i] = v;
-            ss += v * v;
-            if (p.r) store_as(p.r, d.res_dtype, t * d.r_stride + i, v);
+        if (p.gate) {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (at(k, i) < left) {
+                        const float4 g = ga ? slot4<B>(row + sg + (2 * k + i) * db) : load4(gate + at(k, i));
+                        ss += sq(a[k][i]);
+                        a[k][i] = make_float4(a[k][i].x * g.x, a[k][i].y * g.y, a[k][i].z * g.z, a[k][i].w * g.w);
+                    }
+        } else {
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) ss += sq(a[k][i]);
         }
-        if (!p.h) continue;
-        inv = 1.f / sqrtf(block_sum(ss, sm) / H + d.eps);
-        for (int i = threadIdx.x; i < H; i += kThreads)
-            store_as(p.h, d.out_dtype, t * d.h_stride + i, row[i] * inv * (p.w_pre[i] + d.weight_offset));
+        if constexpr (AHEAD) {
+            if (t + (int64_t)p.ahead * step < p.T) fetch(t + p.ahead * step, row);
+            commit();
+            row += stage;
+            if (row == p.ahead * stage) row = 0;
+        }
+        float f = d.res_scale;
+        if (p.w_post) {
+            f /= sqrtf(row_sum<CTA>(ss, sm[0]) * inv_h + d.eps);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (at(k, i) < left) {
+                        const float4 w = *reinterpret_cast<const float4*>(p.w_post + c0 + at(k, i));
+                        a[k][i] = make_float4(a[k][i].x * (w.x + d.weight_offset), a[k][i].y * (w.y + d.weight_offset),
+                                              a[k][i].z * (w.z + d.weight_offset), a[k][i].w * (w.w + d.weight_offset));
+                    }
+        }
+        ss = 0.f;
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                r[k][i] = make_float4(r[k][i].x + f * a[k][i].x, r[k][i].y + f * a[k][i].y, r[k][i].z + f * a[k][i].z,
+                                      r[k][i].w + f * a[k][i].w);
+                ss += sq(r[k][i]);
+                if (p.r && at(k, i) < left) store4(ro + at(k, i), r[k][i]);
+            }
+        if (p.h) {
+            const float inv = 1.f / sqrtf(row_sum<CTA>(ss, sm[1]) * inv_h + d.eps);
+#pragma unroll
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (at(k, i) < left) {
+                        const float4 w = *reinterpret_cast<const float4*>(p.w_pre + c0 + at(k, i)), v = r[k][i];
+                        store4(ho + at(k, i), make_float4(v.x * inv * (w.x + d.weight_offset), v.y * inv * (w.y + d.weight_offset),
+                                                          v.z * inv * (w.z + d.weight_offset), v.w * inv * (w.w + d.weight_offset)));
+                    }
+        }
+        // a row with one sum only: its readers meet before the next row's sum
+        if (CTA && !(p.w_post && p.h)) __syncthreads();
     }
+}
+
+// CTAs of a kernel that the device holds at a time; `held` caches it.
+cudaError_t resident(const void* kernel, int threads, size_t smem, int& held) {
+    if (held) return cudaSuccess;
+    int dev = 0, sms = 0, n = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess && smem)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+    if (e == cudaSuccess) held = sms * (n > 0 ? n : 1);
+    return e;
+}
+
+// Few rows: each has a CTA or a warp of its own. Returns whether the device holds them all.
+template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MINB>
+bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) {
+    const auto kernel = k_block_norm<R, B, O, K, CTA, false, MAXT, MINB>;
+    const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
+    static int held[33];       // by warps of a CTA
+    e = resident(reinterpret_cast<const void*>(kernel), threads, 0, held[threads / 32]);
+    if (e != cudaSuccess) return true;
+    if (need > held[threads / 32]) return false;
+    kernel<<<need, threads, 0, s>>>(p);
+    e = cudaGetLastError();
+    return true;
+}
+
+// Many rows: resident CTAs that copy ahead, 4, 2 or 1 rows, as many as leave the
+// shared memory to `ctas` per SM.
+template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MINB>
+cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
+    const auto kernel = k_block_norm<R, B, O, K, CTA, true, MAXT, MINB>;
+    const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
+    const size_t stage = (size_t)threads * 2 * K * 4 * (sizeof(R) + 2 * sizeof(B));
+    p.ahead = 4;
+    while (p.ahead > 1 && p.ahead * stage * ctas > 200 * 1024) p.ahead /= 2;
+    static int held[33];
+    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, p.ahead * stage, held[threads / 32]);
+    if (e != cudaSuccess) return e;
+    kernel<<<need < held[threads / 32] ? need : held[threads / 32], threads, p.ahead * stage, s>>>(p);
+    return cudaGetLastError();
+}
+
+// By the row's tiles of 256 channels. Up to 4: a warp per row. Up to 32: a warp per
+// tile where the rows are few, for the shortest chain; two tiles per warp where they
+// are many (the reductions and barriers of a row weigh half). Above: four tiles per
+// warp.
+template <typename R, typename B, typename O>
+cudaError_t launch_row(const NormArgs& p, cudaStream_t s) {
+    const int n = (p.d.hidden + 255) / 256;
+    cudaError_t e;
+    if (n == 1) return launch_few<R, B, O, 1, false, 256, 4>(p, 256, s, e) ? e : launch_many<R, B, O, 1, false, 256, 4>(p, 256, 4, s);
+    if (n == 2) return launch_few<R, B, O, 2, false, 256, 3>(p, 256, s, e) ? e : launch_many<R, B, O, 2, false, 256, 3>(p, 256, 3, s);
+    if (n == 3) return launch_few<R, B, O, 3, false, 256, 2>(p, 256, s, e) ? e : launch_many<R, B, O, 3, false, 256, 2>(p, 256, 2, s);
+    if (n == 4) return launch_few<R, B, O, 4, false, 256, 2>(p, 256, s, e) ? e : launch_many<R, B, O, 4, false, 256, 2>(p, 256, 2, s);
+    if (n <= 32) {
+        if (launch_few<R, B, O, 1, true, 1024, 1>(p, n * 32, s, e)) return e;
+        const int threads = (n + 1) / 2 * 32;
+        if (n <= 24) return launch_many<R, B, O, 2, true, 384, 2>(p, threads, 768 / threads, s);
+        return launch_many<R, B, O, 2, true, 512, 2>(p, threads, 2, s);
+    }
+    const int threads = (n + 3) / 4 * 32;
+    return launch_few<R, B, O, 4, true, 512, 1>(p, threads, s, e) ? e : launch_many<R, B, O, 4, true, 512, 1>(p, threads, 1, s);
+}
+
+template <typename R, typename B>
+cudaError_t launch_out(const NormArgs& p, cudaStream_t s) {
+    return p.d.out_dtype == MOE_F32 ? launch_row<R, B, float>(p, s) : launch_row<R, B, __nv_bfloat16>(p, s);
+}
+
+template <typename R>
+cudaError_t launch_block(const NormArgs& p, cudaStream_t s) {
+    return p.d.block_dtype == MOE_F32 ? launch_out<R, float>(p, s) : launch_out<R, __nv_bfloat16>(p, s);
+}
+
+cudaError_t launch(const NormArgs& p, cudaStream_t s) {
+    return p.d.res_dtype == MOE_F32 ? launch_block<float>(p, s) : launch_block<__nv_bfloat16>(p, s);
 }
 
 }  // namespace
@@ -129,13 +352,8 @@ moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const 
     if (st != MOE_OK || T == 0) return st;
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T};
-    const size_t smem = (size_t)desc->hidden * 4;
-    cudaError_t e = cudaFuncSetAttribute(k_block_norm_rows, cudaFuncAttributeMaxDynamicSharedMemorySize, 65536);
-    if (e == cudaSuccess) {
-        k_block_norm_rows<<<T < 4096 ? T : 4096, kThreads, smem, static_cast<cudaStream_t>(stream)>>>(p);
-        e = cudaGetLastError();
-    }
+    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, 1};
+    const cudaError_t e = launch(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "block norm launch");
 }
 

@@ -361,10 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int ahead = w0;
         int issued = 0, put = 0;   // stages issued, and the stage after them
         auto issue = [&]() {       // the looked-up chunk's keys or values into the next stage
-            if (nx_read && (nx_page < 0 || nx_page >= s.n_pages)) {
-                bits |= MOE_KV_BAD_PAGE;
-                nx_page = -1;
-            }
+            if (nx_read) nx_page = kv_page(s, nx_page, bits);
             const uint32_t bar = bw::saddr(&sm_bar[warp][put]);
             const unsigned have = __ballot_sync(~0u, nx_page >= 0);
             if (lane == 0) {

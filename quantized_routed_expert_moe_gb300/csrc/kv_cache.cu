@@ -122,56 +122,26 @@ moe_status check_attend(const moe_kv_desc* d, const moe_kv_attend_args* a) {
 //
 // A head is D / 16 groups of 16 channels, two 16-byte vectors each: a rotated
 // group holds 8 pairs (channels 8g.. and rotary_dim / 2 + 8g.., or the 8 adjacent
-// pairs from 16g), a group past rotary_dim is copied. One thread moves one group
-// of one head of one token and reads both vectors before it writes, so q may be
-// rotated in place.
+// pairs from 16g), a group past rotary_dim is copied. One lane moves a whole group
+// and reads both vectors before it writes, so q may be rotated in place.
 //
 // The angle p * inv_freq is kept as a 64-bit fraction of a turn: turns =
 // frac(inv_freq / 2 pi) * 2^64, and p * turns mod 2^64 is the exact phase of
 // any position, where a 32-bit product loses the phase from 10^5 or so. The
 // upper 32 bits (2^-32 of a turn) go to sincospif.
 
-struct Vec8 {
-    float v[8];
-};
-
-__device__ __forceinline__ Vec8 load8(const __nv_bfloat16* p) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    Vec8 r;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        r.v[2 * i] = __uint_as_float(w[i] << 16);
-        r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-    return r;
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 v) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const Vec8& r) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16(r.v[0], r.v[1]), pack_bf16(r.v[2], r.v[3]),
-                                              pack_bf16(r.v[4], r.v[5]), pack_bf16(r.v[6], r.v[7]));
+// e4m3 of two values / scale: a true division, so that the value stored is the
+// nearest one to the quotient; saturating, NaN stays NaN.
+__device__ __forceinline__ uint32_t quant2(float2 v, float scale) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale)), __NV_SATFINITE, __NV_E4M3);
 }
-
-// e4m3 of r / scale: a true division, so that the value stored is the nearest
-// one to the quotient; saturating, NaN stays NaN.
-__device__ __forceinline__ void store8(uint8_t* p, const Vec8& r, float scale) {
-    uint32_t w[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(r.v[4 * i], scale), __fdiv_rn(r.v[4 * i + 1], scale)), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
-            make_float2(__fdiv_rn(r.v[4 * i + 2], scale), __fdiv_rn(r.v[4 * i + 3], scale)), __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | hi << 16;
-    }
-    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-}
-
 __device__ __forceinline__ void phase(uint64_t turns, int position, float& c, float& s) {
     const uint64_t ph = turns * (uint64_t)position;
     sincospif((float)(int32_t)(ph >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
@@ -184,83 +154,158 @@ struct AppendArgs {
     const uint64_t* turns;
     const float *k_scale, *v_scale;
     unsigned* health;
+    int parts, rounds;   // units and rounds of a token
 };
 
-__global__ void __launch_bounds__(256) k_kv_append(const AppendArgs p) {
+// A round is 32 / (D / 16) heads of a token, one warp's copy of 1 KB; a unit is
+// every `parts`-th round of a token. A warp streams the rounds of its units through
+// its own ring of shared memory, each lane its own vectors (so it waits for nothing
+// but its own copies), kAhead of them on their way, and looks up the next unit's page
+// meanwhile. The lanes share the sines and cosines of a unit's angles. The kernel
+// reads and writes every value once: bound by memory for many tokens, by latency for
+// few, where a warp has one round.
+constexpr int kAhead = 8;
+constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
+
+template <bool ADJACENT, bool E4M3>
+__global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
+    extern __shared__ __align__(16) uint4 ring[];
+    __shared__ __align__(16) float sm_c[8][128], sm_s[8][128];
     const KvShape& s = p.s;
-    const int groups = s.head_dim / 16;
-    const int q_heads = p.a.q ? s.n_heads : 0;
-    const int heads = q_heads + 2 * s.n_kv_heads;
-    const int64_t total = (int64_t)p.a.T * heads * groups;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-        const int g = (int)(i % groups);
-        const int64_t th = i / groups;
-        const int head = (int)(th % heads);
-        const int t = (int)(th / heads);
-        const int pos = p.a.positions[t];
-        const bool is_q = head < q_heads;
-        const bool is_v = head >= q_heads + s.n_kv_heads;
-        const int hk = is_v ? head - q_heads - s.n_kv_heads : head - q_heads;
-        const bool turned = !is_v && 16 * g < s.rotary_dim;
-        // channels of the group's two vectors
-        const int c0 = turned && !s.rotary_adjacent ? 8 * g : 16 * g;
-        const int c1 = turned && !s.rotary_adjacent ? s.rotary_dim / 2 + 8 * g : 16 * g + 8;
-        const __nv_bfloat16* src =
-            is_q ? static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)t * p.a.q_stride + (int64_t)head * s.head_dim
-            : is_v ? static_cast<const __nv_bfloat16*>(p.a.v) + (int64_t)t * p.a.v_stride + (int64_t)hk * s.head_dim
-                   : static_cast<const __nv_bfloat16*>(p.a.k) + (int64_t)t * p.a.k_stride + (int64_t)hk * s.head_dim;
-        Vec8 a{}, b{};
-        if (pos >= 0) {
-            a = load8(src + c0);
-            b = load8(src + c1);
-            if (turned) {
-                if (s.rotary_adjacent) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float c, sn;
-                        phase(p.turns[8 * g + j], pos, c, sn);
-                        float* v = j < 4 ? a.v : b.v;
-                        const float x = v[2 * (j & 3)], y = v[2 * (j & 3) + 1];
-                        v[2 * (j & 3)] = x * c - y * sn;
-                        v[2 * (j & 3) + 1] = y * c + x * sn;
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float c, sn;
-                        phase(p.turns[8 * g + j], pos, c, sn);
-                        const float x = a.v[j], y = b.v[j];
-                        a.v[j] = x * c - y * sn;
-                        b.v[j] = y * c + x * sn;
-                    }
-                }
+    const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+    const int groups = s.head_dim / 16, g = lane % groups, side = 32 / groups, half = s.rotary_dim / 2;
+    const int q_heads = p.a.q ? s.n_heads : 0, k_heads = q_heads + s.n_kv_heads, heads = k_heads + s.n_kv_heads;
+    const bool rotated = 16 * g < s.rotary_dim;
+    // the group's two vectors, where it is rotated and where not
+    const int c0 = rotated && !ADJACENT ? 8 * g : 16 * g, step = rotated && !ADJACENT ? half : 8;
+    const int64_t units = (int64_t)p.a.T * p.parts;
+    const int stride = gridDim.x * 8;
+    uint4* const slots = ring + warp * (kAhead * 64) + lane;
+    uint32_t bits = 0;
+
+    // the copies: round fr of unit fu next, into slot `put`
+    int64_t fu = (int64_t)blockIdx.x * 8 + warp;
+    int fr = (int)(fu % p.parts), put = 0;
+    auto fetch = [&] {
+        if (fu < units) {
+            const int64_t t = fu / p.parts;
+            const int head = fr * side + lane / groups;
+            if (head < heads) {
+                const bool turned = head < k_heads;
+                const __nv_bfloat16* src =
+                    head < q_heads ? static_cast<const __nv_bfloat16*>(p.a.q) + t * p.a.q_stride + head * s.head_dim
+                    : turned ? static_cast<const __nv_bfloat16*>(p.a.k) + t * p.a.k_stride + (head - q_heads) * s.head_dim
+                             : static_cast<const __nv_bfloat16*>(p.a.v) + t * p.a.v_stride + (head - k_heads) * s.head_dim;
+                const uint32_t to = (uint32_t)__cvta_generic_to_shared(slots + put * 64);
+                const int a = turned ? c0 : 16 * g, b = turned ? c0 + step : 16 * g + 8;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + a) : "memory");
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(src + b) : "memory");
+            }
+            if ((fr += p.parts) >= p.rounds) {
+                fu += stride;
+                fr = (int)(fu % p.parts);
             }
         }
-        if (is_q) {
-            __nv_bfloat16* dst =
-                static_cast<__nv_bfloat16*>(p.a.q_out) + ((int64_t)t * s.n_heads + head) * s.head_dim;
-            store8(dst + c0, a);
-            store8(dst + c1, b);
-            continue;
+        put = (put + 1) % kAhead;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int64_t unit = fu;
+    if (unit >= units) return;
+    // position and page of a unit, read one unit ahead
+    int pos = p.a.positions[unit / p.parts], seq = p.a.seq ? p.a.seq[unit / p.parts] : (int)(unit / p.parts);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) fetch();
+    auto look_up = [&](int pos, int seq, bool& read) {
+        const int64_t at = pos >= 0 ? kv_entry(s, p.a.n_seqs, p.a.max_pages, seq, pos, bits) : -1;
+        read = at >= 0;
+        return read ? p.a.block_table[at] : -1;
+    };
+    bool read;
+    int page = look_up(pos, seq, read);
+    for (int take = 0; unit < units;) {
+        const int t = (int)(unit / p.parts), part = (int)(unit - (int64_t)t * p.parts);
+        const int64_t next = unit + stride;
+        int next_pos = -1, next_seq = 0;
+        if (next < units) {
+            next_pos = p.a.positions[next / p.parts];
+            next_seq = p.a.seq ? p.a.seq[next / p.parts] : (int)(next / p.parts);
         }
-        if (pos < 0) continue;
-        uint32_t bits = 0;
-        const int page = kv_page(s, p.a.block_table, p.a.n_seqs, p.a.max_pages, p.a.seq ? p.a.seq[t] : t, pos, bits);
-        if (page < 0) {
-            if (g == 0) atomicOr(p.health, bits);
-            continue;
+        if (pos >= 0)
+            for (int f = lane; f < half; f += 32) phase(p.turns[f], pos, sm_c[warp][f], sm_s[warp][f]);
+        if (read) page = kv_page(s, page, bits);
+        const int64_t row = page >= 0 ? kv_offset(s, page, 0, pos % s.page_size) : 0;
+        bool next_read = false;
+        int next_page = -1;
+        __syncwarp();
+        const float *const c = &sm_c[warp][8 * g], *const sn = &sm_s[warp][8 * g];
+        for (int r = part; r < p.rounds; r += p.parts) {
+            asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+            const uint4 u0 = slots[take * 64], u1 = slots[take * 64 + 32];
+            take = (take + 1) % kAhead;
+            if (r == part) next_page = look_up(next_pos, next_seq, next_read);
+            const int head = r * side + lane / groups;
+            const bool is_q = head < q_heads, is_v = head >= k_heads, turn = rotated && !is_v;
+            if (head < heads && (is_q || page >= 0)) {
+                const int hk = head - (is_v ? k_heads : q_heads);
+                const int at0 = is_v ? 16 * g : c0, at1 = is_v ? 16 * g + 8 : c0 + step;
+                const float scale = E4M3 && !is_q ? (is_v ? p.v_scale : p.k_scale)[hk] : 1.f;
+                uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
+                uint32_t e[2][2] = {};
+                // two channels of either vector at a time
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
+                    if (turn) {
+                        if constexpr (ADJACENT) {
+                            a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
+                            b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
+                        } else {
+                            const float2 cc = *reinterpret_cast<const float2*>(c + 2 * x);
+                            const float2 ss = *reinterpret_cast<const float2*>(sn + 2 * x);
+                            const float2 a0 = a;
+                            a = make_float2(a.x * cc.x - b.x * ss.x, a.y * cc.y - b.y * ss.y);
+                            b = make_float2(b.x * cc.x + a0.x * ss.x, b.y * cc.y + a0.y * ss.y);
+                        }
+                    }
+                    if (E4M3 && !is_q) {
+                        e[0][x / 2] |= quant2(a, scale) << 16 * (x % 2);
+                        e[1][x / 2] |= quant2(b, scale) << 16 * (x % 2);
+                    } else if (turn) {
+                        w[0][x] = pack2(a);
+                        w[1][x] = pack2(b);
+                    }
+                    if (is_q && pos < 0) w[0][x] = w[1][x] = 0;
+                }
+                const int64_t off = row + hk * s.head_stride;
+                if (E4M3 && !is_q) {
+                    uint8_t* to = static_cast<uint8_t*>(is_v ? p.v_pages : p.k_pages) + off;
+                    *reinterpret_cast<uint2*>(to + at0) = make_uint2(e[0][0], e[0][1]);
+                    *reinterpret_cast<uint2*>(to + at1) = make_uint2(e[1][0], e[1][1]);
+                } else {
+                    __nv_bfloat16* dst = is_q ? static_cast<__nv_bfloat16*>(p.a.q_out) + ((int64_t)t * s.n_heads + head) * s.head_dim
+                                              : static_cast<__nv_bfloat16*>(is_v ? p.v_pages : p.k_pages) + off;
+                    *reinterpret_cast<uint4*>(dst + at0) = make_uint4(w[0][0], w[0][1], w[0][2], w[0][3]);
+                    *reinterpret_cast<uint4*>(dst + at1) = make_uint4(w[1][0], w[1][1], w[1][2], w[1][3]);
+                }
+            }
+            fetch();
         }
-        const int64_t off = kv_offset(s, page, hk, pos % s.page_size);
-        void* pool = is_v ? p.v_pages : p.k_pages;
-        if (s.e4m3) {
-            const float sc = (is_v ? p.v_scale : p.k_scale)[hk];
-            store8(static_cast<uint8_t*>(pool) + off + c0, a, sc);
-            store8(static_cast<uint8_t*>(pool) + off + c1, b, sc);
-        } else {
-            store8(static_cast<__nv_bfloat16*>(pool) + off + c0, a);
-            store8(static_cast<__nv_bfloat16*>(pool) + off + c1, b);
-        }
+        unit = next;
+        pos = next_pos;
+        seq = next_seq;
+        page = next_page;
+        read = next_read;
+        __syncwarp();   // every lane is done with the sines
     }
+    if (bits) atomicOr(p.health, bits);
+}
+
+using AppendKernel = void (*)(const AppendArgs);
+
+AppendKernel append_kernel(const KvShape& s) {
+    return s.rotary_adjacent ? (s.e4m3 ? k_kv_append<true, true> : k_kv_append<true, false>)
+                             : (s.e4m3 ? k_kv_append<false, true> : k_kv_append<false, false>);
 }
 
 }  // namespace
@@ -289,7 +334,8 @@ moe_status moe_kv_locate(const moe_kv_desc* desc, const int32_t* block_table, in
     if (head < 0 || head >= desc->n_kv_heads) return fail(MOE_E_INVALID, "head outside 0..n_kv_heads-1");
     const KvShape s = shape_of(*desc);
     uint32_t b = 0;
-    const int page = kv_page(s, block_table, n_seqs, max_pages, seq, position, b);
+    const int64_t at = kv_entry(s, n_seqs, max_pages, seq, position, b);
+    const int page = at >= 0 ? kv_page(s, block_table[at], b) : -1;
     if (bits) *bits = b;
     if (page < 0) return fail(MOE_E_STATE, "the position has no slot (health bits " + std::to_string(b) + ")");
     *offset = kv_offset(s, page, head, position % s.page_size);
@@ -378,6 +424,8 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     if (e == cudaSuccess) e = cudaMemcpy(K.k_scale, ks.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = cudaMemcpy(K.v_scale, vs.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = kv_attend_setup(K);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(append_kernel(K.s), cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendRing);
     // the set-up ran on the legacy stream: finish it before any other stream may run a call
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return bail(cuda_fail(e, "moe_kv_create set-up"));
@@ -405,11 +453,16 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     if (args->T == 0) return MOE_OK;
     DeviceGuard g(K.device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    const AppendArgs p{*args, K.s, K.k_pages, K.v_pages, K.turns, K.k_scale, K.v_scale, K.health};
-    const int64_t total =
-        (int64_t)args->T * ((args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads) * (K.s.head_dim / 16);
-    const int grid = (int)std::min<int64_t>((total + 255) / 256, (int64_t)K.num_sms * 64);
-    k_kv_append<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+    AppendArgs p{*args, K.s, K.k_pages, K.v_pages, K.turns, K.k_scale, K.v_scale, K.health, 1, 1};
+    const int heads = (args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads, side = 32 / (K.s.head_dim / 16);
+    p.rounds = (heads + side - 1) / side;
+    // as few units per token as give every resident warp at least eight, so that the last
+    // ones leave little of the GPU idle; one round per unit where the tokens are few
+    const int64_t warps = (int64_t)K.num_sms * 3 * 8;
+    while (p.parts * 2 <= p.rounds && (int64_t)args->T * p.parts < 8 * warps) p.parts *= 2;
+    if ((int64_t)args->T * p.rounds <= warps) p.parts = p.rounds;
+    const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)args->T * p.parts + 7) / 8, (int64_t)K.num_sms * 3);
+    append_kernel(K.s)<<<grid, 256, kAppendRing, static_cast<cudaStream_t>(stream)>>>(p);
     const cudaError_t e = cudaGetLastError();
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "append launch");
 }

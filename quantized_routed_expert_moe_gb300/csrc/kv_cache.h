@@ -15,10 +15,9 @@ struct KvShape {
     int64_t page_stride, head_stride, token_stride;  // elements
 };
 
-// Page of (seq, position), or -1 with a health bit. The one place where a block
-// table is turned into a page, on the host (moe_kv_locate) and in the kernels.
-__host__ __device__ inline int kv_page(const KvShape& s, const int32_t* table, int n_seqs, int max_pages, int seq,
-                                       int position, uint32_t& bits) {
+// Index of (seq, position)'s entry in the block table, or -1 with a health bit.
+__host__ __device__ inline int64_t kv_entry(const KvShape& s, int n_seqs, int max_pages, int seq, int position,
+                                            uint32_t& bits) {
     if (seq < 0 || seq >= n_seqs) {
         bits |= MOE_KV_BAD_SEQ;
         return -1;
@@ -28,12 +27,14 @@ __host__ __device__ inline int kv_page(const KvShape& s, const int32_t* table, i
         bits |= MOE_KV_BAD_LENGTH;
         return -1;
     }
-    const int page = table[(int64_t)seq * max_pages + at];
-    if (page < 0 || page >= s.n_pages) {
-        bits |= MOE_KV_BAD_PAGE;
-        return -1;
-    }
-    return page;
+    return (int64_t)seq * max_pages + at;
+}
+
+// A page read from the block table, or -1 with a health bit.
+__host__ __device__ inline int kv_page(const KvShape& s, int page, uint32_t& bits) {
+    if (page >= 0 && page < s.n_pages) return page;
+    bits |= MOE_KV_BAD_PAGE;
+    return -1;
 }
 
 // Element offset of a row of a pool; 64-bit throughout.
