@@ -56,8 +56,7 @@ struct NormArgs {
 
 // A row is cut into tiles of 256 channels; a lane holds channels 4 lane.. and 128 +
 // 4 lane.. of its tiles, so that fp32 and bf16 rows are both read in whole lines.
-// Rows pass once, around L1: it keeps the weights, which every row reads. Not the
-// read-only path, as r may be written over x.
+// Rows pass once, around L1. Not the read-only path, as r may be written over x.
 template <typename T>
 __device__ __forceinline__ float4 load4(const T* p) {
     if constexpr (sizeof(T) == 4) {
@@ -103,6 +102,12 @@ __device__ __forceinline__ void store4(T* p, float4 v) {
             make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
     }
 }
+__device__ __forceinline__ void put4(uint32_t slot, float4 v) {
+    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(slot), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ float4 times(float4 a, float4 b) {
+    return make_float4(a.x * b.x, a.y * b.y, a.z * b.z, a.w * b.w);
+}
 __device__ __forceinline__ float sq(float4 v) { return v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w; }
 
 // A row's sum over its warps, in a fixed order. `sm` is used again only after the
@@ -139,42 +144,66 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     const float inv_h = 1.f / d.hidden;
     // vector (k, i) is channels c0 + at(k, i) ..
     auto at = [&](int k, int i) { return k * warps * 256 + i * 128; };
-    // slots of this thread: x's vectors, o's, and the gate's where it has rows
+    // slots of this thread: for each row ahead x's vectors, o's, and the gate's where it has
+    // rows; then the weights, which every row takes
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(slots);
-    const uint32_t stage = 2 * K * blockDim.x * 4 * (sizeof(R) + 2 * sizeof(B));       // of a row
-    const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B);   // between vectors
+    const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B), dw = blockDim.x * 16;   // between vectors
     const uint32_t sx = base + threadIdx.x * 4 * sizeof(R), so = base + 2 * K * dx + threadIdx.x * 4 * sizeof(B);
-    const uint32_t sg = so + 2 * K * db;
-    const bool ga = AHEAD && p.gate && d.gate_stride != 0;
-    auto fetch = [&](int t, uint32_t at_row) {
-        const R* x = static_cast<const R*>(p.x) + t * d.x_stride + c0;
-        const B* o = static_cast<const B*>(p.o) + t * d.o_stride + c0;
-        const B* gate = static_cast<const B*>(p.gate) + t * d.gate_stride + c0;
+    const uint32_t sg = so + 2 * K * db, stage = 2 * K * (dx + 2 * db), end = p.ahead * stage;
+    const uint32_t sw = base + end + threadIdx.x * 16, sn = sw + 2 * K * dw;
+    const bool gate_rows = p.gate && d.gate_stride != 0, gate_row = p.gate && d.gate_stride == 0;
+    const bool weighted = p.w_post || (AHEAD && gate_row);
+    const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
+    if (t0 >= p.T) return;   // a whole CTA, or a warp that meets no other
+    const R* x = static_cast<const R*>(p.x) + t0 * d.x_stride + c0;
+    const B* o = static_cast<const B*>(p.o) + t0 * d.o_stride + c0;
+    const B* gate = static_cast<const B*>(p.gate) + t0 * d.gate_stride + c0;
+    R* ro = static_cast<R*>(p.r) + t0 * d.r_stride + c0;
+    O* ho = static_cast<O*>(p.h) + t0 * d.h_stride + c0;
+    auto next_row = [&] {
+        x += step * d.x_stride;
+        o += step * d.o_stride;
+        gate += step * d.gate_stride;
+    };
+    auto fetch = [&](uint32_t row) {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (at(k, i) < left) {
-                    copy4(at_row + sx + (2 * k + i) * dx, x + at(k, i));
-                    if (p.o) copy4(at_row + so + (2 * k + i) * db, o + at(k, i));
-                    if (ga) copy4(at_row + sg + (2 * k + i) * db, gate + at(k, i));
+                    copy4(row + sx + (2 * k + i) * dx, x + at(k, i));
+                    if (p.o) copy4(row + so + (2 * k + i) * db, o + at(k, i));
+                    if (gate_rows) copy4(row + sg + (2 * k + i) * db, gate + at(k, i));
                 }
+        next_row();
     };
     auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
-    const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
+    auto weight = [&](const float* w, int k, int i) {
+        const float4 v = *reinterpret_cast<const float4*>(w + c0 + at(k, i));
+        return make_float4(v.x + d.weight_offset, v.y + d.weight_offset, v.z + d.weight_offset, v.w + d.weight_offset);
+    };
     uint32_t row = 0;   // of this row's slots
-    if constexpr (AHEAD)
+    if constexpr (AHEAD) {
         for (int i = 0; i < p.ahead; ++i) {
-            if (t0 + (int64_t)i * step < p.T) fetch(t0 + i * step, i * stage);
+            if (t0 + (int64_t)i * step < p.T) fetch(i * stage);
             commit();
         }
+        // a gate of one row is a weight too
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                if (at(k, i) < left) {
+                    if (weighted) {
+                        float4 w = p.w_post ? weight(p.w_post, k, i) : make_float4(1.f, 1.f, 1.f, 1.f);
+                        if (gate_row) w = times(w, load4(static_cast<const B*>(p.gate) + c0 + at(k, i)));
+                        put4(sw + (2 * k + i) * dw, w);
+                    }
+                    if (p.h) put4(sn + (2 * k + i) * dw, weight(p.w_pre, k, i));
+                }
+    }
 
-    for (int t = t0; t < p.T; t += step) {
-        const R* x = static_cast<const R*>(p.x) + t * d.x_stride + c0;
-        const B* o = static_cast<const B*>(p.o) + t * d.o_stride + c0;
-        const B* gate = static_cast<const B*>(p.gate) + t * d.gate_stride + c0;
-        R* ro = static_cast<R*>(p.r) + t * d.r_stride + c0;
-        O* ho = static_cast<O*>(p.h) + t * d.h_stride + c0;
+    for (int64_t t = t0; t < p.T; t += step) {
         float4 r[K][2], a[K][2];
         if constexpr (AHEAD) {
             if (p.ahead == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -191,40 +220,35 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
                 if (on && p.o) a[k][i] = AHEAD ? slot4<B>(row + so + (2 * k + i) * db) : load4(o + at(k, i));
             }
         float ss = 0.f;
-        if (p.gate) {
+#pragma unroll
+        for (int k = 0; k < K; ++k)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) ss += sq(a[k][i]);
+        if (AHEAD ? gate_rows : p.gate != nullptr) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (at(k, i) < left) {
-                        const float4 g = ga ? slot4<B>(row + sg + (2 * k + i) * db) : load4(gate + at(k, i));
-                        ss += sq(a[k][i]);
-                        a[k][i] = make_float4(a[k][i].x * g.x, a[k][i].y * g.y, a[k][i].z * g.z, a[k][i].w * g.w);
-                    }
-        } else {
-#pragma unroll
-            for (int k = 0; k < K; ++k)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) ss += sq(a[k][i]);
+                    if (at(k, i) < left)
+                        a[k][i] = times(a[k][i], AHEAD ? slot4<B>(row + sg + (2 * k + i) * db) : load4(gate + at(k, i)));
         }
         if constexpr (AHEAD) {
-            if (t + (int64_t)p.ahead * step < p.T) fetch(t + p.ahead * step, row);
+            if (t + (int64_t)p.ahead * step < p.T) fetch(row);
             commit();
             row += stage;
-            if (row == p.ahead * stage) row = 0;
+            if (row == end) row = 0;
+        } else {
+            next_row();
         }
         float f = d.res_scale;
-        if (p.w_post) {
-            f /= sqrtf(row_sum<CTA>(ss, sm[0]) * inv_h + d.eps);
+        if (p.w_post) f *= rsqrtf(row_sum<CTA>(ss, sm[0]) * inv_h + d.eps);
+        if (weighted) {
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                    if (at(k, i) < left) {
-                        const float4 w = *reinterpret_cast<const float4*>(p.w_post + c0 + at(k, i));
-                        a[k][i] = make_float4(a[k][i].x * (w.x + d.weight_offset), a[k][i].y * (w.y + d.weight_offset),
-                                              a[k][i].z * (w.z + d.weight_offset), a[k][i].w * (w.w + d.weight_offset));
-                    }
+                    if (at(k, i) < left)
+                        a[k][i] = times(a[k][i], AHEAD ? slot4<float>(sw + (2 * k + i) * dw) : weight(p.w_post, k, i));
         }
         ss = 0.f;
 #pragma unroll
@@ -236,18 +260,19 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
                 ss += sq(r[k][i]);
                 if (p.r && at(k, i) < left) store4(ro + at(k, i), r[k][i]);
             }
+        ro += step * d.r_stride;
         if (p.h) {
-            const float inv = 1.f / sqrtf(row_sum<CTA>(ss, sm[1]) * inv_h + d.eps);
+            const float inv = rsqrtf(row_sum<CTA>(ss, sm[1]) * inv_h + d.eps);
 #pragma unroll
             for (int k = 0; k < K; ++k)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (at(k, i) < left) {
-                        const float4 w = *reinterpret_cast<const float4*>(p.w_pre + c0 + at(k, i)), v = r[k][i];
-                        store4(ho + at(k, i), make_float4(v.x * inv * (w.x + d.weight_offset), v.y * inv * (w.y + d.weight_offset),
-                                                          v.z * inv * (w.z + d.weight_offset), v.w * inv * (w.w + d.weight_offset)));
+                        const float4 w = AHEAD ? slot4<float>(sn + (2 * k + i) * dw) : weight(p.w_pre, k, i), v = r[k][i];
+                        store4(ho + at(k, i), times(make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), w));
                     }
         }
+        ho += step * d.h_stride;
         // a row with one sum only: its readers meet before the next row's sum
         if (CTA && !(p.w_post && p.h)) __syncthreads();
     }
@@ -281,18 +306,20 @@ bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) 
 }
 
 // Many rows: resident CTAs that copy ahead, 4, 2 or 1 rows, as many as leave the
-// shared memory to `ctas` per SM.
+// shared memory to `ctas` per SM with their weights.
 template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MINB>
 cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
     const auto kernel = k_block_norm<R, B, O, K, CTA, true, MAXT, MINB>;
     const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
     const size_t stage = (size_t)threads * 2 * K * 4 * (sizeof(R) + 2 * sizeof(B));
+    const size_t weights = (size_t)threads * 4 * K * 16;
     p.ahead = 4;
-    while (p.ahead > 1 && p.ahead * stage * ctas > 200 * 1024) p.ahead /= 2;
+    while (p.ahead > 1 && (p.ahead * stage + weights + 1024) * ctas > 227 * 1024) p.ahead /= 2;
+    const size_t smem = p.ahead * stage + weights;
     static int held[33];
-    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, p.ahead * stage, held[threads / 32]);
+    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held[threads / 32]);
     if (e != cudaSuccess) return e;
-    kernel<<<need < held[threads / 32] ? need : held[threads / 32], threads, p.ahead * stage, s>>>(p);
+    kernel<<<need < held[threads / 32] ? need : held[threads / 32], threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

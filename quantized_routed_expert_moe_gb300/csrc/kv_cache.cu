@@ -137,10 +137,11 @@ __device__ __forceinline__ uint32_t pack2(float2 v) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
-// e4m3 of two values / scale: a true division, so that the value stored is the
-// nearest one to the quotient; saturating, NaN stays NaN.
-__device__ __forceinline__ uint32_t quant2(float2 v, float scale) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale)), __NV_SATFINITE, __NV_E4M3);
+// e4m3 of two values / scale, by way of the rounded reciprocal: the quotient is off by
+// 2^-23, which changes the nearest of e4m3's values for about one in 10^6. Saturating,
+// NaN stays NaN.
+__device__ __forceinline__ uint32_t quant2(float2 v, float inv) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(v.x * inv, v.y * inv), __NV_SATFINITE, __NV_E4M3);
 }
 __device__ __forceinline__ void phase(uint64_t turns, int position, float& c, float& s) {
     const uint64_t ph = turns * (uint64_t)position;
@@ -178,43 +179,48 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     const bool rotated = 16 * g < s.rotary_dim;
     // the group's two vectors, where it is rotated and where not
     const int c0 = rotated && !ADJACENT ? 8 * g : 16 * g, step = rotated && !ADJACENT ? half : 8;
-    const int64_t units = (int64_t)p.a.T * p.parts;
-    const int stride = gridDim.x * 8;
+    const int stride = gridDim.x * 8, dt = stride / p.parts, dp = stride - dt * p.parts;   // to a warp's next unit
     uint4* const slots = ring + warp * (kAhead * 64) + lane;
     uint32_t bits = 0;
+    auto advance = [&](int& t, int& part) {
+        t += dt;
+        part += dp;
+        if (part >= p.parts) {
+            part -= p.parts;
+            ++t;
+        }
+    };
+    const int first = blockIdx.x * 8 + warp;
+    int t = first / p.parts, part = first - t * p.parts;
+    if (t >= p.a.T) return;
 
-    // the copies: round fr of unit fu next, into slot `put`
-    int64_t fu = (int64_t)blockIdx.x * 8 + warp;
-    int fr = (int)(fu % p.parts), put = 0;
+    // the copies: round fr of unit (ft, fp) next, into slot `put`
+    int ft = t, fp = part, fr = part, put = 0;
     auto fetch = [&] {
-        if (fu < units) {
-            const int64_t t = fu / p.parts;
-            const int head = fr * side + lane / groups;
-            if (head < heads) {
-                const bool turned = head < k_heads;
-                const __nv_bfloat16* src =
-                    head < q_heads ? static_cast<const __nv_bfloat16*>(p.a.q) + t * p.a.q_stride + head * s.head_dim
-                    : turned ? static_cast<const __nv_bfloat16*>(p.a.k) + t * p.a.k_stride + (head - q_heads) * s.head_dim
-                             : static_cast<const __nv_bfloat16*>(p.a.v) + t * p.a.v_stride + (head - k_heads) * s.head_dim;
-                const uint32_t to = (uint32_t)__cvta_generic_to_shared(slots + put * 64);
-                const int a = turned ? c0 : 16 * g, b = turned ? c0 + step : 16 * g + 8;
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src + a) : "memory");
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(src + b) : "memory");
-            }
-            if ((fr += p.parts) >= p.rounds) {
-                fu += stride;
-                fr = (int)(fu % p.parts);
-            }
+        const int head = fr * side + lane / groups;
+        if (ft < p.a.T && head < heads) {
+            const bool turned = head < k_heads;
+            const __nv_bfloat16* src =
+                head < q_heads ? static_cast<const __nv_bfloat16*>(p.a.q) + ft * p.a.q_stride + head * s.head_dim
+                : turned       ? static_cast<const __nv_bfloat16*>(p.a.k) + ft * p.a.k_stride + (head - q_heads) * s.head_dim
+                               : static_cast<const __nv_bfloat16*>(p.a.v) + ft * p.a.v_stride + (head - k_heads) * s.head_dim;
+            const uint32_t to = (uint32_t)__cvta_generic_to_shared(slots + put * 64);
+            src += turned ? c0 : 16 * g;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
+            src += turned ? step : 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(src) : "memory");
+        }
+        if ((fr += p.parts) >= p.rounds) {
+            advance(ft, fp);
+            fr = fp;
         }
         put = (put + 1) % kAhead;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    int64_t unit = fu;
-    if (unit >= units) return;
     // position and page of a unit, read one unit ahead
-    int pos = p.a.positions[unit / p.parts], seq = p.a.seq ? p.a.seq[unit / p.parts] : (int)(unit / p.parts);
-#pragma unroll
+    int pos = p.a.positions[t], seq = p.a.seq ? p.a.seq[t] : t;
+#pragma unroll 1
     for (int i = 0; i < kAhead; ++i) fetch();
     auto look_up = [&](int pos, int seq, bool& read) {
         const int64_t at = pos >= 0 ? kv_entry(s, p.a.n_seqs, p.a.max_pages, seq, pos, bits) : -1;
@@ -223,13 +229,13 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     };
     bool read;
     int page = look_up(pos, seq, read);
-    for (int take = 0; unit < units;) {
-        const int t = (int)(unit / p.parts), part = (int)(unit - (int64_t)t * p.parts);
-        const int64_t next = unit + stride;
+    for (int take = 0; t < p.a.T;) {
+        int nt = t, np = part;
+        advance(nt, np);
         int next_pos = -1, next_seq = 0;
-        if (next < units) {
-            next_pos = p.a.positions[next / p.parts];
-            next_seq = p.a.seq ? p.a.seq[next / p.parts] : (int)(next / p.parts);
+        if (nt < p.a.T) {
+            next_pos = p.a.positions[nt];
+            next_seq = p.a.seq ? p.a.seq[nt] : nt;
         }
         if (pos >= 0)
             for (int f = lane; f < half; f += 32) phase(p.turns[f], pos, sm_c[warp][f], sm_s[warp][f]);
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             if (head < heads && (is_q || page >= 0)) {
                 const int hk = head - (is_v ? k_heads : q_heads);
                 const int at0 = is_v ? 16 * g : c0, at1 = is_v ? 16 * g + 8 : c0 + step;
-                const float scale = E4M3 && !is_q ? (is_v ? p.v_scale : p.k_scale)[hk] : 1.f;
+                const float inv = E4M3 && !is_q ? 1.f / (is_v ? p.v_scale : p.k_scale)[hk] : 1.f;
                 uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
                 uint32_t e[2][2] = {};
                 // two channels of either vector at a time
@@ -269,8 +275,8 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                         }
                     }
                     if (E4M3 && !is_q) {
-                        e[0][x / 2] |= quant2(a, scale) << 16 * (x % 2);
-                        e[1][x / 2] |= quant2(b, scale) << 16 * (x % 2);
+                        e[0][x / 2] |= quant2(a, inv) << 16 * (x % 2);
+                        e[1][x / 2] |= quant2(b, inv) << 16 * (x % 2);
                     } else if (turn) {
                         w[0][x] = pack2(a);
                         w[1][x] = pack2(b);
@@ -291,9 +297,9 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             }
             fetch();
         }
-        unit = next;
+        t = nt;
+        part = np;
         pos = next_pos;
-        seq = next_seq;
         page = next_page;
         read = next_read;
         __syncwarp();   // every lane is done with the sines
