@@ -165,7 +165,7 @@ struct AppendArgs {
 // meanwhile. The lanes share the sines and cosines of a unit's angles. The kernel
 // reads and writes every value once: bound by memory for many tokens, by latency for
 // few, where a warp has one round.
-constexpr int kAhead = 8;
+constexpr int kAhead = 4;
 constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 
 template <bool ADJACENT, bool E4M3>
@@ -218,6 +218,9 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
+    uint64_t turns[4];   // of the angles lane, lane + 32, ...
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turns[i] = lane + 32 * i < half ? p.turns[lane + 32 * i] : 0;
     // position and page of a unit, read one unit ahead
     int pos = p.a.positions[t], seq = p.a.seq ? p.a.seq[t] : t;
 #pragma unroll 1
@@ -238,13 +241,14 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             next_seq = p.a.seq ? p.a.seq[nt] : nt;
         }
         if (pos >= 0)
-            for (int f = lane; f < half; f += 32) phase(p.turns[f], pos, sm_c[warp][f], sm_s[warp][f]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lane + 32 * i < half) phase(turns[i], pos, sm_c[warp][lane + 32 * i], sm_s[warp][lane + 32 * i]);
         if (read) page = kv_page(s, page, bits);
         const int64_t row = page >= 0 ? kv_offset(s, page, 0, pos % s.page_size) : 0;
         bool next_read = false;
         int next_page = -1;
         __syncwarp();
-        const float *const c = &sm_c[warp][8 * g], *const sn = &sm_s[warp][8 * g];
         for (int r = part; r < p.rounds; r += p.parts) {
             asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
             const uint4 u0 = slots[take * 64], u1 = slots[take * 64 + 32];
@@ -258,6 +262,13 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                 const float inv = E4M3 && !is_q ? 1.f / (is_v ? p.v_scale : p.k_scale)[hk] : 1.f;
                 uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
                 uint32_t e[2][2] = {};
+                float c[8], sn[8];
+                if (turn)
+#pragma unroll
+                    for (int x = 0; x < 8; x += 4) {
+                        *reinterpret_cast<float4*>(c + x) = *reinterpret_cast<const float4*>(&sm_c[warp][8 * g + x]);
+                        *reinterpret_cast<float4*>(sn + x) = *reinterpret_cast<const float4*>(&sm_s[warp][8 * g + x]);
+                    }
                 // two channels of either vector at a time
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -267,11 +278,9 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                             a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
                             b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
                         } else {
-                            const float2 cc = *reinterpret_cast<const float2*>(c + 2 * x);
-                            const float2 ss = *reinterpret_cast<const float2*>(sn + 2 * x);
                             const float2 a0 = a;
-                            a = make_float2(a.x * cc.x - b.x * ss.x, a.y * cc.y - b.y * ss.y);
-                            b = make_float2(b.x * cc.x + a0.x * ss.x, b.y * cc.y + a0.y * ss.y);
+                            a = make_float2(a.x * c[2 * x] - b.x * sn[2 * x], a.y * c[2 * x + 1] - b.y * sn[2 * x + 1]);
+                            b = make_float2(b.x * c[2 * x] + a0.x * sn[2 * x], b.y * c[2 * x + 1] + a0.y * sn[2 * x + 1]);
                         }
                     }
                     if (E4M3 && !is_q) {
@@ -463,9 +472,10 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     const int heads = (args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads, side = 32 / (K.s.head_dim / 16);
     p.rounds = (heads + side - 1) / side;
     // as few units per token as give every resident warp at least eight, so that the last
-    // ones leave little of the GPU idle; one round per unit where the tokens are few
+    // ones leave little of the GPU idle, but two rounds or more to each set of angles; one
+    // round per unit where the tokens are few
     const int64_t warps = (int64_t)K.num_sms * 3 * 8;
-    while (p.parts * 2 <= p.rounds && (int64_t)args->T * p.parts < 8 * warps) p.parts *= 2;
+    while (p.parts * 4 <= p.rounds && (int64_t)args->T * p.parts < 8 * warps) p.parts *= 2;
     if ((int64_t)args->T * p.rounds <= warps) p.parts = p.rounds;
     const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)args->T * p.parts + 7) / 8, (int64_t)K.num_sms * 3);
     append_kernel(K.s)<<<grid, 256, kAppendRing, static_cast<cudaStream_t>(stream)>>>(p);
