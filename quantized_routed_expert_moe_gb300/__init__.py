@@ -673,16 +673,19 @@ def _rows(t, name: str, shape, dtype, device: int) -> int:
     st = t.stride()
     if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
         _refuse(t, name, shape, dtype, device)
-    if len(shape) == 2:
-        rows, width = shape
-        if st[1] != 1:
-            _refuse(t, name, shape, dtype, device)
-    else:
-        rows, heads, width = shape
-        if st[2] != 1 or (st[1] != width and heads != 1):
-            _refuse(t, name, shape, dtype, device)
-        width *= heads
-    return st[0] if rows > 1 else width   # a single row has no stride of its own
+    if len(shape) == 3:
+        return _token_stride(t, name, *shape)
+    if st[1] != 1:
+        _refuse(t, name, shape, dtype, device)
+    return st[0] if shape[0] > 1 else shape[1]   # a single row has no stride of its own
+
+
+def _token_stride(t, name: str, rows: int, heads: int, width: int) -> int:
+    """Elements between the tokens of t [rows, heads, width]; heads must be contiguous."""
+    st = t.stride()
+    if st[2] != 1 or (st[1] != width and heads != 1):
+        _refuse(t, name, (rows, heads, width), t.dtype, t.get_device())
+    return st[0] if rows > 1 else heads * width
 
 
 class BlockNorm:
@@ -708,6 +711,7 @@ class BlockNorm:
         self.w_post, self.w_pre = w_post, w_pre
         self._ids = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
         self._buf = ctypes.create_string_buffer(ctypes.sizeof(moe_block_norm_desc))
+        self._buf_addr = ctypes.addressof(self._buf)
         vp, i32 = ctypes.c_void_p, ctypes.c_int32
         self._call = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 8, i32, i32, vp)(("moe_block_norm", lib()))
 
@@ -737,7 +741,7 @@ class BlockNorm:
                              0 if o is None else _rows(o, "o", shape, blk, dev), gs,
                              0 if r is None else _rows(r, "r", shape, res, dev),
                              0 if h is None else _rows(h, "h", shape, out, dev))
-        st = self._call(ctypes.addressof(self._buf), x.data_ptr(), None if o is None else o.data_ptr(),
+        st = self._call(self._buf_addr, x.data_ptr(), None if o is None else o.data_ptr(),
                         None if gate is None else gate.data_ptr(),
                         None if o is None or self.w_post is None else self.w_post.data_ptr(),
                         None if h is None or self.w_pre is None else self.w_pre.data_ptr(),
@@ -785,6 +789,7 @@ class KVCache:
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
         self._heads = (n_heads, hk, d)
         self._buf = ctypes.create_string_buffer(max(self._append_args.size, self._attend_args.size))
+        self._buf_addr = ctypes.addressof(self._buf)
         proto = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
         self._append_call = proto(("moe_kv_append", lib()))
         self._attend_call = proto(("moe_kv_attend", lib()))
@@ -812,18 +817,31 @@ class KVCache:
         [n_seqs, max_pages]."""
         hq, hk, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
-        T = k.shape[0]
-        shape, table = (T, hk, d), block_table.shape
-        if len(table) != 2:
-            raise ValueError("block_table must be [n_seqs, max_pages]")
-        self._append_args.pack_into(
-            self._buf, 0, 0 if q is None else q.data_ptr(), k.data_ptr(), v.data_ptr(),
-            0 if q is None else _rows(q, "q", (T, hq, d), bf16, dev), _rows(k, "k", shape, bf16, dev),
-            _rows(v, "v", shape, bf16, dev), _dense(positions, "positions", (T,), i32, dev),
-            0 if seq is None else _dense(seq, "seq", (T,), i32, dev),
-            _dense(block_table, "block_table", table, i32, dev), T, table[0], table[1],
-            0 if q_out is None else _dense(q_out, "q_out", (T, hq, d), bf16, dev))
-        st = self._append_call(self.handle, ctypes.addressof(self._buf), _stream(stream))
+        shape, table = k.shape, block_table.shape
+        T = shape[0]
+        # one condition for what almost every call passes; the refusals are worked out after it
+        if not (shape == (T, hk, d) and v.shape == shape and positions.shape == (T,) and len(table) == 2
+                and k.dtype is bf16 and v.dtype is bf16 and positions.dtype is i32 and block_table.dtype is i32
+                and k.get_device() == dev and v.get_device() == dev and positions.get_device() == dev
+                and block_table.get_device() == dev and positions.is_contiguous() and block_table.is_contiguous()):
+            _rows(k, "k", (T, hk, d), bf16, dev)
+            _rows(v, "v", (T, hk, d), bf16, dev)
+            _dense(positions, "positions", (T,), i32, dev)
+            if len(table) != 2:
+                raise ValueError("block_table must be [n_seqs, max_pages]")
+            _dense(block_table, "block_table", table, i32, dev)
+        ks, vs = _token_stride(k, "k", T, hk, d), _token_stride(v, "v", T, hk, d)
+        qs = qp = op = sp = 0
+        if q is not None:
+            qs, qp = _rows(q, "q", (T, hq, d), bf16, dev), q.data_ptr()
+        if q_out is not None:
+            op = _dense(q_out, "q_out", (T, hq, d), bf16, dev)
+        if seq is not None:
+            sp = _dense(seq, "seq", (T,), i32, dev)
+        self._append_args.pack_into(self._buf, 0, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, positions.data_ptr(), sp,
+                                    block_table.data_ptr(), T, table[0], table[1], op)
+        st = self._append_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
+                               else _stream(stream))
         if st:
             _check(st, "moe_kv_append")
 
@@ -834,16 +852,25 @@ class KVCache:
         [B, n_heads] or None; scale defaults to 1 / sqrt(d)."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
-        B, table = q.shape[0], block_table.shape
-        shape = (B, hq, d)
-        if len(table) != 2:
-            raise ValueError("block_table must be [B, max_pages]")
+        shape, table = q.shape, block_table.shape
+        B = shape[0]
+        if not (shape == (B, hq, d) and out.shape == shape and lens.shape == (B,) and len(table) == 2 and table[0] == B
+                and q.dtype is bf16 and out.dtype is bf16 and lens.dtype is i32 and block_table.dtype is i32
+                and q.get_device() == dev and out.get_device() == dev and lens.get_device() == dev
+                and block_table.get_device() == dev and out.is_contiguous() and lens.is_contiguous()
+                and block_table.is_contiguous()):
+            _rows(q, "q", (B, hq, d), bf16, dev)
+            _dense(out, "out", (B, hq, d), bf16, dev)
+            _dense(lens, "lens", (B,), i32, dev)
+            if len(table) != 2:
+                raise ValueError("block_table must be [B, max_pages]")
+            _dense(block_table, "block_table", (B, table[1]), i32, dev)
         self._attend_args.pack_into(
-            self._buf, 0, q.data_ptr(), _rows(q, "q", shape, bf16, dev),
-            _dense(block_table, "block_table", (B, table[1]), i32, dev), _dense(lens, "lens", (B,), i32, dev), B,
-            table[1], d ** -0.5 if scale is None else scale, softcap, window, _dense(out, "out", shape, bf16, dev),
+            self._buf, 0, q.data_ptr(), _token_stride(q, "q", B, hq, d), block_table.data_ptr(), lens.data_ptr(), B,
+            table[1], d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
             0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
-        st = self._attend_call(self.handle, ctypes.addressof(self._buf), _stream(stream))
+        st = self._attend_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
+                               else _stream(stream))
         if st:
             _check(st, "moe_kv_attend")
 
