@@ -7,7 +7,7 @@
 // Split. The attended tokens of every (sequence, head tile), a segment, are cut
 // into chunks of 8 KB of keys and 8 KB of values. All chunks of the call, numbered
 // segment by segment, are dealt out evenly and contiguously to one resident CTA
-// per SM and within it to eight warps, from the lengths as they stand on the device:
+// per SM and within it to its warps, from the lengths as they stand on the device:
 // a ragged batch, one long sequence and thousands of short ones are balanced
 // alike, in one launch. A warp that holds a whole segment writes its output; parts
 // of a segment that is cut between warps are joined by their CTA at its end, and
@@ -42,10 +42,9 @@ namespace moe {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
 constexpr int kRing = 16 * 1024;   // bytes of stages per warp
 constexpr int kMaxCtas = 160;
+constexpr int kMinChunks = 8;      // of a CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
@@ -65,11 +64,16 @@ struct Cfg {
     static constexpr int STEPS = RB / 32;                     // and of a row
     static constexpr int FRAGS = NT * DT;                     // output fragments of a segment, 32 lanes x float4
     static constexpr int PART = FRAGS * 512;                  // their bytes
-    static constexpr size_t smem = 1024 + (size_t)kWarps * (kRing + PART);
+    static constexpr int WARPS = FRAGS == 32 ? 6 : 8;         // 6 where the parts of 8 leave no room for their rings
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr size_t smem = 1024 + (size_t)WARPS * (kRing + PART);
 };
 
 // Every warp comes here once, from the end of its chunks or without any.
-__device__ __forceinline__ void warps_meet() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void warps_meet() {
+    asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory");
+}
 
 struct AttendArgs {
     moe_kv_attend_args a;
@@ -198,9 +202,9 @@ __device__ __forceinline__ void finish(const AttendArgs& p, int b, int h0, int h
 }
 
 template <class C>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(C::THREADS, 1)
     k_kv_attend(const AttendArgs p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
-    constexpr int NT = C::NT, CT = C::CT, D = C::D;
+    constexpr int NT = C::NT, CT = C::CT, D = C::D, kWarps = C::WARPS, kThreads = C::THREADS;
     extern __shared__ uint8_t smem_raw[];
     __shared__ int sm_pre[1025];                // chunks before sequence b
     __shared__ int sm_len[1024];
@@ -209,7 +213,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ uint32_t sm_rows[kWarps][C::STAGES];  // which groups of 16 rows a stage holds
     __shared__ __align__(16) float2 sm_ml[kWarps][C::HEADS];   // maximum and sum of the parts below
     __shared__ Place sm_cut[2];                      // segments that go on before and after the CTA
-    __shared__ int sm_on[2], sm_c0[2], sm_n[2];      // whether there are; their CTAs
+    __shared__ int sm_on[2], sm_c0[2];               // how many CTAs they have; the first
+    __shared__ float2 sm_sum[C::HEADS];
     __shared__ int sm_last[2], sm_abort;
 
     const KvShape& s = p.s;
@@ -261,10 +266,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) sm_pre[0] = 0;
         __syncthreads();
     }
-    // Chunks of this CTA, and of its warps. No more CTAs than chunks: each of them
-    // has at least one, so a segment's CTAs are consecutive.
+    // Chunks of this CTA, and of its warps. Few chunks go to few CTAs, one or more per
+    // warp: a segment has less to join. (Each CTA has some: a segment's are consecutive.)
     const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
-    const int ctas = min((int)gridDim.x, total), me = blockIdx.x;
+    const int ctas = min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks), me = blockIdx.x;
     const int share = ctas ? total / ctas : 0, rest = total - share * ctas;
     auto cta_beg = [&](int c) { return c * share + min(c, rest); };
     auto cta_of = [&](int u) { return u < rest * (share + 1) ? u / (share + 1) : rest + (u - rest * (share + 1)) / share; };
@@ -644,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]);
                 }
             }
-            if (last) warps_meet();
+            if (last) warps_meet<C::THREADS>();
             if (!theirs) {
                 for (int x = warp + 1; last && x < kWarps && warp_beg(x) < at.end; ++x) {
                     if (warp_beg(x) == warp_beg(x + 1)) continue;
@@ -673,15 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int side = at.beg < u0 ? 0 : at.end > u1 ? 1 : -1;
-                if (side < 0) {
-                    const float vs = p.v_scale[at.hk];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                        for (int dt = 0; dt < C::DT; ++dt)
-                            finish<C>(p, at.b, h0, heads, nt, dt, vs, o[dt][nt], m[nt], l[nt]);
-                    }
-                } else {
+                bool done = side < 0;
+                if (side >= 0) {
                     float4* dst = p.part_o + (me * 2 + side) * (C::FRAGS * 32) + lane;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
@@ -693,30 +691,84 @@ __global__ void __launch_bounds__(kThreads, 1)
                             __stcg(&p.part_ml[(me * 2 + side) * 8 + nt * 4 + j],
                                    make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]));
                     }
-                    if (lane == 0) {
-                        sm_cut[side] = at;
-                        sm_on[side] = 1;
+                    const int c0 = cta_of(at.beg), n = cta_of(at.end - 1) - c0 + 1;
+                    if (n > 2) {   // joined by a whole CTA, below
+                        if (lane == 0) {
+                            sm_cut[side] = at;
+                            sm_on[side] = n;
+                            sm_c0[side] = c0;
+                        }
+                    } else {       // of two CTAs: the warp that comes second adds the other's part
+                        __threadfence();
+                        __syncwarp();
+                        int before = 0;
+                        if (lane == 0) {
+                            int* arrived = p.arrived + (at.b * s.n_kv_heads + at.hk) * tiles + at.tile;
+                            before = atomicAdd(arrived, 1);
+                            if (before == 1) *arrived = 0;   // for the next call
+                        }
+                        done = __shfl_sync(~0u, before, 0) == 1;
+                        if (done) {
+                            __threadfence();
+                            // the earlier CTA's part is its second, the later one's its first; e0 is the
+                            // earlier one's factor, whichever this is
+                            const int slot = side ? (me + 1) * 2 : (me - 1) * 2 + 1;
+                            const float4* src = p.part_o + slot * (C::FRAGS * 32) + lane;
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                float4 v[C::DT];
+                                const float4 ml = __ldcg(&p.part_ml[slot * 8 + nt * 4 + j]);
+#pragma unroll
+                                for (int dt = 0; dt < C::DT; ++dt) v[dt] = __ldcg(src + (nt * C::DT + dt) * 32);
+                                const float mx[2] = {ml.x, ml.z}, lx[2] = {ml.y, ml.w};
+                                float f[2], e[2];
+#pragma unroll
+                                for (int c = 0; c < 2; ++c) {
+                                    const float top = fmaxf(m[nt][c], mx[c]), base = top == -INFINITY ? 0.f : top;
+                                    f[c] = ex2(m[nt][c] - base);
+                                    e[c] = ex2(mx[c] - base);
+                                    m[nt][c] = top;
+                                    l[nt][c] = side ? fmaf(lx[c], e[c], l[nt][c] * f[c]) : fmaf(l[nt][c], f[c], lx[c] * e[c]);
+                                }
+#pragma unroll
+                                for (int dt = 0; dt < C::DT; ++dt) {
+                                    const float w[4] = {v[dt].x, v[dt].y, v[dt].z, v[dt].w};
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float a = o[dt][nt][i], fa = f[i & 1], eb = e[i & 1];
+                                        o[dt][nt][i] = side ? fmaf(w[i], eb, a * fa) : fmaf(a, fa, w[i] * eb);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+                if (done) {
+                    const float vs = p.v_scale[at.hk];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                        for (int dt = 0; dt < C::DT; ++dt)
+                            finish<C>(p, at.b, h0, heads, nt, dt, vs, o[dt][nt], m[nt], l[nt]);
                     }
                 }
             }
             if (last) break;
         }
     } else {
-        warps_meet();
+        warps_meet<C::THREADS>();
     }
 
-    // ---- segments cut between CTAs -------------------------------------------------------
+    // ---- segments cut between many CTAs ---------------------------------------------------
     __threadfence();
     __syncthreads();
     if (sm_on[0] || sm_on[1]) {
         if (threadIdx.x < 2) {
             sm_last[threadIdx.x] = 0;
-            if (sm_on[threadIdx.x]) {
+            const int n = sm_on[threadIdx.x];
+            if (n) {
                 const Place q = sm_cut[threadIdx.x];
                 int* arrived = p.arrived + (q.b * s.n_kv_heads + q.hk) * tiles + q.tile;
-                const int c0 = cta_of(q.beg), n = cta_of(q.end - 1) - c0 + 1;
-                sm_c0[threadIdx.x] = c0;
-                sm_n[threadIdx.x] = n;
                 if (atomicAdd(arrived, 1) == n - 1) {
                     sm_last[threadIdx.x] = 1;
                     *arrived = 0;   // for the next call
@@ -728,55 +780,64 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int side = 0; side < 2; ++side) {
             if (!sm_last[side]) continue;
             const Place q = sm_cut[side];
-            const int c0 = sm_c0[side], n = sm_n[side];
+            const int c0 = sm_c0[side], n = sm_on[side], heads = heads_of(q);
             const float vs = p.v_scale[q.hk];
-            // parts of all CTAs in order, BATCH of them in flight; the first CTA's part is its
-            // second (its segment begins there), the others' their first
-            constexpr int BATCH = 8, STEP = 2 * C::FRAGS * 32;
+            // a warp per fragment; the first parts are on their way while the warps, a head
+            // each, work out the parts' factors
+            constexpr int BATCH = 16, STEP = 2 * C::FRAGS * 32;
+            float4 v[BATCH];
+            auto fetch = [&](int f, int i0) {
+                const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i)
+                    if (i0 + i < n) v[i] = __ldcg(src + i * STEP + (i0 + i == 0 ? STEP / 2 : 0));
+            };
+            if (warp < C::FRAGS) fetch(warp, 0);
+            float* fac = reinterpret_cast<float*>(smem_raw);   // [n][HEADS]: the rings are idle
+            for (int h = warp; h < C::HEADS; h += kWarps) {
+                float2 ml[kMaxCtas / 32];
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int i = 0; i < kMaxCtas / 32; ++i) {
+                    const int at = lane + 32 * i;
+                    ml[i] = make_float2(-INFINITY, 0.f);
+                    if (at < n)
+                        ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + ((c0 + at) * 2 + (at == 0)) * 16 + h);
+                    M = fmaxf(M, ml[i].x);
+                }
+                for (int x = 16; x; x >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, x));
+                const float mb = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int i = 0; i < kMaxCtas / 32; ++i) {
+                    const float e = ex2(ml[i].x - mb);
+                    if (lane + 32 * i < n) fac[(lane + 32 * i) * C::HEADS + h] = e;
+                    L += e * ml[i].y;
+                }
+                for (int x = 16; x; x >>= 1) L += __shfl_xor_sync(~0u, L, x);
+                if (lane == 0) sm_sum[h] = make_float2(M, L);
+            }
+            __syncthreads();
 #pragma unroll 1
             for (int f = warp; f < C::FRAGS; f += kWarps) {
-                const int nt = f / C::DT;
-                float M[2] = {-INFINITY, -INFINITY}, L[2] = {0.f, 0.f}, a[4] = {0.f, 0.f, 0.f, 0.f};
+                const int h = f / C::DT * 8 + 2 * j;
+                float a[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
                 for (int i0 = 0; i0 < n; i0 += BATCH) {
-                    const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
-                    const float4* sml = p.part_ml + (c0 + i0) * 16 + nt * 4 + j;
-                    float4 v[BATCH], ml[BATCH];
+                    if (f != warp || i0) fetch(f, i0);
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const int second = i0 + i == 0;
-                        ml[i] = i0 + i < n ? __ldcg(sml + i * 16 + second * 8) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
-                        v[i] = i0 + i < n ? __ldcg(src + i * STEP + second * (STEP / 2)) : make_float4(0.f, 0.f, 0.f, 0.f);
-                    }
-                    float m0 = M[0], m1 = M[1];
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        m0 = fmaxf(m0, ml[i].x);
-                        m1 = fmaxf(m1, ml[i].z);
-                    }
-                    const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-                    const float f0 = ex2(M[0] - b0), f1 = ex2(M[1] - b1);
-                    M[0] = m0;
-                    M[1] = m1;
-                    L[0] *= f0;
-                    L[1] *= f1;
-                    a[0] *= f0;
-                    a[1] *= f1;
-                    a[2] *= f0;
-                    a[3] *= f1;
-#pragma unroll
-                    for (int i = 0; i < BATCH; ++i) {
-                        const float e0 = ex2(ml[i].x - b0), e1 = ex2(ml[i].z - b1);
-                        L[0] += e0 * ml[i].y;
-                        L[1] += e1 * ml[i].w;
-                        a[0] += e0 * v[i].x;
-                        a[1] += e1 * v[i].y;
-                        a[2] += e0 * v[i].z;
-                        a[3] += e1 * v[i].w;
-                    }
+                    for (int i = 0; i < BATCH; ++i)
+                        if (i0 + i < n) {
+                            const float2 e = *reinterpret_cast<const float2*>(fac + (i0 + i) * C::HEADS + h);
+                            a[0] += e.x * v[i].x;
+                            a[1] += e.y * v[i].y;
+                            a[2] += e.x * v[i].z;
+                            a[3] += e.y * v[i].w;
+                        }
                 }
-                finish<C>(p, q.b, head_of(q), heads_of(q), nt, f % C::DT, vs, a, M, L);
+                const float M[2] = {sm_sum[h].x, sm_sum[h + 1].x}, L[2] = {sm_sum[h].y, sm_sum[h + 1].y};
+                finish<C>(p, q.b, head_of(q), heads, f / C::DT, f % C::DT, vs, a, M, L);
             }
+            __syncthreads();   // fac and sm_sum are free again
         }
     }
     if (bits) atomicOr(p.health, bits);
@@ -784,24 +845,23 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <class C>
 cudaError_t launch(const Kv& K, const AttendArgs& p, cudaStream_t stream) {
-    k_kv_attend<C><<<std::min(K.num_sms, kMaxCtas), kThreads, C::smem, stream>>>(p, K.tm_k, K.tm_v);
+    k_kv_attend<C><<<std::min(K.num_sms, kMaxCtas), C::THREADS, C::smem, stream>>>(p, K.tm_k, K.tm_v);
     return cudaGetLastError();
 }
 
-// The kernel of a cache: more than 8 heads per key-value head share one pass
-// over it as 16 columns; 16 columns of 256 channels would not fit the registers,
-// so those take a pass per 8 heads.
+// The kernel of a cache: more than 8 heads per key-value head share one pass over it
+// as 16 columns, more than 16 take further passes.
 template <class F>
 auto pick(const KvShape& s, F f) {
     const bool two = s.n_heads / s.n_kv_heads > 8;
     if (s.e4m3) {
         if (s.head_dim == 64) return two ? f(Cfg<64, true, 2>{}) : f(Cfg<64, true, 1>{});
         if (s.head_dim == 128) return two ? f(Cfg<128, true, 2>{}) : f(Cfg<128, true, 1>{});
-        return f(Cfg<256, true, 1>{});
+        return two ? f(Cfg<256, true, 2>{}) : f(Cfg<256, true, 1>{});
     }
     if (s.head_dim == 64) return two ? f(Cfg<64, false, 2>{}) : f(Cfg<64, false, 1>{});
     if (s.head_dim == 128) return two ? f(Cfg<128, false, 2>{}) : f(Cfg<128, false, 1>{});
-    return f(Cfg<256, false, 1>{});
+    return two ? f(Cfg<256, false, 2>{}) : f(Cfg<256, false, 1>{});
 }
 
 }  // namespace
