@@ -33,6 +33,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "kv_cache.h"
 #include "moe_internal.h"
@@ -121,10 +122,15 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// two e4m3 values (a low, b high byte) as an fp16 pair, exact
-__device__ __forceinline__ uint32_t e4m3_pair(uint32_t v16) {
+// two e4m3 values, the lower or upper two bytes of v, as an fp16 pair, exact
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t v) {
     uint32_t d;
-    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(d) : "r"(v16));
+    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(d) : "r"(v));
+    return d;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t v) {
+    uint32_t d;
+    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(d) : "r"(v));
     return d;
 }
 template <bool FP8>
@@ -508,8 +514,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         } else {
 #pragma unroll
                             for (int k2 = 0; k2 < 2; ++k2) {
-                                const uint32_t a[4] = {e4m3_pair(r[2 * k2]), e4m3_pair(r[2 * k2 + 1]),
-                                                       e4m3_pair(r[2 * k2] >> 16), e4m3_pair(r[2 * k2 + 1] >> 16)};
+                                const uint32_t a[4] = {e4m3_lo(r[2 * k2]), e4m3_lo(r[2 * k2 + 1]), e4m3_hi(r[2 * k2]),
+                                                       e4m3_hi(r[2 * k2 + 1])};
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt)
                                     mma<true>(sc[mt][nt], a, qf[2 * st + k2][nt][0], qf[2 * st + k2][nt][1]);
@@ -588,38 +594,42 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
                 // values: tokens that are not attended may hold anything, so their bits are cleared
                 const uint32_t vt = next_stage();
+                auto values = [&](auto masked) {
 #pragma unroll
-                for (int mt = 0; mt < C::MT; ++mt) {
-                    uint32_t keep[2] = {~0u, ~0u};
-                    if (!whole)
+                    for (int mt = 0; mt < C::MT; ++mt) {
+                        uint32_t keep[2] = {~0u, ~0u};
+                        if constexpr (masked)
 #pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            keep[i] = (seen(mt * 16 + 8 * i + 2 * j) ? 0xffffu : 0u) |
-                                      (seen(mt * 16 + 8 * i + 2 * j + 1) ? 0xffff0000u : 0u);
+                            for (int i = 0; i < 2; ++i)
+                                keep[i] = (seen(mt * 16 + 8 * i + 2 * j) ? 0xffffu : 0u) |
+                                          (seen(mt * 16 + 8 * i + 2 * j + 1) ? 0xffff0000u : 0u);
 #pragma unroll
-                    for (int st = 0; st < C::STEPS; ++st) {
-                        uint32_t r[4];
-                        ldm4t(r, vt + va[st % C::UNITS] + (st / C::UNITS) * (CT * C::LINE) + mt * 16 * C::LINE);
-                        if constexpr (!C::FP8) {
+                        for (int st = 0; st < C::STEPS; ++st) {
+                            uint32_t r[4];
+                            ldm4t(r, vt + va[st % C::UNITS] + (st / C::UNITS) * (CT * C::LINE) + mt * 16 * C::LINE);
+                            if constexpr (!C::FP8) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) r[i] &= keep[i >> 1];
+                                for (int i = 0; i < 4; ++i) r[i] &= keep[i >> 1];
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma<false>(o[st][nt], r, pf[mt][nt][0], pf[mt][nt][1]);
-                        } else {
+                                for (int nt = 0; nt < NT; ++nt) mma<false>(o[st][nt], r, pf[mt][nt][0], pf[mt][nt][1]);
+                            } else {
 #pragma unroll
-                            for (int d2 = 0; d2 < 2; ++d2) {
-                                // bytes: channels 2g, 2g + 1 of token 2j, then of token 2j + 1
-                                const uint32_t x = __byte_perm(r[2 * d2], 0, 0x3120);
-                                const uint32_t y = __byte_perm(r[2 * d2 + 1], 0, 0x3120);
-                                const uint32_t a[4] = {e4m3_pair(x) & keep[0], e4m3_pair(x >> 16) & keep[0],
-                                                       e4m3_pair(y) & keep[1], e4m3_pair(y >> 16) & keep[1]};
+                                for (int d2 = 0; d2 < 2; ++d2) {
+                                    // bytes: channels 2g, 2g + 1 of token 2j, then of token 2j + 1
+                                    const uint32_t x = __byte_perm(r[2 * d2], 0, 0x3120);
+                                    const uint32_t y = __byte_perm(r[2 * d2 + 1], 0, 0x3120);
+                                    const uint32_t a[4] = {e4m3_lo(x) & keep[0], e4m3_hi(x) & keep[0], e4m3_lo(y) & keep[1],
+                                                           e4m3_hi(y) & keep[1]};
 #pragma unroll
-                                for (int nt = 0; nt < NT; ++nt)
-                                    mma<true>(o[2 * st + d2][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+                                    for (int nt = 0; nt < NT; ++nt)
+                                        mma<true>(o[2 * st + d2][nt], a, pf[mt][nt][0], pf[mt][nt][1]);
+                                }
                             }
                         }
                     }
-                }
+                };
+                if (whole) values(std::false_type{});
+                else values(std::true_type{});
                 release();
             }
 
@@ -782,18 +792,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const Place q = sm_cut[side];
             const int c0 = sm_c0[side], n = sm_on[side], heads = heads_of(q);
             const float vs = p.v_scale[q.hk];
-            // a warp per fragment; the first parts are on their way while the warps, a head
+            // a warp per GO fragments; the first parts are on their way while the warps, a head
             // each, work out the parts' factors
-            constexpr int BATCH = 16, STEP = 2 * C::FRAGS * 32;
-            float4 v[BATCH];
-            auto fetch = [&](int f, int i0) {
-                const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
+            constexpr int GO = C::FRAGS > kWarps ? 2 : 1, BATCH = 16 / GO, STEP = 2 * C::FRAGS * 32;
+            float4 v[GO][BATCH];
+            auto fetch = [&](int f0, int i0) {
 #pragma unroll
-                for (int i = 0; i < BATCH; ++i)
-                    if (i0 + i < n) v[i] = __ldcg(src + i * STEP + (i0 + i == 0 ? STEP / 2 : 0));
+                for (int k = 0; k < GO; ++k) {
+                    const int f = f0 + k * kWarps;
+                    const float4* src = p.part_o + (c0 + i0) * STEP + f * 32 + lane;
+#pragma unroll
+                    for (int i = 0; i < BATCH; ++i)
+                        if (f < C::FRAGS && i0 + i < n) v[k][i] = __ldcg(src + i * STEP + (i0 + i == 0 ? STEP / 2 : 0));
+                }
             };
-            if (warp < C::FRAGS) fetch(warp, 0);
+            fetch(warp, 0);
             float* fac = reinterpret_cast<float*>(smem_raw);   // [n][HEADS]: the rings are idle
+#pragma unroll
             for (int h = warp; h < C::HEADS; h += kWarps) {
                 float2 ml[kMaxCtas / 32];
                 float M = -INFINITY, L = 0.f;
@@ -818,24 +833,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             __syncthreads();
 #pragma unroll 1
-            for (int f = warp; f < C::FRAGS; f += kWarps) {
-                const int h = f / C::DT * 8 + 2 * j;
-                float a[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int f0 = warp; f0 < C::FRAGS; f0 += GO * kWarps) {
+                float a[GO][4] = {};
 #pragma unroll 1
                 for (int i0 = 0; i0 < n; i0 += BATCH) {
-                    if (f != warp || i0) fetch(f, i0);
+                    if (f0 != warp || i0) fetch(f0, i0);
 #pragma unroll
-                    for (int i = 0; i < BATCH; ++i)
-                        if (i0 + i < n) {
-                            const float2 e = *reinterpret_cast<const float2*>(fac + (i0 + i) * C::HEADS + h);
-                            a[0] += e.x * v[i].x;
-                            a[1] += e.y * v[i].y;
-                            a[2] += e.x * v[i].z;
-                            a[3] += e.y * v[i].w;
-                        }
+                    for (int k = 0; k < GO; ++k) {
+                        const float* e = fac + i0 * C::HEADS + (f0 + k * kWarps) % C::FRAGS / C::DT * 8 + 2 * j;
+#pragma unroll
+                        for (int i = 0; i < BATCH; ++i)
+                            if (i0 + i < n) {
+                                const float2 x = *reinterpret_cast<const float2*>(e + i * C::HEADS);
+                                a[k][0] += x.x * v[k][i].x;
+                                a[k][1] += x.y * v[k][i].y;
+                                a[k][2] += x.x * v[k][i].z;
+                                a[k][3] += x.y * v[k][i].w;
+                            }
+                    }
                 }
-                const float M[2] = {sm_sum[h].x, sm_sum[h + 1].x}, L[2] = {sm_sum[h].y, sm_sum[h + 1].y};
-                finish<C>(p, q.b, head_of(q), heads, f / C::DT, f % C::DT, vs, a, M, L);
+#pragma unroll
+                for (int k = 0; k < GO; ++k) {
+                    const int f = f0 + k * kWarps, h = f / C::DT * 8 + 2 * j;
+                    if (f >= C::FRAGS) break;
+                    const float M[2] = {sm_sum[h].x, sm_sum[h + 1].x}, L[2] = {sm_sum[h].y, sm_sum[h + 1].y};
+                    finish<C>(p, q.b, head_of(q), heads, f / C::DT, f % C::DT, vs, a[k], M, L);
+                }
             }
             __syncthreads();   // fac and sm_sum are free again
         }
