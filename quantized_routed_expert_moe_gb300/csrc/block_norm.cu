@@ -5,6 +5,7 @@
 #include <cmath>
 #include <string>
 
+#include "common.cuh"
 #include "moe_internal.h"
 
 namespace moe {
@@ -154,6 +155,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     const bool gate_rows = p.gate && d.gate_stride != 0, gate_row = p.gate && d.gate_stride == 0;
     const bool weighted = p.w_post || (AHEAD && gate_row);
     const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
+    pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
+    pdl_trigger();
     if (t0 >= p.T) return;   // a whole CTA, or a warp that meets no other
     const R* x = static_cast<const R*>(p.x) + t0 * d.x_stride + c0;
     const B* o = static_cast<const B*>(p.o) + t0 * d.o_stride + c0;
@@ -300,8 +303,7 @@ bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) 
     e = resident(reinterpret_cast<const void*>(kernel), threads, 0, held[threads / 32]);
     if (e != cudaSuccess) return true;
     if (need > held[threads / 32]) return false;
-    kernel<<<need, threads, 0, s>>>(p);
-    e = cudaGetLastError();
+    e = launch_pdl(kernel, dim3(need), dim3(threads), 0, s, true, p);
     return true;
 }
 
@@ -319,8 +321,7 @@ cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
     static int held[33];
     const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held[threads / 32]);
     if (e != cudaSuccess) return e;
-    kernel<<<need < held[threads / 32] ? need : held[threads / 32], threads, smem, s>>>(p);
-    return cudaGetLastError();
+    return launch_pdl(kernel, dim3(need < held[threads / 32] ? need : held[threads / 32]), dim3(threads), smem, s, true, p);
 }
 
 // By the row's tiles of 256 channels. Up to 4: a warp per row. Up to 32: a warp per

@@ -35,6 +35,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "common.cuh"
 #include "kv_cache.h"
 #include "moe_internal.h"
 #include "sm100.cuh"
@@ -232,6 +233,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     if (lane < C::STAGES) bw::mbar_init(bw::saddr(&sm_bar[warp][lane]), 1);
     if (threadIdx.x == 0) sm_abort = sm_on[0] = sm_on[1] = 0;
     bw::mbar_fence_init();
+    if (threadIdx.x == 0) {
+        bw::tma_prefetch_desc(&tm_k);
+        bw::tma_prefetch_desc(&tm_v);
+    }
+    pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
+    pdl_trigger();
 
     // ---- chunks of every sequence, summed ------------------------------------------
     const int G = s.n_heads / s.n_kv_heads;
@@ -868,8 +875,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
 template <class C>
 cudaError_t launch(const Kv& K, const AttendArgs& p, cudaStream_t stream) {
-    k_kv_attend<C><<<std::min(K.num_sms, kMaxCtas), C::THREADS, C::smem, stream>>>(p, K.tm_k, K.tm_v);
-    return cudaGetLastError();
+    return launch_pdl(k_kv_attend<C>, dim3(std::min(K.num_sms, kMaxCtas)), dim3(C::THREADS), C::smem, stream, true, p,
+                      K.tm_k, K.tm_v);
 }
 
 // The kernel of a cache: more than 8 heads per key-value head share one pass over it

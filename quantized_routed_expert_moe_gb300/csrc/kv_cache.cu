@@ -9,6 +9,7 @@
 #include <string>
 #include <vector>
 
+#include "common.cuh"
 #include "kv_cache.h"
 #include "moe_internal.h"
 
@@ -190,6 +191,11 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             ++t;
         }
     };
+    uint64_t turns[4];   // of the angles lane, lane + 32, ...
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turns[i] = lane + 32 * i < half ? p.turns[lane + 32 * i] : 0;
+    pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
+    pdl_trigger();
     const int first = blockIdx.x * 8 + warp;
     int t = first / p.parts, part = first - t * p.parts;
     if (t >= p.a.T) return;
@@ -218,9 +224,6 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    uint64_t turns[4];   // of the angles lane, lane + 32, ...
-#pragma unroll
-    for (int i = 0; i < 4; ++i) turns[i] = lane + 32 * i < half ? p.turns[lane + 32 * i] : 0;
     // position and page of a unit, read one unit ahead
     int pos = p.a.positions[t], seq = p.a.seq ? p.a.seq[t] : t;
 #pragma unroll 1
@@ -478,8 +481,8 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     while (p.parts * 4 <= p.rounds && (int64_t)args->T * p.parts < 8 * warps) p.parts *= 2;
     if ((int64_t)args->T * p.rounds <= warps) p.parts = p.rounds;
     const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)args->T * p.parts + 7) / 8, (int64_t)K.num_sms * 3);
-    append_kernel(K.s)<<<grid, 256, kAppendRing, static_cast<cudaStream_t>(stream)>>>(p);
-    const cudaError_t e = cudaGetLastError();
+    const cudaError_t e =
+        launch_pdl(append_kernel(K.s), dim3(grid), dim3(256), kAppendRing, static_cast<cudaStream_t>(stream), true, p);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "append launch");
 }
 
