@@ -649,7 +649,8 @@ moe_status moe_kv_locate(const moe_kv_desc* desc, const int32_t* block_table, in
                          int32_t seq, int32_t position, int32_t head, int64_t* offset, uint32_t* bits);
 
 /* Wait for the handle's device work, then report what its kernels refused
- * since the last call: MOE_E_STATE with the bits below, MOE_OK otherwise. */
+ * since the last call: MOE_E_STATE with the bits below (MOE_E_TIMEOUT where
+ * MOE_KV_TIMEOUT is among them), MOE_OK otherwise. */
 enum {
     MOE_KV_BAD_SEQ = 1,     /* append: a sequence index outside block_table */
     MOE_KV_BAD_LENGTH = 2,  /* a position or length past max_pages * page_size */

@@ -7,7 +7,6 @@
 #include <cmath>
 #include <new>
 #include <string>
-#include <vector>
 
 #include "common.cuh"
 #include "kv_cache.h"
@@ -426,21 +425,21 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
 
     // inv_freq / 2 pi in double keeps 2^-53 of a turn per position; its fraction
     // times 2^64 is rounded to an integer
-    std::vector<uint64_t> turns(std::max(half, 1), 0);
+    uint64_t turns[128] = {};   // rotary_dim <= 256
     for (int i = 0; i < half; ++i) {
         const double t = inv_freq[i] / 6.283185307179586476925287;
         const double f = t - std::floor(t);
         turns[i] = f >= 1.0 ? 0 : (uint64_t)std::ldexp(f, 64);
     }
-    std::vector<float> ks(Hk, 1.0f), vs(Hk, 1.0f);
-    if (e4m3) {
-        ks.assign(k_scale, k_scale + Hk);
-        vs.assign(v_scale, v_scale + Hk);
+    float ks[256], vs[256];     // n_kv_heads <= 256
+    for (int h = 0; h < Hk; ++h) {
+        ks[h] = e4m3 ? k_scale[h] : 1.0f;
+        vs[h] = e4m3 ? v_scale[h] : 1.0f;
     }
     e = cudaMemset(K.block, 0, need);
-    if (e == cudaSuccess) e = cudaMemcpy(K.turns, turns.data(), turns.size() * 8, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(K.k_scale, ks.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
-    if (e == cudaSuccess) e = cudaMemcpy(K.v_scale, vs.data(), (size_t)Hk * 4, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(K.turns, turns, (size_t)half * 8, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(K.k_scale, ks, (size_t)Hk * 4, cudaMemcpyHostToDevice);
+    if (e == cudaSuccess) e = cudaMemcpy(K.v_scale, vs, (size_t)Hk * 4, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = kv_attend_setup(K);
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(append_kernel(K.s), cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendRing);
@@ -507,6 +506,7 @@ moe_status moe_kv_health(moe_kv* kv, uint32_t* bits) {
     if (bits) *bits = v;
     if (!v) return MOE_OK;
     MOE_CUDA_TRY(cudaMemset(kv->K.health, 0, 4));
+    if (v & MOE_KV_TIMEOUT) return fail(MOE_E_TIMEOUT, "a bounded device-side wait gave up (health bits " + std::to_string(v) + ")");
     return fail(MOE_E_STATE, "kernels refused part of their work (health bits " + std::to_string(v) + ")");
 }
 
