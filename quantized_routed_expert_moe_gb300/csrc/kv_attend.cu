@@ -219,10 +219,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __shared__ __align__(8) uint64_t sm_bar[kWarps][C::STAGES];
     __shared__ uint32_t sm_rows[kWarps][C::STAGES];  // which groups of 16 rows a stage holds
     __shared__ __align__(16) float2 sm_ml[kWarps][C::HEADS];   // maximum and sum of the parts below
-    __shared__ Place sm_cut[2];                      // segments that go on before and after the CTA
-    __shared__ int sm_on[2], sm_c0[2];               // how many CTAs they have; the first
+    __shared__ Place sm_cut[2];                      // segments from before and into after the CTA, to be joined here
+    __shared__ int sm_on[2], sm_c0[2];               // how many CTAs they have, 0 for none; the first
     __shared__ float2 sm_sum[C::HEADS];
-    __shared__ int sm_last[2], sm_abort;
+    __shared__ int sm_abort;
 
     const KvShape& s = p.s;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -279,10 +279,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (threadIdx.x == 0) sm_pre[0] = 0;
         __syncthreads();
     }
-    // Chunks of this CTA, and of its warps. Few chunks go to few CTAs, one or more per
-    // warp: a segment has less to join. (Each CTA has some: a segment's are consecutive.)
+    // Chunks of this CTA, and of its warps. Few chunks go to few CTAs: one or more per
+    // warp, and no more CTAs than pay for their join. A chunk costs a CTA about 0.27 us
+    // of streaming and each of a segment's parts about 0.045 us of joining, so c CTAs on
+    // S segments take 0.27 total / c + 0.045 c / S, least at sqrt(6 total S). (Each CTA
+    // has some chunks: a segment's CTAs are consecutive.)
     const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
-    const int ctas = min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks), me = blockIdx.x;
+    const int ctas = min(min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks),
+                         (int)ceilf(sqrtf(6.f * total * ((float)B * HT))));
+    const int me = blockIdx.x;
     const int share = ctas ? total / ctas : 0, rest = total - share * ctas;
     auto cta_beg = [&](int c) { return c * share + min(c, rest); };
     auto cta_of = [&](int u) { return u < rest * (share + 1) ? u / (share + 1) : rest + (u - rest * (share + 1)) / share; };
@@ -668,6 +673,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             if (last) warps_meet<C::THREADS>();
             if (!theirs) {
+                // of two CTAs with a segment, this is the second where the other has arrived by now
+                int* arrived = p.arrived + (at.b * s.n_kv_heads + at.hk) * tiles + at.tile;
+                const int side = at.beg < u0 ? 0 : at.end > u1 ? 1 : -1;
+                const int c0 = side < 0 ? me : cta_of(at.beg), n = side < 0 ? 1 : cta_of(at.end - 1) - c0 + 1;
+                int before = n == 2 ? *static_cast<volatile int*>(arrived) : 0;
                 for (int x = warp + 1; last && x < kWarps && warp_beg(x) < at.end; ++x) {
                     if (warp_beg(x) == warp_beg(x + 1)) continue;
                     const float4* src = part + x * (C::FRAGS * 32) + lane;
@@ -694,37 +704,37 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                 }
-                const int side = at.beg < u0 ? 0 : at.end > u1 ? 1 : -1;
-                bool done = side < 0;
-                if (side >= 0) {
-                    float4* dst = p.part_o + (me * 2 + side) * (C::FRAGS * 32) + lane;
+                before = __shfl_sync(~0u, before, 0);
+                bool done = n == 1;
+                if (n > 1) {
+                    if (before == 0) {
+                        float4* dst = p.part_o + (me * 2 + side) * (C::FRAGS * 32) + lane;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
+                        for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-                        for (int dt = 0; dt < C::DT; ++dt)
-                            __stcg(dst + (nt * C::DT + dt) * 32,
-                                   make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]));
-                        if (g == 0)
-                            __stcg(&p.part_ml[(me * 2 + side) * 8 + nt * 4 + j],
-                                   make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]));
+                            for (int dt = 0; dt < C::DT; ++dt)
+                                __stcg(dst + (nt * C::DT + dt) * 32,
+                                       make_float4(o[dt][nt][0], o[dt][nt][1], o[dt][nt][2], o[dt][nt][3]));
+                            if (g == 0)
+                                __stcg(&p.part_ml[(me * 2 + side) * 8 + nt * 4 + j],
+                                       make_float4(m[nt][0], l[nt][0], m[nt][1], l[nt][1]));
+                        }
+                        __threadfence();
+                        __syncwarp();
+                        if (lane == 0) before = atomicAdd(arrived, 1);
+                        before = __shfl_sync(~0u, before, 0);
                     }
-                    const int c0 = cta_of(at.beg), n = cta_of(at.end - 1) - c0 + 1;
-                    if (n > 2) {   // joined by a whole CTA, below
-                        if (lane == 0) {
+                    if (before == n - 1 && lane == 0) {
+                        *arrived = 0;       // for the next call
+                        if (n > 2) {        // joined by the whole CTA, below
                             sm_cut[side] = at;
                             sm_on[side] = n;
                             sm_c0[side] = c0;
                         }
-                    } else {       // of two CTAs: the warp that comes second adds the other's part
-                        __threadfence();
-                        __syncwarp();
-                        int before = 0;
-                        if (lane == 0) {
-                            int* arrived = p.arrived + (at.b * s.n_kv_heads + at.hk) * tiles + at.tile;
-                            before = atomicAdd(arrived, 1);
-                            if (before == 1) *arrived = 0;   // for the next call
-                        }
-                        done = __shfl_sync(~0u, before, 0) == 1;
+                    }
+                    // of two CTAs, the warp that comes second adds the other's part
+                    if (n == 2) {
+                        done = before == 1;
                         if (done) {
                             __threadfence();
                             // the earlier CTA's part is its second, the later one's its first; e0 is the
@@ -776,26 +786,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         warps_meet<C::THREADS>();
     }
 
-    // ---- segments cut between many CTAs ---------------------------------------------------
-    __threadfence();
+    // ---- segments of three or more CTAs, by the CTA that finished them -----------------------
     __syncthreads();
     if (sm_on[0] || sm_on[1]) {
-        if (threadIdx.x < 2) {
-            sm_last[threadIdx.x] = 0;
-            const int n = sm_on[threadIdx.x];
-            if (n) {
-                const Place q = sm_cut[threadIdx.x];
-                int* arrived = p.arrived + (q.b * s.n_kv_heads + q.hk) * tiles + q.tile;
-                if (atomicAdd(arrived, 1) == n - 1) {
-                    sm_last[threadIdx.x] = 1;
-                    *arrived = 0;   // for the next call
-                }
-            }
-        }
-        __syncthreads();
         __threadfence();
         for (int side = 0; side < 2; ++side) {
-            if (!sm_last[side]) continue;
+            if (!sm_on[side]) continue;
             const Place q = sm_cut[side];
             const int c0 = sm_c0[side], n = sm_on[side], heads = heads_of(q);
             const float vs = p.v_scale[q.hk];
