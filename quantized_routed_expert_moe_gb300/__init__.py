@@ -682,10 +682,10 @@ def _rows(t, name: str, shape, dtype, device: int) -> int:
 
 def _token_stride(t, name: str, rows: int, heads: int, width: int) -> int:
     """Elements between the tokens of t [rows, heads, width]; heads must be contiguous."""
-    st = t.stride()
-    if st[2] != 1 or (st[1] != width and heads != 1):
+    token, head, one = t.stride()
+    if one != 1 or (head != width and heads != 1):
         _refuse(t, name, (rows, heads, width), t.dtype, t.get_device())
-    return st[0] if rows > 1 else heads * width
+    return token if rows > 1 else heads * width
 
 
 class BlockNorm:
@@ -708,7 +708,9 @@ class BlockNorm:
             if self.device not in (None, w.get_device()):
                 raise ValueError("w_post and w_pre are on two devices")
             self.device = w.get_device()
-        self.w_post, self.w_pre = w_post, w_pre
+        self.w_post, self.w_pre = w_post, w_pre   # kept: the calls take their addresses
+        self._post = None if w_post is None else w_post.data_ptr()
+        self._pre = None if w_pre is None else w_pre.data_ptr()
         self._ids = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
         self._buf = ctypes.create_string_buffer(ctypes.sizeof(moe_block_norm_desc))
         self._buf_addr = ctypes.addressof(self._buf)
@@ -720,13 +722,26 @@ class BlockNorm:
         (may be x) and h [T, H] the outputs (either may be None), gate [T, H],
         [1, H] or [H] of o's type."""
         ids, H, dev = self._ids, self.hidden, x.get_device()
-        if x.dim() != 2 or dev < 0 or self.device not in (None, dev):
-            raise ValueError("x must be a CUDA tensor [T, hidden] on the weights' device")
-        shape = (x.shape[0], H)
-        res, blk, out = x.dtype, x.dtype if o is None else o.dtype, x.dtype if h is None else h.dtype
-        if res not in ids or blk not in ids or out not in ids:
-            raise TypeError("x, o and h must be float32 or bfloat16")
-        gs = 0
+        shape, res = x.shape, x.dtype
+        if len(shape) != 2 or shape[1] != H or res not in ids or dev < 0 or self.device not in (None, dev):
+            raise ValueError("x must be a float32 or bfloat16 CUDA tensor [T, hidden] on the weights' device")
+        blk = res if o is None else o.dtype
+        out = res if h is None else h.dtype
+        if blk not in ids or out not in ids:
+            raise TypeError("o and h must be float32 or bfloat16")
+        # rows without gaps, as almost every call has them, or the stride of each
+        xs = H if x.is_contiguous() else _rows(x, "x", shape, res, dev)
+        os_ = gs = rs = hs = 0
+        op = gp = rp = hp = wp = wn = None
+        if o is not None:
+            plain = o.shape == shape and o.get_device() == dev and o.is_contiguous()
+            os_, op, wp = H if plain else _rows(o, "o", shape, blk, dev), o.data_ptr(), self._post
+        if r is not None:
+            plain = r.shape == shape and r.dtype is res and r.get_device() == dev and r.is_contiguous()
+            rs, rp = H if plain else _rows(r, "r", shape, res, dev), r.data_ptr()
+        if h is not None:
+            plain = h.shape == shape and h.get_device() == dev and h.is_contiguous()
+            hs, hp, wn = H if plain else _rows(h, "h", shape, out, dev), h.data_ptr(), self._pre
         if gate is not None:
             if o is None:
                 raise ValueError("gate needs o")
@@ -736,17 +751,11 @@ class BlockNorm:
                 _dense(gate, "gate", (1, H), blk, dev)
             else:
                 gs = _rows(gate, "gate", shape, blk, dev)
+            gp = gate.data_ptr()
         self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, H, ids[res], ids[blk], ids[out], self.eps, self.scale,
-                             self.weight_offset, _rows(x, "x", shape, res, dev),
-                             0 if o is None else _rows(o, "o", shape, blk, dev), gs,
-                             0 if r is None else _rows(r, "r", shape, res, dev),
-                             0 if h is None else _rows(h, "h", shape, out, dev))
-        st = self._call(self._buf_addr, x.data_ptr(), None if o is None else o.data_ptr(),
-                        None if gate is None else gate.data_ptr(),
-                        None if o is None or self.w_post is None else self.w_post.data_ptr(),
-                        None if h is None or self.w_pre is None else self.w_pre.data_ptr(),
-                        None if r is None else r.data_ptr(), None if h is None else h.data_ptr(), shape[0], dev,
-                        _stream(stream))
+                             self.weight_offset, xs, os_, gs, rs, hs)
+        st = self._call(self._buf_addr, x.data_ptr(), op, gp, wp, wn, rp, hp, shape[0], dev,
+                        stream.cuda_stream if hasattr(stream, "cuda_stream") else _stream(stream))
         if st:
             _check(st, "moe_block_norm")
 
@@ -833,7 +842,9 @@ class KVCache:
         ks, vs = _token_stride(k, "k", T, hk, d), _token_stride(v, "v", T, hk, d)
         qs = qp = op = sp = 0
         if q is not None:
-            qs, qp = _rows(q, "q", (T, hq, d), bf16, dev), q.data_ptr()
+            if not (q.shape == (T, hq, d) and q.dtype is bf16 and q.get_device() == dev):
+                _rows(q, "q", (T, hq, d), bf16, dev)
+            qs, qp = _token_stride(q, "q", T, hq, d), q.data_ptr()
         if q_out is not None:
             op = _dense(q_out, "q_out", (T, hq, d), bf16, dev)
         if seq is not None:
