@@ -148,10 +148,11 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     // slots of this thread: for each row ahead x's vectors, o's, and the gate's where it has
     // rows; then the weights, which every row takes
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(slots);
-    const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B), dw = blockDim.x * 16;   // between vectors
+    const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B);   // between vectors
+    const uint32_t dw = (CTA ? blockDim.x : 32) * 16;   // warps with a row each share the weights
     const uint32_t sx = base + threadIdx.x * 4 * sizeof(R), so = base + 2 * K * dx + threadIdx.x * 4 * sizeof(B);
     const uint32_t sg = so + 2 * K * db, stage = 2 * K * (dx + 2 * db), end = p.ahead * stage;
-    const uint32_t sw = base + end + threadIdx.x * 16, sn = sw + 2 * K * dw;
+    const uint32_t sw = base + end + (CTA ? threadIdx.x : lane) * 16, sn = sw + 2 * K * dw;
     const bool gate_rows = p.gate && d.gate_stride != 0, gate_row = p.gate && d.gate_stride == 0;
     const bool weighted = p.w_post || (AHEAD && gate_row);
     const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
@@ -191,7 +192,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
             if (t0 + (int64_t)i * step < p.T) fetch(i * stage);
             commit();
         }
-        // a gate of one row is a weight too
+        // a gate of one row is a weight too (where warps share the weights, each writes them all:
+        // the same values, and it reads what it wrote)
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -314,7 +316,7 @@ cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
     const auto kernel = k_block_norm<R, B, O, K, CTA, true, MAXT, MINB>;
     const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
     const size_t stage = (size_t)threads * 2 * K * 4 * (sizeof(R) + 2 * sizeof(B));
-    const size_t weights = (size_t)threads * 4 * K * 16;
+    const size_t weights = (size_t)(CTA ? threads : 32) * 4 * K * 16;
     p.ahead = 4;
     while (p.ahead > 1 && (p.ahead * stage + weights + 1024) * ctas > 227 * 1024) p.ahead /= 2;
     const size_t smem = p.ahead * stage + weights;
