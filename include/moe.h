@@ -11,6 +11,10 @@
  *   f_e(x) = W_down,e (silu(W_gate,e x) * W_up,e x)
  *   y      = f_shared(x) + sum_j w_j f_{S_j}(x)
  *
+ * and, beside it, what else a decoder layer does per token: the norms round a
+ * block (moe_block_norm), a paged key-value cache (moe_kv_append) and attention
+ * of one new token over it (moe_kv_attend).
+ *
  * Passages that define these operations:
  *   - router, LFU cache, shared expert and combine: TurboFieldfare article
  *     (GeekNews), section "token generation";

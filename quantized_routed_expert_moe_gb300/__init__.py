@@ -8,6 +8,9 @@ Functions keep the C names (``moe_layer_create``, ``moe_route``,
 ``moe_decode``, ``moe_prefill_chunk``, ``moe_decode_tokens_host``,
 ``moe_cache_stage`` ...). Pointer arguments accept a torch tensor (its
 ``data_ptr()``), a numpy array, a raw integer address or None.
+
+``MoELayer``, ``BlockNorm`` and ``KVCache`` own a handle or weights and take
+tensors; the latter two check shapes, types and devices before a call.
 """
 from __future__ import annotations
 
