@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int len = sm_len[nx.b], first = first_of(len);
             const int tok = (first / CT + u - nx.beg) * CT + bx * p.box_rows;
             if (start) {
-                prefetch_q(nx);
+                if (u != w0) prefetch_q(nx);
                 nx_at = tok / s.page_size;
                 nx_slot = tok - nx_at * s.page_size;
             } else {
@@ -401,9 +401,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (++put == C::STAGES) put = 0;
             if (!(++issued & 1)) lookup(++ahead, false);
         };
-        lookup(ahead, true);
-        for (int i = 0; i < C::STAGES && nx_live; ++i) issue();
-
         // this lane's rows for ldmatrix: of operand A of K Q^T, and of V^T P^T transposed
         uint32_t ka[C::UNITS], va[C::UNITS];
 #pragma unroll
@@ -437,33 +434,45 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             uint32_t qf[C::KS][NT][2];
             float coef[NT][2];           // score in base two per accumulator unit, heads 2j and 2j + 1
             float m[NT][2], l[NT][2], o[C::DT][NT][4];
+            const float ks_unit = p.k_scale[at.hk], vs = p.v_scale[at.hk];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const bool real = nt * 8 + g < heads;
                 const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)at.b * p.a.q_stride +
                                           (int64_t)(h0 + nt * 8 + g) * D;
+#pragma unroll
+                for (int ks = 0; ks < C::KS; ++ks) {
+                    if constexpr (!C::FP8) {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            qf[ks][nt][i] = real ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * j + 8 * i) : 0u;
+                    } else {
+                        // channels 4j..4j+3 of a step stand at k = 2j, 2j+1, 2j+8, 2j+9, as the
+                        // bytes of the keys do
+                        const uint2 v = real ? *reinterpret_cast<const uint2*>(qp + 16 * ks + 4 * j) : make_uint2(0, 0);
+                        qf[ks][nt][0] = v.x;
+                        qf[ks][nt][1] = v.y;
+                    }
+                }
+            }
+            // the first copies follow the first queries, which would wait behind them
+            if (cur == w0) {
+                lookup(w0, true);
+                for (int i = 0; i < C::STAGES && nx_live; ++i) issue();
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
                 float unit = 1.f;
-                if constexpr (!C::FP8) {
+                if constexpr (C::FP8) {
+                    // a head's queries are scaled by a power of two to below 2^15, where fp16 holds
+                    // their 8 bits
+                    float top = 0.f;
 #pragma unroll
                     for (int ks = 0; ks < C::KS; ++ks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
-                            qf[ks][nt][i] = real ? *reinterpret_cast<const uint32_t*>(qp + 16 * ks + 2 * j + 8 * i) : 0u;
-                } else {
-                    // channels 4j..4j+3 of a step stand at k = 2j, 2j+1, 2j+8, 2j+9, as the
-                    // bytes of the keys do. The head's queries are scaled by a power of two
-                    // to below 2^15, where fp16 holds their 8 bits.
-                    float top = 0.f;
-#pragma unroll
-                    for (int ks = 0; ks < C::KS; ++ks) {
-                        const uint2 v = real ? *reinterpret_cast<const uint2*>(qp + 16 * ks + 4 * j) : make_uint2(0, 0);
-                        qf[ks][nt][0] = v.x;
-                        qf[ks][nt][1] = v.y;
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
                             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(qf[ks][nt][i] << 16)),
                                                    fabsf(__uint_as_float(qf[ks][nt][i] & 0xffff0000u))));
-                    }
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
                     // 2^(14 - e) with e the exponent of top, kept within fp32's normal range
@@ -486,7 +495,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int ks = 0; ks < C::KS; ++ks)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) qf[ks][nt][i] ^= 0x80008000u;
-                const float k = p.k_scale[at.hk] * fabsf(p.a.scale);
+                const float k = ks_unit * fabsf(p.a.scale);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     coef[nt][c] = k * __shfl_sync(~0u, unit, (2 * j + c) * 4);
@@ -771,7 +780,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
                 if (done) {
-                    const float vs = p.v_scale[at.hk];
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
