@@ -94,6 +94,9 @@ struct AttendArgs {
     float4* part_ml;    // [CTA][2][8]: maximum (base two) and sum of two heads
     int* arrived;       // [max_batch * head tiles], zero between calls
     int box_rows;       // tokens of one TMA box
+    int boxes_log2;     // boxes of a chunk's column block
+    int page_log2;      // of page_size, -1 where it is no power of two
+    int G, tiles, HT;   // query heads of a key-value head; head tiles of one, and of all
 };
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
@@ -249,10 +252,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     pdl_trigger();
 
     // ---- chunks of every sequence, summed ------------------------------------------
-    const int G = s.n_heads / s.n_kv_heads;
-    const int tiles = (G + C::HEADS - 1) / C::HEADS;   // head tiles per key-value head
-    const int HT = s.n_kv_heads * tiles;
-    const int B = p.a.B;
+    const int G = p.G, tiles = p.tiles, HT = p.HT, B = p.a.B;
     // a sequence attends to tokens [first_of(len), len)
     auto first_of = [&](int len) { return p.a.window > 0 ? max(0, len - p.a.window) : 0; };
     {
@@ -293,8 +293,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // S segments take 0.27 total / c + 0.045 c / S, least at sqrt(6 total S). (Each CTA
     // has some chunks: a segment's CTAs are consecutive.)
     const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
-    const int ctas = min(min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks),
-                         (int)ceilf(sqrtf(6.f * total * ((float)B * HT))));
+    int ctas = min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks);
+    const float sq = 6.f * total * ((float)B * HT);
+    if (sq < (float)ctas * ctas) ctas = (int)ceilf(sqrtf(sq));
     const int me = blockIdx.x;
     const int share = ctas ? total / ctas : 0, rest = total - share * ctas;
     auto cta_beg = [&](int c) { return c * share + min(c, rest); };
@@ -320,15 +321,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // the segment of unit w0
         Place at;
         {
-            int lo = 0, hi = B;   // sm_pre[lo] * HT <= w0 < sm_pre[hi] * HT
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) / 2;
-                if (sm_pre[mid] * HT <= w0) lo = mid;
-                else hi = mid;
-            }
+            // the first b with sm_pre[b + 1] * HT > w0: the block of `step` it is in, then itself
+            const int step = (B + 31) / 32;
+            const int blk = __ffs(__ballot_sync(~0u, sm_pre[min(B, (lane + 1) * step)] * HT > w0)) - 1;
+            const int lo = blk * step - 1 +
+                           __ffs(__ballot_sync(~0u, lane < step && sm_pre[min(B, blk * step + lane + 1)] * HT > w0));
             const int n = sm_pre[lo + 1] - sm_pre[lo], base = sm_pre[lo] * HT, ht = (w0 - base) / n;
             at.b = lo;
-            at.hk = ht / tiles;
+            at.hk = tiles == 1 ? ht : ht / tiles;
             at.tile = ht - at.hk * tiles;
             at.beg = base + ht * n;
             at.end = at.beg + n;
@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ---- the copies of this warp ----------------------------------------------------
         // Stages hold a chunk's keys, then its values, in turn. Box i of either: rows
         // [box * box_rows, ...), one column block; lane i looks its page up a chunk ahead.
-        const int boxes = CT / p.box_rows;
-        const int bx = lane % boxes, col = lane / boxes;
+        const int boxes = 1 << p.boxes_log2;
+        const int bx = lane & (boxes - 1), col = lane >> p.boxes_log2;
         const bool issuer = col < C::COLS;
         // read once, unless further head tiles of the same keys follow
         const uint64_t pol = tiles == 1 ? bw::l2_evict_first() : bw::l2_evict_normal();
@@ -380,7 +380,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int tok = (first / CT + u - nx.beg) * CT + bx * p.box_rows;
             if (start) {
                 if (u != w0) prefetch_q(nx);
-                nx_at = tok / s.page_size;
+                nx_at = p.page_log2 >= 0 ? tok >> p.page_log2 : tok / s.page_size;
                 nx_slot = tok - nx_at * s.page_size;
             } else {
                 for (nx_slot += CT; nx_slot >= s.page_size; nx_slot -= s.page_size) ++nx_at;
@@ -945,14 +945,18 @@ cudaError_t kv_attend_setup(Kv& K) {
 }
 
 moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t stream) {
-    const AttendArgs p{a, K.s, K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml, K.arrived, K.box_rows};
+    const int G = K.s.n_heads / K.s.n_kv_heads;
+    const int ct = pick(K.s, [](auto c) { return decltype(c)::CT; });
+    const int heads = pick(K.s, [](auto c) { return decltype(c)::HEADS; });
+    const int tiles = (G + heads - 1) / heads;
+    int boxes_log2 = 0, page_log2 = 0;
+    while (K.box_rows << boxes_log2 < ct) ++boxes_log2;
+    while (1 << page_log2 < K.s.page_size) ++page_log2;
+    if (1 << page_log2 != K.s.page_size) page_log2 = -1;
+    const AttendArgs p{a,         K.s,        K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml,          K.arrived,
+                       K.box_rows, boxes_log2, page_log2, G,         tiles,    K.s.n_kv_heads * tiles};
     // the kernel counts chunks in 32 bits
-    const int64_t most = pick(K.s, [&](auto c) {
-        using C = decltype(c);
-        const int tiles = (K.s.n_heads / K.s.n_kv_heads + C::HEADS - 1) / C::HEADS;
-        return ((int64_t)a.max_pages * K.s.page_size / C::CT + 1) * a.B * K.s.n_kv_heads * tiles;
-    });
-    if (most > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "the block table spans more chunks than 2^31");
+    if (((int64_t)a.max_pages * K.s.page_size / ct + 1) * a.B * p.HT > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "the block table spans more chunks than 2^31");
     const cudaError_t e = pick(K.s, [&](auto c) { return launch<decltype(c)>(K, p, stream); });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend launch");
 }
