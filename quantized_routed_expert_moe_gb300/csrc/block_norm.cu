@@ -46,6 +46,8 @@ moe_status check_norm(const moe_block_norm_desc* d, const void* x, const void* o
     return MOE_OK;
 }
 
+constexpr int kSlotBytes = 226 * 1024;   // shared memory of a CTA beside its sums
+
 struct NormArgs {
     moe_block_norm_desc d;
     const void *x, *o, *gate;
@@ -53,6 +55,7 @@ struct NormArgs {
     void *r, *h;
     int T;
     int ahead;   // rows on their way
+    bool near;   // the weights are in shared memory
 };
 
 // A row is cut into tiles of 256 channels; a lane holds channels 4 lane.. and 128 +
@@ -188,6 +191,14 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
         const float4 v = *reinterpret_cast<const float4*>(w + c0 + at(k, i));
         return make_float4(v.x + d.weight_offset, v.y + d.weight_offset, v.z + d.weight_offset, v.w + d.weight_offset);
     };
+    // o's factor that every row takes
+    auto factor = [&](int k, int i) {
+        float4 w = p.w_post ? weight(p.w_post, k, i) : make_float4(1.f, 1.f, 1.f, 1.f);
+        if (gate_row) w = times(w, load4(static_cast<const B*>(p.gate) + c0 + at(k, i)));
+        return w;
+    };
+    // only the widest rows can have their weights elsewhere
+    const bool near = AHEAD && (K < 4 || !CTA || p.near);
     uint32_t row = 0;   // of this row's slots
     if constexpr (AHEAD) {
         for (int i = 0; i < p.ahead; ++i) {
@@ -200,12 +211,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                if (at(k, i) < left) {
-                    if (weighted) {
-                        float4 w = p.w_post ? weight(p.w_post, k, i) : make_float4(1.f, 1.f, 1.f, 1.f);
-                        if (gate_row) w = times(w, load4(static_cast<const B*>(p.gate) + c0 + at(k, i)));
-                        put4(sw + (2 * k + i) * dw, w);
-                    }
+                if (near && at(k, i) < left) {
+                    if (weighted) put4(sw + (2 * k + i) * dw, factor(k, i));
                     if (p.h) put4(sn + (2 * k + i) * dw, weight(p.w_pre, k, i));
                 }
     }
@@ -255,7 +262,9 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (at(k, i) < left)
-                        a[k][i] = times(a[k][i], AHEAD ? slot4<float>(sw + (2 * k + i) * dw) : weight(p.w_post, k, i));
+                        a[k][i] = times(a[k][i], near    ? slot4<float>(sw + (2 * k + i) * dw)
+                                                 : AHEAD ? factor(k, i)
+                                                         : weight(p.w_post, k, i));
         }
         ss = 0.f;
 #pragma unroll
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (at(k, i) < left) {
-                        const float4 w = AHEAD ? slot4<float>(sn + (2 * k + i) * dw) : weight(p.w_pre, k, i), v = r[k][i];
+                        const float4 w = near ? slot4<float>(sn + (2 * k + i) * dw) : weight(p.w_pre, k, i), v = r[k][i];
                         store4(ho + at(k, i), times(make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv), w));
                     }
         }
@@ -292,7 +301,7 @@ cudaError_t resident(const void* kernel, int threads, size_t smem, int& held) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (e == cudaSuccess && smem)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 226 * 1024);
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
     if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
     if (e == cudaSuccess) held = sms * (n > 0 ? n : 1);
     return e;
@@ -312,7 +321,8 @@ bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) 
 }
 
 // Many rows: resident CTAs that copy ahead, 4, 2 or 1 rows, as many as leave the
-// shared memory to `ctas` per SM with their weights.
+// shared memory to `ctas` per SM with their weights. A row above some 11000 channels may
+// leave no room for its weights (128 KB for 16384): they are then read for every row.
 template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MINB>
 cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
     const auto kernel = k_block_norm<R, B, O, K, CTA, true, MAXT, MINB>;
@@ -321,7 +331,8 @@ cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
     const size_t weights = (size_t)(CTA ? threads : 32) * 4 * K * 16;
     p.ahead = 4;
     while (p.ahead > 1 && (p.ahead * stage + weights + 1024) * ctas > 227 * 1024) p.ahead /= 2;
-    const size_t smem = p.ahead * stage + weights;
+    p.near = p.ahead * stage + weights <= kSlotBytes;
+    const size_t smem = p.ahead * stage + (p.near ? weights : 0);
     static int held[33];
     const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held[threads / 32]);
     if (e != cudaSuccess) return e;
@@ -384,7 +395,7 @@ moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const 
     if (st != MOE_OK || T == 0) return st;
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, 1};
+    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, 1, true};
     const cudaError_t e = launch(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "block norm launch");
 }

@@ -62,6 +62,15 @@ def test_many_rows(T):
     check(*make(T, 512, gate="row", seed=T))
 
 
+# more rows than the device holds at a time, in every layout of a row
+@pytest.mark.parametrize("res,blk,out,gate", [(F32, BF16, BF16, "full"), (F32, F32, F32, "row"),
+                                              (BF16, BF16, F32, "none"), (BF16, F32, BF16, "full")])
+@pytest.mark.parametrize("T,H", [(20001, 64), (20001, 320), (12345, 768), (12345, 1024), (2501, 1088), (2501, 4160),
+                                 (2501, 6208), (1701, 8192), (701, 8256), (701, 11264), (701, 12352), (701, 16384)])
+def test_many_rows_of_every_layout(T, H, res, blk, out, gate):
+    check(*make(T, H, res, blk, out, True, gate, seed=H), scale=0.75, offset=1.0)
+
+
 @pytest.mark.parametrize("gate", ["full", "row"])
 def test_strided_rows(gate):
     x, o, ga, wp, wn, r, h = make(9, 320, gate=gate, seed=3, pad=24)
