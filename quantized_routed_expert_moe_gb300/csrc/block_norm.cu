@@ -54,7 +54,6 @@ struct NormArgs {
     const float *w_post, *w_pre;
     void *r, *h;
     int T;
-    int ahead;   // rows on their way
     bool near;   // the weights are in shared memory
 };
 
@@ -134,10 +133,12 @@ __device__ __forceinline__ float row_sum(float v, float* sm) {
 // The rows are independent streams: read x, o and gate once, write r and h once,
 // with two sums over the row between (of o, then of r). A row stays in the registers
 // of one CTA (CTA) or of one warp, K tiles per warp. Where a CTA has many rows (AHEAD),
-// a thread copies its channels of the next p.ahead rows into shared memory, so that
-// they are on their way while this one waits for its sums. Measured: 8191 rows of 6144
-// (fp32 x and r, bf16 o, gate and h) 120.5 us, 5.8 TB/s, 86% of the copy rate; 4000 rows
-// of 2816 in bf16 20.5 us; one row of 6144 3.0 us, a chain of two sums.
+// a thread copies its channels of the next row into shared memory, so that they are on
+// their way while this one waits for its sums (two rows ahead: from 13% faster, fp32 x of
+// 5120, to 14% slower, bf16 of 2816; one is kept). Measured: 8191 rows of 6144 (fp32 x and
+// r, bf16 o, gate and h) 108.5 us, 6.5 TB/s, 96% of the copy rate; 4000 rows of 2816 in
+// bf16 18.2 us; 8191 rows of 1024 in bf16 15.6 us; one row of 6144 3.0 us, a chain of two
+// sums.
 template <typename R, typename B, typename O, int K, bool CTA, bool AHEAD, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     __shared__ float sm[2][32];
@@ -150,16 +151,16 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     const float inv_h = 1.f / d.hidden;
     // vector (k, i) is channels c0 + at(k, i) ..
     auto at = [&](int k, int i) { return k * warps * 256 + i * 128; };
-    // slots of this thread: for each row ahead x's vectors, o's, and the gate's where it has
-    // rows; then the weights, which every row takes
+    // slots of this thread: x's vectors of the next row, o's, and the gate's where it has rows;
+    // then the weights, which every row takes
     const uint32_t base = (uint32_t)__cvta_generic_to_shared(slots);
     const uint32_t dx = blockDim.x * 4 * sizeof(R), db = blockDim.x * 4 * sizeof(B);   // between vectors
     const uint32_t dw = (CTA ? blockDim.x : 32) * 16;   // warps with a row each share the weights
     const uint32_t sx = base + threadIdx.x * 4 * sizeof(R), so = base + 2 * K * dx + threadIdx.x * 4 * sizeof(B);
-    const uint32_t sg = so + 2 * K * db, stage = 2 * K * (dx + 2 * db), end = p.ahead * stage;
-    const uint32_t sw = base + end + (CTA ? threadIdx.x : lane) * 16, sn = sw + 2 * K * dw;
     const bool gate_rows = p.gate && d.gate_stride != 0, gate_row = p.gate && d.gate_stride == 0;
     const bool weighted = p.w_post || (AHEAD && gate_row);
+    const uint32_t sg = so + 2 * K * db, stage = 2 * K * (dx + (gate_rows ? 2 : 1) * db);
+    const uint32_t sw = base + stage + (CTA ? threadIdx.x : lane) * 16, sn = sw + (weighted ? 2 * K * dw : 0);
     const int t0 = blockIdx.x * per + (CTA ? 0 : warp), step = gridDim.x * per;
     pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
     pdl_trigger();
@@ -174,19 +175,18 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
         o += step * d.o_stride;
         gate += step * d.gate_stride;
     };
-    auto fetch = [&](uint32_t row) {
+    auto fetch = [&] {
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (at(k, i) < left) {
-                    copy4(row + sx + (2 * k + i) * dx, x + at(k, i));
-                    if (p.o) copy4(row + so + (2 * k + i) * db, o + at(k, i));
-                    if (gate_rows) copy4(row + sg + (2 * k + i) * db, gate + at(k, i));
+                    copy4(sx + (2 * k + i) * dx, x + at(k, i));
+                    if (p.o) copy4(so + (2 * k + i) * db, o + at(k, i));
+                    if (gate_rows) copy4(sg + (2 * k + i) * db, gate + at(k, i));
                 }
         next_row();
     };
-    auto commit = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     auto weight = [&](const float* w, int k, int i) {
         const float4 v = *reinterpret_cast<const float4*>(w + c0 + at(k, i));
         return make_float4(v.x + d.weight_offset, v.y + d.weight_offset, v.z + d.weight_offset, v.w + d.weight_offset);
@@ -197,14 +197,11 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
         if (gate_row) w = times(w, load4(static_cast<const B*>(p.gate) + c0 + at(k, i)));
         return w;
     };
-    // only the widest rows can have their weights elsewhere
-    const bool near = AHEAD && (K < 4 || !CTA || p.near);
-    uint32_t row = 0;   // of this row's slots
+    // only rows above 8192 channels can have their weights elsewhere: up to there a row and its
+    // weights take at most 160 KB
+    const bool near = AHEAD && (K * MAXT <= 1024 || p.near);
     if constexpr (AHEAD) {
-        for (int i = 0; i < p.ahead; ++i) {
-            if (t0 + (int64_t)i * step < p.T) fetch(i * stage);
-            commit();
-        }
+        fetch();
         // a gate of one row is a weight too (where warps share the weights, each writes them all:
         // the same values, and it reads what it wrote)
 #pragma unroll
@@ -219,19 +216,15 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
 
     for (int64_t t = t0; t < p.T; t += step) {
         float4 r[K][2], a[K][2];
-        if constexpr (AHEAD) {
-            if (p.ahead == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
-            else if (p.ahead == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
-            else asm volatile("cp.async.wait_group 3;" ::: "memory");
-        }
+        if constexpr (AHEAD) asm volatile("cp.async.wait_all;" ::: "memory");
 #pragma unroll
         for (int k = 0; k < K; ++k)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const bool on = at(k, i) < left;
                 r[k][i] = a[k][i] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (on) r[k][i] = AHEAD ? slot4<R>(row + sx + (2 * k + i) * dx) : load4(x + at(k, i));
-                if (on && p.o) a[k][i] = AHEAD ? slot4<B>(row + so + (2 * k + i) * db) : load4(o + at(k, i));
+                if (on) r[k][i] = AHEAD ? slot4<R>(sx + (2 * k + i) * dx) : load4(x + at(k, i));
+                if (on && p.o) a[k][i] = AHEAD ? slot4<B>(so + (2 * k + i) * db) : load4(o + at(k, i));
             }
         float ss = 0.f;
 #pragma unroll
@@ -244,13 +237,10 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (at(k, i) < left)
-                        a[k][i] = times(a[k][i], AHEAD ? slot4<B>(row + sg + (2 * k + i) * db) : load4(gate + at(k, i)));
+                        a[k][i] = times(a[k][i], AHEAD ? slot4<B>(sg + (2 * k + i) * db) : load4(gate + at(k, i)));
         }
         if constexpr (AHEAD) {
-            if (t + (int64_t)p.ahead * step < p.T) fetch(row);
-            commit();
-            row += stage;
-            if (row == end) row = 0;
+            if (t + step < p.T) fetch();
         } else {
             next_row();
         }
@@ -320,45 +310,45 @@ bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) 
     return true;
 }
 
-// Many rows: resident CTAs that copy ahead, 4, 2 or 1 rows, as many as leave the
-// shared memory to `ctas` per SM with their weights. A row above some 11000 channels may
-// leave no room for its weights (128 KB for 16384): they are then read for every row.
+// Many rows: resident CTAs that copy a row ahead. A row above some 11000 channels may leave
+// no room for its weights beside it (128 KB for 16384): they are then read for every row.
 template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MINB>
-cudaError_t launch_many(NormArgs p, int threads, int ctas, cudaStream_t s) {
+cudaError_t launch_many(NormArgs p, int threads, cudaStream_t s) {
     const auto kernel = k_block_norm<R, B, O, K, CTA, true, MAXT, MINB>;
     const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
-    const size_t stage = (size_t)threads * 2 * K * 4 * (sizeof(R) + 2 * sizeof(B));
-    const size_t weights = (size_t)(CTA ? threads : 32) * 4 * K * 16;
-    p.ahead = 4;
-    while (p.ahead > 1 && (p.ahead * stage + weights + 1024) * ctas > 227 * 1024) p.ahead /= 2;
-    p.near = p.ahead * stage + weights <= kSlotBytes;
-    const size_t smem = p.ahead * stage + (p.near ? weights : 0);
-    static int held[33];
-    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held[threads / 32]);
+    const bool gate_rows = p.gate && p.d.gate_stride != 0;
+    const int inputs = gate_rows ? 2 : 1, kept = (p.w_post || (p.gate && !gate_rows)) + (p.h != nullptr);
+    const size_t stage = (size_t)threads * 2 * K * 4 * (sizeof(R) + inputs * sizeof(B));
+    const size_t weights = (size_t)(CTA ? threads : 32) * 2 * K * 16 * kept;
+    p.near = stage + weights <= kSlotBytes;
+    const size_t smem = stage + (p.near ? weights : 0);
+    static int kinds[33][2][3];   // the same warps, inputs and weights take the same shared memory
+    int& held = kinds[threads / 32][inputs - 1][kept];
+    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3(need < held[threads / 32] ? need : held[threads / 32]), dim3(threads), smem, s, true, p);
+    return launch_pdl(kernel, dim3(need < held ? need : held), dim3(threads), smem, s, true, p);
 }
 
-// By the row's tiles of 256 channels. Up to 4: a warp per row. Up to 32: a warp per
-// tile where the rows are few, for the shortest chain; two tiles per warp where they
-// are many (the reductions and barriers of a row weigh half). Above: four tiles per
-// warp.
+// By the row's tiles of 256 channels: a warp for one, above that a CTA with a warp per
+// tile (a warp with two to four tiles took 5 to 35% longer over 1024 to 6144 channels,
+// and a warp per row as much over 512 to 1024), above 32 a warp per two. Many rows of up
+// to 18 tiles hold two CTAs per SM or more, with 56 registers; of 16-bit rows of 19 to 24
+// tiles, half as many warps with two tiles each do (57.6 against 68.6 us at 5120).
 template <typename R, typename B, typename O>
 cudaError_t launch_row(const NormArgs& p, cudaStream_t s) {
     const int n = (p.d.hidden + 255) / 256;
     cudaError_t e;
-    if (n == 1) return launch_few<R, B, O, 1, false, 256, 4>(p, 256, s, e) ? e : launch_many<R, B, O, 1, false, 256, 4>(p, 256, 4, s);
-    if (n == 2) return launch_few<R, B, O, 2, false, 256, 3>(p, 256, s, e) ? e : launch_many<R, B, O, 2, false, 256, 3>(p, 256, 3, s);
-    if (n == 3) return launch_few<R, B, O, 3, false, 256, 2>(p, 256, s, e) ? e : launch_many<R, B, O, 3, false, 256, 2>(p, 256, 2, s);
-    if (n == 4) return launch_few<R, B, O, 4, false, 256, 2>(p, 256, s, e) ? e : launch_many<R, B, O, 4, false, 256, 2>(p, 256, 2, s);
+    if (n == 1)
+        return launch_few<R, B, O, 1, false, 256, 4>(p, 256, s, e) ? e : launch_many<R, B, O, 1, false, 256, 4>(p, 256, s);
     if (n <= 32) {
         if (launch_few<R, B, O, 1, true, 1024, 1>(p, n * 32, s, e)) return e;
-        const int threads = (n + 1) / 2 * 32;
-        if (n <= 24) return launch_many<R, B, O, 2, true, 384, 2>(p, threads, 768 / threads, s);
-        return launch_many<R, B, O, 2, true, 512, 2>(p, threads, 2, s);
+        if (n <= 18) return launch_many<R, B, O, 1, true, 576, 2>(p, n * 32, s);
+        if constexpr (sizeof(R) + sizeof(B) + sizeof(O) == 6)
+            if (n <= 24) return launch_many<R, B, O, 2, true, 384, 2>(p, (n + 1) / 2 * 32, s);
+        return launch_many<R, B, O, 1, true, 1024, 1>(p, n * 32, s);
     }
-    const int threads = (n + 3) / 4 * 32;
-    return launch_few<R, B, O, 4, true, 512, 1>(p, threads, s, e) ? e : launch_many<R, B, O, 4, true, 512, 1>(p, threads, 1, s);
+    const int threads = (n + 1) / 2 * 32;
+    return launch_few<R, B, O, 2, true, 1024, 1>(p, threads, s, e) ? e : launch_many<R, B, O, 2, true, 1024, 1>(p, threads, s);
 }
 
 template <typename R, typename B>
@@ -395,7 +385,7 @@ moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const 
     if (st != MOE_OK || T == 0) return st;
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, 1, true};
+    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, true};
     const cudaError_t e = launch(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "block norm launch");
 }

@@ -66,6 +66,7 @@ def test_many_rows(T):
 @pytest.mark.parametrize("res,blk,out,gate", [(F32, BF16, BF16, "full"), (F32, F32, F32, "row"),
                                               (BF16, BF16, F32, "none"), (BF16, F32, BF16, "full")])
 @pytest.mark.parametrize("T,H", [(20001, 64), (20001, 320), (12345, 768), (12345, 1024), (2501, 1088), (2501, 4160),
+                                 (2501, 4608), (2501, 5120), (2501, 6144),
                                  (2501, 6208), (1701, 8192), (701, 8256), (701, 11264), (701, 12352), (701, 16384)])
 def test_many_rows_of_every_layout(T, H, res, blk, out, gate):
     check(*make(T, H, res, blk, out, True, gate, seed=H), scale=0.75, offset=1.0)
