@@ -120,10 +120,12 @@ moe_status check_attend(const moe_kv_desc* d, const moe_kv_attend_args* a) {
 
 // ---- append ---------------------------------------------------------------------
 //
-// A head is D / 16 groups of 16 channels, two 16-byte vectors each: a rotated
-// group holds 8 pairs (channels 8g.. and rotary_dim / 2 + 8g.., or the 8 adjacent
-// pairs from 16g), a group past rotary_dim is copied. One lane moves a whole group
-// and reads both vectors before it writes, so q may be rotated in place.
+// A head is D / 16 groups of 16 channels, two 16-byte vectors each, so laid that
+// neighbouring lanes read and write neighbouring vectors: channels 8g.. and D / 2 + 8g..
+// of a value or of adjacent pairs; of pairs half the rotary channels apart, the 8 pairs
+// 8g.. and rotary_dim / 2 + 8g.., and past rotary_dim the two halves of the rest. One
+// lane moves a whole group and reads both vectors before it writes, so q may be rotated
+// in place.
 //
 // The angle p * inv_freq is kept as a 64-bit fraction of a turn: turns =
 // frac(inv_freq / 2 pi) * 2^64, and p * turns mod 2^64 is the exact phase of
@@ -177,9 +179,12 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int groups = s.head_dim / 16, g = lane % groups, side = 32 / groups, half = s.rotary_dim / 2;
     const int q_heads = p.a.q ? s.n_heads : 0, k_heads = q_heads + s.n_kv_heads, heads = k_heads + s.n_kv_heads;
-    const bool rotated = 16 * g < s.rotary_dim;
-    // the group's two vectors, where it is rotated and where not
-    const int c0 = rotated && !ADJACENT ? 8 * g : 16 * g, step = rotated && !ADJACENT ? half : 8;
+    // the group's two vectors of a query or key, and of a value
+    const bool pairs = !ADJACENT && 16 * g < s.rotary_dim, past = !ADJACENT && !pairs;
+    const int v0 = 8 * g, v1 = v0 + s.head_dim / 2;
+    const int c0 = v0 + (past ? half : 0), c1 = pairs ? c0 + half : v1;
+    const bool turn0 = ADJACENT ? c0 < s.rotary_dim : pairs, turn1 = ADJACENT ? c1 < s.rotary_dim : pairs;
+    const int a0 = ADJACENT ? c0 / 2 : c0, a1 = ADJACENT ? c1 / 2 : c0 + 4;   // their angles, four each
     const int stride = gridDim.x * 8, dt = stride / p.parts, dp = stride - dt * p.parts;   // to a warp's next unit
     uint4* const slots = ring + warp * (kAhead * 64) + lane;
     uint32_t bits = 0;
@@ -211,10 +216,9 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                 : turned       ? static_cast<const __nv_bfloat16*>(p.a.k) + ft * p.a.k_stride + (head - q_heads) * s.head_dim
                                : static_cast<const __nv_bfloat16*>(p.a.v) + ft * p.a.v_stride + (head - k_heads) * s.head_dim;
             const uint32_t to = (uint32_t)__cvta_generic_to_shared(slots + put * 64);
-            src += turned ? c0 : 16 * g;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src) : "memory");
-            src += turned ? step : 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(src) : "memory");
+            const __nv_bfloat16 *src0 = src + (turned ? c0 : v0), *src1 = src + (turned ? c1 : v1);
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(src0) : "memory");
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + 512), "l"(src1) : "memory");
         }
         if ((fr += p.parts) >= p.rounds) {
             advance(ft, fp);
@@ -258,40 +262,41 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             take = (take + 1) % kAhead;
             if (r == part) next_page = look_up(next_pos, next_seq, next_read);
             const int head = r * side + lane / groups;
-            const bool is_q = head < q_heads, is_v = head >= k_heads, turn = rotated && !is_v;
+            const bool is_q = head < q_heads, is_v = head >= k_heads;
             if (head < heads && (is_q || page >= 0)) {
                 const int hk = head - (is_v ? k_heads : q_heads);
-                const int at0 = is_v ? 16 * g : c0, at1 = is_v ? 16 * g + 8 : c0 + step;
+                const int at0 = is_v ? v0 : c0, at1 = is_v ? v1 : c1;
                 const float inv = E4M3 && !is_q ? 1.f / (is_v ? p.v_scale : p.k_scale)[hk] : 1.f;
                 uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
                 uint32_t e[2][2] = {};
                 float c[8], sn[8];
-                if (turn)
-#pragma unroll
-                    for (int x = 0; x < 8; x += 4) {
-                        *reinterpret_cast<float4*>(c + x) = *reinterpret_cast<const float4*>(&sm_c[warp][8 * g + x]);
-                        *reinterpret_cast<float4*>(sn + x) = *reinterpret_cast<const float4*>(&sm_s[warp][8 * g + x]);
-                    }
+                const bool t0 = turn0 && !is_v, t1 = ADJACENT ? turn1 && !is_v : t0;
+                if (t0) {
+                    *reinterpret_cast<float4*>(c) = *reinterpret_cast<const float4*>(&sm_c[warp][a0]);
+                    *reinterpret_cast<float4*>(sn) = *reinterpret_cast<const float4*>(&sm_s[warp][a0]);
+                }
+                if (t1) {
+                    *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&sm_c[warp][a1]);
+                    *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(&sm_s[warp][a1]);
+                }
                 // two channels of either vector at a time
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
-                    if (turn) {
-                        if constexpr (ADJACENT) {
-                            a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
-                            b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
-                        } else {
-                            const float2 a0 = a;
-                            a = make_float2(a.x * c[2 * x] - b.x * sn[2 * x], a.y * c[2 * x + 1] - b.y * sn[2 * x + 1]);
-                            b = make_float2(b.x * c[2 * x] + a0.x * sn[2 * x], b.y * c[2 * x + 1] + a0.y * sn[2 * x + 1]);
-                        }
+                    if constexpr (ADJACENT) {
+                        if (t0) a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
+                        if (t1) b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
+                    } else if (t0) {
+                        const float2 u = a;
+                        a = make_float2(a.x * c[2 * x] - b.x * sn[2 * x], a.y * c[2 * x + 1] - b.y * sn[2 * x + 1]);
+                        b = make_float2(b.x * c[2 * x] + u.x * sn[2 * x], b.y * c[2 * x + 1] + u.y * sn[2 * x + 1]);
                     }
                     if (E4M3 && !is_q) {
                         e[0][x / 2] |= quant2(a, inv) << 16 * (x % 2);
                         e[1][x / 2] |= quant2(b, inv) << 16 * (x % 2);
-                    } else if (turn) {
-                        w[0][x] = pack2(a);
-                        w[1][x] = pack2(b);
+                    } else {
+                        if (t0) w[0][x] = pack2(a);
+                        if (t1) w[1][x] = pack2(b);
                     }
                     if (is_q && pos < 0) w[0][x] = w[1][x] = 0;
                 }
@@ -474,12 +479,24 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     AppendArgs p{*args, K.s, K.k_pages, K.v_pages, K.turns, K.k_scale, K.v_scale, K.health, 1, 1};
     const int heads = (args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads, side = 32 / (K.s.head_dim / 16);
     p.rounds = (heads + side - 1) / side;
-    // as few units per token as give every resident warp at least eight, so that the last
-    // ones leave little of the GPU idle, but two rounds or more to each set of angles; one
-    // round per unit where the tokens are few
+    // Units per token: a warp takes ceil(T n / warps) units, each of rounds / n rounds (the most
+    // of them, where its next unit is always the same part) and about 0.9 of a round for its
+    // angles and page; n with the least of that. 8192 tokens of 16 rounds: n = 4, 42.4 us, with
+    // 3 or 2 47 and 50; 7040 of 12 in 8 bits: n = 1, 28.2, with 2 or 4 30 and 33.
     const int64_t warps = (int64_t)K.num_sms * 3 * 8;
-    while (p.parts * 4 <= p.rounds && (int64_t)args->T * p.parts < 8 * warps) p.parts *= 2;
-    if ((int64_t)args->T * p.rounds <= warps) p.parts = p.rounds;
+    if ((int64_t)args->T * p.rounds <= warps) {
+        p.parts = p.rounds;
+    } else {
+        double least = 0;
+        for (int n = 1; n <= p.rounds; ++n) {
+            const double each = warps % n ? (double)p.rounds / n : (p.rounds + n - 1) / n;
+            const double cost = (double)(((int64_t)args->T * n + warps - 1) / warps) * (each + 0.9);
+            if (n == 1 || cost < least) {
+                least = cost;
+                p.parts = n;
+            }
+        }
+    }
     const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)args->T * p.parts + 7) / 8, (int64_t)K.num_sms * 3);
     const cudaError_t e =
         launch_pdl(append_kernel(K.s), dim3(grid), dim3(256), kAppendRing, static_cast<cudaStream_t>(stream), true, p);

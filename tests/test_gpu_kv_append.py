@@ -109,6 +109,15 @@ def test_shapes(T, Hq, Hk, page):
     run_case(T, Hq, Hk, 64, page, layout="nhd" if T % 2 else "hnd", seed=T, split=T % 3 != 0)
 
 
+# enough tokens that a warp has several units, of one round or more of a token
+@pytest.mark.parametrize("T,Hq,Hk,d,rot,adjacent", [(700, 32, 8, 128, 128, False), (1333, 16, 4, 64, 32, True),
+                                                    (3777, 12, 2, 64, 64, False), (4001, 5, 1, 256, 128, True),
+                                                    (8000, 3, 1, 128, 96, False)])
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+def test_many_tokens(T, Hq, Hk, d, rot, adjacent, dt):
+    run_case(T, Hq, Hk, d, 32, dt, rot, adjacent, seed=T)
+
+
 @pytest.mark.parametrize("dt", [BF16, E4M3])
 def test_far_positions(dt):
     """Angles of 10^6 turns and more: the phase may not lose its fraction."""
