@@ -614,7 +614,7 @@ typedef struct {
  * stay valid until moe_kv_destroy; 16-byte aligned).
  *   inv_freq: host double [rotary_dim / 2], finite, radians per position (the
  *     caller applies any frequency scaling); may be NULL when rotary_dim is 0.
- *   k_scale, v_scale: host fp32 [n_kv_heads], finite and positive: a cached
+ *   k_scale, v_scale: host fp32 [n_kv_heads], positive normal numbers: a cached
  *     e4m3 value c stands for c * scale. Required for MOE_E4M3, NULL for MOE_BF16.
  * The handle owns the frequency table and the workspace of moe_kv_attend
  * (moe_kv_device_bytes). As for a layer, one call at a time, and work of one

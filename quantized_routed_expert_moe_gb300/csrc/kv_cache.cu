@@ -381,8 +381,8 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     if (e4m3 != (k_scale != nullptr) || e4m3 != (v_scale != nullptr))
         return fail(MOE_E_INVALID, "k_scale and v_scale go with an e4m3 cache, and only with it");
     for (int h = 0; e4m3 && h < Hk; ++h)
-        if (!(std::isfinite(k_scale[h]) && k_scale[h] > 0 && std::isfinite(v_scale[h]) && v_scale[h] > 0))
-            return fail(MOE_E_INVALID, "k_scale and v_scale must be finite and positive");
+        if (!(std::isnormal(k_scale[h]) && k_scale[h] > 0 && std::isnormal(v_scale[h]) && v_scale[h] > 0))
+            return fail(MOE_E_INVALID, "k_scale and v_scale must be positive normal numbers");   // and their reciprocals finite
 
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");

@@ -117,6 +117,13 @@ def test_bad_create_arguments():
     refused(moe.moe_kv_create, e, P, P, f, np.array([np.inf, 1], np.float32), one)
 
 
+@pytest.mark.parametrize("bad", [1e-39, -1.0, np.nan, -0.0])
+def test_scales_without_a_finite_reciprocal_are_refused(bad):
+    e, one, two = kv_desc(cache_dtype=moe.MOE_E4M3), np.ones(2, np.float32), np.array([1, bad], np.float32)
+    refused(moe.moe_kv_create, e, P, P, np.ones(32), two, one)
+    refused(moe.moe_kv_create, e, P, P, np.ones(32), one, two)
+
+
 def test_null_handles():
     refused(moe.moe_kv_append, None, append_args())
     refused(moe.moe_kv_attend, None, attend_args())
