@@ -53,6 +53,7 @@ namespace moe {
 namespace {
 
 constexpr int kRing = 16 * 1024;   // bytes of stages per warp
+constexpr int kHalf = 8 * 1024;    // of a chunk's keys, or values
 constexpr int kMaxCtas = 160;
 constexpr int kMinChunks = 8;      // of a CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -63,7 +64,7 @@ struct Cfg {
     static constexpr int D = D_, NT = NT_;
     static constexpr bool FP8 = FP8_;
     static constexpr int RB = D * (FP8 ? 1 : 2);              // bytes of a row
-    static constexpr int CT = RB >= 512 ? 16 : RB >= 256 ? 32 : 64;  // tokens of a chunk
+    static constexpr int CT = kHalf / RB;                     // tokens of a chunk
     static constexpr int LINE = RB < 128 ? RB : 128;          // bytes of a shared-memory row (the swizzle's width)
     static constexpr int COLS = RB / LINE;                    // column blocks of a row
     static constexpr int HALF = CT * RB;                      // bytes of a chunk's keys (or values): one stage
