@@ -27,16 +27,17 @@
 // byte the legacy tensor path has several times the rate that the copy allows.
 // Scores, maxima, sums and outputs are fp32. The weights are rounded once to
 // the operand type of the second product, bf16 for a bf16 cache (2^-8 relative,
-// like the output), fp16 for an e4m3 cache (2^-11), whose keys, values and scaled
-// queries are exact in fp16; the sum is taken before that rounding.
+// like the output), fp16 for an e4m3 cache (2^-11), whose keys and values are exact in
+// fp16, and the queries to 2^-39 of their head's largest; the sum is taken before that
+// rounding.
 //
 // Measured (GB300, inputs larger than L2; copy rate 6.77 TB/s): 131072 tokens of one
-// sequence, 48 heads over 8 of 128 channels, 86.5 us, 6.2 TB/s; 64 sequences of up to
-// 16384 tokens, pages of 16, 226 us, 6.6 TB/s; 32 windows of 1024 tokens, 16 heads over
-// 8 of 256, 38.4 us, 5.3 TB/s; 48 sequences of up to 9001 tokens in 8 bits, 64 heads over
-// 4 of 128, 33.2 us, 4.1 TB/s; 17 tokens 5.1 us. What is above the stream's time is the
+// sequence, 48 heads over 8 of 128 channels, 85.8 us, 6.3 TB/s; 64 sequences of up to
+// 16384 tokens, pages of 16, 223 us, 6.7 TB/s; 32 windows of 1024 tokens, 16 heads over
+// 8 of 256, 37.5 us, 5.4 TB/s; 48 sequences of up to 9001 tokens in 8 bits, 64 heads over
+// 4 of 128, 32.6 us, 4.2 TB/s; 17 tokens 4.9 us. What is above the stream's time is the
 // chain of reads before the first copy (lengths, block table, keys: 3 us) and the last
-// joins (5 to 8 us).
+// joins (5 to 7 us).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
