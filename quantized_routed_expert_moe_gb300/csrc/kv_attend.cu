@@ -291,12 +291,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     // Chunks of this CTA, and of its warps. Few chunks go to few CTAs: one or more per
     // warp, and no more CTAs than pay for their join. A chunk costs a CTA about 0.27 us
-    // of streaming and each of a segment's parts about 0.045 us of joining, so c CTAs on
-    // S segments take 0.27 total / c + 0.045 c / S, least at sqrt(6 total S). (Each CTA
-    // has some chunks: a segment's CTAs are consecutive.)
+    // of streaming and each of a segment's parts about 0.045 us of joining (up to 8
+    // fragments, 4 KB; in proportion above), so c CTAs on S segments take 0.27 total / c
+    // + 0.045 c / S, least at sqrt(6 total S). One sequence of 40189 tokens in 8 bits, 12
+    // heads over 1 of 128 (16 fragments): 19.4 us, by the rule for 8 21.6. (Each CTA has
+    // some chunks: a segment's CTAs are consecutive.)
     const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
     int ctas = min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks);
-    const float sq = 6.f * total * ((float)B * HT);
+    const float sq = 48.f / max(8, C::FRAGS) * total * ((float)B * HT);
     if (sq < (float)ctas * ctas) ctas = (int)ceilf(sqrtf(sq));
     const int me = blockIdx.x;
     const int share = ctas ? total / ctas : 0, rest = total - share * ctas;
