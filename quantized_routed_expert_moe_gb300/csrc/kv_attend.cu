@@ -25,11 +25,14 @@
 // per key-value head cost half of what padding the heads to 16 rows would. P^T is
 // turned into the second product's operand by movmatrix. At 2 G FLOP per cached
 // byte the legacy tensor path has several times the rate that the copy allows.
-// Scores, maxima, sums and outputs are fp32. The weights are rounded once to
-// the operand type of the second product, bf16 for a bf16 cache (2^-8 relative,
-// like the output), fp16 for an e4m3 cache (2^-11), whose keys and values are exact in
-// fp16, and the queries to 2^-39 of their head's largest; the sum is taken before that
-// rounding.
+// Scores, maxima, sums and outputs are fp32. The weights of a bf16 cache enter the
+// second product as two bf16 numbers each, off by 2^-16: rounded to one (2^-8, as much
+// as the output's own rounding) they took the output from 1.7e-3 to 2.0e-3 of its norm,
+// and the product with the rest is hidden by the stream. (Heads of 256 with more than 8
+// queries per key-value head take 10% longer for it, and with a seventh warp 2.5% less.)
+// For an e4m3 cache they are rounded once, to fp16 (2^-11), in which its keys and values
+// are exact, and the queries to 2^-39 of their head's largest; the sum is taken before
+// that rounding.
 //
 // Measured (GB300, inputs larger than L2; copy rate 6.77 TB/s): 131072 tokens of one
 // sequence, 48 heads over 8 of 128 channels, 85.8 us, 6.3 TB/s; 64 sequences of up to
@@ -56,7 +59,6 @@ namespace {
 constexpr int kRing = 16 * 1024;   // bytes of stages per warp
 constexpr int kHalf = 8 * 1024;    // of a chunk's keys, or values
 constexpr int kMaxCtas = 160;
-constexpr int kMinChunks = 8;      // of a CTA
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
@@ -76,9 +78,9 @@ struct Cfg {
     static constexpr int STEPS = RB / 32;                     // and of a row
     static constexpr int FRAGS = NT * DT;                     // output fragments of a segment, 32 lanes x float4
     static constexpr int PART = FRAGS * 512;                  // their bytes
-    static constexpr int WARPS = FRAGS == 32 ? 6 : 8;         // 6 where the parts of 8 leave no room for their rings
+    static constexpr int WARPS = FRAGS == 32 ? 7 : 8;         // 7 where the parts of 8 leave no room for their rings
     static constexpr int THREADS = 32 * WARPS;
-    static constexpr size_t smem = 1024 + (size_t)WARPS * (kRing + PART);
+    static constexpr size_t smem = 1024 + (size_t)WARPS * kRing + (size_t)(WARPS - 1) * PART;   // the first sets none aside
 };
 
 // Every warp comes here once, from the end of its chunks or without any.
@@ -156,6 +158,15 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+}
+// Two weights, each as the sum of two bf16 numbers: its upper 16 bits, and the rest
+// rounded, 2^-16 of the weight at most. The rest is above zero, so that an infinite value
+// times the two is not NaN.
+__device__ __forceinline__ void split_pair(float lo, float hi, uint32_t& upper, uint32_t& rest) {
+    const uint32_t a = __float_as_uint(lo), b = __float_as_uint(hi);
+    upper = __byte_perm(a, b, 0x7632);
+    rest = pack_pair<false>(fmaxf(lo - __uint_as_float(a & 0xffff0000u), 0x1p-126f),
+                            fmaxf(hi - __uint_as_float(b & 0xffff0000u), 0x1p-126f));
 }
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
                                             uint32_t bar, uint64_t pol) {
@@ -297,7 +308,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // heads over 1 of 128 (16 fragments): 19.4 us, by the rule for 8 21.6. (Each CTA has
     // some chunks: a segment's CTAs are consecutive.)
     const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
-    int ctas = min((int)gridDim.x, (total + kMinChunks - 1) / kMinChunks);
+    int ctas = min((int)gridDim.x, (total + kWarps - 1) / kWarps);
     const float sq = 48.f / max(8, C::FRAGS) * total * ((float)B * HT);
     if (sq < (float)ctas * ctas) ctas = (int)ceilf(sqrtf(sq));
     const int me = blockIdx.x;
@@ -309,7 +320,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     auto head_of = [&](const Place& q) { return q.hk * G + q.tile * C::HEADS; };
     auto heads_of = [&](const Place& q) { return min(C::HEADS, G - q.tile * C::HEADS); };
     const int w0 = warp_beg(warp), w1 = warp_beg(warp + 1);
-    // a warp's part of the segment that began before it
+    // a warp's part of the segment that began before it; the first warp has none
     float4* part = reinterpret_cast<float4*>(smem_raw + (ring0 - bw::saddr(smem_raw)) + kWarps * kRing);
 
     // sequences with nothing to attend to
@@ -587,7 +598,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                     if (!on) sc[mt][nt][i + c] = -INFINITY;
                         }
                 }
-                uint32_t pf[C::MT][NT][2];   // weights: operand B of O^T = V^T P^T
+                // weights: operand B of O^T = V^T P^T; of a bf16 cache the upper halves, and the rest
+                uint32_t pf[C::MT][NT][2], pr[C::MT][NT][C::FP8 ? 1 : 2];
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     // scores in base two are `unit` times sc, unit > 0
@@ -620,8 +632,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             w[i] = ex2(fmaf(sc[mt][nt][i], unit[i & 1], -base[i & 1]));
                             l[nt][i & 1] += w[i];
                         }
-                        pf[mt][nt][0] = transpose8(pack_pair<C::FP8>(w[0], w[1]));
-                        pf[mt][nt][1] = transpose8(pack_pair<C::FP8>(w[2], w[3]));
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            if constexpr (C::FP8) {
+                                pf[mt][nt][i] = transpose8(pack_pair<true>(w[2 * i], w[2 * i + 1]));
+                            } else {
+                                uint32_t u, rest;
+                                split_pair(w[2 * i], w[2 * i + 1], u, rest);
+                                pf[mt][nt][i] = transpose8(u);
+                                pr[mt][nt][i] = transpose8(rest);
+                            }
+                        }
                     }
                 }
 
@@ -645,6 +666,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 for (int i = 0; i < 4; ++i) r[i] &= keep[i >> 1];
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) mma<false>(o[st][nt], r, pf[mt][nt][0], pf[mt][nt][1]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) mma<false>(o[st][nt], r, pr[mt][nt][0], pr[mt][nt][1]);
                             } else {
 #pragma unroll
                                 for (int d2 = 0; d2 < 2; ++d2) {
@@ -680,7 +703,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // holds its own part in registers; the others set theirs aside.
             const bool theirs = at.beg < w0 && w0 != u0;
             if (theirs) {
-                float4* dst = part + warp * (C::FRAGS * 32) + lane;
+                float4* dst = part + (warp - 1) * (C::FRAGS * 32) + lane;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -701,7 +724,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 int before = n == 2 ? *static_cast<volatile int*>(arrived) : 0;
                 for (int x = warp + 1; last && x < kWarps && warp_beg(x) < at.end; ++x) {
                     if (warp_beg(x) == warp_beg(x + 1)) continue;
-                    const float4* src = part + x * (C::FRAGS * 32) + lane;
+                    const float4* src = part + (x - 1) * (C::FRAGS * 32) + lane;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const float4 ml = *reinterpret_cast<const float4*>(&sm_ml[x][nt * 8 + 2 * j]);
