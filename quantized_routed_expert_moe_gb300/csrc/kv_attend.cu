@@ -30,9 +30,9 @@
 // as the output's own rounding) they took the output from 1.7e-3 to 2.0e-3 of its norm,
 // and the product with the rest is hidden by the stream. (Heads of 256 with more than 8
 // queries per key-value head take 10% longer for it, and with a seventh warp 2.5% less.)
-// For an e4m3 cache they are rounded once, to fp16 (2^-11), in which its keys and values
-// are exact, and the queries to 2^-39 of their head's largest; the sum is taken before
-// that rounding.
+// For an e4m3 cache they are rounded once, to fp16 (2^-11, or 2^-39 of the largest
+// weight), in which its keys and values are exact, and the queries to 2^-39 of their
+// head's largest; the sum is taken before that rounding.
 //
 // Measured (GB300, inputs larger than L2; copy rate 6.77 TB/s): 131072 tokens of one
 // sequence, 48 heads over 8 of 128 channels, 85.8 us, 6.3 TB/s; 64 sequences of up to
@@ -80,6 +80,9 @@ struct Cfg {
     static constexpr int PART = FRAGS * 512;                  // their bytes
     static constexpr int WARPS = FRAGS == 32 ? 7 : 8;         // 7 where the parts of 8 leave no room for their rings
     static constexpr int THREADS = 32 * WARPS;
+    // Weights are 2^UP times exp(score - maximum), and so are their sums and outputs: in fp16
+    // that leaves 28 octaves below the largest with all 11 bits, where 1 would leave 14.
+    static constexpr float UP = FP8 ? 14.f : 0.f, DOWN = FP8 ? 0x1p-14f : 1.f;
     static constexpr size_t smem = 1024 + (size_t)WARPS * kRing + (size_t)(WARPS - 1) * PART;   // the first sets none aside
 };
 
@@ -228,7 +231,7 @@ __device__ __forceinline__ void finish(const AttendArgs& p, int b, int h0, int h
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int h = nt * 8 + 2 * j + c;
-            if (h < heads) p.a.lse[row + h] = L[c] == 0.f ? -INFINITY : M[c] * kLn2 + logf(L[c]);
+            if (h < heads) p.a.lse[row + h] = L[c] == 0.f ? -INFINITY : M[c] * kLn2 + logf(L[c] * C::DOWN);
         }
 }
 
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     // scores in base two are `unit` times sc, unit > 0
-                    float unit[2], base[2], f[2];
+                    float unit[2], low[2], f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         unit[c] = p.a.softcap != 0.f ? kLog2e : coef[nt][c];
@@ -614,8 +617,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
                         x = fmaxf(m[nt][c], x * unit[c]);
-                        base[c] = x == -INFINITY ? 0.f : x;
-                        f[c] = ex2(m[nt][c] - base[c]);
+                        const float base = x == -INFINITY ? 0.f : x;
+                        f[c] = ex2(m[nt][c] - base);
+                        low[c] = base - C::UP;
                         m[nt][c] = x;
                         l[nt][c] *= f[c];
                     }
@@ -629,7 +633,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         float w[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            w[i] = ex2(fmaf(sc[mt][nt][i], unit[i & 1], -base[i & 1]));
+                            w[i] = ex2(fmaf(sc[mt][nt][i], unit[i & 1], -low[i & 1]));
                             l[nt][i & 1] += w[i];
                         }
 #pragma unroll

@@ -1,11 +1,13 @@
 """moe_kv_attend on the GPU within the bounds that its arithmetic gives, where
 those of test_gpu_kv_attend.py are wider."""
+import numpy as np
 import pytest
 import torch
 
+import quantized_routed_expert_moe_gb300 as moe
 import _decoder_ref
 from _decoder_ref import assert_close, attend, rounded
-from test_gpu_kv_attend import BF16, Case
+from test_gpu_kv_attend import BF16, E4M3, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -25,3 +27,44 @@ def test_bf16_weights_are_not_cut_to_bf16(G, D, monkeypatch):
     monkeypatch.setattr(_decoder_ref, "UP", 2.0 ** -16)
     Case([1, 16, 77, 300, 1025], 2 * G, 2, D, 32, seed=G).check()
     Case([20000], G, 1, D, 64, seed=G).check()
+
+
+@pytest.mark.parametrize("nats", [8, 13, 16, 18, 24])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_flat_tail_beside_a_sink_in_8_bits(D, nats):
+    """One position stands far above the rest and has values of zero, so that the output is
+    the tail's alone. Weights go into the product as fp16: 2^-11 relative, and those 28
+    octaves below the largest within 2^-39 of it."""
+    lens, G, page = [20, 64, 700], 4, 16
+    n_pages = sum(-(-n // page) for n in lens)
+    g = torch.Generator("cuda").manual_seed(D + nats)
+    k = torch.randn(n_pages, 1, page, D, generator=g, device="cuda") * 90
+    v = torch.randn(n_pages, 1, page, D, generator=g, device="cuda") * 90
+    k[..., 0] = 0
+    q = torch.zeros(3, G, D, device="cuda")
+    q[..., 0] = torch.tensor([1.0, 1.125, 0.5, 1.0], device="cuda")
+    table, at = torch.zeros(3, -(-max(lens) // page), dtype=torch.int32), 0
+    for b, (n, sink) in enumerate(zip(lens, (19, 0, 333))):
+        need = -(-n // page)
+        table[b, :need] = torch.arange(at, at + need)
+        k[at + sink // page, 0, sink % page, 0] = nats
+        v[at + sink // page, 0, sink % page] = 0
+        at += need
+    k, v, q = k.clamp(-448, 448).to(E4M3), v.clamp(-448, 448).to(E4M3), q.to(BF16)
+    one = np.ones(1, np.float32)
+    out, lse = torch.empty(3, G, D, dtype=BF16, device="cuda"), torch.empty(3, G, device="cuda")
+    with moe.KVCache(k, v, n_heads=G, k_scale=one, v_scale=one, max_batch=3) as kv:
+        kv.attend(q, table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda"), out, lse=lse, scale=1.0,
+                  stream=torch.cuda.current_stream())
+        assert kv.health() == (0, 0)
+    for b, n in enumerate(lens):
+        kk, vv = (_decoder_ref.gather(x, table, b, 0, n, 0) for x in (k, v))
+        s = q[b].cpu().double() @ kk.T
+        p = torch.softmax(s, 1)
+        # the scores are sums of one term that is not zero: two roundings, and those of the
+        # base and of the exponential's argument, each of a number up to 1.5 * 24 * 1.44
+        rel = 2.0 ** -11 + 2.0 ** -21 + 4 * 52 * 2.0 ** -24 + 2 * n * 2.0 ** -24
+        bound = rel * (p @ vv.abs()) + 2.0 ** -39 * vv.abs().sum(0) * p.amax(1, keepdim=True)
+        assert_close(out[b], p @ vv, rounded(p @ vv, bound, BF16), f"out {b}")
+        L = torch.logsumexp(s, 1)
+        assert_close(lse[b], L, torch.full_like(L, 2.0 ** -21 + (n + 8 + 4 * 52) * 2.0 ** -24), f"lse {b}")
