@@ -141,6 +141,11 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 // two e4m3 values, the lower or upper two bytes of v, as an fp16 pair, exact
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t v) {
     uint32_t d;
@@ -161,6 +166,16 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+}
+// tanh z, off by 8 units of 2^-24 relative to itself: up to 1/2 by an odd polynomial, fitted
+// to the least relative error there (1.5e-8), and where PAST, past it, by 1 - 2 / (exp(2 z) +
+// 1), whose error of 2^-22 would be the larger the nearer to zero.
+template <bool PAST>
+__device__ __forceinline__ float tanh_of(float z) {
+    const float u = z * z;
+    const float r = z * fmaf(fmaf(fmaf(fmaf(0.0172414916f, u, -0.0530454943f), u, 0.13325879f), u, -0.333331439f), u, 1.f);
+    if (!PAST || !(fabsf(z) > 0.5f)) return r;
+    return 1.f - 2.f * rcp(ex2(z * (2.f * kLog2e)) + 1.f);
 }
 // Two weights, each as the sum of two bf16 numbers: its upper 16 bits, and the rest
 // rounded, 2^-16 of the weight at most. The rest is above zero, so that an infinite value
@@ -438,6 +453,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ---- segments ------------------------------------------------------------------
         int take = 0;                    // the stage to be consumed next, and its barrier's phase
         uint32_t phase = 0;
+        // the cap in base two; one above 2^80 bends no score below 2^67, and its reciprocal would
+        // lose bits
+        const float cap2 = fminf(fmaxf(p.a.softcap * kLog2e, 1.2e-38f), 0x1p80f);
         auto next_stage = [&]() {        // waits for it; the stage's shared address
             bw::mbar_wait(bw::saddr(&sm_bar[warp][take]), phase, &sm_abort, p.health, MOE_KV_TIMEOUT);
             __syncwarp();
@@ -458,7 +476,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 
             // queries: operand B of S^T = K Q^T (column g of head tile nt)
             uint32_t qf[C::KS][NT][2];
-            float coef[NT][2];           // score in base two per accumulator unit, heads 2j and 2j + 1
+            float coef[NT][2];           // score in base two (or its share of the cap) per accumulator unit, heads 2j and 2j + 1
             float m[NT][2], l[NT][2], o[C::DT][NT][4];
             const float ks_unit = p.k_scale[at.hk], vs = p.v_scale[at.hk];
 #pragma unroll
@@ -525,8 +543,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     coef[nt][c] = k * __shfl_sync(~0u, unit, (2 * j + c) * 4);
-                    if (p.a.softcap == 0.f) coef[nt][c] *= kLog2e;   // in base two
-                    coef[nt][c] = fmaxf(coef[nt][c], 1.2e-38f);      // keeps -inf times it -inf
+                    coef[nt][c] = fmaxf(coef[nt][c] * kLog2e, 1.2e-38f);   // keeps -inf times it -inf
+                    if (p.a.softcap != 0.f) coef[nt][c] = fminf(coef[nt][c] / cap2, 3.4e38f);
                     m[nt][c] = -INFINITY;
                     l[nt][c] = 0.f;
                 }
@@ -571,17 +589,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 release();
 
-                // tanh(z) = 1 - 2 / (exp(2 z) + 1): off by 2^-22 of the cap
-                if (p.a.softcap != 0.f) {
+                if (p.a.softcap != 0.f) {   // scores become their share of the cap
+                    float most = 0.f;
 #pragma unroll
-                    for (int mt = 0; mt < C::MT; ++mt)
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt)
+                        for (int c = 0; c < 2; ++c) {
+                            float x = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float e = ex2(sc[mt][nt][i] * coef[nt][i & 1] * (2.f * kLog2e / p.a.softcap));
-                                sc[mt][nt][i] = p.a.softcap - __fdividef(2.f * p.a.softcap, e + 1.f);
-                            }
+                            for (int mt = 0; mt < C::MT; ++mt)
+                                x = fmaxf(x, fmaxf(fabsf(sc[mt][nt][c]), fabsf(sc[mt][nt][c + 2])));
+                            most = fmaxf(most, x * coef[nt][c]);
+                        }
+                    auto cap = [&](auto past) {
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) sc[mt][nt][i] = tanh_of<past>(sc[mt][nt][i] * coef[nt][i & 1]);
+                    };
+                    if (__any_sync(~0u, most > 0.5f)) cap(std::true_type{});
+                    else cap(std::false_type{});
                 }
                 // which tokens are attended
                 auto seen = [&](int t) {
@@ -609,7 +638,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     float unit[2], low[2], f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        unit[c] = p.a.softcap != 0.f ? kLog2e : coef[nt][c];
+                        unit[c] = p.a.softcap != 0.f ? cap2 : coef[nt][c];
                         float x = sc[0][nt][c];
 #pragma unroll
                         for (int mt = 0; mt < C::MT; ++mt) x = fmaxf(x, fmaxf(sc[mt][nt][c], sc[mt][nt][c + 2]));

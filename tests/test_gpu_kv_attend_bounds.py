@@ -68,3 +68,30 @@ def test_a_flat_tail_beside_a_sink_in_8_bits(D, nats):
         assert_close(out[b], p @ vv, rounded(p @ vv, bound, BF16), f"out {b}")
         L = torch.logsumexp(s, 1)
         assert_close(lse[b], L, torch.full_like(L, 2.0 ** -21 + (n + 8 + 4 * 52) * 2.0 ** -24), f"lse {b}")
+
+
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("cap", [1e-3, 0.5, 50.0, 1e4, 1e7, 1e12, 3e38])
+def test_caps_of_any_size(cap, dt):
+    """The capped score is off relative to itself, not to the cap."""
+    c = Case([1, 40, 513, 300], 8, 2, 128, 16, dt, seed=21, sharp=3.0)
+    with c.handle() as kv:
+        out, lse = c.run(kv, softcap=cap)
+        assert kv.health() == (0, 0)
+    cap32 = float(np.float32(cap))
+    for b, n in enumerate(c.lens):
+        for h in range(2):
+            k, v = (_decoder_ref.gather(x, c.table, b, 0, n, h) * (1.0 if sc is None else float(sc[h]))
+                    for x, sc in ((c.k, c.scales[0]), (c.v, c.scales[1])))
+            q = c.q[b, 4 * h:4 * h + 4].cpu().double()
+            s = cap32 * torch.tanh(q @ k.T * c.scale / cap32)
+            # before the cap as without one; then the share of the cap, its tanh and the cap
+            es = (128 + 6) * 2.0 ** -24 * (q.abs() @ k.abs().T * c.scale) + 12 * 2.0 ** -24 * s.abs()
+            es = torch.minimum(es, torch.tensor(2 * cap32)).amax(1, keepdim=True)   # both are within the cap
+            up = 2.0 ** (-16 if dt is BF16 else -11)
+            p = torch.softmax(s, 1)
+            rel = 2 * es + 2.0 ** -21 + up + 2 * n * 2.0 ** -24
+            assert_close(out[b, 4 * h:4 * h + 4], p @ v, rounded(p @ v, rel * (p @ v.abs()), BF16), f"out {b} {h}")
+            L = torch.logsumexp(s, 1)
+            assert_close(lse[b, 4 * h:4 * h + 4], L, es[:, 0] + 2.0 ** -21 + n * 2.0 ** -24 + 8 * 2.0 ** -24 * L.abs(),
+                         f"lse {b} {h}")
