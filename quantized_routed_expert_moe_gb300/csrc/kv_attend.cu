@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     // scores in base two are `unit` times sc, unit > 0
-                    float unit[2], low[2], f[2];
+                    float unit[2], base[2], low[2], f[2];
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         unit[c] = p.a.softcap != 0.f ? cap2 : coef[nt][c];
@@ -646,9 +646,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(~0u, x, 16));
                         x = fmaxf(m[nt][c], x * unit[c]);
-                        const float base = x == -INFINITY ? 0.f : x;
-                        f[c] = ex2(m[nt][c] - base);
-                        low[c] = base - C::UP;
+                        base[c] = x == -INFINITY ? 0.f : x;
+                        f[c] = ex2(m[nt][c] - base[c]);
+                        low[c] = base[c] - C::UP;
                         m[nt][c] = x;
                         l[nt][c] *= f[c];
                     }
@@ -657,6 +657,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         for (int dt = 0; dt < C::DT; ++dt)
 #pragma unroll
                             for (int i = 0; i < 4; ++i) o[dt][nt][i] *= f[i & 1];
+                    // The base is a rounded product, and the products below are not: past 2^17 that
+                    // tells (2^-8 of the weights, and at last their whole range), so that there both are.
+                    if (__any_sync(~0u, fabsf(m[nt][0]) > 0x1p17f || fabsf(m[nt][1]) > 0x1p17f)) {
+#pragma unroll
+                        for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sc[mt][nt][i] = __fmul_rn(sc[mt][nt][i], unit[i & 1]) - base[i & 1];
+                        unit[0] = unit[1] = 1.f;
+                        low[0] = low[1] = -C::UP;
+                    }
 #pragma unroll
                     for (int mt = 0; mt < C::MT; ++mt) {
                         float w[4];

@@ -95,3 +95,31 @@ def test_caps_of_any_size(cap, dt):
             L = torch.logsumexp(s, 1)
             assert_close(lse[b, 4 * h:4 * h + 4], L, es[:, 0] + 2.0 ** -21 + n * 2.0 ** -24 + 8 * 2.0 ** -24 * L.abs(),
                          f"lse {b} {h}")
+
+
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("times", [2.0 ** 20, 2.0 ** 40, 2.0 ** 90])
+def test_scores_of_any_finite_size(times, dt):
+    """Where the distance between two scores is far past the exponential's range, the
+    position with the largest takes all."""
+    c = Case([1, 90, 513], 4, 2, 64, 16, dt, seed=23)
+    c.q *= times
+    with c.handle() as kv:
+        out, lse = c.run(kv)
+        assert kv.health() == (0, 0)
+    compared = 0
+    for b, n in enumerate(c.lens):
+        for h in range(4):
+            k, v = (_decoder_ref.gather(x, c.table, b, 0, n, h // 2) * (1.0 if sc is None else float(sc[h // 2]))
+                    for x, sc in ((c.k, c.scales[0]), (c.v, c.scales[1])))
+            q = c.q[b, h].cpu().double()
+            s = k @ q * c.scale
+            # fp32 scores of 64 terms, their scale and the conversion to base two
+            es = (64 + 6) * 2.0 ** -24 * float((k.abs() @ q.abs()).max() * c.scale)
+            assert abs(float(lse[b, h]) - float(s.max())) <= es + 2.0 ** -20 * abs(float(s.max()))
+            top = s.sort(descending=True).values
+            if n == 1 or float(top[0] - top[1]) > 2 * es + 40:
+                one = v[int(s.argmax())]
+                assert_close(out[b, h], one, rounded(one, 2.0 ** -10 * one.abs(), BF16), f"out {b} {h}")
+                compared += 1
+    assert compared >= 10
