@@ -592,6 +592,7 @@ typedef struct {
  * sequence, the new one included. Query head i reads key-value head
  * i / (n_heads / n_kv_heads).
  *   s_j = scale * q . k_j;  softcap > 0: s_j = softcap * tanh(s_j / softcap)
+ *     (a softcap of 2^80 or more counts as none)
  *   window > 0: only j >= len - window
  *   out = sum_j softmax(s)_j v_j: device bf16 [B][n_heads][head_dim] contiguous
  *   lse = log(sum_j exp(s_j)): device fp32 [B][n_heads], or NULL

@@ -453,9 +453,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ---- segments ------------------------------------------------------------------
         int take = 0;                    // the stage to be consumed next, and its barrier's phase
         uint32_t phase = 0;
-        // the cap in base two; one above 2^80 bends no score below 2^67, and its reciprocal would
-        // lose bits
-        const float cap2 = fminf(fmaxf(p.a.softcap * kLog2e, 1.2e-38f), 0x1p80f);
+        const float cap2 = fmaxf(p.a.softcap * kLog2e, 1.2e-38f);   // the cap in base two
         auto next_stage = [&]() {        // waits for it; the stage's shared address
             bw::mbar_wait(bw::saddr(&sm_bar[warp][take]), phase, &sm_abort, p.health, MOE_KV_TIMEOUT);
             __syncwarp();
@@ -1024,8 +1022,10 @@ moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t str
     while (K.box_rows << boxes_log2 < ct) ++boxes_log2;
     while (1 << page_log2 < K.s.page_size) ++page_log2;
     if (1 << page_log2 != K.s.page_size) page_log2 = -1;
-    const AttendArgs p{a,         K.s,        K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml,          K.arrived,
+    AttendArgs p{a,         K.s,        K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml,          K.arrived,
                        K.box_rows, boxes_log2, page_log2, G,         tiles,    K.s.n_kv_heads * tiles};
+    // changes no score below 2^68, and a score's share of it would lose bits
+    if (p.a.softcap >= 0x1p80f) p.a.softcap = 0.f;
     // the kernel counts chunks in 32 bits
     if (((int64_t)a.max_pages * K.s.page_size / ct + 1) * a.B * p.HT > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "the block table spans more chunks than 2^31");
     const cudaError_t e = pick(K.s, [&](auto c) { return launch<decltype(c)>(K, p, stream); });

@@ -98,6 +98,21 @@ def test_caps_of_any_size(cap, dt):
 
 
 @pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("cap,times", [(1e30, 2.0 ** 85), (3e38, 2.0 ** 60), (1e24, 2.0 ** 60)])
+def test_caps_above_large_scores(cap, times, dt):
+    """Of one token the log-sum-exp is its score."""
+    c = Case([1, 1, 1, 1], 4, 2, 64, 16, dt, seed=25)
+    c.q *= times
+    out, lse = c.check(softcap=0.0)
+    with c.handle() as kv:
+        out2, lse2 = c.run(kv, softcap=cap)
+        assert kv.health() == (0, 0)
+    # the scores are below cap / 2^10, the cap takes 2^-20 / 3 off them, in 12 operations more
+    assert float(lse.abs().max()) < cap * 2.0 ** -10
+    assert torch.all((lse - lse2).abs() <= (2.0 ** -21 + 24 * 2.0 ** -24) * lse.abs()) and torch.equal(out, out2)
+
+
+@pytest.mark.parametrize("dt", [BF16, E4M3])
 @pytest.mark.parametrize("times", [2.0 ** 20, 2.0 ** 40, 2.0 ** 90])
 def test_scores_of_any_finite_size(times, dt):
     """Where the distance between two scores is far past the exponential's range, the
