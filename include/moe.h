@@ -660,9 +660,18 @@ enum {
     MOE_KV_BAD_SEQ = 1,     /* append: a sequence index outside block_table */
     MOE_KV_BAD_LENGTH = 2,  /* a position or length past max_pages * page_size */
     MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
-    MOE_KV_TIMEOUT = 8      /* a bounded wait inside moe_kv_attend ran out */
+    MOE_KV_TIMEOUT = 8      /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
+                               out and lse whose cache did not arrive are NaN */
 };
 moe_status moe_kv_health(moe_kv* kv, uint32_t* bits);
+
+/* Options of a handle. */
+enum {
+    /* Test hook: moe_kv_attend starts no copies of this sequence's cache (-1,
+     * the default: none is left out), so that the waits for them run out. */
+    MOE_KV_OPT_TEST_STALL = 1
+};
+moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value);
 
 /* ---- errors ----------------------------------------------------------------- */
 

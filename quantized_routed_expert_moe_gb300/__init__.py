@@ -34,7 +34,7 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_expert_record_bytes", "
            "moe_decode_tokens_host", "moe_cache_stage", "moe_cache_prefetch", "moe_cache_prefetch_stats", "moe_cache_stats", "moe_cache_residency", "moe_cache_usage", "moe_cache_pin", "moe_hottest", "moe_cache_pin_hottest", "moe_lfu_trace", "moe_lfu_trace_pinned",
            "moe_profile_start", "moe_profile_stop", "moe_layer_set_option", "moe_layer_check", "moe_trace_read_split",
            "moe_block_norm", "moe_block_norm_check", "moe_kv_create", "moe_kv_destroy", "moe_kv_device_bytes", "moe_kv_append", "moe_kv_attend",
-           "moe_kv_append_check", "moe_kv_attend_check", "moe_kv_locate", "moe_kv_health",
+           "moe_kv_append_check", "moe_kv_attend_check", "moe_kv_locate", "moe_kv_health", "moe_kv_set_option",
            "moe_status_str", "moe_last_error")
 
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
@@ -43,6 +43,7 @@ MOE_OPT_TEST_STALL_SHARED, MOE_OPT_TRACE = 2, 3
 MOE_OPT_HOST_TIMEOUT_MS, MOE_OPT_TEST_STALL_COPIES_MS, MOE_OPT_CACHE_DEVICE = 4, 5, 6
 MOE_MAX_TOP_K = 8
 MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT = 1, 2, 4, 8
+MOE_KV_OPT_TEST_STALL = 1
 
 
 class MoEError(RuntimeError):
@@ -212,6 +213,8 @@ def lib() -> ctypes.CDLL:
                                         ctypes.POINTER(ctypes.c_uint32)]
             L.moe_kv_health.restype = st
             L.moe_kv_health.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
+            L.moe_kv_set_option.restype = st
+            L.moe_kv_set_option.argtypes = [vp, i32, ctypes.c_int64]
             L.moe_status_str.restype = ctypes.c_char_p
             L.moe_status_str.argtypes = [st]
             L.moe_last_error.restype = ctypes.c_char_p
@@ -544,6 +547,10 @@ def moe_kv_health(handle) -> tuple[int, int]:
     bits = ctypes.c_uint32()
     st = lib().moe_kv_health(handle, ctypes.byref(bits))
     return st, bits.value
+
+
+def moe_kv_set_option(handle, option: int, value: int) -> None:
+    _check(lib().moe_kv_set_option(handle, option, value), "moe_kv_set_option")
 
 
 MOE_TRACE_MAX_CTAS = 1024
@@ -894,6 +901,9 @@ class KVCache:
 
     def health(self):
         return moe_kv_health(self.handle)
+
+    def set_option(self, option: int, value: int):
+        moe_kv_set_option(self.handle, option, value)
 
     @property
     def device_bytes(self):

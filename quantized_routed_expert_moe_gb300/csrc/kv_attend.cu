@@ -104,6 +104,7 @@ struct AttendArgs {
     int boxes_log2;     // boxes of a chunk's column block
     int page_log2;      // of page_size, -1 where it is no power of two
     int G, tiles, HT;   // query heads of a key-value head; head tiles of one, and of all
+    int stall;          // MOE_KV_OPT_TEST_STALL
 };
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t addr) {
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 sm_rows[warp][put] = rows;
             }
             __syncwarp();
-            if (nx_page >= 0)
+            if (nx_page >= 0 && nx.b != p.stall)
                 tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
                             nx.hk, nx_page, bar, pol);
             if (++put == C::STAGES) put = 0;
@@ -454,9 +455,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int take = 0;                    // the stage to be consumed next, and its barrier's phase
         uint32_t phase = 0;
         const float cap2 = fmaxf(p.a.softcap * kLog2e, 1.2e-38f);   // the cap in base two
+        int stop = 1;                    // end of the segment's chunks; 0 once a copy did not arrive in time
         auto next_stage = [&]() {        // waits for it; the stage's shared address
-            bw::mbar_wait(bw::saddr(&sm_bar[warp][take]), phase, &sm_abort, p.health, MOE_KV_TIMEOUT);
-            __syncwarp();
+            const bool here = bw::mbar_wait(bw::saddr(&sm_bar[warp][take]), phase, &sm_abort, p.health, MOE_KV_TIMEOUT);
+            if (!__all_sync(~0u, here)) {
+                stop = 0;
+                nx_live = false;         // no further copy is started
+            }
             return ring + take * C::HALF;
         };
         auto release = [&]() {           // every lane has read it: fill it again
@@ -552,7 +557,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int i = 0; i < 4; ++i) o[dt][nt][i] = 0.f;
             }
 
-            for (; cur < seg_end; ++cur) {
+            if (stop) stop = seg_end;
+            for (; cur < stop; ++cur) {
                 const int tok0 = (first / CT + cur - at.beg) * CT;
                 const uint32_t rows = sm_rows[warp][take];
                 const uint32_t kt = next_stage();
@@ -731,6 +737,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 release();
             }
 
+            // Without its copies the warp goes through the ends of its segments all the same, so that
+            // nothing waits for it, and what it had a part in becomes NaN.
+            cur = seg_end;
+            if (!stop)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) l[nt][0] = l[nt][1] = NAN;
+
             // ---- the segment's end ----------------------------------------------------------
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -741,6 +754,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     l[nt][c] += __shfl_xor_sync(~0u, l[nt][c], 16);
                 }
             const bool last = at.end >= w1;
+            // no copy may land in the rings once the warps have met: every stage's last fill is waited for
+            if (last && !stop) {
+                int own = 0;
+                for (int i = 0; i < C::STAGES && i < issued; ++i)
+                    bw::mbar_wait(bw::saddr(&sm_bar[warp][i]), (issued - 1 - i) / C::STAGES & 1, &own, nullptr, 0);
+                __syncwarp();
+            }
             // A segment that is cut between warps is joined by the first of them, which
             // holds its own part in registers; the others set theirs aside.
             const bool theirs = at.beg < w0 && w0 != u0;
@@ -1022,8 +1042,8 @@ moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t str
     while (K.box_rows << boxes_log2 < ct) ++boxes_log2;
     while (1 << page_log2 < K.s.page_size) ++page_log2;
     if (1 << page_log2 != K.s.page_size) page_log2 = -1;
-    AttendArgs p{a,         K.s,        K.k_scale, K.v_scale, K.health, K.part_o, K.part_ml,          K.arrived,
-                       K.box_rows, boxes_log2, page_log2, G,         tiles,    K.s.n_kv_heads * tiles};
+    AttendArgs p{a,         K.s,        K.k_scale, K.v_scale, K.health, K.part_o,               K.part_ml, K.arrived,
+                 K.box_rows, boxes_log2, page_log2, G,         tiles,    K.s.n_kv_heads * tiles, K.stall};
     // changes no score below 2^68, and a score's share of it would lose bits
     if (p.a.softcap >= 0x1p80f) p.a.softcap = 0.f;
     // the kernel counts chunks in 32 bits

@@ -514,6 +514,14 @@ moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* strea
     return kv_attend_launch(K, *args, static_cast<cudaStream_t>(stream));
 }
 
+moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    if (option != MOE_KV_OPT_TEST_STALL) return fail(MOE_E_INVALID, "unknown option");
+    if (value < -1 || value >= kv->K.d.max_batch) return fail(MOE_E_INVALID, "a sequence, or -1 for none");
+    kv->K.stall = (int)value;
+    return MOE_OK;
+}
+
 moe_status moe_kv_health(moe_kv* kv, uint32_t* bits) {
     if (!kv) return fail(MOE_E_INVALID, "NULL handle");
     DeviceGuard g(kv->K.device);

@@ -54,6 +54,7 @@ struct Kv {
     // CTAs, and how many of a segment's CTAs have arrived
     CUtensorMap tm_k{}, tm_v{};
     int box_rows = 16;
+    int stall = -1;              // MOE_KV_OPT_TEST_STALL
     float4 *part_o = nullptr, *part_ml = nullptr;
     int* arrived = nullptr;
     void* block = nullptr;       // the allocation that holds all of the above

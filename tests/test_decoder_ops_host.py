@@ -222,3 +222,7 @@ def test_bad_norm_descriptors(kw, status):
     dict(r=P + 8), dict(h=P + 1)])
 def test_bad_norm_arguments(kw):
     refused(moe.moe_block_norm_check, norm_desc(), *norm_args(**kw))
+
+
+def test_options_need_a_handle():
+    refused(moe.moe_kv_set_option, None, moe.MOE_KV_OPT_TEST_STALL, 0)
