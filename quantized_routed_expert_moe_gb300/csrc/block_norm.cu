@@ -7,6 +7,7 @@
 
 #include "common.cuh"
 #include "moe_internal.h"
+#include "per_device.h"
 
 namespace moe {
 
@@ -55,6 +56,7 @@ struct NormArgs {
     void *r, *h;
     int T;
     bool near;   // the weights are in shared memory
+    int device;
 };
 
 // A row is cut into tiles of 256 channels; a lane holds channels 4 lane.. and 128 +
@@ -284,17 +286,18 @@ __global__ void __launch_bounds__(MAXT, MINB) k_block_norm(const NormArgs p) {
     }
 }
 
-// CTAs of a kernel that the device holds at a time; `held` caches it.
-cudaError_t resident(const void* kernel, int threads, size_t smem, int& held) {
-    if (held) return cudaSuccess;
-    int dev = 0, sms = 0, n = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess && smem)
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
-    if (e == cudaSuccess) held = sms * (n > 0 ? n : 1);
-    return e;
+// CTAs of a kernel that the device holds at a time, 0 with `e` set on failure. `held` keeps it;
+// the attribute counts for the current device alone.
+int resident(const void* kernel, int threads, size_t smem, int device, PerDevice& held, cudaError_t& e) {
+    e = cudaSuccess;
+    return held.get(device, [&] {
+        int sms = 0, n = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
+        if (e == cudaSuccess && smem)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSlotBytes);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, smem);
+        return e == cudaSuccess ? sms * (n > 0 ? n : 1) : 0;
+    });
 }
 
 // Few rows: each has a CTA or a warp of its own. Returns whether the device holds them all.
@@ -302,10 +305,10 @@ template <typename R, typename B, typename O, int K, bool CTA, int MAXT, int MIN
 bool launch_few(const NormArgs& p, int threads, cudaStream_t s, cudaError_t& e) {
     const auto kernel = k_block_norm<R, B, O, K, CTA, false, MAXT, MINB>;
     const int per = CTA ? 1 : threads / 32, need = (p.T - 1) / per + 1;
-    static int held[33];       // by warps of a CTA
-    e = resident(reinterpret_cast<const void*>(kernel), threads, 0, held[threads / 32]);
-    if (e != cudaSuccess) return true;
-    if (need > held[threads / 32]) return false;
+    static PerDevice kept[33];       // by warps of a CTA
+    const int held = resident(reinterpret_cast<const void*>(kernel), threads, 0, p.device, kept[threads / 32], e);
+    if (!held) return true;
+    if (need > held) return false;
     e = launch_pdl(kernel, dim3(need), dim3(threads), 0, s, true, p);
     return true;
 }
@@ -322,10 +325,11 @@ cudaError_t launch_many(NormArgs p, int threads, cudaStream_t s) {
     const size_t weights = (size_t)(CTA ? threads : 32) * 2 * K * 16 * kept;
     p.near = stage + weights <= kSlotBytes;
     const size_t smem = stage + (p.near ? weights : 0);
-    static int kinds[33][2][3];   // the same warps, inputs and weights take the same shared memory
-    int& held = kinds[threads / 32][inputs - 1][kept];
-    const cudaError_t e = resident(reinterpret_cast<const void*>(kernel), threads, smem, held);
-    if (e != cudaSuccess) return e;
+    static PerDevice kinds[33][2][3];   // the same warps, inputs and weights take the same shared memory
+    cudaError_t e;
+    const int held = resident(reinterpret_cast<const void*>(kernel), threads, smem, p.device,
+                              kinds[threads / 32][inputs - 1][kept], e);
+    if (!held) return e;
     return launch_pdl(kernel, dim3(need < held ? need : held), dim3(threads), smem, s, true, p);
 }
 
@@ -385,7 +389,7 @@ moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const 
     if (st != MOE_OK || T == 0) return st;
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, true};
+    const NormArgs p{*desc, x, o, gate, w_post, w_pre, r, h, T, true, device};
     const cudaError_t e = launch(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "block norm launch");
 }
