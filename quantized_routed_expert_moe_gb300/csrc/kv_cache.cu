@@ -532,6 +532,7 @@ moe_status moe_kv_health(moe_kv* kv, uint32_t* bits) {
     if (bits) *bits = v;
     if (!v) return MOE_OK;
     MOE_CUDA_TRY(cudaMemset(kv->K.health, 0, 4));
+    MOE_CUDA_TRY(cudaDeviceSynchronize());   // before any stream's next call may set a bit
     if (v & MOE_KV_TIMEOUT) return fail(MOE_E_TIMEOUT, "a bounded device-side wait gave up (health bits " + std::to_string(v) + ")");
     return fail(MOE_E_STATE, "kernels refused part of their work (health bits " + std::to_string(v) + ")");
 }
