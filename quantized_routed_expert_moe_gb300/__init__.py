@@ -10,7 +10,9 @@ Functions keep the C names (``moe_layer_create``, ``moe_route``,
 ``data_ptr()``), a numpy array, a raw integer address or None.
 
 ``MoELayer``, ``BlockNorm`` and ``KVCache`` own a handle or weights and take
-tensors; the latter two check shapes, types and devices before a call.
+tensors; the latter two check shapes, types and devices before a call, and run on
+torch's current stream where none is given. Elsewhere stream=None is the legacy
+default stream, as in C.
 """
 from __future__ import annotations
 
@@ -726,11 +728,12 @@ class BlockNorm:
         self._buf_addr = ctypes.addressof(self._buf)
         vp, i32 = ctypes.c_void_p, ctypes.c_int32
         self._call = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 8, i32, i32, vp)(("moe_block_norm", lib()))
+        self._current_stream = torch.cuda.current_stream
 
     def run(self, x, o=None, r=None, h=None, gate=None, stream=None):
         """x [T, H] residual, o [T, H] the block's output or None, r [T, H]
         (may be x) and h [T, H] the outputs (either may be None), gate [T, H],
-        [1, H] or [H] of o's type."""
+        [1, H] or [H] of o's type. stream: torch's current one on x's device by default."""
         ids, H, dev = self._ids, self.hidden, x.get_device()
         shape, res = x.shape, x.dtype
         if len(shape) != 2 or shape[1] != H or res not in ids or dev < 0 or self.device not in (None, dev):
@@ -764,6 +767,8 @@ class BlockNorm:
             gp = gate.data_ptr()
         self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, H, ids[res], ids[blk], ids[out], self.eps, self.scale,
                              self.weight_offset, xs, os_, gs, rs, hs)
+        if stream is None:
+            stream = self._current_stream(dev)
         st = self._call(self._buf_addr, x.data_ptr(), op, gp, wp, wn, rp, hp, shape[0], dev,
                         stream.cuda_stream if hasattr(stream, "cuda_stream") else _stream(stream))
         if st:
@@ -812,6 +817,7 @@ class KVCache:
         proto = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
         self._append_call = proto(("moe_kv_append", lib()))
         self._attend_call = proto(("moe_kv_attend", lib()))
+        self._current_stream = torch.cuda.current_stream
 
     def close(self):
         if getattr(self, "handle", None):
@@ -833,7 +839,7 @@ class KVCache:
     def append(self, q, k, v, positions, block_table, q_out=None, seq=None, stream=None):
         """Rotate and cache T tokens: q [T, n_heads, d] (or None with q_out), k
         and v [T, n_kv_heads, d], positions and seq int32 [T], block_table int32
-        [n_seqs, max_pages]."""
+        [n_seqs, max_pages]. stream: torch's current one on the pools' device by default."""
         hq, hk, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
         shape, table = k.shape, block_table.shape
@@ -861,6 +867,8 @@ class KVCache:
             sp = _dense(seq, "seq", (T,), i32, dev)
         self._append_args.pack_into(self._buf, 0, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, positions.data_ptr(), sp,
                                     block_table.data_ptr(), T, table[0], table[1], op)
+        if stream is None:
+            stream = self._current_stream(dev)
         st = self._append_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
                                else _stream(stream))
         if st:
@@ -870,7 +878,8 @@ class KVCache:
                stream=None):
         """Attention of one new token per sequence: q and out [B, n_heads, d]
         bf16, lens int32 [B], block_table int32 [B, max_pages], lse fp32
-        [B, n_heads] or None; scale defaults to 1 / sqrt(d)."""
+        [B, n_heads] or None; scale defaults to 1 / sqrt(d). stream: torch's current one on the
+        pools' device by default."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
         shape, table = q.shape, block_table.shape
@@ -890,6 +899,8 @@ class KVCache:
             self._buf, 0, q.data_ptr(), _token_stride(q, "q", B, hq, d), block_table.data_ptr(), lens.data_ptr(), B,
             table[1], d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
             0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
+        if stream is None:
+            stream = self._current_stream(dev)
         st = self._attend_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
                                else _stream(stream))
         if st:
