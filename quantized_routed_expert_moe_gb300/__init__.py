@@ -712,17 +712,8 @@ class BlockNorm:
                  weight_offset: float = 0.0):
         import torch
         self.hidden, self.eps, self.scale, self.weight_offset = hidden, eps, scale, weight_offset
-        self.device = None
-        for name, w in (("w_post", w_post), ("w_pre", w_pre)):
-            if w is None:
-                continue
-            _dense(w, name, (hidden,), torch.float32, w.get_device())
-            if self.device not in (None, w.get_device()):
-                raise ValueError("w_post and w_pre are on two devices")
-            self.device = w.get_device()
-        self.w_post, self.w_pre = w_post, w_pre   # kept: the calls take their addresses
-        self._post = None if w_post is None else w_post.data_ptr()
-        self._pre = None if w_pre is None else w_pre.data_ptr()
+        self.w_post, self.w_pre, self._f32 = w_post, w_pre, torch.float32
+        self._bind(next((w.get_device() for w in (w_post, w_pre) if w is not None), None))
         self._ids = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
         self._buf = ctypes.create_string_buffer(ctypes.sizeof(moe_block_norm_desc))
         self._buf_addr = ctypes.addressof(self._buf)
@@ -730,14 +721,29 @@ class BlockNorm:
         self._call = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 8, i32, i32, vp)(("moe_block_norm", lib()))
         self._current_stream = torch.cuda.current_stream
 
+    def _bind(self, device):
+        """Take the weights' addresses. They hold while the aliases keep that memory from other
+        use, so that a call only looks whether an address is still the weight's (moving a module
+        gives its weights new memory)."""
+        at = []
+        for name, w in (("w_post", self.w_post), ("w_pre", self.w_pre)):
+            at.append((w, None if w is None else w.detach(),
+                       None if w is None else _dense(w, name, (self.hidden,), self._f32, device)))
+        (self._post_of, self._post_alias, self._post), (self._pre_of, self._pre_alias, self._pre) = at
+        self.device = device
+
     def run(self, x, o=None, r=None, h=None, gate=None, stream=None):
         """x [T, H] residual, o [T, H] the block's output or None, r [T, H]
         (may be x) and h [T, H] the outputs (either may be None), gate [T, H],
         [1, H] or [H] of o's type. stream: torch's current one on x's device by default."""
         ids, H, dev = self._ids, self.hidden, x.get_device()
         shape, res = x.shape, x.dtype
-        if len(shape) != 2 or shape[1] != H or res not in ids or dev < 0 or self.device not in (None, dev):
-            raise ValueError("x must be a float32 or bfloat16 CUDA tensor [T, hidden] on the weights' device")
+        if len(shape) != 2 or shape[1] != H or res not in ids or dev < 0:
+            raise ValueError("x must be a float32 or bfloat16 CUDA tensor [T, hidden]")
+        post, pre = self.w_post, self.w_pre
+        if (post is not self._post_of or pre is not self._pre_of or (post is not None and post.data_ptr() != self._post)
+                or (pre is not None and pre.data_ptr() != self._pre) or self.device != dev):
+            self._bind(dev)
         blk = res if o is None else o.dtype
         out = res if h is None else h.dtype
         if blk not in ids or out not in ids:
