@@ -784,7 +784,8 @@ class BlockNorm:
 class KVCache:
     """Owns one cache handle over two page pools, tensors [n_pages, n_kv_heads,
     page_size, head_dim] of bfloat16 or float8_e4m3fn in any memory order whose
-    last dimension is contiguous (token-major pages: a permuted view)."""
+    last dimension is contiguous (token-major pages: a permuted view). The handle is
+    bound to the pools' memory: pools that get new memory need a new object."""
 
     # moe_kv_append_args and moe_kv_attend_args, packed in place
     _append_args = struct.Struct("PPPqqqPPPiiiP")
@@ -810,6 +811,7 @@ class KVCache:
             if s is not None and s.shape != (hk,):
                 raise ValueError("k_scale and v_scale hold one value per key-value head")
         self.k_pages, self.v_pages = k_pages, v_pages
+        self._pools_at = (k_pages.data_ptr(), v_pages.data_ptr())
         self.device = k_pages.get_device()
         self.desc = moe_kv_desc(MOE_ABI_VERSION, n_heads, hk, d, page, n_pages, kinds[k_pages.dtype],
                                 0 if freq is None else 2 * freq.size, int(interleaved), max_batch,
@@ -842,12 +844,17 @@ class KVCache:
     def __exit__(self, *a):
         self.close()
 
+    def _pools_moved(self):
+        raise ValueError("k_pages or v_pages has new memory: the handle is bound to that of its construction")
+
     def append(self, q, k, v, positions, block_table, q_out=None, seq=None, stream=None):
         """Rotate and cache T tokens: q [T, n_heads, d] (or None with q_out), k
         and v [T, n_kv_heads, d], positions and seq int32 [T], block_table int32
         [n_seqs, max_pages]. stream: torch's current one on the pools' device by default."""
         hq, hk, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
+        if (self.k_pages.data_ptr(), self.v_pages.data_ptr()) != self._pools_at:
+            self._pools_moved()
         shape, table = k.shape, block_table.shape
         T = shape[0]
         # one condition for what almost every call passes; the refusals are worked out after it
@@ -888,6 +895,8 @@ class KVCache:
         pools' device by default."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
+        if (self.k_pages.data_ptr(), self.v_pages.data_ptr()) != self._pools_at:
+            self._pools_moved()
         shape, table = q.shape, block_table.shape
         B = shape[0]
         if not (shape == (B, hq, d) and out.shape == shape and lens.shape == (B,) and len(table) == 2 and table[0] == B

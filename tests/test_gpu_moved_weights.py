@@ -1,4 +1,4 @@
-"""Weights that get new memory after an object has been made over them."""
+"""Weights and pools that get new memory after an object has been made over them."""
 import pytest
 import torch
 
@@ -38,3 +38,22 @@ def test_the_norm_refuses_what_they_became(which, to):
     setattr(n, which, to(w))
     with pytest.raises(ValueError, match=which):
         n.run(x, o, torch.empty_like(x), torch.empty_like(o))
+
+
+def test_the_cache_refuses_pools_with_new_memory():
+    kp, vp = (torch.nn.Parameter(torch.zeros(3, 2, 16, 64, device="cuda", dtype=BF16), requires_grad=False)
+              for _ in range(2))
+    k, q = torch.randn(1, 2, 64, device="cuda").to(BF16), torch.randn(1, 4, 64, device="cuda").to(BF16)
+    pos, table = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((1,), (1, 1)))
+    for pool in (kp, vp):
+        with moe.KVCache(kp, vp, n_heads=4) as kv:
+            kv.append(None, k, k, pos, table)
+            torch.cuda.synchronize()
+            old, pool.data = pool.data, torch.zeros_like(pool)
+            with pytest.raises(ValueError, match="new memory"):
+                kv.append(None, k, k, pos, table)
+            with pytest.raises(ValueError, match="new memory"):
+                kv.attend(q, table, pos + 1, torch.empty_like(q))
+            pool.data = old
+            kv.attend(q, table, pos + 1, torch.empty_like(q))
+            assert kv.health() == (0, 0)
