@@ -598,7 +598,9 @@ typedef struct {
  *   lse = log(sum_j exp(s_j)): device fp32 [B][n_heads], or NULL
  * A sequence of length <= 0 gives out = 0 and lse = -inf. Slots at or past the
  * length (or before the window) may hold anything, NaN included; table entries of
- * pages that hold no attended position are not read as pages. */
+ * pages that hold no attended position are not read as pages.
+ * MOE_E_UNSUPPORTED: max_pages * page_size tokens of B sequences and all key-value
+ * heads (and of every 16 query heads on one) are 2^31 chunks of 8 KB of keys or more. */
 typedef struct {
     const void* q;
     int64_t q_stride;

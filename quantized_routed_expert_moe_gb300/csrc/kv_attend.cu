@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // + 0.045 c / S, least at sqrt(6 total S). One sequence of 40189 tokens in 8 bits, 12
     // heads over 1 of 128 (16 fragments): 19.4 us, by the rule for 8 21.6. (Each CTA has
     // some chunks: a segment's CTAs are consecutive.)
-    const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_launch
+    const int total = sm_pre[B] * HT;   // below 2^31: kv_attend_countable
     int ctas = min((int)gridDim.x, (total + kWarps - 1) / kWarps);
     const float sq = 48.f / max(8, C::FRAGS) * total * ((float)B * HT);
     if (sq < (float)ctas * ctas) ctas = (int)ceilf(sqrtf(sq));
@@ -1033,6 +1033,13 @@ cudaError_t kv_attend_setup(Kv& K) {
     });
 }
 
+bool kv_attend_countable(const KvShape& s, int B, int max_pages) {
+    const int G = s.n_heads / s.n_kv_heads;
+    const int ct = pick(s, [](auto c) { return decltype(c)::CT; });
+    const int heads = pick(s, [](auto c) { return decltype(c)::HEADS; });
+    return ((int64_t)max_pages * s.page_size / ct + 1) * B * s.n_kv_heads * ((G + heads - 1) / heads) <= INT32_MAX;
+}
+
 moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t stream) {
     const int G = K.s.n_heads / K.s.n_kv_heads;
     const int ct = pick(K.s, [](auto c) { return decltype(c)::CT; });
@@ -1046,8 +1053,6 @@ moe_status kv_attend_launch(Kv& K, const moe_kv_attend_args& a, cudaStream_t str
                  K.box_rows, boxes_log2, page_log2, G,         tiles,    K.s.n_kv_heads * tiles, K.stall};
     // changes no score below 2^68, and a score's share of it would lose bits
     if (p.a.softcap >= 0x1p80f) p.a.softcap = 0.f;
-    // the kernel counts chunks in 32 bits
-    if (((int64_t)a.max_pages * K.s.page_size / ct + 1) * a.B * p.HT > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "the block table spans more chunks than 2^31");
     const cudaError_t e = pick(K.s, [&](auto c) { return launch<decltype(c)>(K, p, stream); });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend launch");
 }

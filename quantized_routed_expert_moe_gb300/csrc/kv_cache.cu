@@ -115,6 +115,8 @@ moe_status check_attend(const moe_kv_desc* d, const moe_kv_attend_args* a) {
     if (!aligned16(a->q) || !aligned16(a->out)) return fail(MOE_E_INVALID, "q and out must be 16-byte aligned");
     if (a->q_stride % 8 || a->q_stride < (int64_t)d->head_dim * d->n_heads)
         return fail(MOE_E_INVALID, "q_stride must be a multiple of 8 and cover the heads");
+    if (!kv_attend_countable(shape_of(*d), a->B, a->max_pages))
+        return fail(MOE_E_UNSUPPORTED, "the block table spans 2^31 chunks or more");
     return MOE_OK;
 }
 

@@ -64,6 +64,8 @@ struct Kv {
 // Bytes of part_o, part_ml and arrived; needs K.d, K.s and K.num_sms.
 size_t kv_attend_workspace(const Kv& K, size_t out[3]);
 cudaError_t kv_attend_setup(Kv& K);
+// Whether the kernel's 32 bits count the chunks of B full rows of a block table.
+bool kv_attend_countable(const KvShape& s, int B, int max_pages);
 moe_status kv_attend_launch(Kv& kv, const moe_kv_attend_args& a, cudaStream_t s);
 
 }  // namespace moe

@@ -226,3 +226,18 @@ def test_bad_norm_arguments(kw):
 
 def test_options_need_a_handle():
     refused(moe.moe_kv_set_option, None, moe.MOE_KV_OPT_TEST_STALL, 0)
+
+
+# 256 key-value heads of 256 in bf16 (16 tokens to a chunk), 1024 sequences: 8192 chunks each are one too many
+@pytest.mark.parametrize("kw,pages,fits", [
+    (dict(n_heads=256, n_kv_heads=256, head_dim=256, head_stride=16 * 256, token_stride=256, page_stride=2 ** 20), 8190, True),
+    (dict(n_heads=256, n_kv_heads=256, head_dim=256, head_stride=16 * 256, token_stride=256, page_stride=2 ** 20), 8191, False),
+    (dict(n_heads=4096, n_kv_heads=1, head_dim=64, head_stride=16 * 64, token_stride=64, page_stride=1024), 4 * 8190, True),
+    (dict(n_heads=4096, n_kv_heads=1, head_dim=64, head_stride=16 * 64, token_stride=64, page_stride=1024), 4 * 8191, False)])
+def test_tables_of_more_chunks_than_the_kernel_counts(kw, pages, fits):
+    d = kv_desc(rotary_dim=0, max_batch=1024, n_pages=4, **kw)
+    a = attend_args(B=1024, max_pages=pages, q_stride=kw["n_heads"] * kw["head_dim"])
+    if fits:
+        moe.moe_kv_attend_check(d, a)
+    else:
+        refused(moe.moe_kv_attend_check, d, a, status=2)
