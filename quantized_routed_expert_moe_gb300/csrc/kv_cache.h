@@ -49,6 +49,7 @@ struct Kv {
     void *k_pages = nullptr, *v_pages = nullptr;
     uint64_t* turns = nullptr;   // [rotary_dim / 2] turns per position, as a fraction of 2^64
     float *k_scale = nullptr, *v_scale = nullptr;  // [n_kv_heads], ones for a bf16 cache
+    float2* scales = nullptr;    // [2][n_kv_heads], as append takes them: scale and its rounded reciprocal
     unsigned* health = nullptr;
     // attention: the page pools as tensor maps, the parts of segments that are cut between
     // CTAs, and how many of a segment's CTAs have arrived
