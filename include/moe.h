@@ -544,7 +544,8 @@ moe_status moe_block_norm_check(const moe_block_norm_desc* desc, const void* x, 
 /* Keys and values of one attention layer in pages of page_size tokens. Both
  * pools hold n_pages pages; element (page, kv head, slot, d) is at
  * page * page_stride + head * head_stride + slot * token_stride + d, so that
- * head-major and token-major pages are both expressed. A sequence's position p
+ * head-major and token-major pages are expressed, and pools whose heads or slots
+ * are outermost. A sequence's position p
  * lives in slot p % page_size of page block_table[seq][p / page_size].
  * Attention and its cache are context in the pages (Inferno README, "Memory
  * Strategy"; TurboFieldfare article, "token generation": exact split-K/V decode
@@ -560,8 +561,9 @@ typedef struct {
     int32_t rotary_dim;       /* leading channels of a head that are rotated: 0 or a multiple of 16, <= head_dim */
     int32_t rotary_adjacent;  /* 0: channel i pairs with i + rotary_dim / 2; 1: channel 2i with 2i + 1 */
     int32_t max_batch;        /* largest B of moe_kv_attend, 1..1024 */
-    int64_t page_stride, head_stride, token_stride; /* elements; multiples of 16 bytes; each pool's rows
-                                 [head_dim] must not overlap */
+    int64_t page_stride, head_stride, token_stride; /* elements; multiples of 16 bytes, in any order of size;
+                                 each pool's rows [head_dim] must not overlap (the stride of a dimension of
+                                 one is not looked at) */
 } moe_kv_desc;
 
 typedef struct moe_kv moe_kv;

@@ -5,6 +5,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <iterator>
 #include <new>
 #include <string>
 
@@ -35,20 +36,18 @@ moe_status check_desc(const moe_kv_desc* d) {
         return fail(MOE_E_INVALID, "rotary_dim must be 0 or a multiple of 16, at most head_dim");
     if (d->rotary_adjacent != 0 && d->rotary_adjacent != 1) return fail(MOE_E_INVALID, "rotary_adjacent must be 0 or 1");
     if (d->max_batch < 1 || d->max_batch > 1024) return fail(MOE_E_INVALID, "max_batch must be in 1..1024");
-    // the rows of a page, in either order, without overlap: the smaller of the
-    // two inner strides steps over rows, the larger over all of the smaller's
+    // The rows of a pool in any order of its three dimensions, without overlap: from the smallest
+    // stride up, each steps over all that the ones below it span. One row needs no step.
     const int64_t step = d->cache_dtype == MOE_E4M3 ? 16 : 8;
-    const int64_t D = d->head_dim, H = d->n_kv_heads, P = d->page_size;
-    for (int64_t st : {d->page_stride, d->head_stride, d->token_stride})
-        if (st < D || st % step || st > ((int64_t)1 << 38))
-            return fail(MOE_E_INVALID, "strides must be multiples of 16 bytes, at least head_dim and at most 2^38");
-    const bool head_major = d->head_stride >= d->token_stride;
-    const int64_t inner = head_major ? d->token_stride * P : d->head_stride * H;
-    const int64_t outer = head_major ? d->head_stride * H : d->token_stride * P;
-    if ((head_major ? d->head_stride : d->token_stride) < inner || d->page_stride < outer) {
-        // a dimension of one row needs no room of its own
-        const bool one = head_major ? H == 1 : P == 1;
-        if (!(one && d->page_stride >= inner)) return fail(MOE_E_INVALID, "rows of a page overlap");
+    struct { int64_t n, st; } dims[] = {{d->n_pages, d->page_stride}, {d->n_kv_heads, d->head_stride}, {d->page_size, d->token_stride}};
+    std::sort(std::begin(dims), std::end(dims), [](const auto& a, const auto& b) { return a.st < b.st; });
+    int64_t span = d->head_dim;
+    for (const auto& m : dims) {
+        if (m.n == 1) continue;
+        if (m.st % step || m.st > ((int64_t)1 << 38))
+            return fail(MOE_E_INVALID, "strides must be multiples of 16 bytes, and at most 2^38");
+        if (m.st < span) return fail(MOE_E_INVALID, "rows of a pool overlap");
+        span = m.st * m.n;
     }
     return MOE_OK;
 }
@@ -63,8 +62,9 @@ KvShape shape_of(const moe_kv_desc& d) {
     s.rotary_dim = d.rotary_dim;
     s.rotary_adjacent = d.rotary_adjacent;
     s.e4m3 = d.cache_dtype == MOE_E4M3;
-    s.page_stride = d.page_stride;
-    s.head_stride = d.head_stride;
+    // (the step over a dimension of one row is never taken, but stands in the tensor maps)
+    s.page_stride = d.n_pages > 1 ? d.page_stride : d.head_dim;
+    s.head_stride = d.n_kv_heads > 1 ? d.head_stride : d.head_dim;
     s.token_stride = d.token_stride;
     return s;
 }

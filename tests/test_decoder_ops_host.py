@@ -241,3 +241,27 @@ def test_tables_of_more_chunks_than_the_kernel_counts(kw, pages, fits):
         moe.moe_kv_attend_check(d, a)
     else:
         refused(moe.moe_kv_attend_check, d, a, status=2)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(page_stride=16 * 64, head_stride=10 * 16 * 64),                                  # heads outermost
+    dict(page_stride=2 * 64, head_stride=64, token_stride=10 * 2 * 64),                   # slots outermost
+    dict(page_stride=64, head_stride=10 * 64, token_stride=2 * 10 * 64),
+    dict(page_stride=80, head_stride=16 * 1000, token_stride=1000),                       # with gaps
+    dict(n_pages=1, page_stride=0), dict(n_kv_heads=1, head_stride=0, page_stride=16 * 64)])
+def test_pools_in_any_order(kw):
+    d = kv_desc(**kw)
+    moe.moe_kv_attend_check(d, attend_args())
+    moe.moe_kv_append_check(d, append_args(k_stride=128, v_stride=128))
+    if d.n_pages > 1 and d.n_kv_heads > 1:
+        t = np.array([[7]], np.int32)
+        assert moe.moe_kv_locate(d, t, 0, 5, 1) == 7 * d.page_stride + d.head_stride + 5 * d.token_stride
+
+
+@pytest.mark.parametrize("kw", [
+    dict(page_stride=16 * 64, head_stride=9 * 16 * 64), dict(page_stride=64, head_stride=64, token_stride=2048),
+    dict(page_stride=2 * 64, head_stride=64, token_stride=9 * 2 * 64), dict(page_stride=56, head_stride=640, token_stride=1280),
+    dict(page_stride=0, head_stride=640, token_stride=1280), dict(page_stride=-2048), dict(token_stride=0),
+    dict(page_stride=68, head_stride=680, token_stride=1360), dict(head_stride=1 << 39)])
+def test_pools_whose_rows_overlap(kw):
+    refused(moe.moe_kv_attend_check, kv_desc(**kw), attend_args())
