@@ -764,15 +764,18 @@ class BlockNorm:
         if gate is not None:
             if o is None:
                 raise ValueError("gate needs o")
-            if gate.dim() == 1:
+            if gate.dim() < 2:
                 _dense(gate, "gate", (H,), blk, dev)
             elif gate.shape[0] == 1:
                 _dense(gate, "gate", (1, H), blk, dev)
             else:
                 gs = _rows(gate, "gate", shape, blk, dev)
             gp = gate.data_ptr()
-        self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, H, ids[res], ids[blk], ids[out], self.eps, self.scale,
-                             self.weight_offset, xs, os_, gs, rs, hs)
+        try:
+            self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, H, ids[res], ids[blk], ids[out], self.eps, self.scale,
+                                 self.weight_offset, xs, os_, gs, rs, hs)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"eps, scale or weight_offset is not a number of fp32's range: {e}") from None
         if stream is None:
             stream = self._current_stream(dev)
         st = self._call(self._buf_addr, x.data_ptr(), op, gp, wp, wn, rp, hp, shape[0], dev,
@@ -910,10 +913,13 @@ class KVCache:
             if len(table) != 2:
                 raise ValueError("block_table must be [B, max_pages]")
             _dense(block_table, "block_table", (B, table[1]), i32, dev)
-        self._attend_args.pack_into(
-            self._buf, 0, q.data_ptr(), _token_stride(q, "q", B, hq, d), block_table.data_ptr(), lens.data_ptr(), B,
-            table[1], d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
-            0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
+        try:
+            self._attend_args.pack_into(
+                self._buf, 0, q.data_ptr(), _token_stride(q, "q", B, hq, d), block_table.data_ptr(), lens.data_ptr(), B,
+                table[1], d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+                0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"scale, softcap or window is not a number of its type's range: {e}") from None
         if stream is None:
             stream = self._current_stream(dev)
         st = self._attend_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
