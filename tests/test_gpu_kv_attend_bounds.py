@@ -138,3 +138,12 @@ def test_scores_of_any_finite_size(times, dt):
                 assert_close(out[b, h], one, rounded(one, 2.0 ** -10 * one.abs(), BF16), f"out {b} {h}")
                 compared += 1
     assert compared >= 10
+
+
+@pytest.mark.parametrize("dt", [BF16, E4M3])
+@pytest.mark.parametrize("n,B,Hk,G,D", [(20011, 1, 1, 16, 256), (30001, 1, 1, 16, 128), (9007, 2, 1, 12, 256),
+                                        (24001, 1, 1, 40, 64), (16001, 1, 2, 9, 256)])
+def test_long_segments_of_more_than_8_queries(n, B, Hk, G, D, dt, monkeypatch):
+    """Two columns of heads: parts of many CTAs, joined in several batches."""
+    monkeypatch.setattr(_decoder_ref, "UP", 2.0 ** (-16 if dt is BF16 else -11))
+    Case([n - 1000 * b for b in range(B)], Hk * G, Hk, D, 64, dt, seed=n).check()
