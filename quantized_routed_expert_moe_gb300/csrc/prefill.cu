@@ -11,6 +11,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <string>
 #include <vector>
 
@@ -737,14 +738,15 @@ __global__ void __launch_bounds__(256) k_pf_combine(const float* __restrict__ yp
 // ---------------------------------------------------------------------------
 
 EncodeTiled tensor_map_encoder() {
-    static EncodeTiled fn = nullptr;
+    static std::atomic<EncodeTiled> kept{nullptr};   // handles may be created from several host threads
+    EncodeTiled fn = kept.load(std::memory_order_relaxed);
     if (!fn) {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult q{};
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
             q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiled>(p);
+            kept.store(fn = reinterpret_cast<EncodeTiled>(p), std::memory_order_relaxed);
     }
     return fn;
 }
