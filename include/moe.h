@@ -639,7 +639,9 @@ size_t moe_kv_device_bytes(const moe_kv* kv);
 moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* stream);
 
 /* Attention of one new token per sequence over the cache (formulas above):
- * fp32 scores, softmax statistics and sums. The length is read on the device
+ * fp32 scores, softmax statistics and sums; a weight enters the product with the
+ * values within 2^-16 (bf16 cache), or rounded to 11 bits (e4m3 cache: 2^-11, and
+ * at least 2^-39 of the largest). The length is read on the device
  * (no host synchronisation, capturable in a graph). The work is split evenly
  * over the GPU by cached tokens and joined in a fixed order, so results are
  * bit-reproducible. A length past the block table is cut to it and an attended

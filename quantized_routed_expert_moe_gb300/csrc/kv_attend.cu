@@ -35,10 +35,10 @@
 // head's largest; the sum is taken before that rounding.
 //
 // Measured (GB300, inputs larger than L2; copy rate 6.77 TB/s): 131072 tokens of one
-// sequence, 48 heads over 8 of 128 channels, 85.8 us, 6.3 TB/s; 64 sequences of up to
-// 16384 tokens, pages of 16, 223 us, 6.7 TB/s; 32 windows of 1024 tokens, 16 heads over
-// 8 of 256, 37.5 us, 5.4 TB/s; 48 sequences of up to 9001 tokens in 8 bits, 64 heads over
-// 4 of 128, 32.6 us, 4.2 TB/s; 17 tokens 4.9 us. What is above the stream's time is the
+// sequence, 48 heads over 8 of 128 channels, 86.5 us, 6.2 TB/s; 64 sequences of up to
+// 16384 tokens, pages of 16, 224 us, 6.6 TB/s; 32 windows of 1024 tokens, 16 heads over
+// 8 of 256, capped, 38.3 us, 5.3 TB/s; 48 sequences of up to 9001 tokens in 8 bits, 64 heads
+// over 4 of 128, 32.6 us, 4.2 TB/s; 17 tokens 5.2 us. What is above the stream's time is the
 // chain of reads before the first copy (lengths, block table, keys: 3 us) and the last
 // joins (5 to 7 us).
 #include <cuda_bf16.h>

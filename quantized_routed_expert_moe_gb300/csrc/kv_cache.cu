@@ -503,7 +503,7 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     // Units per token: a warp takes ceil(T n / warps) units, each of rounds / n rounds (the most
     // of them, where its next unit is always the same part) and about 0.9 of a round for its
     // angles and page; n with the least of that. 8192 tokens of 16 rounds: n = 4, 42.4 us, with
-    // 3 or 2 47 and 50; 7040 of 12 in 8 bits: n = 1, 28.2, with 2 or 4 30 and 33.
+    // 3 or 2 47 and 50; 7040 of 12 in 8 bits: n = 1, 29.1, with 2 or 4 31.3 and 34.7.
     const int64_t warps = (int64_t)K.num_sms * 3 * 8;
     if ((int64_t)args->T * p.rounds <= warps) {
         p.parts = p.rounds;
