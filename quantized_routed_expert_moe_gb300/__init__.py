@@ -245,6 +245,16 @@ def _stream(s) -> int | None:
     return s.cuda_stream if hasattr(s, "cuda_stream") else int(s)
 
 
+def _stream_on(s, current, device: int):
+    """The handle of a stream, or of torch's current one on a device."""
+    if s is None:
+        s = current(device)
+    try:
+        return s.cuda_stream
+    except AttributeError:
+        return _stream(s)
+
+
 def _check(status: int, call: str):
     if status != 0:
         raise MoEError(status, call, moe_last_error())
@@ -776,10 +786,8 @@ class BlockNorm:
                                  self.weight_offset, xs, os_, gs, rs, hs)
         except (struct.error, OverflowError) as e:
             raise ValueError(f"eps, scale or weight_offset is not a number of fp32's range: {e}") from None
-        if stream is None:
-            stream = self._current_stream(dev)
         st = self._call(self._buf_addr, x.data_ptr(), op, gp, wp, wn, rp, hp, shape[0], dev,
-                        stream.cuda_stream if hasattr(stream, "cuda_stream") else _stream(stream))
+                        _stream_on(stream, self._current_stream, dev))
         if st:
             _check(st, "moe_block_norm")
 
@@ -814,7 +822,7 @@ class KVCache:
             if s is not None and s.shape != (hk,):
                 raise ValueError("k_scale and v_scale hold one value per key-value head")
         self.k_pages, self.v_pages = k_pages, v_pages
-        self._pools_at = (k_pages.data_ptr(), v_pages.data_ptr())
+        self._k_at, self._v_at = k_pages.data_ptr(), v_pages.data_ptr()
         self.device = k_pages.get_device()
         self.desc = moe_kv_desc(MOE_ABI_VERSION, n_heads, hk, d, page, n_pages, kinds[k_pages.dtype],
                                 0 if freq is None else 2 * freq.size, int(interleaved), max_batch,
@@ -856,7 +864,7 @@ class KVCache:
         [n_seqs, max_pages]. stream: torch's current one on the pools' device by default."""
         hq, hk, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
-        if (self.k_pages.data_ptr(), self.v_pages.data_ptr()) != self._pools_at:
+        if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
             self._pools_moved()
         shape, table = k.shape, block_table.shape
         T = shape[0]
@@ -883,10 +891,7 @@ class KVCache:
             sp = _dense(seq, "seq", (T,), i32, dev)
         self._append_args.pack_into(self._buf, 0, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, positions.data_ptr(), sp,
                                     block_table.data_ptr(), T, table[0], table[1], op)
-        if stream is None:
-            stream = self._current_stream(dev)
-        st = self._append_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
-                               else _stream(stream))
+        st = self._append_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
         if st:
             _check(st, "moe_kv_append")
 
@@ -898,7 +903,7 @@ class KVCache:
         pools' device by default."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
-        if (self.k_pages.data_ptr(), self.v_pages.data_ptr()) != self._pools_at:
+        if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
             self._pools_moved()
         shape, table = q.shape, block_table.shape
         B = shape[0]
@@ -920,10 +925,7 @@ class KVCache:
                 0 if lse is None else _dense(lse, "lse", (B, hq), self._f32, dev))
         except (struct.error, OverflowError) as e:
             raise ValueError(f"scale, softcap or window is not a number of its type's range: {e}") from None
-        if stream is None:
-            stream = self._current_stream(dev)
-        st = self._attend_call(self.handle, self._buf_addr, stream.cuda_stream if hasattr(stream, "cuda_stream")
-                               else _stream(stream))
+        st = self._attend_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
         if st:
             _check(st, "moe_kv_attend")
 
