@@ -12,8 +12,9 @@
  *   y      = f_shared(x) + sum_j w_j f_{S_j}(x)
  *
  * and, beside it, what else a decoder layer does per token: the norms round a
- * block (moe_block_norm), a paged key-value cache (moe_kv_append) and attention
- * of one new token over it (moe_kv_attend).
+ * block (moe_block_norm), the projections (moe_linear), a paged key-value cache
+ * (moe_kv_append, moe_kv_append_norm) and attention over it, of one new token
+ * (moe_kv_attend) or of a chunk of them (moe_kv_attend_chunk) per sequence.
  *
  * Passages that define these operations:
  *   - router, LFU cache, shared expert and combine: TurboFieldfare article
@@ -539,6 +540,50 @@ moe_status moe_block_norm(const moe_block_norm_desc* desc, const void* x, const 
 moe_status moe_block_norm_check(const moe_block_norm_desc* desc, const void* x, const void* o, const void* gate,
                                 const float* w_post, const float* w_pre, const void* r, const void* h, int32_t T);
 
+/* ---- the rest of a decoder layer: projections ------------------------------------ */
+
+/* The activation of moe_linear. */
+enum {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SILU = 1,       /* z / (1 + exp(-z)) */
+    MOE_ACT_GELU_TANH = 2,  /* z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+    MOE_ACT_SIGMOID = 3     /* 1 / (1 + exp(-z)): the gates that moe_block_norm takes */
+};
+
+/* A matrix product with its epilogue, over T token rows:
+ *
+ *   y = act(x W^T + bias) + residual          (bias and residual: 0 where NULL)
+ *
+ * with x and W in bf16, products and sums in fp32 on the tensor cores, the
+ * epilogue in fp32 and one rounding to the type of y. The projections round an
+ * attention block: queries, keys and values from the block's input, the block's
+ * output onto the residual stream. The pages name them only as part of the layer
+ * (TurboFieldfare article, "implementation scope"). */
+typedef struct {
+    uint32_t abi_version;    /* MOE_ABI_VERSION */
+    int32_t in_features;     /* K, a multiple of 8 */
+    int32_t out_features;    /* N, a multiple of 8 */
+    int32_t out_dtype;       /* MOE_F32 or MOE_BF16: type of y and residual */
+    int32_t activation;      /* MOE_ACT_* */
+    int64_t x_stride, w_stride, y_stride, residual_stride; /* elements between rows, multiples of 8
+                                (of 4 in fp32) and at least the rows' length */
+} moe_linear_desc;
+
+/* One call over T >= 0 rows (T == 0 does nothing). All pointers are device memory
+ * on `device`, 16-byte aligned.
+ *   x: bf16 [T][K]; w: bf16 [N][K]; bias: fp32 [N] or NULL; residual: [T][N] or
+ *   NULL, may be y itself (with y's stride); y: [T][N], may not overlap any other input.
+ * No host synchronisation, no scratch: calls on several streams are independent.
+ * A row's result does not depend on the other rows of its call. Sums are taken in
+ * an order that depends on T, N and K alone, so results are bit-reproducible.
+ * Errors: MOE_E_INVALID, MOE_E_UNSUPPORTED (K or N above 2^20, T above 2^24), MOE_E_CUDA. */
+moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
+                      const void* residual, void* y, int32_t T, int32_t device, void* stream);
+
+/* moe_linear's argument checks alone (host only, no device). */
+moe_status moe_linear_check(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
+                            const void* residual, const void* y, int32_t T);
+
 /* ---- the rest of a decoder layer: paged key-value cache -------------------------- */
 
 /* Keys and values of one attention layer in pages of page_size tokens. Both
@@ -587,6 +632,15 @@ typedef struct {
     void* q_out;
 } moe_kv_append_args;
 
+/* moe_kv_append_norm's norms of every head's queries and keys, taken before the
+ * rotation: z / sqrt(mean(z^2) + eps) * (weight + weight_offset), the mean over the
+ * head's channels. Weights: device fp32 [head_dim], 16-byte aligned; NULL: no norm. */
+typedef struct {
+    const float *q_weight, *k_weight;
+    float eps;               /* finite, >= 0 */
+    float weight_offset;     /* finite; 1 for weights stored as w - 1 */
+} moe_kv_head_norm;
+
 /* moe_kv_attend's arguments: one new token of each of B sequences (0 <= B <=
  * max_batch; 0 does nothing). q: device bf16 [B][n_heads][head_dim], q_stride
  * elements between sequences (a multiple of 8; heads contiguous). block_table:
@@ -614,6 +668,37 @@ typedef struct {
     void* out;
     float* lse;
 } moe_kv_attend_args;
+
+/* moe_kv_attend_chunk's arguments: a chunk of new tokens of each of B sequences (0 <=
+ * B <= max_batch), T rows in all, packed behind one another. q: device bf16
+ * [T][n_heads][head_dim], q_stride elements between tokens (a multiple of 8; heads
+ * contiguous). starts: device int32 [B + 1], not decreasing, within 0..T: sequence b's
+ * tokens are rows starts[b]..starts[b + 1] - 1 (none where they are equal).
+ * block_table: device int32 [B][max_pages]; lens: device int32 [B], cached tokens of
+ * each sequence, its chunk included (append the chunk first). Token i of a chunk of n
+ * stands at position p = len - n + i, and attends to positions j <= p; window > 0: only
+ * j > p - window. Scores, softcap, out ([T][n_heads][head_dim]) and lse ([T][n_heads])
+ * are those of moe_kv_attend. A token at a negative position (a chunk longer than its
+ * sequence's length) gives out = 0 and lse = -inf. Rows outside starts[0]..starts[B] - 1
+ * are left as they were. Cached values that a token does not attend to do not change its
+ * result, whatever they hold, NaN included.
+ * workspace: device memory of at least moe_kv_chunk_workspace bytes, 16-byte aligned, in
+ * any state; calls that share one must not overlap on the GPU (the handles of a model's
+ * layers may share it). MOE_E_UNSUPPORTED: T * n_heads of 2^31 or more. */
+typedef struct {
+    const void* q;
+    int64_t q_stride;
+    const int32_t* starts;
+    const int32_t* block_table;
+    const int32_t* lens;
+    int32_t T, B, max_pages;
+    float scale, softcap;
+    int32_t window;
+    void* out;
+    float* lse;
+    void* workspace;
+    int64_t workspace_bytes;
+} moe_kv_chunk_args;
 
 /* Create the handle over two page pools (device memory, borrowed: they must
  * stay valid until moe_kv_destroy; 16-byte aligned).
@@ -648,7 +733,28 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
  * page id outside the pool is skipped; both set a bit for moe_kv_health. */
 moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* stream);
 
-/* The argument checks of the two calls alone (host only, no device). */
+/* moe_kv_append with the norms of the heads' queries and keys in the same pass, in
+ * fp32 like the rotation: nothing is rounded between them. */
+moe_status moe_kv_append_norm(moe_kv* kv, const moe_kv_append_args* args, const moe_kv_head_norm* norm, void* stream);
+
+/* Attention of a chunk of new tokens per sequence over the cache (formulas above):
+ * products on the tensor cores, scores, softmax statistics and sums in fp32; a weight
+ * enters the product with the values rounded to bf16 (bf16 cache: 2^-9, at its own
+ * size), or to 11 bits (e4m3 cache: fp16, 2^-12, and at least 2^-39 of the largest).
+ * Lengths and starts are read on the device (no host synchronisation, capturable in a
+ * graph). The work is split over the GPU by cached blocks and joined in a fixed order,
+ * so results are bit-reproducible. A length past the block table is cut to it and an
+ * attended page id outside the pool is skipped; both set a bit for moe_kv_health. */
+moe_status moe_kv_attend_chunk(moe_kv* kv, const moe_kv_chunk_args* args, void* stream);
+
+/* Bytes of the workspace that moe_kv_attend_chunk needs (0 for NULL). */
+size_t moe_kv_chunk_workspace(const moe_kv* kv);
+
+/* The argument checks of the calls alone (host only, no device). The chunk's does not
+ * look at the workspace's size, which depends on the device. */
+moe_status moe_kv_append_norm_check(const moe_kv_desc* desc, const moe_kv_append_args* args,
+                                    const moe_kv_head_norm* norm);
+moe_status moe_kv_attend_chunk_check(const moe_kv_desc* desc, const moe_kv_chunk_args* args);
 moe_status moe_kv_append_check(const moe_kv_desc* desc, const moe_kv_append_args* args);
 moe_status moe_kv_attend_check(const moe_kv_desc* desc, const moe_kv_attend_args* args);
 
@@ -666,8 +772,10 @@ enum {
     MOE_KV_BAD_SEQ = 1,     /* append: a sequence index outside block_table */
     MOE_KV_BAD_LENGTH = 2,  /* a position or length past max_pages * page_size */
     MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
-    MOE_KV_TIMEOUT = 8      /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
-                               out and lse whose cache did not arrive are NaN */
+    MOE_KV_TIMEOUT = 8,     /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
+                               out and lse whose cache did not arrive are NaN. Inside
+                               moe_kv_attend_chunk (2 s): rows of the call may hold anything */
+    MOE_KV_BAD_START = 16   /* chunk: starts decrease or leave 0..T; nothing was computed */
 };
 moe_status moe_kv_health(moe_kv* kv, uint32_t* bits);
 

@@ -9,8 +9,8 @@ Functions keep the C names (``moe_layer_create``, ``moe_route``,
 ``moe_cache_stage`` ...). Pointer arguments accept a torch tensor (its
 ``data_ptr()``), a numpy array, a raw integer address or None.
 
-``MoELayer``, ``BlockNorm`` and ``KVCache`` own a handle or weights and take
-tensors; the latter two check shapes, types and devices before a call, and run on
+``MoELayer``, ``BlockNorm``, ``Linear`` and ``KVCache`` own a handle or weights and take
+tensors; the latter three check shapes, types and devices before a call, and run on
 torch's current stream where none is given. Elsewhere stream=None is the legacy
 default stream, as in C.
 """
@@ -35,7 +35,8 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_expert_record_bytes", "
            "moe_layer_device_bytes", "moe_layer_set_next", "moe_layer_set_router_scoring", "moe_route", "moe_layer_selection", "moe_decode", "moe_decode_static_scratch", "moe_prefill_chunk",
            "moe_decode_tokens_host", "moe_cache_stage", "moe_cache_prefetch", "moe_cache_prefetch_stats", "moe_cache_stats", "moe_cache_residency", "moe_cache_usage", "moe_cache_pin", "moe_hottest", "moe_cache_pin_hottest", "moe_lfu_trace", "moe_lfu_trace_pinned",
            "moe_profile_start", "moe_profile_stop", "moe_layer_set_option", "moe_layer_check", "moe_trace_read_split",
-           "moe_block_norm", "moe_block_norm_check", "moe_kv_create", "moe_kv_destroy", "moe_kv_device_bytes", "moe_kv_append", "moe_kv_attend",
+           "moe_block_norm", "moe_block_norm_check", "moe_linear", "moe_linear_check", "moe_kv_append_norm", "moe_kv_append_norm_check",
+           "moe_kv_attend_chunk", "moe_kv_attend_chunk_check", "moe_kv_chunk_workspace", "moe_kv_create", "moe_kv_destroy", "moe_kv_device_bytes", "moe_kv_append", "moe_kv_attend",
            "moe_kv_append_check", "moe_kv_attend_check", "moe_kv_locate", "moe_kv_health", "moe_kv_set_option",
            "moe_status_str", "moe_last_error")
 
@@ -44,7 +45,8 @@ MOE_STATIC_SCRATCH_BYTES = 256 * 1024
 MOE_OPT_TEST_STALL_SHARED, MOE_OPT_TRACE = 2, 3
 MOE_OPT_HOST_TIMEOUT_MS, MOE_OPT_TEST_STALL_COPIES_MS, MOE_OPT_CACHE_DEVICE = 4, 5, 6
 MOE_MAX_TOP_K = 8
-MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT = 1, 2, 4, 8
+MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT, MOE_KV_BAD_START = 1, 2, 4, 8, 16
+MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_SIGMOID = 0, 1, 2, 3
 MOE_KV_OPT_TEST_STALL = 1
 
 
@@ -106,6 +108,25 @@ class moe_kv_attend_args(ctypes.Structure):
                 ("lens", ctypes.c_void_p), ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
                 ("scale", ctypes.c_float), ("softcap", ctypes.c_float), ("window", ctypes.c_int32),
                 ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p)]
+
+
+class moe_linear_desc(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("in_features", ctypes.c_int32), ("out_features", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64)]
+
+
+class moe_kv_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("weight_offset", ctypes.c_float)]
+
+
+class moe_kv_chunk_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("starts", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("T", ctypes.c_int32),
+                ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_int64)]
 
 
 class moe_kernel_time(ctypes.Structure):
@@ -206,6 +227,22 @@ def lib() -> ctypes.CDLL:
             L.moe_kv_append.argtypes = [vp, ap, vp]
             L.moe_kv_attend.restype = st
             L.moe_kv_attend.argtypes = [vp, at, vp]
+            ld, hn = ctypes.POINTER(moe_linear_desc), ctypes.POINTER(moe_kv_head_norm)
+            ac = ctypes.POINTER(moe_kv_chunk_args)
+            L.moe_linear.restype = st
+            L.moe_linear.argtypes = [ld, vp, vp, vp, vp, vp, i32, i32, vp]
+            L.moe_linear_check.restype = st
+            L.moe_linear_check.argtypes = [ld, vp, vp, vp, vp, vp, i32]
+            L.moe_kv_append_norm.restype = st
+            L.moe_kv_append_norm.argtypes = [vp, ap, hn, vp]
+            L.moe_kv_append_norm_check.restype = st
+            L.moe_kv_append_norm_check.argtypes = [kd, ap, hn]
+            L.moe_kv_attend_chunk.restype = st
+            L.moe_kv_attend_chunk.argtypes = [vp, ac, vp]
+            L.moe_kv_attend_chunk_check.restype = st
+            L.moe_kv_attend_chunk_check.argtypes = [kd, ac]
+            L.moe_kv_chunk_workspace.restype = sz
+            L.moe_kv_chunk_workspace.argtypes = [vp]
             L.moe_kv_append_check.restype = st
             L.moe_kv_append_check.argtypes = [kd, ap]
             L.moe_kv_attend_check.restype = st
@@ -534,6 +571,41 @@ def moe_kv_attend(handle, args: moe_kv_attend_args, stream=None) -> None:
     _check(lib().moe_kv_attend(handle, ctypes.byref(args), _stream(stream)), "moe_kv_attend")
 
 
+def moe_linear(desc, x, w, bias, residual, y, T, device=0, stream=None) -> None:
+    _check(lib().moe_linear(ctypes.byref(desc), _addr(x), _addr(w), _addr(bias), _addr(residual), _addr(y), T, device,
+                            _stream(stream)), "moe_linear")
+
+
+def moe_linear_check(desc, x, w, bias, residual, y, T) -> None:
+    """The argument checks of moe_linear alone (host only)."""
+    _check(lib().moe_linear_check(ctypes.byref(desc), _addr(x), _addr(w), _addr(bias), _addr(residual), _addr(y), T),
+           "moe_linear_check")
+
+
+def moe_kv_append_norm(handle, args: moe_kv_append_args, norm: moe_kv_head_norm, stream=None) -> None:
+    _check(lib().moe_kv_append_norm(handle, ctypes.byref(args), ctypes.byref(norm), _stream(stream)),
+           "moe_kv_append_norm")
+
+
+def moe_kv_append_norm_check(desc, args, norm) -> None:
+    """The argument checks of moe_kv_append_norm alone (host only)."""
+    _check(lib().moe_kv_append_norm_check(ctypes.byref(desc), ctypes.byref(args), ctypes.byref(norm)),
+           "moe_kv_append_norm_check")
+
+
+def moe_kv_attend_chunk(handle, args: moe_kv_chunk_args, stream=None) -> None:
+    _check(lib().moe_kv_attend_chunk(handle, ctypes.byref(args), _stream(stream)), "moe_kv_attend_chunk")
+
+
+def moe_kv_attend_chunk_check(desc, args) -> None:
+    """The argument checks of moe_kv_attend_chunk alone (host only)."""
+    _check(lib().moe_kv_attend_chunk_check(ctypes.byref(desc), ctypes.byref(args)), "moe_kv_attend_chunk_check")
+
+
+def moe_kv_chunk_workspace(handle) -> int:
+    return int(lib().moe_kv_chunk_workspace(handle))
+
+
 def moe_kv_append_check(desc, args) -> None:
     """The argument checks of moe_kv_append alone (host only)."""
     _check(lib().moe_kv_append_check(ctypes.byref(desc), ctypes.byref(args)), "moe_kv_append_check")
@@ -792,6 +864,73 @@ class BlockNorm:
             _check(st, "moe_block_norm")
 
 
+class Linear:
+    """A projection with its epilogue (moe_linear): y = act(x W^T + bias) + residual.
+    Keeps the weight, bfloat16 [out_features, in_features] on the device (rows may have
+    gaps), and the bias, fp32 [out_features] or None. activation: "none", "silu",
+    "gelu_tanh" or "sigmoid". One object serves one host thread at a time."""
+
+    # moe_linear_desc, packed in place
+    _desc = struct.Struct("Iiiii4xqqqq")
+    _acts = {"none": MOE_ACT_NONE, "silu": MOE_ACT_SILU, "gelu_tanh": MOE_ACT_GELU_TANH, "sigmoid": MOE_ACT_SIGMOID}
+
+    def __init__(self, weight, bias=None, activation: str = "none"):
+        import torch
+        if activation not in self._acts:
+            raise ValueError(f"activation must be one of {', '.join(self._acts)}")
+        if weight.dim() != 2:
+            raise ValueError("weight must be [out_features, in_features]")
+        self.out_features, self.in_features = weight.shape
+        self.weight, self.bias, self.activation = weight, bias, activation
+        self._act, self._bf16, self._f32 = self._acts[activation], torch.bfloat16, torch.float32
+        self._ids = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
+        self._bind(weight.get_device())
+        self._buf = ctypes.create_string_buffer(ctypes.sizeof(moe_linear_desc))
+        self._buf_addr = ctypes.addressof(self._buf)
+        vp, i32 = ctypes.c_void_p, ctypes.c_int32
+        self._call = ctypes.CFUNCTYPE(ctypes.c_int, *[vp] * 6, i32, i32, vp)(("moe_linear", lib()))
+        self._current_stream = torch.cuda.current_stream
+
+    def _bind(self, device):
+        """Take the weights' addresses, held by aliases as BlockNorm's are."""
+        w, b = self.weight, self.bias
+        shape = (self.out_features, self.in_features)
+        if not w.is_cuda:
+            _refuse(w, "weight", shape, self._bf16, device)
+        self._w_stride = _rows(w, "weight", shape, self._bf16, device)
+        self._b = None if b is None else _dense(b, "bias", (self.out_features,), self._f32, device)
+        self._w, self._w_of, self._b_of = w.data_ptr(), w, b
+        self._alias = w.detach(), None if b is None else b.detach()
+        self.device = device
+
+    def run(self, x, y, residual=None, stream=None):
+        """x [T, in_features] bf16, y [T, out_features] bf16 or fp32 the output, residual of y's
+        shape and type (may be y) or None. stream: torch's current one on x's device by default."""
+        K, N, bf16, dev = self.in_features, self.out_features, self._bf16, x.get_device()
+        w, b = self.weight, self.bias
+        if (w is not self._w_of or b is not self._b_of or w.data_ptr() != self._w
+                or (b is not None and b.data_ptr() != self._b) or self.device != dev):
+            self._bind(dev)
+        shape, out = x.shape, y.dtype
+        if len(shape) != 2 or shape[1] != K or x.dtype is not bf16:
+            _refuse(x, "x", ("T", K), bf16, dev)
+        if out not in self._ids:
+            raise TypeError("y must be float32 or bfloat16")
+        T = shape[0]
+        xs = K if x.is_contiguous() else _rows(x, "x", shape, bf16, dev)
+        plain = y.shape == (T, N) and y.get_device() == dev and y.is_contiguous()
+        ys = N if plain else _rows(y, "y", (T, N), out, dev)
+        rs = rp = 0
+        if residual is not None:
+            plain = residual.shape == (T, N) and residual.dtype is out and residual.get_device() == dev and residual.is_contiguous()
+            rs, rp = N if plain else _rows(residual, "residual", (T, N), out, dev), residual.data_ptr()
+        self._desc.pack_into(self._buf, 0, MOE_ABI_VERSION, K, N, self._ids[out], self._act, xs, self._w_stride, ys, rs)
+        st = self._call(self._buf_addr, x.data_ptr(), self._w, self._b, rp, y.data_ptr(), T, dev,
+                        _stream_on(stream, self._current_stream, dev))
+        if st:
+            _check(st, "moe_linear")
+
+
 class KVCache:
     """Owns one cache handle over two page pools, tensors [n_pages, n_kv_heads,
     page_size, head_dim] of bfloat16 or float8_e4m3fn in any memory order whose
@@ -801,6 +940,8 @@ class KVCache:
     # moe_kv_append_args and moe_kv_attend_args, packed in place
     _append_args = struct.Struct("PPPqqqPPPiiiP")
     _attend_args = struct.Struct("PqPPiiffiPP")
+    _chunk_args = struct.Struct("PqPPPiiiffiPPPq")
+    _head_norm = struct.Struct("PPff")
 
     def __init__(self, k_pages, v_pages, n_heads: int, inv_freq=None, interleaved: bool = False, k_scale=None,
                  v_scale=None, max_batch: int = 1):
@@ -831,17 +972,23 @@ class KVCache:
                                     scales[0], scales[1], self.device)
         self._bf16, self._f32, self._i32 = torch.bfloat16, torch.float32, torch.int32
         self._heads = (n_heads, hk, d)
-        self._buf = ctypes.create_string_buffer(max(self._append_args.size, self._attend_args.size))
+        self._buf = ctypes.create_string_buffer(max(self._append_args.size, self._attend_args.size, self._chunk_args.size))
         self._buf_addr = ctypes.addressof(self._buf)
+        self._norm_buf = ctypes.create_string_buffer(self._head_norm.size)
+        self._norm_addr = ctypes.addressof(self._norm_buf)
         proto = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p)
         self._append_call = proto(("moe_kv_append", lib()))
         self._attend_call = proto(("moe_kv_attend", lib()))
+        self._chunk_call = proto(("moe_kv_attend_chunk", lib()))
+        self._append_norm_call = ctypes.CFUNCTYPE(ctypes.c_int, *[ctypes.c_void_p] * 4)(("moe_kv_append_norm", lib()))
+        self.chunk_workspace_bytes = moe_kv_chunk_workspace(self.handle)
+        self._workspace = None
         self._current_stream = torch.cuda.current_stream
 
     def close(self):
         if getattr(self, "handle", None):
-            moe_kv_destroy(self.handle)
-            self.handle = None
+            moe_kv_destroy(self.handle)   # waits for the device
+            self.handle = self._workspace = None
 
     def __del__(self):
         try:
@@ -858,10 +1005,13 @@ class KVCache:
     def _pools_moved(self):
         raise ValueError("k_pages or v_pages has new memory: the handle is bound to that of its construction")
 
-    def append(self, q, k, v, positions, block_table, q_out=None, seq=None, stream=None):
+    def append(self, q, k, v, positions, block_table, q_out=None, seq=None, stream=None, q_norm=None, k_norm=None,
+               norm_eps: float = 1e-6, norm_offset: float = 0.0):
         """Rotate and cache T tokens: q [T, n_heads, d] (or None with q_out), k
         and v [T, n_kv_heads, d], positions and seq int32 [T], block_table int32
-        [n_seqs, max_pages]. stream: torch's current one on the pools' device by default."""
+        [n_seqs, max_pages]. q_norm and k_norm: weights fp32 [d] of a norm of every
+        query and key head before the rotation (norm_offset is added to them), or None.
+        stream: torch's current one on the pools' device by default."""
         hq, hk, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
         if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
@@ -891,9 +1041,22 @@ class KVCache:
             sp = _dense(seq, "seq", (T,), i32, dev)
         self._append_args.pack_into(self._buf, 0, qp, k.data_ptr(), v.data_ptr(), qs, ks, vs, positions.data_ptr(), sp,
                                     block_table.data_ptr(), T, table[0], table[1], op)
-        st = self._append_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
+        if q_norm is None and k_norm is None:
+            st = self._append_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
+            if st:
+                _check(st, "moe_kv_append")
+            return
+        try:
+            self._head_norm.pack_into(self._norm_buf, 0,
+                                      0 if q_norm is None else _dense(q_norm, "q_norm", (d,), self._f32, dev),
+                                      0 if k_norm is None else _dense(k_norm, "k_norm", (d,), self._f32, dev),
+                                      norm_eps, norm_offset)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"norm_eps or norm_offset is not a number of fp32's range: {e}") from None
+        st = self._append_norm_call(self.handle, self._buf_addr, self._norm_addr,
+                                    _stream_on(stream, self._current_stream, dev))
         if st:
-            _check(st, "moe_kv_append")
+            _check(st, "moe_kv_append_norm")
 
     def attend(self, q, block_table, lens, out, lse=None, scale=None, softcap: float = 0.0, window: int = 0,
                stream=None):
@@ -928,6 +1091,61 @@ class KVCache:
         st = self._attend_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
         if st:
             _check(st, "moe_kv_attend")
+
+    def attend_chunk(self, q, starts, block_table, lens, out, lse=None, scale=None, softcap: float = 0.0,
+                     window: int = 0, workspace=None, stream=None):
+        """Attention of a chunk of new tokens per sequence, each token over what is cached up to
+        its own position: q and out [T, n_heads, d] bf16, starts int32 [B + 1] (sequence b's
+        tokens are rows starts[b] to starts[b + 1] - 1), lens int32 [B] with the chunk
+        counted, block_table int32 [B, max_pages], lse fp32 [T, n_heads] or None; scale
+        defaults to 1 / sqrt(d). workspace: uint8, chunk_workspace_bytes or more, for example
+        one for all layers of a model; without it the object keeps one of its own from its
+        first call on, which is then not to be captured in a graph. stream: torch's current
+        one on the pools' device by default."""
+        hq, _, d = self._heads
+        dev, bf16, i32 = self.device, self._bf16, self._i32
+        if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
+            self._pools_moved()
+        shape, table = q.shape, block_table.shape
+        T, B = shape[0], lens.shape[0]
+        if not (shape == (T, hq, d) and out.shape == shape and lens.shape == (B,) and starts.shape == (B + 1,)
+                and len(table) == 2 and table[0] == B and q.dtype is bf16 and out.dtype is bf16 and lens.dtype is i32
+                and starts.dtype is i32 and block_table.dtype is i32 and q.get_device() == dev
+                and out.get_device() == dev and lens.get_device() == dev and starts.get_device() == dev
+                and block_table.get_device() == dev and out.is_contiguous() and lens.is_contiguous()
+                and starts.is_contiguous() and block_table.is_contiguous()):
+            _rows(q, "q", (T, hq, d), bf16, dev)
+            _dense(out, "out", (T, hq, d), bf16, dev)
+            _dense(lens, "lens", (B,), i32, dev)
+            _dense(starts, "starts", (B + 1,), i32, dev)
+            if len(table) != 2:
+                raise ValueError("block_table must be [B, max_pages]")
+            _dense(block_table, "block_table", (B, table[1]), i32, dev)
+        if workspace is None:
+            workspace = self._workspace
+            if workspace is None:
+                workspace = self._own_workspace()
+        elif workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
+        try:
+            self._chunk_args.pack_into(
+                self._buf, 0, q.data_ptr(), _token_stride(q, "q", T, hq, d), starts.data_ptr(), block_table.data_ptr(),
+                lens.data_ptr(), T, B, table[1], d ** -0.5 if scale is None else scale, softcap, window, out.data_ptr(),
+                0 if lse is None else _dense(lse, "lse", (T, hq), self._f32, dev), workspace.data_ptr(),
+                workspace.nbytes)
+        except (struct.error, OverflowError) as e:
+            raise ValueError(f"scale, softcap or window is not a number of its type's range: {e}") from None
+        st = self._chunk_call(self.handle, self._buf_addr, _stream_on(stream, self._current_stream, dev))
+        if st:
+            _check(st, "moe_kv_attend_chunk")
+
+    def _own_workspace(self):
+        import torch
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("attend_chunk: the first call makes the workspace, which a graph capture cannot; pass "
+                               "workspace=, or call once before the capture")
+        self._workspace = torch.empty(self.chunk_workspace_bytes, dtype=torch.uint8, device=self.k_pages.device)
+        return self._workspace
 
     def locate(self, block_table, seq: int, position: int, head: int = 0) -> int:
         """Element offset of a cached row in a pool (block_table on the host)."""

@@ -120,6 +120,36 @@ moe_status check_attend(const moe_kv_desc* d, const moe_kv_attend_args* a) {
     return MOE_OK;
 }
 
+moe_status check_head_norm(const moe_kv_head_norm* n) {
+    if (!n) return fail(MOE_E_INVALID, "norm is NULL");
+    if (!std::isfinite(n->eps) || n->eps < 0) return fail(MOE_E_INVALID, "eps must be finite and >= 0");
+    if (!std::isfinite(n->weight_offset)) return fail(MOE_E_INVALID, "weight_offset must be finite");
+    if (!aligned16(n->q_weight) || !aligned16(n->k_weight))
+        return fail(MOE_E_INVALID, "q_weight and k_weight must be 16-byte aligned");
+    return MOE_OK;
+}
+
+moe_status check_chunk(const moe_kv_desc* d, const moe_kv_chunk_args* a) {
+    moe_status st = check_desc(d);
+    if (st != MOE_OK) return st;
+    if (!a) return fail(MOE_E_INVALID, "args is NULL");
+    if (a->B < 0 || a->B > d->max_batch) return fail(MOE_E_INVALID, "B must be in 0..max_batch");
+    if (a->T < 0) return fail(MOE_E_INVALID, "T must not be negative");
+    if (!std::isfinite(a->scale)) return fail(MOE_E_INVALID, "scale must be finite");
+    if (!std::isfinite(a->softcap) || a->softcap < 0) return fail(MOE_E_INVALID, "softcap must be finite and >= 0");
+    if (a->window < 0) return fail(MOE_E_INVALID, "window must be >= 0");
+    if (a->B == 0 || a->T == 0) return MOE_OK;
+    if (!a->q || !a->starts || !a->lens || !a->out) return fail(MOE_E_INVALID, "q, starts, lens or out is NULL");
+    st = check_table(a->block_table, a->B, a->max_pages, d->page_size);
+    if (st != MOE_OK) return st;
+    if (!a->workspace || !aligned16(a->workspace)) return fail(MOE_E_INVALID, "workspace must be non-NULL and 16-byte aligned");
+    if (!aligned16(a->q) || !aligned16(a->out)) return fail(MOE_E_INVALID, "q and out must be 16-byte aligned");
+    if (a->q_stride % 8 || a->q_stride < (int64_t)d->head_dim * d->n_heads)
+        return fail(MOE_E_INVALID, "q_stride must be a multiple of 8 and cover the heads");
+    if ((int64_t)a->T * d->n_heads > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "T * n_heads is 2^31 or more");
+    return MOE_OK;
+}
+
 // ---- append ---------------------------------------------------------------------
 //
 // A head is D / 16 groups of 16 channels, two 16-byte vectors each, so laid that
@@ -168,6 +198,7 @@ __device__ __forceinline__ void phase(uint64_t turns, int position, float& c, fl
 
 struct AppendArgs {
     moe_kv_append_args a;
+    moe_kv_head_norm n;
     KvShape s;
     void *k_pages, *v_pages;
     const uint64_t* turns;
@@ -187,7 +218,10 @@ struct AppendArgs {
 constexpr int kAhead = 4;
 constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 
-template <bool ADJACENT, bool E4M3>
+// With NORM the D / 16 lanes of a head sum its squares (values and, where a norm is not
+// asked for, its heads go through unchanged), and read the weights of their channels from
+// the first-level cache.
+template <bool ADJACENT, bool E4M3, bool NORM>
 __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float sm_c[8][128], sm_s[8][128];
@@ -279,6 +313,18 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             if (r == part) next_page = look_up(next_pos, next_seq, next_read);
             const int head = r * side + lane / groups;
             const bool is_q = head < q_heads, is_v = head >= k_heads;
+            const float* const weight = !NORM || is_v ? nullptr : is_q ? p.n.q_weight : p.n.k_weight;
+            float inv = 1.f;
+            if constexpr (NORM) {
+                float sum = 0.f;   // (past the last head the ring holds what it held)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const float2 a = unpack2(u4w(u0, x)), b = unpack2(u4w(u1, x));
+                    sum += a.x * a.x + a.y * a.y + b.x * b.x + b.y * b.y;
+                }
+                for (int o = 1; o < groups; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                inv = 1.f / sqrtf(sum / s.head_dim + p.n.eps);
+            }
             if (head < heads && (is_q || page >= 0)) {
                 const int hk = head - (is_v ? k_heads : q_heads);
                 const int at0 = is_v ? v0 : c0, at1 = is_v ? v1 : c1;
@@ -295,10 +341,25 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                     *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&sm_c[warp][a1]);
                     *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(&sm_s[warp][a1]);
                 }
+                float wn[16];
+                if (NORM && weight) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(weight + (x < 2 ? c0 : c1)) + x % 2);
+                        wn[4 * x] = (f.x + p.n.weight_offset) * inv;
+                        wn[4 * x + 1] = (f.y + p.n.weight_offset) * inv;
+                        wn[4 * x + 2] = (f.z + p.n.weight_offset) * inv;
+                        wn[4 * x + 3] = (f.w + p.n.weight_offset) * inv;
+                    }
+                }
                 // two channels of either vector at a time
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
+                    if (NORM && weight) {
+                        a = make_float2(a.x * wn[2 * x], a.y * wn[2 * x + 1]);
+                        b = make_float2(b.x * wn[8 + 2 * x], b.y * wn[9 + 2 * x]);
+                    }
                     if constexpr (ADJACENT) {
                         if (t0) a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
                         if (t1) b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
@@ -311,8 +372,8 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                         e[0][x / 2] |= quant2(a, scale.x, scale.y) << 16 * (x % 2);
                         e[1][x / 2] |= quant2(b, scale.x, scale.y) << 16 * (x % 2);
                     } else {
-                        if (t0) w[0][x] = pack2(a);
-                        if (t1) w[1][x] = pack2(b);
+                        if (t0 || (NORM && weight)) w[0][x] = pack2(a);
+                        if (t1 || (NORM && weight)) w[1][x] = pack2(b);
                     }
                     if (is_q && pos < 0) w[0][x] = w[1][x] = 0;
                 }
@@ -342,10 +403,12 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
 
 using AppendKernel = void (*)(const AppendArgs);
 
+template <bool NORM>
 AppendKernel append_kernel(const KvShape& s) {
-    return s.rotary_adjacent ? (s.e4m3 ? k_kv_append<true, true> : k_kv_append<true, false>)
-                             : (s.e4m3 ? k_kv_append<false, true> : k_kv_append<false, false>);
+    return s.rotary_adjacent ? (s.e4m3 ? k_kv_append<true, true, NORM> : k_kv_append<true, false, NORM>)
+                             : (s.e4m3 ? k_kv_append<false, true, NORM> : k_kv_append<false, false, NORM>);
 }
+AppendKernel append_kernel(const KvShape& s, bool norm) { return norm ? append_kernel<true>(s) : append_kernel<false>(s); }
 
 }  // namespace
 
@@ -361,6 +424,16 @@ moe_status moe_kv_append_check(const moe_kv_desc* desc, const moe_kv_append_args
 
 moe_status moe_kv_attend_check(const moe_kv_desc* desc, const moe_kv_attend_args* args) {
     return check_attend(desc, args);
+}
+
+moe_status moe_kv_append_norm_check(const moe_kv_desc* desc, const moe_kv_append_args* args,
+                                    const moe_kv_head_norm* norm) {
+    const moe_status st = check_append(desc, args);
+    return st == MOE_OK ? check_head_norm(norm) : st;
+}
+
+moe_status moe_kv_attend_chunk_check(const moe_kv_desc* desc, const moe_kv_chunk_args* args) {
+    return check_chunk(desc, args);
 }
 
 moe_status moe_kv_locate(const moe_kv_desc* desc, const int32_t* block_table, int32_t n_seqs, int32_t max_pages,
@@ -469,7 +542,10 @@ moe_status moe_kv_create(const moe_kv_desc* desc, void* k_pages, void* v_pages, 
     if (e == cudaSuccess) e = cudaMemcpy(K.scales, scales, (size_t)Hk * 16, cudaMemcpyHostToDevice);
     if (e == cudaSuccess) e = kv_attend_setup(K);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(append_kernel(K.s), cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendRing);
+        e = cudaFuncSetAttribute(append_kernel(K.s, false), cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendRing);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(append_kernel(K.s, true), cudaFuncAttributeMaxDynamicSharedMemorySize, kAppendRing);
+    if (e == cudaSuccess) e = kv_chunk_setup(K);
     // the set-up ran on the legacy stream: finish it before any other stream may run a call
     if (e == cudaSuccess) e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return bail(cuda_fail(e, "moe_kv_create set-up"));
@@ -489,15 +565,11 @@ void moe_kv_destroy(moe_kv* kv) {
 
 size_t moe_kv_device_bytes(const moe_kv* kv) { return kv ? kv->K.device_bytes : 0; }
 
-moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* stream) {
-    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+static moe_status append(moe_kv* kv, const moe_kv_append_args* args, const moe_kv_head_norm& norm, void* stream) {
     Kv& K = kv->K;
-    moe_status st = check_append(&K.d, args);
-    if (st != MOE_OK) return st;
-    if (args->T == 0) return MOE_OK;
     DeviceGuard g(K.device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    AppendArgs p{*args, K.s, K.k_pages, K.v_pages, K.turns, K.scales, K.health, 1, 1};
+    AppendArgs p{*args, norm, K.s, K.k_pages, K.v_pages, K.turns, K.scales, K.health, 1, 1};
     const int heads = (args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads, side = 32 / (K.s.head_dim / 16);
     p.rounds = (heads + side - 1) / side;
     // Units per token: a warp takes ceil(T n / warps) units, each of rounds / n rounds (the most
@@ -520,8 +592,22 @@ moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* strea
     }
     const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)args->T * p.parts + 7) / 8, (int64_t)K.num_sms * 3);
     const cudaError_t e =
-        launch_pdl(append_kernel(K.s), dim3(grid), dim3(256), kAppendRing, static_cast<cudaStream_t>(stream), true, p);
+        launch_pdl(append_kernel(K.s, norm.q_weight || norm.k_weight), dim3(grid), dim3(256), kAppendRing,
+                   static_cast<cudaStream_t>(stream), true, p);
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "append launch");
+}
+
+moe_status moe_kv_append(moe_kv* kv, const moe_kv_append_args* args, void* stream) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    const moe_status st = check_append(&kv->K.d, args);
+    return st != MOE_OK || args->T == 0 ? st : append(kv, args, moe_kv_head_norm{}, stream);
+}
+
+moe_status moe_kv_append_norm(moe_kv* kv, const moe_kv_append_args* args, const moe_kv_head_norm* norm, void* stream) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    moe_status st = check_append(&kv->K.d, args);
+    if (st == MOE_OK) st = check_head_norm(norm);
+    return st != MOE_OK || args->T == 0 ? st : append(kv, args, *norm, stream);
 }
 
 moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* stream) {
@@ -534,6 +620,20 @@ moe_status moe_kv_attend(moe_kv* kv, const moe_kv_attend_args* args, void* strea
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
     return kv_attend_launch(K, *args, static_cast<cudaStream_t>(stream));
 }
+
+moe_status moe_kv_attend_chunk(moe_kv* kv, const moe_kv_chunk_args* args, void* stream) {
+    if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    Kv& K = kv->K;
+    const moe_status st = check_chunk(&K.d, args);
+    if (st != MOE_OK || args->B == 0 || args->T == 0) return st;
+    if (args->workspace_bytes < 0 || (size_t)args->workspace_bytes < kv_chunk_workspace(K))
+        return fail(MOE_E_INVALID, "workspace_bytes is below moe_kv_chunk_workspace");
+    DeviceGuard g(K.device);
+    if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
+    return kv_chunk_launch(K, *args, static_cast<cudaStream_t>(stream));
+}
+
+size_t moe_kv_chunk_workspace(const moe_kv* kv) { return kv ? kv_chunk_workspace(kv->K) : 0; }
 
 moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value) {
     if (!kv) return fail(MOE_E_INVALID, "NULL handle");

@@ -67,6 +67,10 @@ size_t kv_attend_workspace(const Kv& K, size_t out[3]);
 cudaError_t kv_attend_setup(Kv& K);
 // Whether the kernel's 32 bits count the chunks of B full rows of a block table.
 bool kv_attend_countable(const KvShape& s, int B, int max_pages);
+// Chunks of new tokens: bytes of the caller's workspace, and the call.
+size_t kv_chunk_workspace(const Kv& K);
+cudaError_t kv_chunk_setup(Kv& K);
+moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t s);
 moe_status kv_attend_launch(Kv& kv, const moe_kv_attend_args& a, cudaStream_t s);
 
 }  // namespace moe
