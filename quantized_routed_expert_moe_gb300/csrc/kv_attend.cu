@@ -49,6 +49,7 @@
 
 #include "common.cuh"
 #include "kv_cache.h"
+#include "kv_math.cuh"
 #include "moe_internal.h"
 #include "sm100.cuh"
 
@@ -59,7 +60,6 @@ namespace {
 constexpr int kRing = 16 * 1024;   // bytes of stages per warp
 constexpr int kHalf = 8 * 1024;    // of a chunk's keys, or values
 constexpr int kMaxCtas = 160;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // Compile-time shape of one kernel: head dimension, cache type, query heads / 8.
 template <int D_, bool FP8_, int NT_>
@@ -137,27 +137,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// two e4m3 values, the lower or upper two bytes of v, as an fp16 pair, exact
-__device__ __forceinline__ uint32_t e4m3_lo(uint32_t v) {
-    uint32_t d;
-    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(d) : "r"(v));
-    return d;
-}
-__device__ __forceinline__ uint32_t e4m3_hi(uint32_t v) {
-    uint32_t d;
-    asm("{.reg .b16 h, l; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(d) : "r"(v));
-    return d;
-}
 template <bool FP8>
 __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     if constexpr (FP8) {
@@ -167,16 +146,6 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
-}
-// tanh z, off by 8 units of 2^-24 relative to itself: up to 1/2 by an odd polynomial, fitted
-// to the least relative error there (1.5e-8), and where PAST, past it, by 1 - 2 / (exp(2 z) +
-// 1), whose error of 2^-22 would be the larger the nearer to zero.
-template <bool PAST>
-__device__ __forceinline__ float tanh_of(float z) {
-    const float u = z * z;
-    const float r = z * fmaf(fmaf(fmaf(fmaf(0.0172414916f, u, -0.0530454943f), u, 0.13325879f), u, -0.333331439f), u, 1.f);
-    if (!PAST || !(fabsf(z) > 0.5f)) return r;
-    return 1.f - 2.f * rcp(ex2(z * (2.f * kLog2e)) + 1.f);
 }
 // Two weights, each as the sum of two bf16 numbers: its upper 16 bits, and the rest
 // rounded, 2^-16 of the weight at most. The rest is above zero, so that an infinite value
