@@ -156,15 +156,6 @@ __device__ __forceinline__ void split_pair(float lo, float hi, uint32_t& upper, 
     rest = pack_pair<false>(fmaxf(lo - __uint_as_float(a & 0xffff0000u), 0x1p-126f),
                             fmaxf(hi - __uint_as_float(b & 0xffff0000u), 0x1p-126f));
 }
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* tm, int x, int y, int z, int w,
-                                            uint32_t bar, uint64_t pol) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst),
-        "l"(tm), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "l"(pol)
-        : "memory");
-}
-
 // Offset of byte `col` (within one line) of row `row` of a stage: rows of LINE
 // bytes, their 16-byte units exchanged as the TMA swizzle does, within 8 of them
 // (128-byte lines) or 4 (64-byte lines). Further column blocks follow CT * LINE on.
@@ -407,7 +398,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             __syncwarp();
             if (nx_page >= 0 && nx.b != p.stall)
-                tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
+                bw::tma_load_4d(ring + put * C::HALF + box_at, issued & 1 ? &tm_v : &tm_k, col * (C::FP8 ? 128 : 64), nx_slot,
                             nx.hk, nx_page, bar, pol);
             if (++put == C::STAGES) put = 0;
             if (!(++issued & 1)) lookup(++ahead, false);

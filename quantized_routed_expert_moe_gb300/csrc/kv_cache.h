@@ -55,6 +55,8 @@ struct Kv {
     // CTAs, and how many of a segment's CTAs have arrived
     CUtensorMap tm_k{}, tm_v{};
     int box_rows = 16;
+    CUtensorMap tm_chunk_k{}, tm_chunk_v{};
+    int chunk_box = 16;          // tokens of one of their boxes
     int stall = -1;              // MOE_KV_OPT_TEST_STALL
     float4 *part_o = nullptr, *part_ml = nullptr;
     int* arrived = nullptr;

@@ -1,92 +1,996 @@
-// Attention of a chunk of new tokens per sequence over a paged key-value cache: a warp
-// per token and query head, its cached positions one after the other.
+// Attention of a chunk of new tokens per sequence over a paged key-value cache, on the
+// 5th-generation tensor cores.
+//
+// The rows of a tile are (token, query head) pairs of one key-value head, tokens outermost:
+// all G = n_heads / n_kv_heads queries of a head share every key and value that is read, and
+// a chunk of few tokens still fills rows. A CTA takes two tiles of 128 rows at a time (heads
+// of 256: one) over the same blocks of 128 cached tokens:
+//
+//   S = Q K^T        both from shared memory, into 128 columns of tensor memory
+//   P = exp(S - m)   by a thread per row, its scores in registers, back over S as 16-bit numbers
+//   O += P V         P from tensor memory, V from shared memory (rows are K), O stays there
+//
+// so that the products of one tile run under the softmax of the other. The running maximum
+// m is raised only when a row's scores pass it by 2^8: until then the weights are at most
+// 2^8 and neither sum nor outputs need a factor. Heads of 256 channels leave room for one
+// tile: its two softmax groups take half the columns each, and S has two buffers.
+//
+// Split. All blocks of all tiles of the call, numbered tile by tile, are dealt out evenly and
+// contiguously to one CTA per SM from the lengths as they stand on the device. A tile that is
+// cut between CTAs leaves unnormalised parts in the workspace, which a second, small launch
+// joins in order.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
+#include <cuda_fp16.h>
 
 #include <algorithm>
 
 #include "common.cuh"
 #include "kv_cache.h"
+#include "kv_math.cuh"
 #include "moe_internal.h"
+#include "sm100.cuh"
 
 namespace moe {
 
 namespace {
 
+constexpr int kBlk = 128;              // cached tokens of a block
+constexpr int kRing = 16;              // blocks whose page flags are kept
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Compile-time shape of one kernel: head dimension, cache type, capped scores.
+template <int D_, bool FP8_, bool CAP_>
+struct Cfg {
+    static constexpr int D = D_;
+    static constexpr bool FP8 = FP8_, CAP = CAP_;
+    static constexpr int NS = D == 256 ? 1 : 2;          // row tiles in flight
+    static constexpr int ROWS = 128 * NS;
+    static constexpr int PARTS = D == 256 ? 2 : 1;       // stages of a block of keys (or values)
+    static constexpr int SR = kBlk / PARTS;              // tokens of a stage
+    static constexpr int PANEL = SR * 128, PANELS = D / 64;   // a stage is panels of 64 channels
+    static constexpr int STAGE = SR * D * 2;
+    static constexpr int QPANEL = 128 * 128, QTILE = 128 * D * 2;
+    static constexpr int NST = FP8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 4);
+    static constexpr int RAW = SR * D, NRAW = FP8 ? 3 : 0;    // 8-bit stages, before conversion
+    static constexpr int WARPS = FP8 ? 16 : 12, THREADS = 32 * WARPS;
+    static constexpr int COLS = NS == 2 ? 128 : 64;      // score columns of a softmax thread
+    static constexpr int O_AT = 256;                     // tensor-memory column of the outputs
+    static constexpr int READY = FP8 ? 4 : 2;            // warps that pass a stage on
+    // An 8-bit cache is exact in fp16, and so are queries scaled to their row's largest; the
+    // weights are 2^7 times their size, at most 2^15: 2^-31 of exp(m) is their smallest step.
+    static constexpr float UP = FP8 ? 7.f : 0.f, DOWN = FP8 ? 0x1p-7f : 1.f;
+    static constexpr size_t smem = 1024 + (size_t)NS * QTILE + (size_t)NST * STAGE + (size_t)NRAW * RAW;
+};
+
+// What a CTA left of a tile that is cut between CTAs.
+enum { REC_CUT = 1, REC_FIRST = 2, REC_LAST = 4 };
+struct Rec {
+    int flags, rows, row0, start, hk, pad[3];
+};
+
 struct ChunkArgs {
     moe_kv_chunk_args a;
     KvShape s;
-    const void *k_pages, *v_pages;
+    const void* v_pages;
     const float *k_scale, *v_scale;
     unsigned* health;
+    Rec* recs;          // [CTA][2]
+    float2* part_ml;    // [CTA][2][ROWS]: maximum (base two) and sum
+    float4* part_o;     // [CTA][2][D / 4][ROWS]
+    int G, box_rows;
 };
 
-__device__ __forceinline__ float cached(const void* pool, int64_t at, int e4m3) {
-    return e4m3 ? (float)static_cast<const __nv_fp8_e4m3*>(pool)[at]
-                : __bfloat162float(static_cast<const __nv_bfloat16*>(pool)[at]);
+// The blocks of one tile that a CTA takes.
+struct Part {
+    int b, hk, row0, rows;    // rows of the sequence's (token, head) pairs
+    int start, base;          // the sequence's first token row; position of its first new token
+    int lo, hi;               // positions that some row attends to
+    int all_lo, all_hi;       // positions that every row attends to
+    int blk0, n;              // blocks
+    int index, busy, gi;      // parts, parts with blocks, and blocks of this CTA before
+    bool first, last;         // of the tile
+};
+
+// Walks a CTA's parts; every role does so by itself.
+template <class C>
+struct Walk {
+    const int *start, *len;   // shared memory
+    int G, Hk, window, b, i, hk, off, index, busy, gi;
+    long long left;
+
+    __device__ __forceinline__ static int blocks_of(int lo, int hi) { return hi > lo ? (hi + kBlk - 1) / kBlk - lo / kBlk : 0; }
+    __device__ __forceinline__ static int first_seen(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
+    __device__ __forceinline__ bool next(Part& q) {
+        if (left <= 0) return false;
+        const int n = start[b + 1] - start[b], R = n * G;
+        q.b = b;
+        q.hk = hk;
+        q.row0 = i * C::ROWS;
+        q.rows = min(R - q.row0, C::ROWS);
+        q.start = start[b];
+        q.base = len[b] - n;
+        const int p0 = q.base + q.row0 / G, p1 = q.base + (q.row0 + q.rows - 1) / G;
+        q.lo = first_seen(p0, window);
+        q.hi = p1 + 1;
+        q.all_lo = first_seen(p1, window);
+        q.all_hi = p0 + 1;
+        const int c = blocks_of(q.lo, q.hi), units = max(c, 1);
+        const int take = (int)min((long long)(units - off), left);
+        q.blk0 = q.lo / kBlk + off;
+        q.n = c ? take : 0;
+        q.first = off == 0;
+        q.index = index++;
+        q.busy = busy;
+        busy += q.n > 0;
+        q.gi = gi;
+        gi += q.n;
+        left -= take;
+        off += take;
+        q.last = off == units;
+        if (q.last) {
+            off = 0;
+            if (++hk == Hk) {
+                hk = 0;
+                if (++i > (R - 1) / C::ROWS) {
+                    i = 0;
+                    if (left > 0)
+                        do ++b;
+                        while (start[b + 1] == start[b]);
+                }
+            }
+        }
+        return true;
+    }
+};
+
+template <class T>
+__device__ __forceinline__ T scan_up(T v) {   // inclusive, over a warp
+    for (int o = 1; o < 32; o <<= 1) {
+        const T u = __shfl_up_sync(~0u, v, o);
+        if ((int)(threadIdx.x % 32) >= o) v += u;
+    }
+    return v;
+}
+// Sum of v over the threads before this one, and over all of them.
+template <class T, int WARPS>
+__device__ __forceinline__ T scan_cta(T v, T* sums, T& total) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const T incl = scan_up(v);
+    __syncthreads();
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    T before = incl - v;
+    total = 0;
+    for (int w = 0; w < WARPS; ++w) {
+        if (w < warp) before += sums[w];
+        total += sums[w];
+    }
+    return before;
 }
 
-template <int D>
-__global__ void __launch_bounds__(256) k_kv_chunk(const ChunkArgs p) {
-    constexpr int C = D / 32;
-    const KvShape& s = p.s;
-    const int lane = threadIdx.x % 32, heads = s.n_heads;
-    pdl_wait();
-    pdl_trigger();
-    uint32_t bits = 0;
-    bool bad = p.a.starts[0] < 0 || p.a.starts[p.a.B] > p.a.T;
-    for (int b = 0; b < p.a.B; ++b) bad |= p.a.starts[b] > p.a.starts[b + 1];
-    if (bad) {
-        if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(p.health, MOE_KV_BAD_START);
-        return;
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// x * y + z of both halves
+__device__ __forceinline__ void fma2(float& a, float& b, float y, float z) {
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %3};"
+        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
+        : "+f"(a), "+f"(b)
+        : "f"(y), "f"(z));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float y, float z) {
+    asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "+f"(a), "+f"(b)
+        : "f"(y), "f"(z));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    if constexpr (F16) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&h);
     }
-    const int first = p.a.starts[0], rows = p.a.starts[p.a.B] - first;
-    for (int64_t w = blockIdx.x * 8 + threadIdx.x / 32; w < (int64_t)rows * heads; w += gridDim.x * 8) {
-        const int t = first + (int)(w / heads), head = (int)(w % heads), hk = head / (heads / s.n_kv_heads);
-        int b = 0;
-        while (p.a.starts[b + 1] <= t) ++b;
+}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ bool all_lanes(bool x) { return __all_sync(~0u, x) != 0; }
+
+// The stages of a part in the order in which the products take them: f(values?, block).
+template <class C, class F>
+__device__ __forceinline__ void each_block(int n, F f) {
+    if (C::NS == 2) {
+        for (int j = 0; j < n; ++j) {
+            f(false, j);
+            f(true, j);
+        }
+    } else if (n > 0) {
+        f(false, 0);
+        for (int j = 0; j < n; ++j) {
+            if (j + 1 < n) f(false, j + 1);
+            f(true, j);
+        }
+    }
+}
+
+template <class C>
+struct Shared {
+    uint64_t full[C::FP8 ? C::NRAW : C::NST], raw_free[4], ready[C::NST], empty[C::NST];
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    long long sums[C::WARPS];
+    long long rem;                    // where this CTA's first tile starts, in units
+    uint32_t tmem;
+    int abort, bad_start, first;
+    uint8_t pages[kRing][2];          // per block and part: groups of 16 tokens whose page is in the pool
+    uint8_t odd[8][4];                // per part and warp: values that are not finite were set aside
+    float row_max[2][2][C::NS == 1 ? 128 : 1], row_sum[2][C::NS == 1 ? 128 : 1];
+    int start[1025], len[1024];
+};
+
+template <class C>
+__global__ void __launch_bounds__(C::THREADS, 1)
+    k_kv_chunk(const ChunkArgs p, const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v) {
+    constexpr int D = C::D, NST = C::NST, G16 = C::SR / 16;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(16) Shared<C> sm;
+    const KvShape& s = p.s;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, B = p.a.B, G = p.G;
+    const uint32_t base = (bw::saddr(smem_raw) + 1023) & ~1023u;
+    const uint32_t q_at = base, stages = base + C::NS * C::QTILE, raws = stages + NST * C::STAGE;
+    const uint32_t full = bw::saddr(sm.full), raw_free = bw::saddr(sm.raw_free), ready = bw::saddr(sm.ready),
+                   empty = bw::saddr(sm.empty), q_full = bw::saddr(sm.q_full), s_full = bw::saddr(sm.s_full),
+                   p_full = bw::saddr(sm.p_full), o_done = bw::saddr(sm.o_done), o_free = bw::saddr(sm.o_free),
+                   drain = bw::saddr(&sm.drain);
+    uint32_t bits = 0;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            if (!C::FP8) bw::mbar_init(full + 8 * i, 1);
+            bw::mbar_init(ready + 8 * i, C::READY);
+            bw::mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < C::NRAW; ++i) {
+            bw::mbar_init(full + 8 * i, 1);
+            bw::mbar_init(raw_free + 8 * i, 4);
+        }
+        for (int i = 0; i < 2; ++i) {
+            bw::mbar_init(q_full + 8 * i, C::NS == 2 ? 4 : 8);
+            bw::mbar_init(s_full + 8 * i, 1);
+            bw::mbar_init(p_full + 8 * i, C::NS == 2 ? 4 : 8);
+            bw::mbar_init(o_done + 8 * i, 1);
+            bw::mbar_init(o_free + 8 * i, C::NS == 2 ? 4 : 8);
+        }
+        bw::mbar_init(drain, 1);
+        sm.abort = sm.bad_start = 0;
+        bw::mbar_fence_init();
+        bw::tma_prefetch_desc(&tm_k);
+        bw::tma_prefetch_desc(&tm_v);
+    }
+    if (warp == 8) bw::tmem_alloc(bw::saddr(&sm.tmem), 512);
+    bw::tc_fence_before();
+    __syncthreads();
+    bw::tc_fence_after();
+    const uint32_t tmem = *const_cast<volatile uint32_t*>(&sm.tmem);
+    pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
+    pdl_trigger();
+
+    // ---- tiles of every sequence, blocks of every tile, this CTA's share of them ---------------
+    Walk<C> walk;
+    {
+        int* const pre = reinterpret_cast<int*>(smem_raw + (base - bw::saddr(smem_raw)));   // tiles before a sequence
         const int most = p.a.max_pages * s.page_size;
-        int len = p.a.lens[b];
-        if (len > most) {
-            bits |= MOE_KV_BAD_LENGTH;
-            len = most;
+        const int per = (B + C::THREADS - 1) / C::THREADS, b0 = threadIdx.x * per, b1 = min(B, b0 + per);
+        int mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int s0 = p.a.starts[b], s1 = p.a.starts[b + 1];
+            int len = max(p.a.lens[b], 0);
+            if (len > most) {
+                len = most;
+                bits |= MOE_KV_BAD_LENGTH;
+            }
+            if (s0 < 0 || s1 < s0 || s1 > p.a.T) sm.bad_start = 1;
+            sm.start[b] = s0;
+            if (b == B - 1) sm.start[B] = s1;
+            sm.len[b] = len;
+            mine += s1 > s0 ? ((s1 - s0) * G - 1) / C::ROWS + 1 : 0;
         }
-        const int pos = len - (p.a.starts[b + 1] - t);
-        float q[C], o[C] = {}, m = -INFINITY, l = 0.f;
-        for (int c = 0; c < C; ++c)
-            q[c] = __bfloat162float(static_cast<const __nv_bfloat16*>(p.a.q)[t * p.a.q_stride + head * D + 32 * c + lane]);
-        const float ks = p.k_scale[hk], vs = p.v_scale[hk];
-        for (int j = p.a.window > 0 ? max(0, pos - p.a.window + 1) : 0; j <= pos; ++j) {
-            const int page = kv_page(s, p.a.block_table[(int64_t)b * p.a.max_pages + j / s.page_size], bits);
-            if (page < 0) continue;
-            const int64_t at = kv_offset(s, page, hk, j % s.page_size) + lane;
-            float z = 0.f;
-            for (int c = 0; c < C; ++c) z += q[c] * cached(p.k_pages, at + 32 * c, s.e4m3);
-            z = warp_sum(z) * ks * p.a.scale;
-            if (p.a.softcap > 0) z = p.a.softcap * tanhf(z / p.a.softcap);
-            const float mn = fmaxf(m, z), base = mn == -INFINITY ? 0.f : mn, f = expf(m - base), e = expf(z - base);
-            l = l * f + e;
-            for (int c = 0; c < C; ++c) o[c] = o[c] * f + e * cached(p.v_pages, at + 32 * c, s.e4m3);
-            m = mn;
+        long long tiles;
+        long long run = scan_cta<long long, C::WARPS>(mine, sm.sums, tiles);
+        for (int b = b0; b < b1; ++b) {
+            pre[b] = (int)run;
+            const int n = sm.start[b + 1] - sm.start[b];
+            run += n > 0 ? (n * G - 1) / C::ROWS + 1 : 0;
         }
-        const float r = l == 0.f ? 0.f : vs / l;
-        for (int c = 0; c < C; ++c)
-            static_cast<__nv_bfloat16*>(p.a.out)[((int64_t)t * heads + head) * D + 32 * c + lane] = __float2bfloat16(o[c] * r);
-        if (lane == 0 && p.a.lse) p.a.lse[(int64_t)t * heads + head] = l == 0.f ? -INFINITY : m + logf(l);
+        if (threadIdx.x == 0) pre[B] = (int)tiles;
+        __syncthreads();
+        // units of tile r of all heads; a tile without blocks counts as one
+        auto find = [&](int r) {
+            int lo = 0, hi = B;   // the last b with pre[b] <= r that has tiles
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (pre[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            return lo;
+        };
+        auto per_head = [&](int r) {
+            const int b = find(r), n = sm.start[b + 1] - sm.start[b], row0 = (r - pre[b]) * C::ROWS;
+            const int p0 = sm.len[b] - n + row0 / G, p1 = sm.len[b] - n + (min(row0 + C::ROWS, n * G) - 1) / G;
+            return max(Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1), 1);
+        };
+        walk.left = 0;
+        if (!sm.bad_start) {
+            const int rt = (int)tiles;
+            long long total = 0, sum = 0;
+            for (int r = threadIdx.x; r < rt; r += C::THREADS) sum += (long long)per_head(r) * s.n_kv_heads;
+            scan_cta<long long, C::WARPS>(sum, sm.sums, total);
+            const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
+            const long long from = c < ctas ? total * c / ctas : total, to = c < ctas ? total * (c + 1) / ctas : total;
+            walk.left = to - from;
+            long long before = 0;
+            for (int r0 = 0; walk.left > 0 && r0 < rt && before <= from; r0 += C::THREADS) {
+                const int r = r0 + threadIdx.x;
+                const long long u = r < rt ? (long long)per_head(r) * s.n_kv_heads : 0;
+                long long chunk;
+                const long long at = before + scan_cta<long long, C::WARPS>(u, sm.sums, chunk);
+                if (at <= from && from < at + u) {
+                    sm.first = r;
+                    sm.rem = from - at;
+                }
+                before += chunk;
+            }
+            __syncthreads();
+            if (walk.left > 0) {
+                const int r = sm.first, b = find(r), u = per_head(r);
+                walk.b = b;
+                walk.i = r - pre[b];
+                walk.hk = (int)(sm.rem / u);
+                walk.off = (int)(sm.rem % u);
+            }
+        } else if (threadIdx.x == 0) {
+            bits |= MOE_KV_BAD_START;
+        }
+        walk.start = sm.start;
+        walk.len = sm.len;
+        walk.G = G;
+        walk.Hk = s.n_kv_heads;
+        walk.window = p.a.window;
+        walk.index = walk.busy = walk.gi = 0;
+        bw::fence_async_smem();   // `pre` lies where copies will land
+        __syncthreads();
+    }
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return all_lanes(bw::mbar_wait(bar, parity & 1, &sm.abort, p.health, MOE_KV_TIMEOUT, kWaitNs));
+    };
+
+    if (warp >= 8) {
+        if (warp < 12) regs_down<56>();
+        else regs_down<72>();
+    }
+    Part q;
+    if (warp == 9) {
+        // ---- copies: a lane per box --------------------------------------------------------------
+        constexpr int RING = C::FP8 ? C::NRAW : NST, BYTES = C::FP8 ? C::RAW : C::STAGE;
+        constexpr int WIDTH = C::FP8 ? 1 : C::PANELS;
+        const uint32_t at = C::FP8 ? raws : stages, gone = C::FP8 ? raw_free : empty;
+        const int boxes = C::SR / p.box_rows, box = lane % boxes, panel = lane / boxes;
+        const uint32_t box_bytes = p.box_rows * (C::FP8 ? D : 128);
+        const uint64_t pol = bw::l2_evict_normal();
+        uint32_t it = 0;
+        bool ok = true;
+        while (walk.next(q))
+            each_block<C>(q.n, [&](bool values, int j) {
+                for (int part = 0; part < C::PARTS; ++part, ++it) {
+                    const int pos = (q.blk0 + j) * kBlk + part * C::SR + box * p.box_rows;
+                    const bool need = panel < WIDTH && pos < q.hi && pos + p.box_rows > q.lo;
+                    int page = -1;
+                    if (need) page = kv_page(s, p.a.block_table[(int64_t)q.b * p.a.max_pages + pos / s.page_size], bits);
+                    const uint32_t st = it % RING, bar = full + 8 * st;
+                    ok = wait(gone + 8 * st, (it / RING) + 1) && ok;
+                    const uint32_t lost = __ballot_sync(~0u, need && page < 0), come = __ballot_sync(~0u, need && page >= 0);
+                    if (lane == 0) {
+                        uint32_t groups = 0;
+                        for (int g = 0; g < G16; ++g) groups |= (lost >> (g * 16 / p.box_rows) & 1 ? 0u : 1u) << g;
+                        sm.pages[(q.gi + j) % kRing][part] = (uint8_t)groups;
+                        if (ok) bw::mbar_arrive_tx(bar, __popc(come) * box_bytes);
+                    }
+                    __syncwarp();
+                    if (ok && need && page >= 0)
+                        bw::tma_load_4d(at + st * BYTES + (C::FP8 ? 0 : panel * C::PANEL) + box * box_bytes, values ? &tm_v : &tm_k,
+                                        panel * 64, pos % s.page_size, q.hk, page, bar, pol);
+                    if (!ok) --it;   // nothing was issued
+                }
+            });
+        // no copy is in flight at the end, after a wait that ran out either
+        int none = 0;
+        for (uint32_t i = it > (uint32_t)RING ? it - RING : 0; i < it; ++i)
+            bw::mbar_wait(full + 8 * (i % RING), (i / RING) & 1, &none, nullptr, 0, kWaitNs);
+    } else if (warp == 8) {
+        // ---- products ------------------------------------------------------------------------------
+        constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
+        uint32_t it = 0, parts[2] = {0, 0}, uses[2] = {0, 0};   // stages; parts and blocks of a slot (of NS == 1: the first's)
+        bool ok = true;
+        auto scores = [&](int slot, uint32_t stage, uint32_t to) {
+            if (ok && bw::elect_one()) {
+                const uint32_t a = q_at + slot * C::QTILE, b = stages + stage * C::STAGE;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    bw::mma_f16(to, bw::desc_sw128(a + (k / 4) * C::QPANEL + (k % 4) * 32),
+                                bw::desc_sw128(b + (k / 4) * C::PANEL + (k % 4) * 32), id_qk, k > 0);
+            }
+            __syncwarp();
+        };
+        auto outputs = [&](uint32_t weights, uint32_t stage, uint32_t to, bool more) {
+            if (ok && bw::elect_one()) {
+                const uint32_t b = stages + stage * C::STAGE;
+#pragma unroll
+                for (int k = 0; k < C::SR / 16; ++k)
+                    bw::mma_f16_ta(to, weights + 8 * k, bw::desc_sw128_mn(b + k * 2048, C::PANEL), id_pv, more || k > 0);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint32_t bar) {
+            if (ok && bw::elect_one()) bw::mma_commit(bar);
+            __syncwarp();
+        };
+        auto stage_in = [&] { ok = wait(ready + 8 * (it % NST), it / NST) && ok; bw::tc_fence_after(); };
+        while (walk.next(q)) {
+            if (q.n == 0) continue;
+            if constexpr (C::NS == 2) {
+                const bool two = q.rows > 128;
+                // scores of a block by both tiles, given that its keys are the next stage
+                auto scores_of = [&](int slot) {
+                    scores(slot, it % NST, tmem + slot * 128);
+                    commit(s_full + 8 * slot);
+                    if (slot == 1 || !two) commit(empty + 8 * (it % NST));
+                };
+                ok = wait(q_full, parts[0]) && ok;
+                stage_in();
+                scores_of(0);
+                if (two) {
+                    ok = wait(q_full + 8, parts[1]) && ok;
+                    bw::tc_fence_after();
+                    scores_of(1);
+                }
+                ++it;
+                for (int j = 0; j < q.n; ++j) {
+                    const uint32_t v = it;
+                    stage_in();
+                    ++it;
+                    for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
+                        ok = wait(p_full + 8 * slot, uses[slot]++) && ok;
+                        if (j == 0) ok = wait(o_free + 8 * slot, parts[slot]++ + 1) && ok;
+                        bw::tc_fence_after();
+                        outputs(tmem + slot * 128, v % NST, tmem + C::O_AT + slot * D, j > 0);
+                        commit(o_done + 8 * slot);
+                        if (slot == 1 || !two) commit(empty + 8 * (v % NST));
+                        if (j + 1 < q.n) {
+                            if (slot == 0) stage_in();
+                            scores_of(slot);
+                        }
+                    }
+                    if (j + 1 < q.n) ++it;
+                }
+            } else {
+                auto scores_of = [&](uint32_t use) {
+                    for (int part = 0; part < C::PARTS; ++part, ++it) {
+                        stage_in();
+                        scores(0, it % NST, tmem + (use & 1) * 128 + part * C::SR);
+                        commit(empty + 8 * (it % NST));
+                    }
+                    commit(s_full + 8 * (use & 1));
+                };
+                ok = wait(q_full, parts[0]) && ok;
+                scores_of(uses[0]);
+                for (int j = 0; j < q.n; ++j) {
+                    const uint32_t use = uses[0]++;
+                    if (j + 1 < q.n) scores_of(use + 1);
+                    ok = wait(p_full + 8 * (use & 1), use >> 1) && ok;
+                    if (j == 0) ok = wait(o_free, parts[0]++ + 1) && ok;
+                    for (int part = 0; part < C::PARTS; ++part, ++it) {
+                        stage_in();
+                        outputs(tmem + (use & 1) * 128 + part * (C::SR / 2), it % NST, tmem + C::O_AT, j > 0 || part > 0);
+                        commit(empty + 8 * (it % NST));
+                    }
+                    commit(o_done);
+                }
+            }
+        }
+        // no product is running at the end
+        if (bw::elect_one()) bw::mma_commit(drain);
+        __syncwarp();
+        int none = 0;
+        bw::mbar_wait(drain, 0, &none, nullptr, 0, kWaitNs);
+    } else if (C::FP8 ? warp >= 12 : warp >= 10) {
+        // ---- between the copies and the products: 8-bit values become fp16; of values that not
+        // every row attends to, rows that none does become zero, and what is not finite too (a
+        // weight of zero would not hide it): its sign to the rows that see it is settled at their end
+        constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = C::FP8 ? 12 : 10, TEAM = 32 * C::READY;
+        const int me = threadIdx.x - 32 * FIRST;
+        uint32_t it = 0;
+        while (walk.next(q)) {
+            if (q.n == 0) continue;
+            volatile uint8_t* const odd = &sm.odd[q.busy % 8][warp - FIRST];
+            if (lane == 0) *odd = 0;
+            __syncwarp();
+            each_block<C>(q.n, [&](bool values, int j) {
+                const int pos = (q.blk0 + j) * kBlk;
+                const bool part_seen = pos < q.all_lo || pos + kBlk > q.all_hi;
+                for (int part = 0; part < C::PARTS; ++part, ++it) {
+                    const int p0 = pos + part * C::SR;
+                    wait(full + 8 * (it % RING), it / RING);
+                    const uint32_t pages = *const_cast<volatile uint8_t*>(&sm.pages[(q.gi + j) % kRing][part]);
+                    const bool look = values && (part_seen || pages != (1u << G16) - 1);
+                    auto live = [&](int row) { return p0 + row >= q.lo && p0 + row < q.hi && (pages >> (row / 16) & 1); };
+                    const uint32_t stage = stages + (it % NST) * C::STAGE;
+                    if constexpr (C::FP8) {
+                        wait(empty + 8 * (it % NST), it / NST + 1);
+                        const uint32_t raw = raws + (it % RING) * C::RAW;
+#pragma unroll 4
+                        for (int i = me; i < C::RAW / 16; i += TEAM) {
+                            const int row = i / (D / 16), u = i % (D / 16), panel = u / 4, unit = 2 * (u % 4);
+                            uint4 w = ld_shared(raw + i * 16);
+                            if (look) {
+                                uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                                const bool on = live(row);
+                                for (int k = 0; k < 4; ++k) {
+                                    // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
+                                    const uint32_t nan = (((x[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                                    if (!on) x[k] = 0;
+                                    else if (part_seen && nan) {
+                                        x[k] &= ~(nan * 0xffu);
+                                        *odd = 1;
+                                    }
+                                }
+                                w = make_uint4(x[0], x[1], x[2], x[3]);
+                            }
+                            uint4 h[2] = {make_uint4(e4m3_lo(w.x), e4m3_hi(w.x), e4m3_lo(w.y), e4m3_hi(w.y)),
+                                          make_uint4(e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w))};
+                            // odd panels store their second half first, so that a row's eight lanes
+                            // meet eight banks' groups
+                            const uint32_t to = stage + panel * C::PANEL + row * 128;
+                            const int f = panel & 1;
+                            st_shared(to + (((unit + f) ^ (row & 7)) << 4), f ? h[1] : h[0]);
+                            st_shared(to + (((unit + 1 - f) ^ (row & 7)) << 4), f ? h[0] : h[1]);
+                        }
+                        bw::fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) bw::mbar_arrive(raw_free + 8 * (it % RING));
+                    } else if (look) {
+                        for (int i = me; i < C::STAGE / 16; i += TEAM) {
+                            const int row = i / 8 % C::SR;   // units change places within a row only
+                            uint4 w = ld_shared(stage + i * 16);
+                            uint32_t x[4] = {w.x, w.y, w.z, w.w}, changed = 0;
+                            const bool on = live(row);
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t before = x[k];
+                                if (!on) x[k] = 0;
+                                else if (part_seen) {
+                                    if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u, *odd = 1;
+                                    if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0xffffu, *odd = 1;
+                                }
+                                changed |= before ^ x[k];
+                            }
+                            if (changed) st_shared(stage + i * 16, make_uint4(x[0], x[1], x[2], x[3]));
+                        }
+                        bw::fence_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0) bw::mbar_arrive(ready + 8 * (it % NST));
+                }
+            });
+        }
+    } else if (warp < 8) {
+        // ---- softmax: a thread per row (heads of 256: two, by columns) -----------------------------
+        if constexpr (C::FP8) regs_up<192>();
+        else regs_up<224>();
+        const int wg = warp / 4, slot = C::NS == 2 ? wg : 0, row = threadIdx.x % 128;
+        const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
+        const uint32_t o_at = lanes + C::O_AT + (C::NS == 2 ? slot * D : wg * (D / 2));
+        constexpr int OC = C::NS == 2 ? D : D / 2;       // output channels of a thread
+        const int ch0 = C::NS == 2 ? 0 : wg * OC;
+        const int64_t token_heads = s.n_heads;
+        uint32_t uses = 0, written = 0;                  // blocks of this slot; cut sides recorded
+        bool ok = true;
+        const float scale = fabsf(p.a.scale) < 0x1p-100f ? 0x1p-100f : fabsf(p.a.scale);
+        const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
+        float c_next = 0.f;
+
+        auto out_row = [&](const Part& q, int r) {       // row of out and lse
+            return (int64_t)(q.start + (q.row0 + r) / G) * token_heads + q.hk * G + (q.row0 + r) % G;
+        };
+        // this thread's row of queries, to shared memory
+        auto load_q = [&](const Part& q) {
+            const int r = slot * 128 + row;
+            const bool on = r < q.rows;
+            const int t = q.start + (q.row0 + r) / G, head = q.hk * G + (q.row0 + r) % G;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)t * p.a.q_stride +
+                                                              (int64_t)head * D);
+            uint4 v[OC / 8];
+#pragma unroll
+            for (int i = 0; i < OC / 8; ++i) v[i] = on ? src[ch0 / 8 + i] : make_uint4(0, 0, 0, 0);
+            float c = scale * p.k_scale[q.hk];
+            float up = 1.f;
+            if constexpr (C::FP8) {
+                // by a power of two, so that the row's largest lies in [2^14, 2^15)
+                uint32_t big = 0;
+                auto look = [&](uint4 w) {
+                    for (uint32_t x : {w.x, w.y, w.z, w.w}) big = max(big, max(x & 0x7fffu, x >> 16 & 0x7fffu));
+                };
+#pragma unroll
+                for (int i = 0; i < OC / 8; ++i) look(v[i]);
+                if (C::NS == 1 && on)
+                    for (int i = 0; i < OC / 8; ++i) look(src[(wg ? 0 : OC / 8) + i]);
+                // exponent field e: the largest is below 2^(e - 126); a factor within fp32's range
+                const int e = big >> 7, by = big == 0 || e == 255 ? 0 : max(-126, min(126, 141 - e));
+                up = exp2i(by);
+                c *= exp2i(-by);
+            }
+#pragma unroll
+            for (int i = 0; i < OC / 8; ++i) {
+                uint32_t x[4] = {v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
+                if constexpr (C::FP8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = pack2<true>(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
+                const int unit = ch0 / 8 + i;
+                st_shared(q_at + slot * C::QTILE + unit / 8 * C::QPANEL + row * 128 + ((unit % 8 ^ (row & 7)) << 4),
+                          make_uint4(x[0], x[1], x[2], x[3]));
+            }
+            bw::fence_async_smem();
+            __syncwarp();
+            if (lane == 0) bw::mbar_arrive(q_full + 8 * slot);
+            c_next = c;
+        };
+        // the next part with blocks for this group; rows of parts without any are written at once
+        auto advance = [&](Part& q) {
+            while (walk.next(q)) {
+                const int r = slot * 128 + row;
+                if (C::NS == 2 && slot && q.rows <= 128) continue;
+                if (q.n) return true;
+                if (r < q.rows) {
+                    const int64_t o = out_row(q, r);
+                    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D + ch0);
+                    for (int i = 0; i < OC / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
+                    if (p.a.lse && ch0 == 0) p.a.lse[o] = -INFINITY;
+                }
+            }
+            return false;
+        };
+
+        bool have = advance(q);
+        if (have) load_q(q);
+        while (have) {
+            const float c = C::CAP ? 1.f : c_next * kLog2e;
+            const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
+            const int pos = q.base + (q.row0 + slot * 128 + row) / G;
+            const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
+            float m = -INFINITY, m_raw = 0.f, l0 = 0.f, l1 = 0.f;   // maximum (scaled, base two; as it came), sums
+#pragma unroll 1
+            for (int j = 0; j < q.n; ++j, ++uses) {
+                const int buf = C::NS == 2 ? slot : uses & 1, phase = C::NS == 2 ? uses : uses >> 1;
+                const int at = (q.blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
+                const uint32_t s_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * C::COLS);
+                ok = wait(s_full + 8 * buf, phase) && ok;
+                bw::tc_fence_after();
+                float x[C::COLS];
+#pragma unroll
+                for (int i = 0; i < C::COLS / 32; ++i) bw::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x) + 32 * i);
+#pragma unroll
+                for (int i = 0; i < C::COLS / 32; ++i) bw::tmem_wait_ld32(reinterpret_cast<uint32_t*>(x) + 32 * i);
+                if constexpr (C::CAP) {
+#pragma unroll
+                    for (int i = 0; i < C::COLS; ++i) x[i] = tanh_of<true>(x[i] * to_cap) * cap;
+                }
+                const volatile uint8_t* pages = sm.pages[(q.gi + j) % kRing];
+                const uint32_t in = C::NS == 2 ? pages[0] : pages[wg];
+                if (at < q.all_lo || at + C::COLS > q.all_hi || in != (1u << C::COLS / 16) - 1) {
+                    const int a = see0 - at, b = see1 - at;
+#pragma unroll
+                    for (int i = 0; i < C::COLS; ++i)
+                        if (i < a || i >= b || !(in >> (i / 16) & 1)) x[i] = -INFINITY;
+                }
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int i = 0; i < C::COLS; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[i + 2 * k], x[i + 2 * k + 1]));
+                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                if constexpr (C::NS == 1) {
+                    sm.row_max[uses & 1][wg][row] = top;
+                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    top = fmaxf(top, sm.row_max[uses & 1][wg ^ 1][row]);
+                }
+                const float cand = top * c;
+                const bool raise = cand > m + 8.f;
+                if (__any_sync(~0u, raise)) {
+                    const float f = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - cand);
+                    if (raise) {
+                        m = cand;
+                        m_raw = top;
+                    }
+                    l0 *= f;
+                    l1 *= f;
+                    if (j > 0) {
+                        ok = wait(o_done + 8 * slot, uses - 1) && ok;
+                        bw::tc_fence_after();
+#pragma unroll 1
+                        for (int i = 0; i < OC; i += 32) {
+                            uint32_t o[32];
+                            bw::tmem_ld32(o_at + i, o);
+                            bw::tmem_wait_ld32(o);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            bw::tmem_st32(o_at + i, o);
+                        }
+                    }
+                }
+                // exp2(x c - m): one rounding, and a maximum that is itself rounded shifts all
+                // weights of a row alike; past 2^20 that shift would be seen, and the
+                // difference is taken first
+                const float mu = m == -INFINITY ? 0.f : m;
+                if (__any_sync(~0u, fabsf(mu) > 0x1p20f)) {
+                    const float raw = m == -INFINITY ? 0.f : m_raw;
+#pragma unroll
+                    for (int i = 0; i < C::COLS; ++i) x[i] = (x[i] - raw) * c + C::UP;
+                } else {
+                    const float minus = C::UP - mu;
+#pragma unroll
+                    for (int i = 0; i < C::COLS; i += 2) fma2(x[i], x[i + 1], c, minus);
+                }
+                float a0 = 0.f, a1 = 0.f;
+                uint32_t w[C::COLS / 2];
+#pragma unroll
+                for (int i = 0; i < C::COLS; i += 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[i + k] = ex2(x[i + k]);
+                    add2(l0, l1, x[i], x[i + 1]);
+                    add2(a0, a1, x[i + 2], x[i + 3]);
+                    w[i / 2] = pack2<C::FP8>(x[i], x[i + 1]);
+                    w[i / 2 + 1] = pack2<C::FP8>(x[i + 2], x[i + 3]);
+                }
+                l0 += a0;
+                l1 += a1;
+                const uint32_t p_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * (C::COLS / 2));
+#pragma unroll
+                for (int i = 0; i < C::COLS / 64; ++i) bw::tmem_st32(p_at + 32 * i, w + 32 * i);
+                bw::tmem_wait_st();
+                bw::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bw::mbar_arrive(p_full + 8 * buf);
+            }
+            // the next part's queries go ahead of this one's end
+            Part nq;
+            const bool more = advance(nq);
+            if (more) load_q(nq);
+
+            float l = l0 + l1;
+            if constexpr (C::NS == 1) {
+                sm.row_sum[wg][row] = l;
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                l = sm.row_sum[0][row] + sm.row_sum[1][row];
+            }
+            // (heads of 256: the last scores do not wait for the last but one product, and a
+            // parity tells a phase from its neighbours only)
+            if (C::NS == 1 && q.n > 1) ok = wait(o_done, uses - 2) && ok;
+            ok = wait(o_done + 8 * slot, uses - 1) && ok;
+            bw::tc_fence_after();
+            const int r = slot * 128 + row;
+            const bool cut = !(q.first && q.last), on = r < q.rows;
+            const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
+            const volatile uint8_t* f = sm.odd[q.busy % 8];
+            bool odd = false;
+            for (int i = 0; i < C::READY; ++i) odd |= f[i] != 0;
+            if (cut && threadIdx.x == 0) {
+                written |= 1u << side;
+                p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
+            }
+            if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, l);
+            const float inv = l == 0.f ? 0.f : p.v_scale[q.hk] / l;
+            const int64_t o_row = on ? out_row(q, r) : 0;
+#pragma unroll 1
+            for (int i = 0; i < OC; i += 32) {
+                uint32_t o[32];
+                bw::tmem_ld32(o_at + i, o);
+                bw::tmem_wait_ld32(o);
+                if (odd && on) {
+                    // what is not finite among the values set aside goes to the rows that see it
+                    for (int j = 0; j < q.n; ++j) {
+                        const int p0 = (q.blk0 + j) * kBlk;
+                        if (p0 >= q.all_lo && p0 + kBlk <= q.all_hi) continue;
+                        for (int at = max(p0, see0); at < min(p0 + kBlk, see1); ++at) {
+                            const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + at / s.page_size];
+                            if (page < 0 || page >= s.n_pages) continue;
+                            const int64_t from = kv_offset(s, page, q.hk, at % s.page_size) + ch0 + i;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) {
+                                float v;
+                                if constexpr (C::FP8)
+                                    v = (static_cast<const uint8_t*>(p.v_pages)[from + k] & 0x7f) == 0x7f ? NAN : 0.f;
+                                else v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pages)[from + k]);
+                                if (!isfinite(v)) o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
+                            }
+                        }
+                    }
+                }
+                if (cut && on) {
+                    float4* to = p.part_o + ((int64_t)rec * (D / 4) + (ch0 + i) / 4) * C::ROWS + r;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        to[k * C::ROWS] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                      __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                } else if (on) {
+                    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o_row * D + ch0 + i);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        uint32_t h[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            h[e] = pack2<false>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                        to[k] = make_uint4(h[0], h[1], h[2], h[3]);
+                    }
+                }
+            }
+            bw::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) bw::mbar_arrive(o_free + 8 * slot);
+            if (!cut && on && p.a.lse && ch0 == 0) p.a.lse[o_row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l * C::DOWN);
+            have = more;
+            q = nq;
+        }
+        if (threadIdx.x == 0)
+            for (int side = 0; side < 2; ++side)
+                if (!(written >> side & 1)) p.recs[blockIdx.x * 2 + side].flags = 0;
     }
     if (bits) atomicOr(p.health, bits);
+    bw::tc_fence_before();
+    __syncthreads();
+    if (warp == 8) {
+        bw::tc_fence_after();
+        bw::tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of the tiles that were cut between CTAs, in order: a CTA per CTA that began
+// such a tile and 32 of its rows, a lane per row, four channels at a time.
+template <class C>
+__global__ void __launch_bounds__(256) k_kv_chunk_join(const ChunkArgs p, int ctas) {
+    constexpr int D = C::D, V = D / 32;   // vectors of four channels of a thread
+    __shared__ int sm_last;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c0 = blockIdx.x, r = blockIdx.y * 32 + lane;
+    pdl_wait();
+    pdl_trigger();
+    for (int side = 0; side < 2; ++side) {
+        const Rec rec = p.recs[c0 * 2 + side];
+        if ((rec.flags & (REC_CUT | REC_FIRST)) != (REC_CUT | REC_FIRST) || blockIdx.y * 32 >= rec.rows) continue;
+        __syncthreads();
+        if (threadIdx.x == 0) sm_last = ctas - 1;
+        __syncthreads();
+        for (int k = c0 + 1 + threadIdx.x; k < ctas; k += 256)
+            if ((p.recs[k * 2].flags & (REC_CUT | REC_FIRST | REC_LAST)) == (REC_CUT | REC_LAST)) {
+                atomicMin(&sm_last, k);
+                break;
+            }
+        __syncthreads();
+        const int n = sm_last - c0 + 1;
+        if (r >= rec.rows) continue;
+        auto part = [&](int i) { return (int64_t)((c0 + i) * 2 + (i ? 0 : side)); };
+        float M = -INFINITY, L = 0.f;
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_ml[part(i) * C::ROWS + r].x);
+        const float mb = M == -INFINITY ? 0.f : M;
+        float4 o[V] = {};
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float2 ml = p.part_ml[part(i) * C::ROWS + r];
+            const float f = ex2(ml.x - mb);
+            L += f * ml.y;
+            const float4* from = p.part_o + (part(i) * (D / 4) + warp) * C::ROWS + r;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float4 x = from[k * 8 * C::ROWS];
+                o[k].x += f * x.x;
+                o[k].y += f * x.y;
+                o[k].z += f * x.z;
+                o[k].w += f * x.w;
+            }
+        }
+        const float inv = L == 0.f ? 0.f : p.v_scale[rec.hk] / L;
+        const int64_t row = (int64_t)(rec.start + (rec.row0 + r) / p.G) * p.s.n_heads + rec.hk * p.G + (rec.row0 + r) % p.G;
+        uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + row * D) + warp;
+#pragma unroll
+        for (int k = 0; k < V; ++k)
+            to[k * 8] = make_uint2(pack2<false>(o[k].x * inv, o[k].y * inv), pack2<false>(o[k].z * inv, o[k].w * inv));
+        if (warp == 0 && p.a.lse) p.a.lse[row] = L == 0.f ? -INFINITY : mb * kLn2 + logf(L * C::DOWN);
+    }
+}
+
+// The kernel of a cache and of capped or plain scores.
+template <class F>
+auto pick(const KvShape& s, bool cap, F f) {
+    if (s.e4m3) {
+        if (s.head_dim == 64) return cap ? f(Cfg<64, true, true>{}) : f(Cfg<64, true, false>{});
+        if (s.head_dim == 128) return cap ? f(Cfg<128, true, true>{}) : f(Cfg<128, true, false>{});
+        return cap ? f(Cfg<256, true, true>{}) : f(Cfg<256, true, false>{});
+    }
+    if (s.head_dim == 64) return cap ? f(Cfg<64, false, true>{}) : f(Cfg<64, false, false>{});
+    if (s.head_dim == 128) return cap ? f(Cfg<128, false, true>{}) : f(Cfg<128, false, false>{});
+    return cap ? f(Cfg<256, false, true>{}) : f(Cfg<256, false, false>{});
+}
+
+struct Space {
+    size_t recs, ml, o;   // bytes, each a multiple of 256
+};
+Space space_of(const Kv& K) {
+    const int rows = pick(K.s, false, [](auto c) { return decltype(c)::ROWS; });
+    const size_t n = (size_t)K.num_sms * 2;
+    return {(n * sizeof(Rec) + 255) / 256 * 256, n * rows * sizeof(float2), n * rows * K.s.head_dim * 4};
 }
 
 }  // namespace
 
-size_t kv_chunk_workspace(const Kv&) { return 256; }
-cudaError_t kv_chunk_setup(Kv&) { return cudaSuccess; }
+size_t kv_chunk_workspace(const Kv& K) {
+    const Space w = space_of(K);
+    return w.recs + w.ml + w.o;
+}
+
+cudaError_t kv_chunk_setup(Kv& K) {
+    const int sr = pick(K.s, false, [](auto c) { return decltype(c)::SR; });
+    K.chunk_box = 16;
+    while (K.chunk_box * 2 <= sr && K.s.page_size % (K.chunk_box * 2) == 0) K.chunk_box *= 2;
+    const auto encode = tensor_map_encoder();
+    if (!encode) return cudaErrorNotSupported;
+    const size_t es = K.s.e4m3 ? 1 : 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)K.s.head_dim, (cuuint64_t)K.s.page_size, (cuuint64_t)K.s.n_kv_heads,
+                                (cuuint64_t)K.s.n_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)K.s.token_stride * es, (cuuint64_t)K.s.head_stride * es,
+                                   (cuuint64_t)K.s.page_stride * es};
+    const cuuint32_t box[4] = {(cuuint32_t)(K.s.e4m3 ? K.s.head_dim : 64), (cuuint32_t)K.chunk_box, 1, 1};
+    const cuuint32_t ones[4] = {1, 1, 1, 1};
+    for (int i = 0; i < 2; ++i)
+        if (encode(i ? &K.tm_chunk_v : &K.tm_chunk_k, K.s.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                   4, i ? K.v_pages : K.k_pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   K.s.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    for (const bool cap : {false, true}) {
+        const cudaError_t e = pick(K.s, cap, [](auto c) {
+            using C = decltype(c);
+            return cudaFuncSetAttribute(k_kv_chunk<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
+        });
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
 
 moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t stream) {
-    const ChunkArgs p{a, K.s, K.k_pages, K.v_pages, K.k_scale, K.v_scale, K.health};
-    const auto kernel = K.s.head_dim == 64 ? k_kv_chunk<64> : K.s.head_dim == 128 ? k_kv_chunk<128> : k_kv_chunk<256>;
-    const unsigned grid = (unsigned)std::min<int64_t>(((int64_t)a.T * K.s.n_heads + 7) / 8, (int64_t)K.num_sms * 8);
-    const cudaError_t e = launch_pdl(kernel, dim3(grid), dim3(256), 0, stream, true, p);
+    const Space w = space_of(K);
+    uint8_t* const at = static_cast<uint8_t*>(a.workspace);
+    ChunkArgs p{a, K.s, K.v_pages, K.k_scale, K.v_scale, K.health, reinterpret_cast<Rec*>(at),
+                reinterpret_cast<float2*>(at + w.recs), reinterpret_cast<float4*>(at + w.recs + w.ml),
+                K.s.n_heads / K.s.n_kv_heads, K.chunk_box};
+    // a window that holds every position is none
+    if (p.a.window >= a.max_pages * K.s.page_size) p.a.window = 0;
+    // changes no score below 2^68, and a score's share of it would lose bits
+    const bool cap = a.softcap > 0.f && a.softcap < 0x1p80f;
+    const cudaError_t e = pick(K.s, cap, [&](auto c) {
+        using C = decltype(c);
+        const cudaError_t e = launch_pdl(k_kv_chunk<C>, dim3(K.num_sms), dim3(C::THREADS), C::smem, stream, true, p,
+                                         K.tm_chunk_k, K.tm_chunk_v);
+        if (e != cudaSuccess) return e;
+        return launch_pdl(k_kv_chunk_join<C>, dim3(K.num_sms, C::ROWS / 32), dim3(256), 0, stream, true, p, K.num_sms);
+    });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend chunk launch");
 }
 

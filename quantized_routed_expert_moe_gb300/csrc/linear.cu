@@ -112,11 +112,6 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
                  : "memory");
     return v;
 }
-// kind::f16 with bf16 operands (both K-major) and an fp32 accumulator
-__host__ __device__ constexpr uint32_t idesc_bf16(int M, int N) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
 // Channel n of tokens t.. t + 15, as far as `count` goes: the lanes of a warp hold
 // neighbouring channels. The residual's reads are all on their way before any is used.
 __device__ __forceinline__ void finish16(const LinearArgs& p, int t, int count, int n, float (&v)[16], float bias) {
@@ -224,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kChunk / 16; ++j)
                         bw::mma_f16(d, bw::desc_sw128(at + 32 * j), bw::desc_sw128(at + kRows * kChunk * 2 + 32 * j),
-                                    idesc_bf16(kRows, BN), k > k0 || j > 0);
+                                    bw::idesc_f16_f32(kRows, BN, true), k > k0 || j > 0);
                     bw::mma_commit(empty + 8 * s);
                     if (k == k1 - 1) bw::mma_commit(done + 8 * (acc & 1));
                 }
