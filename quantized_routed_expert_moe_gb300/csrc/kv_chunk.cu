@@ -36,6 +36,7 @@ namespace {
 
 constexpr int kBlk = 128;              // cached tokens of a block
 constexpr int kRing = 16;              // blocks whose page flags are kept
+constexpr int kTileCost = 2;           // what a tile's beginning and end cost, in blocks
 constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Compile-time shape of one kernel: head dimension, cache type, capped scores.
@@ -88,7 +89,8 @@ struct Part {
     int all_lo, all_hi;       // positions that every row attends to
     int blk0, n;              // blocks
     int index, busy, gi;      // parts, parts with blocks, and blocks of this CTA before
-    bool first, last;         // of the tile
+    bool first, last;         // blocks of the tile are among them
+    bool none;                // the tile has no blocks at all
 };
 
 // Walks a CTA's parts; every role does so by itself.
@@ -115,11 +117,14 @@ struct Walk {
         q.hi = p1 + 1;
         q.all_lo = first_seen(p1, window);
         q.all_hi = p0 + 1;
-        const int c = blocks_of(q.lo, q.hi), units = max(c, 1);
+        const int c = blocks_of(q.lo, q.hi), units = c + kTileCost;
         const int take = (int)min((long long)(units - off), left);
-        q.blk0 = q.lo / kBlk + off;
-        q.n = c ? take : 0;
-        q.first = off == 0;
+        const int b0 = max(off - kTileCost, 0), b1 = max(off + take - kTileCost, 0);
+        q.blk0 = q.lo / kBlk + b0;
+        q.n = b1 - b0;
+        q.first = b0 == 0;
+        q.last = b1 == c;
+        q.none = c == 0;
         q.index = index++;
         q.busy = busy;
         busy += q.n > 0;
@@ -127,8 +132,7 @@ struct Walk {
         gi += q.n;
         left -= take;
         off += take;
-        q.last = off == units;
-        if (q.last) {
+        if (off == units) {
             off = 0;
             if (++hk == Hk) {
                 hk = 0;
@@ -228,7 +232,7 @@ __device__ __forceinline__ void each_block(int n, F f) {
 template <class C>
 struct Shared {
     uint64_t full[C::FP8 ? C::NRAW : C::NST], raw_free[4], ready[C::NST], empty[C::NST];
-    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_free[2], drain;
+    uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], o_free[2], drain;
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
     uint32_t tmem;
@@ -251,7 +255,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t q_at = base, stages = base + C::NS * C::QTILE, raws = stages + NST * C::STAGE;
     const uint32_t full = bw::saddr(sm.full), raw_free = bw::saddr(sm.raw_free), ready = bw::saddr(sm.ready),
                    empty = bw::saddr(sm.empty), q_full = bw::saddr(sm.q_full), s_full = bw::saddr(sm.s_full),
-                   p_full = bw::saddr(sm.p_full), o_done = bw::saddr(sm.o_done), o_free = bw::saddr(sm.o_free),
+                   p_full = bw::saddr(sm.p_full), o_done = bw::saddr(sm.o_done), o_last = bw::saddr(sm.o_last), o_free = bw::saddr(sm.o_free),
                    drain = bw::saddr(&sm.drain);
     uint32_t bits = 0;
 
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::mbar_init(s_full + 8 * i, 1);
             bw::mbar_init(p_full + 8 * i, C::NS == 2 ? 4 : 8);
             bw::mbar_init(o_done + 8 * i, 1);
+            bw::mbar_init(o_last + 8 * i, 1);
             bw::mbar_init(o_free + 8 * i, C::NS == 2 ? 4 : 8);
         }
         bw::mbar_init(drain, 1);
@@ -315,7 +320,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         if (threadIdx.x == 0) pre[B] = (int)tiles;
         __syncthreads();
-        // units of tile r of all heads; a tile without blocks counts as one
+        // units of tile r: its blocks, and what goes before and after them
         auto find = [&](int r) {
             int lo = 0, hi = B;   // the last b with pre[b] <= r that has tiles
             while (hi - lo > 1) {
@@ -328,7 +333,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto per_head = [&](int r) {
             const int b = find(r), n = sm.start[b + 1] - sm.start[b], row0 = (r - pre[b]) * C::ROWS;
             const int p0 = sm.len[b] - n + row0 / G, p1 = sm.len[b] - n + (min(row0 + C::ROWS, n * G) - 1) / G;
-            return max(Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1), 1);
+            return Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1) + kTileCost;
         };
         walk.left = 0;
         if (!sm.bad_start) {
@@ -475,6 +480,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         bw::tc_fence_after();
                         outputs(tmem + slot * 128, v % NST, tmem + C::O_AT + slot * D, j > 0);
                         commit(o_done + 8 * slot);
+                        if (j + 1 == q.n) commit(o_last + 8 * slot);
                         if (slot == 1 || !two) commit(empty + 8 * (v % NST));
                         if (j + 1 < q.n) {
                             if (slot == 0) stage_in();
@@ -505,6 +511,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         commit(empty + 8 * (it % NST));
                     }
                     commit(o_done);
+                    if (j + 1 == q.n) commit(o_last);
                 }
             }
         }
@@ -569,21 +576,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         __syncwarp();
                         if (lane == 0) bw::mbar_arrive(raw_free + 8 * (it % RING));
                     } else if (look) {
-                        for (int i = me; i < C::STAGE / 16; i += TEAM) {
-                            const int row = i / 8 % C::SR;   // units change places within a row only
-                            uint4 w = ld_shared(stage + i * 16);
-                            uint32_t x[4] = {w.x, w.y, w.z, w.w}, changed = 0;
-                            const bool on = live(row);
-                            for (int k = 0; k < 4; ++k) {
-                                const uint32_t before = x[k];
-                                if (!on) x[k] = 0;
-                                else if (part_seen) {
-                                    if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u, *odd = 1;
-                                    if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0xffffu, *odd = 1;
+                        // eight vectors at a time: what needs no change, almost all of them, costs a
+                        // load and a few operations
+#pragma unroll 1
+                        for (int i0 = me; i0 < C::STAGE / 16; i0 += 8 * TEAM) {
+                            uint4 w[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) w[k] = ld_shared(stage + (i0 + k * TEAM) * 16);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                // exponents of ones carry into the sign's place
+                                auto high = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
+                                const uint32_t bad = (high(w[k].x) | high(w[k].y) | high(w[k].z) | high(w[k].w)) & 0x80008000u;
+                                const int i = i0 + k * TEAM;
+                                const bool on = live(i / 8 % C::SR);   // units change places within a row only
+                                if (on && !(bad && part_seen)) continue;
+                                uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                                for (int e = 0; e < 4; ++e) {
+                                    if (!on) x[e] = 0;
+                                    if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u, *odd = 1;
+                                    if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu, *odd = 1;
                                 }
-                                changed |= before ^ x[k];
+                                st_shared(stage + i * 16, make_uint4(x[0], x[1], x[2], x[3]));
                             }
-                            if (changed) st_shared(stage + i * 16, make_uint4(x[0], x[1], x[2], x[3]));
                         }
                         bw::fence_async_smem();
                         __syncwarp();
@@ -602,7 +617,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         constexpr int OC = C::NS == 2 ? D : D / 2;       // output channels of a thread
         const int ch0 = C::NS == 2 ? 0 : wg * OC;
         const int64_t token_heads = s.n_heads;
-        uint32_t uses = 0, written = 0;                  // blocks of this slot; cut sides recorded
+        uint32_t uses = 0, ended = 0, written = 0;       // blocks and parts of this slot; cut sides recorded
         bool ok = true;
         const float scale = fabsf(p.a.scale) < 0x1p-100f ? 0x1p-100f : fabsf(p.a.scale);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
@@ -659,7 +674,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int r = slot * 128 + row;
                 if (C::NS == 2 && slot && q.rows <= 128) continue;
                 if (q.n) return true;
-                if (r < q.rows) {
+                if (q.none && r < q.rows) {
                     const int64_t o = out_row(q, r);
                     uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D + ch0);
                     for (int i = 0; i < OC / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
@@ -723,6 +738,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     l0 *= f;
                     l1 *= f;
                     if (j > 0) {
+                        // (a parity tells a phase from its neighbours: the products up to the last
+                        // but one ended before these scores, and the next has not begun)
                         ok = wait(o_done + 8 * slot, uses - 1) && ok;
                         bw::tc_fence_after();
 #pragma unroll 1
@@ -781,10 +798,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 l = sm.row_sum[0][row] + sm.row_sum[1][row];
             }
-            // (heads of 256: the last scores do not wait for the last but one product, and a
-            // parity tells a phase from its neighbours only)
-            if (C::NS == 1 && q.n > 1) ok = wait(o_done, uses - 2) && ok;
-            ok = wait(o_done + 8 * slot, uses - 1) && ok;
+            ok = wait(o_last + 8 * slot, ended++) && ok;
             bw::tc_fence_after();
             const int r = slot * 128 + row;
             const bool cut = !(q.first && q.last), on = r < q.rows;
