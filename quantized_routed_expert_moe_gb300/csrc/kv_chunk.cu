@@ -55,6 +55,9 @@ struct Cfg {
     static constexpr int RAW = SR * D, NRAW = FP8 ? 3 : 0;    // 8-bit stages, before conversion
     static constexpr int WARPS = FP8 ? 16 : 12, THREADS = 32 * WARPS;
     static constexpr int COLS = NS == 2 ? 128 : 64;      // score columns of a softmax thread
+    // Registers of a softmax thread, and of the others: together those of the launch.
+    static constexpr int SOFTMAX_REGS = FP8 ? 176 : 200, REGS = FP8 ? 80 : 104;
+    static_assert(256 * SOFTMAX_REGS + (THREADS - 256) * REGS <= THREADS * (65536 / THREADS / 8 * 8), "more registers than launched with");
     static constexpr int O_AT = 256;                     // tensor-memory column of the outputs
     static constexpr int READY = FP8 ? 4 : 2;            // warps that pass a stage on
     // An 8-bit cache is exact in fp16, and so are queries scaled to their row's largest; the
@@ -173,6 +176,7 @@ __device__ __forceinline__ T scan_cta(T v, T* sums, T& total) {
     return before;
 }
 
+// The registers of a thread from here on, for the warps of a group of four together.
 template <int N>
 __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
@@ -212,6 +216,15 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
 }
 __device__ __forceinline__ bool all_lanes(bool x) { return __all_sync(~0u, x) != 0; }
 
+__device__ __forceinline__ float max32(const float* x, float top) {
+    float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], fmaxf(x[i + 2 * k], x[i + 2 * k + 1]));
+    return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // The stages of a part in the order in which the products take them: f(values?, block).
 template <class C, class F>
 __device__ __forceinline__ void each_block(int n, F f) {
@@ -236,7 +249,9 @@ struct Shared {
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
     uint32_t tmem;
-    int abort, bad_start, first;
+    int abort, bad_start, first, more[2];
+    Part part[2][2];                  // of a softmax group: its part and the next
+    Walk<C> walk[2];
     uint8_t pages[kRing][2];          // per block and part: groups of 16 tokens whose page is in the pool
     uint8_t odd[8][4];                // per part and warp: values that are not finite were set aside
     float row_max[2][2][C::NS == 1 ? 128 : 1], row_sum[2][C::NS == 1 ? 128 : 1];
@@ -380,11 +395,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         return all_lanes(bw::mbar_wait(bar, parity & 1, &sm.abort, p.health, MOE_KV_TIMEOUT, kWaitNs));
     };
 
-    if (warp >= 8) {
-        if (warp < 12) regs_down<56>();
-        else regs_down<72>();
-    }
-    Part q;
+    if (warp >= 8) regs_down<C::REGS>();
     if (warp == 9) {
         // ---- copies: a lane per box --------------------------------------------------------------
         constexpr int RING = C::FP8 ? C::NRAW : NST, BYTES = C::FP8 ? C::RAW : C::STAGE;
@@ -395,6 +406,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint64_t pol = bw::l2_evict_normal();
         uint32_t it = 0;
         bool ok = true;
+        Part q;
         while (walk.next(q))
             each_block<C>(q.n, [&](bool values, int j) {
                 for (int part = 0; part < C::PARTS; ++part, ++it) {
@@ -451,6 +463,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             __syncwarp();
         };
         auto stage_in = [&] { ok = wait(ready + 8 * (it % NST), it / NST) && ok; bw::tc_fence_after(); };
+        Part q;
         while (walk.next(q)) {
             if (q.n == 0) continue;
             if constexpr (C::NS == 2) {
@@ -507,7 +520,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (j == 0) ok = wait(o_free, parts[0]++ + 1) && ok;
                     for (int part = 0; part < C::PARTS; ++part, ++it) {
                         stage_in();
-                        outputs(tmem + (use & 1) * 128 + part * (C::SR / 2), it % NST, tmem + C::O_AT, j > 0 || part > 0);
+                        outputs(tmem + (use & 1) * 128 + part * C::SR, it % NST, tmem + C::O_AT, j > 0 || part > 0);
                         commit(empty + 8 * (it % NST));
                     }
                     commit(o_done);
@@ -527,6 +540,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = C::FP8 ? 12 : 10, TEAM = 32 * C::READY;
         const int me = threadIdx.x - 32 * FIRST;
         uint32_t it = 0;
+        Part q;
         while (walk.next(q)) {
             if (q.n == 0) continue;
             volatile uint8_t* const odd = &sm.odd[q.busy % 8][warp - FIRST];
@@ -609,8 +623,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp < 8) {
         // ---- softmax: a thread per row (heads of 256: two, by columns) -----------------------------
-        if constexpr (C::FP8) regs_up<192>();
-        else regs_up<224>();
+        regs_up<C::SOFTMAX_REGS>();
         const int wg = warp / 4, slot = C::NS == 2 ? wg : 0, row = threadIdx.x % 128;
         const uint32_t lanes = tmem + ((uint32_t)(warp % 4 * 32) << 16);
         const uint32_t o_at = lanes + C::O_AT + (C::NS == 2 ? slot * D : wg * (D / 2));
@@ -669,8 +682,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             c_next = c;
         };
         // the next part with blocks for this group; rows of parts without any are written at once
+        // (parts stand in shared memory, where a row's scores leave them no registers)
+        if (threadIdx.x % 128 == 0) sm.walk[wg] = walk;
+        auto group_meets = [&] {
+            if (wg) asm volatile("bar.sync 3, 128;" ::: "memory");
+            else asm volatile("bar.sync 2, 128;" ::: "memory");
+        };
         auto advance = [&](Part& q) {
-            while (walk.next(q)) {
+            for (;;) {
+                group_meets();   // what stood there has been read
+                if (threadIdx.x % 128 == 0) sm.more[wg] = sm.walk[wg].next(q);
+                group_meets();
+                if (!*const_cast<volatile int*>(&sm.more[wg])) return false;
                 const int r = slot * 128 + row;
                 if (C::NS == 2 && slot && q.rows <= 128) continue;
                 if (q.n) return true;
@@ -681,47 +704,63 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (p.a.lse && ch0 == 0) p.a.lse[o] = -INFINITY;
                 }
             }
-            return false;
         };
 
-        bool have = advance(q);
-        if (have) load_q(q);
+        uint32_t turn = 0;
+        bool have = advance(sm.part[wg][0]);
+        if (have) load_q(sm.part[wg][0]);
         while (have) {
+            Part& q = sm.part[wg][turn & 1];
+            const volatile Part& v = q;
             const float c = C::CAP ? 1.f : c_next * kLog2e;
             const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
             const int pos = q.base + (q.row0 + slot * 128 + row) / G;
             const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
-            float m = -INFINITY, m_raw = 0.f, l0 = 0.f, l1 = 0.f;   // maximum (scaled, base two; as it came), sums
+            float m = -INFINITY, m_raw = 0.f, l[4] = {};   // maximum (scaled, base two; as it came), sums
 #pragma unroll 1
-            for (int j = 0; j < q.n; ++j, ++uses) {
+            for (int j = 0; j < v.n; ++j, ++uses) {
                 const int buf = C::NS == 2 ? slot : uses & 1, phase = C::NS == 2 ? uses : uses >> 1;
-                const int at = (q.blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
+                const int at = (v.blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
                 const uint32_t s_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * C::COLS);
                 ok = wait(s_full + 8 * buf, phase) && ok;
                 bw::tc_fence_after();
-                float x[C::COLS];
-#pragma unroll
-                for (int i = 0; i < C::COLS / 32; ++i) bw::tmem_ld32(s_at + 32 * i, reinterpret_cast<uint32_t*>(x) + 32 * i);
-#pragma unroll
-                for (int i = 0; i < C::COLS / 32; ++i) bw::tmem_wait_ld32(reinterpret_cast<uint32_t*>(x) + 32 * i);
-                if constexpr (C::CAP) {
-#pragma unroll
-                    for (int i = 0; i < C::COLS; ++i) x[i] = tanh_of<true>(x[i] * to_cap) * cap;
-                }
-                const volatile uint8_t* pages = sm.pages[(q.gi + j) % kRing];
+                const volatile uint8_t* pages = sm.pages[(v.gi + j) % kRing];
                 const uint32_t in = C::NS == 2 ? pages[0] : pages[wg];
-                if (at < q.all_lo || at + C::COLS > q.all_hi || in != (1u << C::COLS / 16) - 1) {
-                    const int a = see0 - at, b = see1 - at;
+                const bool edge = at < v.all_lo || at + C::COLS > v.all_hi || in != (1u << C::COLS / 16) - 1;
+                if (C::CAP || edge) {
+                    // scores are capped, and what this row does not attend to goes out, in place
+#pragma unroll 1
+                    for (int c0 = 0; c0 < C::COLS; c0 += 32) {
+                        uint32_t u[32];
+                        float* const x = reinterpret_cast<float*>(u);
+                        bw::tmem_ld32(s_at + c0, u);
+                        bw::tmem_wait_ld32(u);
+                        if constexpr (C::CAP) {
 #pragma unroll
-                    for (int i = 0; i < C::COLS; ++i)
-                        if (i < a || i >= b || !(in >> (i / 16) & 1)) x[i] = -INFINITY;
+                            for (int i = 0; i < 32; ++i) x[i] = tanh_of<true>(x[i] * to_cap) * cap;
+                        }
+                        if (edge) {
+                            const int a = see0 - at - c0, b = see1 - at - c0;
+                            const uint32_t two = in >> (c0 / 16);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (i < a || i >= b || !(two >> (i / 16) & 1)) x[i] = -INFINITY;
+                        }
+                        bw::tmem_st32(s_at + c0, u);
+                    }
+                    bw::tmem_wait_st();
                 }
-                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                // the row in registers from here on: read again for the exponentials it takes 1340
+                // cycles instead of 905
+                uint32_t u[C::COLS / 32][32];
 #pragma unroll
-                for (int i = 0; i < C::COLS; i += 8)
+                for (int i = 0; i < C::COLS / 32; ++i) bw::tmem_ld32(s_at + 32 * i, u[i]);
+                float top = -INFINITY;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], fmaxf(x[i + 2 * k], x[i + 2 * k + 1]));
-                float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                for (int i = 0; i < C::COLS / 32; ++i) {
+                    bw::tmem_wait_ld32(u[i]);
+                    top = max32(reinterpret_cast<float*>(u[i]), top);
+                }
                 if constexpr (C::NS == 1) {
                     sm.row_max[uses & 1][wg][row] = top;
                     asm volatile("bar.sync 1, 256;" ::: "memory");
@@ -735,8 +774,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         m = cand;
                         m_raw = top;
                     }
-                    l0 *= f;
-                    l1 *= f;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) l[i] *= f;
                     if (j > 0) {
                         // (a parity tells a phase from its neighbours: the products up to the last
                         // but one ended before these scores, and the next has not begun)
@@ -756,47 +795,45 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // exp2(x c - m): one rounding, and a maximum that is itself rounded shifts all
                 // weights of a row alike; past 2^20 that shift would be seen, and the
                 // difference is taken first
-                const float mu = m == -INFINITY ? 0.f : m;
-                if (__any_sync(~0u, fabsf(mu) > 0x1p20f)) {
-                    const float raw = m == -INFINITY ? 0.f : m_raw;
+                const float mu = m == -INFINITY ? 0.f : m, minus = C::UP - mu;
+                const float raw = m == -INFINITY ? 0.f : m_raw;
+                const bool far = __any_sync(~0u, fabsf(mu) > 0x1p20f);
 #pragma unroll
-                    for (int i = 0; i < C::COLS; ++i) x[i] = (x[i] - raw) * c + C::UP;
-                } else {
-                    const float minus = C::UP - mu;
+                for (int c0 = 0; c0 < C::COLS; c0 += 32) {
+                    float* const x = reinterpret_cast<float*>(u[c0 / 32]);
+                    if (far) {
 #pragma unroll
-                    for (int i = 0; i < C::COLS; i += 2) fma2(x[i], x[i + 1], c, minus);
+                        for (int i = 0; i < 32; ++i) x[i] = (x[i] - raw) * c + C::UP;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 2) fma2(x[i], x[i + 1], c, minus);
+                    }
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) x[i + k] = ex2(x[i + k]);
+                        add2(l[0], l[1], x[i], x[i + 1]);
+                        add2(l[2], l[3], x[i + 2], x[i + 3]);
+                        w[i / 2] = pack2<C::FP8>(x[i], x[i + 1]);
+                        w[i / 2 + 1] = pack2<C::FP8>(x[i + 2], x[i + 3]);
+                    }
+                    bw::tmem_st16(s_at + c0 / 2, w);   // over scores that have been read
                 }
-                float a0 = 0.f, a1 = 0.f;
-                uint32_t w[C::COLS / 2];
-#pragma unroll
-                for (int i = 0; i < C::COLS; i += 4) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[i + k] = ex2(x[i + k]);
-                    add2(l0, l1, x[i], x[i + 1]);
-                    add2(a0, a1, x[i + 2], x[i + 3]);
-                    w[i / 2] = pack2<C::FP8>(x[i], x[i + 1]);
-                    w[i / 2 + 1] = pack2<C::FP8>(x[i + 2], x[i + 3]);
-                }
-                l0 += a0;
-                l1 += a1;
-                const uint32_t p_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * (C::COLS / 2));
-#pragma unroll
-                for (int i = 0; i < C::COLS / 64; ++i) bw::tmem_st32(p_at + 32 * i, w + 32 * i);
                 bw::tmem_wait_st();
                 bw::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) bw::mbar_arrive(p_full + 8 * buf);
             }
             // the next part's queries go ahead of this one's end
-            Part nq;
-            const bool more = advance(nq);
-            if (more) load_q(nq);
+            const bool more = advance(sm.part[wg][~turn & 1]);
+            if (more) load_q(sm.part[wg][~turn & 1]);
 
-            float l = l0 + l1;
+            float sum = (l[0] + l[2]) + (l[1] + l[3]);
             if constexpr (C::NS == 1) {
-                sm.row_sum[wg][row] = l;
+                sm.row_sum[wg][row] = sum;
                 asm volatile("bar.sync 1, 256;" ::: "memory");
-                l = sm.row_sum[0][row] + sm.row_sum[1][row];
+                sum = sm.row_sum[0][row] + sm.row_sum[1][row];
             }
             ok = wait(o_last + 8 * slot, ended++) && ok;
             bw::tc_fence_after();
@@ -810,8 +847,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 written |= 1u << side;
                 p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
             }
-            if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, l);
-            const float inv = l == 0.f ? 0.f : p.v_scale[q.hk] / l;
+            if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, sum);
+            const float inv = sum == 0.f ? 0.f : p.v_scale[q.hk] / sum;
             const int64_t o_row = on ? out_row(q, r) : 0;
 #pragma unroll 1
             for (int i = 0; i < OC; i += 32) {
@@ -859,9 +896,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::tc_fence_before();
             __syncwarp();
             if (lane == 0) bw::mbar_arrive(o_free + 8 * slot);
-            if (!cut && on && p.a.lse && ch0 == 0) p.a.lse[o_row] = l == 0.f ? -INFINITY : m * kLn2 + logf(l * C::DOWN);
+            if (!cut && on && p.a.lse && ch0 == 0) p.a.lse[o_row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum * C::DOWN);
             have = more;
-            q = nq;
+            ++turn;
         }
         if (threadIdx.x == 0)
             for (int side = 0; side < 2; ++side)
