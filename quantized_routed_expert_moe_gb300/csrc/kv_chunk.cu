@@ -59,7 +59,7 @@ struct Cfg {
     static constexpr int SOFTMAX_REGS = FP8 ? 176 : 200, REGS = FP8 ? 80 : 104;
     static_assert(256 * SOFTMAX_REGS + (THREADS - 256) * REGS <= THREADS * (65536 / THREADS / 8 * 8), "more registers than launched with");
     static constexpr int O_AT = 256;                     // tensor-memory column of the outputs
-    static constexpr int READY = FP8 ? 4 : 2;            // warps that pass a stage on
+    static constexpr int READY = FP8 ? 4 : 1;            // warps that pass a stage on
     // An 8-bit cache is exact in fp16, and so are queries scaled to their row's largest; the
     // weights are 2^7 times their size, at most 2^15: 2^-31 of exp(m) is their smallest step.
     static constexpr float UP = FP8 ? 7.f : 0.f, DOWN = FP8 ? 0x1p-7f : 1.f;
@@ -153,6 +153,7 @@ struct Walk {
 
 template <class T>
 __device__ __forceinline__ T scan_up(T v) {   // inclusive, over a warp
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const T u = __shfl_up_sync(~0u, v, o);
         if ((int)(threadIdx.x % 32) >= o) v += u;
@@ -169,6 +170,7 @@ __device__ __forceinline__ T scan_cta(T v, T* sums, T& total) {
     __syncthreads();
     T before = incl - v;
     total = 0;
+#pragma unroll 1
     for (int w = 0; w < WARPS; ++w) {
         if (w < warp) before += sums[w];
         total += sums[w];
@@ -225,19 +227,31 @@ __device__ __forceinline__ float max32(const float* x, float top) {
     return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 
+// Stages in the order of their use. A 16-bit cache has a ring for keys and one for values, each
+// filled by a warp of its own (on one ring a warp could take a stage's phase for the one two
+// before); an 8-bit cache has one of each kind, filled in order by one warp.
+template <bool SPLIT, int N>
+struct Turn {
+    uint32_t n[2] = {0, 0}, stage, use;   // use: how often the stage was in use before
+    __device__ __forceinline__ void take(bool values) {
+        const int r = SPLIT && values;
+        constexpr int EACH = SPLIT ? N / 2 : N;
+        stage = r * EACH + n[r] % EACH;
+        use = n[r]++ / EACH;
+    }
+};
+
 // The stages of a part in the order in which the products take them: f(values?, block).
 template <class C, class F>
 __device__ __forceinline__ void each_block(int n, F f) {
-    if (C::NS == 2) {
-        for (int j = 0; j < n; ++j) {
-            f(false, j);
-            f(true, j);
-        }
-    } else if (n > 0) {
-        f(false, 0);
-        for (int j = 0; j < n; ++j) {
-            if (j + 1 < n) f(false, j + 1);
-            f(true, j);
+#pragma unroll 1
+    for (int i = 0; i < 2 * n; ++i) {
+        if (C::NS == 2) {
+            f((i & 1) != 0, i >> 1);
+        } else {   // keys are a block ahead
+            const int t = i >> 1;
+            const bool values = i & 1 ? t + 1 == n : i > 0;
+            f(values, i & 1 ? (values ? t : t + 1) : max(t - 1, 0));
         }
     }
 }
@@ -275,15 +289,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     uint32_t bits = 0;
 
     if (threadIdx.x == 0) {
+#pragma unroll 1
         for (int i = 0; i < NST; ++i) {
             if (!C::FP8) bw::mbar_init(full + 8 * i, 1);
             bw::mbar_init(ready + 8 * i, C::READY);
             bw::mbar_init(empty + 8 * i, 1);
         }
+#pragma unroll 1
         for (int i = 0; i < C::NRAW; ++i) {
             bw::mbar_init(full + 8 * i, 1);
             bw::mbar_init(raw_free + 8 * i, 4);
         }
+#pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             bw::mbar_init(q_full + 8 * i, C::NS == 2 ? 4 : 8);
             bw::mbar_init(s_full + 8 * i, 1);
@@ -313,6 +330,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int most = p.a.max_pages * s.page_size;
         const int per = (B + C::THREADS - 1) / C::THREADS, b0 = threadIdx.x * per, b1 = min(B, b0 + per);
         int mine = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             const int s0 = p.a.starts[b], s1 = p.a.starts[b + 1];
             int len = max(p.a.lens[b], 0);
@@ -328,6 +346,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         long long tiles;
         long long run = scan_cta<long long, C::WARPS>(mine, sm.sums, tiles);
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             pre[b] = (int)run;
             const int n = sm.start[b + 1] - sm.start[b];
@@ -354,12 +373,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (!sm.bad_start) {
             const int rt = (int)tiles;
             long long total = 0, sum = 0;
+#pragma unroll 1
             for (int r = threadIdx.x; r < rt; r += C::THREADS) sum += (long long)per_head(r) * s.n_kv_heads;
             scan_cta<long long, C::WARPS>(sum, sm.sums, total);
             const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
             const long long from = c < ctas ? total * c / ctas : total, to = c < ctas ? total * (c + 1) / ctas : total;
             walk.left = to - from;
             long long before = 0;
+#pragma unroll 1
             for (int r0 = 0; walk.left > 0 && r0 < rt && before <= from; r0 += C::THREADS) {
                 const int r = r0 + threadIdx.x;
                 const long long u = r < rt ? (long long)per_head(r) * s.n_kv_heads : 0;
@@ -392,69 +413,121 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncthreads();
     }
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return all_lanes(bw::mbar_wait(bar, parity & 1, &sm.abort, p.health, MOE_KV_TIMEOUT, kWaitNs));
+        return all_lanes(bw::mbar_wait_asleep(bar, parity & 1, &sm.abort, p.health, MOE_KV_TIMEOUT, kWaitNs));
     };
 
     if (warp >= 8) regs_down<C::REGS>();
-    if (warp == 9) {
-        // ---- copies: a lane per box --------------------------------------------------------------
+    if (warp == 9 || (!C::FP8 && warp == 10)) {
+        // ---- copies: of keys by one warp, of values by another. A lane looks up a box's page a
+        // block ahead, one lane starts the copies ------------------------------------------------------
         constexpr int RING = C::FP8 ? C::NRAW : NST, BYTES = C::FP8 ? C::RAW : C::STAGE;
         constexpr int WIDTH = C::FP8 ? 1 : C::PANELS;
+        const bool keys = warp == 9, vals = C::FP8 || warp == 10;   // whose copies this warp starts
         const uint32_t at = C::FP8 ? raws : stages, gone = C::FP8 ? raw_free : empty;
-        const int boxes = C::SR / p.box_rows, box = lane % boxes, panel = lane / boxes;
+        const int boxes = C::SR / p.box_rows;
         const uint32_t box_bytes = p.box_rows * (C::FP8 ? D : 128);
         const uint64_t pol = bw::l2_evict_normal();
-        uint32_t it = 0;
+        // lane: box `lane` of the block's keys (or values), all of whose channels it stands for
+        struct Box {
+            int page, slot;   // as the table has it; -1 where no row is attended to
+            bool need;
+        };
+        auto look_up = [&](const Part& q, int j) {
+            const int pos = (q.blk0 + j) * kBlk + lane * p.box_rows;
+            Box x;
+            x.need = lane < boxes * C::PARTS && pos < q.hi && pos + p.box_rows > q.lo;
+            const int i = pos / s.page_size;
+            x.slot = pos - i * s.page_size;
+            x.page = x.need ? p.a.block_table[(int64_t)q.b * p.a.max_pages + i] : -1;
+            return x;
+        };
+        auto advance = [&](Part& q) {
+            while (walk.next(q))
+                if (q.n) return true;
+            return false;
+        };
+        Turn<!C::FP8, RING> turn;
+        uint32_t filled = 0, phases = 0;   // stages with a copy of this warp's, and the parity of its phase
         bool ok = true;
-        Part q;
-        while (walk.next(q))
+        Part q, nq;
+        bool have = advance(q);
+        Box ahead{}, seen[2] = {};   // of the next block; of keys that came, for their values
+        if (have) ahead = look_up(q, 0);
+        while (have) {
+            const bool more = advance(nq);
             each_block<C>(q.n, [&](bool values, int j) {
-                for (int part = 0; part < C::PARTS; ++part, ++it) {
-                    const int pos = (q.blk0 + j) * kBlk + part * C::SR + box * p.box_rows;
-                    const bool need = panel < WIDTH && pos < q.hi && pos + p.box_rows > q.lo;
-                    int page = -1;
-                    if (need) page = kv_page(s, p.a.block_table[(int64_t)q.b * p.a.max_pages + pos / s.page_size], bits);
-                    const uint32_t st = it % RING, bar = full + 8 * st;
-                    ok = wait(gone + 8 * st, (it / RING) + 1) && ok;
-                    const uint32_t lost = __ballot_sync(~0u, need && page < 0), come = __ballot_sync(~0u, need && page >= 0);
-                    if (lane == 0) {
-                        uint32_t groups = 0;
-                        for (int g = 0; g < G16; ++g) groups |= (lost >> (g * 16 / p.box_rows) & 1 ? 0u : 1u) << g;
-                        sm.pages[(q.gi + j) % kRing][part] = (uint8_t)groups;
-                        if (ok) bw::mbar_arrive_tx(bar, __popc(come) * box_bytes);
+                if (!(values ? vals : keys)) return;
+                Box x = ahead;
+                if (values && keys) {
+                    x = j & 1 ? seen[1] : seen[0];
+                } else {
+                    if (j & 1) seen[1] = x;
+                    else seen[0] = x;
+                    if (j + 1 < q.n) ahead = look_up(q, j + 1);
+                    else if (more) ahead = look_up(nq, 0);
+                }
+                const int page = x.need ? kv_page(s, x.page, bits) : -1;
+                const uint32_t lost = __ballot_sync(~0u, x.need && page < 0), come = __ballot_sync(~0u, page >= 0);
+                if (!values && lane < C::PARTS) {
+                    uint32_t groups = (1u << G16) - 1;
+#pragma unroll 1
+                    for (int g = 0; lost && g < G16; ++g)
+                        if (lost >> (lane * boxes + g * 16 / p.box_rows) & 1) groups &= ~(1u << g);
+                    sm.pages[(q.gi + j) % kRing][lane] = (uint8_t)groups;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int part = 0; part < C::PARTS; ++part) {
+                    turn.take(values);
+                    const uint32_t bar = full + 8 * turn.stage, to = at + turn.stage * BYTES;
+                    ok = wait(gone + 8 * turn.stage, turn.use + 1) && ok;
+                    if (!ok) continue;   // nothing is issued any more
+                    filled |= 1u << turn.stage;
+                    phases = (phases & ~(1u << turn.stage)) | (turn.use & 1) << turn.stage;
+                    if (bw::elect_one())
+                        bw::mbar_arrive_tx(bar, __popc(come >> (part * boxes) & ((1u << boxes) - 1)) * box_bytes * WIDTH);
+#pragma unroll 1
+                    for (int box = 0; box < boxes; ++box) {
+                        const int from = __shfl_sync(~0u, page, part * boxes + box), slot = __shfl_sync(~0u, x.slot, part * boxes + box);
+                        if (from >= 0 && bw::elect_one())
+#pragma unroll
+                            for (int panel = 0; panel < WIDTH; ++panel)
+                                bw::tma_load_4d(to + (C::FP8 ? 0 : panel * C::PANEL) + box * box_bytes, values ? &tm_v : &tm_k, panel * 64, slot, q.hk, from,
+                                                bar, pol);
                     }
                     __syncwarp();
-                    if (ok && need && page >= 0)
-                        bw::tma_load_4d(at + st * BYTES + (C::FP8 ? 0 : panel * C::PANEL) + box * box_bytes, values ? &tm_v : &tm_k,
-                                        panel * 64, pos % s.page_size, q.hk, page, bar, pol);
-                    if (!ok) --it;   // nothing was issued
                 }
             });
+            q = nq;
+            have = more;
+        }
         // no copy is in flight at the end, after a wait that ran out either
         int none = 0;
-        for (uint32_t i = it > (uint32_t)RING ? it - RING : 0; i < it; ++i)
-            bw::mbar_wait(full + 8 * (i % RING), (i / RING) & 1, &none, nullptr, 0, kWaitNs);
+#pragma unroll 1
+        for (int i = 0; i < RING; ++i)
+            if (filled >> i & 1) bw::mbar_wait(full + 8 * i, phases >> i & 1, &none, nullptr, 0, kWaitNs);
     } else if (warp == 8) {
         // ---- products ------------------------------------------------------------------------------
         constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
-        uint32_t it = 0, parts[2] = {0, 0}, uses[2] = {0, 0};   // stages; parts and blocks of a slot (of NS == 1: the first's)
+        Turn<!C::FP8, NST> turn;
+        uint32_t parts[2] = {0, 0}, uses[2] = {0, 0};   // parts and blocks of a slot (of NS == 1: the first's)
         bool ok = true;
+        // one lane issues; descriptors differ from step to step in their address alone
         auto scores = [&](int slot, uint32_t stage, uint32_t to) {
             if (ok && bw::elect_one()) {
-                const uint32_t a = q_at + slot * C::QTILE, b = stages + stage * C::STAGE;
+                const uint64_t a = bw::desc_sw128(q_at + slot * C::QTILE), b = bw::desc_sw128(stages + stage * C::STAGE);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    bw::mma_f16(to, bw::desc_sw128(a + (k / 4) * C::QPANEL + (k % 4) * 32),
-                                bw::desc_sw128(b + (k / 4) * C::PANEL + (k % 4) * 32), id_qk, k > 0);
+                    bw::mma_f16(to, a + ((k / 4) * C::QPANEL + (k % 4) * 32) / 16, b + ((k / 4) * C::PANEL + (k % 4) * 32) / 16, id_qk,
+                                k > 0);
             }
             __syncwarp();
         };
         auto outputs = [&](uint32_t weights, uint32_t stage, uint32_t to, bool more) {
             if (ok && bw::elect_one()) {
-                const uint32_t b = stages + stage * C::STAGE;
+                const uint64_t b = bw::desc_sw128_mn(stages + stage * C::STAGE, C::PANEL);
 #pragma unroll
-                for (int k = 0; k < C::SR / 16; ++k)
-                    bw::mma_f16_ta(to, weights + 8 * k, bw::desc_sw128_mn(b + k * 2048, C::PANEL), id_pv, more || k > 0);
+                for (int k = 0; k < C::SR / 16; ++k) bw::mma_f16_ta(to, weights + 8 * k, b + k * (2048 / 16), id_pv, more || k > 0);
             }
             __syncwarp();
         };
@@ -462,66 +535,68 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (ok && bw::elect_one()) bw::mma_commit(bar);
             __syncwarp();
         };
-        auto stage_in = [&] { ok = wait(ready + 8 * (it % NST), it / NST) && ok; bw::tc_fence_after(); };
+        auto stage_in = [&](bool values) {
+            turn.take(values);
+            ok = wait(ready + 8 * turn.stage, turn.use) && ok;
+            bw::tc_fence_after();
+            return turn.stage;
+        };
         Part q;
         while (walk.next(q)) {
             if (q.n == 0) continue;
+            // block j's weights by its values, then block j + 1's queries by keys, so that one
+            // tile's products run while the other's scores become weights
             if constexpr (C::NS == 2) {
-                const bool two = q.rows > 128;
-                // scores of a block by both tiles, given that its keys are the next stage
-                auto scores_of = [&](int slot) {
-                    scores(slot, it % NST, tmem + slot * 128);
-                    commit(s_full + 8 * slot);
-                    if (slot == 1 || !two) commit(empty + 8 * (it % NST));
-                };
-                ok = wait(q_full, parts[0]) && ok;
-                stage_in();
-                scores_of(0);
-                if (two) {
-                    ok = wait(q_full + 8, parts[1]) && ok;
-                    bw::tc_fence_after();
-                    scores_of(1);
-                }
-                ++it;
-                for (int j = 0; j < q.n; ++j) {
-                    const uint32_t v = it;
-                    stage_in();
-                    ++it;
-                    for (int slot = 0; slot < (two ? 2 : 1); ++slot) {
+                const int tiles = q.rows > 128 ? 2 : 1;
+                uint32_t k = 0, v = 0;   // stages of the next keys, of the values
+#pragma unroll 1
+                for (int i = -tiles; i < q.n * tiles; ++i) {
+                    const int slot = tiles == 2 ? i & 1 : 0, j = tiles == 2 ? i >> 1 : i;   // (j = -1: scores alone)
+                    const bool last = slot == tiles - 1;
+                    if (j < 0) {
+                        ok = wait(q_full + 8 * slot, parts[slot]) && ok;
+                    } else {
+                        if (slot == 0) v = stage_in(true);
                         ok = wait(p_full + 8 * slot, uses[slot]++) && ok;
                         if (j == 0) ok = wait(o_free + 8 * slot, parts[slot]++ + 1) && ok;
                         bw::tc_fence_after();
-                        outputs(tmem + slot * 128, v % NST, tmem + C::O_AT + slot * D, j > 0);
+                        outputs(tmem + slot * 128, v, tmem + C::O_AT + slot * D, j > 0);
                         commit(o_done + 8 * slot);
+                        if (last) commit(empty + 8 * v);
                         if (j + 1 == q.n) commit(o_last + 8 * slot);
-                        if (slot == 1 || !two) commit(empty + 8 * (v % NST));
-                        if (j + 1 < q.n) {
-                            if (slot == 0) stage_in();
-                            scores_of(slot);
-                        }
                     }
-                    if (j + 1 < q.n) ++it;
+                    if (j + 1 < q.n) {
+                        if (slot == 0) k = stage_in(false);
+                        bw::tc_fence_after();
+                        scores(slot, k, tmem + slot * 128);
+                        commit(s_full + 8 * slot);
+                        if (last) commit(empty + 8 * k);
+                    }
                 }
             } else {
-                auto scores_of = [&](uint32_t use) {
-                    for (int part = 0; part < C::PARTS; ++part, ++it) {
-                        stage_in();
-                        scores(0, it % NST, tmem + (use & 1) * 128 + part * C::SR);
-                        commit(empty + 8 * (it % NST));
+                // the next block's scores go before this one's outputs: they have a buffer of their own
+#pragma unroll 1
+                for (int j = -1; j < q.n; ++j) {
+                    const uint32_t use = uses[0] + (j < 0 ? 0 : 1);   // of the scores
+                    if (j < 0) ok = wait(q_full, parts[0]) && ok;
+                    if (j + 1 < q.n) {
+#pragma unroll 1
+                        for (int part = 0; part < C::PARTS; ++part) {
+                            const uint32_t k = stage_in(false);
+                            scores(0, k, tmem + (use & 1) * 128 + part * C::SR);
+                            commit(empty + 8 * k);
+                        }
+                        commit(s_full + 8 * (use & 1));
                     }
-                    commit(s_full + 8 * (use & 1));
-                };
-                ok = wait(q_full, parts[0]) && ok;
-                scores_of(uses[0]);
-                for (int j = 0; j < q.n; ++j) {
-                    const uint32_t use = uses[0]++;
-                    if (j + 1 < q.n) scores_of(use + 1);
-                    ok = wait(p_full + 8 * (use & 1), use >> 1) && ok;
+                    if (j < 0) continue;
+                    const uint32_t now = uses[0]++;
+                    ok = wait(p_full + 8 * (now & 1), now >> 1) && ok;
                     if (j == 0) ok = wait(o_free, parts[0]++ + 1) && ok;
-                    for (int part = 0; part < C::PARTS; ++part, ++it) {
-                        stage_in();
-                        outputs(tmem + (use & 1) * 128 + part * C::SR, it % NST, tmem + C::O_AT, j > 0 || part > 0);
-                        commit(empty + 8 * (it % NST));
+#pragma unroll 1
+                    for (int part = 0; part < C::PARTS; ++part) {
+                        const uint32_t v = stage_in(true);
+                        outputs(tmem + (now & 1) * 128 + part * C::SR, v, tmem + C::O_AT, j > 0 || part > 0);
+                        commit(empty + 8 * v);
                     }
                     commit(o_done);
                     if (j + 1 == q.n) commit(o_last);
@@ -533,13 +608,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         int none = 0;
         bw::mbar_wait(drain, 0, &none, nullptr, 0, kWaitNs);
-    } else if (C::FP8 ? warp >= 12 : warp >= 10) {
+    } else if (C::FP8 ? warp >= 12 : warp == 11) {
         // ---- between the copies and the products: 8-bit values become fp16; of values that not
         // every row attends to, rows that none does become zero, and what is not finite too (a
         // weight of zero would not hide it): its sign to the rows that see it is settled at their end
-        constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = C::FP8 ? 12 : 10, TEAM = 32 * C::READY;
+        constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = C::FP8 ? 12 : 11, TEAM = 32 * C::READY;
         const int me = threadIdx.x - 32 * FIRST;
-        uint32_t it = 0;
+        Turn<!C::FP8, RING> in;
+        Turn<!C::FP8, NST> turn;
         Part q;
         while (walk.next(q)) {
             if (q.n == 0) continue;
@@ -549,16 +625,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             each_block<C>(q.n, [&](bool values, int j) {
                 const int pos = (q.blk0 + j) * kBlk;
                 const bool part_seen = pos < q.all_lo || pos + kBlk > q.all_hi;
-                for (int part = 0; part < C::PARTS; ++part, ++it) {
+#pragma unroll 1
+                for (int part = 0; part < C::PARTS; ++part) {
                     const int p0 = pos + part * C::SR;
-                    wait(full + 8 * (it % RING), it / RING);
+                    in.take(values);
+                    turn.take(values);
+                    wait(full + 8 * in.stage, in.use);
                     const uint32_t pages = *const_cast<volatile uint8_t*>(&sm.pages[(q.gi + j) % kRing][part]);
                     const bool look = values && (part_seen || pages != (1u << G16) - 1);
                     auto live = [&](int row) { return p0 + row >= q.lo && p0 + row < q.hi && (pages >> (row / 16) & 1); };
-                    const uint32_t stage = stages + (it % NST) * C::STAGE;
+                    const uint32_t stage = stages + turn.stage * C::STAGE;
                     if constexpr (C::FP8) {
-                        wait(empty + 8 * (it % NST), it / NST + 1);
-                        const uint32_t raw = raws + (it % RING) * C::RAW;
+                        wait(empty + 8 * turn.stage, turn.use + 1);
+                        const uint32_t raw = raws + in.stage * C::RAW;
 #pragma unroll 4
                         for (int i = me; i < C::RAW / 16; i += TEAM) {
                             const int row = i / (D / 16), u = i % (D / 16), panel = u / 4, unit = 2 * (u % 4);
@@ -566,6 +645,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (look) {
                                 uint32_t x[4] = {w.x, w.y, w.z, w.w};
                                 const bool on = live(row);
+#pragma unroll
                                 for (int k = 0; k < 4; ++k) {
                                     // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
                                     const uint32_t nan = (((x[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
@@ -588,7 +668,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                         bw::fence_async_smem();
                         __syncwarp();
-                        if (lane == 0) bw::mbar_arrive(raw_free + 8 * (it % RING));
+                        if (lane == 0) bw::mbar_arrive(raw_free + 8 * in.stage);
                     } else if (look) {
                         // eight vectors at a time: what needs no change, almost all of them, costs a
                         // load and a few operations
@@ -606,6 +686,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 const bool on = live(i / 8 % C::SR);   // units change places within a row only
                                 if (on && !(bad && part_seen)) continue;
                                 uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     if (!on) x[e] = 0;
                                     if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u, *odd = 1;
@@ -617,7 +698,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         bw::fence_async_smem();
                         __syncwarp();
                     }
-                    if (lane == 0) bw::mbar_arrive(ready + 8 * (it % NST));
+                    if (lane == 0) bw::mbar_arrive(ready + 8 * turn.stage);
                 }
             });
         }
@@ -660,6 +741,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int i = 0; i < OC / 8; ++i) look(v[i]);
                 if (C::NS == 1 && on)
+#pragma unroll 1
                     for (int i = 0; i < OC / 8; ++i) look(src[(wg ? 0 : OC / 8) + i]);
                 // exponent field e: the largest is below 2^(e - 126); a factor within fp32's range
                 const int e = big >> 7, by = big == 0 || e == 255 ? 0 : max(-126, min(126, 141 - e));
@@ -689,6 +771,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             else asm volatile("bar.sync 2, 128;" ::: "memory");
         };
         auto advance = [&](Part& q) {
+#pragma unroll 1
             for (;;) {
                 group_meets();   // what stood there has been read
                 if (threadIdx.x % 128 == 0) sm.more[wg] = sm.walk[wg].next(q);
@@ -700,6 +783,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (q.none && r < q.rows) {
                     const int64_t o = out_row(q, r);
                     uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D + ch0);
+#pragma unroll 1
                     for (int i = 0; i < OC / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
                     if (p.a.lse && ch0 == 0) p.a.lse[o] = -INFINITY;
                 }
@@ -727,7 +811,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const volatile uint8_t* pages = sm.pages[(v.gi + j) % kRing];
                 const uint32_t in = C::NS == 2 ? pages[0] : pages[wg];
                 const bool edge = at < v.all_lo || at + C::COLS > v.all_hi || in != (1u << C::COLS / 16) - 1;
-                if (C::CAP || edge) {
+                if (C::CAP || __builtin_expect(edge, 0)) {
                     // scores are capped, and what this row does not attend to goes out, in place
 #pragma unroll 1
                     for (int c0 = 0; c0 < C::COLS; c0 += 32) {
@@ -768,7 +852,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 const float cand = top * c;
                 const bool raise = cand > m + 8.f;
-                if (__any_sync(~0u, raise)) {
+                if (__builtin_expect(__any_sync(~0u, raise), 0)) {
                     const float f = !raise ? 1.f : m == -INFINITY ? 0.f : ex2(m - cand);
                     if (raise) {
                         m = cand;
@@ -798,16 +882,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const float mu = m == -INFINITY ? 0.f : m, minus = C::UP - mu;
                 const float raw = m == -INFINITY ? 0.f : m_raw;
                 const bool far = __any_sync(~0u, fabsf(mu) > 0x1p20f);
+                float times = c, plus = minus;
+                if (__builtin_expect(far, 0)) {
+#pragma unroll
+                    for (int i = 0; i < C::COLS; ++i) {
+                        float* const x = reinterpret_cast<float*>(u[i / 32]);
+                        x[i % 32] = (x[i % 32] - raw) * c;
+                    }
+                    times = 1.f;
+                    plus = C::UP;
+                }
 #pragma unroll
                 for (int c0 = 0; c0 < C::COLS; c0 += 32) {
                     float* const x = reinterpret_cast<float*>(u[c0 / 32]);
-                    if (far) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) x[i] = (x[i] - raw) * c + C::UP;
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i += 2) fma2(x[i], x[i + 1], c, minus);
-                    }
+                    for (int i = 0; i < 32; i += 2) fma2(x[i], x[i + 1], times, plus);
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
@@ -842,6 +931,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
             const volatile uint8_t* f = sm.odd[q.busy % 8];
             bool odd = false;
+#pragma unroll 1
             for (int i = 0; i < C::READY; ++i) odd |= f[i] != 0;
             if (cut && threadIdx.x == 0) {
                 written |= 1u << side;
@@ -857,9 +947,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 bw::tmem_wait_ld32(o);
                 if (odd && on) {
                     // what is not finite among the values set aside goes to the rows that see it
+#pragma unroll 1
                     for (int j = 0; j < q.n; ++j) {
                         const int p0 = (q.blk0 + j) * kBlk;
                         if (p0 >= q.all_lo && p0 + kBlk <= q.all_hi) continue;
+#pragma unroll 1
                         for (int at = max(p0, see0); at < min(p0 + kBlk, see1); ++at) {
                             const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + at / s.page_size];
                             if (page < 0 || page >= s.n_pages) continue;
@@ -901,6 +993,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ++turn;
         }
         if (threadIdx.x == 0)
+#pragma unroll 1
             for (int side = 0; side < 2; ++side)
                 if (!(written >> side & 1)) p.recs[blockIdx.x * 2 + side].flags = 0;
     }

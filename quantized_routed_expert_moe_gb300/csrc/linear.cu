@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     // a wait that runs out (2 s) sets s_abort, which ends the others: the CTA's outputs are NaN
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return bw::mbar_wait(bar, parity, &s_abort, nullptr, 0, kWaitNs); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bw::mbar_wait_asleep(bar, parity, &s_abort, nullptr, 0, kWaitNs); };
 
     if (warp == 4) {
         // copies: each stage a box of W and one of x
