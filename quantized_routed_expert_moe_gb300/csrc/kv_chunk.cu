@@ -36,8 +36,8 @@ namespace {
 
 constexpr int kBlk = 128;              // cached tokens of a block
 constexpr int kRing = 16;              // blocks whose page flags are kept
+constexpr int kParts = 4;              // parts that the roles may be apart
 constexpr int kTileCost = 2;           // what a tile's beginning and end cost, in blocks
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 // Compile-time shape of one kernel: head dimension, cache type, capped scores.
 template <int D_, bool FP8_, bool CAP_>
@@ -96,7 +96,7 @@ struct Part {
     bool none;                // the tile has no blocks at all
 };
 
-// Walks a CTA's parts; every role does so by itself.
+// Walks a CTA's parts: by the warp that copies keys, for all roles.
 template <class C>
 struct Walk {
     const int *start, *len;   // shared memory
@@ -260,12 +260,12 @@ template <class C>
 struct Shared {
     uint64_t full[C::FP8 ? C::NRAW : C::NST], raw_free[4], ready[C::NST], empty[C::NST];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], o_free[2], drain;
+    uint64_t part_full[kParts], part_free[kParts], pair[4];
+    Part part[kParts];                // as the keys' copies go ahead; one of -1 blocks is the last
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
     uint32_t tmem;
-    int abort, bad_start, first, more[2];
-    Part part[2][2];                  // of a softmax group: its part and the next
-    Walk<C> walk[2];
+    int abort, bad_start, first;
     uint8_t pages[kRing][2];          // per block and part: groups of 16 tokens whose page is in the pool
     uint8_t odd[8][4];                // per part and warp: values that are not finite were set aside
     float row_max[2][2][C::NS == 1 ? 128 : 1], row_sum[2][C::NS == 1 ? 128 : 1];
@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const uint32_t full = bw::saddr(sm.full), raw_free = bw::saddr(sm.raw_free), ready = bw::saddr(sm.ready),
                    empty = bw::saddr(sm.empty), q_full = bw::saddr(sm.q_full), s_full = bw::saddr(sm.s_full),
                    p_full = bw::saddr(sm.p_full), o_done = bw::saddr(sm.o_done), o_last = bw::saddr(sm.o_last), o_free = bw::saddr(sm.o_free),
-                   drain = bw::saddr(&sm.drain);
+                   drain = bw::saddr(&sm.drain), part_full = bw::saddr(sm.part_full), part_free = bw::saddr(sm.part_free),
+                   pair = bw::saddr(sm.pair);
     uint32_t bits = 0;
 
     if (threadIdx.x == 0) {
@@ -310,6 +311,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::mbar_init(o_free + 8 * i, C::NS == 2 ? 4 : 8);
         }
         bw::mbar_init(drain, 1);
+#pragma unroll 1
+        for (int i = 0; i < kParts; ++i) {
+            bw::mbar_init(part_full + 8 * i, 1);
+            bw::mbar_init(part_free + 8 * i, 8 + 1 + C::READY + (C::FP8 ? 0 : 1));
+            bw::mbar_init(pair + 8 * i, 2);
+        }
         sm.abort = sm.bad_start = 0;
         bw::mbar_fence_init();
         bw::tma_prefetch_desc(&tm_k);
@@ -377,7 +384,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int r = threadIdx.x; r < rt; r += C::THREADS) sum += (long long)per_head(r) * s.n_kv_heads;
             scan_cta<long long, C::WARPS>(sum, sm.sums, total);
             const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
-            const long long from = c < ctas ? total * c / ctas : total, to = c < ctas ? total * (c + 1) / ctas : total;
+            // an even share, the first `more` CTAs one unit more (one 64-bit division)
+            const long long each = ctas ? total / ctas : 0, more = total - each * ctas;
+            const long long from = c < ctas ? each * c + min(c, more) : total, to = c < ctas ? from + each + (c < more) : total;
             walk.left = to - from;
             long long before = 0;
 #pragma unroll 1
@@ -397,8 +406,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int r = sm.first, b = find(r), u = per_head(r);
                 walk.b = b;
                 walk.i = r - pre[b];
-                walk.hk = (int)(sm.rem / u);
-                walk.off = (int)(sm.rem % u);
+                walk.hk = 0;
+#pragma unroll 1
+                for (long long left = sm.rem; left >= u || (walk.off = (int)left, false); left -= u) ++walk.hk;
             }
         } else if (threadIdx.x == 0) {
             bits |= MOE_KV_BAD_START;
@@ -413,7 +423,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncthreads();
     }
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return all_lanes(bw::mbar_wait_asleep(bar, parity & 1, &sm.abort, p.health, MOE_KV_TIMEOUT, kWaitNs));
+        return all_lanes(bw::mbar_wait_asleep(bar, parity & 1, &sm.abort));
+    };
+
+    // the parts in their order: n is the reader's own count, and what it took it gives back
+    auto take = [&](uint32_t n) -> const volatile Part& {
+        const bool there = wait(part_full + 8 * (n % kParts), n / kParts);
+        if (!there && lane == 0) sm.part[n % kParts].n = -1;   // (aborted)
+        __syncwarp();
+        return sm.part[n % kParts];
+    };
+    auto give = [&](uint32_t n) {
+        __syncwarp();
+        if (lane == 0) bw::mbar_arrive(part_free + 8 * (n % kParts));
     };
 
     if (warp >= 8) regs_down<C::REGS>();
@@ -432,7 +454,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             int page, slot;   // as the table has it; -1 where no row is attended to
             bool need;
         };
-        auto look_up = [&](const Part& q, int j) {
+        struct Piece {
+            int b, hk, lo, hi, blk0, n, gi;
+        };
+        auto look_up = [&](const Piece& q, int j) {
             const int pos = (q.blk0 + j) * kBlk + lane * p.box_rows;
             Box x;
             x.need = lane < boxes * C::PARTS && pos < q.hi && pos + p.box_rows > q.lo;
@@ -441,18 +466,52 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             x.page = x.need ? p.a.block_table[(int64_t)q.b * p.a.max_pages + i] : -1;
             return x;
         };
-        auto advance = [&](Part& q) {
-            while (walk.next(q))
-                if (q.n) return true;
-            return false;
+        uint32_t parts = 0;
+        bool ok = true;
+        // the next part with blocks; the keys' warp finds it for all, and writes the rows of tiles
+        // that have no blocks at all
+        auto advance = [&](Piece& q) {
+            if (keys) {
+                Part x;
+#pragma unroll 1
+                for (;;) {
+                    if (!walk.next(x)) {
+                        x.n = -1;
+                        break;
+                    }
+                    if (x.n) break;
+                    if (!x.none) continue;
+#pragma unroll 1
+                    for (int r = lane; r < x.rows; r += 32) {
+                        const int64_t o = (int64_t)(x.start + (x.row0 + r) / G) * s.n_heads + x.hk * G + (x.row0 + r) % G;
+                        uint4* const to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D);
+#pragma unroll 1
+                        for (int i = 0; i < D / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
+                        if (p.a.lse) p.a.lse[o] = -INFINITY;
+                    }
+                }
+                ok = wait(part_free + 8 * (parts % kParts), parts / kParts + 1) && ok;
+                if (!ok) x.n = -1;
+                if (lane == 0) {
+                    sm.part[parts % kParts] = x;
+                    bw::mbar_arrive(part_full + 8 * (parts % kParts));
+                }
+                q = Piece{x.b, x.hk, x.lo, x.hi, x.blk0, x.n, x.gi};
+            } else {
+                const volatile Part& x = take(parts);
+                q = Piece{x.b, x.hk, x.lo, x.hi, x.blk0, x.n, x.gi};
+                give(parts);
+            }
+            ++parts;
+            return q.n > 0;
         };
         Turn<!C::FP8, RING> turn;
         uint32_t filled = 0, phases = 0;   // stages with a copy of this warp's, and the parity of its phase
-        bool ok = true;
-        Part q, nq;
+        Piece q, nq;
         bool have = advance(q);
         Box ahead{}, seen[2] = {};   // of the next block; of keys that came, for their values
         if (have) ahead = look_up(q, 0);
+#pragma unroll 1
         while (have) {
             const bool more = advance(nq);
             each_block<C>(q.n, [&](bool values, int j) {
@@ -505,7 +564,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int none = 0;
 #pragma unroll 1
         for (int i = 0; i < RING; ++i)
-            if (filled >> i & 1) bw::mbar_wait(full + 8 * i, phases >> i & 1, &none, nullptr, 0, kWaitNs);
+            if (filled >> i & 1) bw::mbar_wait_asleep(full + 8 * i, phases >> i & 1, &none);
     } else if (warp == 8) {
         // ---- products ------------------------------------------------------------------------------
         constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
@@ -541,9 +600,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::tc_fence_after();
             return turn.stage;
         };
-        Part q;
-        while (walk.next(q)) {
-            if (q.n == 0) continue;
+        struct {
+            int n, rows;
+        } q;
+#pragma unroll 1
+        for (uint32_t part = 0;; ++part) {
+            const volatile Part& x = take(part);
+            q = {x.n, x.rows};
+            give(part);
+            if (q.n < 0) break;
             // block j's weights by its values, then block j + 1's queries by keys, so that one
             // tile's products run while the other's scores become weights
             if constexpr (C::NS == 2) {
@@ -607,7 +672,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (bw::elect_one()) bw::mma_commit(drain);
         __syncwarp();
         int none = 0;
-        bw::mbar_wait(drain, 0, &none, nullptr, 0, kWaitNs);
+        bw::mbar_wait_asleep(drain, 0, &none);
     } else if (C::FP8 ? warp >= 12 : warp == 11) {
         // ---- between the copies and the products: 8-bit values become fp16; of values that not
         // every row attends to, rows that none does become zero, and what is not finite too (a
@@ -616,10 +681,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int me = threadIdx.x - 32 * FIRST;
         Turn<!C::FP8, RING> in;
         Turn<!C::FP8, NST> turn;
-        Part q;
-        while (walk.next(q)) {
-            if (q.n == 0) continue;
-            volatile uint8_t* const odd = &sm.odd[q.busy % 8][warp - FIRST];
+        struct {
+            int n, blk0, lo, hi, all_lo, all_hi, gi;
+        } q;
+#pragma unroll 1
+        for (uint32_t at = 0;; ++at) {
+            const volatile Part& x = take(at);
+            q = {x.n, x.blk0, x.lo, x.hi, x.all_lo, x.all_hi, x.gi};
+            volatile uint8_t* const odd = &sm.odd[x.busy % 8][warp - FIRST];
+            give(at);
+            if (q.n < 0) break;
             if (lane == 0) *odd = 0;
             __syncwarp();
             each_block<C>(q.n, [&](bool values, int j) {
@@ -677,15 +748,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             uint4 w[8];
 #pragma unroll
                             for (int k = 0; k < 8; ++k) w[k] = ld_shared(stage + (i0 + k * TEAM) * 16);
+                            uint32_t todo = 0;
 #pragma unroll
                             for (int k = 0; k < 8; ++k) {
                                 // exponents of ones carry into the sign's place
                                 auto high = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
                                 const uint32_t bad = (high(w[k].x) | high(w[k].y) | high(w[k].z) | high(w[k].w)) & 0x80008000u;
-                                const int i = i0 + k * TEAM;
-                                const bool on = live(i / 8 % C::SR);   // units change places within a row only
-                                if (on && !(bad && part_seen)) continue;
-                                uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                                if ((bad && part_seen) || !live((i0 + k * TEAM) / 8 % C::SR)) todo |= 1u << k;   // units stay in their row
+                            }
+#pragma unroll 1
+                            for (; todo; todo &= todo - 1) {
+                                const int i = i0 + (__ffs(todo) - 1) * TEAM;
+                                const uint4 v = ld_shared(stage + i * 16);
+                                uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                                const bool on = live(i / 8 % C::SR);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
                                     if (!on) x[e] = 0;
@@ -717,11 +793,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         float c_next = 0.f;
 
-        auto out_row = [&](const Part& q, int r) {       // row of out and lse
+        auto out_row = [&](const volatile Part& q, int r) {       // row of out and lse
             return (int64_t)(q.start + (q.row0 + r) / G) * token_heads + q.hk * G + (q.row0 + r) % G;
         };
         // this thread's row of queries, to shared memory
-        auto load_q = [&](const Part& q) {
+        auto load_q = [&](const volatile Part& q) {
             const int r = slot * 128 + row;
             const bool on = r < q.rows;
             const int t = q.start + (q.row0 + r) / G, head = q.hk * G + (q.row0 + r) % G;
@@ -763,44 +839,114 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (lane == 0) bw::mbar_arrive(q_full + 8 * slot);
             c_next = c;
         };
-        // the next part with blocks for this group; rows of parts without any are written at once
-        // (parts stand in shared memory, where a row's scores leave them no registers)
-        if (threadIdx.x % 128 == 0) sm.walk[wg] = walk;
-        auto group_meets = [&] {
-            if (wg) asm volatile("bar.sync 3, 128;" ::: "memory");
-            else asm volatile("bar.sync 2, 128;" ::: "memory");
-        };
-        auto advance = [&](Part& q) {
-#pragma unroll 1
-            for (;;) {
-                group_meets();   // what stood there has been read
-                if (threadIdx.x % 128 == 0) sm.more[wg] = sm.walk[wg].next(q);
-                group_meets();
-                if (!*const_cast<volatile int*>(&sm.more[wg])) return false;
-                const int r = slot * 128 + row;
-                if (C::NS == 2 && slot && q.rows <= 128) continue;
-                if (q.n) return true;
-                if (q.none && r < q.rows) {
-                    const int64_t o = out_row(q, r);
-                    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D + ch0);
-#pragma unroll 1
-                    for (int i = 0; i < OC / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
-                    if (p.a.lse && ch0 == 0) p.a.lse[o] = -INFINITY;
-                }
-            }
+        // the two warps of a row's columns meet (heads of 256)
+        uint32_t met = 0;
+        auto pair_meets = [&] {
+            __syncwarp();
+            if (lane == 0) bw::mbar_arrive(pair + 8 * (warp % 4));
+            ok = wait(pair + 8 * (warp % 4), met++) && ok;
         };
 
-        uint32_t turn = 0;
-        bool have = advance(sm.part[wg][0]);
-        if (have) load_q(sm.part[wg][0]);
-        while (have) {
-            Part& q = sm.part[wg][turn & 1];
-            const volatile Part& v = q;
+        float m = -INFINITY, m_raw = 0.f, l[4] = {};   // maximum (scaled, base two; as it came), sums
+        uint32_t at_part = 0, parts = 0;
+        bool have = false;
+#pragma unroll 1
+        for (;;) {
+            // the next part's queries go ahead of this one's end; a second tile is not there for
+            // every part (and the end does not wait until it is: the part has to be given back)
+            const volatile Part& v = take(parts);
+            const int blocks = v.n;
+            const bool mine = blocks > 0 && (C::NS == 1 || slot == 0 || v.rows > 128);
+            if (mine) load_q(v);
+            if (have) {
+                const volatile Part& q = sm.part[at_part % kParts];
+                float sum = (l[0] + l[2]) + (l[1] + l[3]);
+                if constexpr (C::NS == 1) {
+                    sm.row_sum[wg][row] = sum;
+                    pair_meets();
+                    sum = sm.row_sum[0][row] + sm.row_sum[1][row];
+                }
+                ok = wait(o_last + 8 * slot, ended++) && ok;
+                bw::tc_fence_after();
+                const int r = slot * 128 + row, pos = q.base + (q.row0 + r) / G;
+                const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
+                const bool cut = !(q.first && q.last), on = r < q.rows;
+                const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
+                const volatile uint8_t* f = sm.odd[q.busy % 8];
+                bool odd = false;
+    #pragma unroll 1
+                for (int i = 0; i < C::READY; ++i) odd |= f[i] != 0;
+                if (cut && threadIdx.x == 0) {
+                    written |= 1u << side;
+                    p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
+                }
+                if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, sum);
+                const float inv = sum == 0.f ? 0.f : p.v_scale[q.hk] / sum;
+                const int64_t o_row = on ? out_row(q, r) : 0;
+    #pragma unroll 1
+                for (int i = 0; i < OC; i += 32) {
+                    uint32_t o[32];
+                    bw::tmem_ld32(o_at + i, o);
+                    bw::tmem_wait_ld32(o);
+                    if (odd && on) {
+                        // what is not finite among the values set aside goes to the rows that see it
+    #pragma unroll 1
+                        for (int j = 0; j < q.n; ++j) {
+                            const int p0 = (q.blk0 + j) * kBlk;
+                            if (p0 >= q.all_lo && p0 + kBlk <= q.all_hi) continue;
+    #pragma unroll 1
+                            for (int at = max(p0, see0); at < min(p0 + kBlk, see1); ++at) {
+                                const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + at / s.page_size];
+                                if (page < 0 || page >= s.n_pages) continue;
+                                const int64_t from = kv_offset(s, page, q.hk, at % s.page_size) + ch0 + i;
+    #pragma unroll
+                                for (int k = 0; k < 32; ++k) {
+                                    float v;
+                                    if constexpr (C::FP8)
+                                        v = (static_cast<const uint8_t*>(p.v_pages)[from + k] & 0x7f) == 0x7f ? NAN : 0.f;
+                                    else v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pages)[from + k]);
+                                    if (!isfinite(v)) o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
+                                }
+                            }
+                        }
+                    }
+                    if (cut && on) {
+                        float4* to = p.part_o + ((int64_t)rec * (D / 4) + (ch0 + i) / 4) * C::ROWS + r;
+    #pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            to[k * C::ROWS] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                    } else if (on) {
+                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o_row * D + ch0 + i);
+    #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            uint32_t h[4];
+    #pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                h[e] = pack2<false>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                            to[k] = make_uint4(h[0], h[1], h[2], h[3]);
+                        }
+                    }
+                }
+                bw::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bw::mbar_arrive(o_free + 8 * slot);
+                if (!cut && on && p.a.lse && ch0 == 0) p.a.lse[o_row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum * C::DOWN);
+                give(at_part);
+            }
+            if (blocks < 0) break;
+            have = mine;
+            if (!mine) {
+                give(parts++);
+                continue;
+            }
+            at_part = parts++;
             const float c = C::CAP ? 1.f : c_next * kLog2e;
             const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
-            const int pos = q.base + (q.row0 + slot * 128 + row) / G;
+            const int pos = v.base + (v.row0 + slot * 128 + row) / G;
             const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
-            float m = -INFINITY, m_raw = 0.f, l[4] = {};   // maximum (scaled, base two; as it came), sums
+            m = -INFINITY;
+            m_raw = l[0] = l[1] = l[2] = l[3] = 0.f;
 #pragma unroll 1
             for (int j = 0; j < v.n; ++j, ++uses) {
                 const int buf = C::NS == 2 ? slot : uses & 1, phase = C::NS == 2 ? uses : uses >> 1;
@@ -847,7 +993,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 if constexpr (C::NS == 1) {
                     sm.row_max[uses & 1][wg][row] = top;
-                    asm volatile("bar.sync 1, 256;" ::: "memory");
+                    pair_meets();
                     top = fmaxf(top, sm.row_max[uses & 1][wg ^ 1][row]);
                 }
                 const float cand = top * c;
@@ -914,92 +1060,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) bw::mbar_arrive(p_full + 8 * buf);
             }
-            // the next part's queries go ahead of this one's end
-            const bool more = advance(sm.part[wg][~turn & 1]);
-            if (more) load_q(sm.part[wg][~turn & 1]);
-
-            float sum = (l[0] + l[2]) + (l[1] + l[3]);
-            if constexpr (C::NS == 1) {
-                sm.row_sum[wg][row] = sum;
-                asm volatile("bar.sync 1, 256;" ::: "memory");
-                sum = sm.row_sum[0][row] + sm.row_sum[1][row];
-            }
-            ok = wait(o_last + 8 * slot, ended++) && ok;
-            bw::tc_fence_after();
-            const int r = slot * 128 + row;
-            const bool cut = !(q.first && q.last), on = r < q.rows;
-            const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
-            const volatile uint8_t* f = sm.odd[q.busy % 8];
-            bool odd = false;
-#pragma unroll 1
-            for (int i = 0; i < C::READY; ++i) odd |= f[i] != 0;
-            if (cut && threadIdx.x == 0) {
-                written |= 1u << side;
-                p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
-            }
-            if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, sum);
-            const float inv = sum == 0.f ? 0.f : p.v_scale[q.hk] / sum;
-            const int64_t o_row = on ? out_row(q, r) : 0;
-#pragma unroll 1
-            for (int i = 0; i < OC; i += 32) {
-                uint32_t o[32];
-                bw::tmem_ld32(o_at + i, o);
-                bw::tmem_wait_ld32(o);
-                if (odd && on) {
-                    // what is not finite among the values set aside goes to the rows that see it
-#pragma unroll 1
-                    for (int j = 0; j < q.n; ++j) {
-                        const int p0 = (q.blk0 + j) * kBlk;
-                        if (p0 >= q.all_lo && p0 + kBlk <= q.all_hi) continue;
-#pragma unroll 1
-                        for (int at = max(p0, see0); at < min(p0 + kBlk, see1); ++at) {
-                            const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + at / s.page_size];
-                            if (page < 0 || page >= s.n_pages) continue;
-                            const int64_t from = kv_offset(s, page, q.hk, at % s.page_size) + ch0 + i;
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) {
-                                float v;
-                                if constexpr (C::FP8)
-                                    v = (static_cast<const uint8_t*>(p.v_pages)[from + k] & 0x7f) == 0x7f ? NAN : 0.f;
-                                else v = __bfloat162float(static_cast<const __nv_bfloat16*>(p.v_pages)[from + k]);
-                                if (!isfinite(v)) o[k] = __float_as_uint(__uint_as_float(o[k]) + v);
-                            }
-                        }
-                    }
-                }
-                if (cut && on) {
-                    float4* to = p.part_o + ((int64_t)rec * (D / 4) + (ch0 + i) / 4) * C::ROWS + r;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        to[k * C::ROWS] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                      __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                } else if (on) {
-                    uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o_row * D + ch0 + i);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        uint32_t h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            h[e] = pack2<false>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                        to[k] = make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                }
-            }
-            bw::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bw::mbar_arrive(o_free + 8 * slot);
-            if (!cut && on && p.a.lse && ch0 == 0) p.a.lse[o_row] = sum == 0.f ? -INFINITY : m * kLn2 + logf(sum * C::DOWN);
-            have = more;
-            ++turn;
         }
         if (threadIdx.x == 0)
 #pragma unroll 1
             for (int side = 0; side < 2; ++side)
                 if (!(written >> side & 1)) p.recs[blockIdx.x * 2 + side].flags = 0;
     }
-    if (bits) atomicOr(p.health, bits);
     bw::tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0 && sm.abort) bits |= MOE_KV_TIMEOUT;
+    if (bits) atomicOr(p.health, bits);
     if (warp == 8) {
         bw::tc_fence_after();
         bw::tmem_dealloc(tmem, 512);
