@@ -53,13 +53,13 @@ struct Cfg {
     static constexpr int QPANEL = 128 * 128, QTILE = 128 * D * 2;
     static constexpr int NST = FP8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 4);
     static constexpr int RAW = SR * D, NRAW = FP8 ? 3 : 0;    // 8-bit stages, before conversion
-    static constexpr int WARPS = FP8 ? 16 : 12, THREADS = 32 * WARPS;
+    static constexpr int WARPS = 16, THREADS = 32 * WARPS;
     static constexpr int COLS = NS == 2 ? 128 : 64;      // score columns of a softmax thread
     // Registers of a softmax thread, and of the others: together those of the launch.
-    static constexpr int SOFTMAX_REGS = FP8 ? 176 : 200, REGS = FP8 ? 80 : 104;
+    static constexpr int SOFTMAX_REGS = 176, REGS = 80;
     static_assert(256 * SOFTMAX_REGS + (THREADS - 256) * REGS <= THREADS * (65536 / THREADS / 8 * 8), "more registers than launched with");
     static constexpr int O_AT = 256;                     // tensor-memory column of the outputs
-    static constexpr int READY = FP8 ? 4 : 1;            // warps that pass a stage on
+    static constexpr int READY = 4;                                // warps that pass a stage on
     // An 8-bit cache is exact in fp16, and so are queries scaled to their row's largest; the
     // weights are 2^7 times their size, at most 2^15: 2^-31 of exp(m) is their smallest step.
     static constexpr float UP = FP8 ? 7.f : 0.f, DOWN = FP8 ? 0x1p-7f : 1.f;
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int i = 0; i < NST; ++i) {
             if (!C::FP8) bw::mbar_init(full + 8 * i, 1);
             bw::mbar_init(ready + 8 * i, C::READY);
-            bw::mbar_init(empty + 8 * i, 1);
+            bw::mbar_init(empty + 8 * i, C::NS);
         }
 #pragma unroll 1
         for (int i = 0; i < C::NRAW; ++i) {
@@ -310,11 +310,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::mbar_init(o_last + 8 * i, 1);
             bw::mbar_init(o_free + 8 * i, C::NS == 2 ? 4 : 8);
         }
-        bw::mbar_init(drain, 1);
+        bw::mbar_init(drain, C::NS);
 #pragma unroll 1
         for (int i = 0; i < kParts; ++i) {
             bw::mbar_init(part_full + 8 * i, 1);
-            bw::mbar_init(part_free + 8 * i, 8 + 1 + C::READY + (C::FP8 ? 0 : 1));
+            bw::mbar_init(part_free + 8 * i, 8 + C::NS + C::READY + (C::FP8 ? 0 : 1));
             bw::mbar_init(pair + 8 * i, 2);
         }
         sm.abort = sm.bad_start = 0;
@@ -565,11 +565,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
         for (int i = 0; i < RING; ++i)
             if (filled >> i & 1) bw::mbar_wait_asleep(full + 8 * i, phases >> i & 1, &none);
-    } else if (warp == 8) {
+    } else if (warp == 8 || (C::NS == 2 && warp == 11)) {
         // ---- products ------------------------------------------------------------------------------
         constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
         Turn<!C::FP8, NST> turn;
-        uint32_t parts[2] = {0, 0}, uses[2] = {0, 0};   // parts and blocks of a slot (of NS == 1: the first's)
+        uint32_t parts = 0, uses = 0;   // of this tile: parts and blocks
+        const int slot = warp == 8 ? 0 : 1;
         bool ok = true;
         // one lane issues; descriptors differ from step to step in their address alone
         auto scores = [&](int slot, uint32_t stage, uint32_t to) {
@@ -609,41 +610,47 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             q = {x.n, x.rows};
             give(part);
             if (q.n < 0) break;
-            // block j's weights by its values, then block j + 1's queries by keys, so that one
-            // tile's products run while the other's scores become weights
+            // Block j's weights by its values, then block j + 1's queries by keys, so that one
+            // tile's products run while the other's scores become weights. Each tile has an issuing
+            // warp: a wait behind issued products ends only when those have left the queue, and
+            // one warp for both left gaps of 400 and 680 cycles in a block's 3000.
             if constexpr (C::NS == 2) {
-                const int tiles = q.rows > 128 ? 2 : 1;
-                uint32_t k = 0, v = 0;   // stages of the next keys, of the values
+                const bool two = q.rows > 128;
+                if (slot && !two) {   // not there: pass the stages on, one by one, so as not to lose count
+                    each_block<C>(q.n, [&](bool values, int) {
+                        const uint32_t st = stage_in(values);
+                        if (bw::elect_one()) bw::mbar_arrive(empty + 8 * st);
+                        __syncwarp();
+                    });
+                    continue;
+                }
 #pragma unroll 1
-                for (int i = -tiles; i < q.n * tiles; ++i) {
-                    const int slot = tiles == 2 ? i & 1 : 0, j = tiles == 2 ? i >> 1 : i;   // (j = -1: scores alone)
-                    const bool last = slot == tiles - 1;
+                for (int j = -1; j < q.n; ++j) {   // (-1: scores alone)
                     if (j < 0) {
-                        ok = wait(q_full + 8 * slot, parts[slot]) && ok;
+                        ok = wait(q_full + 8 * slot, parts) && ok;
                     } else {
-                        if (slot == 0) v = stage_in(true);
-                        ok = wait(p_full + 8 * slot, uses[slot]++) && ok;
-                        if (j == 0) ok = wait(o_free + 8 * slot, parts[slot]++ + 1) && ok;
+                        const uint32_t v = stage_in(true);
+                        ok = wait(p_full + 8 * slot, uses++) && ok;
+                        if (j == 0) ok = wait(o_free + 8 * slot, parts++ + 1) && ok;
                         bw::tc_fence_after();
                         outputs(tmem + slot * 128, v, tmem + C::O_AT + slot * D, j > 0);
                         commit(o_done + 8 * slot);
-                        if (last) commit(empty + 8 * v);
+                        commit(empty + 8 * v);
                         if (j + 1 == q.n) commit(o_last + 8 * slot);
                     }
                     if (j + 1 < q.n) {
-                        if (slot == 0) k = stage_in(false);
-                        bw::tc_fence_after();
+                        const uint32_t k = stage_in(false);
                         scores(slot, k, tmem + slot * 128);
                         commit(s_full + 8 * slot);
-                        if (last) commit(empty + 8 * k);
+                        commit(empty + 8 * k);
                     }
                 }
             } else {
                 // the next block's scores go before this one's outputs: they have a buffer of their own
 #pragma unroll 1
                 for (int j = -1; j < q.n; ++j) {
-                    const uint32_t use = uses[0] + (j < 0 ? 0 : 1);   // of the scores
-                    if (j < 0) ok = wait(q_full, parts[0]) && ok;
+                    const uint32_t use = uses + (j < 0 ? 0 : 1);   // of the scores
+                    if (j < 0) ok = wait(q_full, parts) && ok;
                     if (j + 1 < q.n) {
 #pragma unroll 1
                         for (int part = 0; part < C::PARTS; ++part) {
@@ -654,9 +661,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         commit(s_full + 8 * (use & 1));
                     }
                     if (j < 0) continue;
-                    const uint32_t now = uses[0]++;
+                    const uint32_t now = uses++;
                     ok = wait(p_full + 8 * (now & 1), now >> 1) && ok;
-                    if (j == 0) ok = wait(o_free, parts[0]++ + 1) && ok;
+                    if (j == 0) ok = wait(o_free, parts++ + 1) && ok;
 #pragma unroll 1
                     for (int part = 0; part < C::PARTS; ++part) {
                         const uint32_t v = stage_in(true);
@@ -673,11 +680,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncwarp();
         int none = 0;
         bw::mbar_wait_asleep(drain, 0, &none);
-    } else if (C::FP8 ? warp >= 12 : warp == 11) {
+    } else if (warp >= 12) {
         // ---- between the copies and the products: 8-bit values become fp16; of values that not
         // every row attends to, rows that none does become zero, and what is not finite too (a
         // weight of zero would not hide it): its sign to the rows that see it is settled at their end
-        constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = C::FP8 ? 12 : 11, TEAM = 32 * C::READY;
+        constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = 12, TEAM = 32 * C::READY;
         const int me = threadIdx.x - 32 * FIRST;
         Turn<!C::FP8, RING> in;
         Turn<!C::FP8, NST> turn;
