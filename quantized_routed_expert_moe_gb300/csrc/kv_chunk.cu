@@ -56,7 +56,7 @@ struct Cfg {
     static constexpr int WARPS = 16, THREADS = 32 * WARPS;
     static constexpr int COLS = NS == 2 ? 128 : 64;      // score columns of a softmax thread
     // Registers of a softmax thread, and of the others: together those of the launch.
-    static constexpr int SOFTMAX_REGS = 176, REGS = 80;
+    static constexpr int SOFTMAX_REGS = 184, REGS = 72;
     static_assert(256 * SOFTMAX_REGS + (THREADS - 256) * REGS <= THREADS * (65536 / THREADS / 8 * 8), "more registers than launched with");
     static constexpr int O_AT = 256;                     // tensor-memory column of the outputs
     static constexpr int READY = 4;                                // warps that pass a stage on
@@ -260,12 +260,13 @@ template <class C>
 struct Shared {
     uint64_t full[C::FP8 ? C::NRAW : C::NST], raw_free[4], ready[C::NST], empty[C::NST];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], o_free[2], drain;
-    uint64_t part_full[kParts], part_free[kParts], pair[4];
+    uint64_t part_full[kParts], part_free[kParts], pair[4], order[2];
     Part part[kParts];                // as the keys' copies go ahead; one of -1 blocks is the last
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
     uint32_t tmem;
     int abort, bad_start, first;
+    int lost;                         // some page was not in the pool
     uint8_t pages[kRing][2];          // per block and part: groups of 16 tokens whose page is in the pool
     uint8_t odd[8][4];                // per part and warp: values that are not finite were set aside
     float row_max[2][2][C::NS == 1 ? 128 : 1], row_sum[2][C::NS == 1 ? 128 : 1];
@@ -286,7 +287,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                    empty = bw::saddr(sm.empty), q_full = bw::saddr(sm.q_full), s_full = bw::saddr(sm.s_full),
                    p_full = bw::saddr(sm.p_full), o_done = bw::saddr(sm.o_done), o_last = bw::saddr(sm.o_last), o_free = bw::saddr(sm.o_free),
                    drain = bw::saddr(&sm.drain), part_full = bw::saddr(sm.part_full), part_free = bw::saddr(sm.part_free),
-                   pair = bw::saddr(sm.pair);
+                   pair = bw::saddr(sm.pair), order = bw::saddr(sm.order);
     uint32_t bits = 0;
 
     if (threadIdx.x == 0) {
@@ -311,13 +312,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::mbar_init(o_free + 8 * i, C::NS == 2 ? 4 : 8);
         }
         bw::mbar_init(drain, C::NS);
+        bw::mbar_init(order, 1);
+        bw::mbar_init(order + 8, 1);
 #pragma unroll 1
         for (int i = 0; i < kParts; ++i) {
             bw::mbar_init(part_full + 8 * i, 1);
             bw::mbar_init(part_free + 8 * i, 8 + C::NS + C::READY + (C::FP8 ? 0 : 1));
             bw::mbar_init(pair + 8 * i, 2);
         }
-        sm.abort = sm.bad_start = 0;
+        sm.abort = sm.bad_start = sm.lost = 0;
         bw::mbar_fence_init();
         bw::tma_prefetch_desc(&tm_k);
         bw::tma_prefetch_desc(&tm_v);
@@ -423,7 +426,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         __syncthreads();
     }
     auto wait = [&](uint32_t bar, uint32_t parity) {
-        return all_lanes(bw::mbar_wait_asleep(bar, parity & 1, &sm.abort));
+        return all_lanes(bw::mbar_wait_short(bar, parity & 1, &sm.abort));
     };
 
     // the parts in their order: n is the reader's own count, and what it took it gives back
@@ -533,6 +536,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int g = 0; lost && g < G16; ++g)
                         if (lost >> (lane * boxes + g * 16 / p.box_rows) & 1) groups &= ~(1u << g);
                     sm.pages[(q.gi + j) % kRing][lane] = (uint8_t)groups;
+                    if (lost) *const_cast<volatile int*>(&sm.lost) = 1;
                 }
                 __syncwarp();
 #pragma unroll
@@ -564,12 +568,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         int none = 0;
 #pragma unroll 1
         for (int i = 0; i < RING; ++i)
-            if (filled >> i & 1) bw::mbar_wait_asleep(full + 8 * i, phases >> i & 1, &none);
+            if (filled >> i & 1) bw::mbar_wait_short(full + 8 * i, phases >> i & 1, &none);
     } else if (warp == 8 || (C::NS == 2 && warp == 11)) {
         // ---- products ------------------------------------------------------------------------------
         constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
         Turn<!C::FP8, NST> turn;
-        uint32_t parts = 0, uses = 0;   // of this tile: parts and blocks
+        uint32_t parts = 0, uses = 0, steps = 0;   // of this tile: parts, blocks, turns with the other
         const int slot = warp == 8 ? 0 : 1;
         bool ok = true;
         // one lane issues; descriptors differ from step to step in their address alone
@@ -630,8 +634,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         ok = wait(q_full + 8 * slot, parts) && ok;
                     } else {
                         const uint32_t v = stage_in(true);
-                        ok = wait(p_full + 8 * slot, uses++) && ok;
                         if (j == 0) ok = wait(o_free + 8 * slot, parts++ + 1) && ok;
+                        // in turns, the first tile first: left alone, both tiles' products mix and
+                        // both softmaxes wait for them at the same time (4900 cycles a block)
+                        if (two) ok = wait(order + 8 * slot, slot ? steps : steps + 1) && ok;
+                        steps += two;
+                        ok = wait(p_full + 8 * slot, uses++) && ok;
                         bw::tc_fence_after();
                         outputs(tmem + slot * 128, v, tmem + C::O_AT + slot * D, j > 0);
                         commit(o_done + 8 * slot);
@@ -643,6 +651,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         scores(slot, k, tmem + slot * 128);
                         commit(s_full + 8 * slot);
                         commit(empty + 8 * k);
+                    }
+                    if (two && j >= 0) {
+                        if (bw::elect_one()) bw::mbar_arrive(order + 8 * (slot ^ 1));
+                        __syncwarp();
                     }
                 }
             } else {
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (bw::elect_one()) bw::mma_commit(drain);
         __syncwarp();
         int none = 0;
-        bw::mbar_wait_asleep(drain, 0, &none);
+        bw::mbar_wait_short(drain, 0, &none);
     } else if (warp >= 12) {
         // ---- between the copies and the products: 8-bit values become fp16; of values that not
         // every row attends to, rows that none does become zero, and what is not finite too (a
@@ -952,19 +964,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
             const int pos = v.base + (v.row0 + slot * 128 + row) / G;
             const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
+            const int n = v.n, blk0 = v.blk0, all_lo = v.all_lo, all_hi = v.all_hi;
             m = -INFINITY;
             m_raw = l[0] = l[1] = l[2] = l[3] = 0.f;
 #pragma unroll 1
-            for (int j = 0; j < v.n; ++j, ++uses) {
+            for (int j = 0; j < n; ++j, ++uses) {
                 const int buf = C::NS == 2 ? slot : uses & 1, phase = C::NS == 2 ? uses : uses >> 1;
-                const int at = (v.blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
+                const int at = (blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
                 const uint32_t s_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * C::COLS);
                 ok = wait(s_full + 8 * buf, phase) && ok;
                 bw::tc_fence_after();
-                const volatile uint8_t* pages = sm.pages[(v.gi + j) % kRing];
-                const uint32_t in = C::NS == 2 ? pages[0] : pages[wg];
-                const bool edge = at < v.all_lo || at + C::COLS > v.all_hi || in != (1u << C::COLS / 16) - 1;
+                const bool edge = at < all_lo || at + C::COLS > all_hi || *const_cast<volatile int*>(&sm.lost);
                 if (C::CAP || __builtin_expect(edge, 0)) {
+                    const volatile uint8_t* pages = sm.pages[(v.gi + j) % kRing];
+                    const uint32_t in = C::NS == 2 ? pages[0] : pages[wg];
                     // scores are capped, and what this row does not attend to goes out, in place
 #pragma unroll 1
                     for (int c0 = 0; c0 < C::COLS; c0 += 32) {

@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     pdl_trigger();
     // a wait that runs out (2 s) sets s_abort, which ends the others: the CTA's outputs are NaN
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
-    auto wait = [&](uint32_t bar, uint32_t parity) { return bw::mbar_wait_asleep(bar, parity, &s_abort); };
+    auto wait = [&](uint32_t bar, uint32_t parity) { return bw::mbar_wait_short(bar, parity, &s_abort); };
 
     if (warp == 4) {
         // copies: each stage a box of W and one of x
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // no copy is in flight at the end, after a wait that ran out either
             int none = 0;
             for (uint32_t q = it > (uint32_t)S ? it - S : 0; q < it; ++q)
-                bw::mbar_wait_asleep(full + 8 * (q % S), (q / S) & 1, &none);
+                bw::mbar_wait_short(full + 8 * (q % S), (q / S) & 1, &none);
         }
     } else if (warp == 5) {
         uint32_t it = 0, acc = 0;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (bw::elect_one()) bw::mma_commit(done);
             __syncwarp();
             int none = 0;
-            bw::mbar_wait_asleep(done, 0, &none);
+            bw::mbar_wait_short(done, 0, &none);
         }
     } else if (p.splits == 1) {
         const int row = warp * 32 + lane;
