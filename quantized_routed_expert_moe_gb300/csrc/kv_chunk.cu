@@ -46,9 +46,12 @@ struct Cfg {
     static constexpr bool FP8 = FP8_, CAP = CAP_;
     static constexpr int NS = D == 256 ? 1 : 2;          // row tiles in flight
     static constexpr int ROWS = 128 * NS;
-    static constexpr int PARTS = D == 256 ? 2 : 1;       // stages of a block of keys (or values)
-    static constexpr int SR = kBlk / PARTS;              // tokens of a stage
-    static constexpr int PANEL = SR * 128, PANELS = D / 64;   // a stage is panels of 64 channels
+    // A block of keys or values of heads of 256 takes two stages: values by tokens, keys by
+    // channels, since a product of 128 x 64 takes as long as one of 128 x 128.
+    static constexpr int PARTS = D == 256 ? 2 : 1;
+    static constexpr int SR = kBlk / PARTS;              // tokens of a stage of values
+    static constexpr int KD = D / PARTS;                 // channels of a stage of keys
+    static constexpr int PANEL = SR * 128, KPANEL = kBlk * 128;   // a stage is panels of 64 channels
     static constexpr int STAGE = SR * D * 2;
     static constexpr int QPANEL = 128 * 128, QTILE = 128 * D * 2;
     static constexpr int NST = FP8 ? (D == 64 ? 6 : 3) : (D == 64 ? 8 : 4);
@@ -82,6 +85,7 @@ struct ChunkArgs {
     float2* part_ml;    // [CTA][2][ROWS]: maximum (base two) and sum
     float4* part_o;     // [CTA][2][D / 4][ROWS]
     int G, box_rows;
+    bool whole;         // tiles are not cut: their blocks are few
 };
 
 // The blocks of one tile that a CTA takes.
@@ -101,6 +105,7 @@ template <class C>
 struct Walk {
     const int *start, *len;   // shared memory
     int G, Hk, window, b, i, hk, off, index, busy, gi;
+    bool whole;               // a unit is a tile, not a block
     long long left;
 
     __device__ __forceinline__ static int blocks_of(int lo, int hi) { return hi > lo ? (hi + kBlk - 1) / kBlk - lo / kBlk : 0; }
@@ -121,7 +126,7 @@ struct Walk {
         q.all_lo = first_seen(p1, window);
         q.all_hi = p0 + 1;
         const int c = blocks_of(q.lo, q.hi), units = c + kTileCost;
-        const int take = (int)min((long long)(units - off), left);
+        const int take = whole ? units : (int)min((long long)(units - off), left);
         const int b0 = max(off - kTileCost, 0), b1 = max(off + take - kTileCost, 0);
         q.blk0 = q.lo / kBlk + b0;
         q.n = b1 - b0;
@@ -133,7 +138,7 @@ struct Walk {
         busy += q.n > 0;
         q.gi = gi;
         gi += q.n;
-        left -= take;
+        left -= whole ? 1 : take;
         off += take;
         if (off == units) {
             off = 0;
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto per_head = [&](int r) {
             const int b = find(r), n = sm.start[b + 1] - sm.start[b], row0 = (r - pre[b]) * C::ROWS;
             const int p0 = sm.len[b] - n + row0 / G, p1 = sm.len[b] - n + (min(row0 + C::ROWS, n * G) - 1) / G;
-            return Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1) + kTileCost;
+            return p.whole ? 1 : Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1) + kTileCost;
         };
         walk.left = 0;
         if (!sm.bad_start) {
@@ -421,6 +426,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         walk.G = G;
         walk.Hk = s.n_kv_heads;
         walk.window = p.a.window;
+        walk.whole = p.whole;
         walk.index = walk.busy = walk.gi = 0;
         bw::fence_async_smem();   // `pre` lies where copies will land
         __syncthreads();
@@ -446,11 +452,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // ---- copies: of keys by one warp, of values by another. A lane looks up a box's page a
         // block ahead, one lane starts the copies ------------------------------------------------------
         constexpr int RING = C::FP8 ? C::NRAW : NST, BYTES = C::FP8 ? C::RAW : C::STAGE;
-        constexpr int WIDTH = C::FP8 ? 1 : C::PANELS;
         const bool keys = warp == 9, vals = C::FP8 || warp == 10;   // whose copies this warp starts
         const uint32_t at = C::FP8 ? raws : stages, gone = C::FP8 ? raw_free : empty;
         const int boxes = C::SR / p.box_rows;
-        const uint32_t box_bytes = p.box_rows * (C::FP8 ? D : 128);
         const uint64_t pol = bw::l2_evict_normal();
         // lane: box `lane` of the block's keys (or values), all of whose channels it stands for
         struct Box {
@@ -547,16 +551,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!ok) continue;   // nothing is issued any more
                     filled |= 1u << turn.stage;
                     phases = (phases & ~(1u << turn.stage)) | (turn.use & 1) << turn.stage;
+                    // boxes of this stage, and their panels
+                    const int b0 = values ? part * boxes : 0, b1 = values ? b0 + boxes : C::PARTS * boxes;
+                    const int x0 = values ? 0 : part * C::KD, width = values ? D : C::KD;
+                    const uint32_t box_bytes = p.box_rows * (C::FP8 ? width : 128);
                     if (bw::elect_one())
-                        bw::mbar_arrive_tx(bar, __popc(come >> (part * boxes) & ((1u << boxes) - 1)) * box_bytes * WIDTH);
+                        bw::mbar_arrive_tx(bar, __popc(come >> b0 & ((1u << (b1 - b0)) - 1)) * p.box_rows * width * (C::FP8 ? 1 : 2));
 #pragma unroll 1
-                    for (int box = 0; box < boxes; ++box) {
-                        const int from = __shfl_sync(~0u, page, part * boxes + box), slot = __shfl_sync(~0u, x.slot, part * boxes + box);
+                    for (int box = b0; box < b1; ++box) {
+                        const int from = __shfl_sync(~0u, page, box), slot = __shfl_sync(~0u, x.slot, box);
                         if (from >= 0 && bw::elect_one())
 #pragma unroll
-                            for (int panel = 0; panel < WIDTH; ++panel)
-                                bw::tma_load_4d(to + (C::FP8 ? 0 : panel * C::PANEL) + box * box_bytes, values ? &tm_v : &tm_k, panel * 64, slot, q.hk, from,
-                                                bar, pol);
+                            for (int c = 0; c < (C::FP8 ? 1 : D / 64); ++c)
+                                if (C::FP8 || c * 64 < width)
+                                    bw::tma_load_4d(to + c * (values ? C::PANEL : C::KPANEL) + (box - b0) * box_bytes,
+                                                    values ? &tm_v : &tm_k, x0 + 64 * c, slot, q.hk, from, bar, pol);
                     }
                     __syncwarp();
                 }
@@ -571,19 +580,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (filled >> i & 1) bw::mbar_wait_short(full + 8 * i, phases >> i & 1, &none);
     } else if (warp == 8 || (C::NS == 2 && warp == 11)) {
         // ---- products ------------------------------------------------------------------------------
-        constexpr uint32_t id_qk = bw::idesc_f16_f32(128, C::SR, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
+        constexpr uint32_t id_qk = bw::idesc_f16_f32(128, kBlk, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
         Turn<!C::FP8, NST> turn;
         uint32_t parts = 0, uses = 0, steps = 0;   // of this tile: parts, blocks, turns with the other
         const int slot = warp == 8 ? 0 : 1;
         bool ok = true;
         // one lane issues; descriptors differ from step to step in their address alone
-        auto scores = [&](int slot, uint32_t stage, uint32_t to) {
+        auto scores = [&](int slot, uint32_t stage, uint32_t to, int part) {
             if (ok && bw::elect_one()) {
-                const uint64_t a = bw::desc_sw128(q_at + slot * C::QTILE), b = bw::desc_sw128(stages + stage * C::STAGE);
+                const uint64_t a = bw::desc_sw128(q_at + slot * C::QTILE + part * (C::KD / 64) * C::QPANEL), b = bw::desc_sw128(stages + stage * C::STAGE);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    bw::mma_f16(to, a + ((k / 4) * C::QPANEL + (k % 4) * 32) / 16, b + ((k / 4) * C::PANEL + (k % 4) * 32) / 16, id_qk,
-                                k > 0);
+                for (int k = 0; k < C::KD / 16; ++k)
+                    bw::mma_f16(to, a + ((k / 4) * C::QPANEL + (k % 4) * 32) / 16, b + ((k / 4) * C::KPANEL + (k % 4) * 32) / 16, id_qk,
+                                part > 0 || k > 0);
             }
             __syncwarp();
         };
@@ -648,7 +657,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     if (j + 1 < q.n) {
                         const uint32_t k = stage_in(false);
-                        scores(slot, k, tmem + slot * 128);
+                        scores(slot, k, tmem + slot * 128, 0);
                         commit(s_full + 8 * slot);
                         commit(empty + 8 * k);
                     }
@@ -667,7 +676,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
                         for (int part = 0; part < C::PARTS; ++part) {
                             const uint32_t k = stage_in(false);
-                            scores(0, k, tmem + (use & 1) * 128 + part * C::SR);
+                            scores(0, k, tmem + (use & 1) * 128, part);
                             commit(empty + 8 * k);
                         }
                         commit(s_full + 8 * (use & 1));
@@ -728,9 +737,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if constexpr (C::FP8) {
                         wait(empty + 8 * turn.stage, turn.use + 1);
                         const uint32_t raw = raws + in.stage * C::RAW;
+                        const int wide = (values ? D : C::KD) / 16;   // units of 16 channels in a row
 #pragma unroll 4
                         for (int i = me; i < C::RAW / 16; i += TEAM) {
-                            const int row = i / (D / 16), u = i % (D / 16), panel = u / 4, unit = 2 * (u % 4);
+                            const int row = i / wide, u = i % wide, panel = u / 4, unit = 2 * (u % 4);
                             uint4 w = ld_shared(raw + i * 16);
                             if (look) {
                                 uint32_t x[4] = {w.x, w.y, w.z, w.w};
@@ -751,7 +761,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                           make_uint4(e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w))};
                             // odd panels store their second half first, so that a row's eight lanes
                             // meet eight banks' groups
-                            const uint32_t to = stage + panel * C::PANEL + row * 128;
+                            const uint32_t to = stage + panel * (values ? C::PANEL : C::KPANEL) + row * 128;
                             const int f = panel & 1;
                             st_shared(to + (((unit + f) ^ (row & 7)) << 4), f ? h[1] : h[0]);
                             st_shared(to + (((unit + 1 - f) ^ (row & 7)) << 4), f ? h[0] : h[1]);
@@ -987,7 +997,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         bw::tmem_wait_ld32(u);
                         if constexpr (C::CAP) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = tanh_of<true>(x[i] * to_cap) * cap;
+                            for (int i = 0; i < 32; ++i) x[i] = tanh_flat(x[i] * to_cap) * cap;
                         }
                         if (edge) {
                             const int a = see0 - at - c0, b = see1 - at - c0;
@@ -1190,14 +1200,16 @@ cudaError_t kv_chunk_setup(Kv& K) {
                                 (cuuint64_t)K.s.n_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)K.s.token_stride * es, (cuuint64_t)K.s.head_stride * es,
                                    (cuuint64_t)K.s.page_stride * es};
-    const cuuint32_t box[4] = {(cuuint32_t)(K.s.e4m3 ? K.s.head_dim : 64), (cuuint32_t)K.chunk_box, 1, 1};
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    for (int i = 0; i < 2; ++i)
+    const int key_width = pick(K.s, false, [](auto c) { return decltype(c)::KD; });
+    for (int i = 0; i < 2; ++i) {
+        const cuuint32_t box[4] = {(cuuint32_t)(!K.s.e4m3 ? 64 : i ? K.s.head_dim : key_width), (cuuint32_t)K.chunk_box, 1, 1};
         if (encode(i ? &K.tm_chunk_v : &K.tm_chunk_k, K.s.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                    4, i ? K.v_pages : K.k_pages, dims, strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                    K.s.e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
+    }
     for (const bool cap : {false, true}) {
         const cudaError_t e = pick(K.s, cap, [](auto c) {
             using C = decltype(c);
@@ -1213,16 +1225,18 @@ moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t strea
     uint8_t* const at = static_cast<uint8_t*>(a.workspace);
     ChunkArgs p{a, K.s, K.v_pages, K.k_scale, K.v_scale, K.health, reinterpret_cast<Rec*>(at),
                 reinterpret_cast<float2*>(at + w.recs), reinterpret_cast<float4*>(at + w.recs + w.ml),
-                K.s.n_heads / K.s.n_kv_heads, K.chunk_box};
+                K.s.n_heads / K.s.n_kv_heads, K.chunk_box, false};
     // a window that holds every position is none
     if (p.a.window >= a.max_pages * K.s.page_size) p.a.window = 0;
+    // Up to four blocks of a sequence, a CTA does a tile in less time than the second launch takes.
+    p.whole = a.max_pages * K.s.page_size <= 4 * kBlk;
     // changes no score below 2^68, and a score's share of it would lose bits
     const bool cap = a.softcap > 0.f && a.softcap < 0x1p80f;
     const cudaError_t e = pick(K.s, cap, [&](auto c) {
         using C = decltype(c);
         const cudaError_t e = launch_pdl(k_kv_chunk<C>, dim3(K.num_sms), dim3(C::THREADS), C::smem, stream, true, p,
                                          K.tm_chunk_k, K.tm_chunk_v);
-        if (e != cudaSuccess) return e;
+        if (e != cudaSuccess || p.whole) return e;
         return launch_pdl(k_kv_chunk_join<C>, dim3(K.num_sms, C::ROWS / 32), dim3(256), 0, stream, true, p, K.num_sms);
     });
     return e == cudaSuccess ? MOE_OK : cuda_fail(e, "attend chunk launch");
