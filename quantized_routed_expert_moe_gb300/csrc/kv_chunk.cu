@@ -75,6 +75,20 @@ struct Rec {
     int flags, rows, row0, start, hk, pad[3];
 };
 
+// Division of 0 <= x < 2^31 by a number of 1..4096 that the launch knows: the quotient by its
+// rounded-up reciprocal 2^k / d, exact since d <= 2^(k - 31). (A division in the kernel is
+// twenty instructions, and the cache for those is what the roles wait for.)
+struct Div {
+    uint32_t m;
+    int k, d;
+    explicit Div(int by) : m(0), k(31), d(by) {
+        while ((1 << (k - 31)) < by) ++k;
+        m = (uint32_t)((((uint64_t)1 << k) + by - 1) / by);
+    }
+    __device__ __forceinline__ int of(int x) const { return (int)((uint64_t)(uint32_t)x * m >> k); }
+    __device__ __forceinline__ int rest(int x) const { return x - of(x) * d; }
+};
+
 struct ChunkArgs {
     moe_kv_chunk_args a;
     KvShape s;
@@ -84,7 +98,8 @@ struct ChunkArgs {
     Rec* recs;          // [CTA][2]
     float2* part_ml;    // [CTA][2][ROWS]: maximum (base two) and sum
     float4* part_o;     // [CTA][2][D / 4][ROWS]
-    int G, box_rows;
+    Div G, page;        // query heads of a key-value head, tokens of a page
+    int box_rows;
     bool whole;         // tiles are not cut: their blocks are few
 };
 
@@ -104,7 +119,8 @@ struct Part {
 template <class C>
 struct Walk {
     const int *start, *len;   // shared memory
-    int G, Hk, window, b, i, hk, off, index, busy, gi;
+    Div G;
+    int Hk, window, b, i, hk, off, index, busy, gi;
     bool whole;               // a unit is a tile, not a block
     long long left;
 
@@ -113,14 +129,14 @@ struct Walk {
 
     __device__ __forceinline__ bool next(Part& q) {
         if (left <= 0) return false;
-        const int n = start[b + 1] - start[b], R = n * G;
+        const int n = start[b + 1] - start[b], R = n * G.d;
         q.b = b;
         q.hk = hk;
         q.row0 = i * C::ROWS;
         q.rows = min(R - q.row0, C::ROWS);
         q.start = start[b];
         q.base = len[b] - n;
-        const int p0 = q.base + q.row0 / G, p1 = q.base + (q.row0 + q.rows - 1) / G;
+        const int p0 = q.base + G.of(q.row0), p1 = q.base + G.of(q.row0 + q.rows - 1);
         q.lo = first_seen(p0, window);
         q.hi = p1 + 1;
         q.all_lo = first_seen(p1, window);
@@ -285,7 +301,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(16) Shared<C> sm;
     const KvShape& s = p.s;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, B = p.a.B, G = p.G;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, B = p.a.B;
+    const Div& G = p.G;
     const uint32_t base = (bw::saddr(smem_raw) + 1023) & ~1023u;
     const uint32_t q_at = base, stages = base + C::NS * C::QTILE, raws = stages + NST * C::STAGE;
     const uint32_t full = bw::saddr(sm.full), raw_free = bw::saddr(sm.raw_free), ready = bw::saddr(sm.ready),
@@ -339,7 +356,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     pdl_trigger();
 
     // ---- tiles of every sequence, blocks of every tile, this CTA's share of them ---------------
-    Walk<C> walk;
+    Walk<C> walk{nullptr, nullptr, p.G};
     {
         int* const pre = reinterpret_cast<int*>(smem_raw + (base - bw::saddr(smem_raw)));   // tiles before a sequence
         const int most = p.a.max_pages * s.page_size;
@@ -357,7 +374,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             sm.start[b] = s0;
             if (b == B - 1) sm.start[B] = s1;
             sm.len[b] = len;
-            mine += s1 > s0 ? ((s1 - s0) * G - 1) / C::ROWS + 1 : 0;
+            mine += s1 > s0 ? ((s1 - s0) * G.d - 1) / C::ROWS + 1 : 0;
         }
         long long tiles;
         long long run = scan_cta<long long, C::WARPS>(mine, sm.sums, tiles);
@@ -365,7 +382,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (int b = b0; b < b1; ++b) {
             pre[b] = (int)run;
             const int n = sm.start[b + 1] - sm.start[b];
-            run += n > 0 ? (n * G - 1) / C::ROWS + 1 : 0;
+            run += n > 0 ? (n * G.d - 1) / C::ROWS + 1 : 0;
         }
         if (threadIdx.x == 0) pre[B] = (int)tiles;
         __syncthreads();
@@ -381,7 +398,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         };
         auto per_head = [&](int r) {
             const int b = find(r), n = sm.start[b + 1] - sm.start[b], row0 = (r - pre[b]) * C::ROWS;
-            const int p0 = sm.len[b] - n + row0 / G, p1 = sm.len[b] - n + (min(row0 + C::ROWS, n * G) - 1) / G;
+            const int p0 = sm.len[b] - n + G.of(row0), p1 = sm.len[b] - n + G.of(min(row0 + C::ROWS, n * G.d) - 1);
             return p.whole ? 1 : Walk<C>::blocks_of(Walk<C>::first_seen(p0, p.a.window), p1 + 1) + kTileCost;
         };
         walk.left = 0;
@@ -423,7 +440,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         walk.start = sm.start;
         walk.len = sm.len;
-        walk.G = G;
         walk.Hk = s.n_kv_heads;
         walk.window = p.a.window;
         walk.whole = p.whole;
@@ -468,7 +484,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int pos = (q.blk0 + j) * kBlk + lane * p.box_rows;
             Box x;
             x.need = lane < boxes * C::PARTS && pos < q.hi && pos + p.box_rows > q.lo;
-            const int i = pos / s.page_size;
+            const int i = p.page.of(pos);
             x.slot = pos - i * s.page_size;
             x.page = x.need ? p.a.block_table[(int64_t)q.b * p.a.max_pages + i] : -1;
             return x;
@@ -490,7 +506,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if (!x.none) continue;
 #pragma unroll 1
                     for (int r = lane; r < x.rows; r += 32) {
-                        const int64_t o = (int64_t)(x.start + (x.row0 + r) / G) * s.n_heads + x.hk * G + (x.row0 + r) % G;
+                        const int64_t o = (int64_t)(x.start + G.of(x.row0 + r)) * s.n_heads + x.hk * G.d + G.rest(x.row0 + r);
                         uint4* const to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D);
 #pragma unroll 1
                         for (int i = 0; i < D / 8; ++i) to[i] = make_uint4(0, 0, 0, 0);
@@ -823,13 +839,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         float c_next = 0.f;
 
         auto out_row = [&](const volatile Part& q, int r) {       // row of out and lse
-            return (int64_t)(q.start + (q.row0 + r) / G) * token_heads + q.hk * G + (q.row0 + r) % G;
+            return (int64_t)(q.start + G.of(q.row0 + r)) * token_heads + q.hk * G.d + G.rest(q.row0 + r);
         };
         // this thread's row of queries, to shared memory
         auto load_q = [&](const volatile Part& q) {
             const int r = slot * 128 + row;
             const bool on = r < q.rows;
-            const int t = q.start + (q.row0 + r) / G, head = q.hk * G + (q.row0 + r) % G;
+            const int t = q.start + G.of(q.row0 + r), head = q.hk * G.d + G.rest(q.row0 + r);
             const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)t * p.a.q_stride +
                                                               (int64_t)head * D);
             uint4 v[OC / 8];
@@ -897,7 +913,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 ok = wait(o_last + 8 * slot, ended++) && ok;
                 bw::tc_fence_after();
-                const int r = slot * 128 + row, pos = q.base + (q.row0 + r) / G;
+                const int r = slot * 128 + row, pos = q.base + G.of(q.row0 + r);
                 const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
                 const bool cut = !(q.first && q.last), on = r < q.rows;
                 const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
@@ -925,9 +941,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             if (p0 >= q.all_lo && p0 + kBlk <= q.all_hi) continue;
     #pragma unroll 1
                             for (int at = max(p0, see0); at < min(p0 + kBlk, see1); ++at) {
-                                const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + at / s.page_size];
+                                const int page = p.a.block_table[(int64_t)q.b * p.a.max_pages + p.page.of(at)];
                                 if (page < 0 || page >= s.n_pages) continue;
-                                const int64_t from = kv_offset(s, page, q.hk, at % s.page_size) + ch0 + i;
+                                const int64_t from = kv_offset(s, page, q.hk, p.page.rest(at)) + ch0 + i;
     #pragma unroll
                                 for (int k = 0; k < 32; ++k) {
                                     float v;
@@ -972,7 +988,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             at_part = parts++;
             const float c = C::CAP ? 1.f : c_next * kLog2e;
             const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
-            const int pos = v.base + (v.row0 + slot * 128 + row) / G;
+            const int pos = v.base + G.of(v.row0 + slot * 128 + row);
             const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
             const int n = v.n, blk0 = v.blk0, all_lo = v.all_lo, all_hi = v.all_hi;
             m = -INFINITY;
@@ -1151,7 +1167,7 @@ __global__ void __launch_bounds__(256) k_kv_chunk_join(const ChunkArgs p, int ct
             }
         }
         const float inv = L == 0.f ? 0.f : p.v_scale[rec.hk] / L;
-        const int64_t row = (int64_t)(rec.start + (rec.row0 + r) / p.G) * p.s.n_heads + rec.hk * p.G + (rec.row0 + r) % p.G;
+        const int64_t row = (int64_t)(rec.start + p.G.of(rec.row0 + r)) * p.s.n_heads + rec.hk * p.G.d + p.G.rest(rec.row0 + r);
         uint2* to = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.a.out) + row * D) + warp;
 #pragma unroll
         for (int k = 0; k < V; ++k)
@@ -1225,7 +1241,7 @@ moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t strea
     uint8_t* const at = static_cast<uint8_t*>(a.workspace);
     ChunkArgs p{a, K.s, K.v_pages, K.k_scale, K.v_scale, K.health, reinterpret_cast<Rec*>(at),
                 reinterpret_cast<float2*>(at + w.recs), reinterpret_cast<float4*>(at + w.recs + w.ml),
-                K.s.n_heads / K.s.n_kv_heads, K.chunk_box, false};
+                Div(K.s.n_heads / K.s.n_kv_heads), Div(K.s.page_size), K.chunk_box, false};
     // a window that holds every position is none
     if (p.a.window >= a.max_pages * K.s.page_size) p.a.window = 0;
     // Up to four blocks of a sequence, a CTA does a tile in less time than the second launch takes.
