@@ -217,6 +217,38 @@ __device__ __forceinline__ void add2(float& a, float& b, float y, float z) {
         : "+f"(a), "+f"(b)
         : "f"(y), "f"(z));
 }
+__device__ __forceinline__ void mul2(float& a, float& b, float y, float z) {
+    asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
+        : "+f"(a), "+f"(b)
+        : "f"(y), "f"(z));
+}
+// a = a * b + c of both halves
+__device__ __forceinline__ void fma22(float& a0, float& a1, float b0, float b1, float c) {
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %4};"
+        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
+        : "+f"(a0), "+f"(a1)
+        : "f"(b0), "f"(b1), "f"(c));
+}
+// cap tanh(k x) of two scores, as tanh_of has it, on both sides and without a branch: scores lie
+// on either.
+__device__ __forceinline__ void tanh_cap(float& x0, float& x1, float k, float cap) {
+    mul2(x0, x1, k, k);
+    float u0 = x0, u1 = x1, n0 = 0.0172414916f, n1 = 0.0172414916f, e0 = x0, e1 = x1;
+    mul2(u0, u1, x0, x1);
+    fma22(n0, n1, u0, u1, -0.0530454943f);
+    fma22(n0, n1, u0, u1, 0.13325879f);
+    fma22(n0, n1, u0, u1, -0.333331439f);
+    fma22(n0, n1, u0, u1, 1.f);
+    mul2(n0, n1, x0, x1);
+    mul2(e0, e1, 2.f * kLog2e, 2.f * kLog2e);
+    e0 = ex2(e0), e1 = ex2(e1);
+    add2(e0, e1, 1.f, 1.f);
+    e0 = rcp(e0), e1 = rcp(e1);
+    fma2(e0, e1, -2.f, 1.f);
+    x0 = fabsf(x0) > 0.5f ? e0 : n0;
+    x1 = fabsf(x1) > 0.5f ? e1 : n1;
+    mul2(x0, x1, cap, cap);
+}
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if constexpr (F16) {
@@ -841,42 +873,53 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         auto out_row = [&](const volatile Part& q, int r) {       // row of out and lse
             return (int64_t)(q.start + G.of(q.row0 + r)) * token_heads + q.hk * G.d + G.rest(q.row0 + r);
         };
-        // this thread's row of queries, to shared memory
+        // The queries of this warp's 32 rows, to shared memory: neighbouring lanes read neighbouring
+        // vectors, UR to a row (a lane per row meets 32 lines with every read, 4000 cycles for a
+        // tile). An 8-bit cache's are scaled by a power of two, so that a row's largest lies in
+        // [2^14, 2^15).
         auto load_q = [&](const volatile Part& q) {
+            constexpr int UR = OC / 8, RI = 32 / UR;   // vectors of a row, rows of a read
             const int r = slot * 128 + row;
-            const bool on = r < q.rows;
             const int t = q.start + G.of(q.row0 + r), head = q.hk * G.d + G.rest(q.row0 + r);
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + (int64_t)t * p.a.q_stride +
-                                                              (int64_t)head * D);
-            uint4 v[OC / 8];
-#pragma unroll
-            for (int i = 0; i < OC / 8; ++i) v[i] = on ? src[ch0 / 8 + i] : make_uint4(0, 0, 0, 0);
+            // (rows past the last read the last one's place, and become zero)
+            const int64_t at = r < q.rows ? (int64_t)t * p.a.q_stride + (int64_t)head * D : -1;
             float c = scale * p.k_scale[q.hk];
-            float up = 1.f;
-            if constexpr (C::FP8) {
-                // by a power of two, so that the row's largest lies in [2^14, 2^15)
-                uint32_t big = 0;
-                auto look = [&](uint4 w) {
-                    for (uint32_t x : {w.x, w.y, w.z, w.w}) big = max(big, max(x & 0x7fffu, x >> 16 & 0x7fffu));
-                };
+            uint4 v[UR];
 #pragma unroll
-                for (int i = 0; i < OC / 8; ++i) look(v[i]);
-                if (C::NS == 1 && on)
-#pragma unroll 1
-                    for (int i = 0; i < OC / 8; ++i) look(src[(wg ? 0 : OC / 8) + i]);
-                // exponent field e: the largest is below 2^(e - 126); a factor within fp32's range
-                const int e = big >> 7, by = big == 0 || e == 255 ? 0 : max(-126, min(126, 141 - e));
-                up = exp2i(by);
-                c *= exp2i(-by);
+            for (int i = 0; i < UR; ++i) {
+                const int64_t from = __shfl_sync(~0u, at, RI * i + lane / UR);
+                v[i] = from < 0 ? make_uint4(0, 0, 0, 0)
+                                : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + from + ch0 + lane % UR * 8);
             }
 #pragma unroll
-            for (int i = 0; i < OC / 8; ++i) {
+            for (int i = 0; i < UR; ++i) {
                 uint32_t x[4] = {v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
-                if constexpr (C::FP8)
+                const int rr = warp % 4 * 32 + RI * i + lane / UR, unit = ch0 / 8 + lane % UR;
+                if constexpr (C::FP8) {
+                    uint32_t big = 0;
+                    auto look = [&](uint32_t w) { big = max(big, max(w & 0x7fffu, w >> 16 & 0x7fffu)); };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) look(x[k]);
+                    if constexpr (C::NS == 1) {   // and the other half of the channels
+                        const int64_t from = __shfl_sync(~0u, at, RI * i + lane / UR);
+                        if (from >= 0) {
+                            const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + from + (ch0 ^ OC) +
+                                                                            lane % UR * 8);
+                            look(o.x), look(o.y), look(o.z), look(o.w);
+                        }
+                    }
+#pragma unroll
+                    for (int o = 1; o < UR; o <<= 1) big = max(big, __shfl_xor_sync(~0u, big, o));
+                    // exponent field e: the largest is below 2^(e - 126); a factor within fp32's range
+                    const int e = big >> 7, by = big == 0 || e == 255 ? 0 : max(-126, min(126, 141 - e));
+                    const float up = exp2i(by);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) x[k] = pack2<true>(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
-                const int unit = ch0 / 8 + i;
-                st_shared(q_at + slot * C::QTILE + unit / 8 * C::QPANEL + row * 128 + ((unit % 8 ^ (row & 7)) << 4),
+                    // to the lane whose row it is
+                    const int got = __shfl_sync(~0u, by, lane % RI * UR);
+                    if (lane / RI == i) c *= exp2i(-got);
+                }
+                st_shared(q_at + slot * C::QTILE + unit / 8 * C::QPANEL + rr * 128 + ((unit % 8 ^ (rr & 7)) << 4),
                           make_uint4(x[0], x[1], x[2], x[3]));
             }
             bw::fence_async_smem();
@@ -1013,7 +1056,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         bw::tmem_wait_ld32(u);
                         if constexpr (C::CAP) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) x[i] = tanh_flat(x[i] * to_cap) * cap;
+                            for (int i = 0; i < 16; ++i) tanh_cap(x[2 * i], x[2 * i + 1], to_cap, cap);
                         }
                         if (edge) {
                             const int a = see0 - at - c0, b = see1 - at - c0;

@@ -31,21 +31,12 @@ __device__ __forceinline__ uint32_t e4m3_hi(uint32_t v) {
 // tanh z, off by 8 units of 2^-24 relative to itself: up to 1/2 by an odd polynomial, fitted
 // to the least relative error there (1.5e-8), and where PAST, past it, by 1 - 2 / (exp(2 z) +
 // 1), whose error of 2^-22 would be the larger the nearer to zero.
-__device__ __forceinline__ float tanh_near(float z) {
-    const float u = z * z;
-    return z * fmaf(fmaf(fmaf(fmaf(0.0172414916f, u, -0.0530454943f), u, 0.13325879f), u, -0.333331439f), u, 1.f);
-}
-__device__ __forceinline__ float tanh_past(float z) { return 1.f - 2.f * rcp(ex2(z * (2.f * kLog2e)) + 1.f); }
 template <bool PAST>
 __device__ __forceinline__ float tanh_of(float z) {
-    const float r = tanh_near(z);
+    const float u = z * z;
+    const float r = z * fmaf(fmaf(fmaf(fmaf(0.0172414916f, u, -0.0530454943f), u, 0.13325879f), u, -0.333331439f), u, 1.f);
     if (!PAST || !(fabsf(z) > 0.5f)) return r;
-    return tanh_past(z);
-}
-// Without a branch, for scores that lie on both sides.
-__device__ __forceinline__ float tanh_flat(float z) {
-    const float near = tanh_near(z), past = tanh_past(z);
-    return fabsf(z) > 0.5f ? past : near;
+    return 1.f - 2.f * rcp(ex2(z * (2.f * kLog2e)) + 1.f);
 }
 
 }  // namespace moe
