@@ -78,11 +78,14 @@ __device__ __forceinline__ void activate(float (&z)[N], int act) {
     }
 }
 
-constexpr int kRows = 128, kChunk = 64;             // channels of a tile; K of a stage, 128 bytes
+constexpr int kRows = 128, kChunk = 64;             // channels of a tile; K of a panel, 128 bytes
 constexpr int kRing = 196608;                       // bytes of stages, and of a split tile's sums
 constexpr int kMaxSplits = 8;                       // a portable cluster
 constexpr int kThreads = 192;                       // four epilogue warps, the copies', the products'
-constexpr uint32_t stage_bytes(int BN) { return (kRows + BN) * kChunk * 2; }
+// Panels of a stage. The products wait once per stage, and a wait behind issued products takes
+// 130 cycles more than theirs (89 each up to 128 tokens): two panels where the ring holds them.
+constexpr int panels_of(int BN) { return BN <= 128 ? 2 : 1; }
+constexpr uint32_t stage_bytes(int BN) { return (kRows + BN) * kChunk * 2 * panels_of(BN); }
 constexpr int stages_of(int BN) { return kRing / stage_bytes(BN) < 12 ? kRing / stage_bytes(BN) : 12; }
 
 struct LinearArgs {
@@ -94,6 +97,9 @@ struct LinearArgs {
     int row_tiles, tiles, splits;   // tiles: all of them, channels fastest; splits: CTAs of a cluster
 };
 
+__device__ __forceinline__ void prefetch_2d(const CUtensorMap* tm, int x, int y) {
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(tm), "r"(x), "r"(y) : "memory");
+}
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -142,8 +148,8 @@ __device__ __forceinline__ void finish16(const LinearArgs& p, int t, int count, 
 template <int BN>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const LinearArgs p, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
-    constexpr int S = stages_of(BN);
-    constexpr uint32_t SB = stage_bytes(BN), COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    constexpr int S = stages_of(BN), PN = panels_of(BN);
+    constexpr uint32_t W_PANEL = kRows * kChunk * 2, X_PANEL = BN * kChunk * 2, SB = stage_bytes(BN), COLS = 2 * BN < 32 ? 32 : 2 * BN;
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_done[2], s_free[2];
     __shared__ uint32_t s_tmem;
@@ -152,7 +158,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ring = (bw::saddr(smem_raw) + 1023) & ~1023u;
     const uint32_t full = bw::saddr(s_full), empty = bw::saddr(s_empty), done = bw::saddr(s_done), free_ = bw::saddr(s_free);
     // this CTA's share of every tile's K, in chunks
-    const int split = p.splits > 1 ? (int)cluster_rank() : 0, chunks = (p.K + kChunk - 1) / kChunk;
+    const int split = p.splits > 1 ? (int)cluster_rank() : 0, chunks = (p.K + PN * kChunk - 1) / (PN * kChunk);
     const int k0 = (int)((int64_t)chunks * split / p.splits), k1 = (int)((int64_t)chunks * (split + 1) / p.splits);
     const int first = blockIdx.x / p.splits, step = gridDim.x / p.splits;
 
@@ -175,6 +181,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     bw::tc_fence_after();
     const uint32_t tmem = *const_cast<volatile uint32_t*>(&s_tmem);
+    // the first tile's weights come into the second-level cache while the preceding kernel ends (a
+    // hint: what it may still write there is what the copies find)
+    if (warp == 4 && lane == 0 && first < p.tiles)
+        for (int k = k0; k < min(k1, k0 + S); ++k)
+            for (int q = 0; q < PN; ++q) prefetch_2d(&tm_w, (k * PN + q) * kChunk, first % p.row_tiles * kRows);
     pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
     pdl_trigger();
     // a wait that runs out (2 s) sets s_abort, which ends the others: the CTA's outputs are NaN
@@ -194,8 +205,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t s = it % S, at = ring + s * SB;
                     if (!(ok = wait(empty + 8 * s, ((it / S) & 1) ^ 1))) break;
                     bw::mbar_arrive_tx(full + 8 * s, SB);
-                    bw::tma_load_2d(at, &tm_w, k * kChunk, n0, full + 8 * s, pol_w);
-                    bw::tma_load_2d(at + kRows * kChunk * 2, &tm_x, k * kChunk, t0, full + 8 * s, keep);
+#pragma unroll
+                    for (int q = 0; q < PN; ++q) {
+                        bw::tma_load_2d(at + q * W_PANEL, &tm_w, (k * PN + q) * kChunk, n0, full + 8 * s, pol_w);
+                        bw::tma_load_2d(at + PN * W_PANEL + q * X_PANEL, &tm_x, (k * PN + q) * kChunk, t0, full + 8 * s, keep);
+                    }
                 }
             }
             // no copy is in flight at the end, after a wait that ran out either
@@ -216,8 +230,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 bw::tc_fence_after();
                 if (bw::elect_one()) {
 #pragma unroll
-                    for (int j = 0; j < kChunk / 16; ++j)
-                        bw::mma_f16(d, bw::desc_sw128(at + 32 * j), bw::desc_sw128(at + kRows * kChunk * 2 + 32 * j),
+                    for (int j = 0; j < PN * kChunk / 16; ++j)
+                        bw::mma_f16(d, bw::desc_sw128(at + j / 4 * W_PANEL + 32 * (j % 4)),
+                                    bw::desc_sw128(at + PN * W_PANEL + j / 4 * X_PANEL + 32 * (j % 4)),
                                     bw::idesc_f16_f32(kRows, BN, true), k > k0 || j > 0);
                     bw::mma_commit(empty + 8 * s);
                     if (k == k1 - 1) bw::mma_commit(done + 8 * (acc & 1));
@@ -382,7 +397,7 @@ cudaError_t launch(const moe_linear_desc& d, const void* x, const void* w, const
     // As many CTAs to a tile as leave all clusters resident at once: the SMs lie in groups, and
     // 48 tiles of 3 CTAs, of which 46 fit, take 25.3 us (one token, 6144 x 6144) where 2 take
     // 16.9; 6 tiles of 8 chunks (512 x 768) 3.2 us by 8 CTAs each, 3.9 by 2.
-    const int chunks = (p.K + kChunk - 1) / kChunk;
+    const int stage_k = kChunk * panels_of(s->BN), chunks = (p.K + stage_k - 1) / stage_k;
     for (int n = std::min({sms / p.tiles, kMaxSplits, chunks}); n > 1; --n)
         if (g_clusters[n].get(device, [&] { return resident_clusters(n); }) >= p.tiles) {
             p.splits = n;
