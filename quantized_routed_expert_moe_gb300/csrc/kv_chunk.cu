@@ -785,34 +785,42 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     if constexpr (C::FP8) {
                         wait(empty + 8 * turn.stage, turn.use + 1);
                         const uint32_t raw = raws + in.stage * C::RAW;
-                        const int wide = (values ? D : C::KD) / 16;   // units of 16 channels in a row
-#pragma unroll 4
-                        for (int i = me; i < C::RAW / 16; i += TEAM) {
-                            const int row = i / wide, u = i % wide, panel = u / 4, unit = 2 * (u % 4);
-                            uint4 w = ld_shared(raw + i * 16);
-                            if (look) {
-                                uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                                const bool on = live(row);
+                        const int wide = C::PARTS == 1 || !values ? C::KD / 16 : D / 16;   // units of 16 channels in a row
+                        // four vectors' reads are on their way before the first is converted
+                        constexpr int EACH = C::RAW / 16 / TEAM < 4 ? C::RAW / 16 / TEAM : 4;
+#pragma unroll 1
+                        for (int i0 = me; i0 < C::RAW / 16; i0 += EACH * TEAM) {
+                            uint4 w[EACH];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
-                                    const uint32_t nan = (((x[k] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                                    if (!on) x[k] = 0;
-                                    else if (part_seen && nan) {
-                                        x[k] &= ~(nan * 0xffu);
-                                        *odd = 1;
-                                    }
+                            for (int k = 0; k < EACH; ++k) w[k] = ld_shared(raw + (i0 + k * TEAM) * 16);
+                            if (__builtin_expect(look, 0)) {
+#pragma unroll
+                                for (int k = 0; k < EACH; ++k) {
+                                    const bool on = live((i0 + k * TEAM) / wide);
+                                    auto fix = [&](uint32_t& x) {
+                                        // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
+                                        const uint32_t nan = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                                        if (!on) x = 0;
+                                        else if (part_seen && nan) {
+                                            x &= ~(nan * 0xffu);
+                                            *odd = 1;
+                                        }
+                                    };
+                                    fix(w[k].x), fix(w[k].y), fix(w[k].z), fix(w[k].w);
                                 }
-                                w = make_uint4(x[0], x[1], x[2], x[3]);
                             }
-                            uint4 h[2] = {make_uint4(e4m3_lo(w.x), e4m3_hi(w.x), e4m3_lo(w.y), e4m3_hi(w.y)),
-                                          make_uint4(e4m3_lo(w.z), e4m3_hi(w.z), e4m3_lo(w.w), e4m3_hi(w.w))};
-                            // odd panels store their second half first, so that a row's eight lanes
-                            // meet eight banks' groups
-                            const uint32_t to = stage + panel * (values ? C::PANEL : C::KPANEL) + row * 128;
-                            const int f = panel & 1;
-                            st_shared(to + (((unit + f) ^ (row & 7)) << 4), f ? h[1] : h[0]);
-                            st_shared(to + (((unit + 1 - f) ^ (row & 7)) << 4), f ? h[0] : h[1]);
+#pragma unroll
+                            for (int k = 0; k < EACH; ++k) {
+                                const int i = i0 + k * TEAM, row = i / wide, u = i % wide, panel = u / 4, unit = 2 * (u % 4);
+                                const uint4 h0 = make_uint4(e4m3_lo(w[k].x), e4m3_hi(w[k].x), e4m3_lo(w[k].y), e4m3_hi(w[k].y)),
+                                            h1 = make_uint4(e4m3_lo(w[k].z), e4m3_hi(w[k].z), e4m3_lo(w[k].w), e4m3_hi(w[k].w));
+                                // odd panels store their second half first, so that a row's eight lanes
+                                // meet eight banks' groups
+                                const uint32_t to = stage + panel * (values ? C::PANEL : C::KPANEL) + row * 128;
+                                const int f = panel & 1;
+                                st_shared(to + (((unit + f) ^ (row & 7)) << 4), f ? h1 : h0);
+                                st_shared(to + (((unit + 1 - f) ^ (row & 7)) << 4), f ? h0 : h1);
+                            }
                         }
                         bw::fence_async_smem();
                         __syncwarp();
