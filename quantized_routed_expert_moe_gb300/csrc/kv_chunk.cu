@@ -189,14 +189,10 @@ __device__ __forceinline__ T scan_cta(T v, T* sums, T& total) {
     __syncthreads();
     if (lane == 31) sums[warp] = incl;
     __syncthreads();
-    T before = incl - v;
-    total = 0;
-#pragma unroll 1
-    for (int w = 0; w < WARPS; ++w) {
-        if (w < warp) before += sums[w];
-        total += sums[w];
-    }
-    return before;
+    const T w = scan_up(lane < WARPS ? sums[lane] : T(0));
+    total = __shfl_sync(~0u, w, WARPS - 1);
+    const T before = __shfl_sync(~0u, w, max(warp - 1, 0));
+    return incl - v + (warp ? before : T(0));
 }
 
 // The registers of a thread from here on, for the warps of a group of four together.
@@ -436,10 +432,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         walk.left = 0;
         if (!sm.bad_start) {
             const int rt = (int)tiles;
-            long long total = 0, sum = 0;
+            long long total = 0, sum = 0, chunk = 0, at = 0;
 #pragma unroll 1
             for (int r = threadIdx.x; r < rt; r += C::THREADS) sum += (long long)per_head(r) * s.n_kv_heads;
-            scan_cta<long long, C::WARPS>(sum, sm.sums, total);
+            at = scan_cta<long long, C::WARPS>(sum, sm.sums, total);   // (of use where a thread has one tile)
             const long long ctas = min((long long)gridDim.x, total), c = blockIdx.x;
             // an even share, the first `more` CTAs one unit more (one 64-bit division)
             const long long each = ctas ? total / ctas : 0, more = total - each * ctas;
@@ -449,14 +445,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
             for (int r0 = 0; walk.left > 0 && r0 < rt && before <= from; r0 += C::THREADS) {
                 const int r = r0 + threadIdx.x;
-                const long long u = r < rt ? (long long)per_head(r) * s.n_kv_heads : 0;
-                long long chunk;
-                const long long at = before + scan_cta<long long, C::WARPS>(u, sm.sums, chunk);
+                long long u = sum;
+                if (rt > C::THREADS) {
+                    u = r < rt ? (long long)per_head(r) * s.n_kv_heads : 0;
+                    at = before + scan_cta<long long, C::WARPS>(u, sm.sums, chunk);
+                    before += chunk;
+                }
                 if (at <= from && from < at + u) {
                     sm.first = r;
                     sm.rem = from - at;
                 }
-                before += chunk;
             }
             __syncthreads();
             if (walk.left > 0) {
@@ -892,24 +890,28 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // (rows past the last read the last one's place, and become zero)
             const int64_t at = r < q.rows ? (int64_t)t * p.a.q_stride + (int64_t)head * D : -1;
             float c = scale * p.k_scale[q.hk];
-            uint4 v[UR];
+            // (four reads at a time where they are scaled: the instructions of sixteen do not stay cached)
+            constexpr int BATCH = C::FP8 ? 4 : UR;
+#pragma unroll 1
+            for (int i0 = 0; i0 < UR; i0 += BATCH) {
+            uint4 v[BATCH];
 #pragma unroll
-            for (int i = 0; i < UR; ++i) {
-                const int64_t from = __shfl_sync(~0u, at, RI * i + lane / UR);
+            for (int i = 0; i < BATCH; ++i) {
+                const int64_t from = __shfl_sync(~0u, at, RI * (i0 + i) + lane / UR);
                 v[i] = from < 0 ? make_uint4(0, 0, 0, 0)
                                 : *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + from + ch0 + lane % UR * 8);
             }
 #pragma unroll
-            for (int i = 0; i < UR; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 uint32_t x[4] = {v[i].x ^ flip, v[i].y ^ flip, v[i].z ^ flip, v[i].w ^ flip};
-                const int rr = warp % 4 * 32 + RI * i + lane / UR, unit = ch0 / 8 + lane % UR;
+                const int rr = warp % 4 * 32 + RI * (i0 + i) + lane / UR, unit = ch0 / 8 + lane % UR;
                 if constexpr (C::FP8) {
                     uint32_t big = 0;
                     auto look = [&](uint32_t w) { big = max(big, max(w & 0x7fffu, w >> 16 & 0x7fffu)); };
 #pragma unroll
                     for (int k = 0; k < 4; ++k) look(x[k]);
                     if constexpr (C::NS == 1) {   // and the other half of the channels
-                        const int64_t from = __shfl_sync(~0u, at, RI * i + lane / UR);
+                        const int64_t from = __shfl_sync(~0u, at, RI * (i0 + i) + lane / UR);
                         if (from >= 0) {
                             const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.a.q) + from + (ch0 ^ OC) +
                                                                             lane % UR * 8);
@@ -925,10 +927,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     for (int k = 0; k < 4; ++k) x[k] = pack2<true>(bf16_lo(x[k]) * up, bf16_hi(x[k]) * up);
                     // to the lane whose row it is
                     const int got = __shfl_sync(~0u, by, lane % RI * UR);
-                    if (lane / RI == i) c *= exp2i(-got);
+                    if (lane / RI == i0 + i) c *= exp2i(-got);
                 }
                 st_shared(q_at + slot * C::QTILE + unit / 8 * C::QPANEL + rr * 128 + ((unit % 8 ^ (rr & 7)) << 4),
                           make_uint4(x[0], x[1], x[2], x[3]));
+            }
             }
             bw::fence_async_smem();
             __syncwarp();
