@@ -37,7 +37,9 @@ namespace {
 constexpr int kBlk = 128;              // cached tokens of a block
 constexpr int kRing = 16;              // blocks whose page flags are kept
 constexpr int kParts = 4;              // parts that the roles may be apart
-constexpr int kTileCost = 2;           // what a tile's beginning and end cost, in blocks
+// What a tile's beginning and end cost, in blocks: a prompt of 8192 takes 1138, 930, 778, 730 and
+// 748 us with 1, 2, 3, 4 and 6, a batch in 8 bits 279, 259, 239, 228 and 229.
+constexpr int kTileCost = 4;
 
 // Compile-time shape of one kernel: head dimension, cache type, capped scores.
 template <int D_, bool FP8_, bool CAP_>
