@@ -739,8 +739,8 @@ moe_status moe_kv_append_norm(moe_kv* kv, const moe_kv_append_args* args, const 
 
 /* Attention of a chunk of new tokens per sequence over the cache (formulas above):
  * products on the tensor cores, scores, softmax statistics and sums in fp32; a weight
- * enters the product with the values rounded to bf16 (bf16 cache: 2^-9, at its own
- * size), or to 11 bits (e4m3 cache: fp16, 2^-12, and at least 2^-39 of the largest).
+ * enters the product with the values rounded once, to bf16 (bf16 cache: off by 2^-8 of
+ * itself at most), or to fp16 (e4m3 cache: 2^-11, or 2^-32 of the largest).
  * Lengths and starts are read on the device (no host synchronisation, capturable in a
  * graph). The work is split over the GPU by cached blocks and joined in a fixed order,
  * so results are bit-reproducible. A length past the block table is cut to it and an
@@ -774,15 +774,16 @@ enum {
     MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
     MOE_KV_TIMEOUT = 8,     /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
                                out and lse whose cache did not arrive are NaN. Inside
-                               moe_kv_attend_chunk (2 s): rows of the call may hold anything */
+                               moe_kv_attend_chunk (0.4 s): rows of the call may hold anything */
     MOE_KV_BAD_START = 16   /* chunk: starts decrease or leave 0..T; nothing was computed */
 };
 moe_status moe_kv_health(moe_kv* kv, uint32_t* bits);
 
 /* Options of a handle. */
 enum {
-    /* Test hook: moe_kv_attend starts no copies of this sequence's cache (-1,
-     * the default: none is left out), so that the waits for them run out. */
+    /* Test hook: moe_kv_attend and moe_kv_attend_chunk start no copies of this
+     * sequence's cache (-1, the default: none is left out), so that the waits for
+     * them run out. */
     MOE_KV_OPT_TEST_STALL = 1
 };
 moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value);

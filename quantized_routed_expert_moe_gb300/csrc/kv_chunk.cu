@@ -15,10 +15,30 @@
 // 2^8 and neither sum nor outputs need a factor. Heads of 256 channels leave room for one
 // tile: its two softmax groups take half the columns each, and S has two buffers.
 //
+// Weights of a bf16 cache enter the second product rounded to bf16 (2^-8 of each at most; the
+// sum is taken before): with 64 bits' worth of the rest the outputs are off by 1.6e-3 of their
+// norm, all but the output's own rounding. Those of an 8-bit cache are fp16, in which its keys
+// and values are exact.
+//
+// Roles. Eight softmax warps; an issuing warp per tile (a wait behind issued products ends only
+// when those have left the queue); a warp that walks the CTA's parts for all roles and copies
+// keys, one that copies values; four that turn 8-bit stages into 16-bit ones and look through
+// values that only some rows see. What bounds a block of two tiles of heads of 128 is its 32
+// products at 103 cycles each (64 would be the peak: a product of 128 x 128 x 16 takes 93 at
+// least on one CTA) and two hand-overs of 260: 3820 cycles. All loops are kept as loops: the
+// first form's 135 KB of instructions were read again and again (13000 misses of the cache for
+// them per SM in 41 blocks, 2069 us for a prompt that takes 720).
+//
 // Split. All blocks of all tiles of the call, numbered tile by tile, are dealt out evenly and
 // contiguously to one CTA per SM from the lengths as they stand on the device. A tile that is
 // cut between CTAs leaves unnormalised parts in the workspace, which a second, small launch
 // joins in order.
+//
+// Measured (GB300; floors at 1932 TFLOP/s and 6.78 TB/s): a prompt of 8192 tokens, 48 heads
+// over 8 of 128, 730 us (1130 TFLOP/s, 59%); 8 x 800 tokens after 7200, 64 heads over 4, 1203
+// TFLOP/s (62%), in 8 bits 1013; 128 tokens after 32640 105 us (51%); 64 x 4 tokens after up to
+// 16380, pages of 16, 300 us (5.2 TB/s, 77%); 17 tokens 9.7 us, of which 3.5 us before the first
+// copy (lengths, the walk, the block table) and most of the rest instructions that run once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -101,7 +121,7 @@ struct ChunkArgs {
     float2* part_ml;    // [CTA][2][ROWS]: maximum (base two) and sum
     float4* part_o;     // [CTA][2][D / 4][ROWS]
     Div G, page;        // query heads of a key-value head, tokens of a page
-    int box_rows;
+    int box_rows, stall;   // MOE_KV_OPT_TEST_STALL
     bool whole;         // tiles are not cut: their blocks are few
 };
 
@@ -312,7 +332,7 @@ struct Shared {
     uint64_t full[C::FP8 ? C::NRAW : C::NST], raw_free[4], ready[C::NST], empty[C::NST];
     uint64_t q_full[2], s_full[2], p_full[2], o_done[2], o_last[2], o_free[2], drain;
     uint64_t part_full[kParts], part_free[kParts], pair[4], order[2];
-    Part part[kParts];                // as the keys' copies go ahead; one of -1 blocks is the last
+    Part part[kParts + 1];            // as the keys' copies go ahead; one of -1 blocks is the last, as is the one past them
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
     uint32_t tmem;
@@ -372,6 +392,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::mbar_init(part_free + 8 * i, 8 + C::NS + C::READY + (C::FP8 ? 0 : 1));
             bw::mbar_init(pair + 8 * i, 2);
         }
+        sm.part[kParts].n = -1;
         sm.abort = sm.bad_start = sm.lost = 0;
         bw::mbar_fence_init();
         bw::tma_prefetch_desc(&tm_k);
@@ -483,12 +504,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         return all_lanes(bw::mbar_wait_short(bar, parity & 1, &sm.abort));
     };
 
-    // the parts in their order: n is the reader's own count, and what it took it gives back
+    // A wait that runs out sets sm.abort, which ends all others: a role then leaves, arrives nowhere
+    // any more (a barrier may have no arrivals left in its phase) and writes nothing shared.
+    // The parts in their order: n is the reader's own count, and what it took it gives back.
     auto take = [&](uint32_t n) -> const volatile Part& {
-        const bool there = wait(part_full + 8 * (n % kParts), n / kParts);
-        if (!there && lane == 0) sm.part[n % kParts].n = -1;   // (aborted)
-        __syncwarp();
-        return sm.part[n % kParts];
+        return sm.part[wait(part_full + 8 * (n % kParts), n / kParts) ? n % kParts : kParts];
     };
     auto give = [&](uint32_t n) {
         __syncwarp();
@@ -546,7 +566,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                 }
                 ok = wait(part_free + 8 * (parts % kParts), parts / kParts + 1) && ok;
-                if (!ok) x.n = -1;
+                if (!ok) return false;
                 if (lane == 0) {
                     sm.part[parts % kParts] = x;
                     bw::mbar_arrive(part_full + 8 * (parts % kParts));
@@ -555,6 +575,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             } else {
                 const volatile Part& x = take(parts);
                 q = Piece{x.b, x.hk, x.lo, x.hi, x.blk0, x.n, x.gi};
+                if (q.n < 0) return false;
                 give(parts);
             }
             ++parts;
@@ -570,7 +591,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         while (have) {
             const bool more = advance(nq);
             each_block<C>(q.n, [&](bool values, int j) {
-                if (!(values ? vals : keys)) return;
+                if (!(values ? vals : keys) || !ok) return;
                 Box x = ahead;
                 if (values && keys) {
                     x = j & 1 ? seen[1] : seen[0];
@@ -596,8 +617,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     turn.take(values);
                     const uint32_t bar = full + 8 * turn.stage, to = at + turn.stage * BYTES;
                     ok = wait(gone + 8 * turn.stage, turn.use + 1) && ok;
-                    if (!ok) continue;   // nothing is issued any more
-                    filled |= 1u << turn.stage;
+                    if (!ok) return;
+                    const bool stalled = q.b == p.stall;
+                    if (!stalled) filled |= 1u << turn.stage;
                     phases = (phases & ~(1u << turn.stage)) | (turn.use & 1) << turn.stage;
                     // boxes of this stage, and their panels
                     const int b0 = values ? part * boxes : 0, b1 = values ? b0 + boxes : C::PARTS * boxes;
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll 1
                     for (int box = b0; box < b1; ++box) {
                         const int from = __shfl_sync(~0u, page, box), slot = __shfl_sync(~0u, x.slot, box);
-                        if (from >= 0 && bw::elect_one())
+                        if (from >= 0 && !stalled && bw::elect_one())
 #pragma unroll
                             for (int c = 0; c < (C::FP8 ? 1 : D / 64); ++c)
                                 if (C::FP8 || c * 64 < width)
@@ -619,7 +641,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
             });
             q = nq;
-            have = more;
+            have = more && ok;
         }
         // no copy is in flight at the end, after a wait that ran out either
         int none = 0;
@@ -669,8 +691,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (uint32_t part = 0;; ++part) {
             const volatile Part& x = take(part);
             q = {x.n, x.rows};
+            if (q.n < 0 || !ok) break;
             give(part);
-            if (q.n < 0) break;
             // Block j's weights by its values, then block j + 1's queries by keys, so that one
             // tile's products run while the other's scores become weights. Each tile has an issuing
             // warp: a wait behind issued products ends only when those have left the queue, and
@@ -680,13 +702,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (slot && !two) {   // not there: pass the stages on, one by one, so as not to lose count
                     each_block<C>(q.n, [&](bool values, int) {
                         const uint32_t st = stage_in(values);
-                        if (bw::elect_one()) bw::mbar_arrive(empty + 8 * st);
+                        if (ok && bw::elect_one()) bw::mbar_arrive(empty + 8 * st);
                         __syncwarp();
                     });
                     continue;
                 }
 #pragma unroll 1
-                for (int j = -1; j < q.n; ++j) {   // (-1: scores alone)
+                for (int j = -1; j < q.n && ok; ++j) {   // (-1: scores alone)
                     if (j < 0) {
                         ok = wait(q_full + 8 * slot, parts) && ok;
                     } else {
@@ -710,14 +732,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         commit(empty + 8 * k);
                     }
                     if (two && j >= 0) {
-                        if (bw::elect_one()) bw::mbar_arrive(order + 8 * (slot ^ 1));
+                        if (ok && bw::elect_one()) bw::mbar_arrive(order + 8 * (slot ^ 1));
                         __syncwarp();
                     }
                 }
             } else {
                 // the next block's scores go before this one's outputs: they have a buffer of their own
 #pragma unroll 1
-                for (int j = -1; j < q.n; ++j) {
+                for (int j = -1; j < q.n && ok; ++j) {
                     const uint32_t use = uses + (j < 0 ? 0 : 1);   // of the scores
                     if (j < 0) ok = wait(q_full, parts) && ok;
                     if (j + 1 < q.n) {
@@ -755,6 +777,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         // weight of zero would not hide it): its sign to the rows that see it is settled at their end
         constexpr int RING = C::FP8 ? C::NRAW : NST, FIRST = 12, TEAM = 32 * C::READY;
         const int me = threadIdx.x - 32 * FIRST;
+        bool ok = true;
         Turn<!C::FP8, RING> in;
         Turn<!C::FP8, NST> turn;
         struct {
@@ -765,11 +788,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const volatile Part& x = take(at);
             q = {x.n, x.blk0, x.lo, x.hi, x.all_lo, x.all_hi, x.gi};
             volatile uint8_t* const odd = &sm.odd[x.busy % 8][warp - FIRST];
+            if (q.n < 0 || !ok) break;
             give(at);
-            if (q.n < 0) break;
             if (lane == 0) *odd = 0;
             __syncwarp();
             each_block<C>(q.n, [&](bool values, int j) {
+                if (!ok) return;
                 const int pos = (q.blk0 + j) * kBlk;
                 const bool part_seen = pos < q.all_lo || pos + kBlk > q.all_hi;
 #pragma unroll 1
@@ -777,13 +801,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int p0 = pos + part * C::SR;
                     in.take(values);
                     turn.take(values);
-                    wait(full + 8 * in.stage, in.use);
+                    ok = wait(full + 8 * in.stage, in.use) && ok;
+                    if (!ok) return;
                     const uint32_t pages = *const_cast<volatile uint8_t*>(&sm.pages[(q.gi + j) % kRing][part]);
                     const bool look = values && (part_seen || pages != (1u << G16) - 1);
                     auto live = [&](int row) { return p0 + row >= q.lo && p0 + row < q.hi && (pages >> (row / 16) & 1); };
                     const uint32_t stage = stages + turn.stage * C::STAGE;
                     if constexpr (C::FP8) {
-                        wait(empty + 8 * turn.stage, turn.use + 1);
+                        ok = wait(empty + 8 * turn.stage, turn.use + 1) && ok;
+                        if (!ok) return;
                         const uint32_t raw = raws + in.stage * C::RAW;
                         const int wide = C::PARTS == 1 || !values ? C::KD / 16 : D / 16;   // units of 16 channels in a row
                         // four vectors' reads are on their way before the first is converted
@@ -955,8 +981,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         for (;;) {
             // the next part's queries go ahead of this one's end; a second tile is not there for
             // every part (and the end does not wait until it is: the part has to be given back)
+            if (!ok) break;
             const volatile Part& v = take(parts);
             const int blocks = v.n;
+            if (*const_cast<volatile int*>(&sm.abort)) break;
             const bool mine = blocks > 0 && (C::NS == 1 || slot == 0 || v.rows > 128);
             if (mine) load_q(v);
             if (have) {
@@ -968,6 +996,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     sum = sm.row_sum[0][row] + sm.row_sum[1][row];
                 }
                 ok = wait(o_last + 8 * slot, ended++) && ok;
+                if (!ok) break;
                 bw::tc_fence_after();
                 const int r = slot * 128 + row, pos = q.base + G.of(q.row0 + r);
                 const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
@@ -1055,6 +1084,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int at = (blk0 + j) * kBlk + (C::NS == 2 ? 0 : wg * C::COLS);
                 const uint32_t s_at = lanes + buf * 128 + (C::NS == 2 ? 0 : wg * C::COLS);
                 ok = wait(s_full + 8 * buf, phase) && ok;
+                if (!ok) break;
                 bw::tc_fence_after();
                 const bool edge = at < all_lo || at + C::COLS > all_hi || *const_cast<volatile int*>(&sm.lost);
                 if (C::CAP || __builtin_expect(edge, 0)) {
@@ -1160,6 +1190,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 bw::tmem_wait_st();
                 bw::tc_fence_before();
                 __syncwarp();
+                if (!ok) break;
                 if (lane == 0) bw::mbar_arrive(p_full + 8 * buf);
             }
         }
@@ -1297,7 +1328,7 @@ moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t strea
     uint8_t* const at = static_cast<uint8_t*>(a.workspace);
     ChunkArgs p{a, K.s, K.v_pages, K.k_scale, K.v_scale, K.health, reinterpret_cast<Rec*>(at),
                 reinterpret_cast<float2*>(at + w.recs), reinterpret_cast<float4*>(at + w.recs + w.ml),
-                Div(K.s.n_heads / K.s.n_kv_heads), Div(K.s.page_size), K.chunk_box, false};
+                Div(K.s.n_heads / K.s.n_kv_heads), Div(K.s.page_size), K.chunk_box, K.stall, false};
     // a window that holds every position is none
     if (p.a.window >= a.max_pages * K.s.page_size) p.a.window = 0;
     // Up to four blocks of a sequence, a CTA does a tile in less time than the second launch takes.

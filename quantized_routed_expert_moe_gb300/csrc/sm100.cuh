@@ -72,12 +72,12 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
 
 // The same in a few instructions: a try that does not succeed suspends the warp, for 1.3 us as
 // measured (unless the phase completes: 106 cycles from the arrival), so that warps that wait
-// leave the issue slots and the instruction cache to those that work; 2^20 of them make the
-// limit, 1.4 s.
+// leave the issue slots and the instruction cache to those that work; 2^18 of them make the
+// limit, 0.35 s.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort) {
 #pragma unroll 1
     for (uint32_t n = 0; !mbar_try(bar, parity); ++n) {
-        if (n >> 20) *abort = 1;
+        if (n >> 18) *abort = 1;
         if (*abort) return false;
     }
     return true;
