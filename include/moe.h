@@ -574,7 +574,8 @@ typedef struct {
  *   x: bf16 [T][K]; w: bf16 [N][K]; bias: fp32 [N] or NULL; residual: [T][N] or
  *   NULL, may be y itself (with y's stride); y: [T][N], may not overlap any other input.
  * No host synchronisation, no scratch: calls on several streams are independent.
- * A row's result does not depend on the other rows of its call. Sums are taken in
+ * A row's result does not depend on the other rows of its call. (A bounded wait inside that
+ * runs out, 0.4 s, leaves NaN.) Sums are taken in
  * an order that depends on T, N and K alone, so results are bit-reproducible.
  * Errors: MOE_E_INVALID, MOE_E_UNSUPPORTED (K or N above 2^20, T above 2^24), MOE_E_CUDA. */
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
