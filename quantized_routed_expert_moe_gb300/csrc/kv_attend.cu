@@ -51,7 +51,7 @@
 #include "kv_cache.h"
 #include "kv_math.cuh"
 #include "moe_internal.h"
-#include "sm100.cuh"
+#include "sm100_more.cuh"
 
 namespace moe {
 

@@ -219,12 +219,13 @@ constexpr int kAhead = 4;
 constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 
 // With NORM the D / 16 lanes of a head sum its squares (values and, where a norm is not
-// asked for, its heads go through unchanged), and read the weights of their channels from
-// the first-level cache.
+// asked for, its heads go through unchanged); the weights lie in shared memory with their
+// offset.
 template <bool ADJACENT, bool E4M3, bool NORM>
 __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     extern __shared__ __align__(16) uint4 ring[];
     __shared__ __align__(16) float sm_c[8][128], sm_s[8][128];
+    __shared__ __align__(16) float sm_w[NORM ? 2 : 1][NORM ? 256 : 4];   // of queries, of keys
     const KvShape& s = p.s;
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     const int groups = s.head_dim / 16, g = lane % groups, side = 32 / groups, half = s.rotary_dim / 2;
@@ -251,6 +252,13 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     for (int i = 0; i < 4; ++i) turns[i] = lane + 32 * i < half ? p.turns[lane + 32 * i] : 0;
     pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
     pdl_trigger();
+    if constexpr (NORM) {
+        for (int i = threadIdx.x; i < s.head_dim; i += 256) {
+            sm_w[0][i] = p.n.q_weight ? p.n.q_weight[i] + p.n.weight_offset : 1.f;
+            sm_w[1][i] = p.n.k_weight ? p.n.k_weight[i] + p.n.weight_offset : 1.f;
+        }
+        __syncthreads();
+    }
     const int first = blockIdx.x * 8 + warp;
     int t = first / p.parts, part = first - t * p.parts;
     if (t >= p.a.T) return;
@@ -313,17 +321,18 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             if (r == part) next_page = look_up(next_pos, next_seq, next_read);
             const int head = r * side + lane / groups;
             const bool is_q = head < q_heads, is_v = head >= k_heads;
-            const float* const weight = !NORM || is_v ? nullptr : is_q ? p.n.q_weight : p.n.k_weight;
+            const bool normed = NORM && !is_v && (is_q ? p.n.q_weight : p.n.k_weight);
             float inv = 1.f;
             if constexpr (NORM) {
-                float sum = 0.f;   // (past the last head the ring holds what it held)
+                float2 sum = make_float2(0.f, 0.f);   // (past the last head the ring holds what it held)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const float2 a = unpack2(u4w(u0, x)), b = unpack2(u4w(u1, x));
-                    sum += a.x * a.x + a.y * a.y + b.x * b.x + b.y * b.y;
+                    sum = fma2(a, a, fma2(b, b, sum));
                 }
-                for (int o = 1; o < groups; o <<= 1) sum += __shfl_xor_sync(~0u, sum, o);
-                inv = 1.f / sqrtf(sum / s.head_dim + p.n.eps);
+                float all = sum.x + sum.y;
+                for (int o = 1; o < groups; o <<= 1) all += __shfl_xor_sync(~0u, all, o);
+                inv = rsqrtf(all / s.head_dim + p.n.eps);
             }
             if (head < heads && (is_q || page >= 0)) {
                 const int hk = head - (is_v ? k_heads : q_heads);
@@ -341,24 +350,16 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                     *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&sm_c[warp][a1]);
                     *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(&sm_s[warp][a1]);
                 }
-                float wn[16];
-                if (NORM && weight) {
-#pragma unroll
-                    for (int x = 0; x < 4; ++x) {
-                        const float4 f = __ldg(reinterpret_cast<const float4*>(weight + (x < 2 ? c0 : c1)) + x % 2);
-                        wn[4 * x] = (f.x + p.n.weight_offset) * inv;
-                        wn[4 * x + 1] = (f.y + p.n.weight_offset) * inv;
-                        wn[4 * x + 2] = (f.z + p.n.weight_offset) * inv;
-                        wn[4 * x + 3] = (f.w + p.n.weight_offset) * inv;
-                    }
-                }
+                const float* const weight = sm_w[NORM && !is_q];
+                const float2 inv2 = make_float2(inv, inv);
                 // two channels of either vector at a time
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
-                    if (NORM && weight) {
-                        a = make_float2(a.x * wn[2 * x], a.y * wn[2 * x + 1]);
-                        b = make_float2(b.x * wn[8 + 2 * x], b.y * wn[9 + 2 * x]);
+                    if (normed) {
+                        const float2 none = make_float2(0.f, 0.f);
+                        a = fma2(fma2(a, inv2, none), *reinterpret_cast<const float2*>(weight + c0 + 2 * x), none);
+                        b = fma2(fma2(b, inv2, none), *reinterpret_cast<const float2*>(weight + c1 + 2 * x), none);
                     }
                     if constexpr (ADJACENT) {
                         if (t0) a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
@@ -372,8 +373,8 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                         e[0][x / 2] |= quant2(a, scale.x, scale.y) << 16 * (x % 2);
                         e[1][x / 2] |= quant2(b, scale.x, scale.y) << 16 * (x % 2);
                     } else {
-                        if (t0 || (NORM && weight)) w[0][x] = pack2(a);
-                        if (t1 || (NORM && weight)) w[1][x] = pack2(b);
+                        if (t0 || normed) w[0][x] = pack2(a);
+                        if (t1 || normed) w[1][x] = pack2(b);
                     }
                     if (is_q && pos < 0) w[0][x] = w[1][x] = 0;
                 }

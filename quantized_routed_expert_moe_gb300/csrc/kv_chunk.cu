@@ -48,7 +48,7 @@
 #include "kv_cache.h"
 #include "kv_math.cuh"
 #include "moe_internal.h"
-#include "sm100.cuh"
+#include "sm100_more.cuh"
 
 namespace moe {
 
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (filled >> i & 1) bw::mbar_wait_short(full + 8 * i, phases >> i & 1, &none);
     } else if (warp == 8 || (C::NS == 2 && warp == 11)) {
         // ---- products ------------------------------------------------------------------------------
-        constexpr uint32_t id_qk = bw::idesc_f16_f32(128, kBlk, !C::FP8), id_pv = bw::idesc_f16_f32(128, D, !C::FP8, true);
+        constexpr uint32_t id_qk = bw::idesc_16_f32(128, kBlk, !C::FP8), id_pv = bw::idesc_16_f32(128, D, !C::FP8, true);
         Turn<!C::FP8, NST> turn;
         uint32_t parts = 0, uses = 0, steps = 0;   // of this tile: parts, blocks, turns with the other
         const int slot = warp == 8 ? 0 : 1;

@@ -11,9 +11,9 @@
 // products of the next (two accumulators in tensor memory).
 //
 // Measured (GB300; floors at 6.78 TB/s and 1932 TFLOP/s): one token 6144 x 8192 17.1 us (87% of
-// the copy rate), 512 x 768 3.6 us; 128 tokens 6144 x 6144 onto a fp32 residual 21.5 us (57%:
-// 48 tiles, two CTAs each, and 16 KB of weights per 372 cycles of products; clusters of three
-// do not all fit); 8191 tokens 2816 x 8192 with gelu 240 us, 1.57 PFLOP/s (82%: 48 KB of
+// the copy rate), 512 x 768 3.6 us; 128 tokens 6144 x 6144 onto a fp32 residual 24.7 us (50%:
+// 48 tiles, two CTAs each, and 16 KB of weights per 372 cycles of products and 130 of waiting;
+// clusters of three do not all fit; in bf16 21 us); 8191 tokens 2816 x 8192 with gelu 240 us, 1.57 PFLOP/s (82%: 48 KB of
 // operands for 512 cycles of products come from the second-level cache at 60 bytes a cycle and
 // SM; a pair of CTAs on one tile would need two thirds).
 #include <cuda_bf16.h>
@@ -25,7 +25,7 @@
 #include "common.cuh"
 #include "moe_internal.h"
 #include "per_device.h"
-#include "sm100.cuh"
+#include "sm100_more.cuh"
 
 namespace moe {
 
@@ -91,9 +91,11 @@ constexpr int kMaxSplits = 8;                       // a portable cluster
 constexpr int kThreads = 192;                       // four epilogue warps, the copies', the products'
 // Panels of a stage. The products wait once per stage, and a wait behind issued products takes
 // 130 cycles more than theirs (89 each up to 128 tokens): two panels where the ring holds them.
-constexpr int panels_of(int BN) { return BN <= 128 ? 2 : 1; }
-constexpr uint32_t stage_bytes(int BN) { return (kRows + BN) * kChunk * 2 * panels_of(BN); }
-constexpr int stages_of(int BN) { return kRing / stage_bytes(BN) < 12 ? kRing / stage_bytes(BN) : 12; }
+// (A fine tile's sums, 512 bytes per token, stand behind the stages; see k_linear.)
+constexpr int panels_of(int BN, bool fine) { return BN <= (fine ? 64 : 128) ? 2 : 1; }
+constexpr uint32_t stage_bytes(int BN, bool fine) { return (kRows + BN) * kChunk * 2 * panels_of(BN, fine); }
+constexpr int ring_bytes(int BN, bool fine) { return kRing - (fine ? BN * kRows * 4 : 0); }
+constexpr int stages_of(int BN, bool fine) { return ring_bytes(BN, fine) / stage_bytes(BN, fine); }
 
 struct LinearArgs {
     const float* bias;
@@ -152,17 +154,73 @@ __device__ __forceinline__ void finish16(const LinearArgs& p, int t, int count, 
     }
 }
 
-template <int BN>
+// A tile whose sums lie in shared memory, of as many CTAs as `splits` says: the columns
+// `split`, `split` + `splits`, ..., a warp one at a time, four channels a lane.
+__device__ __forceinline__ void finish_shared(const LinearArgs& p, int tile, int BN, uint32_t sums_at, int split, int splits,
+                                              int warps) {
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int n = tile % p.row_tiles * kRows + 4 * lane, t0 = tile / p.row_tiles * BN, cols = min(BN, p.T - t0);
+    if (n < p.N) {
+        const float4 bias = p.bias ? *reinterpret_cast<const float4*>(p.bias + n) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int c = warp * splits + split; c < cols; c += warps * splits) {
+            const int64_t at = (int64_t)(t0 + c) * p.y_stride + n, rt = (int64_t)(t0 + c) * p.residual_stride + n;
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f), part[kMaxSplits];
+            if (p.residual) {
+                if (p.out_f32) {
+                    r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + rt);
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + rt);
+                    r = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
+                                    __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
+                }
+            }
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < splits) part[s] = ld_cluster4(sums_at + (c * kRows + 4 * lane) * 4, s);
+            float z[4] = {};
+#pragma unroll
+            for (int s = 0; s < kMaxSplits; ++s)
+                if (s < splits) {
+                    z[0] += part[s].x;
+                    z[1] += part[s].y;
+                    z[2] += part[s].z;
+                    z[3] += part[s].w;
+                }
+            z[0] += bias.x;
+            z[1] += bias.y;
+            z[2] += bias.z;
+            z[3] += bias.w;
+            activate(z, p.act);
+            const float4 o = make_float4(z[0] + r.x, z[1] + r.y, z[2] + r.z, z[3] + r.w);
+            if (p.out_f32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = o;
+            } else {
+                const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
+                    make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+            }
+        }
+    }
+}
+
+// FINE (fp32 outputs): the tensor cores cut bits off at every step of a sum, 1.8e-8 of the result
+// and always towards zero: 3.4e-6 of the result after 3072 products; so their sums end after 512
+// and are added by the epilogue's threads, which round: 5e-7. It caps the tokens of a tile at 128, whose sums a
+// thread can hold. The rounding of bf16 outputs, 1.7e-3, hides all that.
+template <int BN, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const LinearArgs p, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
-    constexpr int S = stages_of(BN), PN = panels_of(BN);
-    constexpr uint32_t W_PANEL = kRows * kChunk * 2, X_PANEL = BN * kChunk * 2, SB = stage_bytes(BN), COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    constexpr int S = stages_of(BN, FINE), PN = panels_of(BN, FINE);
+    constexpr uint32_t W_PANEL = kRows * kChunk * 2, X_PANEL = BN * kChunk * 2, SB = stage_bytes(BN, FINE), COLS = 2 * BN < 32 ? 32 : 2 * BN;
+    constexpr int RUN = FINE ? 512 / (PN * kChunk) : 1 << 30;   // stages of one sum
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_full[S], s_empty[S], s_done[2], s_free[2], s_drain;
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const uint32_t ring = (bw::saddr(smem_raw) + 1023) & ~1023u;
+    const uint32_t sums_at = ring + (FINE ? ring_bytes(BN, true) : 0);
     const uint32_t full = bw::saddr(s_full), empty = bw::saddr(s_empty), done = bw::saddr(s_done), free_ = bw::saddr(s_free);
     // this CTA's share of every tile's K, in chunks
     const int split = p.splits > 1 ? (int)cluster_rank() : 0, chunks = (p.K + PN * kChunk - 1) / (PN * kChunk);
@@ -228,12 +286,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 5) {
         uint32_t it = 0, acc = 0;
         bool ok = true;
-        for (int tile = first; tile < p.tiles && ok; tile += step, ++acc) {
-            if (!(ok = all(wait(free_ + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1)))) break;
-            bw::tc_fence_after();
-            const uint32_t d = tmem + (acc & 1) * BN;
-            for (int k = k0; k < k1; ++k, ++it) {
-                const uint32_t s = it % S, at = ring + s * SB;
+        for (int tile = first; tile < p.tiles && ok; tile += step)
+            for (int k = k0; k < k1 && ok; ++k, ++it) {
+                const bool begins = FINE ? (k - k0) % RUN == 0 : k == k0;
+                const bool ends = k == k1 - 1 || (FINE && (k - k0) % RUN == RUN - 1);
+                if (begins) {
+                    if (!(ok = all(wait(free_ + 8 * (acc & 1), ((acc >> 1) & 1) ^ 1)))) break;
+                    bw::tc_fence_after();
+                }
+                const uint32_t d = tmem + (acc & 1) * BN, s = it % S, at = ring + s * SB;
                 if (!(ok = all(wait(full + 8 * s, (it / S) & 1)))) break;
                 bw::tc_fence_after();
                 if (bw::elect_one()) {
@@ -241,100 +302,80 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int j = 0; j < PN * kChunk / 16; ++j)
                         bw::mma_f16(d, bw::desc_sw128(at + j / 4 * W_PANEL + 32 * (j % 4)),
                                     bw::desc_sw128(at + PN * W_PANEL + j / 4 * X_PANEL + 32 * (j % 4)),
-                                    bw::idesc_f16_f32(kRows, BN, true), k > k0 || j > 0);
+                                    bw::idesc_16_f32(kRows, BN, true), !begins || j > 0);
                     bw::mma_commit(empty + 8 * s);
-                    if (k == k1 - 1) bw::mma_commit(done + 8 * (acc & 1));
+                    if (ends) bw::mma_commit(done + 8 * (acc & 1));
                 }
                 __syncwarp();
+                acc += ends;
             }
-        }
         if (!ok) {   // no product is running at the end
             if (bw::elect_one()) bw::mma_commit(bw::saddr(&s_drain));
             __syncwarp();
             int none = 0;
             bw::mbar_wait_short(bw::saddr(&s_drain), 0, &none);
         }
-    } else if (p.splits == 1) {
+    } else {
         const int row = warp * 32 + lane;
+        float* const sums = reinterpret_cast<float*>(smem_raw + (sums_at - bw::saddr(smem_raw)));
         uint32_t acc = 0;
-        for (int tile = first; tile < p.tiles; tile += step, ++acc) {
+        for (int tile = first; tile < p.tiles; tile += step) {
             const int n = tile % p.row_tiles * kRows + row, t0 = tile / p.row_tiles * BN, cols = min(BN, p.T - t0);
             const float bias = p.bias && n < p.N ? p.bias[n] : 0.f;
-            const bool ok = all(wait(done + 8 * (acc & 1), (acc >> 1) & 1) && !*const_cast<volatile int*>(&s_abort));
-            bw::tc_fence_after();
-            const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16) + (acc & 1) * BN;
-            for (int c = 0; c < cols; c += 16) {
-                float v[16];
-                bw::tmem_ld16(from + c, v);
-                if (!ok)
-                    for (int j = 0; j < 16; ++j) v[j] = NAN;
-                if (n < p.N) finish16(p, t0 + c, cols - c, n, v, bias);
-            }
-            bw::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) bw::mbar_arrive(free_ + 8 * (acc & 1));
-        }
-    } else {
-        // the sums of this CTA's share, into the ring: its copies and products are done
-        const int row = warp * 32 + lane, cols = min(BN, p.T - first / p.row_tiles * BN);
-        float* sums = reinterpret_cast<float*>(smem_raw + (ring - bw::saddr(smem_raw)));
-        const bool ok = all(wait(done, 0) && !*const_cast<volatile int*>(&s_abort));
-        bw::tc_fence_after();
-        for (int c = 0; c < cols; c += 16) {
-            float v[16];
-            bw::tmem_ld16(tmem + ((uint32_t)(warp * 32) << 16) + c, v);
+            float sum[FINE ? BN / 16 : 1][16];
+            bool ok = true;
+            if constexpr (FINE)
 #pragma unroll
-            for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + row] = ok ? v[j] : NAN;
+                for (int c = 0; c < BN; ++c) sum[c / 16][c % 16] = 0.f;
+            for (int k = k0; k < k1; k += min(RUN, k1 - k), ++acc) {
+                const bool last = k1 - k <= RUN;
+                ok = all(wait(done + 8 * (acc & 1), (acc >> 1) & 1) && !*const_cast<volatile int*>(&s_abort)) && ok;
+                bw::tc_fence_after();
+                const uint32_t from = tmem + ((uint32_t)(warp * 32) << 16) + (acc & 1) * BN;
+                // out of here, or to shared memory: a fine tile's sums behind the ring, a split tile's
+                // into it (its copies and products are done)
+                if constexpr (FINE) {
+#pragma unroll
+                    for (int i = 0; i < BN / 16; ++i)
+                        if (16 * i < cols) {
+                            float v[16];
+                            bw::tmem_ld16(from + 16 * i, v);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sum[i][j] += v[j];
+                            if (last)
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) sums[(16 * i + j) * kRows + row] = ok ? sum[i][j] : NAN;
+                        }
+                } else {
+                    for (int c = 0; c < cols; c += 16) {
+                        float v[16];
+                        bw::tmem_ld16(from + c, v);
+                        if (!ok)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) v[j] = NAN;
+                        if (p.splits > 1) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + row] = v[j];
+                        } else if (n < p.N) {
+                            finish16(p, t0 + c, cols - c, n, v, bias);
+                        }
+                    }
+                }
+                bw::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) bw::mbar_arrive(free_ + 8 * (acc & 1));
+            }
+            if (FINE && p.splits == 1) {
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                finish_shared(p, tile, BN, sums_at, 0, 1, 4);
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+            }
         }
     }
     __syncwarp();
     if (p.splits > 1) {
         cluster_meet();
-        // every CTA finishes its share of the columns, a warp one at a time, four channels a lane
-        const int n = first % p.row_tiles * kRows + 4 * lane, t0 = first / p.row_tiles * BN;
-        const int cols = min(BN, p.T - t0);
-        if (n < p.N) {
-            const float4 bias = p.bias ? *reinterpret_cast<const float4*>(p.bias + n) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-            for (int c = warp * p.splits + split; c < cols; c += kThreads / 32 * p.splits) {
-                const int64_t at = (int64_t)(t0 + c) * p.y_stride + n, rt = (int64_t)(t0 + c) * p.residual_stride + n;
-                float4 r = make_float4(0.f, 0.f, 0.f, 0.f), part[kMaxSplits];
-                if (p.residual) {
-                    if (p.out_f32) {
-                        r = *reinterpret_cast<const float4*>(static_cast<const float*>(p.residual) + rt);
-                    } else {
-                        const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.residual) + rt);
-                        r = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u),
-                                        __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
-                    }
-                }
-#pragma unroll
-                for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < p.splits) part[s] = ld_cluster4(ring + (c * kRows + 4 * lane) * 4, s);
-                float z[4] = {};
-#pragma unroll
-                for (int s = 0; s < kMaxSplits; ++s)
-                    if (s < p.splits) {
-                        z[0] += part[s].x;
-                        z[1] += part[s].y;
-                        z[2] += part[s].z;
-                        z[3] += part[s].w;
-                    }
-                z[0] += bias.x;
-                z[1] += bias.y;
-                z[2] += bias.z;
-                z[3] += bias.w;
-                activate(z, p.act);
-                const float4 o = make_float4(z[0] + r.x, z[1] + r.y, z[2] + r.z, z[3] + r.w);
-                if (p.out_f32) {
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = o;
-                } else {
-                    const __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y), b = __floats2bfloat162_rn(o.z, o.w);
-                    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + at) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-                }
-            }
-        }
+        finish_shared(p, first, BN, sums_at, split, p.splits, kThreads / 32);
         cluster_meet();   // no CTA leaves while its sums are read
     }
     bw::tc_fence_before();
@@ -350,7 +391,11 @@ struct Shape {
     int BN;
     LinearKernel kernel;
 };
-const Shape kShapes[] = {{16, k_linear<16>}, {32, k_linear<32>}, {64, k_linear<64>}, {128, k_linear<128>}, {256, k_linear<256>}};
+const Shape kShapes[] = {{16, k_linear<16, false>}, {32, k_linear<32, false>}, {64, k_linear<64, false>},
+                         {128, k_linear<128, false>}, {256, k_linear<256, false>},
+                         {16, k_linear<16, true>}, {32, k_linear<32, true>}, {64, k_linear<64, true>},
+                         {128, k_linear<128, true>}};
+constexpr int kFine = 5;   // the first of the fine ones
 
 int set_up(int device) {
     int sms = 0;
@@ -394,8 +439,9 @@ cudaError_t launch(const moe_linear_desc& d, const void* x, const void* w, const
         const cudaError_t e = cudaGetLastError();
         return e == cudaSuccess ? cudaErrorNotSupported : e;
     }
-    const Shape* s = kShapes;
-    while (s->BN < T && s->BN < 256) ++s;
+    const bool fine = d.out_dtype == MOE_F32;
+    const Shape* s = kShapes + (fine ? kFine : 0);
+    while (s->BN < T && s->BN < (fine ? 128 : 256)) ++s;
     LinearArgs p{bias, residual, y, d.y_stride, d.residual_stride, T, d.in_features, d.out_features,
                  d.out_dtype == MOE_F32, d.activation, 0, 0, 1};
     p.row_tiles = (p.N + kRows - 1) / kRows;
@@ -405,7 +451,7 @@ cudaError_t launch(const moe_linear_desc& d, const void* x, const void* w, const
     // As many CTAs to a tile as leave all clusters resident at once: the SMs lie in groups, and
     // 48 tiles of 3 CTAs, of which 46 fit, take 25.3 us (one token, 6144 x 6144) where 2 take
     // 16.9; 6 tiles of 8 chunks (512 x 768) 3.2 us by 8 CTAs each, 3.9 by 2.
-    const int stage_k = kChunk * panels_of(s->BN), chunks = (p.K + stage_k - 1) / stage_k;
+    const int stage_k = kChunk * panels_of(s->BN, fine), chunks = (p.K + stage_k - 1) / stage_k;
     for (int n = std::min({sms / p.tiles, kMaxSplits, chunks}); n > 1; --n)
         if (g_clusters[n].get(device, [&] { return resident_clusters(n); }) >= p.tiles) {
             p.splits = n;
