@@ -346,19 +346,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                                 for (int j = 0; j < 16; ++j) sums[(16 * i + j) * kRows + row] = ok ? sum[i][j] : NAN;
                         }
+                } else if (p.splits > 1) {
+                    for (int c = 0; c < cols; c += 16) {
+                        float v[16];
+                        bw::tmem_ld16(from + c, v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + row] = ok ? v[j] : NAN;
+                    }
                 } else {
                     for (int c = 0; c < cols; c += 16) {
                         float v[16];
                         bw::tmem_ld16(from + c, v);
-                        if (!ok)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) v[j] = NAN;
-                        if (p.splits > 1) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) sums[(c + j) * kRows + row] = v[j];
-                        } else if (n < p.N) {
-                            finish16(p, t0 + c, cols - c, n, v, bias);
-                        }
+                        if (n < p.N) finish16(p, t0 + c, cols - c, n, v, ok ? bias : NAN);
                     }
                 }
                 bw::tc_fence_before();
