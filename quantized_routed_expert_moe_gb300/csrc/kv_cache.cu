@@ -220,7 +220,9 @@ constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 
 // With NORM the D / 16 lanes of a head sum its squares (values and, where a norm is not
 // asked for, its heads go through unchanged); the weights lie in shared memory with their
-// offset.
+// offset. What it costs is the chain from a round's copy over the sum to the rotation, which 24
+// warps an SM do not hide: 8192 tokens of 48 + 8 + 8 heads of 128 take 65.5 us where they take
+// 43 without norms, into 8 bits 71 us (3.5 TB/s, 52% of the copy rate); one token 3.3 us.
 template <bool ADJACENT, bool E4M3, bool NORM>
 __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     extern __shared__ __align__(16) uint4 ring[];

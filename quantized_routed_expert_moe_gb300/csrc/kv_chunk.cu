@@ -16,9 +16,10 @@
 // tile: its two softmax groups take half the columns each, and S has two buffers.
 //
 // Weights of a bf16 cache enter the second product rounded to bf16 (2^-8 of each at most; the
-// sum is taken before): with 64 bits' worth of the rest the outputs are off by 1.6e-3 of their
-// norm, all but the output's own rounding. Those of an 8-bit cache are fp16, in which its keys
-// and values are exact.
+// sum is taken before the rounding): outputs are 2.0e-3 to 2.3e-3 of their norm from 64 bits,
+// of which their own rounding to bf16 is 1.6e-3. A second bf16 number for the rest of a weight
+// would halve the rate of that product. Those of an 8-bit cache are fp16, in which its keys and
+// values are exact: 1.7e-3, all of it the output's own rounding.
 //
 // Roles. Eight softmax warps; an issuing warp per tile (a wait behind issued products ends only
 // when those have left the queue); a warp that walks the CTA's parts for all roles and copies
@@ -27,7 +28,7 @@
 // products at 103 cycles each (64 would be the peak: a product of 128 x 128 x 16 takes 93 at
 // least on one CTA) and two hand-overs of 260: 3820 cycles. All loops are kept as loops: the
 // first form's 135 KB of instructions were read again and again (13000 misses of the cache for
-// them per SM in 41 blocks, 2069 us for a prompt that takes 720).
+// them per SM in 41 blocks, 2069 us for a prompt that takes 735).
 //
 // Split. All blocks of all tiles of the call, numbered tile by tile, are dealt out evenly and
 // contiguously to one CTA per SM from the lengths as they stand on the device. A tile that is
@@ -35,9 +36,9 @@
 // joins in order.
 //
 // Measured (GB300; floors at 1932 TFLOP/s and 6.78 TB/s): a prompt of 8192 tokens, 48 heads
-// over 8 of 128, 730 us (1130 TFLOP/s, 59%); 8 x 800 tokens after 7200, 64 heads over 4, 1203
-// TFLOP/s (62%), in 8 bits 1013; 128 tokens after 32640 105 us (51%); 64 x 4 tokens after up to
-// 16380, pages of 16, 300 us (5.2 TB/s, 77%); 17 tokens 9.7 us, of which 3.5 us before the first
+// over 8 of 128, 735 us (1120 TFLOP/s, 58%); 8 x 800 tokens after 7200, 64 heads over 4, 1203
+// TFLOP/s (62%), in 8 bits 1013; 128 tokens after 32640 106 us (50%); 64 x 4 tokens after up to
+// 16380, pages of 16, 296 us (5.3 TB/s, 78%); 17 tokens 9.5 us, of which 3.5 us before the first
 // copy (lengths, the walk, the block table) and most of the rest instructions that run once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

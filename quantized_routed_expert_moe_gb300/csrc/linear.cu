@@ -13,9 +13,9 @@
 // Measured (GB300; floors at 6.78 TB/s and 1932 TFLOP/s): one token 6144 x 8192 17.1 us (87% of
 // the copy rate), 512 x 768 3.6 us; 128 tokens 6144 x 6144 onto a fp32 residual 24.7 us (50%:
 // 48 tiles, two CTAs each, and 16 KB of weights per 372 cycles of products and 130 of waiting;
-// clusters of three do not all fit; in bf16 21 us); 8191 tokens 2816 x 8192 with gelu 240 us, 1.57 PFLOP/s (82%: 48 KB of
-// operands for 512 cycles of products come from the second-level cache at 60 bytes a cycle and
-// SM; a pair of CTAs on one tile would need two thirds).
+// clusters of three do not all fit; in bf16 21 us); 8191 tokens 2816 x 8192 with gelu 247 us,
+// 1.53 PFLOP/s (79%: 48 KB of operands for 512 cycles of products come from the second-level
+// cache at 60 bytes a cycle and SM; a pair of CTAs on one tile would need two thirds).
 #include <cuda_bf16.h>
 
 #include <algorithm>
