@@ -679,10 +679,10 @@ typedef struct {
  * each sequence, its chunk included (append the chunk first). Token i of a chunk of n
  * stands at position p = len - n + i, and attends to positions j <= p; window > 0: only
  * j > p - window. Scores, softcap, out ([T][n_heads][head_dim]) and lse ([T][n_heads])
- * are those of moe_kv_attend. A token at a negative position (a chunk longer than its
- * sequence's length) gives out = 0 and lse = -inf. Rows outside starts[0]..starts[B] - 1
- * are left as they were. Cached values that a token does not attend to do not change its
- * result, whatever they hold, NaN included.
+ * are those of moe_kv_attend; neither may overlap an input or the workspace. A token at a
+ * negative position (a chunk longer than its sequence's length) gives out = 0 and lse =
+ * -inf. Rows outside starts[0]..starts[B] - 1 are left as they were. Cached values that a
+ * token does not attend to do not change its result, whatever they hold, NaN included.
  * workspace: device memory of at least moe_kv_chunk_workspace bytes, 16-byte aligned, in
  * any state; calls that share one must not overlap on the GPU (the handles of a model's
  * layers may share it). MOE_E_UNSUPPORTED: T * n_heads of 2^31 or more. */

@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const int64_t token_heads = s.n_heads;
         uint32_t uses = 0, ended = 0, written = 0;       // blocks and parts of this slot; cut sides recorded
         bool ok = true;
-        const float scale = fabsf(p.a.scale) < 0x1p-100f ? 0x1p-100f : fabsf(p.a.scale);
+        const float scale = fabsf(p.a.scale);
         const uint32_t flip = p.a.scale < 0.f ? 0x80008000u : 0u;
         float c_next = 0.f;
 
@@ -965,7 +965,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             bw::fence_async_smem();
             __syncwarp();
             if (lane == 0) bw::mbar_arrive(q_full + 8 * slot);
-            c_next = c;
+            // (no score of fp32's range sees the smallest number, and -inf times it stays -inf)
+            c_next = fmaxf(c, 0x1p-149f);
         };
         // the two warps of a row's columns meet (heads of 256)
         uint32_t met = 0;

@@ -227,6 +227,18 @@ def test_scales(scale):
     c.check()
 
 
+@pytest.mark.parametrize("dt,D", [(BF16, 128), (BF16, 256), (E4M3, 128)])
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -104, -2.0 ** -107])
+def test_small_scales_of_large_products(dt, D, scale):
+    """Products of 2^100 and more: a scale that is as small still counts by its value."""
+    c = Case([(70, 200), (3, 3), (1, 40)], 4, 2, D, 16, dt, seed=9)
+    c.q = c.q * 2.0 ** (60 if dt == BF16 else 100)
+    if dt == BF16:
+        c.k = c.k * 2.0 ** 40
+    c.scale = scale
+    c.check()
+
+
 @pytest.mark.parametrize("dt", [BF16, E4M3])
 def test_large_scores(dt):
     """Scores of 10^8 and more: all weight on the largest, no NaN and no zero."""
