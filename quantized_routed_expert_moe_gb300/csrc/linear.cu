@@ -204,10 +204,11 @@ __device__ __forceinline__ void finish_shared(const LinearArgs& p, int tile, int
     }
 }
 
-// FINE (fp32 outputs): the tensor cores cut bits off at every step of a sum, 1.8e-8 of the result
-// and always towards zero: 3.4e-6 of the result after 3072 products; so their sums end after 512
-// and are added by the epilogue's threads, which round: 5e-7. It caps the tokens of a tile at 128, whose sums a
-// thread can hold. The rounding of bf16 outputs, 1.7e-3, hides all that.
+// FINE (fp32 outputs): the tensor cores cut bits off at every step of a sum of 16 products,
+// 1.8e-8 of the result and always towards zero: 1.5e-6 of the norm over 6144 products of both
+// signs. So their sums end after 512 and are added by the epilogue's threads, which round:
+// 2.1e-7. It caps the tokens of a tile at 128, whose sums a thread can hold. The rounding of bf16
+// outputs, 1.7e-3, hides all that.
 template <int BN, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_linear(const LinearArgs p, const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_x) {
@@ -283,6 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t q = it > (uint32_t)S ? it - S : 0; q < it; ++q)
                 bw::mbar_wait_short(full + 8 * (q % S), (q / S) & 1, &none);
         }
+        // after a wait that ran out a copy may have landed on a split tile's sums
+        __syncwarp();
+        if (p.splits > 1 && *const_cast<volatile int*>(&s_abort))
+            for (int i = lane; i < BN * kRows; i += 32) reinterpret_cast<float*>(smem_raw + (sums_at - bw::saddr(smem_raw)))[i] = NAN;
     } else if (warp == 5) {
         uint32_t it = 0, acc = 0;
         bool ok = true;
