@@ -180,6 +180,13 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
         : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
     return d;
 }
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+    float2 d;
+    asm("{.reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a;}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+    return d;
+}
 // e4m3 of two values / scale, saturating, NaN stays NaN; inv = 1 / scale, rounded. The
 // product with inv is off by 2^-23, which takes the wrong neighbour where the quotient is
 // half way between two (one value in 10^6); with the remainder's share added it is the
@@ -205,6 +212,7 @@ struct AppendArgs {
     const float2* scales;   // of the keys, then of the values: scale and its rounded reciprocal
     unsigned* health;
     int parts, rounds;   // units and rounds of a token
+    float share;         // of a channel in a head's mean: a power of two
 };
 
 // A round is 32 / (D / 16) heads of a token, one warp's copy of 1 KB; a unit is
@@ -220,9 +228,12 @@ constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 
 // With NORM the D / 16 lanes of a head sum its squares (values and, where a norm is not
 // asked for, its heads go through unchanged); the weights lie in shared memory with their
-// offset. What it costs is the chain from a round's copy over the sum to the rotation, which 24
-// warps an SM do not hide: 8192 tokens of 48 + 8 + 8 heads of 128 take 65.5 us where they take
-// 43 without norms, into 8 bits 71 us (3.5 TB/s, 52% of the copy rate); one token 3.3 us.
+// offset, fours of channels so that the lanes of a head meet no bank twice. Bound by
+// instructions, 390 to a round (73% of the issue slots): 8192 tokens of 48 + 8 + 8 heads of 128
+// take 53 us (75% of the copy rate; without norms 43), into 8 bits 58.6 us; one token 3.0 us.
+// With the head's sixteen channels unpacked once, then scaled, turned and rounded in steps of
+// their own: 58.6; all three pair by pair, with a branch each, 66.4; before that, weights read by
+// twos and a division for the mean, 71.3.
 template <bool ADJACENT, bool E4M3, bool NORM>
 __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     extern __shared__ __align__(16) uint4 ring[];
@@ -255,9 +266,15 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
     pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
     pdl_trigger();
     if constexpr (NORM) {
-        for (int i = threadIdx.x; i < s.head_dim; i += 256) {
-            sm_w[0][i] = p.n.q_weight ? p.n.q_weight[i] + p.n.weight_offset : 1.f;
-            sm_w[1][i] = p.n.k_weight ? p.n.k_weight[i] + p.n.weight_offset : 1.f;
+        // a lane's fours of channels (c0, c0 + 4, c1, c1 + 4) each behind its neighbour's
+        if (threadIdx.x < groups * 8) {
+            const int four = threadIdx.x / 2 / groups, of = threadIdx.x / 2 % groups, k = threadIdx.x % 2;
+            const bool mine = !ADJACENT && 16 * of < s.rotary_dim;
+            const int first = 8 * of + (!ADJACENT && !mine ? half : 0), second = mine ? first + half : 8 * of + s.head_dim / 2;
+            const float* const from = (k ? p.n.k_weight : p.n.q_weight);
+            for (int i = 0; i < 4; ++i)
+                sm_w[k][four * 64 + of * 4 + i] =
+                    from ? from[(four < 2 ? first : second) + four % 2 * 4 + i] + p.n.weight_offset : 1.f;
         }
         __syncthreads();
     }
@@ -324,23 +341,40 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
             const int head = r * side + lane / groups;
             const bool is_q = head < q_heads, is_v = head >= k_heads;
             const bool normed = NORM && !is_v && (is_q ? p.n.q_weight : p.n.k_weight);
-            float inv = 1.f;
+            float2 a4[NORM ? 4 : 1], b4[NORM ? 4 : 1];   // the two vectors, pair by pair
             if constexpr (NORM) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) a4[x] = unpack2(u4w(u0, x)), b4[x] = unpack2(u4w(u1, x));
+            }
+            if (NORM && r * side < k_heads) {
                 float2 sum = make_float2(0.f, 0.f);   // (past the last head the ring holds what it held)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const float2 a = unpack2(u4w(u0, x)), b = unpack2(u4w(u1, x));
-                    sum = fma2(a, a, fma2(b, b, sum));
-                }
+                for (int x = 0; x < 4; ++x) sum = fma2(a4[x], a4[x], fma2(b4[x], b4[x], sum));
                 float all = sum.x + sum.y;
-                for (int o = 1; o < groups; o <<= 1) all += __shfl_xor_sync(~0u, all, o);
-                inv = rsqrtf(all / s.head_dim + p.n.eps);
+                all += __shfl_xor_sync(~0u, all, 1);
+                all += __shfl_xor_sync(~0u, all, 2);
+                if (groups > 4) all += __shfl_xor_sync(~0u, all, 4);
+                if (groups > 8) all += __shfl_xor_sync(~0u, all, 8);
+                const float inv = rsqrtf(all * p.share + p.n.eps);
+                const float2 inv2 = make_float2(inv, inv);
+                if (normed) {
+                    const float* const weight = sm_w[!is_q] + g * 4;
+#pragma unroll
+                    for (int x = 0; x < 4; x += 2) {
+                        const float4 wa = *reinterpret_cast<const float4*>(weight + x * 32);
+                        const float4 wb = *reinterpret_cast<const float4*>(weight + x * 32 + 128);
+                        a4[x] = mul2(mul2(a4[x], inv2), make_float2(wa.x, wa.y));
+                        a4[x + 1] = mul2(mul2(a4[x + 1], inv2), make_float2(wa.z, wa.w));
+                        b4[x] = mul2(mul2(b4[x], inv2), make_float2(wb.x, wb.y));
+                        b4[x + 1] = mul2(mul2(b4[x + 1], inv2), make_float2(wb.z, wb.w));
+                    }
+                }
             }
             if (head < heads && (is_q || page >= 0)) {
                 const int hk = head - (is_v ? k_heads : q_heads);
                 const int at0 = is_v ? v0 : c0, at1 = is_v ? v1 : c1;
                 const float2 scale = E4M3 && !is_q ? p.scales[(is_v ? s.n_kv_heads : 0) + hk] : make_float2(1.f, 1.f);
-                uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
+                alignas(16) uint32_t w[2][4] = {{u0.x, u0.y, u0.z, u0.w}, {u1.x, u1.y, u1.z, u1.w}};
                 uint32_t e[2][2] = {};
                 float c[8], sn[8];
                 const bool t0 = turn0 && !is_v, t1 = ADJACENT ? turn1 && !is_v : t0;
@@ -352,17 +386,8 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                     *reinterpret_cast<float4*>(c + 4) = *reinterpret_cast<const float4*>(&sm_c[warp][a1]);
                     *reinterpret_cast<float4*>(sn + 4) = *reinterpret_cast<const float4*>(&sm_s[warp][a1]);
                 }
-                const float* const weight = sm_w[NORM && !is_q];
-                const float2 inv2 = make_float2(inv, inv);
                 // two channels of either vector at a time
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
-                    if (normed) {
-                        const float2 none = make_float2(0.f, 0.f);
-                        a = fma2(fma2(a, inv2, none), *reinterpret_cast<const float2*>(weight + c0 + 2 * x), none);
-                        b = fma2(fma2(b, inv2, none), *reinterpret_cast<const float2*>(weight + c1 + 2 * x), none);
-                    }
+                auto turn = [&](int x, float2& a, float2& b) {
                     if constexpr (ADJACENT) {
                         if (t0) a = make_float2(a.x * c[x] - a.y * sn[x], a.y * c[x] + a.x * sn[x]);
                         if (t1) b = make_float2(b.x * c[4 + x] - b.y * sn[4 + x], b.y * c[4 + x] + b.x * sn[4 + x]);
@@ -371,14 +396,38 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                         a = make_float2(a.x * c[2 * x] - b.x * sn[2 * x], a.y * c[2 * x + 1] - b.y * sn[2 * x + 1]);
                         b = make_float2(b.x * c[2 * x] + u.x * sn[2 * x], b.y * c[2 * x + 1] + u.y * sn[2 * x + 1]);
                     }
+                };
+                auto round = [&](int x, float2 a, float2 b) {
                     if (E4M3 && !is_q) {
                         e[0][x / 2] |= quant2(a, scale.x, scale.y) << 16 * (x % 2);
                         e[1][x / 2] |= quant2(b, scale.x, scale.y) << 16 * (x % 2);
                     } else {
-                        if (t0 || normed) w[0][x] = pack2(a);
-                        if (t1 || normed) w[1][x] = pack2(b);
+                        if (NORM || t0) w[0][x] = pack2(a);
+                        if (NORM || t1) w[1][x] = pack2(b);
                     }
-                    if (is_q && pos < 0) w[0][x] = w[1][x] = 0;
+                    if (!NORM && is_q && pos < 0) w[0][x] = w[1][x] = 0;
+                };
+                if constexpr (NORM) {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) turn(x, a4[x], b4[x]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) round(x, a4[x], b4[x]);
+                    // what is neither scaled nor turned keeps its bits, NaN's too
+                    if (!(E4M3 && !is_q) && !normed) {
+                        const uint4* const from = slots + (take + kAhead - 1) % kAhead * 64;
+                        if (!t0) *reinterpret_cast<uint4*>(w[0]) = from[0];
+                        if (!t1) *reinterpret_cast<uint4*>(w[1]) = from[32];
+                    }
+                    if (is_q && pos < 0)
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) w[0][x] = w[1][x] = 0;
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        float2 a = unpack2(w[0][x]), b = unpack2(w[1][x]);
+                        turn(x, a, b);
+                        round(x, a, b);
+                    }
                 }
                 const int64_t off = row + hk * s.head_stride;
                 if (E4M3 && !is_q) {
@@ -572,7 +621,7 @@ static moe_status append(moe_kv* kv, const moe_kv_append_args* args, const moe_k
     Kv& K = kv->K;
     DeviceGuard g(K.device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
-    AppendArgs p{*args, norm, K.s, K.k_pages, K.v_pages, K.turns, K.scales, K.health, 1, 1};
+    AppendArgs p{*args, norm, K.s, K.k_pages, K.v_pages, K.turns, K.scales, K.health, 1, 1, 1.f / K.s.head_dim};
     const int heads = (args->q ? K.s.n_heads : 0) + 2 * K.s.n_kv_heads, side = 32 / (K.s.head_dim / 16);
     p.rounds = (heads + side - 1) / side;
     // Units per token: a warp takes ceil(T n / warps) units, each of rounds / n rounds (the most
