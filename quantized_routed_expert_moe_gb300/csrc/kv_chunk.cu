@@ -812,33 +812,38 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         ok = wait(empty + 8 * turn.stage, turn.use + 1) && ok;
                         if (!ok) return;
                         const uint32_t raw = raws + in.stage * C::RAW;
-                        const int wide = C::PARTS == 1 || !values ? C::KD / 16 : D / 16;   // units of 16 channels in a row
+                        // units of 16 channels in a row, a power of two
+                        constexpr int KU = C::KD / 16, KLOG = KU == 4 ? 2 : 3;
+                        const int log = C::PARTS == 1 || !values ? KLOG : KLOG + 1;
+                        // in place and apart: few stages need it, and the loop below stays short
+                        if (__builtin_expect(look, 0)) {
+#pragma unroll 1
+                            for (int i = me; i < C::RAW / 16; i += TEAM) {
+                                uint4 w = ld_shared(raw + i * 16);
+                                const bool on = live(i >> log);
+                                auto fix = [&](uint32_t& x) {
+                                    // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
+                                    const uint32_t nan = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                                    if (!on) x = 0;
+                                    else if (part_seen && nan) {
+                                        x &= ~(nan * 0xffu);
+                                        *odd = 1;
+                                    }
+                                };
+                                fix(w.x), fix(w.y), fix(w.z), fix(w.w);
+                                st_shared(raw + i * 16, w);
+                            }
+                        }
                         // four vectors' reads are on their way before the first is converted
-                        constexpr int EACH = C::RAW / 16 / TEAM < 4 ? C::RAW / 16 / TEAM : 4;
+                        constexpr int MOST = D == 256 ? 4 : 8, EACH = C::RAW / 16 / TEAM < MOST ? C::RAW / 16 / TEAM : MOST;
 #pragma unroll 1
                         for (int i0 = me; i0 < C::RAW / 16; i0 += EACH * TEAM) {
                             uint4 w[EACH];
 #pragma unroll
                             for (int k = 0; k < EACH; ++k) w[k] = ld_shared(raw + (i0 + k * TEAM) * 16);
-                            if (__builtin_expect(look, 0)) {
-#pragma unroll
-                                for (int k = 0; k < EACH; ++k) {
-                                    const bool on = live((i0 + k * TEAM) / wide);
-                                    auto fix = [&](uint32_t& x) {
-                                        // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
-                                        const uint32_t nan = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                                        if (!on) x = 0;
-                                        else if (part_seen && nan) {
-                                            x &= ~(nan * 0xffu);
-                                            *odd = 1;
-                                        }
-                                    };
-                                    fix(w[k].x), fix(w[k].y), fix(w[k].z), fix(w[k].w);
-                                }
-                            }
 #pragma unroll
                             for (int k = 0; k < EACH; ++k) {
-                                const int i = i0 + k * TEAM, row = i / wide, u = i % wide, panel = u / 4, unit = 2 * (u % 4);
+                                const int i = i0 + k * TEAM, row = i >> log, u = i & ((1 << log) - 1), panel = u / 4, unit = 2 * (u % 4);
                                 const uint4 h0 = make_uint4(e4m3_lo(w[k].x), e4m3_hi(w[k].x), e4m3_lo(w[k].y), e4m3_hi(w[k].y)),
                                             h1 = make_uint4(e4m3_lo(w[k].z), e4m3_hi(w[k].z), e4m3_lo(w[k].w), e4m3_hi(w[k].w));
                                 // odd panels store their second half first, so that a row's eight lanes
