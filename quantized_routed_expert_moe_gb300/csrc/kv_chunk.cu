@@ -288,6 +288,8 @@ __device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
 __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
+// The upper bit of every byte that is an e4m3 NaN (0x7f, 0xff): the sum carries into it.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ bool all_lanes(bool x) { return __all_sync(~0u, x) != 0; }
 
 __device__ __forceinline__ float max32(const float* x, float top) {
@@ -818,20 +820,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         // in place and apart: few stages need it, and the loop below stays short
                         if (__builtin_expect(look, 0)) {
 #pragma unroll 1
-                            for (int i = me; i < C::RAW / 16; i += TEAM) {
-                                uint4 w = ld_shared(raw + i * 16);
-                                const bool on = live(i >> log);
-                                auto fix = [&](uint32_t& x) {
-                                    // bytes of NaN (0x7f, 0xff): the sum carries into bit 7
-                                    const uint32_t nan = (((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
-                                    if (!on) x = 0;
-                                    else if (part_seen && nan) {
-                                        x &= ~(nan * 0xffu);
-                                        *odd = 1;
-                                    }
-                                };
-                                fix(w.x), fix(w.y), fix(w.z), fix(w.w);
-                                st_shared(raw + i * 16, w);
+                            for (int i0 = me; i0 < C::RAW / 16; i0 += 4 * TEAM) {
+                                uint32_t todo = 0;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int i = i0 + k * TEAM;
+                                    const uint4 w = ld_shared(raw + i * 16);
+                                    const bool on = live(i >> log);
+                                    if (!on) st_shared(raw + i * 16, make_uint4(0, 0, 0, 0));
+                                    if (on && (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w))) todo |= 1u << k;
+                                }
+#pragma unroll 1
+                                for (todo = part_seen ? todo : 0; todo; todo &= todo - 1) {
+                                    const uint32_t at = raw + (i0 + (__ffs(todo) - 1) * TEAM) * 16;
+                                    uint4 w = ld_shared(at);
+                                    w.x &= ~((nan_bytes(w.x) >> 7) * 0xffu);
+                                    w.y &= ~((nan_bytes(w.y) >> 7) * 0xffu);
+                                    w.z &= ~((nan_bytes(w.z) >> 7) * 0xffu);
+                                    w.w &= ~((nan_bytes(w.w) >> 7) * 0xffu);
+                                    st_shared(at, w);
+                                    *odd = 1;
+                                }
                             }
                         }
                         // four vectors' reads are on their way before the first is converted
@@ -871,17 +880,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                                 // exponents of ones carry into the sign's place
                                 auto high = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
                                 const uint32_t bad = (high(w[k].x) | high(w[k].y) | high(w[k].z) | high(w[k].w)) & 0x80008000u;
-                                if ((bad && part_seen) || !live((i0 + k * TEAM) / 8 % C::SR)) todo |= 1u << k;   // units stay in their row
+                                const bool on = live((i0 + k * TEAM) / 8 % C::SR);   // units stay in their row
+                                // (without a look at what is there: one at a time they take 7700 cycles a stage)
+                                if (!on) st_shared(stage + (i0 + k * TEAM) * 16, make_uint4(0, 0, 0, 0));
+                                if (on && bad && part_seen) todo |= 1u << k;
                             }
 #pragma unroll 1
                             for (; todo; todo &= todo - 1) {
                                 const int i = i0 + (__ffs(todo) - 1) * TEAM;
                                 const uint4 v = ld_shared(stage + i * 16);
                                 uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                                const bool on = live(i / 8 % C::SR);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
-                                    if (!on) x[e] = 0;
                                     if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u, *odd = 1;
                                     if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu, *odd = 1;
                                 }
