@@ -292,6 +292,24 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint4 v) {
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ bool all_lanes(bool x) { return __all_sync(~0u, x) != 0; }
 
+// v[c] of the row of this lane becomes v[r]: vector lane % 4 of the r-th row of its four lanes.
+__device__ __forceinline__ void turn4(uint4 (&v)[4], int lane) {
+    auto swap = [&](uint4& keep0, uint4& keep1, int by) {   // what the other lane gave comes back
+        uint32_t* const x = reinterpret_cast<uint32_t*>(&keep0);
+        uint32_t* const y = reinterpret_cast<uint32_t*>(&keep1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(~0u, lane & by ? x[e] : y[e], by);
+            if (lane & by) x[e] = got;
+            else y[e] = got;
+        }
+    };
+    swap(v[0], v[2], 2);
+    swap(v[1], v[3], 2);
+    swap(v[0], v[1], 1);
+    swap(v[2], v[3], 1);
+}
+
 __device__ __forceinline__ float max32(const float* x, float top) {
     float m[4] = {top, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -574,6 +592,16 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     sm.part[parts % kParts] = x;
                     bw::mbar_arrive(part_full + 8 * (parts % kParts));
                 }
+                // its queries on their way to the second-level cache while the part before it runs
+                if (parts && x.n > 0) {
+                    const int last = G.of(x.row0 + x.rows - 1);
+#pragma unroll 1
+                    for (int t = G.of(x.row0) + lane; t <= last; t += 32)
+                        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                         static_cast<const __nv_bfloat16*>(p.a.q) + (x.start + t) * p.a.q_stride + x.hk * G.d * D),
+                                     "r"(G.d * D * 2)
+                                     : "memory");
+                }
                 q = Piece{x.b, x.hk, x.lo, x.hi, x.blk0, x.n, x.gi};
             } else {
                 const volatile Part& x = take(parts);
@@ -819,21 +847,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         const int log = C::PARTS == 1 || !values ? KLOG : KLOG + 1;
                         // in place and apart: few stages need it, and the loop below stays short
                         if (__builtin_expect(look, 0)) {
+                            const int rows = TEAM >> log;   // of a step
 #pragma unroll 1
-                            for (int i0 = me; i0 < C::RAW / 16; i0 += 4 * TEAM) {
-                                uint32_t todo = 0;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    const int i = i0 + k * TEAM;
-                                    const uint4 w = ld_shared(raw + i * 16);
-                                    const bool on = live(i >> log);
-                                    if (!on) st_shared(raw + i * 16, make_uint4(0, 0, 0, 0));
-                                    if (on && (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w))) todo |= 1u << k;
-                                }
-#pragma unroll 1
-                                for (todo = part_seen ? todo : 0; todo; todo &= todo - 1) {
-                                    const uint32_t at = raw + (i0 + (__ffs(todo) - 1) * TEAM) * 16;
-                                    uint4 w = ld_shared(at);
+                            for (int r0 = 0; r0 < C::SR; r0 += rows) {
+                                if (p0 + r0 >= q.all_lo && p0 + r0 + rows <= q.all_hi && pages == (1u << G16) - 1) continue;
+                                const uint32_t at = raw + (r0 << log) * 16 + me * 16;
+                                uint4 w = ld_shared(at);
+                                const bool on = live(r0 + (me >> log));
+                                const bool nan = part_seen && (nan_bytes(w.x) | nan_bytes(w.y) | nan_bytes(w.z) | nan_bytes(w.w));
+                                if (!on) {
+                                    st_shared(at, make_uint4(0, 0, 0, 0));
+                                } else if (nan) {
                                     w.x &= ~((nan_bytes(w.x) >> 7) * 0xffu);
                                     w.y &= ~((nan_bytes(w.y) >> 7) * 0xffu);
                                     w.z &= ~((nan_bytes(w.z) >> 7) * 0xffu);
@@ -867,35 +891,35 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         __syncwarp();
                         if (lane == 0) bw::mbar_arrive(raw_free + 8 * in.stage);
                     } else if (look) {
-                        // eight vectors at a time: what needs no change, almost all of them, costs a
-                        // load and a few operations
+                        // sixteen rows at a time: those that all rows attend to need no look, and those
+                        // that none does no read (one vector after the other a stage takes 7700 cycles)
 #pragma unroll 1
-                        for (int i0 = me; i0 < C::STAGE / 16; i0 += 8 * TEAM) {
-                            uint4 w[8];
+                        for (int g = 0; g < G16; ++g) {
+                            const int first = p0 + 16 * g, at = first + me / 8;
+                            const bool here = pages >> g & 1;
+                            if (here && first >= q.all_lo && first + 16 <= q.all_hi) continue;
+                            const bool on = here && at >= q.lo && at < q.hi;
+                            uint4 w[D / 64];
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) w[k] = ld_shared(stage + (i0 + k * TEAM) * 16);
-                            uint32_t todo = 0;
+                            for (int k = 0; k < D / 64; ++k) w[k] = ld_shared(stage + k * C::PANEL + g * 2048 + me * 16);
 #pragma unroll
-                            for (int k = 0; k < 8; ++k) {
+                            for (int k = 0; k < D / 64; ++k) {
+                                const uint32_t to = stage + k * C::PANEL + g * 2048 + me * 16;
                                 // exponents of ones carry into the sign's place
                                 auto high = [](uint32_t x) { return (x & 0x7f807f80u) + 0x00800080u; };
                                 const uint32_t bad = (high(w[k].x) | high(w[k].y) | high(w[k].z) | high(w[k].w)) & 0x80008000u;
-                                const bool on = live((i0 + k * TEAM) / 8 % C::SR);   // units stay in their row
-                                // (without a look at what is there: one at a time they take 7700 cycles a stage)
-                                if (!on) st_shared(stage + (i0 + k * TEAM) * 16, make_uint4(0, 0, 0, 0));
-                                if (on && bad && part_seen) todo |= 1u << k;
-                            }
-#pragma unroll 1
-                            for (; todo; todo &= todo - 1) {
-                                const int i = i0 + (__ffs(todo) - 1) * TEAM;
-                                const uint4 v = ld_shared(stage + i * 16);
-                                uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                                if (!on) {
+                                    st_shared(to, make_uint4(0, 0, 0, 0));
+                                } else if (bad && part_seen) {
+                                    uint32_t* const x = reinterpret_cast<uint32_t*>(&w[k]);
 #pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u, *odd = 1;
-                                    if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu, *odd = 1;
+                                    for (int e = 0; e < 4; ++e) {
+                                        if ((x[e] & 0x7f80u) == 0x7f80u) x[e] &= 0xffff0000u;
+                                        if ((x[e] & 0x7f800000u) == 0x7f800000u) x[e] &= 0xffffu;
+                                    }
+                                    st_shared(to, w[k]);
+                                    *odd = 1;
                                 }
-                                st_shared(stage + i * 16, make_uint4(x[0], x[1], x[2], x[3]));
                             }
                         }
                         bw::fence_async_smem();
@@ -1012,10 +1036,12 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     pair_meets();
                     sum = sm.row_sum[0][row] + sm.row_sum[1][row];
                 }
+                const float of_values = p.v_scale[q.hk];
+                const int r = slot * 128 + row, pos = q.base + G.of(q.row0 + r);
+                const int64_t o_row = r < q.rows ? out_row(q, r) : -1;
                 ok = wait(o_last + 8 * slot, ended++) && ok;
                 if (!ok) break;
                 bw::tc_fence_after();
-                const int r = slot * 128 + row, pos = q.base + G.of(q.row0 + r);
                 const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
                 const bool cut = !(q.first && q.last), on = r < q.rows;
                 const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
@@ -1028,8 +1054,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
                 }
                 if (cut && on && ch0 == 0) p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(m, sum);
-                const float inv = sum == 0.f ? 0.f : p.v_scale[q.hk] / sum;
-                const int64_t o_row = on ? out_row(q, r) : 0;
+                const float inv = sum == 0.f ? 0.f : of_values / sum;
     #pragma unroll 1
                 for (int i = 0; i < OC; i += 32) {
                     uint32_t o[32];
@@ -1057,21 +1082,32 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             }
                         }
                     }
-                    if (cut && on) {
-                        float4* to = p.part_o + ((int64_t)rec * (D / 4) + (ch0 + i) / 4) * C::ROWS + r;
-    #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            to[k * C::ROWS] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
-                                                          __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
-                    } else if (on) {
-                        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o_row * D + ch0 + i);
-    #pragma unroll
+                    if (cut) {
+                        if (on) {
+                            float4* to = p.part_o + ((int64_t)rec * (D / 4) + (ch0 + i) / 4) * C::ROWS + r;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                to[k * C::ROWS] = make_float4(__uint_as_float(o[4 * k]), __uint_as_float(o[4 * k + 1]),
+                                                              __uint_as_float(o[4 * k + 2]), __uint_as_float(o[4 * k + 3]));
+                        }
+                    } else {
+                        // four lanes write 64 bytes of one row together: a lane per row is a line per
+                        // lane and store, 4100 cycles for a tile
+                        uint4 h[4];
+#pragma unroll
                         for (int k = 0; k < 4; ++k) {
-                            uint32_t h[4];
-    #pragma unroll
+                            uint32_t w[4];
+#pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                h[e] = pack2<false>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
-                            to[k] = make_uint4(h[0], h[1], h[2], h[3]);
+                                w[e] = pack2<false>(__uint_as_float(o[8 * k + 2 * e]) * inv, __uint_as_float(o[8 * k + 2 * e + 1]) * inv);
+                            h[k] = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        turn4(h, lane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int64_t to = __shfl_sync(~0u, o_row, (lane & ~3) + k);
+                            if (to >= 0)
+                                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + to * D + ch0 + i + lane % 4 * 8) = h[k];
                         }
                     }
                 }
@@ -1110,6 +1146,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     // scores are capped, and what this row does not attend to goes out, in place
 #pragma unroll 1
                     for (int c0 = 0; c0 < C::COLS; c0 += 32) {
+                        const bool some = edge && (at + c0 < all_lo || at + c0 + 32 > all_hi || *const_cast<volatile int*>(&sm.lost));
+                        if (!C::CAP && !some) continue;
                         uint32_t u[32];
                         float* const x = reinterpret_cast<float*>(u);
                         bw::tmem_ld32(s_at + c0, u);
@@ -1118,7 +1156,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                             for (int i = 0; i < 16; ++i) tanh_cap(x[2 * i], x[2 * i + 1], to_cap, cap);
                         }
-                        if (edge) {
+                        if (some) {
                             const int a = see0 - at - c0, b = see1 - at - c0;
                             const uint32_t two = in >> (c0 / 16);
 #pragma unroll
