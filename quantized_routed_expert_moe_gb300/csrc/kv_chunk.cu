@@ -36,10 +36,12 @@
 // joins in order.
 //
 // Measured (GB300; floors at 1932 TFLOP/s and 6.78 TB/s): a prompt of 8192 tokens, 48 heads
-// over 8 of 128, 735 us (1120 TFLOP/s, 58%); 8 x 800 tokens after 7200, 64 heads over 4, 1203
-// TFLOP/s (62%), in 8 bits 1013; 128 tokens after 32640 106 us (50%); 64 x 4 tokens after up to
-// 16380, pages of 16, 296 us (5.3 TB/s, 78%); 17 tokens 9.5 us, of which 3.5 us before the first
-// copy (lengths, the walk, the block table) and most of the rest instructions that run once.
+// over 8 of 128, 733 us (1125 TFLOP/s, 58%); 8 x 800 tokens after 7200, 64 heads over 4, 1190
+// TFLOP/s (62%), in 8 bits 1147; 128 tokens after 32640 106 us (50%); 64 x 4 tokens after up to
+// 16380, pages of 16, 296 us (5.3 TB/s, 78%); 32 ragged chunks in 8 bits 212 us (770 TFLOP/s); 8
+// chunks of 509 in windows of 1024, capped, heads of 256, 64 us; 17 tokens 9.0 us, of which 3.5
+// before the first copy (lengths, the walk, the block table) and most of the rest instructions
+// that run once.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -58,8 +60,9 @@ namespace {
 constexpr int kBlk = 128;              // cached tokens of a block
 constexpr int kRing = 16;              // blocks whose page flags are kept
 constexpr int kParts = 4;              // parts that the roles may be apart
-// What a tile's beginning and end cost, in blocks: a prompt of 8192 takes 1138, 930, 778, 730 and
-// 748 us with 1, 2, 3, 4 and 6, a batch in 8 bits 279, 259, 239, 228 and 229.
+// What a tile's beginning and end cost, in blocks: a prompt of 8192 takes 1047, 855, 727, 733, 743
+// and 753 us with 1 to 6, a batch in 8 bits 258, 236, 219, 212, 215 and 218. (About 10000 cycles:
+// the last block's edge 2500, the next tile's queries 3500, the outputs 4300; a block is 3800.)
 constexpr int kTileCost = 4;
 
 // Compile-time shape of one kernel: head dimension, cache type, capped scores.
