@@ -207,6 +207,21 @@ def test_later_values_that_are_not_finite():
         c.check()
 
 
+@pytest.mark.parametrize("window", [0, 40, 200])
+@pytest.mark.parametrize("D,dt", [(64, BF16), (128, BF16), (256, BF16), (64, E4M3), (128, E4M3), (256, E4M3)])
+def test_values_that_are_not_finite_on_either_side_of_groups(D, dt, window):
+    """The same at the ends of groups of 16 positions, of which some are seen by all rows of a tile,
+    some by a part of them and some by none, and with pages that end inside them."""
+    c = Case([(130, 400), (17, 33)], 6, 2, D, 48, dt, window=window, seed=D + window)
+    pool = c.v.view(torch.uint8) if dt == E4M3 else c.v
+    for i, p in enumerate((255, 256, 271, 272, 287, 288, 303, 319, 320, 335, 336, 352, 383, 384, 399)):
+        page, slot = int(c.table[0, p // 48]), p % 48
+        if window and p <= 400 - 130 - window:
+            continue   # no token sees it, its page may be none
+        pool[page, i % 2, slot, (7 * i) % D] = 0x7f if dt == E4M3 else (torch.inf, -torch.inf, torch.nan)[i % 3]
+    c.check()
+
+
 def test_later_keys_that_are_not_finite():
     for D, dt in ((128, BF16), (256, BF16), (64, E4M3)):
         c = Case([(10, 30), (130, 400)], 6, 2, D, 16, dt, seed=D)
