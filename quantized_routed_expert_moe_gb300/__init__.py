@@ -1099,9 +1099,9 @@ class KVCache:
         tokens are rows starts[b] to starts[b + 1] - 1), lens int32 [B] with the chunk
         counted, block_table int32 [B, max_pages], lse fp32 [T, n_heads] or None; scale
         defaults to 1 / sqrt(d). workspace: uint8, chunk_workspace_bytes or more, for example
-        one for all layers of a model; without it the object keeps one of its own from its
-        first call on, which is then not to be captured in a graph. stream: torch's current
-        one on the pools' device by default."""
+        one for all layers of a model, whose calls must not overlap on the GPU; without it the
+        object keeps one of its own from its first call on, a call that is then not to be captured
+        in a graph. stream: torch's current one on the pools' device by default."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
         if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
@@ -1124,7 +1124,7 @@ class KVCache:
         if workspace is None:
             workspace = self._workspace
             if workspace is None:
-                workspace = self._own_workspace()
+                workspace = self._own_workspace(stream)
         elif workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
         try:
@@ -1139,12 +1139,17 @@ class KVCache:
         if st:
             _check(st, "moe_kv_attend_chunk")
 
-    def _own_workspace(self):
+    def _own_workspace(self, stream):
+        """The object's own workspace, taken from the memory of the stream that its first call runs
+        on: what that stream still does with the memory's last owner comes before the call."""
         import torch
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("attend_chunk: the first call makes the workspace, which a graph capture cannot; pass "
-                               "workspace=, or call once before the capture")
-        self._workspace = torch.empty(self.chunk_workspace_bytes, dtype=torch.uint8, device=self.k_pages.device)
+        s = torch.cuda.ExternalStream(_stream_on(stream, self._current_stream, self.device), self.device)
+        capturing = torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(s):
+            if capturing or torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("attend_chunk: the first call makes the workspace, which a graph capture cannot; pass "
+                                   "workspace=, or call once before the capture")
+            self._workspace = torch.empty(self.chunk_workspace_bytes, dtype=torch.uint8, device=self.k_pages.device)
         return self._workspace
 
     def locate(self, block_table, seq: int, position: int, head: int = 0) -> int:
