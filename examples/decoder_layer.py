@@ -64,6 +64,7 @@ class DecoderLayer:
                               inv_freq=np.array([10000.0 ** (-2.0 * i / head_dim) for i in range(head_dim // 2)]))
         self.position = torch.zeros(1, dtype=torch.int32, device=device)
         self.length = torch.zeros(1, dtype=torch.int32, device=device)
+        self.one_chunk = torch.arange(2, dtype=torch.int32, device=device)   # times its tokens: where it starts and ends
         # buffers of a step: a caller that serves tokens allocates nothing
         self.h, self.h_mid, self.h_next = (torch.empty(1, H, device=device, dtype=bf16) for _ in range(3))
         self.q_rot, self.o = (torch.empty(1, n_heads, head_dim, device=device, dtype=bf16) for _ in range(2))
@@ -73,47 +74,48 @@ class DecoderLayer:
 
     def step(self, x, stream=None):
         """One token: x [1, H] fp32 residual, updated in place; returns the next layer's
-        input [1, H] bf16. Nothing is read back to the host."""
-        s = torch.cuda.current_stream() if stream is None else stream
-        self.length.add_(1)
-        self.first.run(x, h=self.h, stream=s)
-        self.qkv_proj.run(self.h, self.qkv, stream=s)
-        self.q, self.k, self.v = self.qkv.view(1, -1, self.d).split([self.heads, self.kv_heads, self.kv_heads], 1)
-        self.kv.append(self.q, self.k, self.v, self.position, self.table, self.q_rot, stream=s, q_norm=self.q_norm,
-                       k_norm=self.k_norm)
-        self.kv.attend(self.q_rot, self.table, self.length, self.o, stream=s)
-        self.o_proj.run(self.o.view(1, -1), self.attn, stream=s)
-        self.after_attention.run(x, self.attn, x, self.h_mid, stream=s)
-        self.experts.decode(self.h_mid, self.y, stream=s)
-        self.after_experts.run(x, self.y[None], x, self.h_next, stream=s)
-        self.position.add_(1)
+        input [1, H] bf16. Nothing is read back to the host. All of it runs on one stream,
+        torch's current one by default; x has to be ready there."""
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            self.length.add_(1)
+            self.first.run(x, h=self.h)
+            self.qkv_proj.run(self.h, self.qkv)
+            self.q, self.k, self.v = self.qkv.view(1, -1, self.d).split([self.heads, self.kv_heads, self.kv_heads], 1)
+            self.kv.append(self.q, self.k, self.v, self.position, self.table, self.q_rot, q_norm=self.q_norm,
+                           k_norm=self.k_norm)
+            self.kv.attend(self.q_rot, self.table, self.length, self.o)
+            self.o_proj.run(self.o.view(1, -1), self.attn)
+            self.after_attention.run(x, self.attn, x, self.h_mid)
+            self.experts.decode(self.h_mid, self.y, stream=torch.cuda.current_stream())
+            self.after_experts.run(x, self.y[None], x, self.h_next)
+            self.position.add_(1)
         return self.h_next
 
     def prefill(self, x, stream=None):
         """A chunk of a prompt, at most max_chunk tokens: x [T, H] fp32 residual, updated in
         place; returns the next layer's input [T, H] bf16. Chunks follow one another and come
-        before the steps that continue them."""
-        s = torch.cuda.current_stream() if stream is None else stream
-        T, H = x.shape
+        before the steps that continue them. As for a step, all of it runs on one stream,
+        without a host synchronisation; what it returns is that stream's."""
+        with torch.cuda.stream(torch.cuda.current_stream() if stream is None else stream):
+            T, H = x.shape
 
-        def new(*shape):
-            return torch.empty(*shape, device=x.device, dtype=torch.bfloat16)
-        h, h_mid, h_next, attn, y = (new(T, H) for _ in range(5))
-        qkv, q_rot, o = new(T, self.w_qkv.shape[0]), new(T, self.heads, self.d), new(T, self.heads, self.d)
-        positions = self.position + torch.arange(T, dtype=torch.int32, device=x.device)
-        starts = torch.tensor([0, T], dtype=torch.int32, device=x.device)
-        self.length.add_(T)
-        self.first.run(x, h=h, stream=s)
-        self.qkv_proj.run(h, qkv, stream=s)
-        q, k, v = qkv.view(T, -1, self.d).split([self.heads, self.kv_heads, self.kv_heads], 1)
-        self.kv.append(q, k, v, positions, self.table, q_rot, seq=torch.zeros_like(positions), stream=s,
-                       q_norm=self.q_norm, k_norm=self.k_norm)
-        self.kv.attend_chunk(q_rot, starts, self.table, self.length, o, stream=s)
-        self.o_proj.run(o.view(T, -1), attn, stream=s)
-        self.after_attention.run(x, attn, x, h_mid, stream=s)
-        self.experts.prefill_chunk(h_mid, T, y, stream=s)
-        self.after_experts.run(x, y, x, h_next, stream=s)
-        self.position.add_(T)
+            def new(*shape):
+                return torch.empty(*shape, device=x.device, dtype=torch.bfloat16)
+            h, h_mid, h_next, attn, y = (new(T, H) for _ in range(5))
+            qkv, q_rot, o = new(T, self.w_qkv.shape[0]), new(T, self.heads, self.d), new(T, self.heads, self.d)
+            positions = self.position + torch.arange(T, dtype=torch.int32, device=x.device)
+            self.length.add_(T)
+            self.first.run(x, h=h)
+            self.qkv_proj.run(h, qkv)
+            q, k, v = qkv.view(T, -1, self.d).split([self.heads, self.kv_heads, self.kv_heads], 1)
+            self.kv.append(q, k, v, positions, self.table, q_rot, seq=torch.zeros_like(positions), q_norm=self.q_norm,
+                           k_norm=self.k_norm)
+            self.kv.attend_chunk(q_rot, self.one_chunk * T, self.table, self.length, o)
+            self.o_proj.run(o.view(T, -1), attn)
+            self.after_attention.run(x, attn, x, h_mid)
+            self.experts.prefill_chunk(h_mid, T, y, stream=torch.cuda.current_stream())
+            self.after_experts.run(x, y, x, h_next)
+            self.position.add_(T)
         # what the chunk went through, for who wants to look
         self.chunk = dict(h=h, q=q, k=k, v=v, q_rot=q_rot, o=o, attn=attn, h_mid=h_mid, y=y)
         return h_next
