@@ -775,7 +775,8 @@ enum {
     MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
     MOE_KV_TIMEOUT = 8,     /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
                                out and lse whose cache did not arrive are NaN. Inside
-                               moe_kv_attend_chunk (0.4 s): rows of the call may hold anything */
+                               moe_kv_attend_chunk (0.4 s): so are the rows of the tokens and heads
+                               that the same SM had before and after them */
     MOE_KV_BAD_START = 16   /* chunk: starts decrease or leave 0..T; nothing was computed */
 };
 moe_status moe_kv_health(moe_kv* kv, uint32_t* bits);

@@ -359,6 +359,10 @@ struct Shared {
     Part part[kParts + 1];            // as the keys' copies go ahead; one of -1 blocks is the last, as is the one past them
     long long sums[C::WARPS];
     long long rem;                    // where this CTA's first tile starts, in units
+    struct {
+        long long left;
+        int b, i, hk, off;
+    } share;                          // where this CTA's walk begins
     uint32_t tmem;
     int abort, bad_start, first;
     int lost;                         // some page was not in the pool
@@ -521,6 +525,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         walk.window = p.a.window;
         walk.whole = p.whole;
         walk.index = walk.busy = walk.gi = 0;
+        if (threadIdx.x == 0) sm.share = {walk.left, walk.b, walk.i, walk.hk, walk.off};
         bw::fence_async_smem();   // `pre` lies where copies will land
         __syncthreads();
     }
@@ -529,7 +534,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     };
 
     // A wait that runs out sets sm.abort, which ends all others: a role then leaves, arrives nowhere
-    // any more (a barrier may have no arrivals left in its phase) and writes nothing shared.
+    // any more (a barrier may have no arrivals left in its phase) and writes nothing shared; the
+    // softmax warps fill the CTA's rows with NaN at their end.
     // The parts in their order: n is the reader's own count, and what it took it gives back.
     auto take = [&](uint32_t n) -> const volatile Part& {
         return sm.part[wait(part_full + 8 * (n % kParts), n / kParts) ? n % kParts : kParts];
@@ -1250,6 +1256,42 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 __syncwarp();
                 if (!ok) break;
                 if (lane == 0) bw::mbar_arrive(p_full + 8 * buf);
+            }
+        }
+        // After a wait that ran out the rows of all of this CTA's parts become NaN, by way of their
+        // sums where the tile is cut (some of them may be whole: which is not told).
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (*const_cast<volatile int*>(&sm.abort)) {
+            Walk<C> again{sm.start, sm.len, p.G};
+            again.left = sm.share.left;
+            again.b = sm.share.b, again.i = sm.share.i, again.hk = sm.share.hk, again.off = sm.share.off;
+            again.Hk = s.n_kv_heads;
+            again.window = p.a.window;
+            again.whole = p.whole;
+            again.index = again.busy = again.gi = 0;
+            Part q;
+#pragma unroll 1
+            while (again.next(q)) {
+                if (!q.n && !q.none) continue;
+                const bool cut = !(q.first && q.last);
+                const int side = q.index ? 1 : 0, rec = blockIdx.x * 2 + side;
+                const uint32_t fill = q.none ? 0 : 0x7fff7fffu;
+                if (cut && threadIdx.x == 0) {
+                    written |= 1u << side;
+                    p.recs[rec] = Rec{REC_CUT | (q.first ? REC_FIRST : 0) | (q.last ? REC_LAST : 0), q.rows, q.row0, q.start, q.hk, {}};
+                }
+#pragma unroll 1
+                for (int r = threadIdx.x; r < q.rows; r += 256) {
+                    if (cut) {
+                        p.part_ml[(int64_t)rec * C::ROWS + r] = make_float2(0.f, NAN);
+                        continue;
+                    }
+                    const int64_t o = out_row(q, r);
+                    uint4* const to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.a.out) + o * D);
+#pragma unroll 1
+                    for (int i = 0; i < D / 8; ++i) to[i] = make_uint4(fill, fill, fill, fill);
+                    if (p.a.lse) p.a.lse[o] = q.none ? -INFINITY : NAN;
+                }
             }
         }
         if (threadIdx.x == 0)
