@@ -574,8 +574,9 @@ typedef struct {
  *   x: bf16 [T][K]; w: bf16 [N][K]; bias: fp32 [N] or NULL; residual: [T][N] or
  *   NULL, may be y itself (with y's stride); y: [T][N], may not overlap any other input.
  * No host synchronisation, no scratch: calls on several streams are independent.
- * A row's result does not depend on the other rows of its call. (A bounded wait inside that
- * runs out, 0.4 s, leaves NaN.) Sums are taken in
+ * A row's result does not depend on the other rows of its call. (A wait inside is bounded by
+ * 2^18 tries, 0.4 s as measured; one that runs out leaves NaN in the outputs of its tiles and is told
+ * nowhere else: there is no handle and no health word.) Sums are taken in
  * an order that depends on T, N and K alone, so results are bit-reproducible.
  * Errors: MOE_E_INVALID, MOE_E_UNSUPPORTED (K or N above 2^20, T above 2^24), MOE_E_CUDA. */
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
@@ -775,7 +776,7 @@ enum {
     MOE_KV_BAD_PAGE = 4,    /* a page id outside the pool */
     MOE_KV_TIMEOUT = 8,     /* a bounded wait (0.25 s) inside moe_kv_attend ran out: the rows of
                                out and lse whose cache did not arrive are NaN. Inside
-                               moe_kv_attend_chunk (0.4 s): so are the rows of the tokens and heads
+                               moe_kv_attend_chunk (2^18 tries, 0.4 s as measured): so are the rows of the tokens and heads
                                that the same SM had before and after them */
     MOE_KV_BAD_START = 16   /* chunk: starts decrease or leave 0..T; nothing was computed */
 };

@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < PN; ++q) prefetch_2d(&tm_w, (k * PN + q) * kChunk, first % p.row_tiles * kRows);
     pdl_wait();      // nothing of the caller's is read before the preceding kernel is done
     pdl_trigger();
-    // a wait that runs out (0.35 s) sets s_abort, which ends the others: the CTA's outputs are NaN
+    // a wait that runs out (2^18 tries) sets s_abort, which ends the others: the CTA's outputs are NaN
     auto all = [](bool x) { return __all_sync(~0u, x) != 0; };
     auto wait = [&](uint32_t bar, uint32_t parity) { return bw::mbar_wait_short(bar, parity, &s_abort); };
 

@@ -9,8 +9,11 @@ namespace bw {
 
 // mbar_wait in a few instructions: a try that does not succeed suspends the warp, for 1.3 us as
 // measured (unless the phase completes: 106 cycles from the arrival), so that warps that wait
-// leave the issue slots and the instruction cache to those that work; 2^18 of them make the
-// limit, 0.35 s.
+// leave the issue slots and the instruction cache to those that work. The limit is a count, 2^18
+// tries, and no time: 0.35 s at 1.3 us, which is the machine's choice. (A look at the global timer
+// in this loop takes registers and instructions of every role: a batch of short chunks in 8 bits
+// 214 -> 223 us, windows with heads of 256 64 -> 66.) The longest wait of a call that gets on is that
+// of the tile of a pair that is not there, as long as the other's blocks: 1 ms for 100 000 tokens.
 __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, volatile int* abort) {
 #pragma unroll 1
     for (uint32_t n = 0; !mbar_try(bar, parity); ++n) {
