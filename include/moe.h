@@ -582,6 +582,15 @@ typedef struct {
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
                       const void* residual, void* y, int32_t T, int32_t device, void* stream);
 
+/* Options of the calling host thread's calls of moe_linear. */
+enum {
+    /* Test hook: the copies of this tile (of 128 output channels; the tiles of a call are
+     * numbered channels first) are not started (-1, the default: none is left out), so that
+     * the waits for them run out. */
+    MOE_LINEAR_OPT_TEST_STALL = 1
+};
+moe_status moe_linear_set_option(int32_t option, int64_t value);
+
 /* moe_linear's argument checks alone (host only, no device). */
 moe_status moe_linear_check(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
                             const void* residual, const void* y, int32_t T);

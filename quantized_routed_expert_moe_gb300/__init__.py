@@ -35,7 +35,7 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_expert_record_bytes", "
            "moe_layer_device_bytes", "moe_layer_set_next", "moe_layer_set_router_scoring", "moe_route", "moe_layer_selection", "moe_decode", "moe_decode_static_scratch", "moe_prefill_chunk",
            "moe_decode_tokens_host", "moe_cache_stage", "moe_cache_prefetch", "moe_cache_prefetch_stats", "moe_cache_stats", "moe_cache_residency", "moe_cache_usage", "moe_cache_pin", "moe_hottest", "moe_cache_pin_hottest", "moe_lfu_trace", "moe_lfu_trace_pinned",
            "moe_profile_start", "moe_profile_stop", "moe_layer_set_option", "moe_layer_check", "moe_trace_read_split",
-           "moe_block_norm", "moe_block_norm_check", "moe_linear", "moe_linear_check", "moe_kv_append_norm", "moe_kv_append_norm_check",
+           "moe_block_norm", "moe_block_norm_check", "moe_linear", "moe_linear_check", "moe_linear_set_option", "moe_kv_append_norm", "moe_kv_append_norm_check",
            "moe_kv_attend_chunk", "moe_kv_attend_chunk_check", "moe_kv_chunk_workspace", "moe_kv_create", "moe_kv_destroy", "moe_kv_device_bytes", "moe_kv_append", "moe_kv_attend",
            "moe_kv_append_check", "moe_kv_attend_check", "moe_kv_locate", "moe_kv_health", "moe_kv_set_option",
            "moe_status_str", "moe_last_error")
@@ -46,6 +46,7 @@ MOE_OPT_TEST_STALL_SHARED, MOE_OPT_TRACE = 2, 3
 MOE_OPT_HOST_TIMEOUT_MS, MOE_OPT_TEST_STALL_COPIES_MS, MOE_OPT_CACHE_DEVICE = 4, 5, 6
 MOE_MAX_TOP_K = 8
 MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT, MOE_KV_BAD_START = 1, 2, 4, 8, 16
+MOE_LINEAR_OPT_TEST_STALL = 1
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_SIGMOID = 0, 1, 2, 3
 MOE_KV_OPT_TEST_STALL = 1
 
@@ -233,6 +234,8 @@ def lib() -> ctypes.CDLL:
             L.moe_linear.argtypes = [ld, vp, vp, vp, vp, vp, i32, i32, vp]
             L.moe_linear_check.restype = st
             L.moe_linear_check.argtypes = [ld, vp, vp, vp, vp, vp, i32]
+            L.moe_linear_set_option.restype = st
+            L.moe_linear_set_option.argtypes = [i32, ctypes.c_int64]
             L.moe_kv_append_norm.restype = st
             L.moe_kv_append_norm.argtypes = [vp, ap, hn, vp]
             L.moe_kv_append_norm_check.restype = st
@@ -580,6 +583,11 @@ def moe_linear_check(desc, x, w, bias, residual, y, T) -> None:
     """The argument checks of moe_linear alone (host only)."""
     _check(lib().moe_linear_check(ctypes.byref(desc), _addr(x), _addr(w), _addr(bias), _addr(residual), _addr(y), T),
            "moe_linear_check")
+
+
+def moe_linear_set_option(option: int, value: int) -> None:
+    """Options of this host thread's calls of moe_linear (a test hook)."""
+    _check(lib().moe_linear_set_option(option, value), "moe_linear_set_option")
 
 
 def moe_kv_append_norm(handle, args: moe_kv_append_args, norm: moe_kv_head_norm, stream=None) -> None:

@@ -104,6 +104,7 @@ struct LinearArgs {
     int64_t y_stride, residual_stride;
     int T, K, N, out_f32, act;
     int row_tiles, tiles, splits;   // tiles: all of them, channels fastest; splits: CTAs of a cluster
+    int stall;                      // MOE_LINEAR_OPT_TEST_STALL
 };
 
 __device__ __forceinline__ void prefetch_2d(const CUtensorMap* tm, int x, int y) {
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint64_t stream = bw::l2_evict_first(), keep = bw::l2_evict_last();
             const uint64_t pol_w = p.tiles > p.row_tiles ? keep : stream;
-            uint32_t it = 0;
+            uint32_t it = 0, copied = 0;
             bool ok = true;
             for (int tile = first; tile < p.tiles && ok; tile += step) {
                 const int n0 = tile % p.row_tiles * kRows, t0 = tile / p.row_tiles * BN;
@@ -272,6 +273,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t s = it % S, at = ring + s * SB;
                     if (!(ok = wait(empty + 8 * s, ((it / S) & 1) ^ 1))) break;
                     bw::mbar_arrive_tx(full + 8 * s, SB);
+                    if (tile == p.stall) continue;
+                    copied = it + 1;
 #pragma unroll
                     for (int q = 0; q < PN; ++q) {
                         bw::tma_load_2d(at + q * W_PANEL, &tm_w, (k * PN + q) * kChunk, n0, full + 8 * s, pol_w);
@@ -281,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // no copy is in flight at the end, after a wait that ran out either
             int none = 0;
-            for (uint32_t q = it > (uint32_t)S ? it - S : 0; q < it; ++q)
+            for (uint32_t q = it > (uint32_t)S ? it - S : 0; q < copied; ++q)
                 bw::mbar_wait_short(full + 8 * (q % S), (q / S) & 1, &none);
         }
         // after a wait that ran out a copy may have landed on a split tile's sums
@@ -409,6 +412,7 @@ int set_up(int device) {
         if (cudaFuncSetAttribute(s.kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRing + 1024) != cudaSuccess) return 0;
     return sms;
 }
+thread_local int t_stall = -1;
 PerDevice g_sms, g_clusters[kMaxSplits + 1];
 
 // Clusters of n CTAs that the current device runs at once (every shape takes a whole SM per CTA).
@@ -447,7 +451,7 @@ cudaError_t launch(const moe_linear_desc& d, const void* x, const void* w, const
     const Shape* s = kShapes + (fine ? kFine : 0);
     while (s->BN < T && s->BN < (fine ? 128 : 256)) ++s;
     LinearArgs p{bias, residual, y, d.y_stride, d.residual_stride, T, d.in_features, d.out_features,
-                 d.out_dtype == MOE_F32, d.activation, 0, 0, 1};
+                 d.out_dtype == MOE_F32, d.activation, 0, 0, 1, t_stall};
     p.row_tiles = (p.N + kRows - 1) / kRows;
     const int64_t tiles = (int64_t)p.row_tiles * ((T + s->BN - 1) / s->BN);
     if (tiles > INT32_MAX) return cudaErrorInvalidValue;
@@ -491,6 +495,13 @@ extern "C" {
 moe_status moe_linear_check(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
                             const void* residual, const void* y, int32_t T) {
     return check_linear(desc, x, w, bias, residual, y, T);
+}
+
+moe_status moe_linear_set_option(int32_t option, int64_t value) {
+    if (option != MOE_LINEAR_OPT_TEST_STALL) return fail(MOE_E_INVALID, "unknown option");
+    if (value < -1 || value > INT32_MAX) return fail(MOE_E_INVALID, "a tile, or -1 for none");
+    t_stall = (int)value;
+    return MOE_OK;
 }
 
 moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
