@@ -572,7 +572,8 @@ typedef struct {
 /* One call over T >= 0 rows (T == 0 does nothing). All pointers are device memory
  * on `device`, 16-byte aligned.
  *   x: bf16 [T][K]; w: bf16 [N][K]; bias: fp32 [N] or NULL; residual: [T][N] or
- *   NULL, may be y itself (with y's stride); y: [T][N], may not overlap any other input.
+ *   NULL, may be y itself (with y's stride); y: [T][N], may not overlap any other input (refused;
+ *   columns of one buffer side by side do not overlap).
  * No host synchronisation, no scratch: calls on several streams are independent.
  * A row's result does not depend on the other rows of its call. (A wait inside is bounded by
  * 2^18 tries, 0.4 s as measured; one that runs out leaves NaN in the outputs of its tiles and is told
@@ -591,7 +592,7 @@ enum {
 };
 moe_status moe_linear_set_option(int32_t option, int64_t value);
 
-/* moe_linear's argument checks alone (host only, no device). */
+/* moe_linear's argument checks alone (host only, no device), but for the look at overlaps. */
 moe_status moe_linear_check(const moe_linear_desc* desc, const void* x, const void* w, const float* bias,
                             const void* residual, const void* y, int32_t T);
 
@@ -689,7 +690,8 @@ typedef struct {
  * each sequence, its chunk included (append the chunk first). Token i of a chunk of n
  * stands at position p = len - n + i, and attends to positions j <= p; window > 0: only
  * j > p - window. Scores, softcap, out ([T][n_heads][head_dim]) and lse ([T][n_heads])
- * are those of moe_kv_attend; neither may overlap an input or the workspace. A token at a
+ * are those of moe_kv_attend; neither may overlap an input or the workspace (refused, but for
+ * the pools, which are not looked at). A token at a
  * negative position (a chunk longer than its sequence's length) gives out = 0 and lse =
  * -inf. Rows outside starts[0]..starts[B] - 1 are left as they were. Cached values that a
  * token does not attend to do not change its result, whatever they hold, NaN included.
@@ -762,7 +764,7 @@ moe_status moe_kv_attend_chunk(moe_kv* kv, const moe_kv_chunk_args* args, void* 
 size_t moe_kv_chunk_workspace(const moe_kv* kv);
 
 /* The argument checks of the calls alone (host only, no device). The chunk's does not
- * look at the workspace's size, which depends on the device. */
+ * look at the workspace's size, which depends on the device, nor at overlaps. */
 moe_status moe_kv_append_norm_check(const moe_kv_desc* desc, const moe_kv_append_args* args,
                                     const moe_kv_head_norm* norm);
 moe_status moe_kv_attend_chunk_check(const moe_kv_desc* desc, const moe_kv_chunk_args* args);

@@ -12,6 +12,7 @@
 #include "common.cuh"
 #include "kv_cache.h"
 #include "moe_internal.h"
+#include "overlap.h"
 
 namespace moe {
 
@@ -148,6 +149,19 @@ moe_status check_chunk(const moe_kv_desc* d, const moe_kv_chunk_args* a) {
         return fail(MOE_E_INVALID, "q_stride must be a multiple of 8 and cover the heads");
     if ((int64_t)a->T * d->n_heads > INT32_MAX) return fail(MOE_E_UNSUPPORTED, "T * n_heads is 2^31 or more");
     return MOE_OK;
+}
+
+// Whether what a chunk call writes lies on something else of it (the pools are not looked at).
+bool chunk_overwrites(const moe_kv_desc& d, const moe_kv_chunk_args& a, int64_t workspace) {
+    const auto run = [](const void* at, int64_t bytes) { return Span{at, 1, bytes, bytes}; };
+    const int64_t heads = d.n_heads, row = heads * d.head_dim * 2;
+    const Span written[] = {run(a.out, a.T * row), run(a.lse, a.T * heads * 4), run(a.workspace, workspace)};
+    const Span read[] = {{a.q, a.T, row, a.q_stride * 2}, run(a.starts, (a.B + 1) * 4LL),
+                         run(a.block_table, (int64_t)a.B * a.max_pages * 4), run(a.lens, a.B * 4LL)};
+    for (const Span& w : written)
+        for (const Span& r : read)
+            if (overlap(w, r)) return true;
+    return overlap(written[0], written[1]) || overlap(written[0], written[2]) || overlap(written[1], written[2]);
 }
 
 // ---- append ---------------------------------------------------------------------
@@ -680,6 +694,8 @@ moe_status moe_kv_attend_chunk(moe_kv* kv, const moe_kv_chunk_args* args, void* 
     if (st != MOE_OK || args->B == 0 || args->T == 0) return st;
     if (args->workspace_bytes < 0 || (size_t)args->workspace_bytes < kv_chunk_workspace(K))
         return fail(MOE_E_INVALID, "workspace_bytes is below moe_kv_chunk_workspace");
+    if (chunk_overwrites(K.d, *args, (int64_t)kv_chunk_workspace(K)))
+        return fail(MOE_E_INVALID, "out, lse or the workspace overlaps another argument");
     DeviceGuard g(K.device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
     return kv_chunk_launch(K, *args, static_cast<cudaStream_t>(stream));

@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "moe_internal.h"
+#include "overlap.h"
 #include "per_device.h"
 #include "sm100_more.cuh"
 
@@ -60,6 +61,15 @@ moe_status check_linear(const moe_linear_desc* d, const void* x, const void* w, 
     if (residual == y && residual && d->residual_stride != d->y_stride)
         return fail(MOE_E_INVALID, "residual may be y only with y's stride");
     return MOE_OK;
+}
+
+// Other CTAs still read what a tile's outputs would overwrite.
+bool overwrites(const moe_linear_desc& d, const void* x, const void* w, const float* bias, const void* residual, const void* y,
+                int64_t T) {
+    const int64_t K = d.in_features, N = d.out_features, es = d.out_dtype == MOE_F32 ? 4 : 2;
+    const Span out{y, T, N * es, d.y_stride * es};
+    return overlap(out, {x, T, K * 2, d.x_stride * 2}) || overlap(out, {w, N, K * 2, d.w_stride * 2}) ||
+           overlap(out, {bias, 1, N * 4, N * 4}) || (residual != y && overlap(out, {residual, T, N * es, d.residual_stride * es}));
 }
 
 // 0.5 (1 + tanh u) = 1 / (1 + exp(-2 u)), so that every activation is z times a logistic, or
@@ -508,6 +518,8 @@ moe_status moe_linear(const moe_linear_desc* desc, const void* x, const void* w,
                       const void* residual, void* y, int32_t T, int32_t device, void* stream) {
     const moe_status st = check_linear(desc, x, w, bias, residual, y, T);
     if (st != MOE_OK || T == 0) return st;
+    if (overwrites(*desc, x, w, bias, residual, y, T))
+        return fail(MOE_E_INVALID, "y overlaps an input (residual may be y itself, with y's stride)");
     DeviceGuard g(device);
     if (!g.ok) return cuda_fail(g.err, "cudaSetDevice");
     const cudaError_t e = launch(*desc, x, w, bias, residual, y, T, device, static_cast<cudaStream_t>(stream));
