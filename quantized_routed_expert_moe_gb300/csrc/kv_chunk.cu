@@ -1067,6 +1067,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     #pragma unroll 1
                 for (int i = 0; i < OC; i += 32) {
                     uint32_t o[32];
+                    __syncwarp();   // lanes walk over rows and positions of their own
                     bw::tmem_ld32(o_at + i, o);
                     bw::tmem_wait_ld32(o);
                     if (odd && on) {
@@ -1260,6 +1261,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         // After a wait that ran out the rows of all of this CTA's parts become NaN, by way of their
         // sums where the tile is cut (some of them may be whole: which is not told).
+        __syncwarp();
         asm volatile("bar.sync 1, 256;" ::: "memory");
         if (*const_cast<volatile int*>(&sm.abort)) {
             Walk<C> again{sm.start, sm.len, p.G};
@@ -1303,6 +1305,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     __syncthreads();
     if (threadIdx.x == 0 && sm.abort) bits |= MOE_KV_TIMEOUT;
     if (bits) atomicOr(p.health, bits);
+    __syncwarp();
     if (warp == 8) {
         bw::tc_fence_after();
         bw::tmem_dealloc(tmem, 512);

@@ -376,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v[16];
                         bw::tmem_ld16(from + c, v);
                         if (n < p.N) finish16(p, t0 + c, cols - c, n, v, ok ? bias : NAN);
+                        __syncwarp();   // the next read of tensor memory is all lanes'
                     }
                 }
                 bw::tc_fence_before();
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (FINE && p.splits == 1) {
                 asm volatile("bar.sync 1, 128;" ::: "memory");
                 finish_shared(p, tile, BN, sums_at, 0, 1, 4);
+                __syncwarp();
                 asm volatile("bar.sync 1, 128;" ::: "memory");
             }
         }
@@ -393,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.splits > 1) {
         cluster_meet();
         finish_shared(p, first, BN, sums_at, split, p.splits, kThreads / 32);
+        __syncwarp();
         cluster_meet();   // no CTA leaves while its sums are read
     }
     bw::tc_fence_before();
