@@ -753,7 +753,7 @@ moe_status moe_kv_append_norm(moe_kv* kv, const moe_kv_append_args* args, const 
 /* Attention of a chunk of new tokens per sequence over the cache (formulas above):
  * products on the tensor cores, scores, softmax statistics and sums in fp32; a weight
  * enters the product with the values rounded once, to bf16 (bf16 cache: off by 2^-8 of
- * itself at most), or to fp16 (e4m3 cache: 2^-11, or 2^-32 of the largest).
+ * itself at most; MOE_KV_OPT_CHUNK_WEIGHTS keeps more), or to fp16 (e4m3 cache: 2^-11, or 2^-32 of the largest).
  * Lengths and starts are read on the device (no host synchronisation, capturable in a
  * graph). The work is split over the GPU by cached blocks and joined in a fixed order,
  * so results are bit-reproducible. A length past the block table is cut to it and an
@@ -798,7 +798,12 @@ enum {
     /* Test hook: moe_kv_attend and moe_kv_attend_chunk start no copies of this
      * sequence's cache (-1, the default: none is left out), so that the waits for
      * them run out. */
-    MOE_KV_OPT_TEST_STALL = 1
+    MOE_KV_OPT_TEST_STALL = 1,
+    /* As how many bf16 numbers a weight of moe_kv_attend_chunk over a bf16 cache enters the
+     * product with the values: 1 (the default; off by 2^-8 of itself at most) or 2 (2^-15, the
+     * bits of moe_kv_attend but one; half as many products again). An 8-bit cache's stay as
+     * they are. Calls from then on follow it, a captured one its capture. */
+    MOE_KV_OPT_CHUNK_WEIGHTS = 2
 };
 moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value);
 

@@ -47,6 +47,7 @@ MOE_OPT_HOST_TIMEOUT_MS, MOE_OPT_TEST_STALL_COPIES_MS, MOE_OPT_CACHE_DEVICE = 4,
 MOE_MAX_TOP_K = 8
 MOE_KV_BAD_SEQ, MOE_KV_BAD_LENGTH, MOE_KV_BAD_PAGE, MOE_KV_TIMEOUT, MOE_KV_BAD_START = 1, 2, 4, 8, 16
 MOE_LINEAR_OPT_TEST_STALL = 1
+MOE_KV_OPT_CHUNK_WEIGHTS = 2
 MOE_ACT_NONE, MOE_ACT_SILU, MOE_ACT_GELU_TANH, MOE_ACT_SIGMOID = 0, 1, 2, 3
 MOE_KV_OPT_TEST_STALL = 1
 

@@ -705,6 +705,11 @@ size_t moe_kv_chunk_workspace(const moe_kv* kv) { return kv ? kv_chunk_workspace
 
 moe_status moe_kv_set_option(moe_kv* kv, int32_t option, int64_t value) {
     if (!kv) return fail(MOE_E_INVALID, "NULL handle");
+    if (option == MOE_KV_OPT_CHUNK_WEIGHTS) {
+        if (value != 1 && value != 2) return fail(MOE_E_INVALID, "a weight is one number or two");
+        kv->K.chunk_fine = value == 2;
+        return MOE_OK;
+    }
     if (option != MOE_KV_OPT_TEST_STALL) return fail(MOE_E_INVALID, "unknown option");
     if (value < -1 || value >= kv->K.d.max_batch) return fail(MOE_E_INVALID, "a sequence, or -1 for none");
     kv->K.stall = (int)value;

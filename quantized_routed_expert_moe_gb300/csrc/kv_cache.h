@@ -58,6 +58,7 @@ struct Kv {
     CUtensorMap tm_chunk_k{}, tm_chunk_v{};
     int chunk_box = 16;          // tokens of one of their boxes
     int stall = -1;              // MOE_KV_OPT_TEST_STALL
+    bool chunk_fine = false;     // MOE_KV_OPT_CHUNK_WEIGHTS
     float4 *part_o = nullptr, *part_ml = nullptr;
     int* arrived = nullptr;
     void* block = nullptr;       // the allocation that holds all of the above

@@ -17,9 +17,12 @@
 //
 // Weights of a bf16 cache enter the second product rounded to bf16 (2^-8 of each at most; the
 // sum is taken before the rounding): outputs are 2.0e-3 to 2.3e-3 of their norm from 64 bits,
-// of which their own rounding to bf16 is 1.6e-3. A second bf16 number for the rest of a weight
-// would halve the rate of that product. Those of an 8-bit cache are fp16, in which its keys and
-// values are exact: 1.7e-3, all of it the output's own rounding.
+// of which their own rounding to bf16 is 1.6e-3. Where the handle asks for it (FINE,
+// MOE_KV_OPT_CHUNK_WEIGHTS) a second bf16 number holds what the first one left (2^-15), and the
+// outputs' own rounding is all: half as many products again, a prompt 733 -> 1020 us, 128 tokens
+// far into a document 108 -> 139, drafts 298 -> 433, windows with heads of 256 64 -> 68. Those of an
+// 8-bit cache are fp16, in which its keys and values are exact: 1.7e-3, all of it the output's own
+// rounding.
 //
 // Roles. Eight softmax warps; an issuing warp per tile (a wait behind issued products ends only
 // when those have left the queue); a warp that walks the CTA's parts for all roles and copies
@@ -65,11 +68,12 @@ constexpr int kParts = 4;              // parts that the roles may be apart
 // the last block's edge 2500, the next tile's queries 3500, the outputs 4300; a block is 3800.)
 constexpr int kTileCost = 4;
 
-// Compile-time shape of one kernel: head dimension, cache type, capped scores.
-template <int D_, bool FP8_, bool CAP_>
+// Compile-time shape of one kernel: head dimension, cache type, capped scores, weights as two
+// numbers.
+template <int D_, bool FP8_, bool CAP_, bool FINE_ = false>
 struct Cfg {
     static constexpr int D = D_;
-    static constexpr bool FP8 = FP8_, CAP = CAP_;
+    static constexpr bool FP8 = FP8_, CAP = CAP_, FINE = FINE_;
     static constexpr int NS = D == 256 ? 1 : 2;          // row tiles in flight
     static constexpr int ROWS = 128 * NS;
     // A block of keys or values of heads of 256 takes two stages: values by tokens, keys by
@@ -280,6 +284,19 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     }
+}
+// Two weights, neither negative, as two bf16 numbers each: their upper 16 bits, and what those
+// leave, rounded (2^-8 of 2^-7 of the weight). 2^-20 of the weight is added to that, so that it is
+// not zero where the weight is not: an infinite value times either has the same sign.
+__device__ __forceinline__ void split2(float a, float b, uint32_t& upper, uint32_t& rest) {
+    upper = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+    const float ma = __uint_as_float((__float_as_uint(a) & 0xffff0000u) | 0x80000000u);
+    const float mb = __uint_as_float((__float_as_uint(b) & 0xffff0000u) | 0x80000000u);
+    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %4};"
+        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
+        : "+f"(a), "+f"(b)
+        : "f"(1.f + 0x1p-20f), "f"(ma), "f"(mb));
+    rest = pack2<false>(a, b);
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -711,6 +728,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const uint64_t b = bw::desc_sw128_mn(stages + stage * C::STAGE, C::PANEL);
 #pragma unroll
                 for (int k = 0; k < C::SR / 16; ++k) bw::mma_f16_ta(to, weights + 8 * k, b + k * (2048 / 16), id_pv, more || k > 0);
+                if constexpr (C::FINE)
+#pragma unroll
+                    for (int k = 0; k < C::SR / 16; ++k) bw::mma_f16_ta(to, weights + C::COLS / 2 + 8 * k, b + k * (2048 / 16), id_pv, true);
             }
             __syncwarp();
         };
@@ -1240,17 +1260,23 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     float* const x = reinterpret_cast<float*>(u[c0 / 32]);
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) fma2(x[i], x[i + 1], times, plus);
-                    uint32_t w[16];
+                    uint32_t w[16], rest[C::FINE ? 16 : 1];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[i + k] = ex2(x[i + k]);
                         add2(l[0], l[1], x[i], x[i + 1]);
                         add2(l[2], l[3], x[i + 2], x[i + 3]);
-                        w[i / 2] = pack2<C::FP8>(x[i], x[i + 1]);
-                        w[i / 2 + 1] = pack2<C::FP8>(x[i + 2], x[i + 3]);
+                        if constexpr (C::FINE) {
+                            split2(x[i], x[i + 1], w[i / 2], rest[i / 2]);
+                            split2(x[i + 2], x[i + 3], w[i / 2 + 1], rest[i / 2 + 1]);
+                        } else {
+                            w[i / 2] = pack2<C::FP8>(x[i], x[i + 1]);
+                            w[i / 2 + 1] = pack2<C::FP8>(x[i + 2], x[i + 3]);
+                        }
                     }
                     bw::tmem_st16(s_at + c0 / 2, w);   // over scores that have been read
+                    if constexpr (C::FINE) bw::tmem_st16(s_at + C::COLS / 2 + c0 / 2, rest);
                 }
                 bw::tmem_wait_st();
                 bw::tc_fence_before();
@@ -1366,13 +1392,18 @@ __global__ void __launch_bounds__(256) k_kv_chunk_join(const ChunkArgs p, int ct
     }
 }
 
-// The kernel of a cache and of capped or plain scores.
+// The kernel of a cache, of capped or plain scores, and of weights as one number or two.
 template <class F>
-auto pick(const KvShape& s, bool cap, F f) {
+auto pick(const KvShape& s, bool cap, bool fine, F f) {
     if (s.e4m3) {
         if (s.head_dim == 64) return cap ? f(Cfg<64, true, true>{}) : f(Cfg<64, true, false>{});
         if (s.head_dim == 128) return cap ? f(Cfg<128, true, true>{}) : f(Cfg<128, true, false>{});
         return cap ? f(Cfg<256, true, true>{}) : f(Cfg<256, true, false>{});
+    }
+    if (fine) {
+        if (s.head_dim == 64) return cap ? f(Cfg<64, false, true, true>{}) : f(Cfg<64, false, false, true>{});
+        if (s.head_dim == 128) return cap ? f(Cfg<128, false, true, true>{}) : f(Cfg<128, false, false, true>{});
+        return cap ? f(Cfg<256, false, true, true>{}) : f(Cfg<256, false, false, true>{});
     }
     if (s.head_dim == 64) return cap ? f(Cfg<64, false, true>{}) : f(Cfg<64, false, false>{});
     if (s.head_dim == 128) return cap ? f(Cfg<128, false, true>{}) : f(Cfg<128, false, false>{});
@@ -1383,7 +1414,7 @@ struct Space {
     size_t recs, ml, o;   // bytes, each a multiple of 256
 };
 Space space_of(const Kv& K) {
-    const int rows = pick(K.s, false, [](auto c) { return decltype(c)::ROWS; });
+    const int rows = pick(K.s, false, false, [](auto c) { return decltype(c)::ROWS; });
     const size_t n = (size_t)K.num_sms * 2;
     return {(n * sizeof(Rec) + 255) / 256 * 256, n * rows * sizeof(float2), n * rows * K.s.head_dim * 4};
 }
@@ -1396,7 +1427,7 @@ size_t kv_chunk_workspace(const Kv& K) {
 }
 
 cudaError_t kv_chunk_setup(Kv& K) {
-    const int sr = pick(K.s, false, [](auto c) { return decltype(c)::SR; });
+    const int sr = pick(K.s, false, false, [](auto c) { return decltype(c)::SR; });
     K.chunk_box = 16;
     while (K.chunk_box * 2 <= sr && K.s.page_size % (K.chunk_box * 2) == 0) K.chunk_box *= 2;
     const auto encode = tensor_map_encoder();
@@ -1407,7 +1438,7 @@ cudaError_t kv_chunk_setup(Kv& K) {
     const cuuint64_t strides[3] = {(cuuint64_t)K.s.token_stride * es, (cuuint64_t)K.s.head_stride * es,
                                    (cuuint64_t)K.s.page_stride * es};
     const cuuint32_t ones[4] = {1, 1, 1, 1};
-    const int key_width = pick(K.s, false, [](auto c) { return decltype(c)::KD; });
+    const int key_width = pick(K.s, false, false, [](auto c) { return decltype(c)::KD; });
     for (int i = 0; i < 2; ++i) {
         const cuuint32_t box[4] = {(cuuint32_t)(!K.s.e4m3 ? 64 : i ? K.s.head_dim : key_width), (cuuint32_t)K.chunk_box, 1, 1};
         if (encode(i ? &K.tm_chunk_v : &K.tm_chunk_k, K.s.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -1416,8 +1447,8 @@ cudaError_t kv_chunk_setup(Kv& K) {
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    for (const bool cap : {false, true}) {
-        const cudaError_t e = pick(K.s, cap, [](auto c) {
+    for (const int i : {0, 1, 2, 3}) {
+        const cudaError_t e = pick(K.s, i & 1, i & 2, [](auto c) {
             using C = decltype(c);
             return cudaFuncSetAttribute(k_kv_chunk<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem);
         });
@@ -1438,7 +1469,7 @@ moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t strea
     p.whole = a.max_pages * K.s.page_size <= 4 * kBlk;
     // changes no score below 2^68, and a score's share of it would lose bits
     const bool cap = a.softcap > 0.f && a.softcap < 0x1p80f;
-    const cudaError_t e = pick(K.s, cap, [&](auto c) {
+    const cudaError_t e = pick(K.s, cap, K.chunk_fine, [&](auto c) {
         using C = decltype(c);
         const cudaError_t e = launch_pdl(k_kv_chunk<C>, dim3(K.num_sms), dim3(C::THREADS), C::smem, stream, true, p,
                                          K.tm_chunk_k, K.tm_chunk_v);
