@@ -690,7 +690,7 @@ typedef struct {
  * each sequence, its chunk included (append the chunk first). Token i of a chunk of n
  * stands at position p = len - n + i, and attends to positions j <= p; window > 0: only
  * j > p - window. Scores, softcap, out ([T][n_heads][head_dim]) and lse ([T][n_heads])
- * are those of moe_kv_attend; neither may overlap an input or the workspace (refused, but for
+ * are those of moe_kv_attend (a softcap of 2^126 |scale| or more counts as none too); neither may overlap an input or the workspace (refused, but for
  * the pools, which are not looked at). A token at a
  * negative position (a chunk longer than its sequence's length) gives out = 0 and lse =
  * -inf. Rows outside starts[0]..starts[B] - 1 are left as they were. Cached values that a

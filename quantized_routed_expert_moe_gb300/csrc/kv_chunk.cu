@@ -49,6 +49,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "common.cuh"
 #include "kv_cache.h"
@@ -1155,7 +1156,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             at_part = parts++;
             const float c = C::CAP ? 1.f : c_next * kLog2e;
-            const float to_cap = C::CAP ? c_next / p.a.softcap : 0.f, cap = p.a.softcap * kLog2e;
+            // (no quotient past fp32's range, which would make NaN of a score of zero; one near its end
+            // has few bits: an 8-bit cache's sums are below 2^32, and tanh z is z by far)
+            float to_cap = C::CAP ? fminf(c_next / p.a.softcap, 0x1.fffffep127f) : 0.f, cap = p.a.softcap * kLog2e;
+            if (C::CAP && C::FP8 && to_cap < 0x1p-100f) {
+                to_cap = 0x1p-100f;
+                cap = c_next * 0x1p100f * kLog2e;
+            }
             const int pos = v.base + G.of(v.row0 + slot * 128 + row);
             const int see0 = Walk<C>::first_seen(pos, p.a.window), see1 = pos + 1;
             const int n = v.n, blk0 = v.blk0, all_lo = v.all_lo, all_hi = v.all_hi;
@@ -1467,8 +1474,9 @@ moe_status kv_chunk_launch(Kv& K, const moe_kv_chunk_args& a, cudaStream_t strea
     if (p.a.window >= a.max_pages * K.s.page_size) p.a.window = 0;
     // Up to four blocks of a sequence, a CTA does a tile in less time than the second launch takes.
     p.whole = a.max_pages * K.s.page_size <= 4 * kBlk;
-    // changes no score below 2^68, and a score's share of it would lose bits
-    const bool cap = a.softcap > 0.f && a.softcap < 0x1p80f;
+    // A cap of 2^80 changes no score below 2^68, one of 2^126 times the scale none of products
+    // below 2^114; a score's share of it would lose bits, or all.
+    const bool cap = a.softcap > 0.f && a.softcap < 0x1p80f && a.softcap * 0x1p-126 < std::fabs((double)a.scale);
     const cudaError_t e = pick(K.s, cap, K.chunk_fine, [&](auto c) {
         using C = decltype(c);
         const cudaError_t e = launch_pdl(k_kv_chunk<C>, dim3(K.num_sms), dim3(C::THREADS), C::smem, stream, true, p,
