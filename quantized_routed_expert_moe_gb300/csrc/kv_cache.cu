@@ -11,6 +11,7 @@
 
 #include "common.cuh"
 #include "kv_cache.h"
+#include "kv_math.cuh"
 #include "moe_internal.h"
 #include "overlap.h"
 
@@ -180,26 +181,6 @@ bool chunk_overwrites(const moe_kv_desc& d, const moe_kv_chunk_args& a, int64_t 
 
 __device__ __forceinline__ float2 unpack2(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pack2(float2 v) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(v.x, v.y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-// x * y + z of both halves
-__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
-    float2 d;
-    asm("{.reg .b64 a, b, c; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mov.b64 c, {%6, %7};"
-        " fma.rn.f32x2 a, a, b, c; mov.b64 {%0, %1}, a;}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
-    return d;
-}
-__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
-    float2 d;
-    asm("{.reg .b64 a, b; mov.b64 a, {%2, %3}; mov.b64 b, {%4, %5}; mul.rn.f32x2 a, a, b; mov.b64 {%0, %1}, a;}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
-    return d;
 }
 // e4m3 of two values / scale, saturating, NaN stays NaN; inv = 1 / scale, rounded. The
 // product with inv is off by 2^-23, which takes the wrong neighbour where the quotient is
@@ -416,8 +397,8 @@ __global__ void __launch_bounds__(256, 3) k_kv_append(const AppendArgs p) {
                         e[0][x / 2] |= quant2(a, scale.x, scale.y) << 16 * (x % 2);
                         e[1][x / 2] |= quant2(b, scale.x, scale.y) << 16 * (x % 2);
                     } else {
-                        if (NORM || t0) w[0][x] = pack2(a);
-                        if (NORM || t1) w[1][x] = pack2(b);
+                        if (NORM || t0) w[0][x] = pack_bf16(a.x, a.y);
+                        if (NORM || t1) w[1][x] = pack_bf16(b.x, b.y);
                     }
                     if (!NORM && is_q && pos < 0) w[0][x] = w[1][x] = 0;
                 };

@@ -232,49 +232,21 @@ __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.al
 template <int N>
 __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// x * y + z of both halves
-__device__ __forceinline__ void fma2(float& a, float& b, float y, float z) {
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %3};"
-        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
-        : "+f"(a), "+f"(b)
-        : "f"(y), "f"(z));
-}
-__device__ __forceinline__ void add2(float& a, float& b, float y, float z) {
-    asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; add.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
-        : "+f"(a), "+f"(b)
-        : "f"(y), "f"(z));
-}
-__device__ __forceinline__ void mul2(float& a, float& b, float y, float z) {
-    asm("{.reg .b64 x, y; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mul.rn.f32x2 x, x, y; mov.b64 {%0, %1}, x;}"
-        : "+f"(a), "+f"(b)
-        : "f"(y), "f"(z));
-}
-// a = a * b + c of both halves
-__device__ __forceinline__ void fma22(float& a0, float& a1, float b0, float b1, float c) {
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %3}; mov.b64 z, {%4, %4};"
-        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
-        : "+f"(a0), "+f"(a1)
-        : "f"(b0), "f"(b1), "f"(c));
-}
+// the same of two numbers by one, in place
+__device__ __forceinline__ void put2(float& a, float& b, float2 v) { a = v.x, b = v.y; }
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ void fma_in(float& a, float& b, float y, float z) { put2(a, b, fma2(make_float2(a, b), both(y), both(z))); }
+__device__ __forceinline__ void add_in(float& a, float& b, float y, float z) { put2(a, b, add2(make_float2(a, b), make_float2(y, z))); }
 // cap tanh(k x) of two scores, as tanh_of has it, on both sides and without a branch: scores lie
 // on either.
 __device__ __forceinline__ void tanh_cap(float& x0, float& x1, float k, float cap) {
-    mul2(x0, x1, k, k);
-    float u0 = x0, u1 = x1, n0 = 0.0172414916f, n1 = 0.0172414916f, e0 = x0, e1 = x1;
-    mul2(u0, u1, x0, x1);
-    fma22(n0, n1, u0, u1, -0.0530454943f);
-    fma22(n0, n1, u0, u1, 0.13325879f);
-    fma22(n0, n1, u0, u1, -0.333331439f);
-    fma22(n0, n1, u0, u1, 1.f);
-    mul2(n0, n1, x0, x1);
-    mul2(e0, e1, 2.f * kLog2e, 2.f * kLog2e);
-    e0 = ex2(e0), e1 = ex2(e1);
-    add2(e0, e1, 1.f, 1.f);
-    e0 = rcp(e0), e1 = rcp(e1);
-    fma2(e0, e1, -2.f, 1.f);
-    x0 = fabsf(x0) > 0.5f ? e0 : n0;
-    x1 = fabsf(x1) > 0.5f ? e1 : n1;
-    mul2(x0, x1, cap, cap);
+    const float2 x = mul2(make_float2(x0, x1), both(k)), u = mul2(x, x);
+    float2 n = fma2(fma2(fma2(fma2(both(kTanh9), u, both(kTanh7)), u, both(kTanh5)), u, both(kTanh3)), u, both(1.f));
+    n = mul2(n, x);
+    float2 e = mul2(x, both(2.f * kLog2e));
+    e = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
+    e = fma2(make_float2(rcp(e.x), rcp(e.y)), both(-2.f), both(1.f));
+    put2(x0, x1, mul2(make_float2(fabsf(x.x) > 0.5f ? e.x : n.x, fabsf(x.y) > 0.5f ? e.y : n.y), both(cap)));
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -282,8 +254,7 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
         const __half2 h = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&h);
     } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&h);
+        return pack_bf16(lo, hi);
     }
 }
 // Two weights, neither negative, as two bf16 numbers each: their upper 16 bits, and what those
@@ -291,13 +262,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // not zero where the weight is not: an infinite value times either has the same sign.
 __device__ __forceinline__ void split2(float a, float b, uint32_t& upper, uint32_t& rest) {
     upper = __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-    const float ma = __uint_as_float((__float_as_uint(a) & 0xffff0000u) | 0x80000000u);
-    const float mb = __uint_as_float((__float_as_uint(b) & 0xffff0000u) | 0x80000000u);
-    asm("{.reg .b64 x, y, z; mov.b64 x, {%0, %1}; mov.b64 y, {%2, %2}; mov.b64 z, {%3, %4};"
-        " fma.rn.f32x2 x, x, y, z; mov.b64 {%0, %1}, x;}"
-        : "+f"(a), "+f"(b)
-        : "f"(1.f + 0x1p-20f), "f"(ma), "f"(mb));
-    rest = pack2<false>(a, b);
+    auto minus = [](float x) { return __uint_as_float((__float_as_uint(x) & 0xffff0000u) | 0x80000000u); };   // its upper bits
+    const float2 left = fma2(make_float2(a, b), both(1.f + 0x1p-20f), make_float2(minus(a), minus(b)));
+    rest = pack_bf16(left.x, left.y);
 }
 __device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
@@ -1266,14 +1233,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 for (int c0 = 0; c0 < C::COLS; c0 += 32) {
                     float* const x = reinterpret_cast<float*>(u[c0 / 32]);
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) fma2(x[i], x[i + 1], times, plus);
+                    for (int i = 0; i < 32; i += 2) fma_in(x[i], x[i + 1], times, plus);
                     uint32_t w[16], rest[C::FINE ? 16 : 1];
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) x[i + k] = ex2(x[i + k]);
-                        add2(l[0], l[1], x[i], x[i + 1]);
-                        add2(l[2], l[3], x[i + 2], x[i + 3]);
+                        add_in(l[0], l[1], x[i], x[i + 1]);
+                        add_in(l[2], l[3], x[i + 2], x[i + 3]);
                         if constexpr (C::FINE) {
                             split2(x[i], x[i + 1], w[i / 2], rest[i / 2]);
                             split2(x[i + 2], x[i + 3], w[i / 2 + 1], rest[i / 2 + 1]);
