@@ -67,6 +67,10 @@ constexpr int kParts = 4;              // parts that the roles may be apart
 // What a tile's beginning and end cost, in blocks: a prompt of 8192 takes 1047, 855, 727, 733, 743
 // and 753 us with 1 to 6, a batch in 8 bits 258, 236, 219, 212, 215 and 218. (About 10000 cycles:
 // the last block's edge 2500, the next tile's queries 3500, the outputs 4300; a block is 3800.)
+// Other heads have other blocks and other ends, in much the same proportion: with 1, 2, 3, 4, 6 and
+// 8 a prompt of 8192 takes 529, 431, 392, 395, 408 and 416 on 32/8 heads of 64, 604, 498, 447, 451, 462
+// and 471 on 16/8 of 256, 1221, 1024, 868, 795, 802 and 809 on 48/8 of 128 in 8 bits; windows of heads of
+// 256 60, 56, 57, 57, 59 and 60. Four is within 2% of the best of each.
 constexpr int kTileCost = 4;
 
 // Compile-time shape of one kernel: head dimension, cache type, capped scores, weights as two
