@@ -1317,20 +1317,29 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 }
 
 // Joins the parts of the tiles that were cut between CTAs, in order: a CTA per CTA that began
-// such a tile and 32 of its rows, a lane per row, four channels at a time.
+// such a tile and 32 of its rows, a lane per row, four channels at a time. A record is followed only
+// to rows that the call has: one that another call, on the same workspace at the same time, wrote
+// over it names rows of its own.
 template <class C>
 __global__ void __launch_bounds__(256) k_kv_chunk_join(const ChunkArgs p, int ctas) {
     constexpr int D = C::D, V = D / 32;   // vectors of four channels of a thread
     __shared__ int sm_last;
+    __shared__ Rec sm_rec;
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, c0 = blockIdx.x, r = blockIdx.y * 32 + lane;
     pdl_wait();
     pdl_trigger();
     for (int side = 0; side < 2; ++side) {
-        const Rec rec = p.recs[c0 * 2 + side];
-        if ((rec.flags & (REC_CUT | REC_FIRST)) != (REC_CUT | REC_FIRST) || blockIdx.y * 32 >= rec.rows) continue;
         __syncthreads();
-        if (threadIdx.x == 0) sm_last = ctas - 1;
+        if (threadIdx.x == 0) {
+            sm_rec = p.recs[c0 * 2 + side];
+            sm_last = ctas - 1;
+        }
         __syncthreads();
+        const Rec rec = sm_rec;
+        if ((rec.flags & (REC_CUT | REC_FIRST)) != (REC_CUT | REC_FIRST) || (int)blockIdx.y * 32 >= rec.rows) continue;
+        if (rec.rows > C::ROWS || (unsigned)rec.hk >= (unsigned)p.s.n_kv_heads || rec.start < 0 || rec.row0 < 0 ||
+            rec.row0 > INT32_MAX - C::ROWS || rec.start >= p.a.T - p.G.of(rec.row0 + rec.rows - 1))
+            continue;
         for (int k = c0 + 1 + threadIdx.x; k < ctas; k += 256)
             if ((p.recs[k * 2].flags & (REC_CUT | REC_FIRST | REC_LAST)) == (REC_CUT | REC_LAST)) {
                 atomicMin(&sm_last, k);
