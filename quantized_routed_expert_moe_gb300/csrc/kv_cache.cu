@@ -224,7 +224,7 @@ constexpr int kAppendRing = 8 * kAhead * 1024;   // of a CTA's warps
 // With NORM the D / 16 lanes of a head sum its squares (values and, where a norm is not
 // asked for, its heads go through unchanged); the weights lie in shared memory with their
 // offset, fours of channels so that the lanes of a head meet no bank twice. Bound by
-// instructions, 390 to a round (73% of the issue slots): 8192 tokens of 48 + 8 + 8 heads of 128
+// instructions, 389 to a round into 8 bits (72% of the issue slots): 8192 tokens of 48 + 8 + 8 heads of 128
 // take 53 us (75% of the copy rate; without norms 43), into 8 bits 58.6 us; one token 3.0 us.
 // With the head's sixteen channels unpacked once, then scaled, turned and rounded in steps of
 // their own: 58.6; all three pair by pair, with a branch each, 66.4; before that, weights read by

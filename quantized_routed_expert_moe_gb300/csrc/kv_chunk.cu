@@ -20,7 +20,7 @@
 // of which their own rounding to bf16 is 1.6e-3. Where the handle asks for it (FINE,
 // MOE_KV_OPT_CHUNK_WEIGHTS) a second bf16 number holds what the first one left (2^-15), and the
 // outputs' own rounding is all: half as many products again, a prompt 733 -> 1020 us, 128 tokens
-// far into a document 108 -> 139, drafts 298 -> 433, windows with heads of 256 64 -> 68. Those of an
+// far into a document 107 -> 139, drafts 298 -> 433, windows with heads of 256 64 -> 68. Those of an
 // 8-bit cache are fp16, in which its keys and values are exact: 1.7e-3, all of it the output's own
 // rounding.
 //
@@ -38,13 +38,14 @@
 // cut between CTAs leaves unnormalised parts in the workspace, which a second, small launch
 // joins in order.
 //
-// Measured (GB300; floors at 1932 TFLOP/s and 6.78 TB/s): a prompt of 8192 tokens, 48 heads
-// over 8 of 128, 733 us (1125 TFLOP/s, 58%); 8 x 800 tokens after 7200, 64 heads over 4, 1190
-// TFLOP/s (62%), in 8 bits 1147; 128 tokens after 32640 106 us (50%); 64 x 4 tokens after up to
-// 16380, pages of 16, 296 us (5.3 TB/s, 78%); 32 ragged chunks in 8 bits 212 us (770 TFLOP/s); 8
-// chunks of 509 in windows of 1024, capped, heads of 256, 64 us; 17 tokens 9.0 us, of which 3.5
-// before the first copy (lengths, the walk, the block table) and most of the rest instructions
-// that run once.
+// Measured (GB300; floors at 1897 TFLOP/s and 6.80 TB/s): a prompt of 8192 tokens, 48 heads
+// over 8 of 128, 733 us (1125 TFLOP/s, 59%), in 8 bits 796; 8 x 800 tokens after 7200, 64 heads over
+// 4, 1197 TFLOP/s (63%); 128 tokens after 32640 107 us (51%); 64 x 4 tokens after up to 16380, pages
+// of 16, 298 us (5.3 TB/s, 78%); 32 ragged chunks in 8 bits 212 us (774 TFLOP/s); 8 chunks of 509 in
+// windows of 1024, capped, heads of 256, 64 us; 17 tokens 8.7 us, of which 3.5 before the first copy
+// (lengths, the walk, the block table) and most of the rest instructions that run once, where the
+// block table holds 512 positions at most, and 11.6 with the second launch where it is wider.
+// Heads of 64 do half the operations for the same softmax: a prompt of 8192, 32 over 8, 395 us (37%).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

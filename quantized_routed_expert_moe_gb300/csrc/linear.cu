@@ -10,12 +10,13 @@
 // order. Many tokens: one CTA per SM takes tile after tile, the epilogue of one under the
 // products of the next (two accumulators in tensor memory).
 //
-// Measured (GB300; floors at 6.78 TB/s and 1932 TFLOP/s): one token 6144 x 8192 17.1 us (87% of
-// the copy rate), 512 x 768 3.6 us; 128 tokens 6144 x 6144 onto a fp32 residual 24.7 us (50%:
-// 48 tiles, two CTAs each, and 16 KB of weights per 372 cycles of products and 130 of waiting;
-// clusters of three do not all fit; in bf16 21 us); 8191 tokens 2816 x 8192 with gelu 247 us,
-// 1.53 PFLOP/s (79%: 48 KB of operands for 512 cycles of products come from the second-level
-// cache at 60 bytes a cycle and SM; a pair of CTAs on one tile would need two thirds).
+// Measured (GB300; floors at 6.80 TB/s and 1897 TFLOP/s): one token 6144 x 8192 17.1 us (87% of
+// the copy rate), 6144 x 6144 15.4 us (72%), 512 x 768 3.4 us; 128 tokens 6144 x 6144 onto a fp32
+// residual 24.9 us (49%: 48 tiles, two CTAs each, and 16 KB of weights per 372 cycles of products
+// and 130 of waiting; clusters of three do not all fit; in bf16 21 us), 300 54 us (25%); 8191 tokens
+// 2816 x 8192 with gelu 254 us, 1.49 PFLOP/s (78%: 48 KB of operands for 512 cycles of products come
+// from the second-level cache at 60 bytes a cycle and SM; a pair of CTAs on one tile would need two
+// thirds); 4096 tokens 6144 x 6144 232 us (70%), onto a fp32 residual 520 us (31%: tiles of 128).
 #include <cuda_bf16.h>
 
 #include <algorithm>
