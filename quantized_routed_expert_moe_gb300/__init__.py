@@ -944,7 +944,8 @@ class KVCache:
     """Owns one cache handle over two page pools, tensors [n_pages, n_kv_heads,
     page_size, head_dim] of bfloat16 or float8_e4m3fn in any memory order whose
     last dimension is contiguous (token-major pages: a permuted view). The handle is
-    bound to the pools' memory: pools that get new memory need a new object."""
+    bound to the pools' memory: pools that get new memory need a new object. One call at a
+    time, and calls of one object must not overlap on the GPU (other streams, replayed graphs)."""
 
     # moe_kv_append_args and moe_kv_attend_args, packed in place
     _append_args = struct.Struct("PPPqqqPPPiiiP")
@@ -1110,7 +1111,9 @@ class KVCache:
         defaults to 1 / sqrt(d). workspace: uint8, chunk_workspace_bytes or more, for example
         one for all layers of a model, whose calls must not overlap on the GPU; without it the
         object keeps one of its own from its first call on, a call that is then not to be captured
-        in a graph. stream: torch's current one on the pools' device by default."""
+        in a graph. stream: torch's current one on the pools' device by default.
+        set_option(MOE_KV_OPT_CHUNK_WEIGHTS, 2) keeps 15 bits of a weight over a bf16 cache, where
+        the default rounds it to bf16."""
         hq, _, d = self._heads
         dev, bf16, i32 = self.device, self._bf16, self._i32
         if self.k_pages.data_ptr() != self._k_at or self.v_pages.data_ptr() != self._v_at:
