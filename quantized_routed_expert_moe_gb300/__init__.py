@@ -914,7 +914,8 @@ class Linear:
 
     def run(self, x, y, residual=None, stream=None):
         """x [T, in_features] bf16, y [T, out_features] bf16 or fp32 the output, residual of y's
-        shape and type (may be y) or None. stream: torch's current one on x's device by default."""
+        shape and type (may be y) or None; y may lie on no other input. stream: torch's current one on
+        x's device by default."""
         K, N, bf16, dev = self.in_features, self.out_features, self._bf16, x.get_device()
         w, b = self.weight, self.bias
         if (w is not self._w_of or b is not self._b_of or w.data_ptr() != self._w
